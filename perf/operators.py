@@ -292,7 +292,8 @@ def _run_attend(s):
 def _run_sample(s):
     if own:
         import group_wise_affine_gb300 as gwa
-        return gwa.sample(s["logits"], s["u"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"])
+        token, prob = gwa.sample(s["logits"], s["u"], temperature=s["temperature"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"])
+        return {"token": token, "prob": prob}
     x = s["logits"].float()
     x = x.masked_fill(x != x, -math.inf)
     R, V = x.shape
