@@ -4,6 +4,7 @@
 #include <math.h>
 #include <mutex>
 #include <map>
+#include <set>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string>
@@ -178,6 +179,23 @@ cudaError_t prefer_max_shared(const void *kernel) {
                              (int)cudaSharedmemCarveoutMaxShared);
     if (e == cudaSuccess) done[key] = true;
     return e;
+}
+
+// Opt a kernel in to more than 48 KB of dynamic shared memory (once per
+// device).
+cudaError_t allow_smem(const void *kernel, int bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void *>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count(std::make_pair(dev, kernel))) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bytes);
+    if (e != cudaSuccess) return e;
+    done.insert(std::make_pair(dev, kernel));
+    return cudaSuccess;
 }
 
 // ------------------------------------------------------------ validation

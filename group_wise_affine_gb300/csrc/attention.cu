@@ -37,12 +37,10 @@
 // unpacking, serves better here than a TMEM-accumulated tcgen05 MMA, whose
 // smallest tile is 64 rows.
 #include <algorithm>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
+#include "mma.cuh"
 
 namespace gwa {
 
@@ -97,55 +95,6 @@ struct AttLayout {
     static_assert(kAttRows * D * 4 <= WARP_BYTES, "merge buffer fits the ring");
     static_assert(BLOCKS_PER_SM >= 1, "shared memory per SM");
 };
-
-template <int N>
-__device__ __forceinline__ void cp_async(void *dst, const void *src) {
-    if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)),
-                     "l"(src)
-                     : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)),
-                     "l"(src), "n"(N)
-                     : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// d += a b on bf16 m16n8k16 fragments (fp32 accumulators).
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1,
-                                         uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-        "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The transpose of an 8x8 bf16 matrix held one row pair per lane.
-__device__ __forceinline__ uint32_t movmatrix_t(uint32_t a) {
-    uint32_t d;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// bf16 pair (lo in the low half), round to nearest even.
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t d;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-    return d;
-}
 
 __device__ __forceinline__ uint32_t bf2_bits(__nv_bfloat162 v) {
     return *reinterpret_cast<const uint32_t *>(&v);
@@ -679,23 +628,6 @@ static int attn_blocks_per_sm(int bits, int D) {
     GWA_ATT(8, 64) GWA_ATT(8, 128) GWA_ATT(8, 256)
 #undef GWA_ATT
     return 1;
-}
-
-// Opt a kernel in to more than 48 KB of dynamic shared memory (once per
-// device).
-static cudaError_t allow_smem(const void *kernel, int bytes) {
-    static std::mutex mu;
-    static std::set<std::pair<int, const void *>> done;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    if (done.count(std::make_pair(dev, kernel))) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             bytes);
-    if (e != cudaSuccess) return e;
-    done.insert(std::make_pair(dev, kernel));
-    return cudaSuccess;
 }
 
 template <int BITS, int D>

@@ -128,6 +128,8 @@ int num_sms();
 int resident_clusters(const void *kernel, int cl, int threads, size_t smem);
 // Largest shared-memory carveout for a streaming kernel (once per device).
 cudaError_t prefer_max_shared(const void *kernel);
+// Opts a kernel in to `bytes` of dynamic shared memory (once per device).
+cudaError_t allow_smem(const void *kernel, int bytes);
 
 cudaError_t launch_dense(int mode, const DenseParams &p, cudaStream_t st);
 cudaError_t launch_stream(int mode, const DenseParams &p, cudaStream_t st,
