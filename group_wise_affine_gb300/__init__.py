@@ -9,6 +9,7 @@ arithmetic runs in the library's sm_103a kernels.  There is no fallback: if
 Names mirror the C entry points without the ``gwa_`` prefix:
 ``qmv_affine``, ``qmv_fused_sections``, ``qmv_gate_up_silu``,
 ``qmv_qkv_rope``, ``moe_qmv_gather``, ``quantize_affine``, ``sdpa_dequant_v``,
+``rope_table``, ``kv_append``, ``kv_read``, ``sdpa_paged``, ``sample``,
 ``workspace_bytes``, ``last_error``,
 ``debug_unpack``, ``debug_dequant``.
 
@@ -39,6 +40,9 @@ GWA_MOE_GATE_UP_SILU = 0
 GWA_MOE_DOWN_COMBINE = 1
 # ``bits`` of fp8 (e4m3) weights: 8-bit E4M3 codes in the affine container
 GWA_FP8_E4M3 = 0x108
+# logits of ``sample``
+GWA_BF16 = 0
+GWA_FP32 = 1
 
 
 def code_bits(bits: int) -> int:
@@ -50,7 +54,9 @@ EXPORTS = ("gwa_qmv_affine", "gwa_qmv_fused_sections", "gwa_qmv_gate_up_silu",
            "gwa_pipeline_status", "gwa_debug_unpack", "gwa_debug_dequant",
            "gwa_qmv_affine_noalloc", "gwa_quantize_affine", "gwa_qmv_qkv_rope",
            "gwa_qkv_rope_workspace_bytes", "gwa_sdpa_dequant_v",
-           "gwa_sdpa_workspace_bytes", "gwa_debug_bounded_wait")
+           "gwa_sdpa_workspace_bytes", "gwa_debug_bounded_wait",
+           "gwa_rope_table", "gwa_kv_append", "gwa_kv_read", "gwa_sdpa_paged",
+           "gwa_sdpa_paged_workspace_bytes", "gwa_sample")
 
 
 class GwaError(RuntimeError):
@@ -64,6 +70,21 @@ class _QW(ctypes.Structure):
                 ("biases", ctypes.c_void_p), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("bits", ctypes.c_int32),
                 ("group", ctypes.c_int32)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("kq", ctypes.c_void_p), ("kp", ctypes.c_void_p),
+                ("vq", ctypes.c_void_p), ("vp", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
 
 
 _lib = None
@@ -118,6 +139,19 @@ def load(path: str = LIB_PATH):
     lib.gwa_debug_unpack.argtypes = [_QW, vp, vp]
     lib.gwa_debug_dequant.argtypes = [_QW, vp, vp]
     lib.gwa_debug_bounded_wait.argtypes = [ctypes.c_uint32, vp, vp]
+    lib.gwa_rope_table.argtypes = [vp, i64, i32, ctypes.c_double, vp]
+    lib.gwa_kv_append.argtypes = [vp, i64, vp, i32, vp, i64, vp, i64, _KVCache,
+                                  _KVBatch, vp, i64, i32, vp, vp]
+    lib.gwa_kv_read.argtypes = [_KVCache, _KVBatch, vp, vp, vp, vp]
+    lib.gwa_sdpa_paged.argtypes = [vp, i64, i32, _KVCache, _KVBatch,
+                                   ctypes.c_float, i32, vp, vp, sz, vp, vp]
+    lib.gwa_sdpa_paged_workspace_bytes.argtypes = [i32, _KVCache, _KVBatch]
+    lib.gwa_sdpa_paged_workspace_bytes.restype = sz
+    lib.gwa_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp,
+                               vp, vp]
+    for f in ("gwa_rope_table", "gwa_kv_append", "gwa_kv_read",
+              "gwa_sdpa_paged", "gwa_sample"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("gwa_qmv_affine", "gwa_qmv_fused_sections",
               "gwa_qmv_gate_up_silu", "gwa_moe_qmv_gather",
               "gwa_debug_unpack", "gwa_debug_dequant",
@@ -494,6 +528,225 @@ def sdpa_dequant_v(q: torch.Tensor, k: torch.Tensor, vq: torch.Tensor,
         bits, group, float(scale), int(bool(causal)), _ptr(out), wp, wn,
         _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ serving
+class KVCache:
+    """A paged KV cache (gwa_kv_cache): caller-owned tensors kq, vq int32
+    [pages, heads, page_size, head_dim*bits/32] and kp, vp bfloat16 [pages,
+    heads, page_size, head_dim/64, 2] of (scale, bias).  ``KVCache.empty``
+    allocates them."""
+
+    def __init__(self, kq: torch.Tensor, kp: torch.Tensor, vq: torch.Tensor,
+                 vp: torch.Tensor, bits: int = 4, group: int = 64):
+        if kq.dim() != 4 or kp.dim() != 5:
+            raise ValueError("kq must be [pages, heads, page_size, words], "
+                             "kp [pages, heads, page_size, head_dim/64, 2]")
+        pages, heads, page, words = kq.shape
+        dim = words * 32 // bits if bits in (4, 8) else kp.shape[3] * group
+        par = (pages, heads, page, dim // 64, 2)
+        for name, t, dtype, shape in (("kq", kq, torch.int32, kq.shape),
+                                      ("vq", vq, torch.int32, kq.shape),
+                                      ("kp", kp, torch.bfloat16, par),
+                                      ("vp", vp, torch.bfloat16, par)):
+            if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+                raise ValueError(f"{name} must be {dtype} {list(shape)} "
+                                 f"(got {t.dtype} {list(t.shape)})")
+        self.kq, self.kp, self.vq, self.vp = kq, kp, vq, vp
+        self.bits, self.heads, self.dim, self.page_size = bits, heads, dim, page
+        self.device = kq.device
+        self.c = _KVCache(_ptr(kq), _ptr(kp), _ptr(vq), _ptr(vp), pages, heads,
+                          dim, page, bits, group)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, dim: int,
+              bits: int = 4, device=None) -> "KVCache":
+        """A cache of zeros (what was never written reads as zero)."""
+        dev = device if device is not None else "cuda"
+        q = lambda: torch.zeros((pages, heads, page_size, dim * bits // 32),
+                                dtype=torch.int32, device=dev)
+        p = lambda: torch.zeros((pages, heads, page_size, dim // 64, 2),
+                                dtype=torch.bfloat16, device=dev)
+        return cls(q(), p(), q(), p(), bits=bits)
+
+
+class KVBatch:
+    """A batch over a paged cache (gwa_kv_batch): int32 tensors q_start
+    [batch + 1], kv_len [batch], page_table [batch, max_pages] on the device,
+    and the host's bounds (see include/gwa.h).  The tensors are read when the
+    work runs, so a program may update them in place between steps."""
+
+    def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor,
+                 page_table: torch.Tensor, tokens: int, max_q: int,
+                 max_kv: int):
+        n = kv_len.numel()
+        if (q_start.dtype != torch.int32 or kv_len.dtype != torch.int32
+                or page_table.dtype != torch.int32):
+            raise TypeError("q_start, kv_len and page_table must be int32")
+        if (q_start.numel() != n + 1 or page_table.dim() != 2
+                or page_table.shape[0] != n):
+            raise ValueError("q_start must be [batch + 1], kv_len [batch], "
+                             "page_table [batch, max_pages]")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.tokens, self.max_q, self.max_kv = tokens, max_q, max_kv
+        self.c = _KVBatch(_ptr(q_start), _ptr(kv_len), _ptr(page_table), n,
+                          page_table.shape[1], tokens, max_q, max_kv)
+
+
+def _token_rows(x: torch.Tensor, tokens: int, heads: int, dim: int,
+                name: str):
+    """Pointer and token stride of bfloat16 [tokens, heads, dim], whose
+    tokens may lie apart (a view of a fused projection's rows)."""
+    if x.dtype != torch.bfloat16 or tuple(x.shape) != (tokens, heads, dim):
+        raise ValueError(f"{name} must be bfloat16 [{tokens}, {heads}, {dim}] "
+                         f"(got {x.dtype} {list(x.shape)})")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    s = x.stride()
+    if tokens and (s[2] != 1 or (heads > 1 and s[1] != dim)):
+        raise ValueError(f"{name}: only the token axis may be strided")
+    return x.data_ptr(), s[0] if tokens > 1 else heads * dim
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that belongs to the stream which will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _status(status: Optional[torch.Tensor]) -> Optional[int]:
+    if status is not None and (status.dtype != torch.int32
+                               or status.numel() < 1):
+        raise TypeError("status must be an int32 tensor")
+    return _ptr(status)
+
+
+def rope_table(n: int, rot_dim: int, base: float, device=None,
+               stream=None) -> torch.Tensor:
+    """gwa_rope_table: fp32 [n, rot_dim/2, 2] of (cos, sin) for positions
+    0 .. n-1."""
+    t = _new((n, rot_dim // 2, 2), torch.float32,
+             device if device is not None else "cuda", stream)
+    _check(load().gwa_rope_table(_ptr(t), n, rot_dim, float(base),
+                                 _stream(stream)))
+    return t
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
+              batch: KVBatch, q: Optional[torch.Tensor] = None,
+              rope: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None,
+              stream=None) -> Optional[torch.Tensor]:
+    """gwa_kv_append: the batch's new keys and values (bfloat16 [tokens,
+    heads, head_dim], tokens may be strided) into the cache, keys rotated by
+    ``rope`` (float32 [rows, rot_dim/2, 2], or None).  With ``q`` [tokens, Hq,
+    head_dim] returns its rotated copy."""
+    T, H, D = batch.tokens, cache.heads, cache.dim
+    kp, ks = _token_rows(k, T, H, D, "k")
+    vp, vs = _token_rows(v, T, H, D, "v")
+    qp, qs, op, Hq = None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [tokens, Hq, head_dim]")
+        Hq = q.shape[1]
+        qp, qs = _token_rows(q, T, Hq, D, "q")
+        if q_out is None:
+            q_out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
+        _check_out(q_out, T * Hq * D, "q_out")
+        op = _ptr(q_out)
+    rp, rows, rot = None, 0, 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2:
+            raise ValueError("rope must be float32 [rows, rot_dim/2, 2]")
+        rp, rows, rot = _ptr(rope), rope.shape[0], 2 * rope.shape[1]
+    _check(load().gwa_kv_append(qp, qs, op, Hq, kp, ks, vp, vs, cache.c,
+                                batch.c, rp, rows, rot, _status(status),
+                                _stream(stream)))
+    return q_out
+
+
+def kv_read(cache: KVCache, batch: KVBatch,
+            status: Optional[torch.Tensor] = None, stream=None):
+    """gwa_kv_read: (k, v), bfloat16 [tokens, heads, head_dim], that the cache
+    holds for the batch's tokens."""
+    shape = (batch.tokens, cache.heads, cache.dim)
+    k = _new(shape, torch.bfloat16, cache.device, stream)
+    v = _new(shape, torch.bfloat16, cache.device, stream)
+    _check(load().gwa_kv_read(cache.c, batch.c, _ptr(k), _ptr(v),
+                              _status(status), _stream(stream)))
+    return k, v
+
+
+def make_sdpa_paged_workspace(cache: KVCache, batch: KVBatch,
+                              Hq: int) -> torch.Tensor:
+    n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+
+
+def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
+               scale: Optional[float] = None, causal: bool = True,
+               out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """gwa_sdpa_paged: softmax attention of q [tokens, Hq, head_dim] (tokens
+    may be strided) over the paged cache; bfloat16 [tokens, Hq, head_dim]."""
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, Hq, head_dim]")
+    Hq, D = q.shape[1], cache.dim
+    qp, qs = _token_rows(q, batch.tokens, Hq, D, "q")
+    if out is None:
+        out = _new((batch.tokens, Hq, D), torch.bfloat16, q.device, stream)
+    _check_out(out, batch.tokens * Hq * D, "out")
+    if workspace is None:
+        n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
+        workspace = _new(max(n, 16), torch.uint8, q.device, stream)
+    wp, wn = _ws(workspace)
+    _check(load().gwa_sdpa_paged(
+        qp, qs, Hq, cache.c, batch.c,
+        1.0 / float(D) ** 0.5 if scale is None else float(scale),
+        int(bool(causal)), _ptr(out), wp, wn, _status(status),
+        _stream(stream)))
+    return out
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor,
+           temperature: Optional[torch.Tensor] = None,
+           top_k: Optional[torch.Tensor] = None,
+           top_p: Optional[torch.Tensor] = None,
+           min_p: Optional[torch.Tensor] = None, stream=None):
+    """gwa_sample: (token int32 [rows], prob float32 [rows]) drawn from logits
+    [rows, V] (bfloat16 or float32, rows may be strided) by the uniform
+    numbers u float32 [rows]; the filters are per-row tensors (top_k int32,
+    the others float32) or None."""
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be bfloat16 or float32 [rows, V]")
+    R, V = logits.shape
+    if not logits.is_cuda:
+        raise ValueError("logits must live on a CUDA device")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: only the rows may be strided")
+    for name, t, dtype in (("u", u, torch.float32),
+                           ("temperature", temperature, torch.float32),
+                           ("top_k", top_k, torch.int32),
+                           ("top_p", top_p, torch.float32),
+                           ("min_p", min_p, torch.float32)):
+        if t is not None and (t.dtype != dtype or t.numel() != R):
+            raise ValueError(f"{name} must be {dtype} [{R}]")
+    token = _new(R, torch.int32, logits.device, stream)
+    prob = _new(R, torch.float32, logits.device, stream)
+    _check(load().gwa_sample(
+        logits.data_ptr(),
+        GWA_BF16 if logits.dtype == torch.bfloat16 else GWA_FP32, R, V,
+        logits.stride(0) if R > 1 else V, _ptr(u), _ptr(temperature),
+        _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(prob),
+        _stream(stream)))
+    return token, prob
 
 
 def debug_unpack(w: QWeight, stream=None) -> torch.Tensor:

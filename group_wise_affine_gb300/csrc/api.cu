@@ -766,6 +766,239 @@ size_t gwa_sdpa_workspace_bytes(int64_t B, int32_t Hq, int32_t Hkv, int32_t Lq,
     return attention_workspace_bytes((int)B, Hq, Hkv, Lq, (int)T, D);
 }
 
+// ------------------------------------------------------------ serving
+static int check_kv(const gwa_kv_cache &c, const gwa_kv_batch &b, KvView *kv,
+                    const char *fn) {
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: head_dim=%d (64, 128 or 256)", fn,
+                    (int)c.head_dim);
+    if ((c.bits != 4 && c.bits != 8) || c.group != 64)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: bits=%d group=%d (u4 or u8, group 64)",
+                    fn, (int)c.bits, (int)c.group);
+    if (c.page_size < 16 || c.page_size > 4096 || (c.page_size & (c.page_size - 1)))
+        return fail(GWA_ERR_UNSUPPORTED,
+                    "%s: page_size=%d (a power of two, 16 .. 4096)", fn,
+                    (int)c.page_size);
+    if (c.heads < 1 || c.heads > 65535 || c.num_pages < 0 ||
+        c.num_pages > 0x7fffffffLL)
+        return fail(GWA_ERR_INVALID_ARG, "%s: heads=%d num_pages=%lld", fn,
+                    (int)c.heads, (long long)c.num_pages);
+    if (b.batch < 0 || b.max_pages < 0 || b.tokens < 0 || b.tokens > 0x7fffffffLL ||
+        b.max_q < 0 || b.max_kv < 0)
+        return fail(GWA_ERR_INVALID_ARG,
+                    "%s: batch=%d max_pages=%d tokens=%lld max_q=%d max_kv=%d", fn,
+                    (int)b.batch, (int)b.max_pages, (long long)b.tokens,
+                    (int)b.max_q, (int)b.max_kv);
+    kv->kq = c.kq;
+    kv->vq = c.vq;
+    kv->kp = reinterpret_cast<uint32_t *>(c.kp);
+    kv->vp = reinterpret_cast<uint32_t *>(c.vp);
+    kv->num_pages = c.num_pages;
+    kv->heads = c.heads;
+    kv->dim = c.head_dim;
+    kv->bits = c.bits;
+    kv->page_shift = 0;
+    while ((1 << kv->page_shift) < c.page_size) ++kv->page_shift;
+    kv->q_start = b.q_start;
+    kv->kv_len = b.kv_len;
+    kv->page_table = b.page_table;
+    kv->batch = b.batch;
+    kv->max_pages = b.max_pages;
+    kv->max_q = b.max_q;
+    kv->max_kv = b.max_kv;
+    kv->tokens = b.tokens;
+    return GWA_OK;
+}
+
+// The pointers of a cache and batch that work will be enqueued on.
+static int check_kv_ptrs(const KvView &kv, const char *fn) {
+    if (!kv.q_start || !kv.kv_len || (kv.max_pages > 0 && !kv.page_table))
+        return fail(GWA_ERR_INVALID_ARG, "%s: null batch array", fn);
+    if (kv.num_pages < 1 || !kv.kq || !kv.kp || !kv.vq || !kv.vp)
+        return fail(GWA_ERR_INVALID_ARG, "%s: the cache has no pages", fn);
+    if (!aligned(kv.q_start, 4) || !aligned(kv.kv_len, 4) || !aligned(kv.page_table, 4))
+        return fail(GWA_ERR_MISALIGNED, "%s: batch arrays (4 bytes)", fn);
+    if (!aligned(kv.kq, 16) || !aligned(kv.kp, 16) || !aligned(kv.vq, 16) ||
+        !aligned(kv.vp, 16))
+        return fail(GWA_ERR_MISALIGNED, "%s: cache arrays (16 bytes)", fn);
+    return GWA_OK;
+}
+
+static int check_rows(const void *x, int64_t stride, int64_t need, const char *what,
+                      const char *fn) {
+    if (!x) return fail(GWA_ERR_INVALID_ARG, "%s: null %s", fn, what);
+    if (stride < need || stride % 8 != 0)
+        return fail(GWA_ERR_INVALID_ARG,
+                    "%s: %s stride %lld (a multiple of 8, at least %lld)", fn, what,
+                    (long long)stride, (long long)need);
+    if (!aligned(x, 16))
+        return fail(GWA_ERR_MISALIGNED, "%s: %s must be 16-byte aligned", fn, what);
+    return GWA_OK;
+}
+
+int gwa_rope_table(float *table, int64_t n, int32_t rot_dim, double base,
+                   void *stream) {
+    const char *fn = "gwa_rope_table";
+    g_last_error.clear();
+    if (n < 0 || n > 0x7fffffffLL || rot_dim < 2 || rot_dim > 256 || rot_dim % 2 != 0 ||
+        !(base > 0.0) || !isfinite(base))
+        return fail(GWA_ERR_INVALID_ARG, "%s: n=%lld rot_dim=%d base=%g", fn,
+                    (long long)n, (int)rot_dim, base);
+    if (n == 0) return GWA_OK;
+    if (!table) return fail(GWA_ERR_INVALID_ARG, "%s: null table", fn);
+    if (!aligned(table, 8)) return fail(GWA_ERR_MISALIGNED, "%s: table (8 bytes)", fn);
+    int rc = check_device();
+    if (rc) return rc;
+    cudaError_t e = launch_rope_table(reinterpret_cast<float2 *>(table), n, rot_dim,
+                                      pow(base, -2.0 / rot_dim), nullptr,
+                                      static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+int gwa_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_out,
+                  int32_t Hq, const uint16_t *k, int64_t k_stride,
+                  const uint16_t *v, int64_t v_stride, gwa_kv_cache cache,
+                  gwa_kv_batch batch, const float *rope, int64_t rope_rows,
+                  int32_t rot_dim, int32_t *status, void *stream) {
+    const char *fn = "gwa_kv_append";
+    g_last_error.clear();
+    KvView kv{};
+    int rc = check_kv(cache, batch, &kv, fn);
+    if (rc) return rc;
+    if (rot_dim < 0 || rot_dim > kv.dim || rot_dim % 16 != 0)
+        return fail(GWA_ERR_UNSUPPORTED,
+                    "%s: rot_dim=%d (a multiple of 16 up to head_dim)", fn,
+                    (int)rot_dim);
+    if (Hq < 0 || Hq > 65535 || rope_rows < 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: Hq=%d rope_rows=%lld", fn, (int)Hq,
+                    (long long)rope_rows);
+    if (kv.tokens == 0 || kv.batch == 0) return GWA_OK;
+    if ((rc = check_kv_ptrs(kv, fn))) return rc;
+    const int64_t row = (int64_t)kv.heads * kv.dim;
+    if ((rc = check_rows(k, k_stride, row, "k", fn))) return rc;
+    if ((rc = check_rows(v, v_stride, row, "v", fn))) return rc;
+    if (Hq > 0) {
+        if ((rc = check_rows(q, q_stride, (int64_t)Hq * kv.dim, "q", fn))) return rc;
+        if ((rc = check_rows(q_out, (int64_t)Hq * kv.dim, (int64_t)Hq * kv.dim, "q_out", fn)))
+            return rc;
+        if (q_out == q && q_stride != (int64_t)Hq * kv.dim)
+            return fail(GWA_ERR_INVALID_ARG, "%s: q in place must be contiguous", fn);
+    }
+    if (rot_dim > 0 && !rope)
+        return fail(GWA_ERR_INVALID_ARG, "%s: null rope", fn);
+    if (!aligned(rope, 16) || !aligned(status, 4))
+        return fail(GWA_ERR_MISALIGNED, "%s: rope (16 bytes), status (4)", fn);
+    if ((rc = check_device())) return rc;
+    cudaError_t e = launch_kv_append(q, q_stride, q_out, Hq, k, k_stride, v, v_stride,
+                                     kv, rope, rope_rows, rot_dim, status,
+                                     static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
+                uint16_t *v, int32_t *status, void *stream) {
+    const char *fn = "gwa_kv_read";
+    g_last_error.clear();
+    KvView kv{};
+    int rc = check_kv(cache, batch, &kv, fn);
+    if (rc) return rc;
+    if (kv.tokens == 0) return GWA_OK;
+    if (kv.batch == 0) return fail(GWA_ERR_INVALID_ARG, "%s: tokens of no sequence", fn);
+    if ((rc = check_kv_ptrs(kv, fn))) return rc;
+    const int64_t row = (int64_t)kv.heads * kv.dim;
+    if ((rc = check_rows(k, row, row, "k", fn))) return rc;
+    if ((rc = check_rows(v, row, row, "v", fn))) return rc;
+    if (!aligned(status, 4)) return fail(GWA_ERR_MISALIGNED, "%s: status (4 bytes)", fn);
+    if ((rc = check_device())) return rc;
+    cudaError_t e = launch_kv_read(kv, k, v, status, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+static int check_sdpa_paged(int32_t Hq, const KvView &kv, const char *fn) {
+    if (Hq < kv.heads || Hq > 65535 || Hq % kv.heads != 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: Hq=%d over %d KV heads", fn, (int)Hq,
+                    kv.heads);
+    if ((int64_t)(Hq / kv.heads) * kv.max_q > (1 << 30))
+        return fail(GWA_ERR_INVALID_ARG, "%s: max_q=%d", fn, kv.max_q);
+    return GWA_OK;
+}
+
+size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
+                                      gwa_kv_batch batch) {
+    KvView kv{};
+    if (check_kv(cache, batch, &kv, "gwa_sdpa_paged_workspace_bytes") ||
+        check_sdpa_paged(Hq, kv, "gwa_sdpa_paged_workspace_bytes"))
+        return 0;
+    return sdpa_paged_workspace_bytes(Hq, kv);
+}
+
+int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                   gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                   int32_t causal, uint16_t *out, void *workspace,
+                   size_t workspace_bytes, int32_t *status, void *stream) {
+    const char *fn = "gwa_sdpa_paged";
+    g_last_error.clear();
+    KvView kv{};
+    int rc = check_kv(cache, batch, &kv, fn);
+    if (rc) return rc;
+    if ((rc = check_sdpa_paged(Hq, kv, fn))) return rc;
+    if (!isfinite(scale)) return fail(GWA_ERR_INVALID_ARG, "%s: scale", fn);
+    if (kv.tokens == 0 || kv.batch == 0 || kv.max_q == 0) return GWA_OK;
+    if ((rc = check_kv_ptrs(kv, fn))) return rc;
+    const int64_t row = (int64_t)Hq * kv.dim;
+    if ((rc = check_rows(q, q_stride, row, "q", fn))) return rc;
+    if ((rc = check_rows(out, row, row, "out", fn))) return rc;
+    if (!aligned(status, 4)) return fail(GWA_ERR_MISALIGNED, "%s: status (4 bytes)", fn);
+    const size_t need = sdpa_paged_workspace_bytes(Hq, kv);
+    if (!workspace || workspace_bytes < need)
+        return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn,
+                    need, workspace_bytes);
+    if (!aligned(workspace, 16))
+        return fail(GWA_ERR_MISALIGNED, "%s: workspace alignment", fn);
+    if ((rc = check_device())) return rc;
+    cudaError_t e = launch_sdpa_paged(q, q_stride, Hq, kv, scale, causal ? 1 : 0, out,
+                                      workspace, status, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
+               int64_t row_stride, const float *u, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p,
+               int32_t *token, float *prob, void *stream) {
+    const char *fn = "gwa_sample";
+    g_last_error.clear();
+    if (dtype != GWA_BF16 && dtype != GWA_FP32)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: dtype=%d", fn, (int)dtype);
+    if (V > 524288)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: V=%lld exceeds 524288", fn, (long long)V);
+    if (V < 1 || rows < 0 || rows > (1 << 24) || row_stride < V)
+        return fail(GWA_ERR_INVALID_ARG, "%s: rows=%lld V=%lld row_stride=%lld", fn,
+                    (long long)rows, (long long)V, (long long)row_stride);
+    if (rows == 0) return GWA_OK;
+    if (!logits || !u || !token)
+        return fail(GWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(logits, dtype == GWA_BF16 ? 2 : 4) || !aligned(u, 4) ||
+        !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(token, 4) || !aligned(prob, 4))
+        return fail(GWA_ERR_MISALIGNED, "%s: alignment", fn);
+    int rc = check_device();
+    if (rc) return rc;
+    SampleParams p{};
+    p.logits = logits;
+    p.rows = rows;
+    p.V = V;
+    p.stride = row_stride;
+    p.u = u;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.token = token;
+    p.prob = prob;
+    cudaError_t e = launch_sample(p, dtype == GWA_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
 int gwa_debug_bounded_wait(uint32_t limit_us, uint32_t *out, void *stream) {
     const char *fn = "gwa_debug_bounded_wait";
     g_last_error.clear();

@@ -71,9 +71,49 @@ cudaError_t launch_attention(const uint16_t *q, const uint16_t *k,
                              cudaStream_t st);
 size_t attention_workspace_bytes(int B, int Hq, int Hkv, int Lq, int T, int D);
 
-// (cos, sin) table of the rotary embedding, cs[m * d/2 + i] (rope.cu).
+// (cos, sin) table of the rotary embedding, cs[m * d/2 + i] (rope.cu);
+// positions NULL: token m is at position m.
 cudaError_t launch_rope_table(float2 *cs, int64_t M, int head_dim, double r,
                               const int32_t *positions, cudaStream_t st);
+
+// A paged KV cache and a batch over it (gwa_kv_cache, gwa_kv_batch), checked
+// by the entry points.
+struct KvView {
+    uint32_t *kq, *vq;  // [num_pages, heads, page_size, dim*bits/32]
+    uint32_t *kp, *vp;  // [num_pages, heads, page_size, dim/64] (scale, bias)
+    int64_t num_pages;
+    int heads, dim, page_shift, bits;
+    const int32_t *q_start;     // [batch + 1]
+    const int32_t *kv_len;      // [batch]
+    const int32_t *page_table;  // [batch, max_pages]
+    int batch, max_pages, max_q, max_kv;
+    int64_t tokens;
+};
+cudaError_t launch_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_out,
+                             int Hq, const uint16_t *k, int64_t k_stride,
+                             const uint16_t *v, int64_t v_stride, const KvView &kv,
+                             const float *rope, int64_t rope_rows, int rot_dim,
+                             int32_t *status, cudaStream_t st);
+cudaError_t launch_kv_read(const KvView &kv, uint16_t *k, uint16_t *v,
+                           int32_t *status, cudaStream_t st);
+
+// Attention over the paged cache (paged_attention.cu).
+cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
+                              const KvView &kv, float scale, int causal,
+                              uint16_t *out, void *workspace, int32_t *status,
+                              cudaStream_t st);
+size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv);
+
+// Token sampling (sample.cu).
+struct SampleParams {
+    const void *logits;
+    int64_t rows, V, stride;
+    const float *u, *temperature, *top_p, *min_p;
+    const int32_t *top_k;
+    int32_t *token;
+    float *prob;
+};
+cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st);
 
 // Launches `kernel` on `st` with programmatic stream serialization: it may
 // start while the previous kernel in the stream drains; the kernel itself

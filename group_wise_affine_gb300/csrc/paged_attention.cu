@@ -1,0 +1,901 @@
+// Softmax attention over the paged 4-bit (or 8-bit) KV cache, for tokens by
+// the few: one new token a sequence, drafted tokens, short tails.
+// "Sanctum-MLX", six-changes table row 5 and the paragraph after it (online
+// softmax in fp32, causal mask, GQA without copies), here with the keys
+// quantized too and both in pages.
+//
+//   out[i,h,:] = sum_t p_t (sv_t cv_t + bv_t),
+//   p = softmax_t(scale * q[i,h,:] . (sk_t ck_t + bk_t)),
+//
+// with codes c, and scale s and bias b per token, head and 64 dimensions.
+// Codes enter the tensor cores as they are, centred: c - 8 (u4) or c - 128
+// (u8) is exact in fp16, and the affine map folds into what is already
+// there:
+//   scores  S^T = C_k Q^T    per 64 dimensions, fp32; then
+//           x = sum_g s_g S_g + b'_g sum(Q_g),  b' = b + 8 s (128 s);
+//   values  O^T += C_v^T P'^T  with P' = p * s in fp16, plus sum_t p_t b'_t.
+// Centred codes keep the sums small: with c (0..15) or an offset of 1024
+// left in, an output that averages thousands of values would be the small
+// difference of two large sums.  fp16 holds P' to 2^-12, bf16 only to 2^-9.
+// Its range is met by powers of two: a query row is scaled so that its
+// largest element lies in [2^12, 2^13), and the value scales so that the
+// largest met so far lies in [2^5, 2^6) (the accumulators are rescaled when a
+// larger one comes, as they are for the running maximum).
+//
+// Work split.  The unit is a step of 128 keys of one sequence, KV head and
+// block of up to 8 NN query rows (GQA heads x new tokens); the units of the
+// whole batch are laid end to end and cut into equal runs, one per CTA, so
+// ragged batches and single long sequences both fill the GPU.  A CTA that
+// holds a whole (sequence, head, row block) writes the output itself; the
+// pieces of one that was cut go to the workspace as (output, max, sum) and a
+// second kernel joins them.  Lengths are read from the device; nothing of
+// the split depends on host values but the grid.
+//
+// A warp takes 32 of the step's 128 keys (two MMA tiles of 16), copies their
+// codes and parameters with cp.async into its own ring some steps ahead, and
+// keeps its own softmax state; the four warps merge in shared memory at the
+// end of a piece.  The ring's rows are laid out by 64-dimension group so
+// that the fragment reads hit every bank once.  The order of keys inside a
+// tile is permuted (row j of the scores is key (j >> 1) + 4 (j & 1)), which
+// makes the value fragments' reads contiguous.
+//
+// Warp-level MMAs (m16n8k16) serve here: with 1 to 32 query rows the work is
+// bound by the bytes of the cache and by unpacking codes, and their operands
+// live in registers beside the unpacking; a tcgen05 MMA has at least 64 rows.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv.cuh"
+#include "mma.cuh"
+
+namespace gwa {
+
+constexpr int kPgWarps = 4;
+constexpr int kPgKeys = 32;                    // keys of a warp's step
+constexpr int kPgStep = kPgWarps * kPgKeys;    // keys of a CTA's step
+constexpr int kPgMaxCtas = 2048;
+
+struct PagedParams {
+    const uint16_t *q;
+    int64_t q_stride;
+    int Hq, rep;
+    KvView kv;
+    float scale;
+    int causal;
+    uint16_t *out;    // [tokens, Hq, dim]
+    int4 *desc;       // [ctas]: a cut piece that starts in this CTA
+    float *part;      // [2 ctas][8 NN][dim + 4]
+    int32_t *status;
+};
+
+// Shared memory of one warp's ring stage (32 keys: two tiles of 16).
+template <int BITS, int D, int NN>
+struct PgLayout {
+    static constexpr int G = D / 64;
+    static constexpr int GB = 8 * BITS;          // code bytes of a group
+    static constexpr int TILE = 16 * G * GB;     // codes of a tile
+    static constexpr int PB = 16 * G * 4;        // parameters of a tile
+    static constexpr int K_OFF = 0;
+    static constexpr int V_OFF = 2 * TILE;
+    static constexpr int KP_OFF = 4 * TILE;
+    static constexpr int VP_OFF = KP_OFF + 2 * PB;
+    static constexpr int STAGE = VP_OFF + 2 * PB;
+    static constexpr int S = 3;
+    static constexpr int NQ = 8 * NN;
+    static constexpr int MERGE = NQ * D * 4;     // a warp's output rows
+    static constexpr int WARP_BYTES = S * STAGE > MERGE ? S * STAGE : MERGE;
+    static constexpr int BYTES = kPgWarps * WARP_BYTES;
+    static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 4096);
+    // accumulators, queries and fragments: about 96 + 4 registers per 8 rows
+    // and 16 dimensions
+    static constexpr int BY_REGS = NN * D <= 128 ? 4 : NN * D <= 256 ? 3 : 2;
+    static constexpr int CTAS = BY_SMEM < BY_REGS ? (BY_SMEM < 1 ? 1 : BY_SMEM) : BY_REGS;
+};
+
+// Keys that some row of the sequence sees, in steps; row blocks; units.
+struct PgSeq {
+    int first, count, len, rows, nrg, nt;
+    int64_t units;
+};
+template <int NQ>
+__device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
+    const KvSeq s = kv_seq(p.kv, b);
+    PgSeq r;
+    r.first = s.first;
+    r.count = s.count;
+    r.len = s.len;
+    r.rows = p.rep * min(s.count, p.kv.max_q);
+    r.nrg = (r.rows + NQ - 1) / NQ;
+    r.nt = (s.len + kPgStep - 1) / kPgStep;
+    r.units = (int64_t)p.kv.heads * r.nrg * r.nt;
+    return r;
+}
+
+// CTA c's run of units starts at total * c / ctas.
+__device__ __forceinline__ int64_t pg_start(int64_t total, int c, int ctas) {
+    return total / ctas * c + total % ctas * c / ctas;
+}
+
+template <int BITS>
+__device__ __forceinline__ void k_fragments(const unsigned char *src, uint32_t (&f)[8]) {
+    // sixteen centred codes of one key row, as the pairs the MMA takes
+    if constexpr (BITS == 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(src);
+        const __half2 off = __floats2half2_rn(1032.f, 1032.f);
+        const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+        const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t u = j ? w.y : w.x, u8 = u >> 8;
+            // fields at bits 0 and 16: 1024 + c; at 4 and 20: 1024 + 16 c
+            f[4 * j + 0] = h2_bits(__hsub2(bits_h2((u & 0x000f000fu) | 0x64006400u), off));
+            f[4 * j + 1] = h2_bits(__hfma2(bits_h2((u & 0x00f000f0u) | 0x64006400u), r16, m72));
+            f[4 * j + 2] = h2_bits(__hsub2(bits_h2((u8 & 0x000f000fu) | 0x64006400u), off));
+            f[4 * j + 3] = h2_bits(__hfma2(bits_h2((u8 & 0x00f000f0u) | 0x64006400u), r16, m72));
+        }
+    } else {
+        const uint4 w = *reinterpret_cast<const uint4 *>(src);
+        const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j] = h2_bits(__hsub2(bits_h2((ws[j] & 0x00ff00ffu) | 0x64006400u), off));
+            f[2 * j + 1] =
+                h2_bits(__hsub2(bits_h2(((ws[j] >> 8) & 0x00ff00ffu) | 0x64006400u), off));
+        }
+    }
+}
+
+// Dimension, within its lane's sixteen, of element e of pair i as
+// k_fragments orders them.
+template <int BITS>
+__device__ __forceinline__ constexpr int k_dim(int i, int e) {
+    return BITS == 4 ? 8 * (i / 4) + (i % 4) + 4 * e
+                     : 4 * (i / 2) + (i % 2) + 2 * e;
+}
+
+// 2^e with the largest of a row in [2^12, 2^13), and 2^-e.
+__device__ __forceinline__ void row_scale(float t, float &up, float &down) {
+    int p = 0;
+    if (t > 0.f && t < 3.0e38f) p = 139 - f32_exp_field(t);
+    p = p < -125 ? -125 : p > 125 ? 125 : p;
+    up = __uint_as_float((uint32_t)(127 + p) << 23);
+    down = __uint_as_float((uint32_t)(127 - p) << 23);
+}
+
+template <int BITS, int D, int NN>
+__global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
+    paged_decode_kernel(PagedParams p) {
+    using L = PgLayout<BITS, D, NN>;
+    constexpr int G = L::G, GB = L::GB, S = L::S, NQ = L::NQ;
+    constexpr int NT = D / 16;                  // value m-tiles
+    constexpr int NCP = L::TILE / 16 / kWarp;   // 16-byte copies per lane, tile
+    constexpr int RCH = G * GB / 16;            // 16-byte chunks of a key row
+    constexpr float KC = BITS == 4 ? 8.f : 128.f;
+    constexpr unsigned FULL = 0xffffffffu;
+    static_assert(NCP >= 1, "tile copies");
+    extern __shared__ __align__(16) unsigned char pg_smem[];
+    __shared__ float s_m[kPgWarps][NQ], s_l[kPgWarps][NQ], s_f[kPgWarps][NQ];
+    __shared__ float s_b[kPgWarps][NQ][G];
+    __shared__ float s_den[NQ];
+
+    const int lane = threadIdx.x & (kWarp - 1), warp = threadIdx.x / kWarp;
+    const int g = lane >> 2, t = lane & 3;
+    const int kv_g = (g >> 1) + 4 * (g & 1);    // the key of score row g
+    unsigned char *wsm = pg_smem + warp * L::WARP_BYTES;
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    pdl_wait_primary();
+
+    // ---- this CTA's run of units, found by every warp for itself
+    const int B = p.kv.batch;
+    int64_t total = 0;
+    for (int b0 = 0; b0 < B; b0 += kWarp) {
+        const int b = b0 + lane;
+        int64_t u = b < B ? pg_seq<NQ>(p, b).units : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
+        total += u;
+    }
+    const int ctas = (int)min((int64_t)gridDim.x, total);
+    const int cta = blockIdx.x;
+    // sequences without keys: their rows are zero
+    for (int b = cta; b < B; b += gridDim.x) {
+        const PgSeq s = pg_seq<NQ>(p, b);
+        if (s.nt > 0) continue;
+        uint32_t *o = reinterpret_cast<uint32_t *>(p.out + (int64_t)s.first * p.Hq * D);
+        for (int64_t i = threadIdx.x; i < (int64_t)(s.rows / p.rep) * p.Hq * (D / 2);
+             i += blockDim.x)
+            o[i] = 0u;
+    }
+    if (threadIdx.x == 0) p.desc[cta] = make_int4(-1, 0, 0, 0);
+    if (cta >= ctas) return;
+    const int64_t begin = pg_start(total, cta, ctas), end = pg_start(total, cta + 1, ctas);
+
+    int b = 0;
+    int64_t at = 0;  // units before sequence b
+    for (int b0 = 0; b0 < B; b0 += kWarp) {
+        const int64_t u = b0 + lane < B ? pg_seq<NQ>(p, b0 + lane).units : 0;
+        int64_t incl = u;
+#pragma unroll
+        for (int o = 1; o < kWarp; o <<= 1) {
+            const int64_t v = __shfl_up_sync(FULL, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned past = __ballot_sync(FULL, at + incl > begin);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            b = b0 + l;
+            at += __shfl_sync(FULL, incl - u, l);
+            break;
+        }
+        at += __shfl_sync(FULL, incl, kWarp - 1);
+    }
+    PgSeq sq = pg_seq<NQ>(p, b);
+    int64_t cur = begin;
+    int piece = 0;
+    const float sl2 = p.scale * 1.4426950408889634f;  // scores in base 2
+    constexpr float kLazy = 8.f;
+    const int pmask = (1 << p.kv.page_shift) - 1;
+
+    while (cur < end) {
+        while (cur >= at + sq.units) {
+            at += sq.units;
+            sq = pg_seq<NQ>(p, ++b);
+        }
+        const int64_t in_seq = cur - at;
+        const int seg = (int)(in_seq / sq.nt);  // hk * nrg + rg
+        const int hk = seg / sq.nrg, rg = seg % sq.nrg;
+        const int ta = (int)(in_seq - (int64_t)seg * sq.nt);
+        const int tb = (int)min((int64_t)sq.nt, ta + (end - cur));
+        const int nlive = min(NQ, sq.rows - rg * NQ);
+        const int32_t *table = p.kv.page_table + (int64_t)b * p.kv.max_pages;
+
+        // queries: row 8 nn + g, dimensions 64 gg + 16 t .. + 15
+        uint32_t qf[NN][G][8];
+        float fac[NN][2], qs[NN][G][2];
+        int lim[NN][2];
+#pragma unroll
+        for (int nn = 0; nn < NN; ++nn) {
+            const int r = rg * NQ + 8 * nn + g;
+            float mx = 0.f, down = 1.f, up = 1.f, sum[G];
+            uint4 raw[G][2];
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg) raw[gg][0] = raw[gg][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (8 * nn + g < nlive) {
+                const uint16_t *src = p.q + (sq.first + r / p.rep) * p.q_stride +
+                                      (int64_t)(hk * p.rep + r % p.rep) * D + 16 * t;
+#pragma unroll
+                for (int gg = 0; gg < G; ++gg) {
+                    raw[gg][0] = reinterpret_cast<const uint4 *>(src + 64 * gg)[0];
+                    raw[gg][1] = reinterpret_cast<const uint4 *>(src + 64 * gg)[1];
+                }
+            }
+            auto elem = [&](int gg, int d) {
+                const uint4 &u = raw[gg][d / 8];
+                const int w = (d % 8) / 2;
+                const uint32_t v = w == 0 ? u.x : w == 1 ? u.y : w == 2 ? u.z : u.w;
+                return d & 1 ? bf16_hi(v) : bf16_lo(v);
+            };
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg)
+#pragma unroll
+                for (int d = 0; d < 16; ++d) mx = fmaxf(mx, fabsf(elem(gg, d)));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+            row_scale(mx, up, down);
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg) {
+                sum[gg] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float a = elem(gg, k_dim<BITS>(i, 0)) * up;
+                    const float c = elem(gg, k_dim<BITS>(i, 1)) * up;
+                    qf[nn][gg][i] = pack_f16(a, c);
+                    sum[gg] += a + c;
+                }
+                sum[gg] += __shfl_xor_sync(FULL, sum[gg], 1);
+                sum[gg] += __shfl_xor_sync(FULL, sum[gg], 2);
+            }
+            // the scores' columns 2t, 2t + 1 are rows 8 nn + 2t (+ 1)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int from = (2 * t + h) * 4;
+                fac[nn][h] = __shfl_sync(FULL, down, from) * sl2;
+#pragma unroll
+                for (int gg = 0; gg < G; ++gg) qs[nn][gg][h] = __shfl_sync(FULL, sum[gg], from);
+                const int i = 8 * nn + 2 * t + h, rr = rg * NQ + i;
+                lim[nn][h] = i >= nlive ? 0
+                             : p.causal ? min(sq.len, sq.len - sq.count + rr / p.rep + 1)
+                                        : sq.len;
+            }
+        }
+        // every row of the block sees the keys below `all`
+        int all = 0x7fffffff;
+#pragma unroll
+        for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) all = min(all, lim[nn][h]);
+        if (nlive < NQ) {  // padding rows: masked or not, they are never written
+            all = p.causal ? max(0, sq.len - sq.count + rg * NQ / p.rep + 1) : sq.len;
+        } else {
+            all = __reduce_min_sync(FULL, all);
+        }
+
+        float o[NN][NT][4], m[NN][2], l[NN][2], bs[NN][G][2];
+#pragma unroll
+        for (int nn = 0; nn < NN; ++nn) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                o[nn][j][0] = o[nn][j][1] = o[nn][j][2] = o[nn][j][3] = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[nn][h] = -INFINITY;
+                l[nn][h] = 0.f;
+#pragma unroll
+                for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] = 0.f;
+            }
+        }
+        float vinv = 1.f, vlim = -1.f;  // value scales: times vinv, met up to vlim
+
+        // page ids of the tiles of 16 steps: lane 2 j + u holds step j's tile u
+        int pages = 0, pages_at = -1;
+        auto issue = [&](int step) {  // step in [ta, tb)
+            if (pages_at < 0 || step - pages_at >= 16) {
+                pages_at = step;
+                const int key = (step + (lane >> 1)) * kPgStep + warp * kPgKeys + (lane & 1) * 16;
+                const int j = key >> p.kv.page_shift;
+                pages = 0;
+                if (key < sq.len && j < p.kv.max_pages) {
+                    pages = table[j];
+                    if (pages < 0 || pages >= p.kv.num_pages) {
+                        if (p.status) atomicOr(p.status, (int)kKvBadPage);
+                        pages = 0;
+                    }
+                }
+            }
+            unsigned char *st = wsm + ((step - ta) % S) * L::STAGE;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int page = __shfl_sync(FULL, pages, 2 * (step - pages_at) + u);
+                const int key = step * kPgStep + warp * kPgKeys + u * 16;
+                if (key >= sq.len) continue;
+                const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
+                                    (key & pmask);
+                const uint4 *ks = reinterpret_cast<const uint4 *>(p.kv.kq + row * (D * BITS / 32));
+                const uint4 *vs = reinterpret_cast<const uint4 *>(p.kv.vq + row * (D * BITS / 32));
+#pragma unroll
+                for (int i = 0; i < NCP; ++i) {
+                    const int ci = lane + 32 * i;
+                    const int r = ci / RCH, rem = ci % RCH;
+                    const int gg = rem / (GB / 16), ch = rem % (GB / 16);
+                    const int kr = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
+                    const int vch = BITS == 8 ? ch ^ (((r >> 1) & 1) << 1) : ch;
+                    cp_async<16>(st + L::K_OFF + u * L::TILE + (gg * 16 + kr) * GB + ch * 16, ks + ci);
+                    cp_async<16>(st + L::V_OFF + u * L::TILE + (gg * 16 + r) * GB + vch * 16, vs + ci);
+                }
+                // parameters: lanes below 4 G the keys', the next 4 G the values'
+                if (lane < 8 * G) {
+                    const int i = lane % (4 * G);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        (lane < 4 * G ? p.kv.kp : p.kv.vp) + row * G);
+                    cp_async<16>(st + (lane < 4 * G ? L::KP_OFF : L::VP_OFF) + u * L::PB + i * 16,
+                                 src + i);
+                }
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            if (ta + i < tb) issue(ta + i);
+            cp_async_commit();
+        }
+        for (int step = ta; step < tb; ++step) {
+            if (step + S - 1 < tb) issue(step + S - 1);
+            cp_async_commit();
+            cp_async_wait<S - 1>();
+            __syncwarp();
+            const unsigned char *stg = wsm + ((step - ta) % S) * L::STAGE;
+            const int key0 = step * kPgStep + warp * kPgKeys;
+            if (key0 < sq.len) {  // warp-uniform
+                // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + 8 kk + kv_g
+                float x[2][2][NN][2];
+                float sv[2][2][G], bv[2][2][G];
+                float lm[NN][2], smax = 0.f;
+#pragma unroll
+                for (int nn = 0; nn < NN; ++nn) lm[nn][0] = lm[nn][1] = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float acc[NN][2][2];
+#pragma unroll
+                    for (int nn = 0; nn < NN; ++nn)
+                        acc[nn][0][0] = acc[nn][0][1] = acc[nn][1][0] = acc[nn][1][1] = 0.f;
+#pragma unroll
+                    for (int gg = 0; gg < G; ++gg) {
+                        const unsigned char *ks =
+                            stg + L::K_OFF + u * L::TILE + (gg * 16 + g) * GB + t * 2 * BITS;
+                        uint32_t f0[8], f1[8];
+                        k_fragments<BITS>(ks, f0);
+                        k_fragments<BITS>(ks + 8 * GB, f1);
+                        const uint32_t p0 = *reinterpret_cast<const uint32_t *>(
+                            stg + L::KP_OFF + u * L::PB + (kv_g * G + gg) * 4);
+                        const uint32_t p1 = *reinterpret_cast<const uint32_t *>(
+                            stg + L::KP_OFF + u * L::PB + ((kv_g + 8) * G + gg) * 4);
+                        const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
+                        const float b0 = fmaf(KC, s0, bf16_hi(p0));
+                        const float b1 = fmaf(KC, s1, bf16_hi(p1));
+#pragma unroll
+                        for (int nn = 0; nn < NN; ++nn) {
+                            float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2)
+                                mma_f16(c, f0[i], f1[i], f0[i + 1], f1[i + 1], qf[nn][gg][i],
+                                        qf[nn][gg][i + 1]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                acc[nn][0][h] = fmaf(s0, c[h], fmaf(b0, qs[nn][gg][h], acc[nn][0][h]));
+                                acc[nn][1][h] = fmaf(s1, c[2 + h], fmaf(b1, qs[nn][gg][h], acc[nn][1][h]));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                        for (int gg = 0; gg < G; ++gg) {
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                                stg + L::VP_OFF + u * L::PB + ((kv_g + 8 * kk) * G + gg) * 4);
+                            sv[u][kk][gg] = bf16_lo(w);
+                            bv[u][kk][gg] = fmaf(KC, bf16_lo(w), bf16_hi(w));
+                        }
+#pragma unroll
+                        for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                x[u][kk][nn][h] = acc[nn][kk][h] * fac[nn][h];
+                    }
+                }
+                const bool edge = key0 + kPgKeys > all;
+                if (edge) {
+                    // keys that a row does not see: no score, and no parameter
+                    // (which may be anything) of a key that no row sees
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const int key = key0 + 16 * u + 8 * kk + kv_g;
+#pragma unroll
+                            for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    if (key >= lim[nn][h]) x[u][kk][nn][h] = -INFINITY;
+                            if (key >= sq.len)
+#pragma unroll
+                                for (int gg = 0; gg < G; ++gg) sv[u][kk][gg] = bv[u][kk][gg] = 0.f;
+                        }
+                }
+                bool raise = false;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                        for (int gg = 0; gg < G; ++gg) smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
+#pragma unroll
+                        for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                lm[nn][h] = fmaxf(lm[nn][h], x[u][kk][nn][h]);
+                    }
+                raise = smax > vlim;
+#pragma unroll
+                for (int nn = 0; nn < NN; ++nn)
+                    raise |= lm[nn][0] > m[nn][0] + kLazy || lm[nn][1] > m[nn][1] + kLazy;
+                if (__any_sync(FULL, raise)) {
+                    // a new running maximum (weights stay below 2^kLazy), or a
+                    // larger value scale
+                    float vf = 1.f;
+                    if (smax == INFINITY) {
+                        // an infinite scale makes its own readers' rows
+                        // infinite, and must not take the others' range
+                        smax = 0.f;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                                for (int gg = 0; gg < G; ++gg)
+                                    if (fabsf(sv[u][kk][gg]) < INFINITY)
+                                        smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
+                    }
+                    const float top = __uint_as_float(
+                        __reduce_max_sync(FULL, __float_as_uint(fmaxf(smax, 0.f))));
+                    if (top > vlim) {
+                        // 2^e <= top < 2^(e+1): times 2^(5-e)
+                        const int e = min(max(f32_exp_field(top), 6), 253);
+                        const float ninv = __uint_as_float((uint32_t)(259 - e > 254 ? 254 : 259 - e) << 23);
+                        vf = vlim < 0.f ? 1.f : ninv / vinv;
+                        vinv = ninv;
+                        vlim = __uint_as_float((uint32_t)(e + 1) << 23);
+                    }
+#pragma unroll
+                    for (int nn = 0; nn < NN; ++nn) {
+                        float cr[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float mt = lm[nn][h];
+#pragma unroll
+                            for (int off = 4; off < kWarp; off <<= 1)
+                                mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, off));
+                            const float mn = fmaxf(m[nn][h], mt);
+                            cr[h] = mn == -INFINITY ? 1.f : ex2(m[nn][h] - mn);
+                            m[nn][h] = mn;
+                            l[nn][h] *= cr[h];
+#pragma unroll
+                            for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] *= cr[h];
+                            cr[h] *= vf;
+                        }
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            o[nn][j][0] *= cr[0];
+                            o[nn][j][1] *= cr[1];
+                            o[nn][j][2] *= cr[0];
+                            o[nn][j][3] *= cr[1];
+                        }
+                    }
+                }
+                // ---- weights
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                        for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float &e = x[u][kk][nn][h];
+                                e = e == -INFINITY ? 0.f : ex2(e - m[nn][h]);
+                                l[nn][h] += e;
+                            }
+                // ---- values
+#pragma unroll
+                for (int gg = 0; gg < G; ++gg) {
+                    uint32_t pb[2][NN][2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const float s = sv[u][kk][gg] * vinv, bb = bv[u][kk][gg];
+#pragma unroll
+                            for (int nn = 0; nn < NN; ++nn) {
+                                const float e0 = x[u][kk][nn][0], e1 = x[u][kk][nn][1];
+                                float a0 = e0 * s, a1 = e1 * s;
+                                float c0 = e0 * bb, c1 = e1 * bb;
+                                if (edge) {  // a weight of zero takes nothing, whatever s and b
+                                    a0 = e0 == 0.f ? 0.f : a0;
+                                    a1 = e1 == 0.f ? 0.f : a1;
+                                    c0 = e0 == 0.f ? 0.f : c0;
+                                    c1 = e1 == 0.f ? 0.f : c1;
+                                }
+                                bs[nn][gg][0] += c0;
+                                bs[nn][gg][1] += c1;
+                                pb[u][nn][kk] = movmatrix_t(pack_f16(a0, a1));
+                            }
+                        }
+                    const __half2 off4 = __floats2half2_rn(1032.f, 1032.f);
+                    const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+                    const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
+                    const __half2 off8 = __floats2half2_rn(1152.f, 1152.f);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const unsigned char *vs = stg + L::V_OFF + u * L::TILE + gg * 16 * GB;
+                        // words of keys t, t + 4 (k = 2t, 2t + 1), t + 8, t + 12
+                        uint32_t w[4][BITS / 4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = t + 4 * i;
+                            if constexpr (BITS == 4) {
+                                w[i][0] = *reinterpret_cast<const uint32_t *>(vs + r * GB + g * 4);
+                            } else {
+                                const uint2 v = *reinterpret_cast<const uint2 *>(
+                                    vs + r * GB + (((g >> 1) ^ (((r >> 1) & 1) << 1)) * 16) +
+                                    (g & 1) * 8);
+                                w[i][0] = v.x;
+                                w[i][1] = v.y;
+                            }
+                        }
+#pragma unroll
+                        for (int jj = 0; jj < 4; ++jj) {
+                            uint32_t a[4];
+                            if constexpr (BITS == 4) {
+                                // byte jj: dimensions 8g + 2jj (m-row g), + 1 (g + 8)
+                                const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t r = __byte_perm(w[2 * k][0], w[2 * k + 1][0], sel);
+                                    a[2 * k] = h2_bits(__hsub2(bits_h2((r & 0x000f000fu) | 0x64006400u), off4));
+                                    a[2 * k + 1] = h2_bits(__hfma2(
+                                        bits_h2((r & 0x00f000f0u) | 0x64006400u), r16, m72));
+                                }
+                            } else {
+                                const int e = 2 * (jj & 1);
+                                const uint32_t sel = e | ((e + 1) << 4) | ((4 + e) << 8) | ((5 + e) << 12);
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t r = __byte_perm(w[2 * k][jj / 2], w[2 * k + 1][jj / 2], sel);
+                                    a[2 * k] = h2_bits(__hsub2(bits_h2((r & 0x00ff00ffu) | 0x64006400u), off8));
+                                    a[2 * k + 1] = h2_bits(__hsub2(
+                                        bits_h2(((r >> 8) & 0x00ff00ffu) | 0x64006400u), off8));
+                                }
+                            }
+#pragma unroll
+                            for (int nn = 0; nn < NN; ++nn)
+                                mma_f16(o[nn][4 * gg + jj], a[0], a[1], a[2], a[3], pb[u][nn][0],
+                                        pb[u][nn][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // the stage is free for the next copies
+        }
+        cp_async_wait<0>();
+
+        // ---- the four warps' states to shared memory, and out
+#pragma unroll
+        for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int off = 4; off < kWarp; off <<= 1) {
+                    l[nn][h] += __shfl_xor_sync(FULL, l[nn][h], off);
+#pragma unroll
+                    for (int gg = 0; gg < G; ++gg)
+                        bs[nn][gg][h] += __shfl_xor_sync(FULL, bs[nn][gg][h], off);
+                }
+        __syncwarp();
+        float *so = reinterpret_cast<float *>(wsm);
+        const float back = 1.f / vinv;  // a power of two
+#pragma unroll
+        for (int nn = 0; nn < NN; ++nn) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int d = 64 * (j / 4) + 8 * g + 2 * (j % 4);
+                const int r = 8 * nn + 2 * t;
+                *reinterpret_cast<float2 *>(so + r * D + d) =
+                    make_float2(o[nn][j][0] * back, o[nn][j][2] * back);
+                *reinterpret_cast<float2 *>(so + (r + 1) * D + d) =
+                    make_float2(o[nn][j][1] * back, o[nn][j][3] * back);
+            }
+            if (g == 0)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 8 * nn + 2 * t + h;
+                    s_m[warp][r] = m[nn][h];
+                    s_l[warp][r] = l[nn][h];
+#pragma unroll
+                    for (int gg = 0; gg < G; ++gg) s_b[warp][r][gg] = bs[nn][gg][h];
+                }
+        }
+        __syncthreads();
+        const bool whole = ta == 0 && tb == sq.nt;
+        float *part = p.part + (int64_t)(2 * cta + piece) * NQ * (D + 4);
+        if (threadIdx.x < NQ) {
+            const int i = threadIdx.x;
+            float mx = -INFINITY, den = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) mx = fmaxf(mx, s_m[w][i]);
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) {
+                const float f = s_m[w][i] == -INFINITY ? 0.f : ex2(s_m[w][i] - mx);
+                s_f[w][i] = f;
+                den += f * s_l[w][i];
+            }
+            s_den[i] = den;
+            if (!whole) {
+                part[i * (D + 4) + D] = mx;
+                part[i * (D + 4) + D + 1] = den;
+            }
+        }
+        __syncthreads();
+        constexpr int C4 = D / 4;
+        for (int e = threadIdx.x; e < nlive * C4; e += blockDim.x) {
+            const int i = e / C4, c4 = e % C4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kPgWarps; ++w) {
+                const float f = s_f[w][i], bw = s_b[w][i][c4 / 16];
+                if (f == 0.f) continue;
+                const float4 v =
+                    reinterpret_cast<const float4 *>(pg_smem + w * L::WARP_BYTES)[i * C4 + c4];
+                a.x = fmaf(f, v.x + bw, a.x);
+                a.y = fmaf(f, v.y + bw, a.y);
+                a.z = fmaf(f, v.z + bw, a.z);
+                a.w = fmaf(f, v.w + bw, a.w);
+            }
+            if (whole) {
+                const float r = s_den[i] == 0.f ? 0.f : 1.f / s_den[i];
+                const int rr = rg * NQ + i;
+                uint2 *dst = reinterpret_cast<uint2 *>(
+                    p.out + ((int64_t)(sq.first + rr / p.rep) * p.Hq + hk * p.rep + rr % p.rep) * D);
+                dst[c4] = make_uint2(pack_bf16(a.x * r, a.y * r), pack_bf16(a.z * r, a.w * r));
+            } else {
+                reinterpret_cast<float4 *>(part + i * (D + 4))[c4] = a;
+            }
+        }
+        if (!whole) {
+            // a piece that starts here and goes on: the CTA that holds its end
+            if (ta == 0 && threadIdx.x == 0) {
+                const int64_t last = at + (int64_t)(seg + 1) * sq.nt - 1;
+                int c = (int)((double)last / (double)total * ctas);
+                c = min(max(c, cta), ctas - 1);
+                while (c > cta && pg_start(total, c, ctas) > last) --c;
+                while (c + 1 < ctas && pg_start(total, c + 1, ctas) <= last) ++c;
+                p.desc[cta] = make_int4(b, seg, 2 * cta + piece, c);
+            }
+        }
+        piece = 1;
+        cur = at + (int64_t)seg * sq.nt + tb;
+        __syncthreads();  // the ring is free again
+    }
+}
+
+// Joins the pieces of a (sequence, KV head, row block) that the cut spread
+// over several CTAs: piece i's output, max m_i and sum l_i give
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Block (c, row): the
+// piece that started in CTA c, its continuations are the first pieces of the
+// CTAs up to desc.w.  Threads take four dimensions each and every
+// (256 / (D/4))-th piece.
+template <int D, int NQ>
+__global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
+    constexpr int C4 = D / 4, NG = 256 / C4;
+    __shared__ float s_w[kPgMaxCtas];
+    __shared__ float s_red[8], s_red2[8];
+    __shared__ float4 s_o[NG][C4];
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    pdl_wait_primary();
+    const int c = blockIdx.x, i = blockIdx.y;
+    const int4 d = p.desc[c];
+    if (d.x < 0) return;
+    const PgSeq s = pg_seq<NQ>(p, d.x);
+    const int hk = d.y / s.nrg, rg = d.y % s.nrg;
+    if (i >= min(NQ, s.rows - rg * NQ)) return;
+    const int n = d.w - c + 1;
+    auto piece = [&](int k) {
+        const int slot = k == 0 ? d.z : 2 * (c + k);
+        return p.part + ((int64_t)slot * NQ + i) * (D + 4);
+    };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    float mx = -INFINITY;
+    for (int k = threadIdx.x; k < n; k += 256) {
+        const float m = piece(k)[D];
+        s_w[k] = m;
+        mx = fmaxf(mx, m);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) s_red[warp] = mx;
+    __syncthreads();
+    mx = s_red[0];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) mx = fmaxf(mx, s_red[w]);
+    float den = 0.f;
+    for (int k = threadIdx.x; k < n; k += 256) {
+        const float f = s_w[k] == -INFINITY ? 0.f : ex2(s_w[k] - mx);
+        s_w[k] = f;
+        den += f * piece(k)[D + 1];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane == 0) s_red2[warp] = den;
+    __syncthreads();
+    const int c4 = threadIdx.x % C4, grp = threadIdx.x / C4;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = grp; k < n; k += NG) {
+        const float f = s_w[k];
+        const float4 v = reinterpret_cast<const float4 *>(piece(k))[c4];
+        if (f == 0.f) continue;
+        a.x = fmaf(f, v.x, a.x);
+        a.y = fmaf(f, v.y, a.y);
+        a.z = fmaf(f, v.z, a.z);
+        a.w = fmaf(f, v.w, a.w);
+    }
+    s_o[grp][c4] = a;
+    __syncthreads();
+    if (grp) return;
+    den = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) den += s_red2[w];
+    for (int k = 1; k < NG; ++k) {
+        const float4 v = s_o[k][c4];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+    }
+    const float r = den == 0.f ? 0.f : 1.f / den;
+    const int rr = rg * NQ + i;
+    reinterpret_cast<uint2 *>(
+        p.out + ((int64_t)(s.first + rr / p.rep) * p.Hq + hk * p.rep + rr % p.rep) * D)[c4] =
+        make_uint2(pack_bf16(a.x * r, a.y * r), pack_bf16(a.z * r, a.w * r));
+}
+
+// ---------------------------------------------------------------- host side
+// Row block: the smallest of 8, 16, 32 rows that holds a sequence's rows (16
+// at 256 dimensions, whose accumulators take twice the registers).
+static int pg_nn(int rep, int max_q, int D) {
+    const int64_t rows = (int64_t)rep * max_q;
+    return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
+}
+
+template <int BITS, int D, int NN>
+static int pg_grid(const KvView &kv, int rep) {
+    using L = PgLayout<BITS, D, NN>;
+    const int64_t rows = (int64_t)rep * kv.max_q;
+    const int64_t units = (int64_t)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
+                          (((int64_t)kv.max_kv + kPgStep - 1) / kPgStep);
+    const int64_t full = (int64_t)num_sms() * L::CTAS;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(units, full), kPgMaxCtas));
+}
+
+template <int BITS, int D, int NN>
+static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) {
+    using L = PgLayout<BITS, D, NN>;
+    const void *kfn = reinterpret_cast<const void *>(paged_decode_kernel<BITS, D, NN>);
+    cudaError_t e = allow_smem(kfn, L::BYTES);
+    if (e == cudaSuccess) e = prefer_max_shared(kfn);
+    if (e != cudaSuccess) return e;
+    const int grid = pg_grid<BITS, D, NN>(p.kv, p.rep);
+    p.desc = static_cast<int4 *>(workspace);
+    p.part = reinterpret_cast<float *>(p.desc + kPgMaxCtas);
+    e = launch_pdl(kfn, (unsigned)grid, kPgWarps * kWarp, L::BYTES, st, p);
+    if (e != cudaSuccess) return e;
+    if (grid == 1) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min<int64_t>(L::NQ, (int64_t)p.rep * p.kv.max_q));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, L::NQ>, p);
+}
+
+#define GWA_PG_ALL(X)                                                     \
+    X(4, 64, 1) X(4, 64, 2) X(4, 64, 4) X(4, 128, 1) X(4, 128, 2)         \
+    X(4, 128, 4) X(4, 256, 1) X(4, 256, 2) X(8, 64, 1) X(8, 64, 2)        \
+    X(8, 64, 4) X(8, 128, 1) X(8, 128, 2) X(8, 128, 4) X(8, 256, 1) X(8, 256, 2)
+
+size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {
+    const int rep = Hq / kv.heads, nn = pg_nn(rep, kv.max_q, kv.dim);
+    int grid = 1;
+#define GWA_PG(BB, DD, N) \
+    if (kv.bits == BB && kv.dim == DD && nn == N) grid = pg_grid<BB, DD, N>(kv, rep);
+    GWA_PG_ALL(GWA_PG)
+#undef GWA_PG
+    return kPgMaxCtas * sizeof(int4) + (size_t)grid * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
+}
+
+cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
+                              const KvView &kv, float scale, int causal,
+                              uint16_t *out, void *workspace, int32_t *status,
+                              cudaStream_t st) {
+    PagedParams p{};
+    p.q = q;
+    p.q_stride = q_stride;
+    p.Hq = Hq;
+    p.rep = Hq / kv.heads;
+    p.kv = kv;
+    p.scale = scale;
+    p.causal = causal;
+    p.out = out;
+    p.status = status;
+    const int nn = pg_nn(p.rep, kv.max_q, kv.dim);
+#define GWA_PG(BB, DD, N) \
+    if (kv.bits == BB && kv.dim == DD && nn == N) return launch_pg_t<BB, DD, N>(p, workspace, st);
+    GWA_PG_ALL(GWA_PG)
+#undef GWA_PG
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gwa

@@ -27,11 +27,13 @@ __global__ void __launch_bounds__(256)
     const int64_t step = (int64_t)gridDim.x * blockDim.x;
     float2 v = make_float2(1.0f, 0.0f);
     if (e < entries)
-        v = rope_cos_sin(positions[e / half], (int)(e % half), r);
+        v = rope_cos_sin(positions ? positions[e / half] : (int)(e / half),
+                         (int)(e % half), r);
     pdl_wait_primary();
     if (e < entries) cs[e] = v;
     for (e += step; e < entries; e += step)
-        cs[e] = rope_cos_sin(positions[e / half], (int)(e % half), r);
+        cs[e] = rope_cos_sin(positions ? positions[e / half] : (int)(e / half),
+                             (int)(e % half), r);
 }
 
 cudaError_t launch_rope_table(float2 *cs, int64_t M, int head_dim, double r,

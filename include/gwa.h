@@ -298,6 +298,162 @@ int gwa_quantize_affine(const uint16_t *w, int64_t N, int64_t K, int32_t bits,
                         int32_t group, uint32_t *wq, uint16_t *scales,
                         uint16_t *biases, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Serving: a paged KV cache, attention over it, and sampling.
+ *
+ * The cache holds keys and values in the affine format of this library along
+ * the head dimension, in pages of page_size tokens ("Sanctum-MLX",
+ * six-changes table row 5 and "File map": the 4-bit cache of the pages, which
+ * quantize values only and give no paging).
+ *   kq, vq  uint32 [num_pages, heads, page_size, head_dim*bits/32]: codes,
+ *           lowest bits first
+ *   kp, vp  bf16   [num_pages, heads, page_size, head_dim/64, 2]: (scale,
+ *           bias) per 64 dimensions; x = scale * code + bias
+ * head_dim 64, 128 or 256; bits 4 or 8; group 64; page_size a power of two,
+ * 16 .. 4096.  All four 16-byte aligned, owned by the caller. */
+typedef struct gwa_kv_cache {
+    uint32_t *kq;
+    uint16_t *kp;
+    uint32_t *vq;
+    uint16_t *vp;
+    int64_t num_pages;
+    int32_t heads; /* KV heads */
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t bits;
+    int32_t group;
+} gwa_kv_cache;
+
+/* A batch of `batch` sequences with `tokens` new tokens among them.  The
+ * three arrays lie on the device and are read there when the work runs; the
+ * other fields are host values.
+ *   q_start     int32 [batch + 1], non-decreasing: sequence b's new tokens
+ *               are rows [q_start[b], q_start[b+1]) of the token arrays
+ *   kv_len      int32 [batch]: its length in the cache, new tokens included;
+ *               new token i of n sits at position kv_len - n + i
+ *   page_table  int32 [batch, max_pages]: position t lies in page
+ *               page_table[b][t / page_size], slot t mod page_size; entries
+ *               past the last used page are not read
+ *   max_q       the most new tokens that one sequence has (a sequence with
+ *               more has only its first max_q rows computed)
+ *   max_kv      the longest kv_len, or more: sizes the launch, no result
+ *               depends on it
+ * Any value may be zero.  Lengths beyond max_pages * page_size are cut to it;
+ * a token row that belongs to no sequence, or whose position is negative,
+ * has no place in the cache.  `status` (NULL, or a device int32 that the
+ * caller clears) collects by atomic OR: 1 a page number outside [0,
+ * num_pages) or a position past the table; 2 a position past the rotary
+ * table.  What belongs to such a token is not written, a sequence that reads
+ * such a page gives unspecified values; no address out of range is formed. */
+typedef struct gwa_kv_batch {
+    const int32_t *q_start;
+    const int32_t *kv_len;
+    const int32_t *page_table;
+    int32_t batch;
+    int32_t max_pages;
+    int64_t tokens;
+    int32_t max_q;
+    int32_t max_kv;
+} gwa_kv_batch;
+
+/* gwa_rope_table -- table[p][i] = (cos, sin) of p * base^(-2i/rot_dim), fp32
+ * [n, rot_dim/2, 2], positions 0 .. n-1: the angles of gwa_qmv_qkv_rope
+ * (formed in fp64), made once for a model.  A caller may fill such a table
+ * itself for another frequency rule.  rot_dim even, 2..256; base > 0; table
+ * 8-byte aligned (16 for gwa_kv_append). */
+int gwa_rope_table(float *table, int64_t n, int32_t rot_dim, double base,
+                   void *stream);
+
+/* gwa_kv_append -- writes the batch's new keys and values into the cache, the
+ * rotary embedding applied on the way ("The Cathedral Doubled Itself", "The
+ * trap that ate three hours": RoPE per head at the cache offset).  Per new
+ * token at position p and key head: dimensions [0, rot_dim) are rotated,
+ *   (x[i], x[i + r/2]) -> (x[i] cos - x[i + r/2] sin,
+ *                          x[i + r/2] cos + x[i] sin),  r = rot_dim,
+ * with table row p, in fp32, and rounded to bf16; then each 64 dimensions are
+ * quantized by the rule of gwa_quantize_affine.  So the cache holds exactly
+ * what rotating into a bf16 buffer and quantizing that gives.  Values are
+ * quantized without rotation.  Finite inputs only.
+ *   q         NULL (Hq = 0), or bf16 [tokens, Hq, head_dim]: queries, rotated
+ *             the same way into q_out, contiguous [tokens, Hq, head_dim]
+ *             (q_out may be q itself if q is contiguous)
+ *   k, v      bf16 [tokens, heads, head_dim]
+ *   *_stride  elements from one token to the next, a multiple of 8, at least
+ *             a token's elements (views of one fused projection's rows)
+ *   rope      fp32 [rope_rows, rot_dim/2, 2] (cos, sin); rot_dim a multiple
+ *             of 16, 0 .. head_dim; 0 rotates nothing (keys that come from
+ *             gwa_qmv_qkv_rope are rotated already) and rope may be NULL
+ * All tensors 16-byte aligned.  No two new tokens may share a slot.  Errors:
+ * GWA_ERR_UNSUPPORTED (head_dim, bits, group, page_size, rot_dim),
+ * GWA_ERR_INVALID_ARG, GWA_ERR_MISALIGNED; nothing is enqueued on error. */
+int gwa_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_out,
+                  int32_t Hq, const uint16_t *k, int64_t k_stride,
+                  const uint16_t *v, int64_t v_stride, gwa_kv_cache cache,
+                  gwa_kv_batch batch, const float *rope, int64_t rope_rows,
+                  int32_t rot_dim, int32_t *status, void *stream);
+
+/* gwa_kv_read -- the values that the cache holds for the batch's tokens, k
+ * and v bf16 [tokens, heads, head_dim] contiguous, 16-byte aligned: scale *
+ * code + bias rounded to fp32 and then to bf16; zeros for a token without a
+ * place in the cache.  With n = kv_len new tokens it reads a whole sequence
+ * (to move it, or to check it). */
+int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
+                uint16_t *v, int32_t *status, void *stream);
+
+/* gwa_sdpa_paged -- softmax attention of the batch's new tokens over the
+ * cache (which already holds them), keys and values dequantized inline
+ * ("Sanctum-MLX", six-changes table row 5 and the paragraph after it: fp32
+ * online softmax, causal mask, GQA without copies).
+ *   out[i,h,:] = sum_t p_t v[t,h',:],  p = softmax_t(scale * q[i,h,:] .
+ *   k[t,h',:]), h' = h / (Hq / heads), over t < kv_len (causal: t <= the
+ *   token's own position).  A row that sees no key (kv_len = 0, or a negative
+ *   position) is zero.
+ *   q    bf16 [tokens, Hq, head_dim], q_stride elements from token to token
+ *        (a multiple of 8), 16-byte aligned
+ *   out  bf16 [tokens, Hq, head_dim] contiguous, 16-byte aligned; rows that
+ *        belong to no sequence are not written
+ *   Hq a multiple of cache.heads; scale finite, usually 1/sqrt(head_dim).
+ *   workspace  >= gwa_sdpa_paged_workspace_bytes(...) for the same cache
+ *        shape and batch bounds, 16-byte aligned; its contents are scratch.
+ * Masked keys take no part whatever they hold (NaN and infinities included).
+ * Softmax state and sums are fp32; weights times value scales enter the value
+ * product rounded to fp16, queries are exact in fp16 within 2^24 of their
+ * row's largest element.  Errors as gwa_kv_append, and GWA_ERR_WORKSPACE. */
+int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                   gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                   int32_t causal, uint16_t *out, void *workspace,
+                   size_t workspace_bytes, int32_t *status, void *stream);
+size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
+                                      gwa_kv_batch batch);
+
+/* gwa_sample -- one token a row from logits, by a given random number.
+ *   logits       [rows, V], bf16 (dtype GWA_BF16) or fp32 (GWA_FP32), aligned
+ *                to their element; row_stride elements from row to row
+ *   u            fp32 [rows]: uniform in [0, 1)
+ *   temperature  fp32 [rows] (NULL: 1); not above zero: the largest logit,
+ *                lowest index first, with probability 1
+ *   top_k        int32 [rows] (NULL, or <= 0, or >= V: off)
+ *   top_p        fp32 [rows] (NULL, or not below 1: off)
+ *   min_p        fp32 [rows] (NULL, or not above 0: off)
+ *   token        int32 [rows]; prob NULL or fp32 [rows]: the token's share of
+ *                the kept tokens' probability
+ * Masses are whole numbers, w_i = floor(2^40 exp2f((x_i - max) * c)), c =
+ * (1/T) * log2(e) in fp32.  Tokens are ordered by logit, largest first, equal
+ * ones by index.  Kept are: the first top_k; of those the shortest prefix
+ * whose mass reaches floor(top_p * the mass of those), at least one token; of
+ * those the tokens of at least min_p of the largest mass.  Drawn is the first
+ * kept token, by index, at which the running mass passes floor(u * the kept
+ * mass).  The result does not depend on how the work is split.  NaN logits
+ * count as -inf, which is never drawn; +inf logits share everything; a row of
+ * -inf alone gives token -1, probability 0.
+ *   1 <= V <= 524288.  Errors: GWA_ERR_INVALID_ARG, GWA_ERR_MISALIGNED,
+ * GWA_ERR_UNSUPPORTED (dtype, V); nothing is enqueued on error. */
+enum { GWA_BF16 = 0, GWA_FP32 = 1 };
+int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
+               int64_t row_stride, const float *u, const float *temperature,
+               const int32_t *top_k, const float *top_p, const float *min_p,
+               int32_t *token, float *prob, void *stream);
+
 /* Text of the last error raised on this thread ("" if none). */
 const char *gwa_last_error(void);
 
