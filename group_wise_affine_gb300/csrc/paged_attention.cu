@@ -8,15 +8,17 @@
 //   p = softmax_t(scale * q[i,h,:] . (sk_t ck_t + bk_t)),
 //
 // with codes c, and scale s and bias b per token, head and 64 dimensions.
-// Codes enter the tensor cores as they are, centred: c - 8 (u4) or c - 128
-// (u8) is exact in fp16, and the affine map folds into what is already
-// there:
+// Codes enter the tensor cores as they are, fp16 subnormals c 2^-24 (masked
+// out of the words, nothing else), and the affine map folds into what is
+// already there:
 //   scores  S^T = C_k Q^T    per 64 dimensions, fp32; then
-//           x = sum_g s_g S_g + b'_g sum(Q_g),  b' = b + 8 s (128 s);
-//   values  O^T += C_v^T P'^T  with P' = p * s in fp16, plus sum_t p_t b'_t.
-// Centred codes keep the sums small: with c (0..15) or an offset of 1024
-// left in, an output that averages thousands of values would be the small
-// difference of two large sums.  fp16 holds P' to 2^-12, bf16 only to 2^-9.
+//           x = sum_g s_g S_g + b_g sum(Q_g);
+//   values  O^T += (C_v - c0)^T P'^T  with P' = p * s in fp16, plus
+//           sum_t p_t b'_t, b' = b + c0 s, c0 = 8 (u4) or 128 (u8).
+// The centre c0 comes off by an MMA with a constant operand just before each
+// tile's codes: with it left in, an output that averages thousands of values
+// would be the small difference of two large sums (scores are summed afresh
+// for each tile and need none).  fp16 holds P' to 2^-12, bf16 only to 2^-9.
 // Its range is met by powers of two: a query row is scaled so that its
 // largest element lies in [2^12, 2^13), and the value scales so that the
 // largest met so far lies in [2^5, 2^6) (the accumulators are rescaled when a
@@ -32,17 +34,16 @@
 // the split depends on host values but the grid.
 //
 // A warp takes 32 of the step's 128 keys (two MMA tiles of 16), copies their
-// codes and parameters with cp.async into its own ring some steps ahead, and
+// codes and parameters with cp.async into its own ring two steps ahead, and
 // keeps its own softmax state; the four warps merge in shared memory at the
-// end of a piece.  The ring's rows are laid out by 64-dimension group so
-// that the fragment reads hit every bank once.  The order of keys inside a
-// tile is permuted (row j of the scores is key (j >> 1) + 4 (j & 1)), which
-// makes the value fragments' reads contiguous.
+// end of a piece.  (Bulk copies ran slower: pages of 16 tokens make them 1 KB
+// and 64 to 128 bytes long, about 22 cycles of an SM each whatever their size.)
 //
 // Warp-level MMAs (m16n8k16) serve here: with 1 to 32 query rows the work is
 // bound by the bytes of the cache and by unpacking codes, and their operands
 // live in registers beside the unpacking; a tcgen05 MMA has at least 64 rows.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -69,7 +70,11 @@ struct PagedParams {
     int32_t *status;
 };
 
-// Shared memory of one warp's ring stage (32 keys: two tiles of 16).
+// Shared memory of one warp's ring stage (32 keys: two tiles of 16).  A
+// tile's codes are laid out [group][row][GB bytes], so that the fragment
+// reads hit every bank once: key rows in the order of the scores' rows, value
+// rows in key order (8-bit rows with their two halves swapped in every other
+// pair of rows).
 template <int BITS, int D, int NN>
 struct PgLayout {
     static constexpr int G = D / 64;
@@ -86,11 +91,14 @@ struct PgLayout {
     static constexpr int MERGE = NQ * D * 4;     // a warp's output rows
     static constexpr int WARP_BYTES = S * STAGE > MERGE ? S * STAGE : MERGE;
     static constexpr int BYTES = kPgWarps * WARP_BYTES;
-    static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 4096);
+    static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 1024 + kPgWarps * NQ * (12 + 4 * G) + 4 * NQ);
     // accumulators, queries and fragments: about 96 + 4 registers per 8 rows
     // and 16 dimensions
-    static constexpr int BY_REGS = NN * D <= 128 ? 4 : NN * D <= 256 ? 3 : 2;
+    static constexpr int BY_REGS = NN * D < 128 ? 4 : NN * D <= 256 ? 3 : 2;
     static constexpr int CTAS = BY_SMEM < BY_REGS ? (BY_SMEM < 1 ? 1 : BY_SMEM) : BY_REGS;
+    // key of score row j (0..7; row j + 8: 8 more); the value product's k
+    // positions 2t, 2t + 1, 2t + 8, 2t + 9 are then keys t, t + 4, t + 8, t + 12
+    static __device__ __forceinline__ int key_of_row(int j) { return (j >> 1) + 4 * (j & 1); }
 };
 
 // Keys that some row of the sequence sees, in steps; row blocks; units.
@@ -117,34 +125,35 @@ __device__ __forceinline__ int64_t pg_start(int64_t total, int c, int ctas) {
     return total / ctas * c + total % ctas * c / ctas;
 }
 
+// Sixteen codes of one key row as the fp16 pairs the MMA takes.  A code left
+// in the low mantissa bits of a zero exponent is the fp16 subnormal c 2^-24,
+// exact and linear, so unpacking is masking alone.  u4 fields at bits 4-7
+// are 16 c 2^-24: the queries they meet are divided by 16 (k_sixteenth).
 template <int BITS>
 __device__ __forceinline__ void k_fragments(const unsigned char *src, uint32_t (&f)[8]) {
-    // sixteen centred codes of one key row, as the pairs the MMA takes
     if constexpr (BITS == 4) {
         const uint2 w = *reinterpret_cast<const uint2 *>(src);
-        const __half2 off = __floats2half2_rn(1032.f, 1032.f);
-        const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
-        const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t u = j ? w.y : w.x, u8 = u >> 8;
-            // fields at bits 0 and 16: 1024 + c; at 4 and 20: 1024 + 16 c
-            f[4 * j + 0] = h2_bits(__hsub2(bits_h2((u & 0x000f000fu) | 0x64006400u), off));
-            f[4 * j + 1] = h2_bits(__hfma2(bits_h2((u & 0x00f000f0u) | 0x64006400u), r16, m72));
-            f[4 * j + 2] = h2_bits(__hsub2(bits_h2((u8 & 0x000f000fu) | 0x64006400u), off));
-            f[4 * j + 3] = h2_bits(__hfma2(bits_h2((u8 & 0x00f000f0u) | 0x64006400u), r16, m72));
+            f[4 * j + 0] = u & 0x000f000fu;
+            f[4 * j + 1] = u & 0x00f000f0u;
+            f[4 * j + 2] = u8 & 0x000f000fu;
+            f[4 * j + 3] = u8 & 0x00f000f0u;
         }
     } else {
         const uint4 w = *reinterpret_cast<const uint4 *>(src);
-        const __half2 off = __floats2half2_rn(1152.f, 1152.f);
         const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f[2 * j] = h2_bits(__hsub2(bits_h2((ws[j] & 0x00ff00ffu) | 0x64006400u), off));
-            f[2 * j + 1] =
-                h2_bits(__hsub2(bits_h2(((ws[j] >> 8) & 0x00ff00ffu) | 0x64006400u), off));
+            f[2 * j] = ws[j] & 0x00ff00ffu;
+            f[2 * j + 1] = (ws[j] >> 8) & 0x00ff00ffu;
         }
     }
+}
+template <int BITS>
+__device__ __forceinline__ constexpr bool k_sixteenth(int i) {
+    return BITS == 4 && i % 2 == 1;
 }
 
 // Dimension, within its lane's sixteen, of element e of pair i as
@@ -172,9 +181,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     constexpr int NT = D / 16;                  // value m-tiles
     constexpr int NCP = L::TILE / 16 / kWarp;   // 16-byte copies per lane, tile
     constexpr int RCH = G * GB / 16;            // 16-byte chunks of a key row
+    static_assert(NCP >= 1, "tile copies");
     constexpr float KC = BITS == 4 ? 8.f : 128.f;
     constexpr unsigned FULL = 0xffffffffu;
-    static_assert(NCP >= 1, "tile copies");
     extern __shared__ __align__(16) unsigned char pg_smem[];
     __shared__ float s_m[kPgWarps][NQ], s_l[kPgWarps][NQ], s_f[kPgWarps][NQ];
     __shared__ float s_b[kPgWarps][NQ][G];
@@ -182,8 +191,19 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 
     const int lane = threadIdx.x & (kWarp - 1), warp = threadIdx.x / kWarp;
     const int g = lane >> 2, t = lane & 3;
-    const int kv_g = (g >> 1) + 4 * (g & 1);    // the key of score row g
+    const int kv_g = L::key_of_row(g);
     unsigned char *wsm = pg_smem + warp * L::WARP_BYTES;
+    // the lane's 16-byte copies of a tile: where they go
+    int kdst[NCP], vdst[NCP];
+#pragma unroll
+    for (int i = 0; i < NCP; ++i) {
+        const int ci = lane + 32 * i, r = ci / RCH, rem = ci % RCH;
+        const int gg = rem / (GB / 16), ch = rem % (GB / 16);
+        const int kr = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
+        const int vch = BITS == 8 ? ch ^ (((r >> 1) & 1) << 1) : ch;
+        kdst[i] = L::K_OFF + (gg * 16 + kr) * GB + ch * 16;
+        vdst[i] = L::V_OFF + (gg * 16 + r) * GB + vch * 16;
+    }
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait_primary();
 
@@ -235,7 +255,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     int64_t cur = begin;
     int piece = 0;
     const float sl2 = p.scale * 1.4426950408889634f;  // scores in base 2
-    constexpr float kLazy = 8.f;
+    // The running maximum moves only when a weight passes 2^8 (weights and
+    // their sums stay far inside fp32 and fp16), or from nothing: kNone makes
+    // the first weight infinite.
+    constexpr float kLazy = 256.f, kNone = -3e38f;
     const int pmask = (1 << p.kv.page_shift) - 1;
 
     while (cur < end) {
@@ -291,7 +314,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 for (int i = 0; i < 8; ++i) {
                     const float a = elem(gg, k_dim<BITS>(i, 0)) * up;
                     const float c = elem(gg, k_dim<BITS>(i, 1)) * up;
-                    qf[nn][gg][i] = pack_f16(a, c);
+                    constexpr float r16 = 0.0625f;
+                    qf[nn][gg][i] = k_sixteenth<BITS>(i) ? pack_f16(a * r16, c * r16)
+                                                         : pack_f16(a, c);
                     sum[gg] += a + c;
                 }
                 sum[gg] += __shfl_xor_sync(FULL, sum[gg], 1);
@@ -301,9 +326,11 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int from = (2 * t + h) * 4;
-                fac[nn][h] = __shfl_sync(FULL, down, from) * sl2;
+                // scores stay times 2^-24, as the codes are
+                fac[nn][h] = __shfl_sync(FULL, down, from) * sl2 * 0x1p24f;
 #pragma unroll
-                for (int gg = 0; gg < G; ++gg) qs[nn][gg][h] = __shfl_sync(FULL, sum[gg], from);
+                for (int gg = 0; gg < G; ++gg)
+                    qs[nn][gg][h] = __shfl_sync(FULL, sum[gg], from) * 0x1p-24f;
                 const int i = 8 * nn + 2 * t + h, rr = rg * NQ + i;
                 lim[nn][h] = i >= nlive ? 0
                              : p.causal ? min(sq.len, sq.len - sq.count + rr / p.rep + 1)
@@ -330,7 +357,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 o[nn][j][0] = o[nn][j][1] = o[nn][j][2] = o[nn][j][3] = 0.f;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                m[nn][h] = -INFINITY;
+                m[nn][h] = kNone;
                 l[nn][h] = 0.f;
 #pragma unroll
                 for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] = 0.f;
@@ -338,211 +365,100 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         }
         float vinv = 1.f, vlim = -1.f;  // value scales: times vinv, met up to vlim
 
-        // page ids of the tiles of 16 steps: lane 2 j + u holds step j's tile u
-        int pages = 0, pages_at = -1;
-        auto issue = [&](int step) {  // step in [ta, tb)
-            if (pages_at < 0 || step - pages_at >= 16) {
+        // Page numbers of the tiles of 16 steps: lane 2 j + u holds those of
+        // step j's tile u.
+        int pages = 0, pages_at = ta - 16;
+        auto issue = [&](int step, int to) {
+            if (step - pages_at >= 16) {
                 pages_at = step;
                 const int key = (step + (lane >> 1)) * kPgStep + warp * kPgKeys + (lane & 1) * 16;
-                const int j = key >> p.kv.page_shift;
                 pages = 0;
-                if (key < sq.len && j < p.kv.max_pages) {
-                    pages = table[j];
-                    if (pages < 0 || pages >= p.kv.num_pages) {
+                if (step + (lane >> 1) < tb && key < sq.len) {
+                    pages = table[key >> p.kv.page_shift];
+                    if ((unsigned)pages >= (unsigned)p.kv.num_pages) {
                         if (p.status) atomicOr(p.status, (int)kKvBadPage);
                         pages = 0;
                     }
                 }
             }
-            unsigned char *st = wsm + ((step - ta) % S) * L::STAGE;
+            unsigned char *st = wsm + to * L::STAGE;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int page = __shfl_sync(FULL, pages, 2 * (step - pages_at) + u);
                 const int key = step * kPgStep + warp * kPgKeys + u * 16;
-                if (key >= sq.len) continue;
+                if (key >= sq.len) break;  // warp-uniform
                 const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
                                     (key & pmask);
-                const uint4 *ks = reinterpret_cast<const uint4 *>(p.kv.kq + row * (D * BITS / 32));
-                const uint4 *vs = reinterpret_cast<const uint4 *>(p.kv.vq + row * (D * BITS / 32));
+                const uint4 *ks = reinterpret_cast<const uint4 *>(p.kv.kq) + row * RCH + lane;
+                const uint4 *vs = reinterpret_cast<const uint4 *>(p.kv.vq) + row * RCH + lane;
 #pragma unroll
                 for (int i = 0; i < NCP; ++i) {
-                    const int ci = lane + 32 * i;
-                    const int r = ci / RCH, rem = ci % RCH;
-                    const int gg = rem / (GB / 16), ch = rem % (GB / 16);
-                    const int kr = (r & 8) | ((r & 3) << 1) | ((r >> 2) & 1);
-                    const int vch = BITS == 8 ? ch ^ (((r >> 1) & 1) << 1) : ch;
-                    cp_async<16>(st + L::K_OFF + u * L::TILE + (gg * 16 + kr) * GB + ch * 16, ks + ci);
-                    cp_async<16>(st + L::V_OFF + u * L::TILE + (gg * 16 + r) * GB + vch * 16, vs + ci);
+                    cp_async<16>(st + kdst[i] + u * L::TILE, ks + 32 * i);
+                    cp_async<16>(st + vdst[i] + u * L::TILE, vs + 32 * i);
                 }
                 // parameters: lanes below 4 G the keys', the next 4 G the values'
                 if (lane < 8 * G) {
-                    const int i = lane % (4 * G);
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        (lane < 4 * G ? p.kv.kp : p.kv.vp) + row * G);
-                    cp_async<16>(st + (lane < 4 * G ? L::KP_OFF : L::VP_OFF) + u * L::PB + i * 16,
-                                 src + i);
+                    const bool is_k = lane < 4 * G;
+                    const int i = is_k ? lane : lane - 4 * G;
+                    cp_async<16>(st + (is_k ? L::KP_OFF : L::VP_OFF) + u * L::PB + i * 16,
+                                 (is_k ? p.kv.kp : p.kv.vp) + row * G + 4 * i);
                 }
             }
         };
+        // One step of 32 keys.  EDGE: some row does not see all of them.
+        auto compute = [&](const unsigned char *stg, const int key0, auto edge_t) {
+            constexpr bool EDGE = decltype(edge_t)::value;
+            // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + HALF kk + kv_g,
+            // less the factor fac of the column
+            float x[2][2][NN][2];
+            float sv[2][2][G], bv[2][2][G];
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) {
-            if (ta + i < tb) issue(ta + i);
-            cp_async_commit();
-        }
-        for (int step = ta; step < tb; ++step) {
-            if (step + S - 1 < tb) issue(step + S - 1);
-            cp_async_commit();
-            cp_async_wait<S - 1>();
-            __syncwarp();
-            const unsigned char *stg = wsm + ((step - ta) % S) * L::STAGE;
-            const int key0 = step * kPgStep + warp * kPgKeys;
-            if (key0 < sq.len) {  // warp-uniform
-                // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + 8 kk + kv_g
-                float x[2][2][NN][2];
-                float sv[2][2][G], bv[2][2][G];
-                float lm[NN][2], smax = 0.f;
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
-                for (int nn = 0; nn < NN; ++nn) lm[nn][0] = lm[nn][1] = -INFINITY;
+                for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float acc[NN][2][2];
+                    for (int nn = 0; nn < NN; ++nn) x[u][kk][nn][0] = x[u][kk][nn][1] = 0.f;
+                const unsigned char *kt = stg + L::K_OFF + u * L::TILE + g * GB + t * 2 * BITS;
+                const unsigned char *kp = stg + L::KP_OFF + u * L::PB + kv_g * G * 4;
+                const unsigned char *vp = stg + L::VP_OFF + u * L::PB + kv_g * G * 4;
 #pragma unroll
-                    for (int nn = 0; nn < NN; ++nn)
-                        acc[nn][0][0] = acc[nn][0][1] = acc[nn][1][0] = acc[nn][1][1] = 0.f;
-#pragma unroll
-                    for (int gg = 0; gg < G; ++gg) {
-                        const unsigned char *ks =
-                            stg + L::K_OFF + u * L::TILE + (gg * 16 + g) * GB + t * 2 * BITS;
-                        uint32_t f0[8], f1[8];
-                        k_fragments<BITS>(ks, f0);
-                        k_fragments<BITS>(ks + 8 * GB, f1);
-                        const uint32_t p0 = *reinterpret_cast<const uint32_t *>(
-                            stg + L::KP_OFF + u * L::PB + (kv_g * G + gg) * 4);
-                        const uint32_t p1 = *reinterpret_cast<const uint32_t *>(
-                            stg + L::KP_OFF + u * L::PB + ((kv_g + 8) * G + gg) * 4);
-                        const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
-                        const float b0 = fmaf(KC, s0, bf16_hi(p0));
-                        const float b1 = fmaf(KC, s1, bf16_hi(p1));
-#pragma unroll
-                        for (int nn = 0; nn < NN; ++nn) {
-                            float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2)
-                                mma_f16(c, f0[i], f1[i], f0[i + 1], f1[i + 1], qf[nn][gg][i],
-                                        qf[nn][gg][i + 1]);
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                acc[nn][0][h] = fmaf(s0, c[h], fmaf(b0, qs[nn][gg][h], acc[nn][0][h]));
-                                acc[nn][1][h] = fmaf(s1, c[2 + h], fmaf(b1, qs[nn][gg][h], acc[nn][1][h]));
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                        for (int gg = 0; gg < G; ++gg) {
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                                stg + L::VP_OFF + u * L::PB + ((kv_g + 8 * kk) * G + gg) * 4);
-                            sv[u][kk][gg] = bf16_lo(w);
-                            bv[u][kk][gg] = fmaf(KC, bf16_lo(w), bf16_hi(w));
-                        }
-#pragma unroll
-                        for (int nn = 0; nn < NN; ++nn)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                x[u][kk][nn][h] = acc[nn][kk][h] * fac[nn][h];
-                    }
-                }
-                const bool edge = key0 + kPgKeys > all;
-                if (edge) {
-                    // keys that a row does not see: no score, and no parameter
-                    // (which may be anything) of a key that no row sees
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const int key = key0 + 16 * u + 8 * kk + kv_g;
-#pragma unroll
-                            for (int nn = 0; nn < NN; ++nn)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    if (key >= lim[nn][h]) x[u][kk][nn][h] = -INFINITY;
-                            if (key >= sq.len)
-#pragma unroll
-                                for (int gg = 0; gg < G; ++gg) sv[u][kk][gg] = bv[u][kk][gg] = 0.f;
-                        }
-                }
-                bool raise = false;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                        for (int gg = 0; gg < G; ++gg) smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
-#pragma unroll
-                        for (int nn = 0; nn < NN; ++nn)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                lm[nn][h] = fmaxf(lm[nn][h], x[u][kk][nn][h]);
-                    }
-                raise = smax > vlim;
-#pragma unroll
-                for (int nn = 0; nn < NN; ++nn)
-                    raise |= lm[nn][0] > m[nn][0] + kLazy || lm[nn][1] > m[nn][1] + kLazy;
-                if (__any_sync(FULL, raise)) {
-                    // a new running maximum (weights stay below 2^kLazy), or a
-                    // larger value scale
-                    float vf = 1.f;
-                    if (smax == INFINITY) {
-                        // an infinite scale makes its own readers' rows
-                        // infinite, and must not take the others' range
-                        smax = 0.f;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                                for (int gg = 0; gg < G; ++gg)
-                                    if (fabsf(sv[u][kk][gg]) < INFINITY)
-                                        smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
-                    }
-                    const float top = __uint_as_float(
-                        __reduce_max_sync(FULL, __float_as_uint(fmaxf(smax, 0.f))));
-                    if (top > vlim) {
-                        // 2^e <= top < 2^(e+1): times 2^(5-e)
-                        const int e = min(max(f32_exp_field(top), 6), 253);
-                        const float ninv = __uint_as_float((uint32_t)(259 - e > 254 ? 254 : 259 - e) << 23);
-                        vf = vlim < 0.f ? 1.f : ninv / vinv;
-                        vinv = ninv;
-                        vlim = __uint_as_float((uint32_t)(e + 1) << 23);
-                    }
+                for (int gg = 0; gg < G; ++gg) {
+                    uint32_t f0[8], f1[8];
+                    k_fragments<BITS>(kt + gg * 16 * GB, f0);
+                    k_fragments<BITS>(kt + gg * 16 * GB + 8 * GB, f1);
+                    const uint32_t p0 = *reinterpret_cast<const uint32_t *>(kp + gg * 4);
+                    const uint32_t p1 =
+                        *reinterpret_cast<const uint32_t *>(kp + (8 * G + gg) * 4);
+                    const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
+                    const float b0 = bf16_hi(p0), b1 = bf16_hi(p1);
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn) {
-                        float cr[2];
+                        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            mma_f16(c, f0[i], f1[i], f0[i + 1], f1[i + 1], qf[nn][gg][i],
+                                    qf[nn][gg][i + 1]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float mt = lm[nn][h];
-#pragma unroll
-                            for (int off = 4; off < kWarp; off <<= 1)
-                                mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, off));
-                            const float mn = fmaxf(m[nn][h], mt);
-                            cr[h] = mn == -INFINITY ? 1.f : ex2(m[nn][h] - mn);
-                            m[nn][h] = mn;
-                            l[nn][h] *= cr[h];
-#pragma unroll
-                            for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] *= cr[h];
-                            cr[h] *= vf;
-                        }
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            o[nn][j][0] *= cr[0];
-                            o[nn][j][1] *= cr[1];
-                            o[nn][j][2] *= cr[0];
-                            o[nn][j][3] *= cr[1];
+                            x[u][0][nn][h] = fmaf(s0, c[h], fmaf(b0, qs[nn][gg][h], x[u][0][nn][h]));
+                            x[u][1][nn][h] = fmaf(s1, c[2 + h], fmaf(b1, qs[nn][gg][h], x[u][1][nn][h]));
                         }
                     }
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                            vp + (8 * kk * G + gg) * 4);
+                        sv[u][kk][gg] = bf16_lo(w);
+                        bv[u][kk][gg] = fmaf(KC, bf16_lo(w), bf16_hi(w));
+                        // past the end lie no parameters (but anything)
+                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= sq.len)
+                            sv[u][kk][gg] = bv[u][kk][gg] = 0.f;
+                    }
                 }
-                // ---- weights
+            }
+            // ---- weights, against the maximum so far
+            float e[2][2][NN][2], emax = 0.f, smax = 0.f;
+            auto weigh = [&] {
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -551,92 +467,186 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                float &e = x[u][kk][nn][h];
-                                e = e == -INFINITY ? 0.f : ex2(e - m[nn][h]);
-                                l[nn][h] += e;
+                                e[u][kk][nn][h] = ex2(fmaf(x[u][kk][nn][h], fac[nn][h], -m[nn][h]));
+                                if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= lim[nn][h])
+                                    e[u][kk][nn][h] = 0.f;
                             }
-                // ---- values
+            };
+            weigh();
 #pragma unroll
-                for (int gg = 0; gg < G; ++gg) {
-                    uint32_t pb[2][NN][2];
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                    for (int gg = 0; gg < G; ++gg) smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
+#pragma unroll
+                    for (int nn = 0; nn < NN; ++nn)
+                        emax = fmaxf(emax, fmaxf(e[u][kk][nn][0], e[u][kk][nn][1]));
+                }
+            if (__any_sync(FULL, emax > kLazy || smax > vlim)) {
+                // a new maximum, or a larger value scale
+                float vf = 1.f;
+                if (smax == INFINITY) {
+                    // an infinite scale makes its own readers' rows infinite,
+                    // and must not take the others' range
+                    smax = 0.f;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const float s = sv[u][kk][gg] * vinv, bb = bv[u][kk][gg];
+                        for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                            for (int nn = 0; nn < NN; ++nn) {
-                                const float e0 = x[u][kk][nn][0], e1 = x[u][kk][nn][1];
-                                float a0 = e0 * s, a1 = e1 * s;
-                                float c0 = e0 * bb, c1 = e1 * bb;
-                                if (edge) {  // a weight of zero takes nothing, whatever s and b
-                                    a0 = e0 == 0.f ? 0.f : a0;
-                                    a1 = e1 == 0.f ? 0.f : a1;
-                                    c0 = e0 == 0.f ? 0.f : c0;
-                                    c1 = e1 == 0.f ? 0.f : c1;
-                                }
-                                bs[nn][gg][0] += c0;
-                                bs[nn][gg][1] += c1;
-                                pb[u][nn][kk] = movmatrix_t(pack_f16(a0, a1));
+                            for (int gg = 0; gg < G; ++gg)
+                                if (fabsf(sv[u][kk][gg]) < INFINITY)
+                                    smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
+                }
+                const float top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
+                if (top > vlim) {
+                    // 2^ex <= top < 2^(ex+1): times 2^(5-ex)
+                    const int ex = min(max(f32_exp_field(top), 6), 253);
+                    const float ninv = __uint_as_float((uint32_t)(259 - ex > 254 ? 254 : 259 - ex) << 23);
+                    vf = vlim < 0.f ? 1.f : ninv / vinv;
+                    vinv = ninv;
+                    vlim = __uint_as_float((uint32_t)(ex + 1) << 23);
+                }
+#pragma unroll
+                for (int nn = 0; nn < NN; ++nn) {
+                    float cr[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                if (!EDGE || key0 + 16 * u + 8 * kk + kv_g < lim[nn][h])
+                                    mt = fmaxf(mt, x[u][kk][nn][h] * fac[nn][h]);
+#pragma unroll
+                        for (int off = 4; off < kWarp; off <<= 1)
+                            mt = fmaxf(mt, __shfl_xor_sync(FULL, mt, off));
+                        const float mn = fmaxf(m[nn][h], mt);
+                        cr[h] = ex2(m[nn][h] - mn);
+                        m[nn][h] = mn;
+                        l[nn][h] *= cr[h];
+#pragma unroll
+                        for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] *= cr[h];
+                        cr[h] *= vf;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[nn][j][0] *= cr[0];
+                        o[nn][j][1] *= cr[1];
+                        o[nn][j][2] *= cr[0];
+                        o[nn][j][3] *= cr[1];
+                    }
+                }
+                weigh();
+            }
+#pragma unroll
+            for (int nn = 0; nn < NN; ++nn)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    l[nn][h] += (e[0][0][nn][h] + e[0][1][nn][h]) + (e[1][0][nn][h] + e[1][1][nn][h]);
+            // ---- values
+#pragma unroll
+            for (int gg = 0; gg < G; ++gg) {
+                uint32_t pb[2][NN][2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        const float s = sv[u][kk][gg] * vinv, bb = bv[u][kk][gg];
+#pragma unroll
+                        for (int nn = 0; nn < NN; ++nn) {
+                            const float e0 = e[u][kk][nn][0], e1 = e[u][kk][nn][1];
+                            float a0 = e0 * s, a1 = e1 * s;
+                            if constexpr (EDGE) {  // a weight of zero takes nothing, whatever s and b
+                                a0 = e0 == 0.f ? 0.f : a0;
+                                a1 = e1 == 0.f ? 0.f : a1;
+                                bs[nn][gg][0] += e0 == 0.f ? 0.f : e0 * bb;
+                                bs[nn][gg][1] += e1 == 0.f ? 0.f : e1 * bb;
+                            } else {
+                                bs[nn][gg][0] = fmaf(e0, bb, bs[nn][gg][0]);
+                                bs[nn][gg][1] = fmaf(e1, bb, bs[nn][gg][1]);
+                            }
+                            pb[u][nn][kk] = movmatrix_t(pack_f16(a0, a1));
+                        }
+                    }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int half = BITS == 8 ? (g ^ ((t >> 1) << 2)) * 8 : g * 4;
+                    const unsigned char *vs = stg + L::V_OFF + u * L::TILE + (gg * 16 + t) * GB + half;
+                    // words of the keys at k = 2t, 2t + 1, 2t + 8, 2t + 9
+                    uint32_t w[4][BITS / 4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const unsigned char *src = vs + 4 * i * GB;
+                        if constexpr (BITS == 4) {
+                            w[i][0] = *reinterpret_cast<const uint32_t *>(src);
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                            w[i][0] = v.x;
+                            w[i][1] = v.y;
+                        }
+                    }
+                    // codes as subnormals again, c 2^-24 in rows g and (u4)
+                    // 16 c 2^-24 in rows g + 8; a constant operand takes the
+                    // centre off first, on the same scales
+                    constexpr uint32_t C0 = BITS == 4 ? 0x80088008u : 0x80808080u;
+                    constexpr uint32_t C1 = BITS == 4 ? 0x80808080u : 0x80808080u;
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        uint32_t a[4];
+                        if constexpr (BITS == 4) {
+                            // byte jj: dimensions 8g + 2jj (m-row g), + 1 (g + 8)
+                            const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t r = __byte_perm(w[2 * k][0], w[2 * k + 1][0], sel);
+                                a[2 * k] = r & 0x000f000fu;
+                                a[2 * k + 1] = r & 0x00f000f0u;
+                            }
+                        } else {
+                            const int e2 = 2 * (jj & 1);
+                            const uint32_t sel = e2 | ((e2 + 1) << 4) | ((4 + e2) << 8) | ((5 + e2) << 12);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t r = __byte_perm(w[2 * k][jj / 2], w[2 * k + 1][jj / 2], sel);
+                                a[2 * k] = r & 0x00ff00ffu;
+                                a[2 * k + 1] = (r >> 8) & 0x00ff00ffu;
                             }
                         }
-                    const __half2 off4 = __floats2half2_rn(1032.f, 1032.f);
-                    const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
-                    const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
-                    const __half2 off8 = __floats2half2_rn(1152.f, 1152.f);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const unsigned char *vs = stg + L::V_OFF + u * L::TILE + gg * 16 * GB;
-                        // words of keys t, t + 4 (k = 2t, 2t + 1), t + 8, t + 12
-                        uint32_t w[4][BITS / 4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = t + 4 * i;
-                            if constexpr (BITS == 4) {
-                                w[i][0] = *reinterpret_cast<const uint32_t *>(vs + r * GB + g * 4);
-                            } else {
-                                const uint2 v = *reinterpret_cast<const uint2 *>(
-                                    vs + r * GB + (((g >> 1) ^ (((r >> 1) & 1) << 1)) * 16) +
-                                    (g & 1) * 8);
-                                w[i][0] = v.x;
-                                w[i][1] = v.y;
-                            }
-                        }
-#pragma unroll
-                        for (int jj = 0; jj < 4; ++jj) {
-                            uint32_t a[4];
-                            if constexpr (BITS == 4) {
-                                // byte jj: dimensions 8g + 2jj (m-row g), + 1 (g + 8)
-                                const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint32_t r = __byte_perm(w[2 * k][0], w[2 * k + 1][0], sel);
-                                    a[2 * k] = h2_bits(__hsub2(bits_h2((r & 0x000f000fu) | 0x64006400u), off4));
-                                    a[2 * k + 1] = h2_bits(__hfma2(
-                                        bits_h2((r & 0x00f000f0u) | 0x64006400u), r16, m72));
-                                }
-                            } else {
-                                const int e = 2 * (jj & 1);
-                                const uint32_t sel = e | ((e + 1) << 4) | ((4 + e) << 8) | ((5 + e) << 12);
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint32_t r = __byte_perm(w[2 * k][jj / 2], w[2 * k + 1][jj / 2], sel);
-                                    a[2 * k] = h2_bits(__hsub2(bits_h2((r & 0x00ff00ffu) | 0x64006400u), off8));
-                                    a[2 * k + 1] = h2_bits(__hsub2(
-                                        bits_h2(((r >> 8) & 0x00ff00ffu) | 0x64006400u), off8));
-                                }
-                            }
-#pragma unroll
-                            for (int nn = 0; nn < NN; ++nn)
-                                mma_f16(o[nn][4 * gg + jj], a[0], a[1], a[2], a[3], pb[u][nn][0],
-                                        pb[u][nn][1]);
+                        for (int nn = 0; nn < NN; ++nn) {
+                            mma_f16(o[nn][4 * gg + jj], C0, C1, C0, C1, pb[u][nn][0], pb[u][nn][1]);
+                            mma_f16(o[nn][4 * gg + jj], a[0], a[1], a[2], a[3], pb[u][nn][0],
+                                    pb[u][nn][1]);
                         }
                     }
                 }
             }
-            __syncwarp();  // the stage is free for the next copies
+        };
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            if (ta + i < tb) issue(ta + i, i);
+            cp_async_commit();
         }
-        cp_async_wait<0>();
+        int stage = 0;
+        for (int step = ta; step < tb; ++step) {
+            if (step + S - 1 < tb) issue(step + S - 1, stage == 0 ? S - 1 : stage - 1);
+            cp_async_commit();
+            cp_async_wait<S - 1>();
+            __syncwarp();
+            const int key0 = step * kPgStep + warp * kPgKeys;
+            if (key0 < sq.len) {  // warp-uniform
+                const unsigned char *stg = wsm + stage * L::STAGE;
+                if (key0 + kPgKeys > all)
+                    compute(stg, key0, std::true_type{});
+                else
+                    compute(stg, key0, std::false_type{});
+            }
+            __syncwarp();  // the stage is free for the next copies
+            stage = stage == S - 1 ? 0 : stage + 1;
+        }
 
         // ---- the four warps' states to shared memory, and out
 #pragma unroll
@@ -652,7 +662,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 }
         __syncwarp();
         float *so = reinterpret_cast<float *>(wsm);
-        const float back = 1.f / vinv;  // a power of two
+        // powers of two: the value scales' and the codes' (rows g and g + 8)
+        const float back = 1.f / vinv * 0x1p24f, back1 = BITS == 4 ? back * 0.0625f : back;
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn) {
 #pragma unroll
@@ -660,9 +671,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 const int d = 64 * (j / 4) + 8 * g + 2 * (j % 4);
                 const int r = 8 * nn + 2 * t;
                 *reinterpret_cast<float2 *>(so + r * D + d) =
-                    make_float2(o[nn][j][0] * back, o[nn][j][2] * back);
+                    make_float2(o[nn][j][0] * back, o[nn][j][2] * back1);
                 *reinterpret_cast<float2 *>(so + (r + 1) * D + d) =
-                    make_float2(o[nn][j][1] * back, o[nn][j][3] * back);
+                    make_float2(o[nn][j][1] * back, o[nn][j][3] * back1);
             }
             if (g == 0)
 #pragma unroll
@@ -679,18 +690,18 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         float *part = p.part + (int64_t)(2 * cta + piece) * NQ * (D + 4);
         if (threadIdx.x < NQ) {
             const int i = threadIdx.x;
-            float mx = -INFINITY, den = 0.f;
+            float mx = kNone, den = 0.f;
 #pragma unroll
             for (int w = 0; w < kPgWarps; ++w) mx = fmaxf(mx, s_m[w][i]);
 #pragma unroll
             for (int w = 0; w < kPgWarps; ++w) {
-                const float f = s_m[w][i] == -INFINITY ? 0.f : ex2(s_m[w][i] - mx);
+                const float f = s_l[w][i] == 0.f ? 0.f : ex2(s_m[w][i] - mx);
                 s_f[w][i] = f;
                 den += f * s_l[w][i];
             }
             s_den[i] = den;
             if (!whole) {
-                part[i * (D + 4) + D] = mx;
+                part[i * (D + 4) + D] = mx == kNone ? -INFINITY : mx;
                 part[i * (D + 4) + D + 1] = den;
             }
         }
