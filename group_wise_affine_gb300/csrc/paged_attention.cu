@@ -24,7 +24,7 @@
 // largest met so far lies in [2^5, 2^6) (the accumulators are rescaled when a
 // larger one comes, as they are for the running maximum).
 //
-// Work split.  The unit is a step of 128 keys of one sequence, KV head and
+// Work split.  The unit is a step of some keys (STEP) of one sequence, KV head and
 // block of up to 8 NN query rows (GQA heads x new tokens); the units of the
 // whole batch are laid end to end and cut into equal runs, one per CTA, so
 // ragged batches and single long sequences both fill the GPU.  A CTA that
@@ -33,7 +33,7 @@
 // second kernel joins them.  Lengths are read from the device; nothing of
 // the split depends on host values but the grid.
 //
-// A warp takes 32 of the step's 128 keys (two MMA tiles of 16), copies their
+// A warp takes a quarter of the step (U MMA tiles of 16 keys), copies its
 // codes and parameters with cp.async into its own ring two steps ahead, and
 // keeps its own softmax state; the four warps merge in shared memory at the
 // end of a piece.  (Bulk copies ran slower: pages of 16 tokens make them 1 KB
@@ -53,9 +53,15 @@
 namespace gwa {
 
 constexpr int kPgWarps = 4;
-constexpr int kPgKeys = 32;                    // keys of a warp's step
-constexpr int kPgStep = kPgWarps * kPgKeys;    // keys of a CTA's step
 constexpr int kPgMaxCtas = 2048;
+
+// A (sequence, KV head, row block) that the cut spread over several CTAs: its
+// first piece's slot (-1: nothing to join), further pieces in the slots 2 (cta
+// + k); rows r0 .. r0 + nlive of the sequence whose first token is `first`,
+// query heads from `head`.
+struct PgCut {
+    int slot, cta, n, first, head, r0, nlive, pad;
+};
 
 struct PagedParams {
     const uint16_t *q;
@@ -65,12 +71,14 @@ struct PagedParams {
     float scale;
     int causal;
     uint16_t *out;    // [tokens, Hq, dim]
-    int4 *desc;       // [ctas]: a cut piece that starts in this CTA
+    PgCut *cuts;      // what the join has to do
+    int segs;         // (KV head, row block) pairs of a sequence, at most
+    int by_seg;       // cuts are indexed by sequence and pair, else by CTA
     float *part;      // [2 ctas][8 NN][dim + 4]
     int32_t *status;
 };
 
-// Shared memory of one warp's ring stage (32 keys: two tiles of 16).  A
+// Shared memory of one warp's ring stage (U tiles of 16 keys).  A
 // tile's codes are laid out [group][row][GB bytes], so that the fragment
 // reads hit every bank once: key rows in the order of the scores' rows, value
 // rows in key order (8-bit rows with their two halves swapped in every other
@@ -79,14 +87,17 @@ template <int BITS, int D, int NN>
 struct PgLayout {
     static constexpr int G = D / 64;
     static constexpr int GB = 8 * BITS;          // code bytes of a group
+    static constexpr int U = 2;  //U                // tiles of a warp's step
+    static constexpr int KEYS = 16 * U;          // keys of a warp's step
+    static constexpr int STEP = kPgWarps * KEYS; // keys of a CTA's step
     static constexpr int TILE = 16 * G * GB;     // codes of a tile
     static constexpr int PB = 16 * G * 4;        // parameters of a tile
     static constexpr int K_OFF = 0;
-    static constexpr int V_OFF = 2 * TILE;
-    static constexpr int KP_OFF = 4 * TILE;
-    static constexpr int VP_OFF = KP_OFF + 2 * PB;
-    static constexpr int STAGE = VP_OFF + 2 * PB;
-    static constexpr int S = 3;
+    static constexpr int V_OFF = U * TILE;
+    static constexpr int KP_OFF = 2 * U * TILE;
+    static constexpr int VP_OFF = KP_OFF + U * PB;
+    static constexpr int STAGE = VP_OFF + U * PB;
+    static constexpr int S = 3;  //S
     static constexpr int NQ = 8 * NN;
     static constexpr int MERGE = NQ * D * 4;     // a warp's output rows
     static constexpr int WARP_BYTES = S * STAGE > MERGE ? S * STAGE : MERGE;
@@ -94,7 +105,7 @@ struct PgLayout {
     static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 1024 + kPgWarps * NQ * (12 + 4 * G) + 4 * NQ);
     // accumulators, queries and fragments: about 96 + 4 registers per 8 rows
     // and 16 dimensions
-    static constexpr int BY_REGS = NN * D < 128 ? 4 : NN * D <= 256 ? 3 : 2;
+    static constexpr int BY_REGS = NN * D <= 128 ? 3 : NN * D <= 256 ? 3 : 2;
     static constexpr int CTAS = BY_SMEM < BY_REGS ? (BY_SMEM < 1 ? 1 : BY_SMEM) : BY_REGS;
     // key of score row j (0..7; row j + 8: 8 more); the value product's k
     // positions 2t, 2t + 1, 2t + 8, 2t + 9 are then keys t, t + 4, t + 8, t + 12
@@ -103,10 +114,9 @@ struct PgLayout {
 
 // Keys that some row of the sequence sees, in steps; row blocks; units.
 struct PgSeq {
-    int first, count, len, rows, nrg, nt;
-    int64_t units;
+    int first, count, len, rows, nrg, nt, units;
 };
-template <int NQ>
+template <int NQ, int STEP>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     PgSeq r;
@@ -115,14 +125,18 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     r.len = s.len;
     r.rows = p.rep * min(s.count, p.kv.max_q);
     r.nrg = (r.rows + NQ - 1) / NQ;
-    r.nt = (s.len + kPgStep - 1) / kPgStep;
-    r.units = (int64_t)p.kv.heads * r.nrg * r.nt;
+    r.nt = (s.len + STEP - 1) / STEP;
+    r.units = p.kv.heads * r.nrg * r.nt;  // the entry point keeps the total below 2^31
     return r;
 }
 
-// CTA c's run of units starts at total * c / ctas.
-__device__ __forceinline__ int64_t pg_start(int64_t total, int c, int ctas) {
-    return total / ctas * c + total % ctas * c / ctas;
+// `total` units over `ctas` CTAs: the first total % ctas take one more.
+__device__ __forceinline__ int pg_start(int quot, int rest, int c) {
+    return quot * c + min(c, rest);
+}
+__device__ __forceinline__ int pg_owner(int quot, int rest, int unit) {
+    const int big = rest * (quot + 1);
+    return unit < big ? unit / (quot + 1) : rest + (unit - big) / quot;
 }
 
 // Sixteen codes of one key row as the fp16 pairs the MMA takes.  A code left
@@ -178,6 +192,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     paged_decode_kernel(PagedParams p) {
     using L = PgLayout<BITS, D, NN>;
     constexpr int G = L::G, GB = L::GB, S = L::S, NQ = L::NQ;
+    constexpr int U = L::U, KEYS = L::KEYS, STEP = L::STEP;
     constexpr int NT = D / 16;                  // value m-tiles
     constexpr int NCP = L::TILE / 16 / kWarp;   // 16-byte copies per lane, tile
     constexpr int RCH = G * GB / 16;            // 16-byte chunks of a key row
@@ -209,37 +224,35 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 
     // ---- this CTA's run of units, found by every warp for itself
     const int B = p.kv.batch;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < B; b0 += kWarp) {
-        const int b = b0 + lane;
-        int64_t u = b < B ? pg_seq<NQ>(p, b).units : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) u += __shfl_xor_sync(FULL, u, o);
-        total += u;
-    }
-    const int ctas = (int)min((int64_t)gridDim.x, total);
     const int cta = blockIdx.x;
+    int total = 0;
+    for (int b0 = 0; b0 < B; b0 += kWarp)
+        total += __reduce_add_sync(
+            FULL, b0 + lane < B ? pg_seq<NQ, STEP>(p, b0 + lane).units : 0);
     // sequences without keys: their rows are zero
-    for (int b = cta; b < B; b += gridDim.x) {
-        const PgSeq s = pg_seq<NQ>(p, b);
+    for (int i = cta; i < B; i += gridDim.x) {
+        const PgSeq s = pg_seq<NQ, STEP>(p, i);
+        if (p.by_seg)
+            for (int k = (s.units ? p.kv.heads * s.nrg : 0) + threadIdx.x; k < p.segs; k += blockDim.x)
+                p.cuts[i * p.segs + k].slot = -1;
         if (s.nt > 0) continue;
         uint32_t *o = reinterpret_cast<uint32_t *>(p.out + (int64_t)s.first * p.Hq * D);
-        for (int64_t i = threadIdx.x; i < (int64_t)(s.rows / p.rep) * p.Hq * (D / 2);
-             i += blockDim.x)
-            o[i] = 0u;
+        for (int64_t k = threadIdx.x; k < (int64_t)(s.rows / p.rep) * p.Hq * (D / 2); k += blockDim.x)
+            o[k] = 0u;
     }
-    if (threadIdx.x == 0) p.desc[cta] = make_int4(-1, 0, 0, 0);
+    const int ctas = min((int)gridDim.x, total);
+    if (!p.by_seg && threadIdx.x == 0) p.cuts[cta].slot = -1;
     if (cta >= ctas) return;
-    const int64_t begin = pg_start(total, cta, ctas), end = pg_start(total, cta + 1, ctas);
+    const int quot = total / ctas, rest = total % ctas;
+    const int begin = pg_start(quot, rest, cta), end = pg_start(quot, rest, cta + 1);
 
-    int b = 0;
-    int64_t at = 0;  // units before sequence b
+    int b = 0, at = 0;  // the sequence of the run's first unit, units before it
     for (int b0 = 0; b0 < B; b0 += kWarp) {
-        const int64_t u = b0 + lane < B ? pg_seq<NQ>(p, b0 + lane).units : 0;
-        int64_t incl = u;
+        const int u = b0 + lane < B ? pg_seq<NQ, STEP>(p, b0 + lane).units : 0;
+        int incl = u;
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
-            const int64_t v = __shfl_up_sync(FULL, incl, o);
+            const int v = __shfl_up_sync(FULL, incl, o);
             if (lane >= o) incl += v;
         }
         const unsigned past = __ballot_sync(FULL, at + incl > begin);
@@ -251,8 +264,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         }
         at += __shfl_sync(FULL, incl, kWarp - 1);
     }
-    PgSeq sq = pg_seq<NQ>(p, b);
-    int64_t cur = begin;
+    PgSeq sq = pg_seq<NQ, STEP>(p, b);
+    int cur = begin;
     int piece = 0;
     const float sl2 = p.scale * 1.4426950408889634f;  // scores in base 2
     // The running maximum moves only when a weight passes 2^8 (weights and
@@ -264,13 +277,12 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     while (cur < end) {
         while (cur >= at + sq.units) {
             at += sq.units;
-            sq = pg_seq<NQ>(p, ++b);
+            sq = pg_seq<NQ, STEP>(p, ++b);
         }
-        const int64_t in_seq = cur - at;
-        const int seg = (int)(in_seq / sq.nt);  // hk * nrg + rg
+        const int seg = (cur - at) / sq.nt;  // hk * nrg + rg
         const int hk = seg / sq.nrg, rg = seg % sq.nrg;
-        const int ta = (int)(in_seq - (int64_t)seg * sq.nt);
-        const int tb = (int)min((int64_t)sq.nt, ta + (end - cur));
+        const int ta = cur - at - seg * sq.nt;
+        const int tb = min(sq.nt, ta + (end - cur));
         const int nlive = min(NQ, sq.rows - rg * NQ);
         const int32_t *table = p.kv.page_table + (int64_t)b * p.kv.max_pages;
 
@@ -365,15 +377,15 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         }
         float vinv = 1.f, vlim = -1.f;  // value scales: times vinv, met up to vlim
 
-        // Page numbers of the tiles of 16 steps: lane 2 j + u holds those of
+        // Page numbers of the tiles of 32 / U steps: lane U j + u holds those of
         // step j's tile u.
-        int pages = 0, pages_at = ta - 16;
+        int pages = 0, pages_at = ta - 32;
         auto issue = [&](int step, int to) {
-            if (step - pages_at >= 16) {
+            if (step - pages_at >= 32 / U) {
                 pages_at = step;
-                const int key = (step + (lane >> 1)) * kPgStep + warp * kPgKeys + (lane & 1) * 16;
+                const int key = (step + lane / U) * STEP + warp * KEYS + lane % U * 16;
                 pages = 0;
-                if (step + (lane >> 1) < tb && key < sq.len) {
+                if (step + lane / U < tb && key < sq.len) {
                     pages = table[key >> p.kv.page_shift];
                     if ((unsigned)pages >= (unsigned)p.kv.num_pages) {
                         if (p.status) atomicOr(p.status, (int)kKvBadPage);
@@ -383,9 +395,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             }
             unsigned char *st = wsm + to * L::STAGE;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int page = __shfl_sync(FULL, pages, 2 * (step - pages_at) + u);
-                const int key = step * kPgStep + warp * kPgKeys + u * 16;
+            for (int u = 0; u < U; ++u) {
+                const int page = __shfl_sync(FULL, pages, U * (step - pages_at) + u);
+                const int key = step * STEP + warp * KEYS + u * 16;
                 if (key >= sq.len) break;  // warp-uniform
                 const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
                                     (key & pmask);
@@ -405,22 +417,29 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 }
             }
         };
+        auto scale_rows = [&](int nn, float c0, float c1) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                o[nn][j][0] *= c0;
+                o[nn][j][1] *= c1;
+                o[nn][j][2] *= c0;
+                o[nn][j][3] *= c1;
+            }
+        };
         // One step of 32 keys.  EDGE: some row does not see all of them.
         auto compute = [&](const unsigned char *stg, const int key0, auto edge_t) {
             constexpr bool EDGE = decltype(edge_t)::value;
             // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + HALF kk + kv_g,
             // less the factor fac of the column
-            float x[2][2][NN][2];
-            float sv[2][2][G], bv[2][2][G];
+            float x[U][2][NN][2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn) x[u][kk][nn][0] = x[u][kk][nn][1] = 0.f;
                 const unsigned char *kt = stg + L::K_OFF + u * L::TILE + g * GB + t * 2 * BITS;
                 const unsigned char *kp = stg + L::KP_OFF + u * L::PB + kv_g * G * 4;
-                const unsigned char *vp = stg + L::VP_OFF + u * L::PB + kv_g * G * 4;
 #pragma unroll
                 for (int gg = 0; gg < G; ++gg) {
                     uint32_t f0[8], f1[8];
@@ -444,23 +463,13 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                             x[u][1][nn][h] = fmaf(s1, c[2 + h], fmaf(b1, qs[nn][gg][h], x[u][1][nn][h]));
                         }
                     }
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                            vp + (8 * kk * G + gg) * 4);
-                        sv[u][kk][gg] = bf16_lo(w);
-                        bv[u][kk][gg] = fmaf(KC, bf16_lo(w), bf16_hi(w));
-                        // past the end lie no parameters (but anything)
-                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= sq.len)
-                            sv[u][kk][gg] = bv[u][kk][gg] = 0.f;
-                    }
                 }
             }
             // ---- weights, against the maximum so far
-            float e[2][2][NN][2], emax = 0.f, smax = 0.f;
+            float e[U][2][NN][2], emax = 0.f;
             auto weigh = [&] {
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
@@ -474,40 +483,14 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             };
             weigh();
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-                    for (int gg = 0; gg < G; ++gg) smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
+                for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn)
                         emax = fmaxf(emax, fmaxf(e[u][kk][nn][0], e[u][kk][nn][1]));
-                }
-            if (__any_sync(FULL, emax > kLazy || smax > vlim)) {
-                // a new maximum, or a larger value scale
-                float vf = 1.f;
-                if (smax == INFINITY) {
-                    // an infinite scale makes its own readers' rows infinite,
-                    // and must not take the others' range
-                    smax = 0.f;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                            for (int gg = 0; gg < G; ++gg)
-                                if (fabsf(sv[u][kk][gg]) < INFINITY)
-                                    smax = fmaxf(smax, fabsf(sv[u][kk][gg]));
-                }
-                const float top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
-                if (top > vlim) {
-                    // 2^ex <= top < 2^(ex+1): times 2^(5-ex)
-                    const int ex = min(max(f32_exp_field(top), 6), 253);
-                    const float ninv = __uint_as_float((uint32_t)(259 - ex > 254 ? 254 : 259 - ex) << 23);
-                    vf = vlim < 0.f ? 1.f : ninv / vinv;
-                    vinv = ninv;
-                    vlim = __uint_as_float((uint32_t)(ex + 1) << 23);
-                }
+            if (__any_sync(FULL, emax > kLazy)) {
+                // a new maximum
 #pragma unroll
                 for (int nn = 0; nn < NN; ++nn) {
                     float cr[2];
@@ -515,7 +498,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                     for (int h = 0; h < 2; ++h) {
                         float mt = -INFINITY;
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                        for (int u = 0; u < U; ++u)
 #pragma unroll
                             for (int kk = 0; kk < 2; ++kk)
                                 if (!EDGE || key0 + 16 * u + 8 * kk + kv_g < lim[nn][h])
@@ -529,15 +512,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         l[nn][h] *= cr[h];
 #pragma unroll
                         for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] *= cr[h];
-                        cr[h] *= vf;
                     }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        o[nn][j][0] *= cr[0];
-                        o[nn][j][1] *= cr[1];
-                        o[nn][j][2] *= cr[0];
-                        o[nn][j][3] *= cr[1];
-                    }
+                    scale_rows(nn, cr[0], cr[1]);
                 }
                 weigh();
             }
@@ -545,16 +521,59 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    l[nn][h] += (e[0][0][nn][h] + e[0][1][nn][h]) + (e[1][0][nn][h] + e[1][1][nn][h]);
-            // ---- values
+#pragma unroll
+                    for (int u = 0; u < U; ++u) l[nn][h] += e[u][0][nn][h] + e[u][1][nn][h];
+            // ---- values: their parameters, and a larger scale than any so far
+            uint32_t vw[U][2][G];
+            float smax = 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                    for (int gg = 0; gg < G; ++gg) {
+                        uint32_t &w = vw[u][kk][gg];
+                        w = *reinterpret_cast<const uint32_t *>(stg + L::VP_OFF + u * L::PB +
+                                                                ((kv_g + 8 * kk) * G + gg) * 4);
+                        // past the end lie no parameters (but anything)
+                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= sq.len) w = 0u;
+                        smax = fmaxf(smax, fabsf(bf16_lo(w)));
+                    }
+            if (__any_sync(FULL, smax > vlim)) {
+                if (smax == INFINITY) {
+                    // an infinite scale makes its own readers' rows infinite,
+                    // and must not take the others' range
+                    smax = 0.f;
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                            for (int gg = 0; gg < G; ++gg)
+                                if (fabsf(bf16_lo(vw[u][kk][gg])) < INFINITY)
+                                    smax = fmaxf(smax, fabsf(bf16_lo(vw[u][kk][gg])));
+                }
+                const float top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
+                if (top > vlim) {
+                    // 2^ex <= top < 2^(ex+1): times 2^(5-ex)
+                    const int ex = min(max(f32_exp_field(top), 6), 253);
+                    const float ninv = __uint_as_float((uint32_t)(259 - ex > 254 ? 254 : 259 - ex) << 23);
+                    const float vf = vlim < 0.f ? 1.f : ninv / vinv;
+#pragma unroll
+                    for (int nn = 0; nn < NN; ++nn) scale_rows(nn, vf, vf);
+                    vinv = ninv;
+                    vlim = __uint_as_float((uint32_t)(ex + 1) << 23);
+                }
+            }
 #pragma unroll
             for (int gg = 0; gg < G; ++gg) {
-                uint32_t pb[2][NN][2];
+                uint32_t pb[U][NN][2];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
-                        const float s = sv[u][kk][gg] * vinv, bb = bv[u][kk][gg];
+                        const float s0 = bf16_lo(vw[u][kk][gg]);
+                        const float s = s0 * vinv, bb = fmaf(KC, s0, bf16_hi(vw[u][kk][gg]));
 #pragma unroll
                         for (int nn = 0; nn < NN; ++nn) {
                             const float e0 = e[u][kk][nn][0], e1 = e[u][kk][nn][1];
@@ -572,7 +591,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         }
                     }
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < U; ++u) {
                     const int half = BITS == 8 ? (g ^ ((t >> 1) << 2)) * 8 : g * 4;
                     const unsigned char *vs = stg + L::V_OFF + u * L::TILE + (gg * 16 + t) * GB + half;
                     // words of the keys at k = 2t, 2t + 1, 2t + 8, 2t + 9
@@ -636,10 +655,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             cp_async_commit();
             cp_async_wait<S - 1>();
             __syncwarp();
-            const int key0 = step * kPgStep + warp * kPgKeys;
+            const int key0 = step * STEP + warp * KEYS;
             if (key0 < sq.len) {  // warp-uniform
                 const unsigned char *stg = wsm + stage * L::STAGE;
-                if (key0 + kPgKeys > all)
+                if (key0 + KEYS > all)
                     compute(stg, key0, std::true_type{});
                 else
                     compute(stg, key0, std::false_type{});
@@ -731,101 +750,99 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 reinterpret_cast<float4 *>(part + i * (D + 4))[c4] = a;
             }
         }
-        if (!whole) {
-            // a piece that starts here and goes on: the CTA that holds its end
-            if (ta == 0 && threadIdx.x == 0) {
-                const int64_t last = at + (int64_t)(seg + 1) * sq.nt - 1;
-                int c = (int)((double)last / (double)total * ctas);
-                c = min(max(c, cta), ctas - 1);
-                while (c > cta && pg_start(total, c, ctas) > last) --c;
-                while (c + 1 < ctas && pg_start(total, c + 1, ctas) <= last) ++c;
-                p.desc[cta] = make_int4(b, seg, 2 * cta + piece, c);
+        if (threadIdx.x == 0) {
+            PgCut *cut = p.by_seg ? p.cuts + b * p.segs + seg : p.cuts + cta;
+            if (ta == 0 && !whole) {
+                // starts here and goes on: up to the CTA of its last unit
+                const int last = pg_owner(quot, rest, at + (seg + 1) * sq.nt - 1);
+                *cut = PgCut{2 * cta + piece, cta, last - cta + 1, sq.first, hk * p.rep,
+                             rg * NQ, nlive, 0};
+            } else if (whole && p.by_seg) {
+                cut->slot = -1;
             }
         }
         piece = 1;
-        cur = at + (int64_t)seg * sq.nt + tb;
+        cur = at + seg * sq.nt + tb;
         __syncthreads();  // the ring is free again
     }
 }
 
 // Joins the pieces of a (sequence, KV head, row block) that the cut spread
 // over several CTAs: piece i's output, max m_i and sum l_i give
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Block (c, row): the
-// piece that started in CTA c, its continuations are the first pieces of the
-// CTAs up to desc.w.  Threads take four dimensions each and every
-// (256 / (D/4))-th piece.
+// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Block (x, y): row y of
+// cut x.  Threads take four dimensions each and every NG-th piece, eight
+// pieces' loads in flight, against a maximum of their own; the NG groups meet
+// in shared memory.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
-    constexpr int C4 = D / 4, NG = 256 / C4;
-    __shared__ float s_w[kPgMaxCtas];
-    __shared__ float s_red[8], s_red2[8];
+    constexpr int C4 = D / 4, NG = 256 / C4, AHEAD = 8;
+    __shared__ float s_m[NG], s_l[NG];
     __shared__ float4 s_o[NG][C4];
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait_primary();
-    const int c = blockIdx.x, i = blockIdx.y;
-    const int4 d = p.desc[c];
-    if (d.x < 0) return;
-    const PgSeq s = pg_seq<NQ>(p, d.x);
-    const int hk = d.y / s.nrg, rg = d.y % s.nrg;
-    if (i >= min(NQ, s.rows - rg * NQ)) return;
-    const int n = d.w - c + 1;
-    auto piece = [&](int k) {
-        const int slot = k == 0 ? d.z : 2 * (c + k);
-        return p.part + ((int64_t)slot * NQ + i) * (D + 4);
-    };
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    float mx = -INFINITY;
-    for (int k = threadIdx.x; k < n; k += 256) {
-        const float m = piece(k)[D];
-        s_w[k] = m;
-        mx = fmaxf(mx, m);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (lane == 0) s_red[warp] = mx;
-    __syncthreads();
-    mx = s_red[0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) mx = fmaxf(mx, s_red[w]);
-    float den = 0.f;
-    for (int k = threadIdx.x; k < n; k += 256) {
-        const float f = s_w[k] == -INFINITY ? 0.f : ex2(s_w[k] - mx);
-        s_w[k] = f;
-        den += f * piece(k)[D + 1];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane == 0) s_red2[warp] = den;
-    __syncthreads();
+    const PgCut d = p.cuts[blockIdx.x];
+    const int i = blockIdx.y;
+    if (d.slot < 0 || i >= d.nlive) return;
     const int c4 = threadIdx.x % C4, grp = threadIdx.x / C4;
+    float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = grp; k < n; k += NG) {
-        const float f = s_w[k];
-        const float4 v = reinterpret_cast<const float4 *>(piece(k))[c4];
-        if (f == 0.f) continue;
+    for (int k0 = grp; k0 < d.n; k0 += NG * AHEAD) {
+        float4 v[AHEAD];
+        float2 ml[AHEAD];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const int k = k0 + j * NG;
+            ml[j] = make_float2(-INFINITY, 0.f);
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k >= d.n) continue;
+            const float *src = p.part + ((int64_t)(k == 0 ? d.slot : 2 * (d.cta + k)) * NQ + i) * (D + 4);
+            v[j] = reinterpret_cast<const float4 *>(src)[c4];
+            ml[j] = *reinterpret_cast<const float2 *>(src + D);
+        }
+        float mx = m;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) mx = fmaxf(mx, ml[j].x);
+        if (mx == -INFINITY) mx = 0.f;
+        const float f0 = ex2(m - mx);
+        l *= f0;
+        a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            const float f = ex2(ml[j].x - mx);
+            l = fmaf(f, ml[j].y, l);
+            a.x = fmaf(f, v[j].x, a.x);
+            a.y = fmaf(f, v[j].y, a.y);
+            a.z = fmaf(f, v[j].z, a.z);
+            a.w = fmaf(f, v[j].w, a.w);
+        }
+        m = mx;
+    }
+    if (c4 == 0) {
+        s_m[grp] = m;
+        s_l[grp] = l;
+    }
+    s_o[grp][c4] = a;
+    __syncthreads();
+    if (grp) return;
+    float mx = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int k = 0; k < NG; ++k) mx = fmaxf(mx, s_m[k]);
+    if (mx == -INFINITY) mx = 0.f;
+    a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < NG; ++k) {
+        const float f = ex2(s_m[k] - mx);
+        const float4 v = s_o[k][c4];
+        den = fmaf(f, s_l[k], den);
         a.x = fmaf(f, v.x, a.x);
         a.y = fmaf(f, v.y, a.y);
         a.z = fmaf(f, v.z, a.z);
         a.w = fmaf(f, v.w, a.w);
     }
-    s_o[grp][c4] = a;
-    __syncthreads();
-    if (grp) return;
-    den = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) den += s_red2[w];
-    for (int k = 1; k < NG; ++k) {
-        const float4 v = s_o[k][c4];
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
-    }
     const float r = den == 0.f ? 0.f : 1.f / den;
-    const int rr = rg * NQ + i;
+    const int rr = d.r0 + i;
     reinterpret_cast<uint2 *>(
-        p.out + ((int64_t)(s.first + rr / p.rep) * p.Hq + hk * p.rep + rr % p.rep) * D)[c4] =
+        p.out + ((int64_t)(d.first + rr / p.rep) * p.Hq + d.head + rr % p.rep) * D)[c4] =
         make_uint2(pack_bf16(a.x * r, a.y * r), pack_bf16(a.z * r, a.w * r));
 }
 
@@ -842,7 +859,7 @@ static int pg_grid(const KvView &kv, int rep) {
     using L = PgLayout<BITS, D, NN>;
     const int64_t rows = (int64_t)rep * kv.max_q;
     const int64_t units = (int64_t)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
-                          (((int64_t)kv.max_kv + kPgStep - 1) / kPgStep);
+                          (((int64_t)kv.max_kv + L::STEP - 1) / L::STEP);
     const int64_t full = (int64_t)num_sms() * L::CTAS;
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(units, full), kPgMaxCtas));
 }
@@ -855,13 +872,18 @@ static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) 
     if (e == cudaSuccess) e = prefer_max_shared(kfn);
     if (e != cudaSuccess) return e;
     const int grid = pg_grid<BITS, D, NN>(p.kv, p.rep);
-    p.desc = static_cast<int4 *>(workspace);
-    p.part = reinterpret_cast<float *>(p.desc + kPgMaxCtas);
+    p.cuts = static_cast<PgCut *>(workspace);
+    p.part = reinterpret_cast<float *>(p.cuts + kPgMaxCtas);
+    const int64_t rows = (int64_t)p.rep * p.kv.max_q, nrg = (rows + L::NQ - 1) / L::NQ;
+    const int64_t segs = nrg * p.kv.heads, all_segs = segs * p.kv.batch;
+    // no more joins than segments, and none without a cut: the smaller index
+    p.by_seg = all_segs <= grid;
+    p.segs = (int)std::min<int64_t>(segs, 0x7fffffff);
     e = launch_pdl(kfn, (unsigned)grid, kPgWarps * kWarp, L::BYTES, st, p);
     if (e != cudaSuccess) return e;
     if (grid == 1) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid, (unsigned)std::min<int64_t>(L::NQ, (int64_t)p.rep * p.kv.max_q));
+    cfg.gridDim = dim3((unsigned)(p.by_seg ? all_segs : grid), (unsigned)std::min<int64_t>(L::NQ, rows));
     cfg.blockDim = dim3(256);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -884,7 +906,7 @@ size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {
     if (kv.bits == BB && kv.dim == DD && nn == N) grid = pg_grid<BB, DD, N>(kv, rep);
     GWA_PG_ALL(GWA_PG)
 #undef GWA_PG
-    return kPgMaxCtas * sizeof(int4) + (size_t)grid * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
+    return kPgMaxCtas * sizeof(PgCut) + (size_t)grid * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
