@@ -34,7 +34,7 @@
 // the split depends on host values but the grid.
 //
 // A warp takes a quarter of the step (U MMA tiles of 16 keys), copies its
-// codes and parameters with cp.async into its own ring two steps ahead, and
+// codes and parameters with cp.async into its own ring a step ahead, and
 // keeps its own softmax state; the four warps merge in shared memory at the
 // end of a piece.  (Bulk copies ran slower: pages of 16 tokens make them 1 KB
 // and 64 to 128 bytes long, about 22 cycles of an SM each whatever their size.)
@@ -87,7 +87,7 @@ template <int BITS, int D, int NN>
 struct PgLayout {
     static constexpr int G = D / 64;
     static constexpr int GB = 8 * BITS;          // code bytes of a group
-    static constexpr int U = 2;  //U                // tiles of a warp's step
+    static constexpr int U = 2;                  // tiles of a warp's step
     static constexpr int KEYS = 16 * U;          // keys of a warp's step
     static constexpr int STEP = kPgWarps * KEYS; // keys of a CTA's step
     static constexpr int TILE = 16 * G * GB;     // codes of a tile
@@ -97,15 +97,15 @@ struct PgLayout {
     static constexpr int KP_OFF = 2 * U * TILE;
     static constexpr int VP_OFF = KP_OFF + U * PB;
     static constexpr int STAGE = VP_OFF + U * PB;
-    static constexpr int S = 3;  //S
+    static constexpr int S = 2;
     static constexpr int NQ = 8 * NN;
     static constexpr int MERGE = NQ * D * 4;     // a warp's output rows
     static constexpr int WARP_BYTES = S * STAGE > MERGE ? S * STAGE : MERGE;
     static constexpr int BYTES = kPgWarps * WARP_BYTES;
-    static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 1024 + kPgWarps * NQ * (12 + 4 * G) + 4 * NQ);
-    // accumulators, queries and fragments: about 96 + 4 registers per 8 rows
-    // and 16 dimensions
-    static constexpr int BY_REGS = NN * D <= 128 ? 3 : NN * D <= 256 ? 3 : 2;
+    static constexpr int BY_SMEM = (228 * 1024) / (BYTES + 1024 + kPgWarps * NQ * (12 + 4 * G) + 4 * NQ + NQ * D * 2);
+    // resident CTAs by registers: accumulators (4 per 8 rows and 16
+    // dimensions) and about 96 more
+    static constexpr int BY_REGS = NN * D <= 128 ? 4 : NN * D <= 256 ? 3 : 2;
     static constexpr int CTAS = BY_SMEM < BY_REGS ? (BY_SMEM < 1 ? 1 : BY_SMEM) : BY_REGS;
     // key of score row j (0..7; row j + 8: 8 more); the value product's k
     // positions 2t, 2t + 1, 2t + 8, 2t + 9 are then keys t, t + 4, t + 8, t + 12
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     __shared__ float s_m[kPgWarps][NQ], s_l[kPgWarps][NQ], s_f[kPgWarps][NQ];
     __shared__ float s_b[kPgWarps][NQ][G];
     __shared__ float s_den[NQ];
+    __shared__ uint4 s_q[NN][G][2][kWarp];
 
     const int lane = threadIdx.x & (kWarp - 1), warp = threadIdx.x / kWarp;
     const int g = lane >> 2, t = lane & 3;
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         const int nlive = min(NQ, sq.rows - rg * NQ);
         const int32_t *table = p.kv.page_table + (int64_t)b * p.kv.max_pages;
 
-        // queries: row 8 nn + g, dimensions 64 gg + 16 t .. + 15
-        uint32_t qf[NN][G][8];
+        // queries: row 8 nn + g, dimensions 64 gg + 16 t .. + 15, as the
+        // fragments that every warp reads back for each step
         float fac[NN][2], qs[NN][G][2];
         int lim[NN][2];
 #pragma unroll
@@ -322,14 +323,18 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
             for (int gg = 0; gg < G; ++gg) {
                 sum[gg] = 0.f;
+                uint32_t qf[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float a = elem(gg, k_dim<BITS>(i, 0)) * up;
                     const float c = elem(gg, k_dim<BITS>(i, 1)) * up;
                     constexpr float r16 = 0.0625f;
-                    qf[nn][gg][i] = k_sixteenth<BITS>(i) ? pack_f16(a * r16, c * r16)
-                                                         : pack_f16(a, c);
+                    qf[i] = k_sixteenth<BITS>(i) ? pack_f16(a * r16, c * r16) : pack_f16(a, c);
                     sum[gg] += a + c;
+                }
+                if ((nn * G + gg) % kPgWarps == warp) {
+                    s_q[nn][gg][0][lane] = make_uint4(qf[0], qf[1], qf[2], qf[3]);
+                    s_q[nn][gg][1][lane] = make_uint4(qf[4], qf[5], qf[6], qf[7]);
                 }
                 sum[gg] += __shfl_xor_sync(FULL, sum[gg], 1);
                 sum[gg] += __shfl_xor_sync(FULL, sum[gg], 2);
@@ -349,6 +354,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                                         : sq.len;
             }
         }
+        __syncthreads();
         // every row of the block sees the keys below `all`
         int all = 0x7fffffff;
 #pragma unroll
@@ -433,30 +439,37 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             // less the factor fac of the column
             float x[U][2][NN][2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn) x[u][kk][nn][0] = x[u][kk][nn][1] = 0.f;
-                const unsigned char *kt = stg + L::K_OFF + u * L::TILE + g * GB + t * 2 * BITS;
-                const unsigned char *kp = stg + L::KP_OFF + u * L::PB + kv_g * G * 4;
 #pragma unroll
-                for (int gg = 0; gg < G; ++gg) {
+            for (int gg = 0; gg < G; ++gg) {
+                uint4 qa[NN], qb[NN];
+#pragma unroll
+                for (int nn = 0; nn < NN; ++nn) {
+                    qa[nn] = s_q[nn][gg][0][lane];
+                    qb[nn] = s_q[nn][gg][1][lane];
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const unsigned char *kt = stg + L::K_OFF + u * L::TILE + g * GB + t * 2 * BITS;
+                    const unsigned char *kp = stg + L::KP_OFF + u * L::PB + kv_g * G * 4;
                     uint32_t f0[8], f1[8];
                     k_fragments<BITS>(kt + gg * 16 * GB, f0);
                     k_fragments<BITS>(kt + gg * 16 * GB + 8 * GB, f1);
                     const uint32_t p0 = *reinterpret_cast<const uint32_t *>(kp + gg * 4);
-                    const uint32_t p1 =
-                        *reinterpret_cast<const uint32_t *>(kp + (8 * G + gg) * 4);
+                    const uint32_t p1 = *reinterpret_cast<const uint32_t *>(kp + (8 * G + gg) * 4);
                     const float s0 = bf16_lo(p0), s1 = bf16_lo(p1);
                     const float b0 = bf16_hi(p0), b1 = bf16_hi(p1);
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn) {
                         float c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 8; i += 2)
-                            mma_f16(c, f0[i], f1[i], f0[i + 1], f1[i + 1], qf[nn][gg][i],
-                                    qf[nn][gg][i + 1]);
+                        mma_f16(c, f0[0], f1[0], f0[1], f1[1], qa[nn].x, qa[nn].y);
+                        mma_f16(c, f0[2], f1[2], f0[3], f1[3], qa[nn].z, qa[nn].w);
+                        mma_f16(c, f0[4], f1[4], f0[5], f1[5], qb[nn].x, qb[nn].y);
+                        mma_f16(c, f0[6], f1[6], f0[7], f1[7], qb[nn].z, qb[nn].w);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             x[u][0][nn][h] = fmaf(s0, c[h], fmaf(b0, qs[nn][gg][h], x[u][0][nn][h]));
