@@ -360,7 +360,7 @@ int gwa_pipeline_status(uint32_t *timeouts, int32_t reset) {
     if (e != cudaSuccess) return cuda_fail(e, "gwa_pipeline_status");
     *timeouts = group_timeouts(reset != 0) + stream_timeouts(reset != 0) +
                 moe_stream_timeouts(reset != 0) + qmm_timeouts(reset != 0) +
-                mma_timeouts(reset != 0);
+                mma_timeouts(reset != 0) + prefill_timeouts(reset != 0);
     e = cudaGetLastError();
     return e == cudaSuccess ? GWA_OK : cuda_fail(e, "gwa_pipeline_status");
 }

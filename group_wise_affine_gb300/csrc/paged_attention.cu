@@ -49,34 +49,11 @@
 #include "internal.h"
 #include "kv.cuh"
 #include "mma.cuh"
+#include "paged.cuh"
 
 namespace gwa {
 
 constexpr int kPgWarps = 4;
-constexpr int kPgMaxCtas = 2048;
-
-// A (sequence, KV head, row block) that the cut spread over several CTAs: its
-// first piece's slot (-1: nothing to join), further pieces in the slots 2 (cta
-// + k); rows r0 .. r0 + nlive of the sequence whose first token is `first`,
-// query heads from `head`.
-struct PgCut {
-    int slot, cta, n, first, head, r0, nlive, pad;
-};
-
-struct PagedParams {
-    const uint16_t *q;
-    int64_t q_stride;
-    int Hq, rep;
-    KvView kv;
-    float scale;
-    int causal;
-    uint16_t *out;    // [tokens, Hq, dim]
-    PgCut *cuts;      // what the join has to do
-    int segs;         // (KV head, row block) pairs of a sequence, at most
-    int by_seg;       // cuts are indexed by sequence and pair, else by CTA
-    float *part;      // [2 ctas][8 NN][dim + 4]
-    int32_t *status;
-};
 
 // Shared memory of one warp's ring stage (U tiles of 16 keys).  A
 // tile's codes are laid out [group][row][GB bytes], so that the fragment
@@ -124,19 +101,11 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     r.count = s.count;
     r.len = s.len;
     r.rows = p.rep * min(s.count, p.kv.max_q);
+    if (r.rows > p.split) r.rows = 0;  // the prompt kernel's
     r.nrg = (r.rows + NQ - 1) / NQ;
     r.nt = (s.len + STEP - 1) / STEP;
     r.units = p.kv.heads * r.nrg * r.nt;  // the entry point keeps the total below 2^31
     return r;
-}
-
-// `total` units over `ctas` CTAs: the first total % ctas take one more.
-__device__ __forceinline__ int pg_start(int quot, int rest, int c) {
-    return quot * c + min(c, rest);
-}
-__device__ __forceinline__ int pg_owner(int quot, int rest, int unit) {
-    const int big = rest * (quot + 1);
-    return unit < big ? unit / (quot + 1) : rest + (unit - big) / quot;
 }
 
 // Sixteen codes of one key row as the fp16 pairs the MMA takes.  A code left
@@ -276,10 +245,12 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     const int pmask = (1 << p.kv.page_shift) - 1;
 
     while (cur < end) {
-        while (cur >= at + sq.units) {
+        while (cur >= at + sq.units && b + 1 < B) {
             at += sq.units;
             sq = pg_seq<NQ, STEP>(p, ++b);
         }
+        // (never, unless the lengths change meanwhile)
+        if (cur >= at + sq.units) break;
         const int seg = (cur - at) / sq.nt;  // hk * nrg + rg
         const int hk = seg / sq.nrg, rg = seg % sq.nrg;
         const int ta = cur - at - seg * sq.nt;
@@ -862,15 +833,13 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
 // ---------------------------------------------------------------- host side
 // Row block: the smallest of 8, 16, 32 rows that holds a sequence's rows (16
 // at 256 dimensions, whose accumulators take twice the registers).
-static int pg_nn(int rep, int max_q, int D) {
-    const int64_t rows = (int64_t)rep * max_q;
+static int pg_nn(int64_t rows, int D) {
     return rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
 }
 
 template <int BITS, int D, int NN>
-static int pg_grid(const KvView &kv, int rep) {
+static int pg_grid(const KvView &kv, int64_t rows) {
     using L = PgLayout<BITS, D, NN>;
-    const int64_t rows = (int64_t)rep * kv.max_q;
     const int64_t units = (int64_t)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
                           (((int64_t)kv.max_kv + L::STEP - 1) / L::STEP);
     const int64_t full = (int64_t)num_sms() * L::CTAS;
@@ -884,10 +853,11 @@ static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) 
     cudaError_t e = allow_smem(kfn, L::BYTES);
     if (e == cudaSuccess) e = prefer_max_shared(kfn);
     if (e != cudaSuccess) return e;
-    const int grid = pg_grid<BITS, D, NN>(p.kv, p.rep);
+    const int64_t rows = std::min<int64_t>((int64_t)p.rep * p.kv.max_q, p.split);
+    const int grid = pg_grid<BITS, D, NN>(p.kv, rows);
     p.cuts = static_cast<PgCut *>(workspace);
     p.part = reinterpret_cast<float *>(p.cuts + kPgMaxCtas);
-    const int64_t rows = (int64_t)p.rep * p.kv.max_q, nrg = (rows + L::NQ - 1) / L::NQ;
+    const int64_t nrg = (rows + L::NQ - 1) / L::NQ;
     const int64_t segs = nrg * p.kv.heads, all_segs = segs * p.kv.batch;
     // no more joins than segments, and none without a cut: the smaller index
     p.by_seg = all_segs <= grid;
@@ -912,14 +882,29 @@ static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) 
     X(4, 128, 4) X(4, 256, 1) X(4, 256, 2) X(8, 64, 1) X(8, 64, 2)        \
     X(8, 64, 4) X(8, 128, 1) X(8, 128, 2) X(8, 128, 4) X(8, 256, 1) X(8, 256, 2)
 
+// Rows up to which a sequence goes to the few-row kernel (PG_SPLIT_TEXT)
+constexpr int kPgSplit = 32;
+
+// Whether a batch can have sequences on either side.
+static int pg_split(const KvView &kv, int rep) {
+    const int64_t rows = (int64_t)rep * kv.max_q;
+    if (rows <= kPgSplit) return (int)rows;  // no prompts
+    return kv.batch == 1 ? 0 : kPgSplit;     // a prompt alone, or both
+}
+
 size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {
-    const int rep = Hq / kv.heads, nn = pg_nn(rep, kv.max_q, kv.dim);
-    int grid = 1;
-#define GWA_PG(BB, DD, N) \
-    if (kv.bits == BB && kv.dim == DD && nn == N) grid = pg_grid<BB, DD, N>(kv, rep);
+    const int rep = Hq / kv.heads, split = pg_split(kv, rep);
+    const int64_t rows = std::min<int64_t>((int64_t)rep * kv.max_q, split);
+    const int nn = pg_nn(rows, kv.dim);
+    size_t few = 0;
+#define GWA_PG(BB, DD, N)                                                              \
+    if (kv.bits == BB && kv.dim == DD && nn == N)                                      \
+        few = (size_t)pg_grid<BB, DD, N>(kv, rows) * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
     GWA_PG_ALL(GWA_PG)
 #undef GWA_PG
-    return kPgMaxCtas * sizeof(PgCut) + (size_t)grid * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
+    const size_t many =
+        (int64_t)rep * kv.max_q > split ? paged_prefill_workspace_bytes(kv, rep) : 0;
+    return kPgMaxCtas * sizeof(PgCut) + std::max(few, many);
 }
 
 cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
@@ -936,12 +921,19 @@ cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
     p.causal = causal;
     p.out = out;
     p.status = status;
-    const int nn = pg_nn(p.rep, kv.max_q, kv.dim);
+    p.split = pg_split(kv, p.rep);
+    const int64_t all = (int64_t)p.rep * kv.max_q;
+    cudaError_t e = cudaSuccess;
+    if (p.split > 0) {
+        const int nn = pg_nn(std::min<int64_t>(all, p.split), kv.dim);
+        e = cudaErrorInvalidValue;
 #define GWA_PG(BB, DD, N) \
-    if (kv.bits == BB && kv.dim == DD && nn == N) return launch_pg_t<BB, DD, N>(p, workspace, st);
-    GWA_PG_ALL(GWA_PG)
+    if (kv.bits == BB && kv.dim == DD && nn == N) e = launch_pg_t<BB, DD, N>(p, workspace, st);
+        GWA_PG_ALL(GWA_PG)
 #undef GWA_PG
-    return cudaErrorInvalidValue;
+    }
+    if (e == cudaSuccess && all > p.split) e = launch_paged_prefill(p, workspace, st);
+    return e;
 }
 
 }  // namespace gwa

@@ -1,0 +1,1011 @@
+// Softmax attention over the paged 4-bit (or 8-bit) KV cache for prompts and
+// chunks of them, on the 5th-generation tensor cores (tcgen05).  The same
+// operation as paged_attention.cu, for the sequences with many query rows
+// (new tokens x query heads of a KV head), where the work is a pair of dense
+// products and the bytes of the cache are few.
+//
+// A CTA holds a block of MT * 128 rows of one (sequence, KV head) and goes
+// over the keys in tiles of 128:
+//   S = Q K'^T   (M = 128 rows, N = 128 keys; Q and K' in shared memory)
+//   P = 2^(S f - m), written to tensor memory over S as fp16
+//   O += P V'    (M = 128 rows, N = head_dim; P from tensor memory, V'
+//                transposed in shared memory)
+// with the running maximum m and sum per row in fp32, one thread to a row; m
+// moves only when a tile's maximum passes it by 8 (weights up to 2^8), and
+// then O is rescaled in tensor memory.
+//
+// Operands.  u4 keys enter exactly, as the prefill projections' weights do:
+// scale * (code - 8) has at most 11 significant bits and is exact in fp16, and
+// the rest of the affine map, b' = b + 8 s per group, goes into 16 further
+// columns as fp16 hi and lo parts against those of the queries' group sums.
+// (u8: scale * (code - 128) has up to 15 bits and is rounded to 11, relative
+// 2^-12; two exact parts would double the products.)  Values enter as fp16
+// s (c - c0) + b', rounded once, 2^-12 of a value, and weights as fp16.  A
+// query row is scaled by a power of two, and each tile's keys and values by
+// one each, so fp16's range does not limit the inputs: the keys' comes back in
+// the row's factor f, the values' only ever grows within a block and rescales
+// O as the maximum does.
+//
+// Warps: 0 issues the MMAs (one thread) and owns the tensor memory; 4-7 and
+// 8-11 are the softmax of row tiles 0 and 1 (with one row tile of 256
+// dimensions 4-7 alone), they also load and convert the queries and write the
+// output; 12-19 unpack keys and values from global memory into the operand
+// tiles, the next tile's codes already in registers.  With two row tiles the
+// tensor cores work on one while the softmax of the other runs; with one, the
+// scores of the next tile are computed ahead into a second buffer.
+//
+// The work of the batch, counted in (row block, key tile) units with the
+// causal mask's empty tiles left out, is cut into equal runs, one per CTA and
+// one CTA per SM, as in the few-row kernel; cut blocks are joined by a second
+// kernel.  Every wait is bounded (2 s): a wait that runs out is counted and
+// the kernel unwinds without hanging.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "kv.cuh"
+#include "mma.cuh"
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace gwa {
+
+constexpr int kPfThreads = 640;
+constexpr int kPfDeqWarps = 8;
+constexpr int kPfDeq0 = 12;    // first unpacking warp
+constexpr int kPfSlots = 4;    // tiles whose range factors are kept
+
+static __device__ unsigned int g_prefill_timeouts;
+
+// D[tmem] (+)= A[smem] . B[smem]^T, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of a K-major tile of 128 rows and 16 columns without swizzle:
+// 8-row, 16-byte core matrices, the two of a row 2048 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_ext(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3fffu);
+    d |= (uint64_t)(2048 >> 4) << 16;  // leading: next 8 columns
+    d |= (uint64_t)(128 >> 4) << 32;   // stride: next 8 rows
+    d |= (uint64_t)1 << 46;
+    return d;
+}
+
+// fp16 inputs, fp32 accumulators, both operands K-major, M = 128.
+__device__ __forceinline__ constexpr uint32_t pf_idesc(int n) {
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+template <int BITS, int D>
+struct PfLayout {
+    static constexpr int G = D / 64;
+    static constexpr int MT = D <= 128 ? 2 : 1;      // row tiles
+    static constexpr int RB = 128 * MT;              // rows of a block
+    static constexpr int ST = D <= 128 ? 2 : 1;      // key and value stages
+    static constexpr int RCH = D * BITS / 128;       // 16-byte chunks of a key's codes
+    static constexpr int TILE = 128 * D * 2;         // an operand tile
+    static constexpr int EXT = 128 * 32;             // the further columns of one
+    static constexpr size_t Q_OFF = 0;
+    static constexpr size_t QX_OFF = Q_OFF + (size_t)MT * TILE;
+    static constexpr size_t KX_OFF = QX_OFF + (size_t)MT * EXT;
+    static constexpr size_t K_OFF = KX_OFF + (size_t)ST * EXT;
+    static constexpr size_t V_OFF = K_OFF + (size_t)ST * TILE;
+    static constexpr size_t BYTES = V_OFF + (size_t)ST * TILE;
+    static constexpr size_t SMEM = BYTES + 1024;     // alignment slack
+    // tensor memory: two score buffers, then the outputs
+    static constexpr int O_COL = 256;
+    // unpacking units of a warp: keys KB x CB chunks; values 64 keys x 32
+    // dimensions
+    static constexpr int KB = RCH >= 4 ? 8 : 16, CB = RCH >= 4 ? 4 : 2;
+    static constexpr int KU = 128 / KB * (RCH / CB) / kPfDeqWarps;
+    static constexpr int VU = 4 * G / kPfDeqWarps > 0 ? 4 * G / kPfDeqWarps : 1;
+    static constexpr int VUNITS = 4 * G;             // of a tile
+    static constexpr int VW = BITS / 4;              // words of 8 dimensions
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+// One tile's powers of two, and its keys whose value parameters are not finite.
+struct PfTile {
+    float k_down, v_up, v_down;
+    uint32_t bad[4];  // bit l of word j: key 4 l + j
+};
+
+// What is left of a CTA's run: the block and tile it stands at.
+struct PfCursor {
+    int b, hk, rb, tile, left;
+    KvSeq s;
+    int rows, nrb;
+};
+
+// Keys that rows [rb * RB, ...) of a sequence see, in tiles of 128.
+template <int RB>
+__device__ __forceinline__ int pf_tiles(const PagedParams &p, const KvSeq &s, int rows, int rb) {
+    int seen = s.len;
+    if (p.causal) {
+        const int last = (min(rows, (rb + 1) * RB) - 1) / p.rep;
+        seen = min(seen, s.len - s.count + last + 1);
+    }
+    return seen > 0 ? (seen + 127) / 128 : 0;
+}
+template <int RB>
+__device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
+    const int rows = p.rep * min(s.count, p.kv.max_q);
+    return rows > p.split ? rows : 0;
+}
+template <int RB>
+__device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
+    const KvSeq s = kv_seq(p.kv, b);
+    const int rows = pf_rows<RB>(p, s);
+    const int nrb = (rows + RB - 1) / RB;
+    if (!p.causal) return p.kv.heads * nrb * ((s.len + 127) / 128);
+    int n = 0;
+    for (int rb = 0; rb < nrb; ++rb) n += pf_tiles<RB>(p, s, rows, rb);
+    return p.kv.heads * n;
+}
+
+// A block's piece of the run: tiles [ta, tb) of nt.
+struct PfPiece {
+    int b, hk, rb, ta, tb, nt, rows;
+    KvSeq s;
+};
+template <int RB>
+__device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor &c, PfPiece &w) {
+    if (c.left <= 0) return false;
+    int nt = pf_tiles<RB>(p, c.s, c.rows, c.rb);
+    while (c.tile >= nt) {  // the next block that sees a key
+        c.tile = 0;
+        if (++c.rb >= c.nrb) {
+            c.rb = 0;
+            if (++c.hk >= p.kv.heads || c.nrb == 0) {
+                c.hk = 0;
+                do {
+                    // (never past the batch, unless the lengths change meanwhile)
+                    if (++c.b >= p.kv.batch) return false;
+                    c.s = kv_seq(p.kv, c.b);
+                    c.rows = pf_rows<RB>(p, c.s);
+                    c.nrb = (c.rows + RB - 1) / RB;
+                } while (c.nrb == 0);
+            }
+        }
+        nt = pf_tiles<RB>(p, c.s, c.rows, c.rb);
+    }
+    w.b = c.b;
+    w.hk = c.hk;
+    w.rb = c.rb;
+    w.ta = c.tile;
+    w.tb = min(nt, c.tile + c.left);
+    w.nt = nt;
+    w.rows = c.rows;
+    w.s = c.s;
+    c.left -= w.tb - w.ta;
+    c.tile = w.tb;
+    return true;
+}
+
+template <int BITS, int D>
+__global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParams p) {
+    using L = PfLayout<BITS, D>;
+    constexpr int G = L::G, MT = L::MT, RB = L::RB, ST = L::ST;
+    constexpr float KC = BITS == 4 ? 8.f : 128.f;
+    constexpr unsigned FULL = 0xffffffffu;
+    extern __shared__ __align__(1024) unsigned char pf_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t kfull[ST], kempty[ST], vfull[ST], vempty[ST];
+    __shared__ uint64_t sfull[2], pfull[2], odone[MT], ofree[MT], qfull[MT];
+    __shared__ PfTile s_tile[kPfSlots];
+    __shared__ PfCursor s_cur;
+    __shared__ int s_ctas, s_quot, s_rest, s_begin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&kfull[i], kPfDeqWarps);
+            mbar_init(&vfull[i], kPfDeqWarps);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+        }
+        for (int i = 0; i < MT; ++i) {
+            mbar_init(&odone[i], 1);
+            mbar_init(&ofree[i], 4);
+            mbar_init(&qfull[i], 4);
+        }
+        fence_mbar_init();
+        s_fail = 0;
+        pdl_launch_dependents();
+    }
+    if (warp == 0) tmem_alloc(&s_tmem, 512);
+    pdl_wait_primary();
+    const int cta = blockIdx.x, B = p.kv.batch;
+    // ---- this CTA's run
+    if (warp == 1) {
+        int total = 0;
+        for (int b0 = 0; b0 < B; b0 += 32)
+            total += __reduce_add_sync(FULL, b0 + lane < B ? pf_units<RB>(p, b0 + lane) : 0);
+        const int ctas = min((int)gridDim.x, total);
+        const int quot = ctas ? total / ctas : 0, rest = ctas ? total % ctas : 0;
+        const int begin = pg_start(quot, rest, cta), end = pg_start(quot, rest, cta + 1);
+        int at = 0, b = 0;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            const int u = b0 + lane < B ? pf_units<RB>(p, b0 + lane) : 0;
+            int incl = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(FULL, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const unsigned past = __ballot_sync(FULL, at + incl > begin);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                b = b0 + l;
+                at += __shfl_sync(FULL, incl - u, l);
+                break;
+            }
+            at += __shfl_sync(FULL, incl, 31);
+        }
+        if (lane == 0) {
+            PfCursor c{};
+            c.left = cta < ctas ? end - begin : 0;
+            if (c.left > 0) {
+                c.b = b;
+                c.s = kv_seq(p.kv, b);
+                c.rows = pf_rows<RB>(p, c.s);
+                c.nrb = (c.rows + RB - 1) / RB;
+                const int head = pf_units<RB>(p, b) / p.kv.heads;
+                c.hk = (begin - at) / head;
+                int in = (begin - at) - c.hk * head;
+                for (int nt; in >= (nt = pf_tiles<RB>(p, c.s, c.rows, c.rb)); ++c.rb) in -= nt;
+                c.tile = in;
+            }
+            s_cur = c;
+            s_ctas = ctas;
+            s_quot = quot;
+            s_rest = rest;
+            s_begin = begin;
+            p.cuts[cta].slot = -1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    PfCursor cur = s_cur;
+    PfPiece w;
+
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_wait_sleep(bar, parity)) return true;
+        atomicAdd(&g_prefill_timeouts, 1u);
+        s_fail = 1;
+        return false;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t id_s = pf_idesc(128), id_o = pf_idesc(D);
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::Q_OFF));
+            const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + L::K_OFF));
+            const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + L::V_OFF));
+            const uint64_t qx_desc = smem_desc_ext(smem_u32(smem + L::QX_OFF));
+            const uint64_t kx_desc = smem_desc_ext(smem_u32(smem + L::KX_OFF));
+            uint32_t n = 0;               // tiles so far
+            uint32_t nr[2] = {0, 0};      // tiles of each row tile (one: of each buffer)
+            uint32_t pieces[2] = {0, 0};  // blocks of each row tile
+            bool ok = true;
+            // scores of row tile r against the keys of stage st into buffer s
+            auto scores = [&](int r, int st, int s) {
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_ss(tmem + s * 128,
+                                  q_desc + (uint64_t)((r * L::TILE + g * 16384) >> 4) + 2 * k,
+                                  k_desc + (uint64_t)((st * L::TILE + g * 16384) >> 4) + 2 * k, id_s,
+                                  g | k);
+                tc_mma_ss(tmem + s * 128, qx_desc + (uint64_t)((r * L::EXT) >> 4),
+                          kx_desc + (uint64_t)((st * L::EXT) >> 4), id_s, 1u);
+                tc_commit(&sfull[s]);
+            };
+            auto values = [&](int r, int st, int s, bool first) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_ts(tmem + L::O_COL + r * D, tmem + s * 128 + (h * 4 + k) * 8,
+                                  v_desc + (uint64_t)((st * L::TILE + h * D * 128) >> 4) + 2 * k, id_o,
+                                  first && (h | k) == 0 ? 0u : 1u);
+                tc_commit(&odone[r]);
+            };
+            while (ok && pf_next<RB>(p, cur, w)) {
+                const int nlive = min(RB, w.rows - w.rb * RB);
+                const int mt = MT == 2 && nlive > 128 ? 2 : 1;
+                const int tiles = w.tb - w.ta;
+                for (int r = 0; ok && r < mt; ++r) ok = wait(&qfull[r], pieces[r] & 1);
+                // the first tile's scores
+                ok = ok && wait(&kfull[n % ST], (n / ST) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int r = 0; r < mt; ++r) scores(r, n % ST, MT == 2 ? r : (int)(n & 1));
+                tc_commit(&kempty[n % ST]);
+                for (int i = 0; ok && i < tiles; ++i, ++n) {
+                    const int st = n % ST, st1 = (n + 1) % ST;
+                    const bool more = i + 1 < tiles;
+                    if (MT == 1 && more) {
+                        // one row tile: the next scores before these values
+                        ok = wait(&kfull[st1], ((n + 1) / ST) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(0, st1, (n + 1) & 1);
+                        tc_commit(&kempty[st1]);
+                    }
+                    ok = wait(&vfull[st], (n / ST) & 1);
+                    for (int r = 0; ok && r < mt; ++r) {
+                        const int s = MT == 2 ? r : (int)(n & 1);
+                        ok = wait(&pfull[s], nr[s] & 1);
+                        if (ok && i == 0 && pieces[r] > 0) ok = wait(&ofree[r], (pieces[r] - 1) & 1);
+                        if (!ok) break;
+                        ++nr[s];
+                        tc_fence_after();
+                        values(r, st, s, i == 0);
+                        if (r == mt - 1) tc_commit(&vempty[st]);
+                        if (MT == 2 && more) {
+                            if (r == 0) {
+                                ok = wait(&kfull[st1], ((n + 1) / ST) & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                            }
+                            scores(r, st1, r);
+                            if (r == mt - 1) tc_commit(&kempty[st1]);
+                        }
+                    }
+                }
+                for (int r = 0; r < mt; ++r) ++pieces[r];
+            }
+        }
+    } else if (warp >= 4 && warp < 4 + 4 * MT) {
+        // ------------------------------------------------ softmax of a row tile
+        const int r = (warp - 4) / 4;              // row tile
+        const int q4 = warp & 3;                   // tensor-memory lane quarter
+        const int row = q4 * 32 + lane;            // of the tile
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const uint32_t t_o = tmem + L::O_COL + r * D + lane_off;
+        uint32_t n = 0, nr = 0;  // tiles so far: of the CTA, of this row tile
+        int pieces = 0, piece = 0;
+        int begin = s_begin;     // the unit the run stands at
+        bool ok = true;
+        while (ok && pf_next<RB>(p, cur, w)) {
+            const int nlive = min(RB, w.rows - w.rb * RB);
+            const int tiles = w.tb - w.ta;
+            if (r * 128 < nlive) {
+                // ---- the row's queries: fp16 at a power of two, the group
+                // sums in the further columns
+                const int i_blk = r * 128 + row;
+                const bool live = i_blk < nlive;
+                const int rr = w.rb * RB + (live ? i_blk : 0);
+                const uint4 *src = reinterpret_cast<const uint4 *>(
+                    p.q + (int64_t)(w.s.first + rr / p.rep) * p.q_stride +
+                    (int64_t)(w.hk * p.rep + rr % p.rep) * D);
+                float mx = 0.f, sum[G];
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    sum[g] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 u = live ? src[g * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float a = bf16_lo(uw[k]), b = bf16_hi(uw[k]);
+                            mx = fmaxf(mx, fmaxf(fabsf(a), fabsf(b)));
+                            sum[g] += a + b;
+                        }
+                    }
+                    mx = fmaxf(mx, fabsf(sum[g]));
+                }
+                float up, down;
+                range_scale(mx, up, down);
+                if (p.scale < 0.f) up = -up;  // factors are kept non-negative
+                unsigned char *qt = smem + L::Q_OFF + (size_t)r * L::TILE + row * 128;
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 u = live ? src[g * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
+                        float v[8];
+                        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x);
+                        v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+                        v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z);
+                        v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] *= up;
+                        // the order in which the keys' codes unpack
+                        uint4 o;
+                        if constexpr (BITS == 4)
+                            o = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]),
+                                           pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
+                        else
+                            o = make_uint4(pack_f16(v[0], v[2]), pack_f16(v[1], v[3]),
+                                           pack_f16(v[4], v[6]), pack_f16(v[5], v[7]));
+                        *reinterpret_cast<uint4 *>(qt + g * 16384 + ((c ^ (row & 7)) * 16)) = o;
+                    }
+                {
+                    // per group (hi, lo, hi) against the keys' (hi, hi, lo)
+                    float e[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) e[k] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float x = sum[g] * up, hi = __half2float(__float2half_rn(x));
+                        e[3 * g] = e[3 * g + 2] = hi;
+                        e[3 * g + 1] = x - hi;
+                    }
+                    unsigned char *qx = smem + L::QX_OFF + (size_t)r * L::EXT + (row >> 3) * 128 + (row & 7) * 16;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4 *>(qx + k * 2048) =
+                            make_uint4(pack_f16(e[8 * k], e[8 * k + 1]), pack_f16(e[8 * k + 2], e[8 * k + 3]),
+                                       pack_f16(e[8 * k + 4], e[8 * k + 5]), pack_f16(e[8 * k + 6], e[8 * k + 7]));
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qfull[r]);
+
+                const float fac = down * fabsf(p.scale) * 1.4426950408889634f;
+                const int lim = !live ? w.s.len
+                                : p.causal ? min(w.s.len, w.s.len - w.s.count + rr / p.rep + 1)
+                                           : w.s.len;
+                const int least = __reduce_min_sync(FULL, lim);
+                float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
+                for (int i = 0; ok && i < tiles; ++i) {
+                    const uint32_t at = n + i;
+                    const int s = MT == 2 ? r : (int)(at & 1);
+                    const uint32_t t_s = tmem + s * 128 + lane_off;
+                    const uint32_t use = MT == 2 ? nr : at >> 1;
+                    ok = __all_sync(FULL, wait(&sfull[s], use & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const PfTile &pt = s_tile[at % kPfSlots];
+                    const float f = fac * pt.k_down;
+                    const int key0 = (w.ta + i) * 128;
+                    const bool edge = key0 + 128 > least;
+                    // ---- the tile's maximum
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        tc_ld32(t_s + c * 32, v);
+                        if (edge) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (key0 + c * 32 + k < lim) mx = fmaxf(mx, v[k]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+                        }
+                    }
+                    mx *= f;  // (-inf times zero: no key seen, or a scale of zero)
+                    if (!(mx > -INFINITY)) mx = edge && key0 >= lim ? -INFINITY : f == 0.f ? 0.f : mx;
+                    // ---- rescale
+                    float corr = 1.f;
+                    if (mx > m + 8.f) {
+                        corr = m == -INFINITY ? 0.f : ex2(m - mx);
+                        m = mx;
+                        l *= corr;
+                    }
+                    if (i == 0) {
+                        v_up = pt.v_up;
+                        v_down = pt.v_down;
+                        corr = 1.f;
+                    } else {
+                        if (pt.v_up != v_up) {
+                            corr *= pt.v_up * v_down;
+                            v_up = pt.v_up;
+                            v_down = pt.v_down;
+                        }
+                        if (__any_sync(FULL, corr != 1.f)) {
+                            ok = __all_sync(FULL, wait(&odone[r], (nr - 1) & 1));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                float v[32];
+                                uint32_t o[32];
+                                tc_ld32(t_o + c * 32, v);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(v[k] * corr);
+                                tc_st32(t_o + c * 32, o);
+                            }
+                            tc_wait_st();
+                        }
+                    }
+                    // ---- weights
+                    const float sub = m == -INFINITY ? 0.f : m;
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        uint32_t o[16];
+                        tc_ld32(t_s + c * 32, v);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            v[k] = ex2(fmaf(v[k], f, -sub));
+                            if (edge && key0 + c * 32 + k >= lim) v[k] = 0.f;
+                            acc[k & 3] += v[k];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = pack_f16(v[2 * k], v[2 * k + 1]);
+                        tc_st16(t_s + c * 16, o);
+                    }
+                    l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    if (pt.bad[0] | pt.bad[1] | pt.bad[2] | pt.bad[3]) {
+                        // a value that is not finite leaves the products; the
+                        // rows that see it are not finite either
+                        for (int k = 0; k < 128; ++k)
+                            if ((pt.bad[k & 3] >> (k >> 2)) & 1 && key0 + k < lim) l = NAN;
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&pfull[s]);
+                    ++nr;
+                }
+                // ---- out
+                if (ok) ok = __all_sync(FULL, wait(&odone[r], (nr - 1) & 1));
+                if (ok) {
+                    tc_fence_after();
+                    const bool whole = w.ta == 0 && w.tb == w.nt;
+                    const float inv = l == 0.f ? 0.f : v_down / l;
+                    float *part = p.part + ((int64_t)(2 * cta + piece) * RB + i_blk) * (D + 4);
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        p.out + ((int64_t)(w.s.first + rr / p.rep) * p.Hq + w.hk * p.rep + rr % p.rep) * D);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        float v[32];
+                        tc_ld32(t_o + c * 32, v);
+                        if (live && whole) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float *x = v + 8 * k;
+                                dst[c * 4 + k] = make_uint4(
+                                    pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv),
+                                    pack_bf16(x[4] * inv, x[5] * inv), pack_bf16(x[6] * inv, x[7] * inv));
+                            }
+                        } else if (live) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                reinterpret_cast<float4 *>(part + c * 32)[k] =
+                                    make_float4(v[4 * k] * v_down, v[4 * k + 1] * v_down,
+                                                v[4 * k + 2] * v_down, v[4 * k + 3] * v_down);
+                        }
+                    }
+                    if (live && !whole) {
+                        part[D] = m;
+                        part[D + 1] = l;
+                    }
+                    if (r == 0 && row == 0 && w.ta == 0 && !whole) {
+                        const int last = pg_owner(s_quot, s_rest, begin + w.nt - 1);
+                        p.cuts[cta] = PgCut{2 * cta + piece, cta, last - cta + 1, w.s.first,
+                                            w.hk * p.rep, w.rb * RB, nlive, 0};
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ofree[r]);
+                ++pieces;
+            }
+            n += tiles;
+            begin += tiles;
+            piece = 1;
+        }
+    } else if (warp >= kPfDeq0) {
+        // ------------------------------------------------ keys and values
+        const int dw = warp - kPfDeq0;
+        constexpr int KU = L::KU, VU = L::VU, RCH = L::RCH, VW = L::VW;
+        constexpr int KBS = 128 / L::KB;  // key blocks of a tile
+        const int pmask = (1 << p.kv.page_shift) - 1;
+        const int kl = RCH >= 4 ? lane & 7 : (lane & 7) + 8 * (lane >> 4);  // key of a key unit
+        const int kc = RCH >= 4 ? lane >> 3 : (lane >> 3) & 1;              // chunk of it
+        const int vc = lane & 7, vd = lane >> 3;  // 8 keys and 8 dimensions of a value unit
+        uint32_t n = 0;
+        bool ok = true;
+        while (ok && pf_next<RB>(p, cur, w)) {
+            const int32_t *table = p.kv.page_table + (int64_t)w.b * p.kv.max_pages;
+            // page numbers of a tile's eight 16-key blocks, on lanes 0..7
+            auto pages_of = [&](int tile) {
+                const int key = tile * 128 + lane * 16;
+                int pg = 0;
+                if (tile < w.tb && lane < 8 && key < w.s.len) {
+                    pg = table[key >> p.kv.page_shift];
+                    if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
+                        if (p.status) atomicOr(p.status, (int)kKvBadPage);
+                        pg = 0;
+                    }
+                }
+                return pg;
+            };
+            // a key's row in the code and parameter arrays (every lane calls)
+            auto row_of = [&](int pg, int tile, int k) {
+                const int page = __shfl_sync(FULL, pg, k >> 4);
+                return (((int64_t)page * p.kv.heads + w.hk) << p.kv.page_shift) +
+                       ((tile * 128 + k) & pmask);
+            };
+            float v_lim = -1.f, v_up = 1.f, v_down = 1.f;  // value range met so far
+            uint4 kreg[KU];
+            uint32_t kpar[KU];
+            uint32_t vreg[VU][8][VW], vpar[VU][8];
+            uint32_t xk[4][G], xv[4][G];  // parameters of keys 4 lane + j
+            auto load_k = [&](int pg, int tile) {
+                const int left = w.s.len - tile * 128;  // keys of the tile
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;
+                    const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
+                    const int64_t row = row_of(pg, tile, k);
+                    kreg[u] = make_uint4(0u, 0u, 0u, 0u);
+                    kpar[u] = 0u;
+                    if (k < left) {
+                        kreg[u] = reinterpret_cast<const uint4 *>(p.kv.kq)[row * RCH + c];
+                        kpar[u] = p.kv.kp[row * G + c / (RCH / G)];
+                    }
+                }
+                const int64_t row = row_of(pg, tile, 4 * lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const bool in = 4 * lane + j < left;
+                        xk[j][g] = in ? p.kv.kp[(row + j) * G + g] : 0u;
+                        xv[j][g] = in ? p.kv.vp[(row + j) * G + g] : 0u;
+                    }
+            };
+            auto load_v = [&](int pg, int tile) {
+                const int left = w.s.len - tile * 128;
+#pragma unroll
+                for (int u = 0; u < VU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
+                    const int k0 = id % 2 * 64 + vc * 8, d32 = id / 2;
+                    const int64_t row = row_of(pg, tile, k0 & 127);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const bool in = id < L::VUNITS && k0 + j < left;
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) vreg[u][j][x] = 0u;
+                        vpar[u][j] = 0u;
+                        if (in) {
+                            const uint32_t *src = p.kv.vq + (row + j) * (D * BITS / 32) + d32 * BITS + vd * VW;
+                            if constexpr (VW == 1) {
+                                vreg[u][j][0] = *src;
+                            } else {
+                                const uint2 t = *reinterpret_cast<const uint2 *>(src);
+                                vreg[u][j][0] = t.x;
+                                vreg[u][j][1] = t.y;
+                            }
+                            vpar[u][j] = p.kv.vp[(row + j) * G + d32 / 2];
+                        }
+                    }
+                }
+            };
+            int pg = pages_of(w.ta), pg1 = pages_of(w.ta + 1);
+            load_k(pg, w.ta);
+            load_v(pg, w.ta);
+            for (int tile = w.ta; ok && tile < w.tb; ++tile, ++n) {
+                const int st = n % ST;
+                const int left = w.s.len - tile * 128;
+                // ---- the tile's ranges, from every parameter (each warp for
+                // itself, the same result)
+                float tk = 0.f, tv = 0.f;
+                uint32_t bad = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+                        const float ks = fabsf(bf16_lo(xk[j][g]));
+                        const float kb = fabsf(fmaf(KC, bf16_lo(xk[j][g]), bf16_hi(xk[j][g])));
+                        if (ks < INFINITY && kb < INFINITY) tk = fmaxf(tk, fmaxf(KC * ks, kb));
+                        const float vs = fabsf(bf16_lo(xv[j][g]));
+                        const float vb = fabsf(fmaf(KC, bf16_lo(xv[j][g]), bf16_hi(xv[j][g])));
+                        const float t = fmaf(KC, vs, vb);
+                        if (t < INFINITY)
+                            tv = fmaxf(tv, t);
+                        else
+                            bad |= 1u << j;
+                    }
+                tk = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(tk)));
+                tv = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(tv)));
+                float k_up, k_down;
+                range_scale(tk, k_up, k_down);
+                if (tv > v_lim) {
+                    // into [2^14, 2^15), with a further 2 to grow before the next
+                    range_scale(tv, v_up, v_down);
+                    v_lim = 32768.f * v_down;
+                }
+                if (dw == 0) {
+                    const uint32_t b0 = __ballot_sync(FULL, bad & 1u), b1 = __ballot_sync(FULL, bad & 2u);
+                    const uint32_t b2 = __ballot_sync(FULL, bad & 4u), b3 = __ballot_sync(FULL, bad & 8u);
+                    if (lane == 0)
+                        s_tile[n % kPfSlots] = PfTile{k_down, v_up, v_down, {b0, b1, b2, b3}};
+                }
+                // ---- keys
+                if (n >= ST) {
+                    ok = __all_sync(FULL, wait(&kempty[st], ((n / ST) & 1) ^ 1));
+                    if (!ok) break;
+                }
+                unsigned char *kt = smem + L::K_OFF + (size_t)st * L::TILE;
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;
+                    const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
+                    const float sc = bf16_lo(kpar[u]) * k_up;
+                    const __half2 s2 = __floats2half2_rn(sc, sc);
+                    const uint32_t wd[4] = {kreg[u].x, kreg[u].y, kreg[u].z, kreg[u].w};
+                    if constexpr (BITS == 4) {
+                        const __half2 off = __floats2half2_rn(1032.f, 1032.f);
+                        const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+                        const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
+                        unsigned char *dst = kt + (c / 2) * 16384 + k * 128;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = wd[j], b = wd[j] >> 8;
+                            uint4 o;
+                            o.x = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x000f000fu) | 0x64006400u), off), s2));
+                            o.y = h2_bits(__hmul2(__hfma2(bits_h2((a & 0x00f000f0u) | 0x64006400u), r16, m72), s2));
+                            o.z = h2_bits(__hmul2(__hsub2(bits_h2((b & 0x000f000fu) | 0x64006400u), off), s2));
+                            o.w = h2_bits(__hmul2(__hfma2(bits_h2((b & 0x00f000f0u) | 0x64006400u), r16, m72), s2));
+                            *reinterpret_cast<uint4 *>(dst + ((((c & 1) * 4 + j) ^ (k & 7)) * 16)) = o;
+                        }
+                    } else {
+                        const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+                        unsigned char *dst = kt + (c / 4) * 16384 + k * 128;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const uint32_t a = wd[2 * j + x];
+                                o[2 * x] = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x00ff00ffu) | 0x64006400u), off), s2));
+                                o[2 * x + 1] = h2_bits(
+                                    __hmul2(__hsub2(bits_h2(((a >> 8) & 0x00ff00ffu) | 0x64006400u), off), s2));
+                            }
+                            *reinterpret_cast<uint4 *>(dst + ((((c & 3) * 2 + j) ^ (k & 7)) * 16)) =
+                                make_uint4(o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                }
+                // the further columns of 16 keys: b' as (hi, hi, lo) per group
+                if (lane / 4 == dw) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float e[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) e[x] = 0.f;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            const float x = fmaf(KC, bf16_lo(xk[j][g]), bf16_hi(xk[j][g])) * k_up;
+                            const float hi = __half2float(__float2half_rn(x));
+                            e[3 * g] = e[3 * g + 1] = hi;
+                            e[3 * g + 2] = x - hi;
+                        }
+                        const int k = 4 * lane + j;
+                        unsigned char *kx = smem + L::KX_OFF + (size_t)st * L::EXT + (k >> 3) * 128 + (k & 7) * 16;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            *reinterpret_cast<uint4 *>(kx + x * 2048) =
+                                make_uint4(pack_f16(e[8 * x], e[8 * x + 1]), pack_f16(e[8 * x + 2], e[8 * x + 3]),
+                                           pack_f16(e[8 * x + 4], e[8 * x + 5]), pack_f16(e[8 * x + 6], e[8 * x + 7]));
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kfull[st]);
+                const int pg2 = pages_of(tile + 2);
+                if (tile + 1 < w.tb) load_k(pg1, tile + 1);
+
+                // ---- values, transposed
+                if (n >= ST) {
+                    ok = __all_sync(FULL, wait(&vempty[st], ((n / ST) & 1) ^ 1));
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int u = 0; u < VU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;
+                    if (id >= L::VUNITS) break;
+                    unsigned char *vt = smem + L::V_OFF + (size_t)st * L::TILE + (id % 2) * (D * 128);
+                    const int d0 = id / 2 * 32 + vd * 8;
+                    __half2 s2[4], b2[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float s[2], b[2];
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t t = vpar[u][2 * j + x];
+                            s[x] = bf16_lo(t) * v_up;
+                            b[x] = fmaf(KC, bf16_lo(t), bf16_hi(t)) * v_up;
+                            // not finite (or past the end): nothing enters
+                            if (!(fabsf(s[x]) < INFINITY && fabsf(b[x]) < INFINITY)) s[x] = b[x] = 0.f;
+                        }
+                        s2[j] = __floats2half2_rn(s[0], s[1]);
+                        b2[j] = __floats2half2_rn(b[0], b[1]);
+                    }
+                    const __half2 off4 = __floats2half2_rn(1032.f, 1032.f);
+                    const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+                    const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
+                    const __half2 off8 = __floats2half2_rn(1152.f, 1152.f);
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        uint32_t lo[4], hi[4];  // dimensions 2 jj, 2 jj + 1 of the 8
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if constexpr (BITS == 4) {
+                                const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
+                                const uint32_t t = __byte_perm(vreg[u][2 * j][0], vreg[u][2 * j + 1][0], sel);
+                                lo[j] = h2_bits(__hfma2(
+                                    __hsub2(bits_h2((t & 0x000f000fu) | 0x64006400u), off4), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(
+                                    __hfma2(bits_h2((t & 0x00f000f0u) | 0x64006400u), r16, m72), s2[j], b2[j]));
+                            } else {
+                                const int e = 2 * (jj & 1);
+                                const uint32_t sel = e | ((e + 1) << 4) | ((4 + e) << 8) | ((5 + e) << 12);
+                                const uint32_t t = __byte_perm(vreg[u][2 * j][VW == 2 ? jj / 2 : 0],
+                                                               vreg[u][2 * j + 1][VW == 2 ? jj / 2 : 0], sel);
+                                lo[j] = h2_bits(__hfma2(
+                                    __hsub2(bits_h2((t & 0x00ff00ffu) | 0x64006400u), off8), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(
+                                    __hsub2(bits_h2(((t >> 8) & 0x00ff00ffu) | 0x64006400u), off8), s2[j], b2[j]));
+                            }
+                        }
+                        unsigned char *row = vt + (d0 + 2 * jj) * 128;
+                        *reinterpret_cast<uint4 *>(row + ((vc ^ ((2 * jj) & 7)) * 16)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4 *>(row + 128 + ((vc ^ ((2 * jj + 1) & 7)) * 16)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&vfull[st]);
+                if (tile + 1 < w.tb) load_v(pg1, tile + 1);
+                pg1 = pg2;
+                (void)left;
+            }
+        }
+    }
+    // ---- rows that see no key are zero: sequences, and blocks of them
+    // (written here, beside the products, by the spare warps)
+    if (warp >= 2 && warp < 4) {
+        const int tid = threadIdx.x - 64;
+        for (int b = cta; b < B; b += gridDim.x) {
+            const KvSeq s = kv_seq(p.kv, b);
+            const int rows = pf_rows<RB>(p, s);
+            for (int rb = 0; rb * RB < rows; ++rb) {
+                if (pf_tiles<RB>(p, s, rows, rb) > 0) continue;
+                const int n = min(RB, rows - rb * RB);
+                for (int i = tid; i < n * p.kv.heads * (D / 8); i += 64) {
+                    const int c = i % (D / 8), h = i / (D / 8) % p.kv.heads, rr = rb * RB + i / (D / 8) / p.kv.heads;
+                    reinterpret_cast<uint4 *>(p.out + ((int64_t)(s.first + rr / p.rep) * p.Hq + h * p.rep +
+                                                       rr % p.rep) * D)[c] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        }
+    }
+    // ---- teardown: without a wait that ran out, every MMA was waited for
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && s_fail) {
+        uint64_t *bar = &sfull[0];
+        tc_commit(bar);  // completes after every MMA issued; give it a moment
+        mbar_wait(bar, 0, 1000000ull);
+        mbar_wait(bar, 1, 1000000ull);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins cut blocks: a warp to a row, lanes over the dimensions, the pieces
+// (two mostly) one after the other.
+template <int D>
+__global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, int rb) {
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    pdl_wait_primary();
+    const PgCut d = p.cuts[blockIdx.x];
+    const int i = blockIdx.y * 8 + threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (d.slot < 0 || i >= d.nlive) return;
+    constexpr int V = D / 32;  // dimensions of a lane
+    float m = -INFINITY, l = 0.f, a[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) a[k] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < d.n; ++k) {
+        const float *src = p.part + ((int64_t)(k == 0 ? d.slot : 2 * (d.cta + k)) * rb + i) * (D + 4);
+        float v[V];
+#pragma unroll
+        for (int x = 0; x < V; x += 2) {
+            const float2 t = *reinterpret_cast<const float2 *>(src + 64 * (x / 2) + 2 * lane);
+            v[x] = t.x;
+            v[x + 1] = t.y;
+        }
+        const float mk = src[D], lk = src[D + 1];
+        const float mx = fmaxf(m, mk), sub = mx == -INFINITY ? 0.f : mx;
+        const float f0 = ex2(m - sub), f1 = ex2(mk - sub);
+        m = mx;
+        l = fmaf(l, f0, lk * f1);
+#pragma unroll
+        for (int x = 0; x < V; ++x) a[x] = fmaf(a[x], f0, v[x] * f1);
+    }
+    const float r = l == 0.f ? 0.f : 1.f / l;
+    const int rr = d.r0 + i;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(
+        p.out + ((int64_t)(d.first + rr / p.rep) * p.Hq + d.head + rr % p.rep) * D);
+#pragma unroll
+    for (int x = 0; x < V; x += 2) dst[32 * (x / 2) + lane] = pack_bf16(a[x] * r, a[x + 1] * r);
+}
+
+// One CTA per SM, no more than there can be units of work.
+static int pf_grid(const KvView &kv, int rep) {
+    const int rb = kv.dim <= 128 ? 256 : 128;
+    const int64_t units = (int64_t)kv.batch * kv.heads * (((int64_t)rep * kv.max_q + rb - 1) / rb) *
+                          (((int64_t)kv.max_kv + 127) / 128);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms()));
+}
+
+template <int BITS, int D>
+static cudaError_t launch_pf_t(PagedParams p, void *workspace, cudaStream_t st) {
+    using L = PfLayout<BITS, D>;
+    const void *kfn = reinterpret_cast<const void *>(paged_prefill_kernel<BITS, D>);
+    cudaError_t e = allow_smem(kfn, (int)L::SMEM);
+    if (e != cudaSuccess) return e;
+    const int grid = pf_grid(p.kv, p.rep);
+    p.cuts = static_cast<PgCut *>(workspace);
+    p.part = reinterpret_cast<float *>(p.cuts + kPgMaxCtas);
+    e = launch_pdl(kfn, (unsigned)grid, kPfThreads, L::SMEM, st, p);
+    if (e != cudaSuccess || grid == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(L::RB / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_prefill_join_kernel<D>, p, L::RB);
+}
+
+cudaError_t launch_paged_prefill(PagedParams p, void *workspace, cudaStream_t st) {
+#define GWA_PF(BB, DD) \
+    if (p.kv.bits == BB && p.kv.dim == DD) return launch_pf_t<BB, DD>(p, workspace, st);
+    GWA_PF(4, 64) GWA_PF(4, 128) GWA_PF(4, 256)
+    GWA_PF(8, 64) GWA_PF(8, 128) GWA_PF(8, 256)
+#undef GWA_PF
+    return cudaErrorInvalidValue;
+}
+
+size_t paged_prefill_workspace_bytes(const KvView &kv, int rep) {
+    const int rb = kv.dim <= 128 ? 256 : 128;
+    return (size_t)pf_grid(kv, rep) * 2 * rb * (kv.dim + 4) * sizeof(float);
+}
+
+unsigned int prefill_timeouts(bool reset) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_prefill_timeouts, sizeof v);
+    if (reset) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_prefill_timeouts, &z, sizeof z);
+    }
+    return v;
+}
+
+}  // namespace gwa
