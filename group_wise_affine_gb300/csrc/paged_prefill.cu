@@ -97,7 +97,10 @@ struct PfLayout {
     static constexpr size_t KX_OFF = QX_OFF + (size_t)MT * EXT;
     static constexpr size_t K_OFF = KX_OFF + (size_t)ST * EXT;
     static constexpr size_t V_OFF = K_OFF + (size_t)ST * TILE;
-    static constexpr size_t BYTES = V_OFF + (size_t)ST * TILE;
+    // per slot: key scales, value scales and biases, fp16 [G][128] each
+    static constexpr int PAR = 3 * G * 256;
+    static constexpr size_t P_OFF = V_OFF + (size_t)ST * TILE;
+    static constexpr size_t BYTES = P_OFF + (size_t)kPfSlots * PAR;
     static constexpr size_t SMEM = BYTES + 1024;     // alignment slack
     // tensor memory: two score buffers, then the outputs
     static constexpr int O_COL = 256;
@@ -110,6 +113,9 @@ struct PfLayout {
     static constexpr int VW = BITS / 4;              // words of 8 dimensions
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// The values' operands are 2^-21 of what their power of two makes them.
+constexpr float kVDown = 0x1p21f;
 
 // One tile's powers of two, and its keys whose value parameters are not finite.
 struct PfTile {
@@ -156,7 +162,7 @@ struct PfPiece {
     KvSeq s;
 };
 template <int RB>
-__device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor &c, PfPiece &w) {
+__device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece &w) {
     if (c.left <= 0) return false;
     int nt = pf_tiles<RB>(p, c.s, c.rows, c.rb);
     while (c.tile >= nt) {  // the next block that sees a key
@@ -189,6 +195,37 @@ __device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor &c, PfPie
     return true;
 }
 
+// Rows (of one head) of a tile's eight 16-key blocks, on lanes 0..7.
+struct PfPages {
+    const PagedParams &p;
+    int len, tb, hk, b;
+    __device__ __forceinline__ int64_t look(int tile, int lane) const {
+        const int key = tile * 128 + lane * 16;
+        int pg = 0;
+        if (tile < tb && lane < 8 && key < len) {
+            pg = p.kv.page_table[(int64_t)b * p.kv.max_pages + (key >> p.kv.page_shift)];
+            if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
+                if (p.status) atomicOr(p.status, (int)kKvBadPage);
+                pg = 0;
+            }
+        }
+        return (((int64_t)pg * p.kv.heads + hk) << p.kv.page_shift) +
+               (key & ((1 << p.kv.page_shift) - 1));
+    }
+};
+
+// The next piece of a warp's own walk through the run, in shared memory (the
+// walk is the same for every warp; registers are short).
+template <int RB>
+__device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor *c, PfPiece *w, int lane) {
+    __syncwarp();
+    int more = 0;
+    if (lane == 0) more = pf_step<RB>(p, *c, *w);
+    more = __shfl_sync(0xffffffffu, more, 0);
+    __syncwarp();
+    return more != 0;
+}
+
 template <int BITS, int D>
 __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParams p) {
     using L = PfLayout<BITS, D>;
@@ -201,15 +238,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     __shared__ uint64_t kfull[ST], kempty[ST], vfull[ST], vempty[ST];
     __shared__ uint64_t sfull[2], pfull[2], odone[MT], ofree[MT], qfull[MT];
     __shared__ PfTile s_tile[kPfSlots];
-    __shared__ PfCursor s_cur;
-    __shared__ int s_ctas, s_quot, s_rest, s_begin;
+    __shared__ PfCursor s_cur[kPfThreads / 32];
+    __shared__ PfPiece s_piece[kPfThreads / 32];
+    __shared__ uint64_t rfull[kPfSlots], rempty[kPfSlots];
+    __shared__ int s_quot, s_rest, s_begin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < ST; ++i) {
-            mbar_init(&kfull[i], kPfDeqWarps);
+            mbar_init(&kfull[i], kPfDeqWarps + 1);
             mbar_init(&vfull[i], kPfDeqWarps);
             mbar_init(&kempty[i], 1);
             mbar_init(&vempty[i], 1);
@@ -222,6 +261,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             mbar_init(&odone[i], 1);
             mbar_init(&ofree[i], 4);
             mbar_init(&qfull[i], 4);
+        }
+        for (int i = 0; i < kPfSlots; ++i) {
+            mbar_init(&rfull[i], 2);
+            mbar_init(&rempty[i], 1);
         }
         fence_mbar_init();
         s_fail = 0;
@@ -256,8 +299,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             }
             at += __shfl_sync(FULL, incl, 31);
         }
-        if (lane == 0) {
-            PfCursor c{};
+        PfCursor c{};
+        {
             c.left = cta < ctas ? end - begin : 0;
             if (c.left > 0) {
                 c.b = b;
@@ -270,8 +313,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 for (int nt; in >= (nt = pf_tiles<RB>(p, c.s, c.rows, c.rb)); ++c.rb) in -= nt;
                 c.tile = in;
             }
-            s_cur = c;
-            s_ctas = ctas;
+        }
+        if (lane < kPfThreads / 32) s_cur[lane] = c;
+        if (lane == 0) {
             s_quot = quot;
             s_rest = rest;
             s_begin = begin;
@@ -282,8 +326,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    PfCursor cur = s_cur;
-    PfPiece w;
+    PfCursor *const cur = &s_cur[warp];
+    const PfPiece &w = s_piece[warp];
 
     auto wait = [&](uint64_t *bar, uint32_t parity) {
         if (mbar_wait_sleep(bar, parity)) return true;
@@ -329,7 +373,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                                   first && (h | k) == 0 ? 0u : 1u);
                 tc_commit(&odone[r]);
             };
-            while (ok && pf_next<RB>(p, cur, w)) {
+            while (ok && pf_step<RB>(p, *cur, s_piece[warp])) {
                 const int nlive = min(RB, w.rows - w.rb * RB);
                 const int mt = MT == 2 && nlive > 128 ? 2 : 1;
                 const int tiles = w.tb - w.ta;
@@ -360,7 +404,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         ++nr[s];
                         tc_fence_after();
                         values(r, st, s, i == 0);
-                        if (r == mt - 1) tc_commit(&vempty[st]);
+                        if (r == mt - 1) {
+                            tc_commit(&vempty[st]);
+                            tc_commit(&rempty[n % kPfSlots]);
+                        }
                         if (MT == 2 && more) {
                             if (r == 0) {
                                 ok = wait(&kfull[st1], ((n + 1) / ST) & 1);
@@ -386,7 +433,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         int pieces = 0, piece = 0;
         int begin = s_begin;     // the unit the run stands at
         bool ok = true;
-        while (ok && pf_next<RB>(p, cur, w)) {
+        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
             const int nlive = min(RB, w.rows - w.rb * RB);
             const int tiles = w.tb - w.ta;
             if (r * 128 < nlive) {
@@ -484,16 +531,27 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // ---- the tile's maximum
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        tc_ld32(t_s + c * 32, v);
+                    for (int c = 0; c < 2; ++c) {
+                        float v0[32], v1[32];
+                        tc_ld32_async(t_s + c * 64, v0);
+                        tc_ld32_async(t_s + c * 64 + 32, v1);
+                        tc_ld_wait(v0);
+                        tc_ld_tie(v1);
                         if (edge) {
+                            const int n_in = lim - key0 - c * 64;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (key0 + c * 32 + k < lim) mx = fmaxf(mx, v[k]);
+                            for (int k = 0; k < 32; ++k) {
+                                if (k < n_in) mx = fmaxf(mx, v0[k]);
+                                if (k + 32 < n_in) mx = fmaxf(mx, v1[k]);
+                            }
                         } else {
+                            float ma = -INFINITY, mb = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+                            for (int k = 0; k < 32; k += 2) {
+                                mx = fmaxf(mx, fmaxf(v0[k], v0[k + 1]));
+                                ma = fmaxf(ma, fmaxf(v1[k], v1[k + 1]));
+                            }
+                            mx = fmaxf(mx, fmaxf(ma, mb));
                         }
                     }
                     mx *= f;  // (-inf times zero: no key seen, or a scale of zero)
@@ -519,7 +577,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             ok = __all_sync(FULL, wait(&odone[r], (nr - 1) & 1));
                             if (!ok) break;
                             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 float v[32];
                                 uint32_t o[32];
@@ -533,23 +591,43 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     }
                     // ---- weights
                     const float sub = m == -INFINITY ? 0.f : m;
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                    const float2 f2 = make_float2(f, f), s2 = make_float2(-sub, -sub);
+                    float2 acc[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        uint32_t o[16];
-                        tc_ld32(t_s + c * 32, v);
+                    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            v[k] = ex2(fmaf(v[k], f, -sub));
-                            if (edge && key0 + c * 32 + k >= lim) v[k] = 0.f;
-                            acc[k & 3] += v[k];
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        float v0[32], v1[32];
+                        tc_ld32_async(t_s + c * 64, v0);
+                        tc_ld32_async(t_s + c * 64 + 32, v1);
+                        tc_ld_wait(v0);
+                        tc_ld_tie(v1);
+                        uint32_t o[32];
+                        auto weigh = [&](float *v, uint32_t *to, int first) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = pack_f16(v[2 * k], v[2 * k + 1]);
-                        tc_st16(t_s + c * 16, o);
+                            for (int k = 0; k < 32; k += 2) {
+                                const float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
+                                v[k] = ex2(x.x);
+                                v[k + 1] = ex2(x.y);
+                            }
+                            if (edge) {
+                                const int n_in = lim - key0 - first;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k)
+                                    if (k >= n_in) v[k] = 0.f;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 32; k += 2) {
+                                acc[(k / 2) & 3] = add2(acc[(k / 2) & 3], make_float2(v[k], v[k + 1]));
+                                to[k / 2] = pack_f16(v[k], v[k + 1]);
+                            }
+                        };
+                        weigh(v0, o, c * 64);
+                        weigh(v1, o + 16, c * 64 + 32);
+                        tc_st32(t_s + c * 32, o);
                     }
-                    l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                    acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+                    l += acc[0].x + acc[0].y;
                     if (pt.bad[0] | pt.bad[1] | pt.bad[2] | pt.bad[3]) {
                         // a value that is not finite leaves the products; the
                         // rows that see it are not finite either
@@ -580,15 +658,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             for (int k = 0; k < 4; ++k) {
                                 const float *x = v + 8 * k;
                                 dst[c * 4 + k] = make_uint4(
-                                    pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv),
-                                    pack_bf16(x[4] * inv, x[5] * inv), pack_bf16(x[6] * inv, x[7] * inv));
+                                    pack_bf16(x[0] * kVDown * inv, x[1] * kVDown * inv),
+                                    pack_bf16(x[2] * kVDown * inv, x[3] * kVDown * inv),
+                                    pack_bf16(x[4] * kVDown * inv, x[5] * kVDown * inv),
+                                    pack_bf16(x[6] * kVDown * inv, x[7] * kVDown * inv));
                             }
                         } else if (live) {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 reinterpret_cast<float4 *>(part + c * 32)[k] =
-                                    make_float4(v[4 * k] * v_down, v[4 * k + 1] * v_down,
-                                                v[4 * k + 2] * v_down, v[4 * k + 3] * v_down);
+                                    make_float4(v[4 * k] * kVDown * v_down, v[4 * k + 1] * kVDown * v_down,
+                                                v[4 * k + 2] * kVDown * v_down, v[4 * k + 3] * kVDown * v_down);
                         }
                     }
                     if (live && !whole) {
@@ -610,146 +690,202 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             begin += tiles;
             piece = 1;
         }
-    } else if (warp >= kPfDeq0) {
-        // ------------------------------------------------ keys and values
-        const int dw = warp - kPfDeq0;
-        constexpr int KU = L::KU, VU = L::VU, RCH = L::RCH, VW = L::VW;
-        constexpr int KBS = 128 / L::KB;  // key blocks of a tile
-        const int pmask = (1 << p.kv.page_shift) - 1;
-        const int kl = RCH >= 4 ? lane & 7 : (lane & 7) + 8 * (lane >> 4);  // key of a key unit
-        const int kc = RCH >= 4 ? lane >> 3 : (lane >> 3) & 1;              // chunk of it
-        const int vc = lane & 7, vd = lane >> 3;  // 8 keys and 8 dimensions of a value unit
+    } else if (warp == 2 || warp == 3) {
+        // ------------------------------------------------ parameters
+        // Warp 2 the keys', warp 3 the values': a tile's power of two, then
+        // its parameters on that scale as fp16; the keys' further columns.
+        const bool is_k = warp == 2;
+        const uint32_t *src = is_k ? p.kv.kp : p.kv.vp;
         uint32_t n = 0;
         bool ok = true;
-        while (ok && pf_next<RB>(p, cur, w)) {
-            const int32_t *table = p.kv.page_table + (int64_t)w.b * p.kv.max_pages;
-            // page numbers of a tile's eight 16-key blocks, on lanes 0..7
-            auto pages_of = [&](int tile) {
-                const int key = tile * 128 + lane * 16;
-                int pg = 0;
-                if (tile < w.tb && lane < 8 && key < w.s.len) {
-                    pg = table[key >> p.kv.page_shift];
-                    if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
-                        if (p.status) atomicOr(p.status, (int)kKvBadPage);
-                        pg = 0;
-                    }
-                }
-                return pg;
-            };
-            // a key's row in the code and parameter arrays (every lane calls)
-            auto row_of = [&](int pg, int tile, int k) {
-                const int page = __shfl_sync(FULL, pg, k >> 4);
-                return (((int64_t)page * p.kv.heads + w.hk) << p.kv.page_shift) +
-                       ((tile * 128 + k) & pmask);
-            };
-            float v_lim = -1.f, v_up = 1.f, v_down = 1.f;  // value range met so far
-            uint4 kreg[KU];
-            uint32_t kpar[KU];
-            uint32_t vreg[VU][8][VW], vpar[VU][8];
-            uint32_t xk[4][G], xv[4][G];  // parameters of keys 4 lane + j
-            auto load_k = [&](int pg, int tile) {
-                const int left = w.s.len - tile * 128;  // keys of the tile
-#pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    const int id = dw + u * kPfDeqWarps;
-                    const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
-                    const int64_t row = row_of(pg, tile, k);
-                    kreg[u] = make_uint4(0u, 0u, 0u, 0u);
-                    kpar[u] = 0u;
-                    if (k < left) {
-                        kreg[u] = reinterpret_cast<const uint4 *>(p.kv.kq)[row * RCH + c];
-                        kpar[u] = p.kv.kp[row * G + c / (RCH / G)];
-                    }
-                }
-                const int64_t row = row_of(pg, tile, 4 * lane);
+        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
+            const PfPages pages{p, w.s.len, w.tb, w.hk, w.b};
+            float v_lim = -1.f, up = 1.f, down = 1.f;
+            uint32_t x[4][G];  // keys 4 lane + j
+            auto load = [&](int64_t base, int tile) {
+                const int64_t row = __shfl_sync(FULL, base, lane >> 2) + (lane & 3) * 4;
+                const int left = w.s.len - tile * 128;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const bool in = 4 * lane + j < left;
-                        xk[j][g] = in ? p.kv.kp[(row + j) * G + g] : 0u;
-                        xv[j][g] = in ? p.kv.vp[(row + j) * G + g] : 0u;
-                    }
+                    for (int g = 0; g < G; ++g)
+                        x[j][g] = 4 * lane + j < left ? src[(row + j) * G + g] : 0u;
             };
-            auto load_v = [&](int pg, int tile) {
-                const int left = w.s.len - tile * 128;
-#pragma unroll
-                for (int u = 0; u < VU; ++u) {
-                    const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
-                    const int k0 = id % 2 * 64 + vc * 8, d32 = id / 2;
-                    const int64_t row = row_of(pg, tile, k0 & 127);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const bool in = id < L::VUNITS && k0 + j < left;
-#pragma unroll
-                        for (int x = 0; x < VW; ++x) vreg[u][j][x] = 0u;
-                        vpar[u][j] = 0u;
-                        if (in) {
-                            const uint32_t *src = p.kv.vq + (row + j) * (D * BITS / 32) + d32 * BITS + vd * VW;
-                            if constexpr (VW == 1) {
-                                vreg[u][j][0] = *src;
-                            } else {
-                                const uint2 t = *reinterpret_cast<const uint2 *>(src);
-                                vreg[u][j][0] = t.x;
-                                vreg[u][j][1] = t.y;
-                            }
-                            vpar[u][j] = p.kv.vp[(row + j) * G + d32 / 2];
-                        }
-                    }
-                }
-            };
-            int pg = pages_of(w.ta), pg1 = pages_of(w.ta + 1);
-            load_k(pg, w.ta);
-            load_v(pg, w.ta);
+            int64_t base = pages.look(w.ta, lane);
+            load(base, w.ta);
+            base = pages.look(w.ta + 1, lane);
             for (int tile = w.ta; ok && tile < w.tb; ++tile, ++n) {
-                const int st = n % ST;
-                const int left = w.s.len - tile * 128;
-                // ---- the tile's ranges, from every parameter (each warp for
-                // itself, the same result)
-                float tk = 0.f, tv = 0.f;
+                const uint32_t slot = n % kPfSlots;
+                float t = 0.f;
                 uint32_t bad = 0u;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        const float ks = fabsf(bf16_lo(xk[j][g]));
-                        const float kb = fabsf(fmaf(KC, bf16_lo(xk[j][g]), bf16_hi(xk[j][g])));
-                        if (ks < INFINITY && kb < INFINITY) tk = fmaxf(tk, fmaxf(KC * ks, kb));
-                        const float vs = fabsf(bf16_lo(xv[j][g]));
-                        const float vb = fabsf(fmaf(KC, bf16_lo(xv[j][g]), bf16_hi(xv[j][g])));
-                        const float t = fmaf(KC, vs, vb);
-                        if (t < INFINITY)
-                            tv = fmaxf(tv, t);
-                        else
+                        const float s = fabsf(bf16_lo(x[j][g]));
+                        const float b = fabsf(fmaf(KC, bf16_lo(x[j][g]), bf16_hi(x[j][g])));
+                        const float e = fmaf(KC, s, b);
+                        if (e < INFINITY) {
+                            t = fmaxf(t, e);
+                        } else {
                             bad |= 1u << j;
+                            // a value that is not finite does not enter the
+                            // products (the rows that see it are told)
+                            if (!is_k) x[j][g] = 0u;
+                        }
                     }
-                tk = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(tk)));
-                tv = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(tv)));
-                float k_up, k_down;
-                range_scale(tk, k_up, k_down);
-                if (tv > v_lim) {
-                    // into [2^14, 2^15), with a further 2 to grow before the next
-                    range_scale(tv, v_up, v_down);
-                    v_lim = 32768.f * v_down;
+                t = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(t)));
+                if (is_k) {
+                    range_scale(t, up, down);
+                } else if (t > v_lim || (t > 0.f && t < v_lim * 0x1p-7f)) {
+                    // [2^14, 2^15), and kVDown below: into [2^-7, 2^-6), where
+                    // scale 2^24 is in range too, with a further 2 to grow and
+                    // 2^7 to shrink
+                    range_scale(t, up, down);
+                    v_lim = t > 0.f ? 32768.f * down : -1.f;
                 }
-                if (dw == 0) {
-                    const uint32_t b0 = __ballot_sync(FULL, bad & 1u), b1 = __ballot_sync(FULL, bad & 2u);
-                    const uint32_t b2 = __ballot_sync(FULL, bad & 4u), b3 = __ballot_sync(FULL, bad & 8u);
-                    if (lane == 0)
-                        s_tile[n % kPfSlots] = PfTile{k_down, v_up, v_down, {b0, b1, b2, b3}};
-                }
-                // ---- keys
-                if (n >= ST) {
-                    ok = __all_sync(FULL, wait(&kempty[st], ((n / ST) & 1) ^ 1));
+                const float to = is_k ? up : up * (1.f / kVDown);
+                if (n >= kPfSlots) {
+                    ok = __all_sync(FULL, wait(&rempty[slot], ((n / kPfSlots) & 1) ^ 1));
                     if (!ok) break;
                 }
+                unsigned char *par = smem + L::P_OFF + slot * L::PAR + lane * 8;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    float s[4], b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[j] = bf16_lo(x[j][g]) * to;
+                        b[j] = bf16_hi(x[j][g]) * to;
+                    }
+                    if (is_k) {
+                        *reinterpret_cast<uint2 *>(par + g * 256) =
+                            make_uint2(pack_f16(s[0], s[1]), pack_f16(s[2], s[3]));
+                    } else {
+                        constexpr float c = 0x1p24f;  // codes enter as c 2^-24
+                        *reinterpret_cast<uint2 *>(par + (G + g) * 256) =
+                            make_uint2(pack_f16(s[0] * c, s[1] * c), pack_f16(s[2] * c, s[3] * c));
+                        *reinterpret_cast<uint2 *>(par + (2 * G + g) * 256) =
+                            make_uint2(pack_f16(b[0], b[1]), pack_f16(b[2], b[3]));
+                    }
+                }
+                if (is_k) {
+                    if (lane == 0) s_tile[slot].k_down = down;
+                } else {
+                    uint32_t m[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) m[j] = __ballot_sync(FULL, (bad >> j) & 1u);
+                    if (lane == 0) {
+                        s_tile[slot].v_up = up;
+                        s_tile[slot].v_down = down;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s_tile[slot].bad[j] = m[j];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&rfull[slot]);
+                if (is_k) {
+                    // b' as (hi, hi, lo) per group
+                    if (n >= ST) {
+                        ok = __all_sync(FULL, wait(&kempty[n % ST], ((n / ST) & 1) ^ 1));
+                        if (!ok) break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float e[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) e[k] = 0.f;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            const float b = fmaf(KC, bf16_lo(x[j][g]), bf16_hi(x[j][g])) * up;
+                            const float hi = __half2float(__float2half_rn(b));
+                            e[3 * g] = e[3 * g + 1] = hi;
+                            e[3 * g + 2] = b - hi;
+                        }
+                        const int k = 4 * lane + j;
+                        unsigned char *kx = smem + L::KX_OFF + (size_t)(n % ST) * L::EXT + (k >> 3) * 128 + (k & 7) * 16;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<uint4 *>(kx + h * 2048) =
+                                make_uint4(pack_f16(e[8 * h], e[8 * h + 1]), pack_f16(e[8 * h + 2], e[8 * h + 3]),
+                                           pack_f16(e[8 * h + 4], e[8 * h + 5]), pack_f16(e[8 * h + 6], e[8 * h + 7]));
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kfull[n % ST]);
+                }
+                if (tile + 1 < w.tb) load(base, tile + 1);
+                base = pages.look(tile + 2, lane);
+            }
+        }
+    } else if (warp >= kPfDeq0) {
+        // ------------------------------------------------ keys and values
+        const int dw = warp - kPfDeq0;
+        constexpr int KU = L::KU, VU = L::VU, RCH = L::RCH, VW = L::VW;
+        constexpr int KBS = 128 / L::KB;  // key blocks of a tile
+        const int kl = RCH >= 4 ? lane & 7 : (lane & 7) + 8 * (lane >> 4);  // key of a key unit
+        const int kc = RCH >= 4 ? lane >> 3 : (lane >> 3) & 1;              // chunk of it
+        const int vc = lane & 7, vd = lane >> 3;  // 8 keys and 8 dimensions of a value unit
+        uint32_t n = 0;
+        bool ok = true;
+        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
+            const PfPages pages{p, w.s.len, w.tb, w.hk, w.b};
+            uint4 kreg[KU];
+            uint32_t vreg[VU][8][VW];
+            auto load_k = [&](int64_t base, int tile) {
+                const int left = w.s.len - tile * 128;  // keys of the tile
+#pragma unroll
+                for (int u = 0; u < KU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;
+                    const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
+                    const int64_t row = __shfl_sync(FULL, base, k >> 4) + (k & 15);
+                    kreg[u] = make_uint4(0u, 0u, 0u, 0u);
+                    if (k < left) kreg[u] = reinterpret_cast<const uint4 *>(p.kv.kq)[row * RCH + c];
+                }
+            };
+            auto load_v = [&](int64_t base, int tile) {
+                const int left = w.s.len - tile * 128;
+#pragma unroll
+                for (int u = 0; u < VU; ++u) {
+                    const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
+                    const int k0 = id % 2 * 64 + vc * 8, d32 = id / 2;
+                    const int64_t row = __shfl_sync(FULL, base, k0 >> 4) + (k0 & 15);
+                    const uint32_t *src = p.kv.vq + row * (D * BITS / 32) + d32 * BITS + vd * VW;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                        for (int x = 0; x < VW; ++x) vreg[u][j][x] = 0u;
+                        if (id < L::VUNITS && k0 + j < left) {
+                            if constexpr (VW == 1) {
+                                vreg[u][j][0] = src[j * (D * BITS / 32)];
+                            } else {
+                                const uint2 t = *reinterpret_cast<const uint2 *>(src + j * (D * BITS / 32));
+                                vreg[u][j][0] = t.x;
+                                vreg[u][j][1] = t.y;
+                            }
+                        }
+                    }
+                }
+            };
+            int64_t base = pages.look(w.ta, lane);
+            load_k(base, w.ta);
+            load_v(base, w.ta);
+            base = pages.look(w.ta + 1, lane);
+            for (int tile = w.ta; ok && tile < w.tb; ++tile, ++n) {
+                const int st = n % ST;
+                const uint32_t slot = n % kPfSlots;
+                const unsigned char *par = smem + L::P_OFF + slot * L::PAR;
+                ok = __all_sync(FULL, wait(&rfull[slot], (n / kPfSlots) & 1));
+                // ---- keys: scale (code - centre), exact
+                if (ok && n >= ST) ok = __all_sync(FULL, wait(&kempty[st], ((n / ST) & 1) ^ 1));
+                if (!ok) break;
                 unsigned char *kt = smem + L::K_OFF + (size_t)st * L::TILE;
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
                     const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
-                    const float sc = bf16_lo(kpar[u]) * k_up;
-                    const __half2 s2 = __floats2half2_rn(sc, sc);
+                    const __half2 s2 = __half2half2(
+                        *reinterpret_cast<const __half *>(par + c / (RCH / G) * 256 + k * 2));
                     const uint32_t wd[4] = {kreg[u].x, kreg[u].y, kreg[u].z, kreg[u].w};
                     if constexpr (BITS == 4) {
                         const __half2 off = __floats2half2_rn(1032.f, 1032.f);
@@ -784,36 +920,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         }
                     }
                 }
-                // the further columns of 16 keys: b' as (hi, hi, lo) per group
-                if (lane / 4 == dw) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float e[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) e[x] = 0.f;
-#pragma unroll
-                        for (int g = 0; g < G; ++g) {
-                            const float x = fmaf(KC, bf16_lo(xk[j][g]), bf16_hi(xk[j][g])) * k_up;
-                            const float hi = __half2float(__float2half_rn(x));
-                            e[3 * g] = e[3 * g + 1] = hi;
-                            e[3 * g + 2] = x - hi;
-                        }
-                        const int k = 4 * lane + j;
-                        unsigned char *kx = smem + L::KX_OFF + (size_t)st * L::EXT + (k >> 3) * 128 + (k & 7) * 16;
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            *reinterpret_cast<uint4 *>(kx + x * 2048) =
-                                make_uint4(pack_f16(e[8 * x], e[8 * x + 1]), pack_f16(e[8 * x + 2], e[8 * x + 3]),
-                                           pack_f16(e[8 * x + 4], e[8 * x + 5]), pack_f16(e[8 * x + 6], e[8 * x + 7]));
-                    }
-                }
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&kfull[st]);
-                const int pg2 = pages_of(tile + 2);
-                if (tile + 1 < w.tb) load_k(pg1, tile + 1);
+                if (tile + 1 < w.tb) load_k(base, tile + 1);
 
-                // ---- values, transposed
+                // ---- values, transposed: code 2^-24 (an fp16 subnormal) times
+                // scale 2^24 plus bias
                 if (n >= ST) {
                     ok = __all_sync(FULL, wait(&vempty[st], ((n / ST) & 1) ^ 1));
                     if (!ok) break;
@@ -824,25 +937,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     if (id >= L::VUNITS) break;
                     unsigned char *vt = smem + L::V_OFF + (size_t)st * L::TILE + (id % 2) * (D * 128);
                     const int d0 = id / 2 * 32 + vd * 8;
-                    __half2 s2[4], b2[4];
+                    const unsigned char *vp = par + (G + id / 4) * 256 + (id % 2 * 64 + vc * 8) * 2;
+                    const uint4 sw = *reinterpret_cast<const uint4 *>(vp);
+                    const uint4 bw = *reinterpret_cast<const uint4 *>(vp + G * 256);
+                    const __half2 s2[4] = {bits_h2(sw.x), bits_h2(sw.y), bits_h2(sw.z), bits_h2(sw.w)};
+                    const __half2 b2[4] = {bits_h2(bw.x), bits_h2(bw.y), bits_h2(bw.z), bits_h2(bw.w)};
+                    __half2 t2[4];  // for codes left at bits 4-7: 16 c 2^-24
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float s[2], b[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const uint32_t t = vpar[u][2 * j + x];
-                            s[x] = bf16_lo(t) * v_up;
-                            b[x] = fmaf(KC, bf16_lo(t), bf16_hi(t)) * v_up;
-                            // not finite (or past the end): nothing enters
-                            if (!(fabsf(s[x]) < INFINITY && fabsf(b[x]) < INFINITY)) s[x] = b[x] = 0.f;
-                        }
-                        s2[j] = __floats2half2_rn(s[0], s[1]);
-                        b2[j] = __floats2half2_rn(b[0], b[1]);
-                    }
-                    const __half2 off4 = __floats2half2_rn(1032.f, 1032.f);
-                    const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
-                    const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
-                    const __half2 off8 = __floats2half2_rn(1152.f, 1152.f);
+                    for (int j = 0; j < 4; ++j) t2[j] = __hmul2(s2[j], __floats2half2_rn(0.0625f, 0.0625f));
 #pragma unroll
                     for (int jj = 0; jj < 4; ++jj) {
                         uint32_t lo[4], hi[4];  // dimensions 2 jj, 2 jj + 1 of the 8
@@ -851,19 +953,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             if constexpr (BITS == 4) {
                                 const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
                                 const uint32_t t = __byte_perm(vreg[u][2 * j][0], vreg[u][2 * j + 1][0], sel);
-                                lo[j] = h2_bits(__hfma2(
-                                    __hsub2(bits_h2((t & 0x000f000fu) | 0x64006400u), off4), s2[j], b2[j]));
-                                hi[j] = h2_bits(__hfma2(
-                                    __hfma2(bits_h2((t & 0x00f000f0u) | 0x64006400u), r16, m72), s2[j], b2[j]));
+                                lo[j] = h2_bits(__hfma2(bits_h2(t & 0x000f000fu), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(bits_h2(t & 0x00f000f0u), t2[j], b2[j]));
                             } else {
                                 const int e = 2 * (jj & 1);
                                 const uint32_t sel = e | ((e + 1) << 4) | ((4 + e) << 8) | ((5 + e) << 12);
                                 const uint32_t t = __byte_perm(vreg[u][2 * j][VW == 2 ? jj / 2 : 0],
                                                                vreg[u][2 * j + 1][VW == 2 ? jj / 2 : 0], sel);
-                                lo[j] = h2_bits(__hfma2(
-                                    __hsub2(bits_h2((t & 0x00ff00ffu) | 0x64006400u), off8), s2[j], b2[j]));
-                                hi[j] = h2_bits(__hfma2(
-                                    __hsub2(bits_h2(((t >> 8) & 0x00ff00ffu) | 0x64006400u), off8), s2[j], b2[j]));
+                                lo[j] = h2_bits(__hfma2(bits_h2(t & 0x00ff00ffu), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(bits_h2((t >> 8) & 0x00ff00ffu), s2[j], b2[j]));
                             }
                         }
                         unsigned char *row = vt + (d0 + 2 * jj) * 128;
@@ -876,9 +974,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&vfull[st]);
-                if (tile + 1 < w.tb) load_v(pg1, tile + 1);
-                pg1 = pg2;
-                (void)left;
+                if (tile + 1 < w.tb) load_v(base, tile + 1);
+                base = pages.look(tile + 2, lane);
             }
         }
     }
