@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             bool ok = true;
             // scores of row tile r against the keys of stage st into buffer s
             auto scores = [&](int r, int st, int s) {
-#pragma unroll
+#pragma unroll 1
                 for (int g = 0; g < G; ++g)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 tc_commit(&sfull[s]);
             };
             auto values = [&](int r, int st, int s, bool first) {
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -528,9 +528,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     const float f = fac * pt.k_down;
                     const int key0 = (w.ta + i) * 128;
                     const bool edge = key0 + 128 > least;
-                    // ---- the tile's maximum
+                    // ---- the tile's maximum (rolled loops here and below: the
+                    // warps' code together is more than the instruction caches
+                    // hold close)
                     float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         float v0[32], v1[32];
                         tc_ld32_async(t_s + c * 64, v0);
@@ -595,7 +597,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     float2 acc[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
                         float v0[32], v1[32];
                         tc_ld32_async(t_s + c * 64, v0);
@@ -945,21 +947,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     __half2 t2[4];  // for codes left at bits 4-7: 16 c 2^-24
 #pragma unroll
                     for (int j = 0; j < 4; ++j) t2[j] = __hmul2(s2[j], __floats2half2_rn(0.0625f, 0.0625f));
-#pragma unroll
+#pragma unroll 1
                     for (int jj = 0; jj < 4; ++jj) {
                         uint32_t lo[4], hi[4];  // dimensions 2 jj, 2 jj + 1 of the 8
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if constexpr (BITS == 4) {
-                                const uint32_t sel = jj | (jj << 4) | ((4 + jj) << 8) | ((4 + jj) << 12);
+                                const uint32_t sel = 0x4400u + 0x1111u * jj;
                                 const uint32_t t = __byte_perm(vreg[u][2 * j][0], vreg[u][2 * j + 1][0], sel);
                                 lo[j] = h2_bits(__hfma2(bits_h2(t & 0x000f000fu), s2[j], b2[j]));
                                 hi[j] = h2_bits(__hfma2(bits_h2(t & 0x00f000f0u), t2[j], b2[j]));
                             } else {
-                                const int e = 2 * (jj & 1);
-                                const uint32_t sel = e | ((e + 1) << 4) | ((4 + e) << 8) | ((5 + e) << 12);
-                                const uint32_t t = __byte_perm(vreg[u][2 * j][VW == 2 ? jj / 2 : 0],
-                                                               vreg[u][2 * j + 1][VW == 2 ? jj / 2 : 0], sel);
+                                const uint32_t sel = 0x5410u + 0x2222u * (jj & 1);
+                                const uint32_t t =
+                                    __byte_perm(jj < 2 ? vreg[u][2 * j][0] : vreg[u][2 * j][VW - 1],
+                                                jj < 2 ? vreg[u][2 * j + 1][0] : vreg[u][2 * j + 1][VW - 1], sel);
                                 lo[j] = h2_bits(__hfma2(bits_h2(t & 0x00ff00ffu), s2[j], b2[j]));
                                 hi[j] = h2_bits(__hfma2(bits_h2((t >> 8) & 0x00ff00ffu), s2[j], b2[j]));
                             }
