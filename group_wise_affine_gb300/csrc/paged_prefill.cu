@@ -26,7 +26,8 @@
 // the row's factor f, the values' only ever grows within a block and rescales
 // O as the maximum does.
 //
-// Warps: 0 issues the MMAs (one thread) and owns the tensor memory; 4-7 and
+// Warps: 0 and 1 issue the MMAs (a thread each); 2 and 3 turn the keys' and
+// the values' parameters into fp16 on the tile's power of two; 4-7 and
 // 8-11 are the softmax of row tiles 0 and 1 (with one row tile of 256
 // dimensions 4-7 alone), they also load and convert the queries and write the
 // output; 12-19 unpack keys and values from global memory into the operand
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t kfull[ST], kempty[ST], vfull[ST], vempty[ST];
-    __shared__ uint64_t sfull[2], pfull[2], odone[MT], ofree[MT], qfull[MT];
+    __shared__ uint64_t sfull[2], pfull[2], odone[2], ofree[MT], qfull[MT];
     __shared__ PfTile s_tile[kPfSlots];
     __shared__ PfCursor s_cur[kPfThreads / 32];
     __shared__ PfPiece s_piece[kPfThreads / 32];
@@ -250,21 +251,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         for (int i = 0; i < ST; ++i) {
             mbar_init(&kfull[i], kPfDeqWarps + 1);
             mbar_init(&vfull[i], kPfDeqWarps);
-            mbar_init(&kempty[i], 1);
-            mbar_init(&vempty[i], 1);
+            mbar_init(&kempty[i], MT);
+            mbar_init(&vempty[i], MT);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
+            mbar_init(&odone[i], 1);
             mbar_init(&pfull[i], 4);
         }
         for (int i = 0; i < MT; ++i) {
-            mbar_init(&odone[i], 1);
             mbar_init(&ofree[i], 4);
             mbar_init(&qfull[i], 4);
         }
         for (int i = 0; i < kPfSlots; ++i) {
             mbar_init(&rfull[i], 2);
-            mbar_init(&rempty[i], 1);
+            mbar_init(&rempty[i], MT);
         }
         fence_mbar_init();
         s_fail = 0;
@@ -336,8 +337,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         return false;
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------ MMA issuer
+    if (warp < 2) {
+        // ------------------------------------------------ MMA issuers
+        // Two row tiles: a warp each issues a tile's scores and values.  One:
+        // warp 0 issues the scores, a tile ahead, warp 1 the values.  (One
+        // thread for all of them spent about 100 cycles on an MMA of 64.)
         if (lane == 0) {
             constexpr uint32_t id_s = pf_idesc(128), id_o = pf_idesc(D);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::Q_OFF));
@@ -345,81 +349,79 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + L::V_OFF));
             const uint64_t qx_desc = smem_desc_ext(smem_u32(smem + L::QX_OFF));
             const uint64_t kx_desc = smem_desc_ext(smem_u32(smem + L::KX_OFF));
-            uint32_t n = 0;               // tiles so far
-            uint32_t nr[2] = {0, 0};      // tiles of each row tile (one: of each buffer)
-            uint32_t pieces[2] = {0, 0};  // blocks of each row tile
+            uint32_t n = 0;       // tiles so far
+            uint32_t nr = 0;      // of this row tile
+            uint32_t pieces = 0;  // blocks of this row tile
             bool ok = true;
             // scores of row tile r against the keys of stage st into buffer s
             auto scores = [&](int r, int st, int s) {
-#pragma unroll 1
-                for (int g = 0; g < G; ++g)
+                const uint32_t d = tmem + s * 128;
+                uint64_t a = q_desc + (uint64_t)((r * L::TILE) >> 4);
+                uint64_t b = k_desc + (uint64_t)((st * L::TILE) >> 4);
+                tc_mma_ss(d, qx_desc + (uint64_t)((r * L::EXT) >> 4),
+                          kx_desc + (uint64_t)((st * L::EXT) >> 4), id_s, 0u);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_ss(tmem + s * 128,
-                                  q_desc + (uint64_t)((r * L::TILE + g * 16384) >> 4) + 2 * k,
-                                  k_desc + (uint64_t)((st * L::TILE + g * 16384) >> 4) + 2 * k, id_s,
-                                  g | k);
-                tc_mma_ss(tmem + s * 128, qx_desc + (uint64_t)((r * L::EXT) >> 4),
-                          kx_desc + (uint64_t)((st * L::EXT) >> 4), id_s, 1u);
+                for (int k = 0; k < 4 * G; ++k)
+                    tc_mma_ss(d, a + (k / 4) * 1024 + 2 * (k % 4), b + (k / 4) * 1024 + 2 * (k % 4),
+                              id_s, 1u);
                 tc_commit(&sfull[s]);
             };
             auto values = [&](int r, int st, int s, bool first) {
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h)
+                const uint32_t d = tmem + L::O_COL + r * D, a = tmem + s * 128;
+                const uint64_t b = v_desc + (uint64_t)((st * L::TILE) >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_ts(tmem + L::O_COL + r * D, tmem + s * 128 + (h * 4 + k) * 8,
-                                  v_desc + (uint64_t)((st * L::TILE + h * D * 128) >> 4) + 2 * k, id_o,
-                                  first && (h | k) == 0 ? 0u : 1u);
-                tc_commit(&odone[r]);
+                for (int k = 0; k < 8; ++k)
+                    tc_mma_ts(d, a + k * 8, b + (k / 4) * (D * 8) + 2 * (k % 4), id_o,
+                              first && k == 0 ? 0u : 1u);
+                tc_commit(&odone[s]);
+                tc_commit(&vempty[st]);
             };
             while (ok && pf_step<RB>(p, *cur, s_piece[warp])) {
                 const int nlive = min(RB, w.rows - w.rb * RB);
-                const int mt = MT == 2 && nlive > 128 ? 2 : 1;
                 const int tiles = w.tb - w.ta;
-                for (int r = 0; ok && r < mt; ++r) ok = wait(&qfull[r], pieces[r] & 1);
-                // the first tile's scores
-                ok = ok && wait(&kfull[n % ST], (n / ST) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                for (int r = 0; r < mt; ++r) scores(r, n % ST, MT == 2 ? r : (int)(n & 1));
-                tc_commit(&kempty[n % ST]);
-                for (int i = 0; ok && i < tiles; ++i, ++n) {
-                    const int st = n % ST, st1 = (n + 1) % ST;
-                    const bool more = i + 1 < tiles;
-                    if (MT == 1 && more) {
-                        // one row tile: the next scores before these values
-                        ok = wait(&kfull[st1], ((n + 1) / ST) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(0, st1, (n + 1) & 1);
-                        tc_commit(&kempty[st1]);
+                if (MT == 2 && warp * 128 >= nlive) {
+                    // no rows here: the stages are free as soon as they are full
+                    for (int i = 0; ok && i < tiles; ++i, ++n) {
+                        ok = wait(&kfull[n % ST], (n / ST) & 1);
+                        if (ok) mbar_arrive(&kempty[n % ST]);
+                        ok = ok && wait(&vfull[n % ST], (n / ST) & 1);
+                        if (ok) {
+                            mbar_arrive(&vempty[n % ST]);
+                            mbar_arrive(&rempty[n % kPfSlots]);
+                        }
                     }
-                    ok = wait(&vfull[st], (n / ST) & 1);
-                    for (int r = 0; ok && r < mt; ++r) {
-                        const int s = MT == 2 ? r : (int)(n & 1);
-                        ok = wait(&pfull[s], nr[s] & 1);
-                        if (ok && i == 0 && pieces[r] > 0) ok = wait(&ofree[r], (pieces[r] - 1) & 1);
+                    continue;
+                }
+                const int r = MT == 2 ? warp : 0;
+                if (MT == 2 || warp == 0) ok = wait(&qfull[r], pieces & 1);
+                for (int i = MT == 2 ? -1 : 0; ok && i < tiles; ++i) {
+                    // two row tiles: values of tile i, then scores of i + 1
+                    const uint32_t at = n + i, nx = MT == 2 ? at + 1 : at;
+                    const bool first = i == 0;
+                    if ((MT == 2 && i >= 0) || (MT == 1 && warp == 1)) {
+                        const int st = at % ST, s = MT == 2 ? r : (int)(at & 1);
+                        ok = wait(&vfull[st], (at / ST) & 1) &&
+                             wait(&pfull[s], (MT == 2 ? nr : at >> 1) & 1);
+                        if (ok && first && pieces > 0) ok = wait(&ofree[r], (pieces - 1) & 1);
                         if (!ok) break;
-                        ++nr[s];
+                        ++nr;
                         tc_fence_after();
-                        values(r, st, s, i == 0);
-                        if (r == mt - 1) {
-                            tc_commit(&vempty[st]);
-                            tc_commit(&rempty[n % kPfSlots]);
-                        }
-                        if (MT == 2 && more) {
-                            if (r == 0) {
-                                ok = wait(&kfull[st1], ((n + 1) / ST) & 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                            }
-                            scores(r, st1, r);
-                            if (r == mt - 1) tc_commit(&kempty[st1]);
-                        }
+                        values(r, st, s, first);
+                        tc_commit(&rempty[at % kPfSlots]);
+                    }
+                    if ((MT == 2 && i + 1 < tiles) || (MT == 1 && warp == 0)) {
+                        const int st = nx % ST, s = MT == 2 ? r : (int)(nx & 1);
+                        ok = wait(&kfull[st], (nx / ST) & 1);
+                        // one row tile: the buffer's last weights are used
+                        if (MT == 1 && ok && nx >= 2) ok = wait(&odone[s], ((nx >> 1) - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(r, st, s);
+                        tc_commit(&kempty[st]);
                     }
                 }
-                for (int r = 0; r < mt; ++r) ++pieces[r];
+                n += tiles;
+                ++pieces;
             }
         }
     } else if (warp >= 4 && warp < 4 + 4 * MT) {
@@ -533,27 +535,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // hold close)
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float v0[32], v1[32];
-                        tc_ld32_async(t_s + c * 64, v0);
-                        tc_ld32_async(t_s + c * 64 + 32, v1);
-                        tc_ld_wait(v0);
-                        tc_ld_tie(v1);
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        tc_ld32(t_s + c * 32, v);
                         if (edge) {
-                            const int n_in = lim - key0 - c * 64;
+                            const int n_in = lim - key0 - c * 32;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                if (k < n_in) mx = fmaxf(mx, v0[k]);
-                                if (k + 32 < n_in) mx = fmaxf(mx, v1[k]);
-                            }
+                            for (int k = 0; k < 32; ++k)
+                                if (k < n_in) mx = fmaxf(mx, v[k]);
                         } else {
-                            float ma = -INFINITY, mb = -INFINITY;
+                            float ma = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                mx = fmaxf(mx, fmaxf(v0[k], v0[k + 1]));
-                                ma = fmaxf(ma, fmaxf(v1[k], v1[k + 1]));
+                            for (int k = 0; k < 32; k += 4) {
+                                mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
+                                ma = fmaxf(ma, fmaxf(v[k + 2], v[k + 3]));
                             }
-                            mx = fmaxf(mx, fmaxf(ma, mb));
+                            mx = fmaxf(mx, ma);
                         }
                     }
                     mx *= f;  // (-inf times zero: no key seen, or a scale of zero)
@@ -576,7 +573,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             v_down = pt.v_down;
                         }
                         if (__any_sync(FULL, corr != 1.f)) {
-                            ok = __all_sync(FULL, wait(&odone[r], (nr - 1) & 1));
+                            ok = __all_sync(FULL, wait(&odone[MT == 2 ? r : (int)((at - 1) & 1)],
+                                                       (MT == 2 ? nr - 1 : (at - 1) >> 1) & 1));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -598,35 +596,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 #pragma unroll
                     for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
 #pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        float v0[32], v1[32];
-                        tc_ld32_async(t_s + c * 64, v0);
-                        tc_ld32_async(t_s + c * 64 + 32, v1);
-                        tc_ld_wait(v0);
-                        tc_ld_tie(v1);
-                        uint32_t o[32];
-                        auto weigh = [&](float *v, uint32_t *to, int first) {
+                    for (int c = 0; c < 4; ++c) {
+                        float v[32];
+                        uint32_t o[16];
+                        tc_ld32(t_s + c * 32, v);
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                const float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
-                                v[k] = ex2(x.x);
-                                v[k + 1] = ex2(x.y);
-                            }
-                            if (edge) {
-                                const int n_in = lim - key0 - first;
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
+                            v[k] = ex2(x.x);
+                            v[k + 1] = ex2(x.y);
+                        }
+                        if (edge) {
+                            const int n_in = lim - key0 - c * 32;
 #pragma unroll
-                                for (int k = 0; k < 32; ++k)
-                                    if (k >= n_in) v[k] = 0.f;
-                            }
+                            for (int k = 0; k < 32; ++k)
+                                if (k >= n_in) v[k] = 0.f;
+                        }
 #pragma unroll
-                            for (int k = 0; k < 32; k += 2) {
-                                acc[(k / 2) & 3] = add2(acc[(k / 2) & 3], make_float2(v[k], v[k + 1]));
-                                to[k / 2] = pack_f16(v[k], v[k + 1]);
-                            }
-                        };
-                        weigh(v0, o, c * 64);
-                        weigh(v1, o + 16, c * 64 + 32);
-                        tc_st32(t_s + c * 32, o);
+                        for (int k = 0; k < 32; k += 2) {
+                            acc[(k / 2) & 3] = add2(acc[(k / 2) & 3], make_float2(v[k], v[k + 1]));
+                            o[k / 2] = pack_f16(v[k], v[k + 1]);
+                        }
+                        tc_st16(t_s + c * 16, o);
                     }
                     acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
                     l += acc[0].x + acc[0].y;
@@ -643,7 +634,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     ++nr;
                 }
                 // ---- out
-                if (ok) ok = __all_sync(FULL, wait(&odone[r], (nr - 1) & 1));
+                const uint32_t end = n + tiles - 1;
+                if (ok)
+                    ok = __all_sync(FULL, wait(&odone[MT == 2 ? r : (int)(end & 1)],
+                                               (MT == 2 ? nr - 1 : end >> 1) & 1));
                 if (ok) {
                     tc_fence_after();
                     const bool whole = w.ta == 0 && w.tb == w.nt;
@@ -1002,11 +996,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     // ---- teardown: without a wait that ran out, every MMA was waited for
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && s_fail) {
-        uint64_t *bar = &sfull[0];
-        tc_commit(bar);  // completes after every MMA issued; give it a moment
-        mbar_wait(bar, 0, 1000000ull);
-        mbar_wait(bar, 1, 1000000ull);
+    if (warp < 2 && lane == 0 && s_fail) {
+        tc_commit(&sfull[warp]);  // completes after every MMA this thread issued
+        mbar_wait(&sfull[warp], 0, 1000000ull);
+        mbar_wait(&sfull[warp], 1, 1000000ull);
     }
     __syncthreads();
     tc_fence_after();
