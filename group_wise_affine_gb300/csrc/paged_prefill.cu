@@ -5,14 +5,16 @@
 // products and the bytes of the cache are few.
 //
 // A CTA holds a block of MT * 128 rows of one (sequence, KV head) and goes
-// over the keys in tiles of 128:
-//   S = Q K'^T   (M = 128 rows, N = 128 keys; Q and K' in shared memory)
+// over the keys in steps of 64:
+//   S = Q K'^T   (M = 128 rows, N = 64 keys; Q and K' in shared memory)
 //   P = 2^(S f - m), written to tensor memory over S as fp16
 //   O += P V'    (M = 128 rows, N = head_dim; P from tensor memory, V'
 //                transposed in shared memory)
 // with the running maximum m and sum per row in fp32, one thread to a row; m
-// moves only when a tile's maximum passes it by 8 (weights up to 2^8), and
-// then O is rescaled in tensor memory.
+// moves only when a step's maximum passes it by 8 (weights up to 2^8), and
+// then O is rescaled in tensor memory.  Each row tile has two score buffers,
+// and its scores run two steps ahead of its values, so the tensor cores and
+// the softmax of one row tile overlap.
 //
 // Operands.  u4 keys enter exactly, as the prefill projections' weights do:
 // scale * (code - 8) has at most 11 significant bits and is exact in fp16, and
@@ -68,12 +70,12 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d_tmem, uint64_t a_desc, uint
         : "memory");
 }
 
-// Descriptor of a K-major tile of 128 rows and 16 columns without swizzle:
-// 8-row, 16-byte core matrices, the two of a row 2048 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_ext(uint32_t saddr) {
+// Descriptor of a K-major tile of `rows` rows and 16 columns without swizzle:
+// 8-row, 16-byte core matrices, the two of a row 16 * rows bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_ext(uint32_t saddr, int rows) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr >> 4) & 0x3fffu);
-    d |= (uint64_t)(2048 >> 4) << 16;  // leading: next 8 columns
+    d |= (uint64_t)rows << 16;  // leading: next 8 columns
     d |= (uint64_t)(128 >> 4) << 32;   // stride: next 8 rows
     d |= (uint64_t)1 << 46;
     return d;
@@ -89,29 +91,34 @@ struct PfLayout {
     static constexpr int G = D / 64;
     static constexpr int MT = D <= 128 ? 2 : 1;      // row tiles
     static constexpr int RB = 128 * MT;              // rows of a block
-    static constexpr int ST = D <= 128 ? 2 : 1;      // key and value stages
+    static constexpr int KT = D <= 128 ? 128 : 64;   // keys of a tile
+    static constexpr int NH = KT / 64;               // score steps of a tile
+    static constexpr int ST = 2;                     // key and value stages
     static constexpr int RCH = D * BITS / 128;       // 16-byte chunks of a key's codes
-    static constexpr int TILE = 128 * D * 2;         // an operand tile
-    static constexpr int EXT = 128 * 32;             // the further columns of one
+    static constexpr int QTILE = 128 * D * 2;        // a row tile's queries
+    static constexpr int TILE = KT * D * 2;          // a tile's keys, or values
+    static constexpr int QEXT = 128 * 32, KEXT = KT * 32;  // their further columns
     static constexpr size_t Q_OFF = 0;
-    static constexpr size_t QX_OFF = Q_OFF + (size_t)MT * TILE;
-    static constexpr size_t KX_OFF = QX_OFF + (size_t)MT * EXT;
-    static constexpr size_t K_OFF = KX_OFF + (size_t)ST * EXT;
+    static constexpr size_t QX_OFF = Q_OFF + (size_t)MT * QTILE;
+    static constexpr size_t KX_OFF = QX_OFF + (size_t)MT * QEXT;
+    static constexpr size_t K_OFF = KX_OFF + (size_t)ST * KEXT;
     static constexpr size_t V_OFF = K_OFF + (size_t)ST * TILE;
-    // per slot: key scales, value scales and biases, fp16 [G][128] each
-    static constexpr int PAR = 3 * G * 256;
+    // per slot: key scales, value scales and biases, fp16 [G][KT] each
+    static constexpr int PROW = KT * 2, PAR = 3 * G * PROW;
     static constexpr size_t P_OFF = V_OFF + (size_t)ST * TILE;
     static constexpr size_t BYTES = P_OFF + (size_t)kPfSlots * PAR;
     static constexpr size_t SMEM = BYTES + 1024;     // alignment slack
-    // tensor memory: two score buffers, then the outputs
+    // tensor memory: two score buffers of 64 columns a row tile, then the
+    // outputs
     static constexpr int O_COL = 256;
     // unpacking units of a warp: keys KB x CB chunks; values 64 keys x 32
     // dimensions
     static constexpr int KB = RCH >= 4 ? 8 : 16, CB = RCH >= 4 ? 4 : 2;
-    static constexpr int KU = 128 / KB * (RCH / CB) / kPfDeqWarps;
-    static constexpr int VU = 4 * G / kPfDeqWarps > 0 ? 4 * G / kPfDeqWarps : 1;
-    static constexpr int VUNITS = 4 * G;             // of a tile
+    static constexpr int KU = KT / KB * (RCH / CB) / kPfDeqWarps;
+    static constexpr int VUNITS = NH * 2 * G;        // of a tile
+    static constexpr int VU = (VUNITS + kPfDeqWarps - 1) / kPfDeqWarps;
     static constexpr int VW = BITS / 4;              // words of 8 dimensions
+    static_assert(KU >= 1 && K_OFF % 1024 == 0 && TILE % 1024 == 0, "tiles");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -131,29 +138,29 @@ struct PfCursor {
     int rows, nrb;
 };
 
-// Keys that rows [rb * RB, ...) of a sequence see, in tiles of 128.
-template <int RB>
+// Keys that rows [rb * RB, ...) of a sequence see, in tiles of KT.
+template <int RB, int KT>
 __device__ __forceinline__ int pf_tiles(const PagedParams &p, const KvSeq &s, int rows, int rb) {
     int seen = s.len;
     if (p.causal) {
         const int last = (min(rows, (rb + 1) * RB) - 1) / p.rep;
         seen = min(seen, s.len - s.count + last + 1);
     }
-    return seen > 0 ? (seen + 127) / 128 : 0;
+    return seen > 0 ? (seen + KT - 1) / KT : 0;
 }
 template <int RB>
 __device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
     const int rows = p.rep * min(s.count, p.kv.max_q);
     return rows > p.split ? rows : 0;
 }
-template <int RB>
+template <int RB, int KT>
 __device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     const int rows = pf_rows<RB>(p, s);
     const int nrb = (rows + RB - 1) / RB;
-    if (!p.causal) return p.kv.heads * nrb * ((s.len + 127) / 128);
+    if (!p.causal) return p.kv.heads * nrb * ((s.len + KT - 1) / KT);
     int n = 0;
-    for (int rb = 0; rb < nrb; ++rb) n += pf_tiles<RB>(p, s, rows, rb);
+    for (int rb = 0; rb < nrb; ++rb) n += pf_tiles<RB, KT>(p, s, rows, rb);
     return p.kv.heads * n;
 }
 
@@ -162,10 +169,10 @@ struct PfPiece {
     int b, hk, rb, ta, tb, nt, rows;
     KvSeq s;
 };
-template <int RB>
+template <int RB, int KT>
 __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece &w) {
     if (c.left <= 0) return false;
-    int nt = pf_tiles<RB>(p, c.s, c.rows, c.rb);
+    int nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
     while (c.tile >= nt) {  // the next block that sees a key
         c.tile = 0;
         if (++c.rb >= c.nrb) {
@@ -181,7 +188,7 @@ __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece 
                 } while (c.nrb == 0);
             }
         }
-        nt = pf_tiles<RB>(p, c.s, c.rows, c.rb);
+        nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
     }
     w.b = c.b;
     w.hk = c.hk;
@@ -196,14 +203,15 @@ __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece 
     return true;
 }
 
-// Rows (of one head) of a tile's eight 16-key blocks, on lanes 0..7.
+// Rows (of one head) of a tile's 16-key blocks, on the first lanes.
+template <int KT>
 struct PfPages {
     const PagedParams &p;
     int len, tb, hk, b;
     __device__ __forceinline__ int64_t look(int tile, int lane) const {
-        const int key = tile * 128 + lane * 16;
+        const int key = tile * KT + lane * 16;
         int pg = 0;
-        if (tile < tb && lane < 8 && key < len) {
+        if (tile < tb && lane < KT / 16 && key < len) {
             pg = p.kv.page_table[(int64_t)b * p.kv.max_pages + (key >> p.kv.page_shift)];
             if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
                 if (p.status) atomicOr(p.status, (int)kKvBadPage);
@@ -217,11 +225,11 @@ struct PfPages {
 
 // The next piece of a warp's own walk through the run, in shared memory (the
 // walk is the same for every warp; registers are short).
-template <int RB>
+template <int RB, int KT>
 __device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor *c, PfPiece *w, int lane) {
     __syncwarp();
     int more = 0;
-    if (lane == 0) more = pf_step<RB>(p, *c, *w);
+    if (lane == 0) more = pf_step<RB, KT>(p, *c, *w);
     more = __shfl_sync(0xffffffffu, more, 0);
     __syncwarp();
     return more != 0;
@@ -230,14 +238,14 @@ __device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor *c, PfPie
 template <int BITS, int D>
 __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParams p) {
     using L = PfLayout<BITS, D>;
-    constexpr int G = L::G, MT = L::MT, RB = L::RB, ST = L::ST;
+    constexpr int G = L::G, MT = L::MT, RB = L::RB, ST = L::ST, KT = L::KT, NH = L::NH;
     constexpr float KC = BITS == 4 ? 8.f : 128.f;
     constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(1024) unsigned char pf_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t kfull[ST], kempty[ST], vfull[ST], vempty[ST];
-    __shared__ uint64_t sfull[2], pfull[2], odone[2], ofree[MT], qfull[MT];
+    __shared__ uint64_t sfull[MT][2], pfull[MT][2], odone[MT][2], ofree[MT], qfull[MT];
     __shared__ PfTile s_tile[kPfSlots];
     __shared__ PfCursor s_cur[kPfThreads / 32];
     __shared__ PfPiece s_piece[kPfThreads / 32];
@@ -254,10 +262,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             mbar_init(&kempty[i], MT);
             mbar_init(&vempty[i], MT);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&odone[i], 1);
-            mbar_init(&pfull[i], 4);
+        for (int i = 0; i < 2 * MT; ++i) {
+            mbar_init(&sfull[i / 2][i % 2], 1);
+            mbar_init(&odone[i / 2][i % 2], 1);
+            mbar_init(&pfull[i / 2][i % 2], 4);
         }
         for (int i = 0; i < MT; ++i) {
             mbar_init(&ofree[i], 4);
@@ -278,13 +286,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     if (warp == 1) {
         int total = 0;
         for (int b0 = 0; b0 < B; b0 += 32)
-            total += __reduce_add_sync(FULL, b0 + lane < B ? pf_units<RB>(p, b0 + lane) : 0);
+            total += __reduce_add_sync(FULL, b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0);
         const int ctas = min((int)gridDim.x, total);
         const int quot = ctas ? total / ctas : 0, rest = ctas ? total % ctas : 0;
         const int begin = pg_start(quot, rest, cta), end = pg_start(quot, rest, cta + 1);
         int at = 0, b = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
-            const int u = b0 + lane < B ? pf_units<RB>(p, b0 + lane) : 0;
+            const int u = b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0;
             int incl = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -308,10 +316,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 c.s = kv_seq(p.kv, b);
                 c.rows = pf_rows<RB>(p, c.s);
                 c.nrb = (c.rows + RB - 1) / RB;
-                const int head = pf_units<RB>(p, b) / p.kv.heads;
+                const int head = pf_units<RB, KT>(p, b) / p.kv.heads;
                 c.hk = (begin - at) / head;
                 int in = (begin - at) - c.hk * head;
-                for (int nt; in >= (nt = pf_tiles<RB>(p, c.s, c.rows, c.rb)); ++c.rb) in -= nt;
+                for (int nt; in >= (nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb)); ++c.rb) in -= nt;
                 c.tile = in;
             }
         }
@@ -340,45 +348,66 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     if (warp < 2) {
         // ------------------------------------------------ MMA issuers
         // Two row tiles: a warp each issues a tile's scores and values.  One:
-        // warp 0 issues the scores, a tile ahead, warp 1 the values.  (One
+        // warp 0 issues the scores, warp 1 the values.  (One
         // thread for all of them spent about 100 cycles on an MMA of 64.)
         if (lane == 0) {
-            constexpr uint32_t id_s = pf_idesc(128), id_o = pf_idesc(D);
+            constexpr uint32_t id_s = pf_idesc(64), id_o = pf_idesc(D);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::Q_OFF));
             const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + L::K_OFF));
             const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + L::V_OFF));
-            const uint64_t qx_desc = smem_desc_ext(smem_u32(smem + L::QX_OFF));
-            const uint64_t kx_desc = smem_desc_ext(smem_u32(smem + L::KX_OFF));
+            const uint64_t qx_desc = smem_desc_ext(smem_u32(smem + L::QX_OFF), 128);
+            const uint64_t kx_desc = smem_desc_ext(smem_u32(smem + L::KX_OFF), KT);
+            const int r = MT == 2 ? warp : 0;
             uint32_t n = 0;       // tiles so far
-            uint32_t nr = 0;      // of this row tile
+            uint32_t nr = 0;      // score steps of this row tile
             uint32_t pieces = 0;  // blocks of this row tile
             bool ok = true;
-            // scores of row tile r against the keys of stage st into buffer s
-            auto scores = [&](int r, int st, int s) {
-                const uint32_t d = tmem + s * 128;
-                uint64_t a = q_desc + (uint64_t)((r * L::TILE) >> 4);
-                uint64_t b = k_desc + (uint64_t)((st * L::TILE) >> 4);
-                tc_mma_ss(d, qx_desc + (uint64_t)((r * L::EXT) >> 4),
-                          kx_desc + (uint64_t)((st * L::EXT) >> 4), id_s, 0u);
+            // step j of a piece: scores against 64 keys into buffer s
+            auto scores = [&](int j) {
+                const uint32_t tile = n + j / NH;
+                const int st = tile % ST, h = j % NH, s = (nr + j) & 1;
+                if (h == 0 && !wait(&kfull[st], (tile / ST) & 1)) return false;
+                // issued by another thread than the values: the buffer's last
+                // weights are used
+                if (MT == 1 && nr + j >= 2 && !wait(&odone[0][s], (((nr + j) >> 1) - 1) & 1))
+                    return false;
+                tc_fence_after();
+                const uint32_t d = tmem + r * 128 + s * 64;
+                const uint64_t a = q_desc + (uint64_t)((r * L::QTILE) >> 4);
+                const uint64_t b = k_desc + (uint64_t)((st * L::TILE + h * 8192) >> 4);
+                tc_mma_ss(d, qx_desc + (uint64_t)((r * L::QEXT) >> 4),
+                          kx_desc + (uint64_t)((st * L::KEXT + h * 1024) >> 4), id_s, 0u);
 #pragma unroll
                 for (int k = 0; k < 4 * G; ++k)
-                    tc_mma_ss(d, a + (k / 4) * 1024 + 2 * (k % 4), b + (k / 4) * 1024 + 2 * (k % 4),
+                    tc_mma_ss(d, a + (k / 4) * 1024 + 2 * (k % 4), b + (k / 4) * (KT * 8) + 2 * (k % 4),
                               id_s, 1u);
-                tc_commit(&sfull[s]);
+                tc_commit(&sfull[r][s]);
+                if (h == NH - 1) tc_commit(&kempty[st]);
+                return true;
             };
-            auto values = [&](int r, int st, int s, bool first) {
-                const uint32_t d = tmem + L::O_COL + r * D, a = tmem + s * 128;
-                const uint64_t b = v_desc + (uint64_t)((st * L::TILE) >> 4);
+            // step j: weights in buffer s times the values of its 64 keys
+            auto values = [&](int j) {
+                const uint32_t tile = n + j / NH;
+                const int st = tile % ST, h = j % NH, s = (nr + j) & 1;
+                if (h == 0 && !wait(&vfull[st], (tile / ST) & 1)) return false;
+                if (!wait(&pfull[r][s], ((nr + j) >> 1) & 1)) return false;
+                if (j == 0 && pieces > 0 && !wait(&ofree[r], (pieces - 1) & 1)) return false;
+                tc_fence_after();
+                const uint32_t d = tmem + L::O_COL + r * D, a = tmem + r * 128 + s * 64;
+                const uint64_t b = v_desc + (uint64_t)((st * L::TILE + h * D * 128) >> 4);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    tc_mma_ts(d, a + k * 8, b + (k / 4) * (D * 8) + 2 * (k % 4), id_o,
-                              first && k == 0 ? 0u : 1u);
-                tc_commit(&odone[s]);
-                tc_commit(&vempty[st]);
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_ts(d, a + k * 8, b + 2 * k, id_o, j == 0 && k == 0 ? 0u : 1u);
+                tc_commit(&odone[r][s]);
+                if (h == NH - 1) {
+                    tc_commit(&vempty[st]);
+                    tc_commit(&rempty[tile % kPfSlots]);
+                }
+                return true;
             };
-            while (ok && pf_step<RB>(p, *cur, s_piece[warp])) {
+            while (ok && pf_step<RB, KT>(p, *cur, s_piece[warp])) {
                 const int nlive = min(RB, w.rows - w.rb * RB);
-                const int tiles = w.tb - w.ta;
+                const int tiles = w.tb - w.ta, steps = tiles * NH;
                 if (MT == 2 && warp * 128 >= nlive) {
                     // no rows here: the stages are free as soon as they are full
                     for (int i = 0; ok && i < tiles; ++i, ++n) {
@@ -392,35 +421,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     }
                     continue;
                 }
-                const int r = MT == 2 ? warp : 0;
                 if (MT == 2 || warp == 0) ok = wait(&qfull[r], pieces & 1);
-                for (int i = MT == 2 ? -1 : 0; ok && i < tiles; ++i) {
-                    // two row tiles: values of tile i, then scores of i + 1
-                    const uint32_t at = n + i, nx = MT == 2 ? at + 1 : at;
-                    const bool first = i == 0;
-                    if ((MT == 2 && i >= 0) || (MT == 1 && warp == 1)) {
-                        const int st = at % ST, s = MT == 2 ? r : (int)(at & 1);
-                        ok = wait(&vfull[st], (at / ST) & 1) &&
-                             wait(&pfull[s], (MT == 2 ? nr : at >> 1) & 1);
-                        if (ok && first && pieces > 0) ok = wait(&ofree[r], (pieces - 1) & 1);
-                        if (!ok) break;
-                        ++nr;
-                        tc_fence_after();
-                        values(r, st, s, first);
-                        tc_commit(&rempty[at % kPfSlots]);
-                    }
-                    if ((MT == 2 && i + 1 < tiles) || (MT == 1 && warp == 0)) {
-                        const int st = nx % ST, s = MT == 2 ? r : (int)(nx & 1);
-                        ok = wait(&kfull[st], (nx / ST) & 1);
-                        // one row tile: the buffer's last weights are used
-                        if (MT == 1 && ok && nx >= 2) ok = wait(&odone[s], ((nx >> 1) - 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(r, st, s);
-                        tc_commit(&kempty[st]);
-                    }
+                // scores run two steps ahead of the values
+                for (int j = -2; ok && j < steps; ++j) {
+                    if (j >= 0 && (MT == 2 || warp == 1)) ok = values(j);
+                    if (ok && j + 2 < steps && (MT == 2 || warp == 0)) ok = scores(j + 2);
                 }
                 n += tiles;
+                nr += steps;
                 ++pieces;
             }
         }
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         int pieces = 0, piece = 0;
         int begin = s_begin;     // the unit the run stands at
         bool ok = true;
-        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
+        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
             const int nlive = min(RB, w.rows - w.rb * RB);
             const int tiles = w.tb - w.ta;
             if (r * 128 < nlive) {
@@ -467,7 +475,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 float up, down;
                 range_scale(mx, up, down);
                 if (p.scale < 0.f) up = -up;  // factors are kept non-negative
-                unsigned char *qt = smem + L::Q_OFF + (size_t)r * L::TILE + row * 128;
+                unsigned char *qt = smem + L::Q_OFF + (size_t)r * L::QTILE + row * 128;
 #pragma unroll
                 for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -501,7 +509,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         e[3 * g] = e[3 * g + 2] = hi;
                         e[3 * g + 1] = x - hi;
                     }
-                    unsigned char *qx = smem + L::QX_OFF + (size_t)r * L::EXT + (row >> 3) * 128 + (row & 7) * 16;
+                    unsigned char *qx = smem + L::QX_OFF + (size_t)r * L::QEXT + (row >> 3) * 128 + (row & 7) * 16;
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         *reinterpret_cast<uint4 *>(qx + k * 2048) =
@@ -518,43 +526,39 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                                            : w.s.len;
                 const int least = __reduce_min_sync(FULL, lim);
                 float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
-                for (int i = 0; ok && i < tiles; ++i) {
-                    const uint32_t at = n + i;
-                    const int s = MT == 2 ? r : (int)(at & 1);
-                    const uint32_t t_s = tmem + s * 128 + lane_off;
-                    const uint32_t use = MT == 2 ? nr : at >> 1;
-                    ok = __all_sync(FULL, wait(&sfull[s], use & 1));
+                const int steps = tiles * NH;
+                for (int i = 0; ok && i < steps; ++i) {
+                    const uint32_t at = nr + i;  // step of this row tile
+                    const int s = at & 1;
+                    const uint32_t t_s = tmem + r * 128 + s * 64 + lane_off;
+                    ok = __all_sync(FULL, wait(&sfull[r][s], (at >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    const PfTile &pt = s_tile[at % kPfSlots];
-                    const float f = fac * pt.k_down;
-                    const int key0 = (w.ta + i) * 128;
-                    const bool edge = key0 + 128 > least;
-                    // ---- the tile's maximum (rolled loops here and below: the
-                    // warps' code together is more than the instruction caches
-                    // hold close)
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        tc_ld32(t_s + c * 32, v);
-                        if (edge) {
-                            const int n_in = lim - key0 - c * 32;
+                    const PfTile &pt = s_tile[(n + i / NH) % kPfSlots];
+                    // (never zero, so that a masked score stays -inf: a factor
+                    // below leaves every score at zero either way)
+                    const float f = fmaxf(fac * pt.k_down, 1e-37f);
+                    const int key0 = w.ta * KT + i * 64;
+                    float v0[32], v1[32];
+                    tc_ld32_async(t_s, v0);
+                    tc_ld32_async(t_s + 32, v1);
+                    tc_ld_wait(v0);
+                    tc_ld_tie(v1);
+                    if (key0 + 64 > least) {
+                        const int n_in = lim - key0;
 #pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (k < n_in) mx = fmaxf(mx, v[k]);
-                        } else {
-                            float ma = -INFINITY;
-#pragma unroll
-                            for (int k = 0; k < 32; k += 4) {
-                                mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
-                                ma = fmaxf(ma, fmaxf(v[k + 2], v[k + 3]));
-                            }
-                            mx = fmaxf(mx, ma);
+                        for (int k = 0; k < 32; ++k) {
+                            if (k >= n_in) v0[k] = -INFINITY;
+                            if (k + 32 >= n_in) v1[k] = -INFINITY;
                         }
                     }
-                    mx *= f;  // (-inf times zero: no key seen, or a scale of zero)
-                    if (!(mx > -INFINITY)) mx = edge && key0 >= lim ? -INFINITY : f == 0.f ? 0.f : mx;
+                    float mx = -INFINITY, ma = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        mx = fmaxf(mx, fmaxf(v0[k], v0[k + 1]));
+                        ma = fmaxf(ma, fmaxf(v1[k], v1[k + 1]));
+                    }
+                    mx = fmaxf(mx, ma) * f;
                     // ---- rescale
                     float corr = 1.f;
                     if (mx > m + 8.f) {
@@ -573,18 +577,17 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             v_down = pt.v_down;
                         }
                         if (__any_sync(FULL, corr != 1.f)) {
-                            ok = __all_sync(FULL, wait(&odone[MT == 2 ? r : (int)((at - 1) & 1)],
-                                                       (MT == 2 ? nr - 1 : (at - 1) >> 1) & 1));
+                            ok = __all_sync(FULL, wait(&odone[r][s ^ 1], ((at - 1) >> 1) & 1));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float v[32];
-                                uint32_t o[32];
-                                tc_ld32(t_o + c * 32, v);
+                            for (int c = 0; c < D; c += 16) {
+                                float x[16];
+                                uint32_t o[16];
+                                tc_ld16(t_o + c, x);
 #pragma unroll
-                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(v[k] * corr);
-                                tc_st32(t_o + c * 32, o);
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(x[k] * corr);
+                                tc_st16(t_o + c, o);
                             }
                             tc_wait_st();
                         }
@@ -592,52 +595,42 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // ---- weights
                     const float sub = m == -INFINITY ? 0.f : m;
                     const float2 f2 = make_float2(f, f), s2 = make_float2(-sub, -sub);
-                    float2 acc[4];
+                    float2 acc[2];
+                    acc[0] = acc[1] = make_float2(0.f, 0.f);
+                    uint32_t o[32];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float v[32];
-                        uint32_t o[16];
-                        tc_ld32(t_s + c * 32, v);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            const float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
-                            v[k] = ex2(x.x);
-                            v[k + 1] = ex2(x.y);
-                        }
-                        if (edge) {
-                            const int n_in = lim - key0 - c * 32;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (k >= n_in) v[k] = 0.f;
-                        }
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            acc[(k / 2) & 3] = add2(acc[(k / 2) & 3], make_float2(v[k], v[k + 1]));
-                            o[k / 2] = pack_f16(v[k], v[k + 1]);
-                        }
-                        tc_st16(t_s + c * 16, o);
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 x = fma2(make_float2(v0[k], v0[k + 1]), f2, s2);
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        acc[0] = add2(acc[0], x);
+                        o[k / 2] = pack_f16(x.x, x.y);
                     }
-                    acc[0] = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) {
+                        float2 x = fma2(make_float2(v1[k], v1[k + 1]), f2, s2);
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        acc[1] = add2(acc[1], x);
+                        o[16 + k / 2] = pack_f16(x.x, x.y);
+                    }
+                    tc_st32(t_s, o);
+                    acc[0] = add2(acc[0], acc[1]);
                     l += acc[0].x + acc[0].y;
                     if (pt.bad[0] | pt.bad[1] | pt.bad[2] | pt.bad[3]) {
                         // a value that is not finite leaves the products; the
                         // rows that see it are not finite either
-                        for (int k = 0; k < 128; ++k)
-                            if ((pt.bad[k & 3] >> (k >> 2)) & 1 && key0 + k < lim) l = NAN;
+                        for (int k = 0; k < 64; ++k) {
+                            const int x = (i % NH) * 64 + k;
+                            if ((pt.bad[x & 3] >> (x >> 2)) & 1 && key0 + k < lim) l = NAN;
+                        }
                     }
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&pfull[s]);
-                    ++nr;
+                    if (lane == 0) mbar_arrive(&pfull[r][s]);
                 }
+                nr += steps;
                 // ---- out
-                const uint32_t end = n + tiles - 1;
-                if (ok)
-                    ok = __all_sync(FULL, wait(&odone[MT == 2 ? r : (int)(end & 1)],
-                                               (MT == 2 ? nr - 1 : end >> 1) & 1));
+                if (ok) ok = __all_sync(FULL, wait(&odone[r][(nr - 1) & 1], ((nr - 1) >> 1) & 1));
                 if (ok) {
                     tc_fence_after();
                     const bool whole = w.ta == 0 && w.tb == w.nt;
@@ -694,13 +687,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         const uint32_t *src = is_k ? p.kv.kp : p.kv.vp;
         uint32_t n = 0;
         bool ok = true;
-        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
-            const PfPages pages{p, w.s.len, w.tb, w.hk, w.b};
+        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
+            const PfPages<KT> pages{p, w.s.len, w.tb, w.hk, w.b};
             float v_lim = -1.f, up = 1.f, down = 1.f;
             uint32_t x[4][G];  // keys 4 lane + j
             auto load = [&](int64_t base, int tile) {
                 const int64_t row = __shfl_sync(FULL, base, lane >> 2) + (lane & 3) * 4;
-                const int left = w.s.len - tile * 128;
+                const int left = min(KT, w.s.len - tile * KT);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -746,8 +739,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     if (!ok) break;
                 }
                 unsigned char *par = smem + L::P_OFF + slot * L::PAR + lane * 8;
+                const bool mine = lane < KT / 4;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
+                    if (!mine) break;
                     float s[4], b[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -755,13 +750,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         b[j] = bf16_hi(x[j][g]) * to;
                     }
                     if (is_k) {
-                        *reinterpret_cast<uint2 *>(par + g * 256) =
+                        *reinterpret_cast<uint2 *>(par + g * L::PROW) =
                             make_uint2(pack_f16(s[0], s[1]), pack_f16(s[2], s[3]));
                     } else {
                         constexpr float c = 0x1p24f;  // codes enter as c 2^-24
-                        *reinterpret_cast<uint2 *>(par + (G + g) * 256) =
+                        *reinterpret_cast<uint2 *>(par + (G + g) * L::PROW) =
                             make_uint2(pack_f16(s[0] * c, s[1] * c), pack_f16(s[2] * c, s[3] * c));
-                        *reinterpret_cast<uint2 *>(par + (2 * G + g) * 256) =
+                        *reinterpret_cast<uint2 *>(par + (2 * G + g) * L::PROW) =
                             make_uint2(pack_f16(b[0], b[1]), pack_f16(b[2], b[3]));
                     }
                 }
@@ -788,6 +783,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        if (!mine) break;
                         float e[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) e[k] = 0.f;
@@ -799,10 +795,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             e[3 * g + 2] = b - hi;
                         }
                         const int k = 4 * lane + j;
-                        unsigned char *kx = smem + L::KX_OFF + (size_t)(n % ST) * L::EXT + (k >> 3) * 128 + (k & 7) * 16;
+                        unsigned char *kx = smem + L::KX_OFF + (size_t)(n % ST) * L::KEXT + (k >> 3) * 128 + (k & 7) * 16;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<uint4 *>(kx + h * 2048) =
+                            *reinterpret_cast<uint4 *>(kx + h * (KT * 16)) =
                                 make_uint4(pack_f16(e[8 * h], e[8 * h + 1]), pack_f16(e[8 * h + 2], e[8 * h + 3]),
                                            pack_f16(e[8 * h + 4], e[8 * h + 5]), pack_f16(e[8 * h + 6], e[8 * h + 7]));
                     }
@@ -818,18 +814,18 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         // ------------------------------------------------ keys and values
         const int dw = warp - kPfDeq0;
         constexpr int KU = L::KU, VU = L::VU, RCH = L::RCH, VW = L::VW;
-        constexpr int KBS = 128 / L::KB;  // key blocks of a tile
+        constexpr int KBS = KT / L::KB;  // key blocks of a tile
         const int kl = RCH >= 4 ? lane & 7 : (lane & 7) + 8 * (lane >> 4);  // key of a key unit
         const int kc = RCH >= 4 ? lane >> 3 : (lane >> 3) & 1;              // chunk of it
         const int vc = lane & 7, vd = lane >> 3;  // 8 keys and 8 dimensions of a value unit
         uint32_t n = 0;
         bool ok = true;
-        while (ok && pf_next<RB>(p, cur, &s_piece[warp], lane)) {
-            const PfPages pages{p, w.s.len, w.tb, w.hk, w.b};
+        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
+            const PfPages<KT> pages{p, w.s.len, w.tb, w.hk, w.b};
             uint4 kreg[KU];
             uint32_t vreg[VU][8][VW];
             auto load_k = [&](int64_t base, int tile) {
-                const int left = w.s.len - tile * 128;  // keys of the tile
+                const int left = min(KT, w.s.len - tile * KT);  // keys of the tile
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
@@ -840,11 +836,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 }
             };
             auto load_v = [&](int64_t base, int tile) {
-                const int left = w.s.len - tile * 128;
+                const int left = min(KT, w.s.len - tile * KT);
 #pragma unroll
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
-                    const int k0 = id % 2 * 64 + vc * 8, d32 = id / 2;
+                    const int k0 = id % NH * 64 + vc * 8, d32 = id / NH;
                     const int64_t row = __shfl_sync(FULL, base, k0 >> 4) + (k0 & 15);
                     const uint32_t *src = p.kv.vq + row * (D * BITS / 32) + d32 * BITS + vd * VW;
 #pragma unroll
@@ -881,13 +877,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     const int id = dw + u * kPfDeqWarps;
                     const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
                     const __half2 s2 = __half2half2(
-                        *reinterpret_cast<const __half *>(par + c / (RCH / G) * 256 + k * 2));
+                        *reinterpret_cast<const __half *>(par + c / (RCH / G) * L::PROW + k * 2));
                     const uint32_t wd[4] = {kreg[u].x, kreg[u].y, kreg[u].z, kreg[u].w};
                     if constexpr (BITS == 4) {
                         const __half2 off = __floats2half2_rn(1032.f, 1032.f);
                         const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
                         const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
-                        unsigned char *dst = kt + (c / 2) * 16384 + k * 128;
+                        unsigned char *dst = kt + (c / 2) * (KT * 128) + k * 128;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t a = wd[j], b = wd[j] >> 8;
@@ -900,7 +896,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         }
                     } else {
                         const __half2 off = __floats2half2_rn(1152.f, 1152.f);
-                        unsigned char *dst = kt + (c / 4) * 16384 + k * 128;
+                        unsigned char *dst = kt + (c / 4) * (KT * 128) + k * 128;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             uint32_t o[4];
@@ -931,11 +927,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
                     if (id >= L::VUNITS) break;
-                    unsigned char *vt = smem + L::V_OFF + (size_t)st * L::TILE + (id % 2) * (D * 128);
-                    const int d0 = id / 2 * 32 + vd * 8;
-                    const unsigned char *vp = par + (G + id / 4) * 256 + (id % 2 * 64 + vc * 8) * 2;
+                    unsigned char *vt = smem + L::V_OFF + (size_t)st * L::TILE + (id % NH) * (D * 128);
+                    const int d0 = id / NH * 32 + vd * 8;
+                    const unsigned char *vp = par + (G + id / (2 * NH)) * L::PROW + (id % NH * 64 + vc * 8) * 2;
                     const uint4 sw = *reinterpret_cast<const uint4 *>(vp);
-                    const uint4 bw = *reinterpret_cast<const uint4 *>(vp + G * 256);
+                    const uint4 bw = *reinterpret_cast<const uint4 *>(vp + G * L::PROW);
                     const __half2 s2[4] = {bits_h2(sw.x), bits_h2(sw.y), bits_h2(sw.z), bits_h2(sw.w)};
                     const __half2 b2[4] = {bits_h2(bw.x), bits_h2(bw.y), bits_h2(bw.z), bits_h2(bw.w)};
                     __half2 t2[4];  // for codes left at bits 4-7: 16 c 2^-24
@@ -983,7 +979,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             const KvSeq s = kv_seq(p.kv, b);
             const int rows = pf_rows<RB>(p, s);
             for (int rb = 0; rb * RB < rows; ++rb) {
-                if (pf_tiles<RB>(p, s, rows, rb) > 0) continue;
+                if (pf_tiles<RB, KT>(p, s, rows, rb) > 0) continue;
                 const int n = min(RB, rows - rb * RB);
                 for (int i = tid; i < n * p.kv.heads * (D / 8); i += 64) {
                     const int c = i % (D / 8), h = i / (D / 8) % p.kv.heads, rr = rb * RB + i / (D / 8) / p.kv.heads;
@@ -997,9 +993,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     tc_fence_before();
     __syncthreads();
     if (warp < 2 && lane == 0 && s_fail) {
-        tc_commit(&sfull[warp]);  // completes after every MMA this thread issued
-        mbar_wait(&sfull[warp], 0, 1000000ull);
-        mbar_wait(&sfull[warp], 1, 1000000ull);
+        tc_commit(&sfull[0][warp]);  // completes after every MMA this thread issued
+        mbar_wait(&sfull[0][warp], 0, 1000000ull);
+        mbar_wait(&sfull[0][warp], 1, 1000000ull);
     }
     __syncthreads();
     tc_fence_after();
@@ -1049,7 +1045,7 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, 
 static int pf_grid(const KvView &kv, int rep) {
     const int rb = kv.dim <= 128 ? 256 : 128;
     const int64_t units = (int64_t)kv.batch * kv.heads * (((int64_t)rep * kv.max_q + rb - 1) / rb) *
-                          (((int64_t)kv.max_kv + 127) / 128);
+                          (((int64_t)kv.max_kv + 63) / 64);
     return (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms()));
 }
 
