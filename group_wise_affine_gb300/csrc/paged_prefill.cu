@@ -235,6 +235,15 @@ __device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor *c, PfPie
     return more != 0;
 }
 
+// The bounded wait, out of line: the roles' loops are short of instruction
+// cache.
+__device__ __noinline__ bool pf_wait(uint64_t *bar, uint32_t parity, int *fail) {
+    if (mbar_wait_sleep(bar, parity)) return true;
+    atomicAdd(&g_prefill_timeouts, 1u);
+    *fail = 1;
+    return false;
+}
+
 template <int BITS, int D>
 __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParams p) {
     using L = PfLayout<BITS, D>;
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     extern __shared__ __align__(1024) unsigned char pf_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(pf_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t kfull[ST], kempty[ST], vfull[ST], vempty[ST];
+    __shared__ uint64_t kfull[ST], vfull[ST];
     __shared__ uint64_t sfull[MT][2], pfull[MT][2], odone[MT][2], ofree[MT], qfull[MT];
     __shared__ PfTile s_tile[kPfSlots];
     __shared__ PfCursor s_cur[kPfThreads / 32];
@@ -259,8 +268,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         for (int i = 0; i < ST; ++i) {
             mbar_init(&kfull[i], kPfDeqWarps + 1);
             mbar_init(&vfull[i], kPfDeqWarps);
-            mbar_init(&kempty[i], MT);
-            mbar_init(&vempty[i], MT);
         }
         for (int i = 0; i < 2 * MT; ++i) {
             mbar_init(&sfull[i / 2][i % 2], 1);
@@ -339,10 +346,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     const PfPiece &w = s_piece[warp];
 
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (mbar_wait_sleep(bar, parity)) return true;
-        atomicAdd(&g_prefill_timeouts, 1u);
-        s_fail = 1;
-        return false;
+        return mbar_try_wait(bar, parity) || pf_wait(bar, parity, &s_fail);
     };
 
     if (warp < 2) {
@@ -382,11 +386,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     tc_mma_ss(d, a + (k / 4) * 1024 + 2 * (k % 4), b + (k / 4) * (KT * 8) + 2 * (k % 4),
                               id_s, 1u);
                 tc_commit(&sfull[r][s]);
-                if (h == NH - 1) tc_commit(&kempty[st]);
                 return true;
             };
             // step j: weights in buffer s times the values of its 64 keys
-            auto values = [&](int j) {
+            auto values = [&](int j, int steps) {
                 const uint32_t tile = n + j / NH;
                 const int st = tile % ST, h = j % NH, s = (nr + j) & 1;
                 if (h == 0 && !wait(&vfull[st], (tile / ST) & 1)) return false;
@@ -398,11 +401,13 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tc_mma_ts(d, a + k * 8, b + 2 * k, id_o, j == 0 && k == 0 ? 0u : 1u);
-                tc_commit(&odone[r][s]);
-                if (h == NH - 1) {
-                    tc_commit(&vempty[st]);
-                    tc_commit(&rempty[tile % kPfSlots]);
-                }
+                // two row tiles: scores of step j + 2, issued after these, tell
+                // of them as well, but at the end
+                if (MT == 1)
+                    tc_commit(&odone[0][s]);
+                else if (j + 2 >= steps)
+                    tc_commit(&odone[r][steps - 1 - j]);
+                if (h == NH - 1) tc_commit(&rempty[tile % kPfSlots]);
                 return true;
             };
             while (ok && pf_step<RB, KT>(p, *cur, s_piece[warp])) {
@@ -412,19 +417,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // no rows here: the stages are free as soon as they are full
                     for (int i = 0; ok && i < tiles; ++i, ++n) {
                         ok = wait(&kfull[n % ST], (n / ST) & 1);
-                        if (ok) mbar_arrive(&kempty[n % ST]);
                         ok = ok && wait(&vfull[n % ST], (n / ST) & 1);
-                        if (ok) {
-                            mbar_arrive(&vempty[n % ST]);
-                            mbar_arrive(&rempty[n % kPfSlots]);
-                        }
+                        if (ok) mbar_arrive(&rempty[n % kPfSlots]);
                     }
                     continue;
                 }
                 if (MT == 2 || warp == 0) ok = wait(&qfull[r], pieces & 1);
                 // scores run two steps ahead of the values
                 for (int j = -2; ok && j < steps; ++j) {
-                    if (j >= 0 && (MT == 2 || warp == 1)) ok = values(j);
+                    if (j >= 0 && (MT == 2 || warp == 1)) ok = values(j, steps);
                     if (ok && j + 2 < steps && (MT == 2 || warp == 0)) ok = scores(j + 2);
                 }
                 n += tiles;
@@ -441,6 +442,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         const uint32_t t_o = tmem + L::O_COL + r * D + lane_off;
         uint32_t n = 0, nr = 0;  // tiles so far: of the CTA, of this row tile
         int pieces = 0, piece = 0;
+        int longer = 0;          // of the pieces, those of two steps and more
         int begin = s_begin;     // the unit the run stands at
         bool ok = true;
         while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
@@ -577,7 +579,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             v_down = pt.v_down;
                         }
                         if (__any_sync(FULL, corr != 1.f)) {
-                            ok = __all_sync(FULL, wait(&odone[r][s ^ 1], ((at - 1) >> 1) & 1));
+                            // the previous step's values are in
+                            if (MT == 1)
+                                ok = wait(&odone[0][s ^ 1], ((at - 1) >> 1) & 1);
+                            else if (i + 1 < steps)
+                                ok = wait(&sfull[r][s ^ 1], ((at + 1) >> 1) & 1);
+                            else
+                                ok = wait(&odone[r][1], longer & 1);
+                            ok = __all_sync(FULL, ok);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -630,7 +639,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 }
                 nr += steps;
                 // ---- out
-                if (ok) ok = __all_sync(FULL, wait(&odone[r][(nr - 1) & 1], ((nr - 1) >> 1) & 1));
+                if (ok)
+                    ok = __all_sync(FULL, MT == 1 ? wait(&odone[0][(nr - 1) & 1], ((nr - 1) >> 1) & 1)
+                                                  : wait(&odone[r][0], pieces & 1));
+                if (steps > 1) ++longer;
                 if (ok) {
                     tc_fence_after();
                     const bool whole = w.ta == 0 && w.tb == w.nt;
@@ -778,7 +790,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 if (is_k) {
                     // b' as (hi, hi, lo) per group
                     if (n >= ST) {
-                        ok = __all_sync(FULL, wait(&kempty[n % ST], ((n / ST) & 1) ^ 1));
+                        ok = __all_sync(FULL, wait(&rempty[(n - ST) % kPfSlots], ((n - ST) / kPfSlots) & 1));
                         if (!ok) break;
                     }
 #pragma unroll
@@ -869,46 +881,54 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 const unsigned char *par = smem + L::P_OFF + slot * L::PAR;
                 ok = __all_sync(FULL, wait(&rfull[slot], (n / kPfSlots) & 1));
                 // ---- keys: scale (code - centre), exact
-                if (ok && n >= ST) ok = __all_sync(FULL, wait(&kempty[st], ((n / ST) & 1) ^ 1));
+                if (ok && n >= ST)
+                    ok = __all_sync(FULL, wait(&rempty[(n - ST) % kPfSlots], ((n - ST) / kPfSlots) & 1));
                 if (!ok) break;
                 unsigned char *kt = smem + L::K_OFF + (size_t)st * L::TILE;
+                {
+                    __half2 s2[KU];
+                    unsigned char *dst[KU];
+                    int sw[KU];  // chunk of the row's 128 bytes, swizzled
+                    constexpr int OUT = BITS == 4 ? 4 : 2;  // 16-byte chunks out of one in
 #pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    const int id = dw + u * kPfDeqWarps;
-                    const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
-                    const __half2 s2 = __half2half2(
-                        *reinterpret_cast<const __half *>(par + c / (RCH / G) * L::PROW + k * 2));
-                    const uint32_t wd[4] = {kreg[u].x, kreg[u].y, kreg[u].z, kreg[u].w};
-                    if constexpr (BITS == 4) {
-                        const __half2 off = __floats2half2_rn(1032.f, 1032.f);
-                        const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
-                        const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
-                        unsigned char *dst = kt + (c / 2) * (KT * 128) + k * 128;
+                    for (int u = 0; u < KU; ++u) {
+                        const int id = dw + u * kPfDeqWarps;
+                        const int k = id % KBS * L::KB + kl, c = id / KBS * L::CB + kc;
+                        constexpr int CG = RCH / G;  // chunks of a group
+                        s2[u] = __half2half2(
+                            *reinterpret_cast<const __half *>(par + c / CG * L::PROW + k * 2));
+                        dst[u] = kt + c / CG * (KT * 128) + k * 128;
+                        sw[u] = (c % CG * OUT) ^ (k & 7);
+                    }
+                    // (rolled over a chunk's words, the unpacked one always in x)
+#pragma unroll 1
+                    for (int j = 0; j < OUT; ++j) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t a = wd[j], b = wd[j] >> 8;
+                        for (int u = 0; u < KU; ++u) {
                             uint4 o;
-                            o.x = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x000f000fu) | 0x64006400u), off), s2));
-                            o.y = h2_bits(__hmul2(__hfma2(bits_h2((a & 0x00f000f0u) | 0x64006400u), r16, m72), s2));
-                            o.z = h2_bits(__hmul2(__hsub2(bits_h2((b & 0x000f000fu) | 0x64006400u), off), s2));
-                            o.w = h2_bits(__hmul2(__hfma2(bits_h2((b & 0x00f000f0u) | 0x64006400u), r16, m72), s2));
-                            *reinterpret_cast<uint4 *>(dst + ((((c & 1) * 4 + j) ^ (k & 7)) * 16)) = o;
-                        }
-                    } else {
-                        const __half2 off = __floats2half2_rn(1152.f, 1152.f);
-                        unsigned char *dst = kt + (c / 4) * (KT * 128) + k * 128;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const uint32_t a = wd[2 * j + x];
-                                o[2 * x] = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x00ff00ffu) | 0x64006400u), off), s2));
-                                o[2 * x + 1] = h2_bits(
-                                    __hmul2(__hsub2(bits_h2(((a >> 8) & 0x00ff00ffu) | 0x64006400u), off), s2));
+                            if constexpr (BITS == 4) {
+                                const __half2 off = __floats2half2_rn(1032.f, 1032.f);
+                                const __half2 r16 = __floats2half2_rn(0.0625f, 0.0625f);
+                                const __half2 m72 = __floats2half2_rn(-72.f, -72.f);
+                                const uint32_t a = kreg[u].x, b = a >> 8;
+                                kreg[u].x = kreg[u].y;
+                                kreg[u].y = kreg[u].z;
+                                kreg[u].z = kreg[u].w;
+                                o.x = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x000f000fu) | 0x64006400u), off), s2[u]));
+                                o.y = h2_bits(__hmul2(__hfma2(bits_h2((a & 0x00f000f0u) | 0x64006400u), r16, m72), s2[u]));
+                                o.z = h2_bits(__hmul2(__hsub2(bits_h2((b & 0x000f000fu) | 0x64006400u), off), s2[u]));
+                                o.w = h2_bits(__hmul2(__hfma2(bits_h2((b & 0x00f000f0u) | 0x64006400u), r16, m72), s2[u]));
+                            } else {
+                                const __half2 off = __floats2half2_rn(1152.f, 1152.f);
+                                const uint32_t a = kreg[u].x, b = kreg[u].y;
+                                kreg[u].x = kreg[u].z;
+                                kreg[u].y = kreg[u].w;
+                                o.x = h2_bits(__hmul2(__hsub2(bits_h2((a & 0x00ff00ffu) | 0x64006400u), off), s2[u]));
+                                o.y = h2_bits(__hmul2(__hsub2(bits_h2(((a >> 8) & 0x00ff00ffu) | 0x64006400u), off), s2[u]));
+                                o.z = h2_bits(__hmul2(__hsub2(bits_h2((b & 0x00ff00ffu) | 0x64006400u), off), s2[u]));
+                                o.w = h2_bits(__hmul2(__hsub2(bits_h2(((b >> 8) & 0x00ff00ffu) | 0x64006400u), off), s2[u]));
                             }
-                            *reinterpret_cast<uint4 *>(dst + ((((c & 3) * 2 + j) ^ (k & 7)) * 16)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
+                            *reinterpret_cast<uint4 *>(dst[u] + ((sw[u] ^ j) * 16)) = o;
                         }
                     }
                 }
@@ -919,10 +939,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 
                 // ---- values, transposed: code 2^-24 (an fp16 subnormal) times
                 // scale 2^24 plus bias
-                if (n >= ST) {
-                    ok = __all_sync(FULL, wait(&vempty[st], ((n / ST) & 1) ^ 1));
-                    if (!ok) break;
-                }
 #pragma unroll
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
