@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     __shared__ uint64_t sfull[MT][2], pfull[MT][2], odone[MT][2], ofree[MT], qfull[MT];
     __shared__ PfTile s_tile[kPfSlots];
     __shared__ PfCursor s_cur[kPfThreads / 32];
-    __shared__ PfPiece s_piece[kPfThreads / 32];
+    __shared__ PfPiece s_piece[kPfThreads / 32], s_soft[8][2];
     __shared__ uint64_t rfull[kPfSlots], rempty[kPfSlots];
     __shared__ int s_quot, s_rest, s_begin;
     __shared__ uint32_t s_tmem;
@@ -445,25 +445,52 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         int longer = 0;          // of the pieces, those of two steps and more
         int begin = s_begin;     // the unit the run stands at
         bool ok = true;
-        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
+        int turn = 0;
+        bool more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][0], lane);
+        for (; ok && more; turn ^= 1) {
+            const PfPiece &w = s_soft[warp - 4][turn];
+            more = false;
             const int nlive = min(RB, w.rows - w.rb * RB);
             const int tiles = w.tb - w.ta;
-            if (r * 128 < nlive) {
+            if (r * 128 >= nlive) {
+                more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
+            } else {
                 // ---- the row's queries: fp16 at a power of two, the group
-                // sums in the further columns
+                // sums in the further columns.  The warp copies its 32 rows
+                // into the tile as they are, whole rows at a time; then each
+                // thread converts its own row in place.
                 const int i_blk = r * 128 + row;
                 const bool live = i_blk < nlive;
                 const int rr = w.rb * RB + (live ? i_blk : 0);
-                const uint4 *src = reinterpret_cast<const uint4 *>(
-                    p.q + (int64_t)(w.s.first + rr / p.rep) * p.q_stride +
-                    (int64_t)(w.hk * p.rep + rr % p.rep) * D);
+                const int tok = rr / p.rep, head = w.hk * p.rep + rr % p.rep;
+                const uint16_t *src = p.q + (int64_t)(w.s.first + tok) * p.q_stride + (int64_t)head * D;
+                unsigned char *const qt = smem + L::Q_OFF + (size_t)r * L::QTILE;
+                // chunk c (16 bytes) of a row of the tile
+                auto q_at = [&](int row_, int c) {
+                    return qt + (c >> 3) * 16384 + row_ * 128 + (((c & 7) ^ (row_ & 7)) * 16);
+                };
+                constexpr int CR = D / 8, RPI = 32 / CR;  // chunks of a row, rows at a time
+#pragma unroll 4
+                for (int it = 0; it < 32 / RPI; ++it) {
+                    const int from = it * RPI + lane / CR, c = lane % CR;
+                    const uint16_t *ptr = reinterpret_cast<const uint16_t *>(
+                        __shfl_sync(FULL, reinterpret_cast<unsigned long long>(src), from));
+                    unsigned char *dst = q_at(q4 * 32 + from, c);
+                    if (r * 128 + q4 * 32 + from < nlive)
+                        cp_async<16>(dst, ptr + c * 8);
+                    else
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                __syncwarp();
                 float mx = 0.f, sum[G];
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     sum[g] = 0.f;
-#pragma unroll
+#pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
-                        const uint4 u = live ? src[g * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
+                        const uint4 u = *reinterpret_cast<const uint4 *>(q_at(row, g * 8 + c));
                         const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -477,29 +504,25 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 float up, down;
                 range_scale(mx, up, down);
                 if (p.scale < 0.f) up = -up;  // factors are kept non-negative
-                unsigned char *qt = smem + L::Q_OFF + (size_t)r * L::QTILE + row * 128;
+#pragma unroll 2
+                for (int c = 0; c < CR; ++c) {
+                    uint4 *at = reinterpret_cast<uint4 *>(q_at(row, c));
+                    const uint4 u = *at;
+                    float v[8];
+                    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x);
+                    v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+                    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z);
+                    v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
 #pragma unroll
-                for (int g = 0; g < G; ++g)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint4 u = live ? src[g * 8 + c] : make_uint4(0u, 0u, 0u, 0u);
-                        float v[8];
-                        v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x);
-                        v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
-                        v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z);
-                        v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] *= up;
-                        // the order in which the keys' codes unpack
-                        uint4 o;
-                        if constexpr (BITS == 4)
-                            o = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]),
-                                           pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
-                        else
-                            o = make_uint4(pack_f16(v[0], v[2]), pack_f16(v[1], v[3]),
-                                           pack_f16(v[4], v[6]), pack_f16(v[5], v[7]));
-                        *reinterpret_cast<uint4 *>(qt + g * 16384 + ((c ^ (row & 7)) * 16)) = o;
-                    }
+                    for (int k = 0; k < 8; ++k) v[k] *= up;
+                    // the order in which the keys' codes unpack
+                    if constexpr (BITS == 4)
+                        *at = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]),
+                                         pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
+                    else
+                        *at = make_uint4(pack_f16(v[0], v[2]), pack_f16(v[1], v[3]),
+                                         pack_f16(v[4], v[6]), pack_f16(v[5], v[7]));
+                }
                 {
                     // per group (hi, lo, hi) against the keys' (hi, hi, lo)
                     float e[16];
@@ -521,10 +544,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[r]);
+                // the next piece, while this one's scores start
+                more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
 
                 const float fac = down * fabsf(p.scale) * 1.4426950408889634f;
                 const int lim = !live ? w.s.len
-                                : p.causal ? min(w.s.len, w.s.len - w.s.count + rr / p.rep + 1)
+                                : p.causal ? min(w.s.len, w.s.len - w.s.count + tok + 1)
                                            : w.s.len;
                 const int least = __reduce_min_sync(FULL, lim);
                 float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
@@ -647,34 +672,56 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     tc_fence_after();
                     const bool whole = w.ta == 0 && w.tb == w.nt;
                     const float inv = l == 0.f ? 0.f : v_down / l;
+                    // the rows leave through the (free) query tile, whole rows at
+                    // a time: bf16 at once, fp32 pieces in two halves
                     float *part = p.part + ((int64_t)(2 * cta + piece) * RB + i_blk) * (D + 4);
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        p.out + ((int64_t)(w.s.first + rr / p.rep) * p.Hq + w.hk * p.rep + rr % p.rep) * D);
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        float v[32];
-                        tc_ld32(t_o + c * 32, v);
-                        if (live && whole) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float *x = v + 8 * k;
-                                dst[c * 4 + k] = make_uint4(
-                                    pack_bf16(x[0] * kVDown * inv, x[1] * kVDown * inv),
-                                    pack_bf16(x[2] * kVDown * inv, x[3] * kVDown * inv),
-                                    pack_bf16(x[4] * kVDown * inv, x[5] * kVDown * inv),
-                                    pack_bf16(x[6] * kVDown * inv, x[7] * kVDown * inv));
-                            }
-                        } else if (live) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                reinterpret_cast<float4 *>(part + c * 32)[k] =
-                                    make_float4(v[4 * k] * kVDown * v_down, v[4 * k + 1] * kVDown * v_down,
-                                                v[4 * k + 2] * kVDown * v_down, v[4 * k + 3] * kVDown * v_down);
+                    uint16_t *o_row = p.out + ((int64_t)(w.s.first + tok) * p.Hq + head) * D;
+                    auto flush = [&](void *mine) {
+                        __syncwarp();
+#pragma unroll 4
+                        for (int it = 0; it < 32 / RPI; ++it) {
+                            const int from = it * RPI + lane / CR, c = lane % CR;
+                            uint4 *dst = reinterpret_cast<uint4 *>(
+                                __shfl_sync(FULL, reinterpret_cast<unsigned long long>(mine), from));
+                            const uint4 u = *reinterpret_cast<const uint4 *>(q_at(q4 * 32 + from, c));
+                            if (r * 128 + q4 * 32 + from < nlive) dst[c] = u;
                         }
-                    }
-                    if (live && !whole) {
-                        part[D] = m;
-                        part[D + 1] = l;
+                        __syncwarp();
+                    };
+                    if (whole) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            float x[16];
+                            tc_ld16(t_o + c * 16, x);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) x[k] = x[k] * kVDown * inv;
+                            *reinterpret_cast<uint4 *>(q_at(row, 2 * c)) =
+                                make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                           pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+                            *reinterpret_cast<uint4 *>(q_at(row, 2 * c + 1)) =
+                                make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]),
+                                           pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
+                        }
+                        flush(o_row);
+                    } else {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float x[16];
+                                tc_ld16(t_o + h * (D / 2) + c * 16, x);
+#pragma unroll
+                                for (int k = 0; k < 16; k += 4)
+                                    *reinterpret_cast<float4 *>(q_at(row, 4 * c + k / 4)) =
+                                        make_float4(x[k] * kVDown * v_down, x[k + 1] * kVDown * v_down,
+                                                    x[k + 2] * kVDown * v_down, x[k + 3] * kVDown * v_down);
+                            }
+                            flush(part + h * (D / 2));
+                        }
+                        if (live) {
+                            part[D] = m;
+                            part[D + 1] = l;
+                        }
                     }
                     if (r == 0 && row == 0 && w.ta == 0 && !whole) {
                         const int last = pg_owner(s_quot, s_rest, begin + w.nt - 1);
