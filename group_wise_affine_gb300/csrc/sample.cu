@@ -13,27 +13,43 @@
 // whole at 2^19 tokens.
 //
 // The kept tokens are a prefix of the order (logit descending, index
-// ascending): all logits above a cut, and the first n that equal it.  The
-// cut is found digit by digit on order-preserving integer keys of the
-// logits (16 bits for bf16, 32 for fp32) with a histogram per digit, of
-// counts for top-k and of masses for top-p.
+// ascending), so a cut is one logit and one index: kept are the logits above
+// it and its equals up to the index.  It is found in two steps: a histogram,
+// counts and masses together, over 2048 equal steps of the base-2 exponent y
+// between the row's smallest value (or 2^-41, whose masses are zero) and its
+// largest, which serves top-k and top-p alike; then the tokens of the one
+// step that holds the cut (a few hundred) are gathered and ranked by one CTA.
+// Steps of y spread the tokens of a real row over many counters (the high
+// bits of the logits put most of them on a handful, whose atomics then
+// queue).  A step that holds more than 2048 tokens (equal or clustered
+// logits) is searched digit by digit on order-preserving integer keys
+// instead.
 //
 // A row belongs to a cluster of CTAs.  Each keeps its slice of the row in
-// shared memory as keys, read from HBM once; histograms and sums are joined
-// through distributed shared memory, each CTA adding up a share of the bins
-// and handing it to all.  One launch per call.  The cluster is the smallest
-// that holds the row, made larger while the rows leave SMs idle.
+// shared memory, read from HBM once; histograms and sums are joined through
+// distributed shared memory, each CTA adding up a share of the steps and
+// handing it to all.  One launch per call.  The cluster is the smallest that
+// holds the row, made larger while the rows leave SMs idle.
+//
+// Bound: instructions.  The logits are read once (256 rows of 151669 bf16,
+// 78 MB, are 11.5 us of HBM bandwidth), but top-p forms every token's mass
+// and counts it with three shared-memory atomics.
 #include <algorithm>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "mma.cuh"
 
 namespace gwa {
 
-constexpr int kSmThreads = 512;
+constexpr int kSmThreads = 1024;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 2048;
+constexpr int kSmList = 2048;  // tokens that one CTA ranks
 constexpr int kSmMaxCluster = 16;
 constexpr int64_t kSmSliceBytes = 160 * 1024;
 
@@ -80,22 +96,28 @@ struct SmKey<false> {
     static __device__ __forceinline__ int width(int pass) { return pass == 2 ? 10 : 11; }
 };
 
-// Shared memory besides the keys.  `mine` is filled by this CTA, `all` by
-// every CTA of the cluster.
+// Shared memory besides the slice.
 struct SmShared {
-    uint32_t cnt[kSmBins], lo[kSmBins], hi[kSmBins];  // this CTA's histogram
-    uint32_t all_cnt[kSmBins];
-    u64 all_mass[kSmBins];
-    u64 x_mass[kSmMaxCluster];   // one value from every CTA
+    union {
+        struct {
+            uint32_t cnt[kSmBins], lo[kSmBins], hi[kSmBins];  // this CTA's histogram
+            uint32_t all_cnt[kSmBins];                        // the cluster's
+            u64 all_mass[kSmBins];
+        };
+        u64 list[kSmList];  // gathered tokens (in rank 0), see list_key
+    };
+    u64 x_mass[kSmMaxCluster];      // one value from every CTA
+    float x_top[kSmMaxCluster], x_low[kSmMaxCluster];
     uint32_t x_word[kSmMaxCluster];
-    u64 w_mass[kSmWarps];        // one value from every warp
-    uint32_t w_word[kSmWarps];
-    u64 t_mass[kSmThreads / 32 + 1];
-    uint32_t t_cnt[kSmThreads / 32 + 1];
-    // the digit a search settled on
-    uint32_t f_digit, f_count;
+    u64 w_mass[kSmWarps], t_mass[kSmWarps];  // one value from every warp
+    uint32_t w_word[kSmWarps], t_cnt[kSmWarps];
+    float w_top[kSmWarps], w_low[kSmWarps];
+    uint32_t list_n;                // gathered so far (in rank 0)
+    // what a search settled on
+    uint32_t f_bin, f_count, f_above_cnt;
     u64 f_above_mass;
-    uint32_t f_above_cnt;
+    float cut_x;
+    uint32_t cut_idx;
 };
 
 template <typename T>
@@ -108,11 +130,20 @@ __device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
 // A row's weights.
 struct SmRow {
     float top, per;
+    // base-2 exponent of a logit's mass relative to the largest's: <= 0, NaN
+    // for a NaN logit
+    __device__ __forceinline__ float expo(float x) const {
+        return x == top ? 0.f : __fmul_rn(__fsub_rn(x, top), per);
+    }
+    // floor(2^40 exp2f(y)).  From -44 to 0 exp2f gives ex2's value (checked
+    // for every float there); below -40 the mass is zero.
+    static __device__ __forceinline__ u64 mass_of(float y) {
+        if (!(y >= -41.f)) return 0;
+        const uint32_t b = __float_as_uint(ex2(y));  // 2^-41 .. 1
+        return ((u64)((b & 0x7fffffu) | 0x800000u) << 17) >> (127 - (b >> 23));
+    }
     __device__ __forceinline__ u64 mass(float x) const {
-        if (x == -INFINITY) return 0;
-        const float y = x == top ? 0.f : __fmul_rn(__fsub_rn(x, top), per);
-        const float e = exp2f(y);
-        return e <= 1.f ? __float2ull_rz(e * 1099511627776.f) : 0;
+        return x == -INFINITY ? 0 : mass_of(expo(x));
     }
 };
 
@@ -125,123 +156,32 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
 template <bool BF16>
 struct Sampler {
     using K = SmKey<BF16>;
-    using Key = typename K::Key;
+    using Raw = typename K::Raw;
+    static constexpr int PER = 16 / sizeof(Raw);  // logits of a 16-byte chunk
     SmShared &sh;
-    Key *keys;
-    int n;          // keys of this CTA, a multiple of 8, padding (0) included
+    const Raw *raw;   // the slice; element e is token base + e
+    int first, last;  // its elements [first, last)
+    int64_t base;
     int cl, rank;
     SmRow row;
+    float steps;      // histogram steps per unit of y
 
-    // The digit search: the cut where the summed counts (MASS false) or
-    // masses reach `goal` from the top, over keys >= floor (keys equal to it
-    // taken floor_n times by rank 0).  Returns the cut's key; `above` is what
-    // lies above it, `count` the keys equal to it.
-    template <bool MASS>
-    __device__ Key search(u64 goal, bool whole_goal, float frac, Key floor_key, uint32_t floor_n,
-                          u64 &above, uint32_t &count) {
-        uint32_t prefix = 0;
-        int done = 0;  // bits settled
-        above = 0;
-        for (int pass = 0; pass < K::PASSES; ++pass) {
-            const int sft = K::shift(pass), wid = K::width(pass), bins = 1 << wid;
-            for (int i = threadIdx.x; i < bins; i += kSmThreads) {
-                sh.cnt[i] = 0;
-                if (MASS) sh.lo[i] = sh.hi[i] = 0;
-            }
-            __syncthreads();
-            auto add = [&](uint32_t bin, uint32_t c, u64 w) {
-                atomicAdd(&sh.cnt[bin], c);
-                if (MASS) {
-                    const uint32_t wl = (uint32_t)w;
-                    const uint32_t old = atomicAdd(&sh.lo[bin], wl);
-                    const uint32_t up = (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u);
-                    if (up) atomicAdd(&sh.hi[bin], up);
-                }
-            };
-            for (int i = threadIdx.x; i < n; i += kSmThreads) {
-                const uint32_t k = keys[i];
-                if (k <= floor_key) continue;
-                if (done && (k >> (K::BITS - done)) != prefix) continue;
-                const u64 w = MASS ? row.mass(K::value((Key)k)) : 0;
-                if (MASS && w == 0) continue;
-                add((k >> sft) & (bins - 1), 1u, w);
-            }
-            if (rank == 0 && threadIdx.x == 0 && floor_n &&
-                (!done || ((uint32_t)floor_key >> (K::BITS - done)) == prefix)) {
-                const u64 w = MASS ? row.mass(K::value(floor_key)) * floor_n : 0;
-                add(((uint32_t)floor_key >> sft) & (bins - 1), floor_n, w);
-            }
-            // join: each CTA adds a share of the bins and hands it to all
-            cluster_sync_all();
-            const int share = bins / cl;
-            for (int j = threadIdx.x; j < share; j += kSmThreads) {
-                const int bin = rank * share + j;
-                uint32_t c = 0;
-                u64 m = 0;
-                for (int r = 0; r < cl; ++r) {
-                    c += *cluster_ptr(&sh.cnt[bin], r);
-                    if (MASS)
-                        m += (u64)*cluster_ptr(&sh.lo[bin], r) +
-                             ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
-                }
-                for (int r = 0; r < cl; ++r) {
-                    *cluster_ptr(&sh.all_cnt[bin], r) = c;
-                    if (MASS) *cluster_ptr(&sh.all_mass[bin], r) = m;
-                }
-            }
-            cluster_sync_all();
-            // from the top: thread i holds bins top - per*i ..
-            const int per = bins > kSmThreads ? bins / kSmThreads : 1;
-            u64 sum = 0;
-            const int hi_bin = bins - 1 - threadIdx.x * per;
-            for (int j = 0; j < per; ++j)
-                if (hi_bin - j >= 0)
-                    sum += MASS ? sh.all_mass[hi_bin - j] : (u64)sh.all_cnt[hi_bin - j];
-            u64 incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
-                if ((int)(threadIdx.x & 31) >= o) incl += v;
-            }
-            if ((threadIdx.x & 31) == 31) sh.t_mass[threadIdx.x / 32] = incl;
-            __syncthreads();
-            u64 before = incl - sum, total = 0;
-            for (int w = 0; w < kSmWarps; ++w) {
-                if (w < (int)(threadIdx.x / 32)) before += sh.t_mass[w];
-                total += sh.t_mass[w];
-            }
-            if (pass == 0 && !whole_goal) {
-                // a share of everything; at least the first token
-                goal = (u64)((double)total * (double)frac);
-                if (goal < 1) goal = 1;
-            }
-            const u64 left = goal - above;  // within this prefix, >= 1
-            if (before < left && left <= before + sum) {
-                u64 a = before;
-                for (int j = 0; j < per; ++j) {
-                    const u64 v = MASS ? sh.all_mass[hi_bin - j] : (u64)sh.all_cnt[hi_bin - j];
-                    if (left <= a + v) {
-                        sh.f_digit = hi_bin - j;
-                        sh.f_above_mass = a;
-                        sh.f_count = sh.all_cnt[hi_bin - j];
-                        break;
-                    }
-                    a += v;
-                }
-            }
-            __syncthreads();
-            prefix = (prefix << wid) | sh.f_digit;
-            above += sh.f_above_mass;
-            count = sh.f_count;
-            done += wid;
-        }
-        goal_ = goal;
-        return (Key)prefix;
+    // NaN as -inf
+    __device__ __forceinline__ float value(int e) const {
+        const float x = __uint_as_float(BF16 ? (uint32_t)raw[e] << 16 : (uint32_t)raw[e]);
+        return x == x ? x : -INFINITY;
     }
-    u64 goal_;
+    // Ascending in the order of the tokens: logit downwards, then index.
+    static __device__ __forceinline__ u64 list_key(float x, uint32_t idx) {
+        return ((u64)~SmKey<false>::make(__float_as_uint(x)) << 32) | idx;
+    }
+    __device__ __forceinline__ int bin_of(float x) const {
+        // NaN and -inf (and everything past the range) in the last step
+        const float t = fminf(-row.expo(x) * steps, (float)(kSmBins - 1));
+        return x == -INFINITY ? kSmBins - 1 : (int)t;
+    }
 
-    // Sum over the cluster of one value from every CTA, and the sum of the
-    // lower ranks'.
+    // The cluster's sum of one value from every CTA, and the lower ranks'.
     __device__ u64 cluster_total(u64 v, u64 &before) {
         if (threadIdx.x < (unsigned)cl) *cluster_ptr(&sh.x_mass[rank], threadIdx.x) = v;
         cluster_sync_all();
@@ -253,147 +193,452 @@ struct Sampler {
         }
         return t;
     }
+
+    __device__ __forceinline__ void add(uint32_t bin, uint32_t c, u64 w, bool mass) {
+        atomicAdd(&sh.cnt[bin], c);
+        if (mass && w) {
+            // 64-bit sum from two 32-bit words: the carry shows in the old one
+            const uint32_t wl = (uint32_t)w;
+            const uint32_t old = atomicAdd(&sh.lo[bin], wl);
+            const uint32_t up = (uint32_t)(w >> 32) + (old + wl < old ? 1u : 0u);
+            if (up) atomicAdd(&sh.hi[bin], up);
+        }
+    }
+    __device__ void clear(int bins) {
+        for (int i = threadIdx.x; i < bins; i += kSmThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
+        __syncthreads();
+    }
+    // Adds the CTAs' histograms up, a share of the bins each (a lane per bin
+    // and CTA), and hands the sums to all.
+    __device__ void join(int bins) {
+        cluster_sync_all();
+        const int share = bins / cl;
+        for (int i = threadIdx.x; i < share * cl; i += kSmThreads) {  // whole warps: bins >= 256
+            const int bin = rank * share + i / cl, r = i % cl;
+            uint32_t c = *cluster_ptr(&sh.cnt[bin], r);
+            u64 m = (u64)*cluster_ptr(&sh.lo[bin], r) + ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
+            for (int o = 1; o < cl; o <<= 1) {
+                c += __shfl_xor_sync(0xffffffffu, c, o);
+                m += __shfl_xor_sync(0xffffffffu, m, o);
+            }
+            *cluster_ptr(&sh.all_cnt[bin], r) = c;
+            *cluster_ptr(&sh.all_mass[bin], r) = m;
+        }
+        cluster_sync_all();
+    }
+    // The bin where the count, or the mass, first reaches `goal`, walking the
+    // bins upwards (or DOWN from the last); `goal` of 0 with share >= 0 is
+    // that share of the total (at least 1).  Returns the goal; f_* are set.
+    template <bool DOWN>
+    __device__ u64 locate(int bins, bool mass, u64 goal, float share) {
+        const int per = (bins + kSmThreads - 1) / kSmThreads;
+        u64 sum = 0;
+        uint32_t cn = 0;
+        for (int j = 0; j < per; ++j) {
+            const int b = threadIdx.x * per + j;
+            if (b < bins) {
+                sum += sh.all_mass[DOWN ? bins - 1 - b : b];
+                cn += sh.all_cnt[DOWN ? bins - 1 - b : b];
+            }
+        }
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        u64 im = sum;
+        uint32_t ic = cn;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 v = __shfl_up_sync(0xffffffffu, im, o);
+            const uint32_t c = __shfl_up_sync(0xffffffffu, ic, o);
+            if (lane >= o) {
+                im += v;
+                ic += c;
+            }
+        }
+        if (lane == 31) {
+            sh.t_mass[warp] = im;
+            sh.t_cnt[warp] = ic;
+        }
+        __syncthreads();
+        u64 bm = im - sum, total = 0;
+        uint32_t bc = ic - cn;
+        for (int w = 0; w < kSmWarps; ++w) {
+            if (w < warp) {
+                bm += sh.t_mass[w];
+                bc += sh.t_cnt[w];
+            }
+            total += sh.t_mass[w];
+        }
+        if (share >= 0.f) {
+            goal = (u64)((double)total * (double)share);
+            if (goal < 1) goal = 1;
+        }
+        for (int j = 0; j < per; ++j) {
+            const int k = threadIdx.x * per + j, b = DOWN ? bins - 1 - k : k;
+            if (k >= bins) break;
+            const u64 m = sh.all_mass[b];
+            const uint32_t c = sh.all_cnt[b];
+            const u64 at = mass ? bm : bc, v = mass ? m : c;
+            if (at < goal && goal <= at + v) {
+                sh.f_bin = b;
+                sh.f_count = c;
+                sh.f_above_mass = bm;
+                sh.f_above_cnt = bc;
+            }
+            bm += m;
+            bc += c;
+        }
+        __syncthreads();
+        return goal;
+    }
+
+    // ---- the cut among the tokens of histogram step `bin` that lie above
+    // (x, idx): their first `want` (by count), or as many as reach `want`
+    // (by mass).  Leaves the last kept token in cut_x, cut_idx.
+    __device__ void refine(int bin, uint32_t count, bool mass, u64 want, bool cut, float cut_x,
+                           uint32_t cut_idx) {
+        auto in = [&](float x, uint32_t idx) {
+            return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
+        };
+        if (count <= kSmList) {
+            // gathered in rank 0, in any order
+            if (threadIdx.x == 0) sh.list_n = 0;
+            cluster_sync_all();  // (also: the histogram is read, the list may overwrite it)
+            uint32_t *const n = cluster_ptr(&sh.list_n, 0);
+            u64 *const list = cluster_ptr(sh.list, 0);
+            const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+            for (int e0 = first & ~31; e0 < last; e0 += kSmThreads) {
+                const int e = e0 + threadIdx.x;
+                const bool ok = e >= first && e < last && in(value(e), (uint32_t)(base + e));
+                const unsigned m = __ballot_sync(0xffffffffu, ok);
+                if (!m) continue;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(n, (uint32_t)__popc(m));
+                at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+                if (ok && at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
+            }
+            cluster_sync_all();
+            if (rank == 0) {
+                // in order, by a bitonic sort, and counted up
+                const int total = min((int)sh.list_n, kSmList);
+                int size = 2;
+                while (size < total) size *= 2;
+                for (int i = total + threadIdx.x; i < size; i += kSmThreads) sh.list[i] = ~0ull;
+                __syncthreads();
+                for (int k = 2; k <= size; k *= 2)
+                    for (int d = k / 2; d > 0; d /= 2) {
+                        for (int i = threadIdx.x; i < size / 2; i += kSmThreads) {
+                            const int a = 2 * i - (i & (d - 1)), b = a + d;
+                            const u64 x = sh.list[a], y = sh.list[b];
+                            if ((x > y) == ((a & k) == 0)) {
+                                sh.list[a] = y;
+                                sh.list[b] = x;
+                            }
+                        }
+                        __syncthreads();
+                    }
+                constexpr int PT = kSmList / kSmThreads;
+                u64 own[PT], sum = 0;
+                float x[PT];
+#pragma unroll
+                for (int j = 0; j < PT; ++j) {
+                    const int i = threadIdx.x * PT + j;
+                    x[j] = i < total ? SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32)) : 0.f;
+                    own[j] = i >= total ? 0 : mass ? row.mass(x[j]) : 1;
+                    sum += own[j];
+                }
+                u64 incl = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                if (lane == 31) sh.t_mass[warp] = incl;
+                __syncthreads();
+                u64 before = incl - sum;
+                for (int w = 0; w < warp; ++w) before += sh.t_mass[w];
+#pragma unroll
+                for (int j = 0; j < PT; ++j) {
+                    if (before < want && want <= before + own[j])
+                        for (int r = 0; r < cl; ++r) {
+                            *cluster_ptr(&sh.cut_x, r) = x[j];
+                            *cluster_ptr(&sh.cut_idx, r) = (uint32_t)sh.list[threadIdx.x * PT + j];
+                        }
+                    before += own[j];
+                }
+            }
+            cluster_sync_all();
+            return;
+        }
+        // too many: digit by digit on integer keys
+        uint32_t prefix = 0;
+        int done = 0;
+        u64 above = 0;
+        for (int pass = 0; pass < K::PASSES; ++pass) {
+            const int sft = K::shift(pass), wid = K::width(pass), bins = 1 << wid;
+            if (pass == 0) cluster_sync_all();  // the histogram is read
+            clear(bins);
+            for (int e = first + threadIdx.x; e < last; e += kSmThreads) {
+                const float x = value(e);
+                if (!in(x, (uint32_t)(base + e))) continue;
+                const uint32_t k = K::make(raw[e]);
+                if (done && (k >> (K::BITS - done)) != prefix) continue;
+                add((k >> sft) & (bins - 1), 1u, mass ? row.mass(x) : 0, mass);
+            }
+            join(bins);
+            locate<true>(bins, mass, want - above, -1.f);
+            prefix = (prefix << wid) | sh.f_bin;
+            above += mass ? sh.f_above_mass : sh.f_above_cnt;
+            done += wid;
+            __syncthreads();
+        }
+        // the cut's key; of its equals, so many by index
+        const float x = K::value((typename K::Key)prefix);
+        const u64 left = want - above;
+        const u64 own = mass ? row.mass(x) : 1;
+        const u64 nth = (left + own - 1) / own;  // 1-based
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        const int run = ((last - first + kSmWarps - 1) / kSmWarps + 31) & ~31;
+        const int a = first + warp * run, b = min(last, a + run);
+        uint32_t c = 0;
+        for (int e0 = a; e0 < b; e0 += 32) {
+            const int e = e0 + lane;
+            c += __popc(__ballot_sync(0xffffffffu, e < b && value(e) == x && in(x, (uint32_t)(base + e))));
+        }
+        if (lane == 0) sh.w_word[warp] = c;
+        __syncthreads();
+        u64 mine = 0, before = 0, at = 0;
+        for (int w = 0; w < kSmWarps; ++w) {
+            if (w < warp) at += sh.w_word[w];
+            mine += sh.w_word[w];
+        }
+        cluster_total(mine, before);
+        at += before;
+        if (at < nth && nth <= at + c)
+            for (int e0 = a; e0 < b; e0 += 32) {
+                const int e = e0 + lane;
+                const bool eq = e < b && value(e) == x && in(x, (uint32_t)(base + e));
+                const unsigned m = __ballot_sync(0xffffffffu, eq);
+                if (eq && at + __popc(m & ((1u << lane) - 1u)) + 1 == nth)
+                    for (int r = 0; r < cl; ++r) {
+                        *cluster_ptr(&sh.cut_x, r) = x;
+                        *cluster_ptr(&sh.cut_idx, r) = (uint32_t)(base + e);
+                    }
+                at += __popc(m);
+            }
+        cluster_sync_all();
+    }
 };
 
 template <bool BF16>
 __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, int cl) {
-    using K = SmKey<BF16>;
-    using Key = typename K::Key;
-    using Raw = typename K::Raw;
-    constexpr int PER = 16 / sizeof(Raw);  // logits of a 16-byte chunk
+    using S = Sampler<BF16>;
+    using Raw = typename S::Raw;
+    constexpr int PER = S::PER;
+    constexpr unsigned FULL = 0xffffffffu;
     extern __shared__ __align__(16) unsigned char sm_raw[];
     SmShared &sh = *reinterpret_cast<SmShared *>(sm_raw);
-    Key *keys = reinterpret_cast<Key *>(sm_raw + ((sizeof(SmShared) + 15) / 16) * 16);
+    Raw *slice = reinterpret_cast<Raw *>(sm_raw + ((sizeof(SmShared) + 15) / 16) * 16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int rank = cl > 1 ? (int)cluster_rank() : 0;
     const int64_t r = blockIdx.x / cl;
     if (tid == 0) pdl_launch_dependents();
     pdl_wait_primary();
 
-    // ---- this CTA's slice as keys; chunks start on 16 bytes of the input
+    // ---- this CTA's slice; chunks start on 16 bytes of the input, so the
+    // slice starts at element `mis` of its first chunk
     const int64_t per_cta = (p.V + cl - 1) / cl;
     const int64_t lo = min(p.V, rank * per_cta), hi = min(p.V, lo + per_cta);
     const Raw *src = static_cast<const Raw *>(p.logits) + r * p.stride + lo;
     const int len = (int)(hi - lo);
     const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Raw));
     const int chunks = (len + mis + PER - 1) / PER;
-    uint32_t top_key = 0;
+    float top = -INFINITY, low = INFINITY;  // low: the smallest finite logit
+    auto see = [&](Raw v) {
+        const float x = BF16 ? __uint_as_float((uint32_t)v << 16) : __uint_as_float((uint32_t)v);
+        top = fmaxf(top, x);
+        low = fminf(low, x == -INFINITY ? INFINITY : x);
+    };
     for (int j = tid; j < chunks; j += kSmThreads) {
         const int e0 = j * PER - mis;
-        Raw v[PER];
-        Key k[PER];
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
         if (e0 >= 0 && e0 + PER <= len) {
-            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(src + e0);
+            u = *reinterpret_cast<const uint4 *>(src + e0);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < PER; ++i) k[i] = K::make(v[i]);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF16) {
+                    see((Raw)(w[i] & 0xffffu));
+                    see((Raw)(w[i] >> 16));
+                } else {
+                    see(w[i]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(slice + j * PER) = u;
         } else {
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                k[i] = e0 + i >= 0 && e0 + i < len ? K::make(src[e0 + i]) : (Key)0;
+                if (e0 + i >= 0 && e0 + i < len) {
+                    const Raw v = src[e0 + i];
+                    see(v);
+                    slice[j * PER + i] = v;
+                }
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) top_key = max(top_key, (uint32_t)k[i]);
-        *reinterpret_cast<uint4 *>(keys + j * PER) = *reinterpret_cast<uint4 *>(k);
     }
-    const int n = chunks * PER;
-    top_key = __reduce_max_sync(0xffffffffu, top_key);
-    if (lane == 0) sh.w_word[warp] = top_key;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+        low = fminf(low, __shfl_xor_sync(FULL, low, o));
+    }
+    if (lane == 0) {
+        sh.w_top[warp] = top;
+        sh.w_low[warp] = low;
+    }
     __syncthreads();
-    for (int w = 0; w < kSmWarps; ++w) top_key = max(top_key, sh.w_word[w]);
+    for (int w = 0; w < kSmWarps; ++w) {
+        top = fmaxf(top, sh.w_top[w]);
+        low = fminf(low, sh.w_low[w]);
+    }
     // every CTA of the cluster runs: its shared memory may be written
     cluster_sync_all();
-    if (tid < cl) *cluster_ptr(&sh.x_word[rank], tid) = top_key;
+    if (tid < cl) {
+        *cluster_ptr(&sh.x_top[rank], tid) = top;
+        *cluster_ptr(&sh.x_low[rank], tid) = low;
+    }
     cluster_sync_all();
-    for (int c = 0; c < cl; ++c) top_key = max(top_key, sh.x_word[c]);
+    for (int c = 0; c < cl; ++c) {
+        top = fmaxf(top, sh.x_top[c]);
+        low = fminf(low, sh.x_low[c]);
+    }
+    if (top == -INFINITY) {  // nothing to draw (the whole cluster leaves)
+        if (rank == 0 && tid == 0) {
+            p.token[r] = -1;
+            if (p.prob) p.prob[r] = 0.f;
+        }
+        return;
+    }
 
     const float T = p.temperature ? p.temperature[r] : 1.f;
     const int kq = p.top_k ? p.top_k[r] : 0;
     const float tp = p.top_p ? p.top_p[r] : 1.f;
     const float mp = p.min_p ? p.min_p[r] : 0.f;
     const float u = p.u[r];
-    SmRow row;
-    row.top = K::value((Key)top_key);
-    row.per = __fmul_rn(__fdiv_rn(1.f, T), 1.4426950408889634f);
-    const bool none = row.top == -INFINITY, greedy = !(T > 0.f);
+    const bool greedy = !(T > 0.f);
+    S s{sh, slice, mis, mis + len, lo - mis, cl, rank, {top, 0.f}, 0.f};
+    s.row.per = __fmul_rn(__fdiv_rn(1.f, T), 1.4426950408889634f);
 
-    Sampler<BF16> s{sh, keys, n, cl, rank, row, 0};
-    // the cut: keys above it are kept, and the first cut_n equal to it
-    Key cut = (Key)0;
-    uint32_t cut_n = 0;
-    bool limited = false;
-    u64 dummy = 0;
-    if (none) {
-        if (rank == 0 && tid == 0) {
-            p.token[r] = -1;
-            if (p.prob) p.prob[r] = 0.f;
+    // ---- the cut: kept are logits above cut_x, and its equals up to cut_idx
+    bool cut = false;
+    float cut_x = 0.f;
+    uint32_t cut_idx = 0;
+    const bool by_k = !greedy && kq > 0 && kq < p.V, by_p = !greedy && tp < 1.f;
+    if (by_k || by_p) {
+        const float range = fminf(41.f, low < top ? -s.row.expo(low) : 0.f);
+        s.steps = range > 0.f ? fminf((float)kSmBins / range, 1e30f) : 0.f;
+        s.clear(kSmBins);
+        // (the mass only where top-p needs it)
+        for (int j = tid; j < chunks; j += kSmThreads) {
+            const uint4 c = *reinterpret_cast<const uint4 *>(slice + j * PER);
+            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = j * PER + i;
+                if (e < mis || e >= mis + len) continue;
+                const float x = BF16 ? (i & 1 ? bf16_hi(cw[i / 2]) : bf16_lo(cw[i / 2]))
+                                     : __uint_as_float(cw[i % 4]);
+                const float y = s.row.expo(x);
+                const float t = fminf(-y * s.steps, (float)(kSmBins - 1));
+                const int bin = x == -INFINITY ? kSmBins - 1 : (int)t;
+                s.add(bin, 1u, by_p && x != -INFINITY ? SmRow::mass_of(y) : 0, by_p);
+            }
         }
-        return;  // the whole cluster returns; nothing remote is in flight
-    }
-    if (greedy) {
-        cut = (Key)top_key;
-        cut_n = 1;
-        limited = true;
-    } else {
-        if (kq > 0 && kq < p.V) {
-            u64 above;
-            uint32_t count;
-            cut = s.template search<false>((u64)kq, true, 0.f, (Key)0, 0, above, count);
-            cut_n = (uint32_t)((u64)kq - above);
-            limited = cut_n < count;
+        s.join(kSmBins);
+        int bin_k = kSmBins;
+        if (by_k) {
+            s.template locate<false>(kSmBins, false, (u64)kq, -1.f);
+            bin_k = sh.f_bin;
+            const uint32_t n = sh.f_count, above = sh.f_above_cnt;
+            __syncthreads();
+            // the steps' own sums stay with a thread each while the list (on
+            // the same memory) is in use
+            u64 keep_m[kSmBins / kSmThreads];
+            uint32_t keep_c[kSmBins / kSmThreads];
+#pragma unroll
+            for (int i = 0; i < kSmBins / kSmThreads; ++i) {
+                keep_m[i] = sh.all_mass[tid + i * kSmThreads];
+                keep_c[i] = sh.all_cnt[tid + i * kSmThreads];
+            }
+            s.refine(bin_k, n, false, (u64)kq - above, false, 0.f, 0);
+            cut = true;
+            cut_x = sh.cut_x;
+            cut_idx = sh.cut_idx;
+            __syncthreads();
+            if (by_p) {
+                // what top-p goes by: the steps above, and of this one the kept
+                u64 m = 0;
+                uint32_t c = 0;
+                for (int e = mis + tid; e < mis + len; e += kSmThreads) {
+                    const float x = s.value(e);
+                    if (!(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) continue;
+                    if (s.bin_of(x) != bin_k) continue;
+                    m += s.row.mass(x);
+                    ++c;
+                }
+                m = warp_sum64(m);
+                c = __reduce_add_sync(FULL, c);
+                if (lane == 0) {
+                    sh.w_mass[warp] = m;
+                    sh.w_word[warp] = c;
+                }
+                __syncthreads();
+                m = 0;
+                c = 0;
+                for (int w = 0; w < kSmWarps; ++w) {
+                    m += sh.w_mass[w];
+                    c += sh.w_word[w];
+                }
+                u64 before;
+                if (tid < cl) *cluster_ptr(&sh.x_word[rank], tid) = c;
+                m = s.cluster_total(m, before);
+                c = 0;
+                for (int w = 0; w < cl; ++w) c += sh.x_word[w];
+#pragma unroll
+                for (int i = 0; i < kSmBins / kSmThreads; ++i) {
+                    const int b = tid + i * kSmThreads;
+                    sh.all_mass[b] = b < bin_k ? keep_m[i] : b == bin_k ? m : 0;
+                    sh.all_cnt[b] = b < bin_k ? keep_c[i] : b == bin_k ? c : 0;
+                }
+                __syncthreads();
+            }
         }
-        if (tp < 1.f) {
-            u64 above;
-            uint32_t count;
-            const Key c = s.template search<true>(0, false, fmaxf(tp, 0.f), cut, cut_n, above, count);
-            const u64 w = row.mass(K::value(c));
-            const uint32_t cn = (uint32_t)((s.goal_ - above + w - 1) / w);
-            limited = c == cut && cut_n ? limited || cn < cut_n : cn < count;
-            cut = c;
-            cut_n = cn;
+        if (by_p) {
+            const u64 goal = s.template locate<false>(kSmBins, true, 0, fmaxf(tp, 0.f));
+            const int bin = sh.f_bin;
+            const uint32_t n = sh.f_count;
+            const u64 above = sh.f_above_mass;
+            __syncthreads();
+            s.refine(bin, n, true, goal - above, cut, cut_x, cut_idx);
+            cut = true;
+            cut_x = sh.cut_x;
+            cut_idx = sh.cut_idx;
         }
     }
     const u64 least = !greedy && mp > 0.f
                           ? __float2ull_rz(fminf(mp, 1.f) * 1099511627776.f) : 0;
-    const bool has_cut = cut_n > 0;
-    // a warp takes a run of whole 32-key steps, in index order
-    const int steps = (n + 31) / 32;
-    const int s0 = (int)((int64_t)steps * warp / kSmWarps);
-    const int s1 = (int)((int64_t)steps * (warp + 1) / kSmWarps);
-    u64 eq_before = 0;  // keys equal to the cut before this warp's run
-    if (limited) {
-        uint32_t c = 0;
-        for (int st = s0; st < s1; ++st) {
-            const int i = st * 32 + lane;
-            c += __popc(__ballot_sync(0xffffffffu, i < n && keys[i] == cut));
-        }
-        if (lane == 0) sh.w_word[warp] = c;
-        __syncthreads();
-        u64 mine = 0, before;
-        for (int w = 0; w < kSmWarps; ++w) {
-            if (w < warp) eq_before += sh.w_word[w];
-            mine += sh.w_word[w];
-        }
-        cluster_sync_all();  // x_mass may still be read
-        s.cluster_total(mine, before);
-        eq_before += before;
-        __syncthreads();
-    }
-    auto kept = [&](int i, u64 &eq) -> u64 {  // i < n or not: every lane calls
-        const Key k = i < n ? keys[i] : (Key)0;
-        bool in = !has_cut || k > cut;
-        if (has_cut) {
-            const unsigned m = __ballot_sync(0xffffffffu, k == cut);
-            if (k == cut)
-                in = !limited || eq + __popc(m & ((1u << lane) - 1u)) < cut_n;
-            eq += __popc(m);
-        }
-        if (!in || k == 0) return 0;
-        const u64 w = greedy ? 1 : row.mass(K::value(k));
+    // ---- the kept masses: a warp takes a run of whole 32-token steps, in
+    // index order
+    const int run = (((len + mis) + kSmWarps - 1) / kSmWarps + 31) & ~31;
+    const int a = warp * run, b = min(mis + len, a + run);
+    auto kept = [&](int e) -> u64 {
+        if (e < mis || e >= b) return 0;
+        const float x = s.value(e);
+        if (greedy) return x == top ? 1 : 0;
+        if (cut && !(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) return 0;
+        const u64 w = s.row.mass(x);
         return w >= least ? w : 0;
     };
-    u64 mine = 0, eq = eq_before;
-    for (int st = s0; st < s1; ++st) mine += kept(st * 32 + lane, eq);
+    u64 mine = 0;
+    for (int e0 = a; e0 < b; e0 += 32) mine += kept(e0 + lane);
     mine = warp_sum64(mine);
+    __syncthreads();
     if (lane == 0) sh.w_mass[warp] = mine;
     __syncthreads();
     u64 cta = 0, warp_before = 0, cta_before;
@@ -403,34 +648,47 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     }
     cluster_sync_all();  // x_mass may still be read
     const u64 all = s.cluster_total(cta, cta_before);
-    // the first token whose running mass passes u * all
-    u64 goal = (u64)((double)fmaxf(u, 0.f) * (double)all);
+    // the first token whose running mass passes u * all (greedy: the first)
+    u64 goal = greedy ? 0 : (u64)((double)fmaxf(u, 0.f) * (double)all);
     if (goal > all - 1) goal = all - 1;
     const u64 start = cta_before + warp_before;
     if (goal >= start && goal < start + mine) {
-        u64 run = start;
-        eq = eq_before;
-        for (int st = s0; st < s1; ++st) {
-            const int i = st * 32 + lane;
-            const u64 w = kept(i, eq);
+        u64 at = start;
+        for (int e0 = a; e0 < b; e0 += 32) {
+            const u64 w = kept(e0 + lane);
+            const u64 sum = warp_sum64(w);
+            if (goal >= at + sum) {
+                at += sum;
+                continue;
+            }
             u64 incl = w;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
+                const u64 v = __shfl_up_sync(FULL, incl, o);
                 if (lane >= o) incl += v;
             }
-            const unsigned past = __ballot_sync(0xffffffffu, run + incl > goal);
-            if (past) {
-                if (lane == __ffs(past) - 1) {
-                    p.token[r] = (int32_t)(lo + i - mis);
-                    if (p.prob) p.prob[r] = (float)((double)w / (double)all);
-                }
-                break;
+            const unsigned past = __ballot_sync(FULL, at + incl > goal);
+            if (lane == __ffs(past) - 1) {
+                p.token[r] = (int32_t)(s.base + e0 + lane);
+                if (p.prob) p.prob[r] = greedy ? 1.f : (float)((double)w / (double)all);
             }
-            run += __shfl_sync(0xffffffffu, incl, 31);
+            break;
         }
     }
-    (void)dummy;
+}
+
+// Clusters of more than eight CTAs, once per device and kernel.
+static cudaError_t allow_wide_clusters(const void *kernel) {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void *>> done;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({dev, kernel})) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.insert({dev, kernel});
+    return e;
 }
 
 template <bool BF16>
@@ -443,8 +701,7 @@ static cudaError_t launch_sample_t(const SampleParams &p, cudaStream_t st) {
     while (cl < kSmMaxCluster && p.rows * cl * 2 <= num_sms() && p.V / (2 * cl) >= 2048) cl *= 2;
     const size_t smem = head + ((size_t)((p.V + cl - 1) / cl) * esz + 48) / 16 * 16;
     cudaError_t e = allow_smem(kfn, (int)(head + kSmSliceBytes + 48));
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(kfn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = allow_wide_clusters(kfn);
     if (e != cudaSuccess) return e;
     return launch_pdl_cluster(kfn, (unsigned)(p.rows * cl), (unsigned)cl, kSmThreads, smem, st, p, cl);
 }
