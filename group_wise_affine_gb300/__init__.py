@@ -230,7 +230,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream, without the object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -597,15 +598,15 @@ def _token_rows(x: torch.Tensor, tokens: int, heads: int, dim: int,
                 name: str):
     """Pointer and token stride of bfloat16 [tokens, heads, dim], whose
     tokens may lie apart (a view of a fused projection's rows)."""
-    if x.dtype != torch.bfloat16 or tuple(x.shape) != (tokens, heads, dim):
+    if x.dtype != torch.bfloat16 or x.shape != (tokens, heads, dim):
         raise ValueError(f"{name} must be bfloat16 [{tokens}, {heads}, {dim}] "
                          f"(got {x.dtype} {list(x.shape)})")
     if not x.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    s = x.stride()
-    if tokens and (s[2] != 1 or (heads > 1 and s[1] != dim)):
+    row, head, one = x.stride()
+    if tokens and (one != 1 or (head != dim and heads > 1)):
         raise ValueError(f"{name}: only the token axis may be strided")
-    return x.data_ptr(), s[0] if tokens > 1 else heads * dim
+    return x.data_ptr(), row if tokens > 1 else heads * dim
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
@@ -657,16 +658,19 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache,
         qp, qs = _token_rows(q, T, Hq, D, "q")
         if q_out is None:
             q_out = _new((T, Hq, D), torch.bfloat16, q.device, stream)
-        _check_out(q_out, T * Hq * D, "q_out")
-        op = _ptr(q_out)
+            op = q_out.data_ptr()
+        else:
+            _check_out(q_out, T * Hq * D, "q_out")
+            op = _ptr(q_out)
     rp, rows, rot = None, 0, 0
     if rope is not None:
         if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[2] != 2:
             raise ValueError("rope must be float32 [rows, rot_dim/2, 2]")
         rp, rows, rot = _ptr(rope), rope.shape[0], 2 * rope.shape[1]
-    _check(load().gwa_kv_append(qp, qs, op, Hq, kp, ks, vp, vs, cache.c,
-                                batch.c, rp, rows, rot, _status(status),
-                                _stream(stream)))
+    rc = load().gwa_kv_append(qp, qs, op, Hq, kp, ks, vp, vs, cache.c, batch.c,
+                              rp, rows, rot, _status(status), _stream(stream))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -677,8 +681,10 @@ def kv_read(cache: KVCache, batch: KVBatch,
     shape = (batch.tokens, cache.heads, cache.dim)
     k = _new(shape, torch.bfloat16, cache.device, stream)
     v = _new(shape, torch.bfloat16, cache.device, stream)
-    _check(load().gwa_kv_read(cache.c, batch.c, _ptr(k), _ptr(v),
-                              _status(status), _stream(stream)))
+    rc = load().gwa_kv_read(cache.c, batch.c, k.data_ptr(), v.data_ptr(),
+                            _status(status), _stream(stream))
+    if rc:
+        _check(rc)
     return k, v
 
 
@@ -702,17 +708,29 @@ def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
     qp, qs = _token_rows(q, batch.tokens, Hq, D, "q")
     if out is None:
         out = _new((batch.tokens, Hq, D), torch.bfloat16, q.device, stream)
-    _check_out(out, batch.tokens * Hq * D, "out")
+        op = out.data_ptr()
+    else:
+        _check_out(out, batch.tokens * Hq * D, "out")
+        op = _ptr(out)
     if workspace is None:
         n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
         workspace = _new(max(n, 16), torch.uint8, q.device, stream)
     wp, wn = _ws(workspace)
-    _check(load().gwa_sdpa_paged(
+    rc = load().gwa_sdpa_paged(
         qp, qs, Hq, cache.c, batch.c,
-        1.0 / float(D) ** 0.5 if scale is None else float(scale),
-        int(bool(causal)), _ptr(out), wp, wn, _status(status),
-        _stream(stream)))
+        1.0 / float(D) ** 0.5 if scale is None else scale,
+        1 if causal else 0, op, wp, wn, _status(status), _stream(stream))
+    if rc:
+        _check(rc)
     return out
+
+
+def _row_values(t: Optional[torch.Tensor], name: str, dtype, rows: int):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != rows:
+        raise ValueError(f"{name} must be {dtype} [{rows}]")
+    return _ptr(t)
 
 
 def sample(logits: torch.Tensor, u: torch.Tensor,
@@ -731,21 +749,20 @@ def sample(logits: torch.Tensor, u: torch.Tensor,
         raise ValueError("logits must live on a CUDA device")
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("logits: only the rows may be strided")
-    for name, t, dtype in (("u", u, torch.float32),
-                           ("temperature", temperature, torch.float32),
-                           ("top_k", top_k, torch.int32),
-                           ("top_p", top_p, torch.float32),
-                           ("min_p", min_p, torch.float32)):
-        if t is not None and (t.dtype != dtype or t.numel() != R):
-            raise ValueError(f"{name} must be {dtype} [{R}]")
+    up = _row_values(u, "u", torch.float32, R)
+    tp = _row_values(temperature, "temperature", torch.float32, R)
+    kp = _row_values(top_k, "top_k", torch.int32, R)
+    pp = _row_values(top_p, "top_p", torch.float32, R)
+    mp = _row_values(min_p, "min_p", torch.float32, R)
     token = _new(R, torch.int32, logits.device, stream)
     prob = _new(R, torch.float32, logits.device, stream)
-    _check(load().gwa_sample(
+    rc = load().gwa_sample(
         logits.data_ptr(),
         GWA_BF16 if logits.dtype == torch.bfloat16 else GWA_FP32, R, V,
-        logits.stride(0) if R > 1 else V, _ptr(u), _ptr(temperature),
-        _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(prob),
-        _stream(stream)))
+        logits.stride(0) if R > 1 else V, up, tp, kp, pp, mp,
+        token.data_ptr(), prob.data_ptr(), _stream(stream))
+    if rc:
+        _check(rc)
     return token, prob
 
 
