@@ -51,7 +51,7 @@ constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 2048;
 constexpr int kSmList = 2048;  // tokens that one CTA ranks
 constexpr int kSmMaxCluster = 16;
-constexpr int64_t kSmSliceBytes = 160 * 1024;
+constexpr int64_t kSmSliceBytes = 152 * 1024;
 
 using u64 = unsigned long long;
 
@@ -98,14 +98,11 @@ struct SmKey<false> {
 
 // Shared memory besides the slice.
 struct SmShared {
-    union {
-        struct {
-            uint32_t cnt[kSmBins], lo[kSmBins], hi[kSmBins];  // this CTA's histogram
-            uint32_t all_cnt[kSmBins];                        // the cluster's
-            u64 all_mass[kSmBins];
-        };
-        u64 list[kSmList];  // gathered tokens (in rank 0), see list_key
-    };
+    uint32_t cnt[kSmBins], lo[kSmBins], hi[kSmBins];  // this CTA's histogram
+    uint32_t all_cnt[kSmBins];                        // the cluster's
+    u64 all_mass[kSmBins];
+    // gathered tokens (in rank 0), see list_key; partial sums of join
+    u64 list[kSmList];
     u64 x_mass[kSmMaxCluster];      // one value from every CTA
     float x_top[kSmMaxCluster], x_low[kSmMaxCluster];
     uint32_t x_word[kSmMaxCluster];
@@ -114,10 +111,11 @@ struct SmShared {
     float w_top[kSmWarps], w_low[kSmWarps];
     uint32_t list_n;                // gathered so far (in rank 0)
     // what a search settled on
-    uint32_t f_bin, f_count, f_above_cnt;
+    uint32_t f_bin, f_above_cnt;
     u64 f_above_mass;
     float cut_x;
     uint32_t cut_idx;
+    u64 cut_mass;                   // of the tokens kept by a count
 };
 
 template <typename T>
@@ -171,6 +169,14 @@ struct Sampler {
         const float x = __uint_as_float(BF16 ? (uint32_t)raw[e] << 16 : (uint32_t)raw[e]);
         return x == x ? x : -INFINITY;
     }
+    // The logits of chunk j (whatever lies outside the slice included).
+    __device__ __forceinline__ void load(int j, float (&x)[PER]) const {
+        const uint4 c = *reinterpret_cast<const uint4 *>(raw + j * PER);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            x[i] = BF16 ? (i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2])) : __uint_as_float(w[i % 4]);
+    }
     // Ascending in the order of the tokens: logit downwards, then index.
     static __device__ __forceinline__ u64 list_key(float x, uint32_t idx) {
         return ((u64)~SmKey<false>::make(__float_as_uint(x)) << 32) | idx;
@@ -194,9 +200,9 @@ struct Sampler {
         return t;
     }
 
-    __device__ __forceinline__ void add(uint32_t bin, uint32_t c, u64 w, bool mass) {
-        atomicAdd(&sh.cnt[bin], c);
-        if (mass && w) {
+    __device__ __forceinline__ void add(uint32_t bin, bool count, u64 w) {
+        if (count) atomicAdd(&sh.cnt[bin], 1u);
+        if (w) {
             // 64-bit sum from two 32-bit words: the carry shows in the old one
             const uint32_t wl = (uint32_t)w;
             const uint32_t old = atomicAdd(&sh.lo[bin], wl);
@@ -208,37 +214,61 @@ struct Sampler {
         for (int i = threadIdx.x; i < bins; i += kSmThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
         __syncthreads();
     }
-    // Adds the CTAs' histograms up, a share of the bins each (a lane per bin
-    // and CTA), and hands the sums to all.
+    // Adds the CTAs' histograms up, a share of the bins each, and hands the
+    // sums to all.  A warp reads, and writes, consecutive bins of one CTA;
+    // groups of threads take different CTAs.
     __device__ void join(int bins) {
-        cluster_sync_all();
-        const int share = bins / cl;
-        for (int i = threadIdx.x; i < share * cl; i += kSmThreads) {  // whole warps: bins >= 256
-            const int bin = rank * share + i / cl, r = i % cl;
-            uint32_t c = *cluster_ptr(&sh.cnt[bin], r);
-            u64 m = (u64)*cluster_ptr(&sh.lo[bin], r) + ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
-            for (int o = 1; o < cl; o <<= 1) {
-                c += __shfl_xor_sync(0xffffffffu, c, o);
-                m += __shfl_xor_sync(0xffffffffu, m, o);
+        const int tid = threadIdx.x;
+        if (cl == 1) {
+            __syncthreads();
+            for (int b = tid; b < bins; b += kSmThreads) {
+                sh.all_cnt[b] = sh.cnt[b];
+                sh.all_mass[b] = (u64)sh.lo[b] + ((u64)sh.hi[b] << 32);
             }
-            *cluster_ptr(&sh.all_cnt[bin], r) = c;
-            *cluster_ptr(&sh.all_mass[bin], r) = m;
+            __syncthreads();
+            return;
+        }
+        cluster_sync_all();
+        const int share = bins / cl, groups = min(cl, kSmThreads / share);
+        const int b = tid % share, g = tid / share, bin = rank * share + b;
+        uint32_t *const pc = reinterpret_cast<uint32_t *>(sh.list + kSmThreads);  // after the masses
+        uint32_t c = 0;
+        u64 m = 0;
+        if (g < groups) {
+            for (int r = g; r < cl; r += groups) {
+                c += *cluster_ptr(&sh.cnt[bin], r);
+                m += (u64)*cluster_ptr(&sh.lo[bin], r) + ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
+            }
+            pc[tid] = c;
+            sh.list[tid] = m;
+        }
+        __syncthreads();
+        if (g < groups) {
+            c = 0;
+            m = 0;
+            for (int k = 0; k < groups; ++k) {
+                c += pc[k * share + b];
+                m += sh.list[k * share + b];
+            }
+            for (int r = g; r < cl; r += groups) {
+                *cluster_ptr(&sh.all_cnt[bin], r) = c;
+                *cluster_ptr(&sh.all_mass[bin], r) = m;
+            }
         }
         cluster_sync_all();
     }
     // The bin where the count, or the mass, first reaches `goal`, walking the
-    // bins upwards (or DOWN from the last); `goal` of 0 with share >= 0 is
+    // bins upwards (or down from the last); `goal` of 0 with share >= 0 is
     // that share of the total (at least 1).  Returns the goal; f_* are set.
-    template <bool DOWN>
-    __device__ u64 locate(int bins, bool mass, u64 goal, float share) {
+    __device__ u64 locate(int bins, bool down, bool mass, u64 goal, float share) {
         const int per = (bins + kSmThreads - 1) / kSmThreads;
         u64 sum = 0;
         uint32_t cn = 0;
         for (int j = 0; j < per; ++j) {
             const int b = threadIdx.x * per + j;
             if (b < bins) {
-                sum += sh.all_mass[DOWN ? bins - 1 - b : b];
-                cn += sh.all_cnt[DOWN ? bins - 1 - b : b];
+                sum += sh.all_mass[down ? bins - 1 - b : b];
+                cn += sh.all_cnt[down ? bins - 1 - b : b];
             }
         }
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
@@ -272,14 +302,13 @@ struct Sampler {
             if (goal < 1) goal = 1;
         }
         for (int j = 0; j < per; ++j) {
-            const int k = threadIdx.x * per + j, b = DOWN ? bins - 1 - k : k;
+            const int k = threadIdx.x * per + j, b = down ? bins - 1 - k : k;
             if (k >= bins) break;
             const u64 m = sh.all_mass[b];
             const uint32_t c = sh.all_cnt[b];
             const u64 at = mass ? bm : bc, v = mass ? m : c;
             if (at < goal && goal <= at + v) {
                 sh.f_bin = b;
-                sh.f_count = c;
                 sh.f_above_mass = bm;
                 sh.f_above_cnt = bc;
             }
@@ -292,30 +321,44 @@ struct Sampler {
 
     // ---- the cut among the tokens of histogram step `bin` that lie above
     // (x, idx): their first `want` (by count), or as many as reach `want`
-    // (by mass).  Leaves the last kept token in cut_x, cut_idx.
-    __device__ void refine(int bin, uint32_t count, bool mass, u64 want, bool cut, float cut_x,
-                           uint32_t cut_idx) {
+    // (by mass).  Leaves the last kept token in cut_x, cut_idx, and for a
+    // count the mass of the kept in cut_mass.
+    __device__ void refine(int bin, bool mass, u64 want, bool cut, float cut_x, uint32_t cut_idx) {
         auto in = [&](float x, uint32_t idx) {
             return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
         };
-        if (count <= kSmList) {
-            // gathered in rank 0, in any order
-            if (threadIdx.x == 0) sh.list_n = 0;
-            cluster_sync_all();  // (also: the histogram is read, the list may overwrite it)
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        // gathered in rank 0, in any order
+        if (threadIdx.x == 0) sh.list_n = 0;
+        if (cl > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
+        {
             uint32_t *const n = cluster_ptr(&sh.list_n, 0);
             u64 *const list = cluster_ptr(sh.list, 0);
-            const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-            for (int e0 = first & ~31; e0 < last; e0 += kSmThreads) {
-                const int e = e0 + threadIdx.x;
-                const bool ok = e >= first && e < last && in(value(e), (uint32_t)(base + e));
-                const unsigned m = __ballot_sync(0xffffffffu, ok);
-                if (!m) continue;
-                uint32_t at = 0;
-                if (lane == 0) at = atomicAdd(n, (uint32_t)__popc(m));
-                at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
-                if (ok && at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
+            // most tokens fail by y alone (a step wider on both sides)
+            const float y_hi = steps > 0.f && bin > 0 ? (float)(1 - bin) / steps : INFINITY;
+            const float y_lo = steps > 0.f && bin < kSmBins - 1 ? -(float)(bin + 2) / steps : -INFINITY;
+            for (int j = threadIdx.x; j < (last + PER - 1) / PER; j += kSmThreads) {
+                float x[PER];
+                load(j, x);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const float y = row.expo(x[i]);
+                    if (y > y_hi || y < y_lo) continue;
+                    const int e = j * PER + i;
+                    if (e < first || e >= last || !in(value(e), (uint32_t)(base + e))) continue;
+                    const uint32_t at = atomicAdd(n, 1u);
+                    if (at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
+                }
             }
+        }
+        if (cl > 1)
             cluster_sync_all();
+        else
+            __syncthreads();
+        if (*cluster_ptr(&sh.list_n, 0) <= kSmList) {
             if (rank == 0) {
                 // in order, by a bitonic sort, and counted up
                 const int total = min((int)sh.list_n, kSmList);
@@ -355,6 +398,21 @@ struct Sampler {
                 __syncthreads();
                 u64 before = incl - sum;
                 for (int w = 0; w < warp; ++w) before += sh.t_mass[w];
+                if (!mass) {
+                    u64 kept = 0;
+#pragma unroll
+                    for (int j = 0; j < PT; ++j)
+                        if (threadIdx.x * PT + j < min((u64)total, want)) kept += row.mass(x[j]);
+                    kept = warp_sum64(kept);
+                    __syncthreads();
+                    if (lane == 0) sh.t_mass[warp] = kept;
+                    __syncthreads();
+                    if (threadIdx.x < cl) {
+                        kept = 0;
+                        for (int w = 0; w < kSmWarps; ++w) kept += sh.t_mass[w];
+                        *cluster_ptr(&sh.cut_mass, threadIdx.x) = kept;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < PT; ++j) {
                     if (before < want && want <= before + own[j])
@@ -365,7 +423,10 @@ struct Sampler {
                     before += own[j];
                 }
             }
-            cluster_sync_all();
+            if (cl > 1)
+                cluster_sync_all();
+            else
+                __syncthreads();
             return;
         }
         // too many: digit by digit on integer keys
@@ -374,17 +435,17 @@ struct Sampler {
         u64 above = 0;
         for (int pass = 0; pass < K::PASSES; ++pass) {
             const int sft = K::shift(pass), wid = K::width(pass), bins = 1 << wid;
-            if (pass == 0) cluster_sync_all();  // the histogram is read
+            if (pass == 0) save();
             clear(bins);
             for (int e = first + threadIdx.x; e < last; e += kSmThreads) {
                 const float x = value(e);
                 if (!in(x, (uint32_t)(base + e))) continue;
                 const uint32_t k = K::make(raw[e]);
                 if (done && (k >> (K::BITS - done)) != prefix) continue;
-                add((k >> sft) & (bins - 1), 1u, mass ? row.mass(x) : 0, mass);
+                add((k >> sft) & (bins - 1), !mass, mass ? row.mass(x) : 0);
             }
             join(bins);
-            locate<true>(bins, mass, want - above, -1.f);
+            locate(bins, true, mass, want - above, -1.f);
             prefix = (prefix << wid) | sh.f_bin;
             above += mass ? sh.f_above_mass : sh.f_above_cnt;
             done += wid;
@@ -395,7 +456,6 @@ struct Sampler {
         const u64 left = want - above;
         const u64 own = mass ? row.mass(x) : 1;
         const u64 nth = (left + own - 1) / own;  // 1-based
-        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
         const int run = ((last - first + kSmWarps - 1) / kSmWarps + 31) & ~31;
         const int a = first + warp * run, b = min(last, a + run);
         uint32_t c = 0;
@@ -425,6 +485,46 @@ struct Sampler {
                 at += __popc(m);
             }
         cluster_sync_all();
+        if (!mass) {
+            // the mass of the kept
+            const float cx = sh.cut_x;
+            const uint32_t ci = sh.cut_idx;
+            u64 kept = 0;
+            for (int e = first + threadIdx.x; e < last; e += kSmThreads) {
+                const float v = value(e);
+                if ((v > cx || (v == cx && (uint32_t)(base + e) <= ci)) && in(v, (uint32_t)(base + e)))
+                    kept += row.mass(v);
+            }
+            kept = warp_sum64(kept);
+            if (lane == 0) sh.w_mass[warp] = kept;
+            __syncthreads();
+            kept = 0;
+            for (int w = 0; w < kSmWarps; ++w) kept += sh.w_mass[w];
+            kept = cluster_total(kept, before);
+            if (threadIdx.x == 0) sh.cut_mass = kept;
+        }
+        restore();
+    }
+    // The steps' sums, over a search by digits on the same arrays: a few a
+    // thread.
+    u64 kept_m[kSmBins / kSmThreads];
+    uint32_t kept_c[kSmBins / kSmThreads];
+    __device__ void save() {
+#pragma unroll
+        for (int i = 0; i < kSmBins / kSmThreads; ++i) {
+            kept_m[i] = sh.all_mass[threadIdx.x + i * kSmThreads];
+            kept_c[i] = sh.all_cnt[threadIdx.x + i * kSmThreads];
+        }
+        cluster_sync_all();
+    }
+    __device__ void restore() {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSmBins / kSmThreads; ++i) {
+            sh.all_mass[threadIdx.x + i * kSmThreads] = kept_m[i];
+            sh.all_cnt[threadIdx.x + i * kSmThreads] = kept_c[i];
+        }
+        __syncthreads();
     }
 };
 
@@ -442,6 +542,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     const int64_t r = blockIdx.x / cl;
     if (tid == 0) pdl_launch_dependents();
     pdl_wait_primary();
+
+    // (waited for before the first word goes to another CTA: all of the
+    // cluster run by then)
+    if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 
     // ---- this CTA's slice; chunks start on 16 bytes of the input, so the
     // slice starts at element `mis` of its first chunk
@@ -497,16 +601,17 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         top = fmaxf(top, sh.w_top[w]);
         low = fminf(low, sh.w_low[w]);
     }
-    // every CTA of the cluster runs: its shared memory may be written
-    cluster_sync_all();
-    if (tid < cl) {
-        *cluster_ptr(&sh.x_top[rank], tid) = top;
-        *cluster_ptr(&sh.x_low[rank], tid) = low;
-    }
-    cluster_sync_all();
-    for (int c = 0; c < cl; ++c) {
-        top = fmaxf(top, sh.x_top[c]);
-        low = fminf(low, sh.x_low[c]);
+    if (cl > 1) {
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        if (tid < cl) {
+            *cluster_ptr(&sh.x_top[rank], tid) = top;
+            *cluster_ptr(&sh.x_low[rank], tid) = low;
+        }
+        cluster_sync_all();
+        for (int c = 0; c < cl; ++c) {
+            top = fmaxf(top, sh.x_top[c]);
+            low = fminf(low, sh.x_low[c]);
+        }
     }
     if (top == -INFINITY) {  // nothing to draw (the whole cluster leaves)
         if (rank == 0 && tid == 0) {
@@ -534,88 +639,44 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         const float range = fminf(41.f, low < top ? -s.row.expo(low) : 0.f);
         s.steps = range > 0.f ? fminf((float)kSmBins / range, 1e30f) : 0.f;
         s.clear(kSmBins);
-        // (the mass only where top-p needs it)
         for (int j = tid; j < chunks; j += kSmThreads) {
-            const uint4 c = *reinterpret_cast<const uint4 *>(slice + j * PER);
-            const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+            float x[PER];
+            s.load(j, x);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int e = j * PER + i;
                 if (e < mis || e >= mis + len) continue;
-                const float x = BF16 ? (i & 1 ? bf16_hi(cw[i / 2]) : bf16_lo(cw[i / 2]))
-                                     : __uint_as_float(cw[i % 4]);
-                const float y = s.row.expo(x);
-                const float t = fminf(-y * s.steps, (float)(kSmBins - 1));
-                const int bin = x == -INFINITY ? kSmBins - 1 : (int)t;
-                s.add(bin, 1u, by_p && x != -INFINITY ? SmRow::mass_of(y) : 0, by_p);
+                const float y = s.row.expo(x[i]);
+                // (-inf, and NaN, in the last step; counts only for top-k,
+                // masses only for top-p)
+                const int bin = x[i] == -INFINITY ? kSmBins - 1
+                                                  : (int)fminf(-y * s.steps, (float)(kSmBins - 1));
+                s.add(bin, by_k, by_p && x[i] != -INFINITY ? SmRow::mass_of(y) : 0);
             }
         }
         s.join(kSmBins);
-        int bin_k = kSmBins;
         if (by_k) {
-            s.template locate<false>(kSmBins, false, (u64)kq, -1.f);
-            bin_k = sh.f_bin;
-            const uint32_t n = sh.f_count, above = sh.f_above_cnt;
+            s.locate(kSmBins, false, false, (u64)kq, -1.f);
+            const int bin = sh.f_bin;
+            const u64 want = (u64)kq - sh.f_above_cnt;
             __syncthreads();
-            // the steps' own sums stay with a thread each while the list (on
-            // the same memory) is in use
-            u64 keep_m[kSmBins / kSmThreads];
-            uint32_t keep_c[kSmBins / kSmThreads];
-#pragma unroll
-            for (int i = 0; i < kSmBins / kSmThreads; ++i) {
-                keep_m[i] = sh.all_mass[tid + i * kSmThreads];
-                keep_c[i] = sh.all_cnt[tid + i * kSmThreads];
-            }
-            s.refine(bin_k, n, false, (u64)kq - above, false, 0.f, 0);
+            s.refine(bin, false, want, false, 0.f, 0);
             cut = true;
             cut_x = sh.cut_x;
             cut_idx = sh.cut_idx;
-            __syncthreads();
             if (by_p) {
                 // what top-p goes by: the steps above, and of this one the kept
-                u64 m = 0;
-                uint32_t c = 0;
-                for (int e = mis + tid; e < mis + len; e += kSmThreads) {
-                    const float x = s.value(e);
-                    if (!(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) continue;
-                    if (s.bin_of(x) != bin_k) continue;
-                    m += s.row.mass(x);
-                    ++c;
-                }
-                m = warp_sum64(m);
-                c = __reduce_add_sync(FULL, c);
-                if (lane == 0) {
-                    sh.w_mass[warp] = m;
-                    sh.w_word[warp] = c;
-                }
-                __syncthreads();
-                m = 0;
-                c = 0;
-                for (int w = 0; w < kSmWarps; ++w) {
-                    m += sh.w_mass[w];
-                    c += sh.w_word[w];
-                }
-                u64 before;
-                if (tid < cl) *cluster_ptr(&sh.x_word[rank], tid) = c;
-                m = s.cluster_total(m, before);
-                c = 0;
-                for (int w = 0; w < cl; ++w) c += sh.x_word[w];
-#pragma unroll
-                for (int i = 0; i < kSmBins / kSmThreads; ++i) {
-                    const int b = tid + i * kSmThreads;
-                    sh.all_mass[b] = b < bin_k ? keep_m[i] : b == bin_k ? m : 0;
-                    sh.all_cnt[b] = b < bin_k ? keep_c[i] : b == bin_k ? c : 0;
-                }
+                for (int i = tid; i < kSmBins; i += kSmThreads)
+                    if (i >= bin) sh.all_mass[i] = i == bin ? sh.cut_mass : 0;
                 __syncthreads();
             }
         }
         if (by_p) {
-            const u64 goal = s.template locate<false>(kSmBins, true, 0, fmaxf(tp, 0.f));
+            const u64 goal = s.locate(kSmBins, false, true, 0, fmaxf(tp, 0.f));
             const int bin = sh.f_bin;
-            const uint32_t n = sh.f_count;
             const u64 above = sh.f_above_mass;
             __syncthreads();
-            s.refine(bin, n, true, goal - above, cut, cut_x, cut_idx);
+            s.refine(bin, true, goal - above, cut, cut_x, cut_idx);
             cut = true;
             cut_x = sh.cut_x;
             cut_idx = sh.cut_idx;
@@ -627,16 +688,22 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     // index order
     const int run = (((len + mis) + kSmWarps - 1) / kSmWarps + 31) & ~31;
     const int a = warp * run, b = min(mis + len, a + run);
-    auto kept = [&](int e) -> u64 {
+    auto kept_of = [&](int e, float x) -> u64 {
+        if (cut && x < cut_x) return 0;
         if (e < mis || e >= b) return 0;
-        const float x = s.value(e);
         if (greedy) return x == top ? 1 : 0;
         if (cut && !(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) return 0;
         const u64 w = s.row.mass(x);
         return w >= least ? w : 0;
     };
+    auto kept = [&](int e) { return e < b ? kept_of(e, s.value(e)) : 0; };
     u64 mine = 0;
-    for (int e0 = a; e0 < b; e0 += 32) mine += kept(e0 + lane);
+    for (int j = a / PER + lane; j * PER < b; j += 32) {
+        float x[PER];
+        s.load(j, x);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mine += kept_of(j * PER + i, x[i]);
+    }
     mine = warp_sum64(mine);
     __syncthreads();
     if (lane == 0) sh.w_mass[warp] = mine;
