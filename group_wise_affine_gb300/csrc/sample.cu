@@ -50,6 +50,7 @@ constexpr int kSmThreads = 1024;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 2048;
 constexpr int kSmList = 2048;  // tokens that one CTA ranks
+constexpr int kSmShort = kSmThreads / 2;  // top-k of up to this: see the kernel
 constexpr int kSmMaxCluster = 16;
 constexpr int64_t kSmSliceBytes = 152 * 1024;
 
@@ -214,10 +215,23 @@ struct Sampler {
         for (int i = threadIdx.x; i < bins; i += kSmThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
         __syncthreads();
     }
+    // y of the tokens of a step, a step wider on either side.
+    __device__ __forceinline__ float y_above(int bin) const {
+        return steps > 0.f && bin > 0 ? (float)(1 - bin) / steps : INFINITY;
+    }
+    __device__ __forceinline__ float y_below(int bin) const {
+        return steps > 0.f && bin < kSmBins - 1 ? -(float)(bin + 2) / steps : -INFINITY;
+    }
+    __device__ __forceinline__ void sync_all() {
+        if (cl > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
+    }
     // Adds the CTAs' histograms up, a share of the bins each, and hands the
-    // sums to all.  A warp reads, and writes, consecutive bins of one CTA;
+    // sums to all (masses: or the counts only).  A warp reads, and writes, consecutive bins of one CTA;
     // groups of threads take different CTAs.
-    __device__ void join(int bins) {
+    __device__ void join(int bins, bool masses) {
         const int tid = threadIdx.x;
         if (cl == 1) {
             __syncthreads();
@@ -237,7 +251,8 @@ struct Sampler {
         if (g < groups) {
             for (int r = g; r < cl; r += groups) {
                 c += *cluster_ptr(&sh.cnt[bin], r);
-                m += (u64)*cluster_ptr(&sh.lo[bin], r) + ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
+                if (masses)
+                    m += (u64)*cluster_ptr(&sh.lo[bin], r) + ((u64)*cluster_ptr(&sh.hi[bin], r) << 32);
             }
             pc[tid] = c;
             sh.list[tid] = m;
@@ -252,7 +267,7 @@ struct Sampler {
             }
             for (int r = g; r < cl; r += groups) {
                 *cluster_ptr(&sh.all_cnt[bin], r) = c;
-                *cluster_ptr(&sh.all_mass[bin], r) = m;
+                if (masses) *cluster_ptr(&sh.all_mass[bin], r) = m;
             }
         }
         cluster_sync_all();
@@ -298,8 +313,7 @@ struct Sampler {
             total += sh.t_mass[w];
         }
         if (share >= 0.f) {
-            goal = (u64)((double)total * (double)share);
-            if (goal < 1) goal = 1;
+            goal = share_of(total, share);
         }
         for (int j = 0; j < per; ++j) {
             const int k = threadIdx.x * per + j, b = down ? bins - 1 - k : k;
@@ -319,6 +333,126 @@ struct Sampler {
         return goal;
     }
 
+    // Gathers, in rank 0 and in any order, the tokens that pass in(x, token);
+    // those whose y lies outside [y_lo, y_hi] are known not to.  Returns how
+    // many there are; the list holds the first kSmList that arrived.
+    template <class In>
+    __device__ uint32_t gather(float y_lo, float y_hi, In in) {
+        if (threadIdx.x == 0) sh.list_n = 0;
+        sync_all();
+        uint32_t *const n = cluster_ptr(&sh.list_n, 0);
+        u64 *const list = cluster_ptr(sh.list, 0);
+        for (int j = threadIdx.x; j < (last + PER - 1) / PER; j += kSmThreads) {
+            float x[PER];
+            load(j, x);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const float y = row.expo(x[i]);
+                if (y > y_hi || y < y_lo) continue;
+                const int e = j * PER + i;
+                if (e < first || e >= last || !in(value(e), (uint32_t)(base + e))) continue;
+                const uint32_t at = atomicAdd(n, 1u);
+                if (at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
+            }
+        }
+        sync_all();
+        return *n;
+    }
+    // Sorts the list's first `total` words upwards (this CTA's; bitonic).
+    __device__ void sort(int total) {
+        int size = 2;
+        while (size < total) size *= 2;
+        for (int i = total + threadIdx.x; i < size; i += kSmThreads) sh.list[i] = ~0ull;
+        __syncthreads();
+        for (int k = 2; k <= size; k *= 2)
+            for (int d = k / 2; d > 0; d /= 2) {
+                for (int i = threadIdx.x; i < size / 2; i += kSmThreads) {
+                    const int a = 2 * i - (i & (d - 1)), b = a + d;
+                    const u64 x = sh.list[a], y = sh.list[b];
+                    if ((x > y) == ((a & k) == 0)) {
+                        sh.list[a] = y;
+                        sh.list[b] = x;
+                    }
+                }
+                __syncthreads();
+            }
+    }
+    // The lower threads' sum of v in this CTA, and all threads'.
+    __device__ u64 scan(u64 v, u64 &total) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+        u64 incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 w = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += w;
+        }
+        __syncthreads();
+        if (lane == 31) sh.t_mass[warp] = incl;
+        __syncthreads();
+        u64 before = incl - v;
+        total = 0;
+        for (int w = 0; w < kSmWarps; ++w) {
+            if (w < warp) before += sh.t_mass[w];
+            total += sh.t_mass[w];
+        }
+        return before;
+    }
+    static constexpr int PT = kSmList / kSmThreads;  // list words of a thread, side by side
+
+    // ---- a whole draw from a sorted list that holds the row's first tokens
+    // (this CTA's): its first n, of those as many as reach the share tp
+    // (by_p), of those the masses of at least `least`
+    __device__ void draw(int n, bool by_p, float tp, u64 least, float u, int32_t *token, float *prob) {
+        u64 own[PT], sum = 0, total;
+        uint32_t idx[PT];
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const int i = threadIdx.x * PT + j;
+            own[j] = i < n ? row.mass(SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32))) : 0;
+            idx[j] = i < n ? (uint32_t)sh.list[i] : 0u;
+            sum += own[j];
+        }
+        u64 before = scan(sum, total);
+        const u64 goal = by_p ? share_of(total, tp) : ~0ull;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const int i = threadIdx.x * PT + j;
+            const bool keep = before < goal && own[j] >= least;
+            before += own[j];
+            // by token from here on: 19 bits of it, 41 of mass
+            if (i < n) sh.list[i] = ((u64)idx[j] << 41) | (keep ? own[j] : 0);
+        }
+        sort(n);
+        sum = 0;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const int i = threadIdx.x * PT + j;
+            const u64 w = i < n ? sh.list[i] : 0;
+            own[j] = w & ((1ull << 41) - 1);
+            idx[j] = (uint32_t)(w >> 41);
+            sum += own[j];
+        }
+        before = scan(sum, total);
+        const u64 at = drawn_at(u, total);
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            if (before <= at && at < before + own[j]) {
+                *token = (int32_t)idx[j];
+                if (prob) *prob = (float)((double)own[j] / (double)total);
+            }
+            before += own[j];
+        }
+    }
+    // What top-p has to reach, and where a random number falls.
+    static __device__ __forceinline__ u64 share_of(u64 total, float tp) {
+        const u64 goal = (u64)((double)total * (double)fmaxf(tp, 0.f));
+        return goal < 1 ? 1 : goal;
+    }
+    static __device__ __forceinline__ u64 drawn_at(float u, u64 total) {
+        const u64 at = (u64)((double)fmaxf(u, 0.f) * (double)total);
+        return at > total - 1 ? total - 1 : at;
+    }
+
     // ---- the cut among the tokens of histogram step `bin` that lie above
     // (x, idx): their first `want` (by count), or as many as reach `want`
     // (by mass).  Leaves the last kept token in cut_x, cut_idx, and for a
@@ -328,91 +462,22 @@ struct Sampler {
             return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
         };
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-        // gathered in rank 0, in any order
-        if (threadIdx.x == 0) sh.list_n = 0;
-        if (cl > 1)
-            cluster_sync_all();
-        else
-            __syncthreads();
-        {
-            uint32_t *const n = cluster_ptr(&sh.list_n, 0);
-            u64 *const list = cluster_ptr(sh.list, 0);
-            // most tokens fail by y alone (a step wider on both sides)
-            const float y_hi = steps > 0.f && bin > 0 ? (float)(1 - bin) / steps : INFINITY;
-            const float y_lo = steps > 0.f && bin < kSmBins - 1 ? -(float)(bin + 2) / steps : -INFINITY;
-            for (int j = threadIdx.x; j < (last + PER - 1) / PER; j += kSmThreads) {
-                float x[PER];
-                load(j, x);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const float y = row.expo(x[i]);
-                    if (y > y_hi || y < y_lo) continue;
-                    const int e = j * PER + i;
-                    if (e < first || e >= last || !in(value(e), (uint32_t)(base + e))) continue;
-                    const uint32_t at = atomicAdd(n, 1u);
-                    if (at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
-                }
-            }
-        }
-        if (cl > 1)
-            cluster_sync_all();
-        else
-            __syncthreads();
-        if (*cluster_ptr(&sh.list_n, 0) <= kSmList) {
+        if (gather(y_below(bin), y_above(bin), in) <= kSmList) {
             if (rank == 0) {
-                // in order, by a bitonic sort, and counted up
-                const int total = min((int)sh.list_n, kSmList);
-                int size = 2;
-                while (size < total) size *= 2;
-                for (int i = total + threadIdx.x; i < size; i += kSmThreads) sh.list[i] = ~0ull;
-                __syncthreads();
-                for (int k = 2; k <= size; k *= 2)
-                    for (int d = k / 2; d > 0; d /= 2) {
-                        for (int i = threadIdx.x; i < size / 2; i += kSmThreads) {
-                            const int a = 2 * i - (i & (d - 1)), b = a + d;
-                            const u64 x = sh.list[a], y = sh.list[b];
-                            if ((x > y) == ((a & k) == 0)) {
-                                sh.list[a] = y;
-                                sh.list[b] = x;
-                            }
-                        }
-                        __syncthreads();
-                    }
-                constexpr int PT = kSmList / kSmThreads;
-                u64 own[PT], sum = 0;
+                // in order, and counted up
+                const int n = (int)sh.list_n;
+                sort(n);
+                u64 own[PT], sum = 0, kept = 0, total;
                 float x[PT];
 #pragma unroll
                 for (int j = 0; j < PT; ++j) {
                     const int i = threadIdx.x * PT + j;
-                    x[j] = i < total ? SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32)) : 0.f;
-                    own[j] = i >= total ? 0 : mass ? row.mass(x[j]) : 1;
+                    x[j] = i < n ? SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32)) : 0.f;
+                    own[j] = i >= n ? 0 : mass ? row.mass(x[j]) : 1;
                     sum += own[j];
+                    if (!mass && i < min((u64)n, want)) kept += row.mass(x[j]);
                 }
-                u64 incl = sum;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 v = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += v;
-                }
-                if (lane == 31) sh.t_mass[warp] = incl;
-                __syncthreads();
-                u64 before = incl - sum;
-                for (int w = 0; w < warp; ++w) before += sh.t_mass[w];
-                if (!mass) {
-                    u64 kept = 0;
-#pragma unroll
-                    for (int j = 0; j < PT; ++j)
-                        if (threadIdx.x * PT + j < min((u64)total, want)) kept += row.mass(x[j]);
-                    kept = warp_sum64(kept);
-                    __syncthreads();
-                    if (lane == 0) sh.t_mass[warp] = kept;
-                    __syncthreads();
-                    if (threadIdx.x < cl) {
-                        kept = 0;
-                        for (int w = 0; w < kSmWarps; ++w) kept += sh.t_mass[w];
-                        *cluster_ptr(&sh.cut_mass, threadIdx.x) = kept;
-                    }
-                }
+                u64 before = scan(sum, total);
 #pragma unroll
                 for (int j = 0; j < PT; ++j) {
                     if (before < want && want <= before + own[j])
@@ -422,11 +487,12 @@ struct Sampler {
                         }
                     before += own[j];
                 }
+                if (!mass) {
+                    scan(kept, total);
+                    if (threadIdx.x < cl) *cluster_ptr(&sh.cut_mass, threadIdx.x) = total;
+                }
             }
-            if (cl > 1)
-                cluster_sync_all();
-            else
-                __syncthreads();
+            sync_all();
             return;
         }
         // too many: digit by digit on integer keys
@@ -444,7 +510,7 @@ struct Sampler {
                 if (done && (k >> (K::BITS - done)) != prefix) continue;
                 add((k >> sft) & (bins - 1), !mass, mass ? row.mass(x) : 0);
             }
-            join(bins);
+            join(bins, mass);
             locate(bins, true, mass, want - above, -1.f);
             prefix = (prefix << wid) | sh.f_bin;
             above += mass ? sh.f_above_mass : sh.f_above_cnt;
@@ -561,32 +627,38 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         top = fmaxf(top, x);
         low = fminf(low, x == -INFINITY ? INFINITY : x);
     };
-    for (int j = tid; j < chunks; j += kSmThreads) {
-        const int e0 = j * PER - mis;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (e0 >= 0 && e0 + PER <= len) {
-            u = *reinterpret_cast<const uint4 *>(src + e0);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    auto whole = [&](int j) { return j * PER >= mis && (j + 1) * PER - mis <= len; };
+    for (int j0 = tid; j0 < chunks; j0 += 4 * kSmThreads) {
+        uint4 c[4];  // four loads in flight
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (BF16) {
-                    see((Raw)(w[i] & 0xffffu));
-                    see((Raw)(w[i] >> 16));
-                } else {
-                    see(w[i]);
+        for (int k = 0; k < 4; ++k)
+            if (const int j = j0 + k * kSmThreads; whole(j))
+                c[k] = *reinterpret_cast<const uint4 *>(src + (j * PER - mis));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int j = j0 + k * kSmThreads;
+            if (whole(j)) {
+                const uint32_t w[4] = {c[k].x, c[k].y, c[k].z, c[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (BF16) {
+                        see((Raw)(w[i] & 0xffffu));
+                        see((Raw)(w[i] >> 16));
+                    } else {
+                        see(w[i]);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(slice + j * PER) = c[k];
+            } else if (j < chunks) {  // an end of the slice
+                for (int e = max(j * PER, mis); e < min((j + 1) * PER, mis + len); ++e) {
+                    const Raw v = src[e - mis];
+                    see(v);
+                    slice[e] = v;
                 }
             }
-            *reinterpret_cast<uint4 *>(slice + j * PER) = u;
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (e0 + i >= 0 && e0 + i < len) {
-                    const Raw v = src[e0 + i];
-                    see(v);
-                    slice[j * PER + i] = v;
-                }
         }
     }
+    const float mine_top = top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
@@ -630,14 +702,60 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     S s{sh, slice, mis, mis + len, lo - mis, cl, rank, {top, 0.f}, 0.f};
     s.row.per = __fmul_rn(__fdiv_rn(1.f, T), 1.4426950408889634f);
 
+    if (greedy) {
+        // the first of the largest
+        if (tid == 0) sh.list_n = 0xffffffffu;
+        s.sync_all();
+        for (int j = tid; j < chunks; j += kSmThreads) {
+            float x[PER];
+            s.load(j, x);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int e = j * PER + i;
+                if (x[i] == top && e >= mis && e < mis + len)
+                    atomicMin(cluster_ptr(&sh.list_n, 0), (uint32_t)(s.base + e));
+            }
+        }
+        s.sync_all();
+        if (rank == 0 && tid == 0) {
+            p.token[r] = (int32_t)sh.list_n;
+            if (p.prob) p.prob[r] = 1.f;
+        }
+        return;
+    }
+    const u64 least = mp > 0.f ? __float2ull_rz(fminf(mp, 1.f) * 1099511627776.f) : 0;
+
     // ---- the cut: kept are logits above cut_x, and its equals up to cut_idx
     bool cut = false;
     float cut_x = 0.f;
     uint32_t cut_idx = 0;
-    const bool by_k = !greedy && kq > 0 && kq < p.V, by_p = !greedy && tp < 1.f;
+    const bool by_k = kq > 0 && kq < p.V, by_p = tp < 1.f;
     if (by_k || by_p) {
         const float range = fminf(41.f, low < top ? -s.row.expo(low) : 0.f);
         s.steps = range > 0.f ? fminf((float)kSmBins / range, 1e30f) : 0.f;
+    }
+    if (by_k && kq <= kSmShort) {
+        s.clear(kSmBins);
+        if (tid == 0) sh.f_bin = kSmBins - 1;
+        if (mine_top > -INFINITY) s.add(s.bin_of(mine_top), true, 0);
+        s.join(kSmBins, false);
+        s.locate(kSmBins, false, false, (u64)kq, -1.f);
+        const int bin = sh.f_bin;
+        const uint32_t n = s.gather(s.y_below(bin), INFINITY, [&](float x, uint32_t) {
+            return x > -INFINITY && s.bin_of(x) <= bin;
+        });
+        if (n <= kSmList) {
+            // (rank 0 stays until all have read its counter)
+            if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+            if (rank == 0) {
+                s.sort((int)n);
+                s.draw(min((int)n, kq), by_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
+            }
+            if (cl > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            return;
+        }
+    }
+    if (by_k || by_p) {
         s.clear(kSmBins);
         for (int j = tid; j < chunks; j += kSmThreads) {
             float x[PER];
@@ -654,7 +772,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
                 s.add(bin, by_k, by_p && x[i] != -INFINITY ? SmRow::mass_of(y) : 0);
             }
         }
-        s.join(kSmBins);
+        s.join(kSmBins, by_p);
         if (by_k) {
             s.locate(kSmBins, false, false, (u64)kq, -1.f);
             const int bin = sh.f_bin;
@@ -682,8 +800,6 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             cut_idx = sh.cut_idx;
         }
     }
-    const u64 least = !greedy && mp > 0.f
-                          ? __float2ull_rz(fminf(mp, 1.f) * 1099511627776.f) : 0;
     // ---- the kept masses: a warp takes a run of whole 32-token steps, in
     // index order
     const int run = (((len + mis) + kSmWarps - 1) / kSmWarps + 31) & ~31;
@@ -691,7 +807,6 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     auto kept_of = [&](int e, float x) -> u64 {
         if (cut && x < cut_x) return 0;
         if (e < mis || e >= b) return 0;
-        if (greedy) return x == top ? 1 : 0;
         if (cut && !(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) return 0;
         const u64 w = s.row.mass(x);
         return w >= least ? w : 0;
@@ -715,9 +830,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     }
     cluster_sync_all();  // x_mass may still be read
     const u64 all = s.cluster_total(cta, cta_before);
-    // the first token whose running mass passes u * all (greedy: the first)
-    u64 goal = greedy ? 0 : (u64)((double)fmaxf(u, 0.f) * (double)all);
-    if (goal > all - 1) goal = all - 1;
+    // the first token whose running mass passes u * all 
+    const u64 goal = S::drawn_at(u, all);
     const u64 start = cta_before + warp_before;
     if (goal >= start && goal < start + mine) {
         u64 at = start;
@@ -737,7 +851,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             const unsigned past = __ballot_sync(FULL, at + incl > goal);
             if (lane == __ffs(past) - 1) {
                 p.token[r] = (int32_t)(s.base + e0 + lane);
-                if (p.prob) p.prob[r] = greedy ? 1.f : (float)((double)w / (double)all);
+                if (p.prob) p.prob[r] = (float)((double)w / (double)all);
             }
             break;
         }
