@@ -201,6 +201,19 @@ struct Sampler {
         return t;
     }
 
+    // The cluster's sum of a value from every thread.
+    __device__ u64 sum_all(u64 v) {
+        v = warp_sum64(v);
+        if ((threadIdx.x & 31) == 0) sh.w_mass[threadIdx.x / 32] = v;
+        sync_all();  // (x_mass is read, too)
+        v = 0;
+        for (int w = 0; w < kSmWarps; ++w) v += sh.w_mass[w];
+        u64 before;
+        v = cluster_total(v, before);
+        __syncthreads();
+        return v;
+    }
+
     __device__ __forceinline__ void add(uint32_t bin, bool count, u64 w) {
         if (count) atomicAdd(&sh.cnt[bin], 1u);
         if (w) {
@@ -400,9 +413,9 @@ struct Sampler {
     static constexpr int PT = kSmList / kSmThreads;  // list words of a thread, side by side
 
     // ---- a whole draw from a sorted list that holds the row's first tokens
-    // (this CTA's): its first n, of those as many as reach the share tp
-    // (by_p), of those the masses of at least `least`
-    __device__ void draw(int n, bool by_p, float tp, u64 least, float u, int32_t *token, float *prob) {
+    // (this CTA's): its first n, of those as many as reach `goal` (0: the
+    // share tp of the n), of those the masses of at least `least`
+    __device__ void draw(int n, u64 goal, float tp, u64 least, float u, int32_t *token, float *prob) {
         u64 own[PT], sum = 0, total;
         uint32_t idx[PT];
 #pragma unroll
@@ -413,7 +426,7 @@ struct Sampler {
             sum += own[j];
         }
         u64 before = scan(sum, total);
-        const u64 goal = by_p ? share_of(total, tp) : ~0ull;
+        if (goal == 0) goal = tp < 1.f ? share_of(total, tp) : ~0ull;
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
             const int i = threadIdx.x * PT + j;
@@ -749,7 +762,44 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
             if (rank == 0) {
                 s.sort((int)n);
-                s.draw(min((int)n, kq), by_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
+                s.draw(min((int)n, kq), 0, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
+            }
+            if (cl > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            return;
+        }
+    }
+    u64 goal_p = 0, prune = 0;
+    if (!by_k && (by_p || least > 0)) {
+        u64 total = 0;
+        for (int j = tid; j < chunks; j += kSmThreads) {
+            float x[PER];
+            s.load(j, x);
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (const int e = j * PER + i; e >= mis && e < mis + len) total += s.row.mass(x[i]);
+        }
+        total = s.sum_all(total);
+        if (by_p) {
+            goal_p = S::share_of(total, tp);
+            prune = (total - goal_p) / (u64)p.V;
+        }
+        const u64 thr = max(least, prune + 1);
+        // (y of thr to within the margin)
+        const float y_thr = __log2f((float)thr) - 40.01f;
+        int n = 0;
+        for (int j = tid; j < chunks; j += kSmThreads) {
+            float x[PER];
+            s.load(j, x);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) n += s.row.expo(x[i]) >= y_thr;
+        }
+        if (s.sum_all((u64)n) <= kSmList) {
+            n = (int)s.gather(y_thr, INFINITY, [&](float x, uint32_t) { return s.row.mass(x) >= thr; });
+            // (rank 0 stays until all have read its counter)
+            if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+            if (rank == 0) {
+                s.sort(n);
+                s.draw(n, goal_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
             }
             if (cl > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             return;
@@ -767,9 +817,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
                 const float y = s.row.expo(x[i]);
                 // (-inf, and NaN, in the last step; counts only for top-k,
                 // masses only for top-p)
+                const u64 w = by_p && x[i] != -INFINITY ? SmRow::mass_of(y) : 0;
+                if (!by_k && w <= prune) continue;
                 const int bin = x[i] == -INFINITY ? kSmBins - 1
                                                   : (int)fminf(-y * s.steps, (float)(kSmBins - 1));
-                s.add(bin, by_k, by_p && x[i] != -INFINITY ? SmRow::mass_of(y) : 0);
+                s.add(bin, by_k, w);
             }
         }
         s.join(kSmBins, by_p);
@@ -790,7 +842,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             }
         }
         if (by_p) {
-            const u64 goal = s.locate(kSmBins, false, true, 0, fmaxf(tp, 0.f));
+            const u64 goal = s.locate(kSmBins, false, true, goal_p, by_k ? fmaxf(tp, 0.f) : -1.f);
             const int bin = sh.f_bin;
             const u64 above = sh.f_above_mass;
             __syncthreads();

@@ -56,7 +56,7 @@ def allowed(x, u, T, k, p, mp):
     if mp > 0:
         lo = int((ws >= min(mp, 1.0) * (1 + EPS)).sum())
         hi = int((ws >= min(mp, 1.0) * (1 - EPS)).sum())
-        lens = {max(1, min(m, c)) for m in lens for c in (lo, hi)}
+        lens = {max(1, min(m, c)) for m in lens for c in range(lo, hi + 1)}
     out = []
     for m in lens:
         keep = np.sort(order[:m])
@@ -141,6 +141,35 @@ def test_the_token_does_not_depend_on_the_split():
             t1, p1 = gwa.sample(x, u[:1], **one)
             t2, p2 = gwa.sample(x.expand(many, -1).contiguous(), u, **a)
             assert (t2 == t1).all() and (p2 == p1).all()
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("V", [9001, 40011, 200001])
+def test_rows_that_keep_many_tokens(V, bf16):
+    # nearly flat rows, whose kept tokens no short list holds: each filter,
+    # from few tokens to nearly all, few rows (wide clusters) and many
+    rng = np.random.default_rng(V + bf16)
+    for n in (2, 160):
+        x = rng.standard_normal((n, V)).astype(np.float32) * 0.4
+        off = lambda a, z: np.where(rng.random(n) < 0.4, z, a)
+        run(x, rng.random(n), T=rng.uniform(0.5, 1.5, n),
+            k=off(rng.integers(400, V, n), 0), p=off(rng.uniform(0.05, 0.999, n), 1.0),
+            mp=off(rng.uniform(0.0, 0.5, n), 0.0), bf16=bf16)
+        if n * V > 2e6:
+            break
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_many_equal_logits_around_the_cut(bf16):
+    # a few values only: thousands of equals at the cut of a small top-k
+    rng = np.random.default_rng(11)
+    x = np.round(rng.standard_normal((24, 30011)) * 1.5).astype(np.float32)
+    x = np.minimum(x, 2)
+    k = np.resize([1, 2, 60, 512, 513, 2500], 24)
+    run(x, rng.random(24), T=rng.uniform(0.5, 1.5, 24), k=k, bf16=bf16)
+    run(x, rng.random(24), T=rng.uniform(0.5, 1.5, 24), k=k, p=rng.uniform(0.1, 0.99, 24),
+        mp=rng.uniform(0, 0.3, 24), bf16=bf16)
+    run(x, rng.random(24), p=rng.uniform(0.01, 0.99, 24), mp=rng.uniform(0, 1, 24), bf16=bf16)
 
 
 def test_ties_go_to_the_lowest_index():
