@@ -116,6 +116,7 @@ struct SmShared {
     u64 f_above_mass;
     float cut_x;
     uint32_t cut_idx;
+    u64 one;
     u64 cut_mass;                   // of the tokens kept by a count
 };
 
@@ -129,23 +130,43 @@ __device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
 // A row's weights.
 struct SmRow {
     float top, per;
-    // base-2 exponent of a logit's mass relative to the largest's: <= 0, NaN
-    // for a NaN logit
+    // base-2 exponent of a logit's mass relative to the largest's: <= 0; for
+    // a NaN NaN, for -inf -inf or (infinite T) NaN
     __device__ __forceinline__ float expo(float x) const {
         return x == top ? 0.f : __fmul_rn(__fsub_rn(x, top), per);
     }
-    // floor(2^40 exp2f(y)).  From -44 to 0 exp2f gives ex2's value (checked
-    // for every float there); below -40 the mass is zero.
+    // floor(2^40 exp2f(y)): the 24-bit significand shifted by the exponent.
+    // From -44 to 0 exp2f gives ex2's value (checked for every float there);
+    // below -40 the shifts leave zero, and so they do for a NaN, whose counts
+    // all lie past 31.
     static __device__ __forceinline__ u64 mass_of(float y) {
-        if (!(y >= -41.f)) return 0;
-        const uint32_t b = __float_as_uint(ex2(y));  // 2^-41 .. 1
-        return ((u64)((b & 0x7fffffu) | 0x800000u) << 17) >> (127 - (b >> 23));
+        const uint32_t b = __float_as_uint(ex2(y)), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
+        return ((u64)shr(m, 142u - e) << 32) | (shl(m, e - 110u) | shr(m, 110u - e));
     }
-    __device__ __forceinline__ u64 mass(float x) const {
-        return x == -INFINITY ? 0 : mass_of(expo(x));
+    __device__ __forceinline__ u64 mass(float x) const { return mass_of(expo(x)); }
+    // (zero past 31)
+    static __device__ __forceinline__ uint32_t shl(uint32_t v, uint32_t n) {
+        uint32_t r;
+        asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+        return r;
+    }
+    static __device__ __forceinline__ uint32_t shr(uint32_t v, uint32_t n) {
+        uint32_t r;
+        asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
+        return r;
     }
 };
 
+// Of a warp's 32 lanes: the sums up to and with one's own.
+template <typename T>
+__device__ __forceinline__ T warp_scan(T v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T w = __shfl_up_sync(0xffffffffu, v, o);
+        if ((int)(threadIdx.x & 31) >= o) v += w;
+    }
+    return v;
+}
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -170,7 +191,7 @@ struct Sampler {
         const float x = __uint_as_float(BF16 ? (uint32_t)raw[e] << 16 : (uint32_t)raw[e]);
         return x == x ? x : -INFINITY;
     }
-    // The logits of chunk j (whatever lies outside the slice included).
+    // The logits of chunk j (-inf outside the slice).
     __device__ __forceinline__ void load(int j, float (&x)[PER]) const {
         const uint4 c = *reinterpret_cast<const uint4 *>(raw + j * PER);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -206,10 +227,8 @@ struct Sampler {
         v = warp_sum64(v);
         if ((threadIdx.x & 31) == 0) sh.w_mass[threadIdx.x / 32] = v;
         sync_all();  // (x_mass is read, too)
-        v = 0;
-        for (int w = 0; w < kSmWarps; ++w) v += sh.w_mass[w];
         u64 before;
-        v = cluster_total(v, before);
+        v = cluster_total(warp_sum64(sh.w_mass[threadIdx.x & 31]), before);
         __syncthreads();
         return v;
     }
@@ -228,12 +247,12 @@ struct Sampler {
         for (int i = threadIdx.x; i < bins; i += kSmThreads) sh.cnt[i] = sh.lo[i] = sh.hi[i] = 0;
         __syncthreads();
     }
-    // y of the tokens of a step, a step wider on either side.
-    __device__ __forceinline__ float y_above(int bin) const {
-        return steps > 0.f && bin > 0 ? (float)(1 - bin) / steps : INFINITY;
+    // The logits of a step, a step wider on either side.
+    __device__ __forceinline__ float x_high(int bin) const {
+        return steps > 0.f && bin > 1 ? x_above((float)(1 - bin) / steps) : INFINITY;
     }
-    __device__ __forceinline__ float y_below(int bin) const {
-        return steps > 0.f && bin < kSmBins - 1 ? -(float)(bin + 2) / steps : -INFINITY;
+    __device__ __forceinline__ float x_low(int bin) const {
+        return steps > 0.f && bin < kSmBins - 1 ? x_below(-(float)(bin + 2) / steps) : -INFINITY;
     }
     __device__ __forceinline__ void sync_all() {
         if (cl > 1)
@@ -300,34 +319,18 @@ struct Sampler {
             }
         }
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-        u64 im = sum;
-        uint32_t ic = cn;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 v = __shfl_up_sync(0xffffffffu, im, o);
-            const uint32_t c = __shfl_up_sync(0xffffffffu, ic, o);
-            if (lane >= o) {
-                im += v;
-                ic += c;
-            }
-        }
+        const u64 im = warp_scan(sum);
+        const uint32_t ic = warp_scan(cn);
         if (lane == 31) {
             sh.t_mass[warp] = im;
             sh.t_cnt[warp] = ic;
         }
         __syncthreads();
-        u64 bm = im - sum, total = 0;
-        uint32_t bc = ic - cn;
-        for (int w = 0; w < kSmWarps; ++w) {
-            if (w < warp) {
-                bm += sh.t_mass[w];
-                bc += sh.t_cnt[w];
-            }
-            total += sh.t_mass[w];
-        }
-        if (share >= 0.f) {
-            goal = share_of(total, share);
-        }
+        const u64 wm = warp_scan(sh.t_mass[lane]);
+        const uint32_t wc = warp_scan(sh.t_cnt[lane]);
+        u64 bm = im - sum + __shfl_sync(0xffffffffu, wm, max(warp - 1, 0)) * (warp > 0);
+        uint32_t bc = ic - cn + __shfl_sync(0xffffffffu, wc, max(warp - 1, 0)) * (warp > 0);
+        if (share >= 0.f) goal = share_goal(__shfl_sync(0xffffffffu, wm, 31), share);
         for (int j = 0; j < per; ++j) {
             const int k = threadIdx.x * per + j, b = down ? bins - 1 - k : k;
             if (k >= bins) break;
@@ -347,10 +350,10 @@ struct Sampler {
     }
 
     // Gathers, in rank 0 and in any order, the tokens that pass in(x, token);
-    // those whose y lies outside [y_lo, y_hi] are known not to.  Returns how
-    // many there are; the list holds the first kSmList that arrived.
+    // those outside [x_lo, x_hi] are known not to.  Returns how many there
+    // are; the list holds the first kSmList that arrived.
     template <class In>
-    __device__ uint32_t gather(float y_lo, float y_hi, In in) {
+    __device__ uint32_t gather(float x_lo, float x_hi, In in) {
         if (threadIdx.x == 0) sh.list_n = 0;
         sync_all();
         uint32_t *const n = cluster_ptr(&sh.list_n, 0);
@@ -358,20 +361,32 @@ struct Sampler {
         for (int j = threadIdx.x; j < (last + PER - 1) / PER; j += kSmThreads) {
             float x[PER];
             load(j, x);
+            bool any = false;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const float y = row.expo(x[i]);
-                if (y > y_hi || y < y_lo) continue;
-                const int e = j * PER + i;
-                if (e < first || e >= last || !in(value(e), (uint32_t)(base + e))) continue;
+            for (int i = 0; i < PER; ++i) any |= !(x[i] < x_lo) && !(x[i] > x_hi);
+            if (!any) continue;
+            for (int e = max(j * PER, first); e < min((j + 1) * PER, last); ++e) {
+                const float v = value(e);
+                if (v < x_lo || v > x_hi || !in(v, (uint32_t)(base + e))) continue;
                 const uint32_t at = atomicAdd(n, 1u);
-                if (at < kSmList) list[at] = list_key(value(e), (uint32_t)(base + e));
+                if (at < kSmList) list[at] = list_key(v, (uint32_t)(base + e));
             }
         }
         sync_all();
         return *n;
     }
-    // Sorts the list's first `total` words upwards (this CTA's; bitonic).
+    // The logit whose exponent is y, or a little below (above) it.
+    __device__ __forceinline__ float x_below(float y) const {
+        const float x = __fadd_rd(row.top, __fdiv_rd(y, row.per));
+        return x == x ? x : -INFINITY;
+    }
+    __device__ __forceinline__ float x_above(float y) const {
+        const float x = __fadd_ru(row.top, __fdiv_ru(y, row.per));
+        return x == x ? x : INFINITY;
+    }
+    // Sorts the list's first `total` words upwards (this CTA's; bitonic).  A
+    // warp's 32 pairs at a distance of up to 32 are 64 neighbouring words, so
+    // those steps wait for the warp only.
     __device__ void sort(int total) {
         int size = 2;
         while (size < total) size *= 2;
@@ -387,28 +402,23 @@ struct Sampler {
                         sh.list[b] = x;
                     }
                 }
-                __syncthreads();
+                if (d > 32 || (d == 1 && k >= 64))
+                    __syncthreads();
+                else
+                    __syncwarp();
             }
+        if (size < 64) __syncthreads();
     }
     // The lower threads' sum of v in this CTA, and all threads'.
     __device__ u64 scan(u64 v, u64 &total) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-        u64 incl = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const u64 w = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += w;
-        }
+        const u64 incl = warp_scan(v);
         __syncthreads();
         if (lane == 31) sh.t_mass[warp] = incl;
         __syncthreads();
-        u64 before = incl - v;
-        total = 0;
-        for (int w = 0; w < kSmWarps; ++w) {
-            if (w < warp) before += sh.t_mass[w];
-            total += sh.t_mass[w];
-        }
-        return before;
+        const u64 wm = warp_scan(sh.t_mass[lane]);
+        total = __shfl_sync(0xffffffffu, wm, 31);
+        return incl - v + __shfl_sync(0xffffffffu, wm, max(warp - 1, 0)) * (warp > 0);
     }
     static constexpr int PT = kSmList / kSmThreads;  // list words of a thread, side by side
 
@@ -426,7 +436,7 @@ struct Sampler {
             sum += own[j];
         }
         u64 before = scan(sum, total);
-        if (goal == 0) goal = tp < 1.f ? share_of(total, tp) : ~0ull;
+        if (goal == 0) goal = tp < 1.f ? share_goal(total, tp) : ~0ull;
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
             const int i = threadIdx.x * PT + j;
@@ -456,14 +466,28 @@ struct Sampler {
             before += own[j];
         }
     }
-    // What top-p has to reach, and where a random number falls.
-    static __device__ __forceinline__ u64 share_of(u64 total, float tp) {
-        const u64 goal = (u64)((double)total * (double)fmaxf(tp, 0.f));
-        return goal < 1 ? 1 : goal;
+    // What top-p has to reach, and where a random number falls: the same
+    // value for all of the CTA's threads, worked out by one (of 64-bit
+    // floating point an SM does a few operations a cycle).
+    __device__ u64 share_goal(u64 total, float tp) {
+        if (threadIdx.x == 0) {
+            const u64 goal = (u64)((double)total * (double)fmaxf(tp, 0.f));
+            sh.one = goal < 1 ? 1 : goal;
+        }
+        return one();
     }
-    static __device__ __forceinline__ u64 drawn_at(float u, u64 total) {
-        const u64 at = (u64)((double)fmaxf(u, 0.f) * (double)total);
-        return at > total - 1 ? total - 1 : at;
+    __device__ u64 drawn_at(float u, u64 total) {
+        if (threadIdx.x == 0) {
+            const u64 at = (u64)((double)fmaxf(u, 0.f) * (double)total);
+            sh.one = at > total - 1 ? total - 1 : at;
+        }
+        return one();
+    }
+    __device__ u64 one() {
+        __syncthreads();
+        const u64 v = sh.one;
+        __syncthreads();
+        return v;
     }
 
     // ---- the cut among the tokens of histogram step `bin` that lie above
@@ -475,7 +499,7 @@ struct Sampler {
             return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
         };
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-        if (gather(y_below(bin), y_above(bin), in) <= kSmList) {
+        if (gather(x_low(bin), x_high(bin), in) <= kSmList) {
             if (rank == 0) {
                 // in order, and counted up
                 const int n = (int)sh.list_n;
@@ -662,9 +686,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
                     }
                 }
                 *reinterpret_cast<uint4 *>(slice + j * PER) = c[k];
-            } else if (j < chunks) {  // an end of the slice
-                for (int e = max(j * PER, mis); e < min((j + 1) * PER, mis + len); ++e) {
-                    const Raw v = src[e - mis];
+            } else if (j < chunks) {  // an end of the slice; -inf outside it
+                for (int e = j * PER; e < (j + 1) * PER; ++e) {
+                    const Raw v = e >= mis && e < mis + len ? src[e - mis]
+                                                            : (Raw)(BF16 ? 0xff80u : 0xff800000u);
                     see(v);
                     slice[e] = v;
                 }
@@ -682,9 +707,12 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         sh.w_low[warp] = low;
     }
     __syncthreads();
-    for (int w = 0; w < kSmWarps; ++w) {
-        top = fmaxf(top, sh.w_top[w]);
-        low = fminf(low, sh.w_low[w]);
+    top = sh.w_top[lane];
+    low = sh.w_low[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(FULL, top, o));
+        low = fminf(low, __shfl_xor_sync(FULL, low, o));
     }
     if (cl > 1) {
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -724,9 +752,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             s.load(j, x);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int e = j * PER + i;
-                if (x[i] == top && e >= mis && e < mis + len)
-                    atomicMin(cluster_ptr(&sh.list_n, 0), (uint32_t)(s.base + e));
+                if (x[i] == top)
+                    atomicMin(cluster_ptr(&sh.list_n, 0), (uint32_t)(s.base + j * PER + i));
             }
         }
         s.sync_all();
@@ -754,7 +781,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         s.join(kSmBins, false);
         s.locate(kSmBins, false, false, (u64)kq, -1.f);
         const int bin = sh.f_bin;
-        const uint32_t n = s.gather(s.y_below(bin), INFINITY, [&](float x, uint32_t) {
+        const uint32_t n = s.gather(s.x_low(bin), INFINITY, [&](float x, uint32_t) {
             return x > -INFINITY && s.bin_of(x) <= bin;
         });
         if (n <= kSmList) {
@@ -776,25 +803,26 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             s.load(j, x);
 #pragma unroll
             for (int i = 0; i < PER; ++i)
-                if (const int e = j * PER + i; e >= mis && e < mis + len) total += s.row.mass(x[i]);
+                total += s.row.mass(x[i]);
         }
         total = s.sum_all(total);
         if (by_p) {
-            goal_p = S::share_of(total, tp);
+            goal_p = s.share_goal(total, tp);
             prune = (total - goal_p) / (u64)p.V;
         }
         const u64 thr = max(least, prune + 1);
-        // (y of thr to within the margin)
-        const float y_thr = __log2f((float)thr) - 40.01f;
+        // (its logit, 0.01 of y below: the rounding of log2, of the exponent and
+        // of the way back)
+        const float x_thr = s.x_below(__log2f((float)thr) - 40.01f);
         int n = 0;
         for (int j = tid; j < chunks; j += kSmThreads) {
             float x[PER];
             s.load(j, x);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) n += s.row.expo(x[i]) >= y_thr;
+            for (int i = 0; i < PER; ++i) n += x[i] >= x_thr;
         }
         if (s.sum_all((u64)n) <= kSmList) {
-            n = (int)s.gather(y_thr, INFINITY, [&](float x, uint32_t) { return s.row.mass(x) >= thr; });
+            n = (int)s.gather(x_thr, INFINITY, [&](float x, uint32_t) { return s.row.mass(x) >= thr; });
             // (rank 0 stays until all have read its counter)
             if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
             if (rank == 0) {
@@ -817,7 +845,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
                 const float y = s.row.expo(x[i]);
                 // (-inf, and NaN, in the last step; counts only for top-k,
                 // masses only for top-p)
-                const u64 w = by_p && x[i] != -INFINITY ? SmRow::mass_of(y) : 0;
+                const u64 w = by_p ? SmRow::mass_of(y) : 0;
                 if (!by_k && w <= prune) continue;
                 const int bin = x[i] == -INFINITY ? kSmBins - 1
                                                   : (int)fminf(-y * s.steps, (float)(kSmBins - 1));
@@ -857,13 +885,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     const int run = (((len + mis) + kSmWarps - 1) / kSmWarps + 31) & ~31;
     const int a = warp * run, b = min(mis + len, a + run);
     auto kept_of = [&](int e, float x) -> u64 {
-        if (cut && x < cut_x) return 0;
-        if (e < mis || e >= b) return 0;
         if (cut && !(x > cut_x || (x == cut_x && (uint32_t)(s.base + e) <= cut_idx))) return 0;
         const u64 w = s.row.mass(x);
         return w >= least ? w : 0;
     };
-    auto kept = [&](int e) { return e < b ? kept_of(e, s.value(e)) : 0; };
+    auto kept = [&](int e) { return e >= mis && e < b ? kept_of(e, s.value(e)) : 0; };
     u64 mine = 0;
     for (int j = a / PER + lane; j * PER < b; j += 32) {
         float x[PER];
@@ -875,15 +901,13 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     __syncthreads();
     if (lane == 0) sh.w_mass[warp] = mine;
     __syncthreads();
-    u64 cta = 0, warp_before = 0, cta_before;
-    for (int w = 0; w < kSmWarps; ++w) {
-        if (w < warp) warp_before += sh.w_mass[w];
-        cta += sh.w_mass[w];
-    }
+    const u64 wm = warp_scan(sh.w_mass[lane]), cta = __shfl_sync(FULL, wm, 31);
+    const u64 warp_before = __shfl_sync(FULL, wm, max(warp - 1, 0)) * (warp > 0);
+    u64 cta_before;
     cluster_sync_all();  // x_mass may still be read
     const u64 all = s.cluster_total(cta, cta_before);
     // the first token whose running mass passes u * all 
-    const u64 goal = S::drawn_at(u, all);
+    const u64 goal = s.drawn_at(u, all);
     const u64 start = cta_before + warp_before;
     if (goal >= start && goal < start + mine) {
         u64 at = start;
