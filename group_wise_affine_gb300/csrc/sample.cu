@@ -143,6 +143,8 @@ struct SmRow {
         const uint32_t b = __float_as_uint(ex2(y)), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
         return ((u64)shr(m, 142u - e) << 32) | (shl(m, e - 110u) | shr(m, 110u - e));
     }
+    // exp2f(y), and for a NaN zero: the mass times 2^-40, before its floor.
+    static __device__ __forceinline__ float part_of(float y) { return fmaxf(ex2(y), 0.f); }
     __device__ __forceinline__ u64 mass(float x) const { return mass_of(expo(x)); }
     // (zero past 31)
     static __device__ __forceinline__ uint32_t shl(uint32_t v, uint32_t n) {
@@ -167,6 +169,24 @@ __device__ __forceinline__ T warp_scan(T v) {
     }
     return v;
 }
+// A sum of masses, each from its part t = exp2f(y), without a shift: 8 + t
+// rounded towards zero holds the mass's upper 21 bits at the end of its
+// significand, 2^-17 plus what is left of t its lower 20.  The words are
+// added as they are and the constants taken off at the end; up to 2048 masses
+// a thread (of 2^19 tokens on 1024 threads at most 512).
+struct MassSum {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float t) {
+        const float s = __fadd_rz(t, 8.f);
+        hi += __float_as_uint(s);
+        lo += __float_as_uint(__fadd_rz(__fsub_rn(t, __fsub_rn(s, 8.f)), 0x1p-17f));
+    }
+    __device__ __forceinline__ u64 total(uint32_t count) const {
+        return ((u64)(hi - count * __float_as_uint(8.f)) << 20) +
+               (u64)(uint32_t)(lo - count * __float_as_uint(0x1p-17f));
+    }
+};
+
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -351,29 +371,45 @@ struct Sampler {
 
     // Gathers, in rank 0 and in any order, the tokens that pass in(x, token);
     // those outside [x_lo, x_hi] are known not to.  Returns how many there
-    // are; the list holds the first kSmList that arrived.
+    // are; the list holds the first kSmList of them.  Every CTA fills its own
+    // list (an atomic on another CTA's counter takes most of a microsecond),
+    // which then goes to rank 0 behind the lower ranks'.
     template <class In>
     __device__ uint32_t gather(float x_lo, float x_hi, In in) {
         if (threadIdx.x == 0) sh.list_n = 0;
-        sync_all();
-        uint32_t *const n = cluster_ptr(&sh.list_n, 0);
-        u64 *const list = cluster_ptr(sh.list, 0);
+        __syncthreads();
         for (int j = threadIdx.x; j < (last + PER - 1) / PER; j += kSmThreads) {
             float x[PER];
             load(j, x);
-            bool any = false;
+            uint32_t hits = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) any |= !(x[i] < x_lo) && !(x[i] > x_hi);
-            if (!any) continue;
-            for (int e = max(j * PER, first); e < min((j + 1) * PER, last); ++e) {
+            for (int i = 0; i < PER; ++i)
+                if (!(x[i] < x_lo) && !(x[i] > x_hi)) hits |= 1u << i;
+            for (; hits; hits &= hits - 1) {
+                const int e = j * PER + __ffs(hits) - 1;
                 const float v = value(e);
-                if (v < x_lo || v > x_hi || !in(v, (uint32_t)(base + e))) continue;
-                const uint32_t at = atomicAdd(n, 1u);
-                if (at < kSmList) list[at] = list_key(v, (uint32_t)(base + e));
+                if (e < first || e >= last || !in(v, (uint32_t)(base + e))) continue;
+                const uint32_t at = atomicAdd(&sh.list_n, 1u);
+                if (at < kSmList) sh.list[at] = list_key(v, (uint32_t)(base + e));
             }
         }
-        sync_all();
-        return *n;
+        __syncthreads();
+        const uint32_t own = sh.list_n;
+        if (cl == 1) return own;
+        if (threadIdx.x < cl) *cluster_ptr(&sh.x_word[rank], threadIdx.x) = own;
+        cluster_sync_all();
+        uint32_t before = 0, n = 0;
+        for (int r = 0; r < cl; ++r) {
+            if (r < rank) before += sh.x_word[r];
+            n += sh.x_word[r];
+        }
+        if (rank > 0) {
+            u64 *const list = cluster_ptr(sh.list, 0);
+            for (uint32_t i = threadIdx.x; i < own && before + i < kSmList; i += kSmThreads)
+                list[before + i] = sh.list[i];
+        }
+        cluster_sync_all();
+        return n;
     }
     // The logit whose exponent is y, or a little below (above) it.
     __device__ __forceinline__ float x_below(float y) const {
@@ -384,30 +420,31 @@ struct Sampler {
         const float x = __fadd_ru(row.top, __fdiv_ru(y, row.per));
         return x == x ? x : INFINITY;
     }
-    // Sorts the list's first `total` words upwards (this CTA's; bitonic).  A
+    // Sorts the list's first `total` words upwards (this CTA's; bitonic, a
+    // pair of words a thread and step, by as many warps as that takes).  A
     // warp's 32 pairs at a distance of up to 32 are 64 neighbouring words, so
     // those steps wait for the warp only.
     __device__ void sort(int total) {
-        int size = 2;
+        int size = 64;
         while (size < total) size *= 2;
         for (int i = total + threadIdx.x; i < size; i += kSmThreads) sh.list[i] = ~0ull;
         __syncthreads();
-        for (int k = 2; k <= size; k *= 2)
-            for (int d = k / 2; d > 0; d /= 2) {
-                for (int i = threadIdx.x; i < size / 2; i += kSmThreads) {
+        const int i = threadIdx.x;
+        if (i < size / 2)
+            for (int k = 2; k <= size; k *= 2)
+                for (int d = k / 2; d > 0; d /= 2) {
                     const int a = 2 * i - (i & (d - 1)), b = a + d;
                     const u64 x = sh.list[a], y = sh.list[b];
                     if ((x > y) == ((a & k) == 0)) {
                         sh.list[a] = y;
                         sh.list[b] = x;
                     }
+                    if (size > 64 && (d > 32 || (d == 1 && k >= 64)))
+                        asm volatile("bar.sync 1, %0;" ::"r"(size / 2) : "memory");
+                    else
+                        __syncwarp();
                 }
-                if (d > 32 || (d == 1 && k >= 64))
-                    __syncthreads();
-                else
-                    __syncwarp();
-            }
-        if (size < 64) __syncthreads();
+        __syncthreads();
     }
     // The lower threads' sum of v in this CTA, and all threads'.
     __device__ u64 scan(u64 v, u64 &total) {
@@ -499,11 +536,11 @@ struct Sampler {
             return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
         };
         const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-        if (gather(x_low(bin), x_high(bin), in) <= kSmList) {
+        const uint32_t n = gather(x_low(bin), x_high(bin), in);
+        if (n <= kSmList) {
             if (rank == 0) {
                 // in order, and counted up
-                const int n = (int)sh.list_n;
-                sort(n);
+                sort((int)n);
                 u64 own[PT], sum = 0, kept = 0, total;
                 float x[PT];
 #pragma unroll
@@ -512,7 +549,7 @@ struct Sampler {
                     x[j] = i < n ? SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32)) : 0.f;
                     own[j] = i >= n ? 0 : mass ? row.mass(x[j]) : 1;
                     sum += own[j];
-                    if (!mass && i < min((u64)n, want)) kept += row.mass(x[j]);
+                    if (!mass && (u64)i < min((u64)n, want)) kept += row.mass(x[j]);
                 }
                 u64 before = scan(sum, total);
 #pragma unroll
@@ -785,27 +822,25 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             return x > -INFINITY && s.bin_of(x) <= bin;
         });
         if (n <= kSmList) {
-            // (rank 0 stays until all have read its counter)
-            if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
             if (rank == 0) {
                 s.sort((int)n);
                 s.draw(min((int)n, kq), 0, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
             }
-            if (cl > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             return;
         }
     }
     u64 goal_p = 0, prune = 0;
+    float x_prune = -INFINITY;
     if (!by_k && (by_p || least > 0)) {
-        u64 total = 0;
-        for (int j = tid; j < chunks; j += kSmThreads) {
+        MassSum sum;
+        int n = 0;
+        for (int j = tid; j < chunks; j += kSmThreads, n += PER) {
             float x[PER];
             s.load(j, x);
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                total += s.row.mass(x[i]);
+            for (int i = 0; i < PER; ++i) sum.add(SmRow::part_of(s.row.expo(x[i])));
         }
-        total = s.sum_all(total);
+        const u64 total = s.sum_all(sum.total(n));
         if (by_p) {
             goal_p = s.share_goal(total, tp);
             prune = (total - goal_p) / (u64)p.V;
@@ -814,7 +849,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         // (its logit, 0.01 of y below: the rounding of log2, of the exponent and
         // of the way back)
         const float x_thr = s.x_below(__log2f((float)thr) - 40.01f);
-        int n = 0;
+        x_prune = s.x_below(__log2f((float)(prune + 1)) - 40.01f);
+        n = 0;
         for (int j = tid; j < chunks; j += kSmThreads) {
             float x[PER];
             s.load(j, x);
@@ -823,13 +859,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         }
         if (s.sum_all((u64)n) <= kSmList) {
             n = (int)s.gather(x_thr, INFINITY, [&](float x, uint32_t) { return s.row.mass(x) >= thr; });
-            // (rank 0 stays until all have read its counter)
-            if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
             if (rank == 0) {
                 s.sort(n);
                 s.draw(n, goal_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
             }
-            if (cl > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             return;
         }
     }
@@ -842,11 +875,13 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             for (int i = 0; i < PER; ++i) {
                 const int e = j * PER + i;
                 if (e < mis || e >= mis + len) continue;
+                // (counts only for top-k, masses only for top-p and above its
+                // floor)
+                if (!by_k && x[i] < x_prune) continue;
                 const float y = s.row.expo(x[i]);
-                // (-inf, and NaN, in the last step; counts only for top-k,
-                // masses only for top-p)
                 const u64 w = by_p ? SmRow::mass_of(y) : 0;
                 if (!by_k && w <= prune) continue;
+                // (-inf, and NaN, in the last step)
                 const int bin = x[i] == -INFINITY ? kSmBins - 1
                                                   : (int)fminf(-y * s.steps, (float)(kSmBins - 1));
                 s.add(bin, by_k, w);
@@ -890,13 +925,23 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         return w >= least ? w : 0;
     };
     auto kept = [&](int e) { return e >= mis && e < b ? kept_of(e, s.value(e)) : 0; };
+    // (floor(t 2^40) >= least where t >= least 2^-40, which a float holds:
+    // least comes from one)
+    const float least_t = (float)least * 0x1p-40f, floor_x = cut ? cut_x : -INFINITY;
+    MassSum sum;
+    int n = 0;
     u64 mine = 0;
-    for (int j = a / PER + lane; j * PER < b; j += 32) {
+    for (int j = a / PER + lane; j * PER < b; j += 32, n += PER) {
         float x[PER];
         s.load(j, x);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mine += kept_of(j * PER + i, x[i]);
+        for (int i = 0; i < PER; ++i) {
+            const float t = SmRow::part_of(s.row.expo(x[i]));
+            sum.add(x[i] > floor_x && t >= least_t ? t : 0.f);
+            if (cut && x[i] == cut_x) mine += kept_of(j * PER + i, x[i]);
+        }
     }
+    mine += sum.total(n);
     mine = warp_sum64(mine);
     __syncthreads();
     if (lane == 0) sh.w_mass[warp] = mine;
