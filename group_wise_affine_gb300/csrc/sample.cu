@@ -116,7 +116,6 @@ struct SmShared {
     u64 f_above_mass;
     float cut_x;
     uint32_t cut_idx;
-    u64 one;
     u64 cut_mass;                   // of the tokens kept by a count
 };
 
@@ -350,7 +349,7 @@ struct Sampler {
         const uint32_t wc = warp_scan(sh.t_cnt[lane]);
         u64 bm = im - sum + __shfl_sync(0xffffffffu, wm, max(warp - 1, 0)) * (warp > 0);
         uint32_t bc = ic - cn + __shfl_sync(0xffffffffu, wc, max(warp - 1, 0)) * (warp > 0);
-        if (share >= 0.f) goal = share_goal(__shfl_sync(0xffffffffu, wm, 31), share);
+        if (share >= 0.f) goal = share_of(__shfl_sync(0xffffffffu, wm, 31), share);
         for (int j = 0; j < per; ++j) {
             const int k = threadIdx.x * per + j, b = down ? bins - 1 - k : k;
             if (k >= bins) break;
@@ -473,7 +472,7 @@ struct Sampler {
             sum += own[j];
         }
         u64 before = scan(sum, total);
-        if (goal == 0) goal = tp < 1.f ? share_goal(total, tp) : ~0ull;
+        if (goal == 0) goal = tp < 1.f ? share_of(total, tp) : ~0ull;
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
             const int i = threadIdx.x * PT + j;
@@ -493,38 +492,36 @@ struct Sampler {
             sum += own[j];
         }
         before = scan(sum, total);
-        const u64 at = drawn_at(u, total);
+        const u64 at = drawn_at(total, u);
 #pragma unroll
         for (int j = 0; j < PT; ++j) {
             if (before <= at && at < before + own[j]) {
                 *token = (int32_t)idx[j];
-                if (prob) *prob = (float)((double)own[j] / (double)total);
+                if (prob) *prob = share(own[j], total);
             }
             before += own[j];
         }
     }
-    // What top-p has to reach, and where a random number falls: the same
-    // value for all of the CTA's threads, worked out by one (of 64-bit
-    // floating point an SM does a few operations a cycle).
-    __device__ u64 share_goal(u64 total, float tp) {
-        if (threadIdx.x == 0) {
-            const u64 goal = (u64)((double)total * (double)fmaxf(tp, 0.f));
-            sh.one = goal < 1 ? 1 : goal;
-        }
-        return one();
+    // floor(total f) for f in [0, 1): the float's significand times the total,
+    // shifted (64-bit floating point takes thousands of cycles here).
+    static __device__ __forceinline__ u64 part(u64 total, float f) {
+        const uint32_t b = __float_as_uint(fmaxf(f, 0.f));
+        const u64 m = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+        const int sh = 150 - max((int)(b >> 23), 1);  // f = m 2^-sh, sh >= 24
+        const u64 lo = total * m, hi = __umul64hi(total, m);
+        return sh < 64 ? lo >> sh | hi << (64 - sh) : sh < 128 ? hi >> (sh - 64) : 0;
     }
-    __device__ u64 drawn_at(float u, u64 total) {
-        if (threadIdx.x == 0) {
-            const u64 at = (u64)((double)fmaxf(u, 0.f) * (double)total);
-            sh.one = at > total - 1 ? total - 1 : at;
-        }
-        return one();
+    // What top-p has to reach, and where a random number falls.
+    static __device__ __forceinline__ u64 share_of(u64 total, float tp) {
+        const u64 goal = part(total, tp);
+        return goal < 1 ? 1 : goal;
     }
-    __device__ u64 one() {
-        __syncthreads();
-        const u64 v = sh.one;
-        __syncthreads();
-        return v;
+    static __device__ __forceinline__ u64 drawn_at(u64 total, float u) {
+        return u >= 1.f ? total - 1 : part(total, u);
+    }
+    // A token's share of the kept (rounded three times).
+    static __device__ __forceinline__ float share(u64 w, u64 total) {
+        return __fdiv_rn(__ull2float_rn(w), __ull2float_rn(total));
     }
 
     // ---- the cut among the tokens of histogram step `bin` that lie above
@@ -842,7 +839,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         }
         const u64 total = s.sum_all(sum.total(n));
         if (by_p) {
-            goal_p = s.share_goal(total, tp);
+            goal_p = S::share_of(total, tp);
             prune = (total - goal_p) / (u64)p.V;
         }
         const u64 thr = max(least, prune + 1);
@@ -952,7 +949,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     cluster_sync_all();  // x_mass may still be read
     const u64 all = s.cluster_total(cta, cta_before);
     // the first token whose running mass passes u * all 
-    const u64 goal = s.drawn_at(u, all);
+    const u64 goal = S::drawn_at(all, u);
     const u64 start = cta_before + warp_before;
     if (goal >= start && goal < start + mine) {
         u64 at = start;
@@ -972,7 +969,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             const unsigned past = __ballot_sync(FULL, at + incl > goal);
             if (lane == __ffs(past) - 1) {
                 p.token[r] = (int32_t)(s.base + e0 + lane);
-                if (p.prob) p.prob[r] = (float)((double)w / (double)all);
+                if (p.prob) p.prob[r] = S::share(w, all);
             }
             break;
         }
