@@ -120,10 +120,10 @@ cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st);
 // start while the previous kernel in the stream drains; the kernel itself
 // waits (griddepcontrol.wait) before touching anything that kernel wrote.
 template <typename... Args>
-cudaError_t launch_pdl(const void *kernel, unsigned grid, unsigned threads,
+cudaError_t launch_pdl(const void *kernel, dim3 grid, unsigned threads,
                        size_t smem, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;

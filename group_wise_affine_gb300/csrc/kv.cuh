@@ -17,16 +17,19 @@ constexpr unsigned kKvBadRope = 2u;  // position past the rotary table
 struct KvSeq {
     int first, count, len;
 };
-__device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int b) {
+__device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int start, int next, int len) {
     const int n = (int)kv.tokens;
-    const int a = min(max(kv.q_start[b], 0), n);
-    const int e = min(max(kv.q_start[b + 1], a), n);
+    const int a = min(max(start, 0), n);
+    const int e = min(max(next, a), n);
     const int64_t cap = (int64_t)kv.max_pages << kv.page_shift;
     KvSeq s;
     s.first = a;
     s.count = e - a;
-    s.len = (int)min((int64_t)max(kv.kv_len[b], 0), min(cap, (int64_t)0x7fffff00));
+    s.len = (int)min((int64_t)max(len, 0), min(cap, (int64_t)0x7fffff00));
     return s;
+}
+__device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int b) {
+    return kv_seq(kv, kv.q_start[b], kv.q_start[b + 1], kv.kv_len[b]);
 }
 
 // The sequence of a token and its position there (seq -1: none; a negative
@@ -36,19 +39,30 @@ struct KvToken {
     int seq, pos;
 };
 __device__ __forceinline__ KvToken kv_locate(const KvView &kv, int64_t tok, int lane) {
+    constexpr unsigned FULL = 0xffffffffu;
     int lo = 0, n = kv.batch + 1;  // the answer's entry lies in [lo, lo + n)
     KvToken r{-1, -1};
+    int start, next, len;  // of the lane's entry in the last round
     while (true) {
         const int step = (n + 31) / 32, i = lo + lane * step;
-        const bool le = lane * step < n && kv.q_start[i] <= tok;
-        const int c = __popc(__ballot_sync(0xffffffffu, le));
+        const bool in = lane * step < n;
+        start = in ? kv.q_start[i] : 0;
+        // (read along with the starts: the answer needs no further look)
+        next = in && step == 1 && i < kv.batch ? kv.q_start[i + 1] : 0;
+        len = in && step == 1 && i < kv.batch ? kv.kv_len[i] : 0;
+        const int c = __popc(__ballot_sync(FULL, in && start <= tok));
         if (c == 0) return r;
         lo += (c - 1) * step;
         n = min(step, n - (c - 1) * step);
-        if (step == 1) break;
+        if (step == 1) {
+            start = __shfl_sync(FULL, start, c - 1);
+            next = __shfl_sync(FULL, next, c - 1);
+            len = __shfl_sync(FULL, len, c - 1);
+            break;
+        }
     }
     if (lo >= kv.batch) return r;
-    const KvSeq s = kv_seq(kv, lo);
+    const KvSeq s = kv_seq(kv, start, next, len);
     const int i = (int)(tok - s.first);
     if (i < 0 || i >= s.count) return r;
     r.seq = lo;

@@ -17,12 +17,20 @@
 //
 // Bound: bytes.  A token moves (2 Hq + 2 Hkv) D 2 bytes of bf16 (q in and
 // out, k and v in) and writes 2 Hkv (D b/8 + D/16) of cache, so 8192 tokens
-// of 40 + 8 heads of 128 are 249 MB, 37 us of HBM bandwidth; one token is a
-// launch.  A lane holds eight dimensions (one 16-byte load), a head takes
-// D/8 lanes, eight lanes share a group's minimum and maximum by shuffles,
-// and the partner of a rotated pair sits rot_dim/16 lanes away.  A warp
-// keeps its lanes' cos and sin in registers over several heads of one token
-// (reading them per head would be four times the bytes of the head itself).
+// of 32 + 2 x 8 heads of 128 are 177 MB, 26 us of HBM bandwidth; one token is
+// a launch.  Measured: 46 us for those (the append alone; 3.9 TB/s), 5 us for
+// one token with its read-back.  A warp takes one token's heads in steps of 32
+// lanes x 16 dimensions (two 16-byte loads a lane, two steps in flight).
+// Queries and keys are loaded so that a lane holds both pieces of a rotated
+// pair; its cos and sin stay in registers for all the token's heads (reading
+// them per head would be four times the head's own bytes).  A rotated key
+// then goes through shared memory into the order of its groups, four lanes
+// each.  What the time above the bytes goes to is the instructions of the
+// quantization (about 350 of a step's 450); dividing lanes took it from 42 to
+// 72 us, and a lane of eight values per group, with the pairs exchanged by
+// shuffles, took 64.
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 #include "kv.cuh"
@@ -40,39 +48,51 @@ struct AppendParams {
     const float2 *rope;
     int64_t rope_rows;
     int rot;    // rotated dimensions
-    int qsteps, steps;  // a token's warp steps: queries', and all
+    int qsteps, ksteps, steps;  // a token's warp steps: queries', keys', and all
     int per;    // steps of a warp task
     int nblk;   // warp tasks per token
     int32_t *status;
 };
 
-// Eight table entries.
-__device__ __forceinline__ void load_cs(const float2 *src, float2 (&cs)[8]) {
+// A rotated pair's pieces of eight dimensions, a of the first half and b of
+// the second: a cos - b sin and b cos + a sin, each product and each sum
+// rounded once.
+__device__ __forceinline__ void kv_turn(uint4 &a, uint4 &b, const float2 (&cs)[8]) {
+    uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float4 t = reinterpret_cast<const float4 *>(src)[i];
-        cs[2 * i] = make_float2(t.x, t.y);
-        cs[2 * i + 1] = make_float2(t.z, t.w);
+        const float2 e = cs[2 * i], f = cs[2 * i + 1];
+        const float x0 = bf16_lo(x[i]), x1 = bf16_hi(x[i]);
+        const float y0 = bf16_lo(y[i]), y1 = bf16_hi(y[i]);
+        x[i] = pack_bf16(__fsub_rn(__fmul_rn(x0, e.x), __fmul_rn(y0, e.y)),
+                         __fsub_rn(__fmul_rn(x1, f.x), __fmul_rn(y1, f.y)));
+        y[i] = pack_bf16(__fadd_rn(__fmul_rn(y0, e.x), __fmul_rn(x0, e.y)),
+                         __fadd_rn(__fmul_rn(y1, f.x), __fmul_rn(x1, f.y)));
     }
+    a = make_uint4(x[0], x[1], x[2], x[3]);
+    b = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
 template <int BITS, int D>
-__global__ void __launch_bounds__(256, 4) kv_append_kernel(AppendParams p) {
-    constexpr int CH = D / 8;       // 16-byte pieces of a head
-    constexpr int HPW = 32 / CH;    // heads of a key or value step
-    constexpr int QPW = 2 * HPW;    // heads of a query step
-    constexpr int UNROLL = 2;       // steps with their loads in flight
-    constexpr unsigned FULL = 0xffffffffu;
+__global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
+    constexpr int CH = D / 8;      // 16-byte pieces of a head
+    constexpr int LPH = CH / 2;    // lanes per head, two pieces each
+    constexpr int HPW = 32 / LPH;  // heads of a step
+    constexpr int UNROLL = 2;      // steps with their loads in flight
+    __shared__ uint4 stage[8][64];  // a warp's step, from one order of pieces to the other
     if (threadIdx.x == 0) pdl_launch_dependents();
     pdl_wait_primary();
     const int lane = threadIdx.x & 31;
+    const int l = lane % LPH, hsub = lane / LPH;
+    uint4 *const own = &stage[threadIdx.x / 32][hsub * CH];
     const int Hkv = p.kv.heads;
     const int half8 = p.rot / 16;   // pieces of a rotated half
-    const int64_t tasks = p.kv.tokens * p.nblk;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32; w < tasks;
-         w += (int64_t)gridDim.x * blockDim.x / 32) {
-        const int64_t tok = w / p.nblk;
-        const int blk = (int)(w % p.nblk);
+    // queries and keys: a lane's two pieces are those of a rotated pair,
+    // where there is one, so nothing passes between lanes
+    const int c0 = l < half8 ? l : 2 * l, c1 = l < half8 ? l + half8 : 2 * l + 1;
+    const int s_begin = blockIdx.y * p.per, s_end = min(p.steps, s_begin + p.per);
+    for (int64_t tok = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; tok < p.kv.tokens;
+         tok += (int64_t)gridDim.x * 8) {
         const KvToken at = kv_locate(p.kv, tok, lane);
         if (at.seq < 0) continue;  // a token of no sequence: nothing is written
         // where the token's keys and values go (-1: nowhere)
@@ -89,123 +109,79 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(AppendParams p) {
             }
         }
         if (bad && lane == 0 && p.status) atomicOr(p.status, (int)bad);
-        const float2 *const table = p.rope + (int64_t)at.pos * (p.rot / 2);  // read where turn
-        int s0 = blk * p.per;
-        const int s1 = min(p.steps, s0 + p.per);
-
-        // ---- queries: a lane holds two pieces, those of a rotated pair
-        // where there is one, so nothing passes between lanes
-        if (s0 < p.qsteps) {
-            const int l = lane % (CH / 2), hsub = lane / (CH / 2);
-            const bool rot = turn && l < half8;
-            const int c0 = l < half8 ? l : 2 * l, c1 = l < half8 ? l + half8 : 2 * l + 1;
-            float2 cs[8];
-            if (rot) load_cs(table + l * 8, cs);
-            const uint4 *const src = reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride);
-            uint4 *const dst = reinterpret_cast<uint4 *>(p.q_out + tok * p.Hq * D);
-            for (const int s2 = min(s1, p.qsteps); s0 < s2; s0 += UNROLL) {
-                uint4 a[UNROLL], b[UNROLL];
-#pragma unroll
-                for (int j = 0; j < UNROLL; ++j)
-                    if (const int h = (s0 + j) * QPW + hsub; s0 + j < s2 && h < p.Hq) {
-                        a[j] = src[h * CH + c0];
-                        b[j] = src[h * CH + c1];
-                    }
-#pragma unroll
-                for (int j = 0; j < UNROLL; ++j) {
-                    const int h = (s0 + j) * QPW + hsub;
-                    if (s0 + j >= s2 || h >= p.Hq) continue;
-                    if (rot) {
-                        uint32_t x[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
-                        uint32_t y[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 e = cs[2 * i], f = cs[2 * i + 1];
-                            const float x0 = bf16_lo(x[i]), x1 = bf16_hi(x[i]);
-                            const float y0 = bf16_lo(y[i]), y1 = bf16_hi(y[i]);
-                            x[i] = pack_bf16(__fsub_rn(__fmul_rn(x0, e.x), __fmul_rn(y0, e.y)),
-                                             __fsub_rn(__fmul_rn(x1, f.x), __fmul_rn(y1, f.y)));
-                            y[i] = pack_bf16(__fadd_rn(__fmul_rn(y0, e.x), __fmul_rn(x0, e.y)),
-                                             __fadd_rn(__fmul_rn(y1, f.x), __fmul_rn(x1, f.y)));
-                        }
-                        a[j] = make_uint4(x[0], x[1], x[2], x[3]);
-                        b[j] = make_uint4(y[0], y[1], y[2], y[3]);
-                    }
-                    dst[h * CH + c0] = a[j];
-                    dst[h * CH + c1] = b[j];
-                }
-            }
-            s0 = p.qsteps;
-        }
-        if (s0 >= s1 || row < 0) continue;
-
-        // ---- keys and values: a lane holds one piece, a group eight lanes
-        const int c = lane % CH, hsub = lane / CH;
-        const bool rot = turn && c < 2 * half8, second = c >= half8;
-        const int partner = !rot ? lane : second ? lane - half8 : lane + half8;
+        turn = turn && l < half8;
         float2 cs[8];
-        if (rot) {
-            load_cs(table + (second ? c - half8 : c) * 8, cs);
-            // first half: a cos - b sin; second: b cos + a sin
+        if (turn && s_begin < p.qsteps + p.ksteps) {
+            const float4 *const src = reinterpret_cast<const float4 *>(
+                p.rope + (int64_t)at.pos * (p.rot / 2) + l * 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) cs[i].y = second ? cs[i].y : -cs[i].y;
+            for (int i = 0; i < 4; ++i) {
+                const float4 t = src[i];
+                cs[2 * i] = make_float2(t.x, t.y);
+                cs[2 * i + 1] = make_float2(t.z, t.w);
+            }
         }
-        for (; s0 < s1; s0 += UNROLL) {
-            uint4 u[UNROLL];
+        for (int s0 = s_begin; s0 < s_end; s0 += UNROLL) {
+            uint4 a[UNROLL], b[UNROLL];
+            // a step: its kind (queries, keys, values), first head and heads
+            auto step = [&](int s, int &kind, int &h, int &n) {
+                kind = s < p.qsteps ? 0 : s < p.qsteps + p.ksteps ? 1 : 2;
+                h = (kind == 0 ? s : kind == 1 ? s - p.qsteps : s - p.qsteps - p.ksteps) * HPW + hsub;
+                n = kind == 0 ? p.Hq : Hkv;
+            };
 #pragma unroll
             for (int j = 0; j < UNROLL; ++j) {
-                const int h = (s0 + j - p.qsteps) * HPW + hsub;
-                u[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (s0 + j < s1 && h < 2 * Hkv) {
-                    const uint16_t *src = h < Hkv ? p.k + tok * p.k_stride + h * D
-                                                  : p.v + tok * p.v_stride + (h - Hkv) * D;
-                    u[j] = reinterpret_cast<const uint4 *>(src)[c];
+                int kind, h, n;
+                step(s0 + j, kind, h, n);
+                a[j] = b[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (s0 + j < s_end && h < n) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        kind == 0   ? p.q + tok * p.q_stride
+                        : kind == 1 ? p.k + tok * p.k_stride
+                                    : p.v + tok * p.v_stride) + h * CH;
+                    a[j] = src[kind < 2 ? c0 : 2 * l];
+                    b[j] = src[kind < 2 ? c1 : 2 * l + 1];
                 }
             }
 #pragma unroll
             for (int j = 0; j < UNROLL; ++j) {
-                if (s0 + j >= s1) break;
-                const int h = (s0 + j - p.qsteps) * HPW + hsub;
-                uint4 o = u[j];
-                if (turn && (s0 + j - p.qsteps) * HPW < Hkv) {  // a step with keys
-                    uint4 other;
-                    other.x = __shfl_sync(FULL, o.x, partner);
-                    other.y = __shfl_sync(FULL, o.y, partner);
-                    other.z = __shfl_sync(FULL, o.z, partner);
-                    other.w = __shfl_sync(FULL, o.w, partner);
-                    if (rot && h < Hkv) {
-                        const uint32_t a[4] = {o.x, o.y, o.z, o.w};
-                        const uint32_t b[4] = {other.x, other.y, other.z, other.w};
-                        uint32_t r[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 e = cs[2 * i], f = cs[2 * i + 1];
-                            r[i] = pack_bf16(__fadd_rn(__fmul_rn(bf16_lo(a[i]), e.x),
-                                                       __fmul_rn(bf16_lo(b[i]), e.y)),
-                                             __fadd_rn(__fmul_rn(bf16_hi(a[i]), f.x),
-                                                       __fmul_rn(bf16_hi(b[i]), f.y)));
-                        }
-                        o = make_uint4(r[0], r[1], r[2], r[3]);
+                if (s0 + j >= s_end) break;
+                int kind, h, n;
+                step(s0 + j, kind, h, n);
+                if (kind < 2 && turn) kv_turn(a[j], b[j], cs);
+                if (kind == 0) {
+                    if (h < n) {
+                        uint4 *const dst = reinterpret_cast<uint4 *>(p.q_out + (tok * p.Hq + h) * D);
+                        dst[c0] = a[j];
+                        dst[c1] = b[j];
                     }
+                    continue;
                 }
-                float x[8];
-                x[0] = bf16_lo(o.x); x[1] = bf16_hi(o.x);
-                x[2] = bf16_lo(o.y); x[3] = bf16_hi(o.y);
-                x[4] = bf16_lo(o.z); x[5] = bf16_hi(o.z);
-                x[6] = bf16_lo(o.w); x[7] = bf16_hi(o.w);
-                uint32_t code[8];
+                if (row < 0) continue;
+                if (kind == 1) {
+                    // neighbouring pieces from here on: four lanes a group
+                    __syncwarp();
+                    own[c0] = a[j];
+                    own[c1] = b[j];
+                    __syncwarp();
+                    a[j] = own[2 * l];
+                    b[j] = own[2 * l + 1];
+                }
+                const uint32_t x[8] = {a[j].x, a[j].y, a[j].z, a[j].w,
+                                       b[j].x, b[j].y, b[j].z, b[j].w};
+                uint32_t word[BITS / 2];
                 uint16_t sb, bb;
-                quantize_group8<BITS>(x, code, sb, bb);
-                if (h >= 2 * Hkv) continue;
-                const bool is_v = h >= Hkv;
-                const int64_t at_h = kv_head_row(p.kv, row, is_v ? h - Hkv : h);
-                uint32_t *dst = (is_v ? p.kv.vq : p.kv.kq) + at_h * (D * BITS / 32);
+                quantize_group16<BITS>(x, word, sb, bb);
+                if (h >= n) continue;
+                const int64_t at_h = kv_head_row(p.kv, row, h);
+                uint32_t *const dst = (kind == 2 ? p.kv.vq : p.kv.kq) + at_h * (D * BITS / 32);
                 if constexpr (BITS == 4)
-                    dst[c] = pack_u4(code);
+                    reinterpret_cast<uint2 *>(dst)[l] = make_uint2(word[0], word[1]);
                 else
-                    reinterpret_cast<uint2 *>(dst)[c] = pack_u8(code);
-                if ((c & 7) == 0)
-                    ((is_v ? p.kv.vp : p.kv.kp) + at_h * (D / 64))[c >> 3] =
+                    reinterpret_cast<uint4 *>(dst)[l] =
+                        make_uint4(word[0], word[1], word[2], word[3]);
+                if ((l & 3) == 0)
+                    ((kind == 2 ? p.kv.vp : p.kv.kp) + at_h * (D / 64))[l >> 2] =
                         (uint32_t)sb | ((uint32_t)bb << 16);
             }
         }
@@ -218,7 +194,7 @@ __global__ void __launch_bounds__(256, 4) kv_append_kernel(AppendParams p) {
 // against D b/8 + D/16 read.
 template <int BITS, int D>
 __global__ void __launch_bounds__(256)
-    kv_read_kernel(KvView kv, int per, int nblk, uint16_t *__restrict__ k,
+    kv_read_kernel(KvView kv, int per, uint16_t *__restrict__ k,
                    uint16_t *__restrict__ v, int32_t *status) {
     constexpr int CH = D / 8, HPW = 32 / CH;
     constexpr int UNROLL = 4;  // steps with their loads in flight
@@ -227,10 +203,9 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     const int c = lane % CH, hsub = lane / CH;
     const int heads = 2 * kv.heads, steps = (heads + HPW - 1) / HPW;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / 32;
-         w < kv.tokens * nblk; w += (int64_t)gridDim.x * blockDim.x / 32) {
-        const int64_t tok = w / nblk;
-        const int blk = (int)(w % nblk);
+    const int blk = blockIdx.y;
+    for (int64_t tok = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; tok < kv.tokens;
+         tok += (int64_t)gridDim.x * 8) {
         const KvToken at = kv_locate(kv, tok, lane);
         const int64_t row =
             at.seq >= 0 && at.pos >= 0 ? kv_row(kv, at.seq, at.pos) : -1;
@@ -283,15 +258,14 @@ __global__ void __launch_bounds__(256)
 // more heads.
 static void kv_tasks(int64_t tokens, int steps, int &per, int &nblk) {
     per = steps;
-    while (per > 2 && tokens * ((steps + per - 1) / per) < (int64_t)num_sms() * 64)
+    while (per > 2 && tokens * ((steps + per - 1) / per) < (int64_t)num_sms() * 32)
         per = (per + 1) / 2;
     nblk = (steps + per - 1) / per;
 }
 
-// Warp tasks of 8-warp blocks, at most eight blocks an SM (all its warps).
-static unsigned kv_grid(int64_t tasks) {
-    const int64_t blocks = (tasks + 7) / 8, cap = (int64_t)num_sms() * 8;
-    return (unsigned)(blocks < cap ? blocks : cap);
+// Blocks of eight warps, a token each; y: a token's tasks.
+static dim3 kv_grid(int64_t tokens, int nblk) {
+    return dim3((unsigned)std::min<int64_t>((tokens + 7) / 8, 1 << 20), (unsigned)nblk);
 }
 
 cudaError_t launch_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_out,
@@ -308,11 +282,12 @@ cudaError_t launch_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_ou
     p.rope_rows = rope_rows;
     p.rot = rot_dim;
     p.status = status;
-    const int hpw = 32 / (kv.dim / 8);
-    p.qsteps = (Hq + 2 * hpw - 1) / (2 * hpw);
-    p.steps = p.qsteps + (2 * kv.heads + hpw - 1) / hpw;
+    const int hpw = 32 / (kv.dim / 16);
+    p.qsteps = (Hq + hpw - 1) / hpw;
+    p.ksteps = (kv.heads + hpw - 1) / hpw;
+    p.steps = p.qsteps + 2 * p.ksteps;
     kv_tasks(kv.tokens, p.steps, p.per, p.nblk);
-    const unsigned grid = kv_grid(kv.tokens * p.nblk);
+    const dim3 grid = kv_grid(kv.tokens, p.nblk);
 #define GWA_KV(BB, DD)                                                         \
     if (kv.bits == BB && kv.dim == DD)                                         \
         return launch_pdl(reinterpret_cast<const void *>(kv_append_kernel<BB, DD>), \
@@ -329,11 +304,11 @@ cudaError_t launch_kv_read(const KvView &kv, uint16_t *k, uint16_t *v,
     const int steps = (2 * kv.heads + hpw - 1) / hpw;
     int per, nblk;
     kv_tasks(kv.tokens, steps, per, nblk);
-    const unsigned grid = kv_grid(kv.tokens * nblk);
+    const dim3 grid = kv_grid(kv.tokens, nblk);
 #define GWA_KV(BB, DD)                                                       \
     if (kv.bits == BB && kv.dim == DD)                                       \
         return launch_pdl(reinterpret_cast<const void *>(kv_read_kernel<BB, DD>), \
-                          grid, 256u, 0, st, kv, per, nblk, k, v, status);
+                          grid, 256u, 0, st, kv, per, k, v, status);
     GWA_KV(4, 64) GWA_KV(4, 128) GWA_KV(4, 256)
     GWA_KV(8, 64) GWA_KV(8, 128) GWA_KV(8, 256)
 #undef GWA_KV
