@@ -566,26 +566,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // below leaves every score at zero either way)
                     const float f = fmaxf(fac * pt.k_down, 1e-37f);
                     const int key0 = w.ta * KT + i * 64;
-                    float v0[32], v1[32];
-                    tc_ld32_async(t_s, v0);
-                    tc_ld32_async(t_s + 32, v1);
-                    tc_ld_wait(v0);
-                    tc_ld_tie(v1);
-                    if (key0 + 64 > least) {
-                        const int n_in = lim - key0;
+                    const int n_in = key0 + 64 > least ? lim - key0 : 64;
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        float v[32];
+                        tc_ld32_async(t_s + c, v);
+                        tc_ld_wait(v);
+                        if (key0 + c + 32 > least) {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            if (k >= n_in) v0[k] = -INFINITY;
-                            if (k + 32 >= n_in) v1[k] = -INFINITY;
+                            for (int k = 0; k < 32; ++k)
+                                if (k + c >= n_in) v[k] = -INFINITY;
                         }
-                    }
-                    float mx = -INFINITY, ma = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        mx = fmaxf(mx, fmaxf(v0[k], v0[k + 1]));
-                        ma = fmaxf(ma, fmaxf(v1[k], v1[k + 1]));
+                        for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
                     }
-                    mx = fmaxf(mx, ma) * f;
+                    mx *= f;
                     // ---- rescale
                     float corr = 1.f;
                     if (mx > m + 8.f) {
@@ -629,26 +625,28 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // ---- weights
                     const float sub = m == -INFINITY ? 0.f : m;
                     const float2 f2 = make_float2(f, f), s2 = make_float2(-sub, -sub);
-                    float2 acc[2];
-                    acc[0] = acc[1] = make_float2(0.f, 0.f);
-                    uint32_t o[32];
+                    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        float v[32];
+                        uint32_t o[16];
+                        tc_ld32_async(t_s + c, v);
+                        tc_ld_wait(v);
+                        if (key0 + c + 32 > least) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float2 x = fma2(make_float2(v0[k], v0[k + 1]), f2, s2);
-                        x = make_float2(ex2(x.x), ex2(x.y));
-                        acc[0] = add2(acc[0], x);
-                        o[k / 2] = pack_f16(x.x, x.y);
-                    }
+                            for (int k = 0; k < 32; ++k)
+                                if (k + c >= n_in) v[k] = -INFINITY;
+                        }
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) {
-                        float2 x = fma2(make_float2(v1[k], v1[k + 1]), f2, s2);
-                        x = make_float2(ex2(x.x), ex2(x.y));
-                        acc[1] = add2(acc[1], x);
-                        o[16 + k / 2] = pack_f16(x.x, x.y);
+                        for (int k = 0; k < 32; k += 2) {
+                            float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
+                            x = make_float2(ex2(x.x), ex2(x.y));
+                            acc = add2(acc, x);
+                            o[k / 2] = pack_f16(x.x, x.y);
+                        }
+                        tc_st16(t_s + c / 2, o);
                     }
-                    tc_st32(t_s, o);
-                    acc[0] = add2(acc[0], acc[1]);
-                    l += acc[0].x + acc[0].y;
+                    l += acc.x + acc.y;
                     if (pt.bad[0] | pt.bad[1] | pt.bad[2] | pt.bad[3]) {
                         // a value that is not finite leaves the products; the
                         // rows that see it are not finite either
