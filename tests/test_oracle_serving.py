@@ -1,0 +1,151 @@
+"""The plain implementations of the serving operators (oracle/serving.py)
+pinned to independent statements of the same definitions, and the refusals of
+their C entry points, all without a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import serving
+
+RNG = np.random.default_rng
+
+
+def test_bf16_rounds_to_nearest_even():
+    x = np.array([1.0, 1.0 + 2.0 ** -8, 1.0 + 3 * 2.0 ** -8, 1.0 + 2.0 ** -8 + 2.0 ** -20, -2.5],
+                 np.float32)
+    got = serving.bf16_value(serving.bf16_round(x))
+    assert got.tolist() == [1.0, 1.0, 1.0 + 2.0 ** -6, 1.0 + 2.0 ** -7, -2.5]
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_quantized_values_are_within_half_a_step(bits):
+    x = serving.bf16_round(RNG(bits).standard_normal((5, 3, 128)).astype(np.float32))
+    code, par = serving.quantize(x, bits)
+    assert code.min() >= 0 and code.max() <= 2 ** bits - 1
+    got = serving.values(serving.pack(code, bits), par, bits)
+    v = serving.bf16_value(x).astype(np.float64)
+    step = np.repeat(serving.bf16_value(par[..., 0]), 64, axis=-1).astype(np.float64)
+    # half a step, and what the scale's rounding to bf16 takes from the top
+    assert (np.abs(got - v) <= step * (0.5 + (2 ** bits - 1) * 2.0 ** -8)).all()
+
+
+@pytest.mark.parametrize("rot", [16, 64, 128])
+def test_rotation_turns_pairs_by_the_position(rot):
+    D, base = 128, 1e4
+    x = serving.bf16_round(RNG(rot).standard_normal((4, 2, D)).astype(np.float32))
+    pos = np.array([0, 1, 7, 200])
+    got = serving.bf16_value(serving.rotate(x, serving.rope_table(256, rot, base), pos))
+    v = serving.bf16_value(x).astype(np.float64)
+    want = v.copy()
+    for t in range(4):
+        for i in range(rot // 2):
+            a = pos[t] * base ** (-2 * i / rot)
+            z = (v[t, :, i] + 1j * v[t, :, i + rot // 2]) * np.exp(1j * a)
+            want[t, :, i], want[t, :, i + rot // 2] = z.real, z.imag
+    assert np.abs(got - want).max() <= 2.0 ** -8 * np.abs(v).max() * 2
+    assert (got[0] == v[0]).all() and (got[..., rot:] == v[..., rot:]).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_against_one_row_at_a_time(causal):
+    rng = RNG(3)
+    lens = [(1, 5), (0, 3), (4, 4), (2, 0), (3, 9)]  # (new tokens, cache length)
+    q_start = np.concatenate([[0], np.cumsum([a for a, _ in lens])])
+    kl = np.array([b for _, b in lens])
+    q = rng.standard_normal((q_start[-1], 4, 8))
+    k = [rng.standard_normal((n, 2, 8)) for n in kl]
+    v = [rng.standard_normal((n, 2, 8)) for n in kl]
+    got = serving.attention(q, k, v, q_start, kl, 0.3, causal)
+    for b, (n, length) in enumerate(lens):
+        for i in range(n):
+            pos = length - n + i
+            see = min(length, pos + 1) if causal else length
+            for h in range(4):
+                want = np.zeros(8)
+                if see > 0:
+                    s = np.array([0.3 * (q[q_start[b] + i, h] * k[b][t, h // 2]).sum()
+                                  for t in range(see)])
+                    p = np.exp(s - s.max())
+                    want = (p[:, None] * v[b][:see, h // 2]).sum(0) / p.sum()
+                assert np.allclose(got[q_start[b] + i, h], want, atol=1e-12)
+
+
+def test_sampling_order_and_masses():
+    x = np.array([0.5, 2.0, -np.inf, 2.0, 1.0])
+    assert serving.sample_order(x).tolist()[:4] == [1, 3, 4, 0]
+    w = serving.sample_masses(x, 0.5)
+    assert np.allclose(w / w.max(), np.exp((x - 2.0) / 0.5)) and w[2] == 0
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import group_wise_affine_gb300 as gwa
+    gwa.build()
+    return gwa.load()
+
+
+def cache(gwa, **kw):
+    a = dict(kq=1 << 20, kp=1 << 20, vq=1 << 20, vp=1 << 20, num_pages=4, heads=2, head_dim=128,
+             page_size=16, bits=4, group=64)
+    a.update(kw)
+    return gwa._KVCache(**a)
+
+
+def batch(gwa, **kw):
+    a = dict(q_start=1 << 20, kv_len=1 << 20, page_table=1 << 20, batch=1, max_pages=4, tokens=3,
+             max_q=3, max_kv=10)
+    a.update(kw)
+    return gwa._KVBatch(**a)
+
+
+BAD = [("head_dim", 96, "UNSUPPORTED"), ("bits", 3, "UNSUPPORTED"), ("group", 32, "UNSUPPORTED"),
+       ("page_size", 24, "UNSUPPORTED"), ("page_size", 8192, "UNSUPPORTED"),
+       ("heads", 0, "INVALID_ARG"), ("kq", 0, "INVALID_ARG"), ("vp", (1 << 20) + 4, "MISALIGNED")]
+BAD_BATCH = [("q_start", 0, "INVALID_ARG"), ("tokens", -1, "INVALID_ARG"),
+             ("kv_len", (1 << 20) + 2, "MISALIGNED"), ("max_pages", -1, "INVALID_ARG")]
+
+
+@pytest.mark.parametrize("field,value,code", BAD + BAD_BATCH)
+def test_cache_and_batch_are_checked(lib, field, value, code):
+    import group_wise_affine_gb300 as gwa
+    want = getattr(gwa, "GWA_ERR_" + code)
+    c = cache(gwa, **({field: value} if (field, value, code) in BAD else {}))
+    b = batch(gwa, **({field: value} if (field, value, code) in BAD_BATCH else {}))
+    p = ctypes.c_void_p(1 << 20)
+    assert lib.gwa_kv_append(None, 0, None, 0, p, 256, p, 256, c, b, None, 0, 0, None, None) == want
+    assert lib.gwa_kv_read(c, b, p, p, None, None) == want
+    assert lib.gwa_sdpa_paged(p, 512, 4, c, b, 0.1, 1, p, p, 1 << 30, None, None) == want
+    assert gwa.last_error()
+
+
+def test_append_attend_and_sample_arguments_are_checked(lib):
+    import group_wise_affine_gb300 as gwa
+    c, b, p, odd = cache(gwa), batch(gwa), ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 2)
+    invalid, misaligned = gwa.GWA_ERR_INVALID_ARG, gwa.GWA_ERR_MISALIGNED
+
+    def append(q=None, qs=0, qo=None, Hq=0, k=p, ks=256, v=p, vs=256, rope=None, rows=0, rot=0):
+        return lib.gwa_kv_append(q, qs, qo, Hq, k, ks, v, vs, c, b, rope, rows, rot, None, None)
+
+    assert append(k=None) == invalid and append(k=odd) == misaligned
+    assert append(ks=252) in (invalid, misaligned) and append(vs=128) == invalid
+    assert append(rope=p, rows=10, rot=24) == gwa.GWA_ERR_UNSUPPORTED
+    assert append(rope=None, rows=10, rot=64) == invalid
+    assert append(q=p, qs=512, qo=None, Hq=4) == invalid
+
+    def attend(q=p, qs=512, Hq=4, scale=0.1, out=p, ws=p, size=1 << 30):
+        return lib.gwa_sdpa_paged(q, qs, Hq, c, b, scale, 1, out, ws, size, None, None)
+
+    assert attend(Hq=3) == invalid and attend(scale=float("inf")) == invalid
+    assert attend(q=odd) == misaligned and attend(out=None) == invalid
+    assert attend(size=16) == gwa.GWA_ERR_WORKSPACE
+
+    def draw(x=p, dtype=0, rows=2, V=100, stride=100, u=p, token=p):
+        return lib.gwa_sample(x, dtype, rows, V, stride, u, None, None, None, None, token, None,
+                              None)
+
+    assert draw(dtype=2) == gwa.GWA_ERR_UNSUPPORTED and draw(V=524289, stride=1 << 20) == \
+        gwa.GWA_ERR_UNSUPPORTED
+    assert draw(V=0) == invalid and draw(stride=99) == invalid and draw(u=None) == invalid
+    assert draw(x=ctypes.c_void_p((1 << 20) + 1)) == misaligned
+    assert draw(rows=0) == 0
