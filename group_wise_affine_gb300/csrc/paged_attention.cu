@@ -882,14 +882,22 @@ static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) 
     X(4, 128, 4) X(4, 256, 1) X(4, 256, 2) X(8, 64, 1) X(8, 64, 2)        \
     X(8, 64, 4) X(8, 128, 1) X(8, 128, 2) X(8, 128, 4) X(8, 256, 1) X(8, 256, 2)
 
-// Rows up to which a sequence goes to the few-row kernel (PG_SPLIT_TEXT)
-constexpr int kPgSplit = 32;
+// Rows (new tokens x query heads of a KV head) up to which a sequence goes to
+// the few-row kernel.  That kernel against the prompt kernel, u4, eight KV
+// heads, us: heads of 128, one sequence of 4096 keys, 32 rows 20.0 : 25.7, 64
+// rows 24.0 : 25.6; one of 32768, 32 rows 49.5 : 55.2, 64 rows 73.3 : 55.5;
+// 16 of 4096, 16 rows 45 : 86, 32 rows 91 : 86, 64 rows 155 : 87.  Heads of
+// 256 (two KV heads), where the prompt kernel has one row tile: one sequence
+// of 4096, 64 rows 18 : 49; one of 32768, 48 : 77; 16 of 4096, 32 rows 51 :
+// 60, 64 rows 78 : 61.
+static int pg_split_rows(int dim) { return dim == 256 ? 64 : 32; }
 
 // Whether a batch can have sequences on either side.
 static int pg_split(const KvView &kv, int rep) {
     const int64_t rows = (int64_t)rep * kv.max_q;
-    if (rows <= kPgSplit) return (int)rows;  // no prompts
-    return kv.batch == 1 ? 0 : kPgSplit;     // a prompt alone, or both
+    const int most = pg_split_rows(kv.dim);
+    if (rows <= most) return (int)rows;  // no prompts
+    return kv.batch == 1 ? 0 : most;     // a prompt alone, or both
 }
 
 size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {

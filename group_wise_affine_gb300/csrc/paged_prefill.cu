@@ -352,8 +352,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     if (warp < 2) {
         // ------------------------------------------------ MMA issuers
         // Two row tiles: a warp each issues a tile's scores and values.  One:
-        // warp 0 issues the scores, warp 1 the values.  (One
-        // thread for all of them spent about 100 cycles on an MMA of 64.)
+        // warp 0 issues the scores, warp 1 the values.  (A thread spends 50 to
+        // 100 cycles on an MMA or a commit, so one for all of them was the
+        // last to finish.)
         if (lane == 0) {
             constexpr uint32_t id_s = pf_idesc(64), id_o = pf_idesc(D);
             const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::Q_OFF));
