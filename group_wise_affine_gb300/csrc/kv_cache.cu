@@ -17,8 +17,8 @@
 //
 // Bound: bytes.  A token moves (2 Hq + 2 Hkv) D 2 bytes of bf16 (q in and
 // out, k and v in) and writes 2 Hkv (D b/8 + D/16) of cache, so 8192 tokens
-// of 32 + 2 x 8 heads of 128 are 177 MB, 26 us of HBM bandwidth; one token is
-// a launch.  Measured: 46 us for those (the append alone; 3.9 TB/s), 5 us for
+// of 40 + 2 x 8 heads of 128 are 211 MB, 31 us of HBM bandwidth; one token is
+// a launch.  Measured: 46 us for those (the append alone; 4.6 TB/s), 5 us for
 // one token with its read-back.  A warp takes one token's heads in steps of 32
 // lanes x 16 dimensions (two 16-byte loads a lane, two steps in flight).
 // Queries and keys are loaded so that a lane holds both pieces of a rotated
@@ -26,9 +26,9 @@
 // them per head would be four times the head's own bytes).  A rotated key
 // then goes through shared memory into the order of its groups, four lanes
 // each.  What the time above the bytes goes to is the instructions of the
-// quantization (about 350 of a step's 450); dividing lanes took it from 42 to
-// 72 us, and a lane of eight values per group, with the pairs exchanged by
-// shuffles, took 64.
+// quantization (about 350 of a step's 450): with 32 query heads 42 us, where
+// lanes that divide when a quotient is near a half-integer made it 78, and
+// eight values a lane with the pairs exchanged by shuffles 50.
 #include <algorithm>
 
 #include "common.cuh"

@@ -13,17 +13,24 @@
 // whole at 2^19 tokens.
 //
 // The kept tokens are a prefix of the order (logit descending, index
-// ascending), so a cut is one logit and one index: kept are the logits above
-// it and its equals up to the index.  It is found in two steps: a histogram,
-// counts and masses together, over 2048 equal steps of the base-2 exponent y
-// between the row's smallest value (or 2^-41, whose masses are zero) and its
-// largest, which serves top-k and top-p alike; then the tokens of the one
-// step that holds the cut (a few hundred) are gathered and ranked by one CTA.
-// Steps of y spread the tokens of a real row over many counters (the high
-// bits of the logits put most of them on a handful, whose atomics then
-// queue).  A step that holds more than 2048 tokens (equal or clustered
-// logits) is searched digit by digit on order-preserving integer keys
-// instead.
+// ascending).  Three ways to them, each exact:
+//   top-k of up to 512: the step of exponent in which the k-th largest of the
+//     threads' maxima lies bounds the k-th token from below; the tokens above
+//     the bound (a few more than k) are gathered, sorted and drawn from by one
+//     CTA.  No token but the maxima is counted.
+//   no top-k: with the row's total mass known, a token below (total - goal) /
+//     V cannot be among the first that reach top-p's goal, nor one below
+//     min-p's mass be kept; if 2048 tokens or fewer are left they go the same
+//     way.
+//   otherwise: a histogram over 2048 equal steps of the base-2 exponent y
+//     between the row's smallest value (or 2^-41, whose masses are zero) and
+//     its largest, which serves top-k and top-p alike; then the tokens of the
+//     one step that holds the cut are gathered and ranked by one CTA.  Steps
+//     of y spread the tokens of a real row over many counters (the high bits
+//     of the logits put most of them on a handful, whose atomics then queue).
+//     A step that holds more than 2048 tokens (equal or clustered logits) is
+//     searched digit by digit on order-preserving integer keys instead.  The
+//     cut is one logit and one index, and a last pass draws.
 //
 // A row belongs to a cluster of CTAs.  Each keeps its slice of the row in
 // shared memory, read from HBM once; histograms and sums are joined through
@@ -31,9 +38,14 @@
 // handing it to all.  One launch per call.  The cluster is the smallest that
 // holds the row, made larger while the rows leave SMs idle.
 //
-// Bound: instructions.  The logits are read once (256 rows of 151669 bf16,
-// 78 MB, are 11.5 us of HBM bandwidth), but top-p forms every token's mass
-// and counts it with three shared-memory atomics.
+// Bound: instructions and the latency of a dozen barriers.  The logits are
+// read once (256 rows of 151669 bf16, 78 MB, 11.5 us of HBM bandwidth; a CTA
+// loads its 150 KB slice in 7.5 thousand cycles, near that rate), then a row
+// with top-k takes about 30 thousand cycles more (bound 11, gather 11, sort
+// and draw 12), one with top-p alone and a flat distribution 110 (masses 14,
+// histogram 45, ranking and the last pass 45), and nothing of the next row is
+// loaded meanwhile: 130 us for those rows with filters of all kinds, 16 us for
+// one row of 131072 fp32 on 16 CTAs.
 #include <algorithm>
 #include <mutex>
 #include <set>
@@ -50,7 +62,10 @@ constexpr int kSmThreads = 1024;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmBins = 2048;
 constexpr int kSmList = 2048;  // tokens that one CTA ranks
-constexpr int kSmShort = kSmThreads / 2;  // top-k of up to this: see the kernel
+// top-k of up to this goes by the threads' maxima: at half as many as a CTA's
+// threads the bound lets about 1.4 k tokens through, and 2048 hold them (256 x
+// 151669 rows with filters of all kinds: 173 us with it, 231 without)
+constexpr int kSmShort = kSmThreads / 2;
 constexpr int kSmMaxCluster = 16;
 constexpr int64_t kSmSliceBytes = 152 * 1024;
 

@@ -418,7 +418,11 @@ int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
  * Masked keys take no part whatever they hold (NaN and infinities included).
  * Softmax state and sums are fp32; weights times value scales enter the value
  * product rounded to fp16, queries are exact in fp16 within 2^24 of their
- * row's largest element.  Errors as gwa_kv_append, and GWA_ERR_WORKSPACE. */
+ * row's largest element.  Sequences of many rows (new tokens x query heads of
+ * a KV head; 33 and more, 65 with heads of 256) take values rounded to fp16,
+ * and of 8-bit keys scale * (code - 128) rounded to 11 bits (2^-12 of it);
+ * there a visible value that is not finite makes the whole row NaN.
+ * Errors as gwa_kv_append, and GWA_ERR_WORKSPACE. */
 int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
                    gwa_kv_cache cache, gwa_kv_batch batch, float scale,
                    int32_t causal, uint16_t *out, void *workspace,
@@ -443,7 +447,9 @@ size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
  * whose mass reaches floor(top_p * the mass of those), at least one token; of
  * those the tokens of at least min_p of the largest mass.  Drawn is the first
  * kept token, by index, at which the running mass passes floor(u * the kept
- * mass).  The result does not depend on how the work is split.  NaN logits
+ * mass); u outside [0, 1) is drawn as the nearer end, NaN as 0.  The result
+ * does not depend on how the work is split; prob is a quotient of two fp32
+ * roundings of the masses.  NaN logits
  * count as -inf, which is never drawn; +inf logits share everything; a row of
  * -inf alone gives token -1, probability 0.
  *   1 <= V <= 524288.  Errors: GWA_ERR_INVALID_ARG, GWA_ERR_MISALIGNED,
