@@ -144,9 +144,10 @@ struct PfTile {
     uint32_t bad[4];  // bit l of word j: key 4 l + j
 };
 
-// What is left of a CTA's run: the block and tile it stands at.
+// What is left of a CTA's run: the block and the unit of it where it stands,
+// and that unit counted over the whole batch.
 struct PfCursor {
-    int b, hk, rb, tile, left;
+    int b, hk, rb, unit, left, at;
     KvSeq s;
     int rows, nrb;
 };
@@ -166,54 +167,71 @@ __device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
     const int rows = p.rep * min(s.count, p.kv.max_q);
     return rows > p.split ? rows : 0;
 }
+// Units of work.  A block's start and end (queries in, rows out) count as
+// kPfHead tiles in front of its own: 13 thousand cycles where a tile of 128
+// keys takes 7, with one row tile 19 where a tile of 64 keys takes 4.5.  With
+// tiles alone as units, CTAs that hold many short blocks were the last to
+// finish (ragged prompts of 256 dimensions: 158 us, 126 with).
+template <int KT>
+__device__ __forceinline__ int pf_cost(int tiles) {
+    constexpr int kPfHead = KT == 64 ? 4 : 2;
+    return tiles > 0 ? tiles + kPfHead : 0;
+}
 template <int RB, int KT>
 __device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     const int rows = pf_rows<RB>(p, s);
     const int nrb = (rows + RB - 1) / RB;
-    if (!p.causal) return p.kv.heads * nrb * ((s.len + KT - 1) / KT);
+    if (!p.causal) return p.kv.heads * nrb * pf_cost<KT>((s.len + KT - 1) / KT);
     int n = 0;
-    for (int rb = 0; rb < nrb; ++rb) n += pf_tiles<RB, KT>(p, s, rows, rb);
+    for (int rb = 0; rb < nrb; ++rb) n += pf_cost<KT>(pf_tiles<RB, KT>(p, s, rows, rb));
     return p.kv.heads * n;
 }
 
-// A block's piece of the run: tiles [ta, tb) of nt.
+// A block's piece of the run: tiles [ta, tb) of nt; the block's last unit.
 struct PfPiece {
-    int b, hk, rb, ta, tb, nt, rows;
+    int b, hk, rb, ta, tb, nt, rows, last;
     KvSeq s;
 };
 template <int RB, int KT>
 __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece &w) {
-    if (c.left <= 0) return false;
-    int nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
-    while (c.tile >= nt) {  // the next block that sees a key
-        c.tile = 0;
-        if (++c.rb >= c.nrb) {
-            c.rb = 0;
-            if (++c.hk >= p.kv.heads || c.nrb == 0) {
-                c.hk = 0;
-                do {
-                    // (never past the batch, unless the lengths change meanwhile)
-                    if (++c.b >= p.kv.batch) return false;
-                    c.s = kv_seq(p.kv, c.b);
-                    c.rows = pf_rows<RB>(p, c.s);
-                    c.nrb = (c.rows + RB - 1) / RB;
-                } while (c.nrb == 0);
+    while (c.left > 0) {
+        int nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
+        while (c.unit >= pf_cost<KT>(nt)) {  // the next block that sees a key
+            c.unit = 0;
+            if (++c.rb >= c.nrb) {
+                c.rb = 0;
+                if (++c.hk >= p.kv.heads || c.nrb == 0) {
+                    c.hk = 0;
+                    do {
+                        // (never past the batch, unless the lengths change meanwhile)
+                        if (++c.b >= p.kv.batch) return false;
+                        c.s = kv_seq(p.kv, c.b);
+                        c.rows = pf_rows<RB>(p, c.s);
+                        c.nrb = (c.rows + RB - 1) / RB;
+                    } while (c.nrb == 0);
+                }
             }
+            nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
         }
-        nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
+        const int cost = pf_cost<KT>(nt), head = cost - nt;
+        const int from = c.unit, to = min(cost, from + c.left);
+        w.last = c.at - from + cost - 1;
+        c.left -= to - from;
+        c.at += to - from;
+        c.unit = to;
+        if (to <= head) continue;  // none of its tiles
+        w.b = c.b;
+        w.hk = c.hk;
+        w.rb = c.rb;
+        w.ta = max(from - head, 0);
+        w.tb = to - head;
+        w.nt = nt;
+        w.rows = c.rows;
+        w.s = c.s;
+        return true;
     }
-    w.b = c.b;
-    w.hk = c.hk;
-    w.rb = c.rb;
-    w.ta = c.tile;
-    w.tb = min(nt, c.tile + c.left);
-    w.nt = nt;
-    w.rows = c.rows;
-    w.s = c.s;
-    c.left -= w.tb - w.ta;
-    c.tile = w.tb;
-    return true;
+    return false;
 }
 
 // Rows (of one head) of a tile's 16-key blocks, on the first lanes.
@@ -272,7 +290,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     __shared__ PfCursor s_cur[kPfThreads / 32];
     __shared__ PfPiece s_piece[kPfThreads / 32], s_soft[8][2];
     __shared__ uint64_t rfull[kPfSlots], rempty[kPfSlots];
-    __shared__ int s_quot, s_rest, s_begin;
+    __shared__ int s_quot, s_rest;
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
 
@@ -339,15 +357,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 const int head = pf_units<RB, KT>(p, b) / p.kv.heads;
                 c.hk = (begin - at) / head;
                 int in = (begin - at) - c.hk * head;
-                for (int nt; in >= (nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb)); ++c.rb) in -= nt;
-                c.tile = in;
+                for (int n; in >= (n = pf_cost<KT>(pf_tiles<RB, KT>(p, c.s, c.rows, c.rb))); ++c.rb) in -= n;
+                c.unit = in;
+                c.at = begin;
             }
         }
         if (lane < kPfThreads / 32) s_cur[lane] = c;
         if (lane == 0) {
             s_quot = quot;
             s_rest = rest;
-            s_begin = begin;
             p.cuts[cta].slot = -1;
         }
     }
@@ -457,7 +475,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         uint32_t n = 0, nr = 0;  // tiles so far: of the CTA, of this row tile
         int pieces = 0, piece = 0;
         int longer = 0;          // of the pieces, those of two steps and more
-        int begin = s_begin;     // the unit the run stands at
         bool ok = true;
         int turn = 0;
         bool more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][0], lane);
@@ -736,7 +753,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         }
                     }
                     if (r == 0 && row == 0 && w.ta == 0 && !whole) {
-                        const int last = pg_owner(s_quot, s_rest, begin + w.nt - 1);
+                        const int last = pg_owner(s_quot, s_rest, w.last);
                         p.cuts[cta] = PgCut{2 * cta + piece, cta, last - cta + 1, w.s.first,
                                             w.hk * p.rep, w.rb * RB, nlive, 0};
                     }
@@ -747,7 +764,6 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 ++pieces;
             }
             n += tiles;
-            begin += tiles;
             piece = 1;
         }
     } else if (warp == 2 || warp == 3) {
