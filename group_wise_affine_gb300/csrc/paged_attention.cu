@@ -97,10 +97,15 @@ struct PgLayout {
     static __device__ __forceinline__ int key_of_row(int j) { return (j >> 1) + 4 * (j & 1); }
 };
 
-// Keys that some row of the sequence sees, in steps; row blocks; units.
+// Keys that some row of the sequence sees, in steps; row blocks; segments
+// (KV head and row block) with keys.
 struct PgSeq {
-    int first, count, len, rows, nrg, nt, units;
+    int first, count, len, rows, nrg, nt, segs;
 };
+// Steps that a segment's start and end (queries, merging the warps, the
+// output) count for in runs of kPgLong steps and more; shorter runs are cut by
+// steps alone.  (64 sequences of many lengths: 82 us without, 70 with.)
+constexpr int kPgHead = 2, kPgLong = 16;
 template <int NQ, int STEP>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
@@ -112,7 +117,7 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     if (r.rows > p.split) r.rows = 0;  // the prompt kernel's
     r.nrg = (r.rows + NQ - 1) / NQ;
     r.nt = (s.len + STEP - 1) / STEP;
-    r.units = p.kv.heads * r.nrg * r.nt;  // the entry point keeps the total below 2^31
+    r.segs = r.nt > 0 ? p.kv.heads * r.nrg : 0;  // (times nt: the entry point keeps the total below 2^31)
     return r;
 }
 
@@ -203,15 +208,20 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     // ---- this CTA's run of units, found by every warp for itself
     const int B = p.kv.batch;
     const int cta = blockIdx.x;
-    int total = 0;
-    for (int b0 = 0; b0 < B; b0 += kWarp)
-        total += __reduce_add_sync(
-            FULL, b0 + lane < B ? pg_seq<NQ, STEP>(p, b0 + lane).units : 0);
+    int total = 0, segs = 0;
+    for (int b0 = 0; b0 < B; b0 += kWarp) {
+        PgSeq s{};
+        if (b0 + lane < B) s = pg_seq<NQ, STEP>(p, b0 + lane);
+        total += __reduce_add_sync(FULL, s.segs * s.nt);
+        segs += __reduce_add_sync(FULL, s.segs);
+    }
+    const int head = total / kPgLong >= (int)gridDim.x ? kPgHead : 0;
+    total += segs * head;
     // sequences without keys: their rows are zero
     for (int i = cta; i < B; i += gridDim.x) {
         const PgSeq s = pg_seq<NQ, STEP>(p, i);
         if (p.by_seg)
-            for (int k = (s.units ? p.kv.heads * s.nrg : 0) + threadIdx.x; k < p.segs; k += blockDim.x)
+            for (int k = s.segs + threadIdx.x; k < p.segs; k += blockDim.x)
                 p.cuts[i * p.segs + k].slot = -1;
         if (s.nt > 0) continue;
         uint32_t *o = reinterpret_cast<uint32_t *>(p.out + (int64_t)s.first * p.Hq * D);
@@ -226,7 +236,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 
     int b = 0, at = 0;  // the sequence of the run's first unit, units before it
     for (int b0 = 0; b0 < B; b0 += kWarp) {
-        const int u = b0 + lane < B ? pg_seq<NQ, STEP>(p, b0 + lane).units : 0;
+        PgSeq s{};
+        if (b0 + lane < B) s = pg_seq<NQ, STEP>(p, b0 + lane);
+        const int u = s.segs * (s.nt + head);
         int incl = u;
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
@@ -253,16 +265,20 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     const int pmask = (1 << p.kv.page_shift) - 1;
 
     while (cur < end) {
-        while (cur >= at + sq.units && b + 1 < B) {
-            at += sq.units;
+        const int cost = sq.nt + head;  // of a segment
+        if (cur >= at + sq.segs * cost) {
+            // (never past the batch, unless the lengths change meanwhile)
+            if (b + 1 >= B) break;
+            at += sq.segs * cost;
             sq = pg_seq<NQ, STEP>(p, ++b);
+            continue;
         }
-        // (never, unless the lengths change meanwhile)
-        if (cur >= at + sq.units) break;
-        const int seg = (cur - at) / sq.nt;  // hk * nrg + rg
+        const int seg = (cur - at) / cost;  // hk * nrg + rg
+        const int from = cur - at - seg * cost, to = min(cost, from + (end - cur));
+        cur += to - from;
+        if (to <= head) continue;  // none of its steps
         const int hk = seg / sq.nrg, rg = seg % sq.nrg;
-        const int ta = cur - at - seg * sq.nt;
-        const int tb = min(sq.nt, ta + (end - cur));
+        const int ta = max(from - head, 0), tb = to - head;
         const int nlive = min(NQ, sq.rows - rg * NQ);
         const int32_t *table = p.kv.page_table + (int64_t)b * p.kv.max_pages;
 
@@ -746,7 +762,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             PgCut *cut = p.by_seg ? p.cuts + b * p.segs + seg : p.cuts + cta;
             if (ta == 0 && !whole) {
                 // starts here and goes on: up to the CTA of its last unit
-                const int last = pg_owner(quot, rest, at + (seg + 1) * sq.nt - 1);
+                const int last = pg_owner(quot, rest, at + (seg + 1) * cost - 1);
                 *cut = PgCut{2 * cta + piece, cta, last - cta + 1, sq.first, hk * p.rep,
                              rg * NQ, nlive, 0};
             } else if (whole && p.by_seg) {
@@ -754,7 +770,6 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             }
         }
         piece = 1;
-        cur = at + seg * sq.nt + tb;
         __syncthreads();  // the ring is free again
     }
 }
