@@ -105,7 +105,7 @@ struct PgSeq {
 // Steps that a segment's start and end (queries, merging the warps, the
 // output) count for in runs of kPgLong steps and more; shorter runs are cut by
 // steps alone.  (64 sequences of many lengths: 82 us without, 70 with.)
-constexpr int kPgHead = 2, kPgLong = 16;
+constexpr int kPgHead = 2, kPgLong = 6;
 template <int NQ, int STEP>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
