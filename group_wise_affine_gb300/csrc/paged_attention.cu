@@ -44,8 +44,8 @@
 // live in registers beside the unpacking; a tcgen05 MMA has at least 64 rows.
 //
 // Measured (u4, both kernels): one token over 4096 keys of 8 heads of 128 10.7
-// us, over 131071 42.3 us (3.6 TB/s of cache); 64 sequences of up to 8192, 32
-// heads, 81.6 us (3.2 TB/s).  Bound: instructions.  A warp spends about 340 on
+// us, over 131071 41.6 us (3.6 TB/s of cache); 64 sequences of up to 8192, 32
+// heads, 70 us (3.7 TB/s).  Bound: instructions.  A warp spends about 340 on
 // 16 keys of a head (128 of the MMAs, whose 8 cycles each fill half the tensor
 // pipe, the rest unpacking and softmax), issued at 2.1 a cycle and SM; the
 // bytes alone would take half the time.  Short caches are two launches and

@@ -45,7 +45,7 @@
 //
 // Measured: 2048 tokens of 40 heads of 128 over 8192 keys (8 KV heads, u4, 301
 // GFLOP) 346 us, 870 TFLOP/s; ragged prompts of up to 1100 tokens, 16 heads of
-// 256 over 1733 keys, 155 us.  Bound: the latency from one role to the next,
+// 256 over 1733 keys, 126 us.  Bound: the latency from one role to the next,
 // not a unit's rate.  A step of 64 keys and 256 rows takes 3300 cycles; its
 // MMAs take 1400 (those of 64 keys run at the rate of shared memory, 49
 // cycles each, the values' at the tensor cores', 64), its exponentials 1024

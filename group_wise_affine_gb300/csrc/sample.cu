@@ -44,7 +44,7 @@
 // with top-k takes about 30 thousand cycles more (bound 11, gather 11, sort
 // and draw 12), one with top-p alone and a flat distribution 110 (masses 14,
 // histogram 45, ranking and the last pass 45), and nothing of the next row is
-// loaded meanwhile: 130 us for those rows with filters of all kinds, 16 us for
+// loaded meanwhile: 101 us for those rows with filters of all kinds, 16 us for
 // one row of 131072 fp32 on 16 CTAs.
 #include <algorithm>
 #include <mutex>
@@ -681,7 +681,7 @@ struct Sampler {
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, int cl) {
+__global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, int cl, bool in_turn) {
     using S = Sampler<BF16>;
     using Raw = typename S::Raw;
     constexpr int PER = S::PER;
@@ -691,9 +691,35 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     Raw *slice = reinterpret_cast<Raw *>(sm_raw + ((sizeof(SmShared) + 15) / 16) * 16);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int rank = cl > 1 ? (int)cluster_rank() : 0;
-    const int64_t r = blockIdx.x / cl;
+    int64_t r = blockIdx.x / cl;
     if (tid == 0) pdl_launch_dependents();
     pdl_wait_primary();
+
+    if (in_turn) {
+        // the row of this place in the order of the classes: top-p without a
+        // short top-k, other draws, greedy rows
+        int cls = 3;
+        if (tid < p.rows) {
+            const int k = p.top_k ? p.top_k[tid] : 0;
+            cls = p.temperature && !(p.temperature[tid] > 0.f)      ? 2
+                  : k > 0 && k <= kSmShort                          ? 1
+                  : p.top_p && p.top_p[tid] < 1.f                   ? 0
+                                                                    : 1;
+        }
+        const u64 one = cls < 3 ? 1ull << (16 * cls) : 0;  // three counts in a word
+        const u64 incl = warp_scan(one);
+        if (lane == 31) sh.t_mass[warp] = incl;
+        __syncthreads();
+        const u64 wm = warp_scan(sh.t_mass[lane]), all = __shfl_sync(FULL, wm, 31);
+        u64 place = incl - one + __shfl_sync(FULL, wm, max(warp - 1, 0)) * (warp > 0);
+        place = (place >> (16 * cls)) & 0xffffu;
+        if (cls > 0) place += all & 0xffffu;
+        if (cls > 1) place += (all >> 16) & 0xffffu;
+        if (cls < 3 && (int64_t)place == r) sh.list_n = tid;
+        __syncthreads();
+        r = sh.list_n;
+        __syncthreads();
+    }
 
     // (waited for before the first word goes to another CTA: all of the
     // cluster run by then)
@@ -1017,7 +1043,11 @@ static cudaError_t launch_sample_t(const SampleParams &p, cudaStream_t st) {
     cudaError_t e = allow_smem(kfn, (int)(head + kSmSliceBytes + 48));
     if (e == cudaSuccess) e = allow_wide_clusters(kfn);
     if (e != cudaSuccess) return e;
-    return launch_pdl_cluster(kfn, (unsigned)(p.rows * cl), (unsigned)cl, kSmThreads, smem, st, p, cl);
+    // Rows differ in work by ten: where they take more than one wave, the
+    // heavy ones go first (256 x 151669 bf16, filters of all kinds: 130 us in
+    // the rows' order, 101 so); for a row a thread at most.
+    const bool in_turn = p.rows * cl > num_sms() && p.rows <= kSmThreads;
+    return launch_pdl_cluster(kfn, (unsigned)(p.rows * cl), (unsigned)cl, kSmThreads, smem, st, p, cl, in_turn);
 }
 
 cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st) {
