@@ -45,11 +45,12 @@
 //
 // Measured: 2048 tokens of 40 heads of 128 over 8192 keys (8 KV heads, u4, 301
 // GFLOP) 346 us, 870 TFLOP/s; ragged prompts of up to 1100 tokens, 16 heads of
-// 256 over 1733 keys, 126 us.  Bound: the latency from one role to the next,
-// not a unit's rate.  A step of 64 keys and 256 rows takes 3300 cycles; its
+// 256 over 1733 keys, 126 us.  Bound: instructions and the latency from one
+// role to the next.  A step of 64 keys and 256 rows takes 2700 cycles; its
 // MMAs take 1400 (those of 64 keys run at the rate of shared memory, 49
 // cycles each, the values' at the tensor cores', 64), its exponentials 1024
-// on the special-function units, and issue slots are used to a third.  The
+// on the special-function units, and issue slots are used to 63% (39% with one
+// row tile).  The
 // roles' loops also displace one another in the instruction caches: rolling
 // the softmax's two passes over halves of the scores, which reads the scores
 // twice, took 395 us to 346.  A block of 256 dimensions has one row tile, so
