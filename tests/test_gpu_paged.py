@@ -287,6 +287,36 @@ def test_bad_pages_raise_the_status():
             assert torch.equal(got[:q], good[:q])
 
 
+@pytest.mark.parametrize("D,rep,causal", [(64, 2, True), (128, 8, True), (256, 4, False)])
+def test_many_short_prompts(D, rep, causal):
+    # hundreds of blocks of a tile or two, cut anywhere: lengths from none to
+    # several tiles, some with more new tokens than keys
+    rng = np.random.default_rng(D)
+    lens = [(int(q), int(kv)) for q, kv in zip(rng.integers(0, 90, 60), rng.integers(0, 300, 60))]
+    lens += [(70, 0), (1, 1), (64, 64), (33, 129), (200, 128)]
+    check_attention(Case(D + 1, lens, Hq=4 * rep, Hkv=4, D=D), causal=causal)
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_many_sequences_in_long_runs(bits):
+    # enough work for runs of many steps a CTA, over segments from one step to
+    # dozens and sequences without keys
+    rng = np.random.default_rng(bits)
+    kv = np.concatenate([rng.integers(0, 6000, 40), rng.integers(0, 200, 40), [0, 1, 127, 128, 129]])
+    check_attention(Case(bits + 40, [(1, int(n)) for n in kv], Hq=8, Hkv=8, D=64, bits=bits))
+
+
+def test_scores_that_grow_along_the_keys():
+    # the running maximum moves in nearly every step, in either half of it
+    # (scores reach a few dozen, so a key's 2^-12 counts for more: twice the bar)
+    for q in (1, 48):
+        c = Case(50 + q, [(q, 400)], Hq=4, Hkv=2, D=128, bits=8)
+        pg, sl = c.table[0, np.arange(400) // c.page], np.arange(400) % c.page
+        grow = serving.bf16_value(c.kp[pg, :, sl]) * np.linspace(0.1, 12, 400)[:, None, None, None]
+        c.kp[pg, :, sl] = serving.bf16_round(grow.astype(np.float32))
+        check_attention(c, qscale=1.0, tight=2.0 ** -9)
+
+
 def test_another_stream():
     c = Case(17, [(1, 3000)] * 4, Hq=8, Hkv=2).device()
     q = dev_bf16(rand_bf16(c.rng, c.T, c.Hq, c.D))
