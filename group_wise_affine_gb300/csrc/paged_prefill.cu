@@ -22,11 +22,12 @@
 // columns as fp16 hi and lo parts against those of the queries' group sums.
 // (u8: scale * (code - 128) has up to 15 bits and is rounded to 11, relative
 // 2^-12; two exact parts would double the products.)  Values enter as fp16
-// s (c - c0) + b', rounded once, 2^-12 of a value, and weights as fp16.  A
+// s c + b, rounded once, 2^-11 of a value, and weights as fp16.  A
 // query row is scaled by a power of two, and each tile's keys and values by
-// one each, so fp16's range does not limit the inputs: the keys' comes back in
-// the row's factor f, the values' only ever grows within a block and rescales
-// O as the maximum does.
+// one each, the values' so that the tile's largest is 2^14 or a little less:
+// those down to 2^-21 of it keep their 11 bits, whether a row sees the largest
+// or not; smaller ones are rounded to 2^-32 of it.  The keys' power comes back
+// in the row's factor f, the values' rescales O as the maximum does.
 //
 // Warps: 0 and 1 issue the MMAs (a thread each); 2 and 3 turn the keys' and
 // the values' parameters into fp16 on the tile's power of two; 4-7 and
@@ -135,9 +136,6 @@ struct PfLayout {
     static_assert(KU >= 1 && K_OFF % 1024 == 0 && TILE % 1024 == 0, "tiles");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-
-// The values' operands are 2^-21 of what their power of two makes them.
-constexpr float kVDown = 0x1p21f;
 
 // One tile's powers of two, and its keys whose value parameters are not finite.
 struct PfTile {
@@ -724,7 +722,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             float x[16];
                             tc_ld16(t_o + c * 16, x);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) x[k] = x[k] * kVDown * inv;
+                            for (int k = 0; k < 16; ++k) x[k] *= inv;
                             *reinterpret_cast<uint4 *>(q_at(row, 2 * c)) =
                                 make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
@@ -743,8 +741,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 #pragma unroll
                                 for (int k = 0; k < 16; k += 4)
                                     *reinterpret_cast<float4 *>(q_at(row, 4 * c + k / 4)) =
-                                        make_float4(x[k] * kVDown * v_down, x[k + 1] * kVDown * v_down,
-                                                    x[k + 2] * kVDown * v_down, x[k + 3] * kVDown * v_down);
+                                        make_float4(x[k] * v_down, x[k + 1] * v_down,
+                                                    x[k + 2] * v_down, x[k + 3] * v_down);
                             }
                             flush(part + h * (D / 2));
                         }
@@ -815,13 +813,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 if (is_k) {
                     range_scale(t, up, down);
                 } else if (t > v_lim || (t > 0.f && t < v_lim * 0x1p-7f)) {
-                    // [2^14, 2^15), and kVDown below: into [2^-7, 2^-6), where
-                    // scale 2^24 is in range too, with a further 2 to grow and
-                    // 2^7 to shrink
+                    // into [2^14, 2^15), with a further 2^7 to shrink: values
+                    // down to 2^-21 of the tile's largest are normal fp16 numbers
                     range_scale(t, up, down);
                     v_lim = t > 0.f ? 32768.f * down : -1.f;
                 }
-                const float to = is_k ? up : up * (1.f / kVDown);
                 if (n >= kPfSlots) {
                     ok = __all_sync(FULL, wait(&rempty[slot], ((n / kPfSlots) & 1) ^ 1));
                     if (!ok) break;
@@ -834,16 +830,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     float s[4], b[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s[j] = bf16_lo(x[j][g]) * to;
-                        b[j] = bf16_hi(x[j][g]) * to;
+                        // (value codes enter as code / KC)
+                        s[j] = bf16_lo(x[j][g]) * (is_k ? up : up * KC);
+                        b[j] = bf16_hi(x[j][g]) * up;
                     }
                     if (is_k) {
                         *reinterpret_cast<uint2 *>(par + g * L::PROW) =
                             make_uint2(pack_f16(s[0], s[1]), pack_f16(s[2], s[3]));
                     } else {
-                        constexpr float c = 0x1p24f;  // codes enter as c 2^-24
                         *reinterpret_cast<uint2 *>(par + (G + g) * L::PROW) =
-                            make_uint2(pack_f16(s[0] * c, s[1] * c), pack_f16(s[2] * c, s[3] * c));
+                            make_uint2(pack_f16(s[0], s[1]), pack_f16(s[2], s[3]));
                         *reinterpret_cast<uint2 *>(par + (2 * G + g) * L::PROW) =
                             make_uint2(pack_f16(b[0], b[1]), pack_f16(b[2], b[3]));
                     }
@@ -1013,8 +1009,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 if (lane == 0) mbar_arrive(&kfull[st]);
                 if (tile + 1 < w.tb) load_k(base, tile + 1);
 
-                // ---- values, transposed: code 2^-24 (an fp16 subnormal) times
-                // scale 2^24 plus bias
+                // ---- values, transposed: code / KC, exact from 1024 + code,
+                // times KC scale plus bias.  (Codes left as the subnormals
+                // code 2^-24 save an operation, but want scales 2^24 times
+                // larger and so leave fp16 only 2^8 of range below the tile's
+                // largest value: 2048 tokens over 8192 keys 346 us, 351 so.)
 #pragma unroll
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
@@ -1026,9 +1025,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     const uint4 bw = *reinterpret_cast<const uint4 *>(vp + G * L::PROW);
                     const __half2 s2[4] = {bits_h2(sw.x), bits_h2(sw.y), bits_h2(sw.z), bits_h2(sw.w)};
                     const __half2 b2[4] = {bits_h2(bw.x), bits_h2(bw.y), bits_h2(bw.z), bits_h2(bw.w)};
-                    __half2 t2[4];  // for codes left at bits 4-7: 16 c 2^-24
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) t2[j] = __hmul2(s2[j], __floats2half2_rn(0.0625f, 0.0625f));
+                    // the fp16 pair 1024 + c as c / by
+                    auto over = [](uint32_t c, float by) {
+                        return __hfma2(bits_h2(c | 0x64006400u), __floats2half2_rn(1.f / by, 1.f / by),
+                                       __floats2half2_rn(-1024.f / by, -1024.f / by));
+                    };
 #pragma unroll 1
                     for (int jj = 0; jj < 4; ++jj) {
                         uint32_t lo[4], hi[4];  // dimensions 2 jj, 2 jj + 1 of the 8
@@ -1037,15 +1038,16 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             if constexpr (BITS == 4) {
                                 const uint32_t sel = 0x4400u + 0x1111u * jj;
                                 const uint32_t t = __byte_perm(vreg[u][2 * j][0], vreg[u][2 * j + 1][0], sel);
-                                lo[j] = h2_bits(__hfma2(bits_h2(t & 0x000f000fu), s2[j], b2[j]));
-                                hi[j] = h2_bits(__hfma2(bits_h2(t & 0x00f000f0u), t2[j], b2[j]));
+                                // (codes at bits 4-7 are 16 times their own)
+                                lo[j] = h2_bits(__hfma2(over(t & 0x000f000fu, KC), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(over(t & 0x00f000f0u, 16.f * KC), s2[j], b2[j]));
                             } else {
                                 const uint32_t sel = 0x5410u + 0x2222u * (jj & 1);
                                 const uint32_t t =
                                     __byte_perm(jj < 2 ? vreg[u][2 * j][0] : vreg[u][2 * j][VW - 1],
                                                 jj < 2 ? vreg[u][2 * j + 1][0] : vreg[u][2 * j + 1][VW - 1], sel);
-                                lo[j] = h2_bits(__hfma2(bits_h2(t & 0x00ff00ffu), s2[j], b2[j]));
-                                hi[j] = h2_bits(__hfma2(bits_h2((t >> 8) & 0x00ff00ffu), s2[j], b2[j]));
+                                lo[j] = h2_bits(__hfma2(over(t & 0x00ff00ffu, KC), s2[j], b2[j]));
+                                hi[j] = h2_bits(__hfma2(over((t >> 8) & 0x00ff00ffu, KC), s2[j], b2[j]));
                             }
                         }
                         unsigned char *row = vt + (d0 + 2 * jj) * 128;

@@ -1,0 +1,70 @@
+"""Edges of the paged cache and the attention over it: values far apart in
+size, lengths past the page table, rows without a place, loose bounds.
+
+Attention tolerances are those of ``test_gpu_paged`` (2^-8 of the output and
+2^-10 of the largest value that the row can see).
+"""
+import numpy as np
+import pytest
+import torch
+
+import group_wise_affine_gb300 as gwa
+from helpers import bf16_to_f64, dev_bf16
+from oracle import serving
+from test_gpu_paged import Case, check_attention, i32, rand_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    gwa.build()
+    gwa.load()
+    assert torch.cuda.is_available()
+
+
+def scale_values(c, b, first, last, factor):
+    """Multiplies the values of keys [first, last) of sequence b."""
+    t = np.arange(first, last)
+    pg, sl = c.table[b, t // c.page], t % c.page
+    c.vp[pg, :, sl] = serving.bf16_round(serving.bf16_value(c.vp[pg, :, sl]) * np.float32(factor))
+
+
+def attend(c, q, **kw):
+    """Output and fp64 reference of one call over the case's cache."""
+    c.device()
+    got = bf16_to_f64(gwa.sdpa_paged(dev_bf16(q), c.cache, c.batch, **kw))
+    kv = [c.sequence(b) for b in range(len(c.kl))]
+    want = serving.attention(serving.bf16_value(q).astype(np.float64), [k for k, _ in kv],
+                             [v for _, v in kv], c.q_start, c.kl, 1 / np.sqrt(c.D), True)
+    return got, want, kv
+
+
+def within(got, want, peak):
+    return np.isfinite(got).all() and (
+        np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -10 * peak).all()
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 16, 2.0 ** 24])
+@pytest.mark.parametrize("D,bits", [(64, 4), (128, 4), (256, 4), (64, 8), (128, 8), (256, 8)])
+def test_a_later_value_that_is_large_stays_with_its_readers_prompts(D, bits, ratio):
+    # the last token's value is finite and much larger than all others: the
+    # rows before it do not see it, and their values keep their precision
+    c = Case(D + bits, [(70, 100)], Hq=4, Hkv=2, D=D, bits=bits)
+    scale_values(c, 0, 99, 100, ratio)
+    got, want, kv = attend(c, rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7))
+    v = np.abs(kv[0][1])
+    assert within(got[:-1], want[:-1], v[:-1].max())
+    assert within(got[-1:], want[-1:], v.max())
+
+
+@pytest.mark.parametrize("D,bits", [(128, 4), (256, 8)])
+def test_a_large_value_of_no_weight_leaves_the_others_prompts(D, bits):
+    # the first key's score is hundreds below the others'
+    c = Case(D, [(70, 400)], Hq=4, Hkv=2, D=D, bits=bits)
+    scale_values(c, 0, 0, 1, 2.0 ** 24)
+    pg = c.table[0, 0]
+    c.kp[pg, :, 0] = serving.bf16_round(np.array([0.0, -100.0], np.float32))
+    q = serving.bf16_round(np.abs(serving.bf16_value(rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7))))
+    got, want, kv = attend(c, q)
+    assert within(got, want, np.abs(kv[0][1])[1:].max())
