@@ -9,6 +9,9 @@
 namespace gwa {
 
 constexpr int kPgMaxCtas = 2048;
+// The joins' weights are at most 2^-11: of 2048 pieces they sum up to no more
+// than 1, and their sums of means stay in the values' range.
+constexpr float kPgJoin = 11.f;
 
 // A (sequence, KV head, row block) that the cut spread over several CTAs: its
 // first piece's slot (-1: nothing to join), further pieces in the slots 2 (cta
@@ -29,7 +32,7 @@ struct PagedParams {
     PgCut *cuts;      // what the join has to do
     int segs;         // (KV head, row block) pairs of a sequence, at most
     int by_seg;       // cuts are indexed by sequence and pair, else by CTA
-    float *part;      // [2 ctas][rows of a block][dim + 4]
+    float *part;      // [2 ctas][rows of a block][dim + 4], see the joins
     int32_t *status;
     // sequences with up to `split` rows (new tokens x query heads of a KV
     // head) go to the few-row kernel, the others to the prompt kernel

@@ -24,10 +24,11 @@
 // 2^-12; two exact parts would double the products.)  Values enter as fp16
 // s c + b, rounded once, 2^-11 of a value, and weights as fp16.  A
 // query row is scaled by a power of two, and each tile's keys and values by
-// one each, the values' so that the tile's largest is 2^14 or a little less:
-// those down to 2^-21 of it keep their 11 bits, whether a row sees the largest
-// or not; smaller ones are rounded to 2^-32 of it.  The keys' power comes back
-// in the row's factor f, the values' rescales O as the maximum does.
+// one each.  The keys' comes back in the row's factor f; the values' puts the
+// largest that the block has met so far into [2^14, 2^15), and where it falls,
+// O is rescaled as for the maximum.  Values down to 2^-28 of that largest keep
+// their 11 bits, whether a row sees the largest or not; smaller ones are
+// rounded to 2^-39 of it.
 //
 // Warps: 0 and 1 issue the MMAs (a thread each); 2 and 3 turn the keys' and
 // the values' parameters into fp16 on the tile's power of two; 4-7 and
@@ -699,7 +700,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 if (ok) {
                     tc_fence_after();
                     const bool whole = w.ta == 0 && w.tb == w.nt;
-                    const float inv = l == 0.f ? 0.f : v_down / l;
+                    // (l first, the values' power second: both stay in range)
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
                     // the rows leave through the (free) query tile, whole rows at
                     // a time: bf16 at once, fp32 pieces in two halves
                     float *part = p.part + ((int64_t)(2 * cta + piece) * RB + i_blk) * (D + 4);
@@ -722,7 +724,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             float x[16];
                             tc_ld16(t_o + c * 16, x);
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) x[k] *= inv;
+                            for (int k = 0; k < 16; ++k) x[k] = x[k] * inv * v_down;
                             *reinterpret_cast<uint4 *>(q_at(row, 2 * c)) =
                                 make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
@@ -741,15 +743,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 #pragma unroll
                                 for (int k = 0; k < 16; k += 4)
                                     *reinterpret_cast<float4 *>(q_at(row, 4 * c + k / 4)) =
-                                        make_float4(x[k] * v_down, x[k + 1] * v_down,
-                                                    x[k + 2] * v_down, x[k + 3] * v_down);
+                                        make_float4(x[k] * inv * v_down, x[k + 1] * inv * v_down,
+                                                    x[k + 2] * inv * v_down, x[k + 3] * inv * v_down);
                             }
                             flush(part + h * (D / 2));
                         }
-                        if (live) {
-                            part[D] = m;
-                            part[D + 1] = l;
-                        }
+                        if (live) part[D] = l == 0.f ? -INFINITY : m + __log2f(l);
                     }
                     if (r == 0 && row == 0 && w.ta == 0 && !whole) {
                         const int last = pg_owner(s_quot, s_rest, w.last);
@@ -797,10 +796,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
-                        const float s = fabsf(bf16_lo(x[j][g]));
-                        const float b = fabsf(fmaf(KC, bf16_lo(x[j][g]), bf16_hi(x[j][g])));
-                        const float e = fmaf(KC, s, b);
-                        if (e < INFINITY) {
+                        // a quarter of KC |scale| + |b'|: below 2^127 where the
+                        // group's values are finite
+                        const float s = 0.25f * KC * bf16_lo(x[j][g]);
+                        const float e = fabsf(s) + fabsf(fmaf(0.25f, bf16_hi(x[j][g]), s));
+                        if (e < 0x1p127f) {
                             t = fmaxf(t, e);
                         } else {
                             bad |= 1u << j;
@@ -810,13 +810,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         }
                     }
                 t = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(t)));
-                if (is_k) {
+                if (is_k || t > v_lim) {
+                    // into [2^14, 2^15).  The values' power only falls within
+                    // a block (were it to rise by as much as the values may
+                    // shrink, the outputs so far could leave fp32's range).
                     range_scale(t, up, down);
-                } else if (t > v_lim || (t > 0.f && t < v_lim * 0x1p-7f)) {
-                    // into [2^14, 2^15), with a further 2^7 to shrink: values
-                    // down to 2^-21 of the tile's largest are normal fp16 numbers
-                    range_scale(t, up, down);
-                    v_lim = t > 0.f ? 32768.f * down : -1.f;
+                    up *= 0.25f;
+                    down *= 4.f;
+                    v_lim = t > 0.f ? 8192.f * down : -1.f;
                 }
                 if (n >= kPfSlots) {
                     ok = __all_sync(FULL, wait(&rempty[slot], ((n / kPfSlots) & 1) ^ 1));
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         // (value codes enter as code / KC)
-                        s[j] = bf16_lo(x[j][g]) * (is_k ? up : up * KC);
+                        s[j] = bf16_lo(x[j][g]) * (is_k ? 1.f : KC) * up;
                         b[j] = bf16_hi(x[j][g]) * up;
                     }
                     if (is_k) {
@@ -1097,7 +1098,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
 }
 
 // Joins cut blocks: a warp to a row, lanes over the dimensions, the pieces
-// (two mostly) one after the other.
+// (two mostly) one after the other.  A piece is its keys' mean value o_i and
+// the base-2 logarithm c_i of its weights' sum: out = sum_i 2^(c_i - M) o_i /
+// sum_i 2^(c_i - M).
 template <int D>
 __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, int rb) {
     if (threadIdx.x == 0) pdl_launch_dependents();
@@ -1119,11 +1122,11 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, 
             v[x] = t.x;
             v[x + 1] = t.y;
         }
-        const float mk = src[D], lk = src[D + 1];
+        const float mk = src[D];
         const float mx = fmaxf(m, mk), sub = mx == -INFINITY ? 0.f : mx;
-        const float f0 = ex2(m - sub), f1 = ex2(mk - sub);
+        const float f0 = ex2(m - sub), f1 = ex2(mk - sub - kPgJoin);
         m = mx;
-        l = fmaf(l, f0, lk * f1);
+        l = fmaf(l, f0, f1);
 #pragma unroll
         for (int x = 0; x < V; ++x) a[x] = fmaf(a[x], f0, v[x] * f1);
     }

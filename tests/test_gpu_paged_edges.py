@@ -68,3 +68,20 @@ def test_a_large_value_of_no_weight_leaves_the_others_prompts(D, bits):
     q = serving.bf16_round(np.abs(serving.bf16_value(rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7))))
     got, want, kv = attend(c, q)
     assert within(got, want, np.abs(kv[0][1])[1:].max())
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("first,then", [(1e30, 1e-10), (1e-10, 1e30), (1e-30, 1e30)])
+def test_values_that_fall_and_rise_by_many_powers_prompts(D, first, then):
+    c = Case(31, [(80, 700)], Hq=4, Hkv=2, D=D)
+    scale_values(c, 0, 0, 256, first)
+    scale_values(c, 0, 256, 700, then)
+    check_attention(c)
+
+
+@pytest.mark.parametrize("vscale", [1e-36, 1e34, 3e37])
+@pytest.mark.parametrize("D,bits", [(128, 4), (256, 8)])
+def test_values_near_the_ends_of_the_range_prompts(D, bits, vscale):
+    # (blocks of one CTA, and blocks cut over many)
+    check_attention(Case(32, [(80, 1500)], Hq=4, Hkv=2, D=D, bits=bits, vscale=vscale))
+    check_attention(Case(33, [(80, 90)] * 2, Hq=4, Hkv=2, D=D, bits=bits, vscale=vscale))
