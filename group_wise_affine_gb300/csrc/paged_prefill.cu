@@ -11,8 +11,8 @@
 //   O += P V'    (M = 128 rows, N = head_dim; P from tensor memory, V'
 //                transposed in shared memory)
 // with the running maximum m and sum per row in fp32, one thread to a row; m
-// moves only when a step's maximum passes it by 8 (weights up to 2^8), and
-// then O is rescaled in tensor memory.  Each row tile has two score buffers,
+// moves only when a step's maximum passes it by 8 (weights up to 2^8, held
+// times 2^7), and then O is rescaled in tensor memory.  Each row tile has two score buffers,
 // and its scores run two steps ahead of its values, so the tensor cores and
 // the softmax of one row tile overlap.
 //
@@ -137,6 +137,10 @@ struct PfLayout {
     static_assert(KU >= 1 && K_OFF % 1024 == 0 && TILE % 1024 == 0, "tiles");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
+
+// A row's weights are 2^(kUp + x - m), where a score x passes the running
+// maximum m by up to kLazy: at most 2^15.
+constexpr float kLazy = 8.f, kUp = 7.f;
 
 // One tile's powers of two, and its keys whose value parameters are not finite.
 struct PfTile {
@@ -615,7 +619,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     mx *= f;
                     // ---- rescale
                     float corr = 1.f;
-                    if (mx > m + 8.f) {
+                    if (mx > m + kLazy) {
                         corr = m == -INFINITY ? 0.f : ex2(m - mx);
                         m = mx;
                         l *= corr;
@@ -654,7 +658,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         }
                     }
                     // ---- weights
-                    const float sub = m == -INFINITY ? 0.f : m;
+                    // (times 2^7, as their sum: up to 2^15, so that weights
+                    // down to 2^-32 of the largest are not lost in fp16)
+                    const float sub = m == -INFINITY ? 0.f : m - kUp;
                     const float2 f2 = make_float2(f, f), s2 = make_float2(-sub, -sub);
                     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll 1

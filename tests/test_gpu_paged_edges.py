@@ -85,3 +85,26 @@ def test_values_near_the_ends_of_the_range_prompts(D, bits, vscale):
     # (blocks of one CTA, and blocks cut over many)
     check_attention(Case(32, [(80, 1500)], Hq=4, Hkv=2, D=D, bits=bits, vscale=vscale))
     check_attention(Case(33, [(80, 90)] * 2, Hq=4, Hkv=2, D=D, bits=bits, vscale=vscale))
+
+
+@pytest.mark.parametrize("q", [1, 80])
+def test_many_small_weights_beside_one_that_takes_all(q):
+    # one key takes the weight and has a value of zero, 131071 others take
+    # 2^-25.2 each of it: the output is a few thousandths of their values.  152
+    # sequences over the same pages, so that a block's keys are not cut
+    n, B = 131072, 152
+    c = Case(35, [(q, n + q)], Hq=2, Hkv=1, D=64, page=4096)
+    c.kq[:] = 0
+    c.kp[:] = 0
+    c.vp[:] = serving.bf16_round(np.array([2.0 ** -6, 1.0], np.float32))
+    pg = c.table[0, 0]
+    c.kp[pg, :, 0] = serving.bf16_round(np.array([0.0, 4.375], np.float32))
+    c.vp[pg, :, 0] = 0
+    qb = serving.bf16_round(np.full((c.T, 2, 64), 0.5, np.float32))
+    _, want, kv = attend(c, qb)     # scores 4.375 * 32 / 8 = 17.5 and 0
+    assert 0.003 < want.min() and want.max() < 0.005
+    batch = gwa.KVBatch(i32(np.arange(B + 1) * q), i32([n + q] * B), i32(np.repeat(c.table, B, 0)),
+                        B * q, q, n + q)
+    got = bf16_to_f64(gwa.sdpa_paged(dev_bf16(np.tile(qb, (B, 1, 1))), c.cache, batch))
+    for b in range(B):
+        assert within(got[b * q:(b + 1) * q], want, np.abs(kv[0][1]).max())
