@@ -22,7 +22,10 @@
 // Its range is met by powers of two: a query row is scaled so that its
 // largest element lies in [2^12, 2^13), and the value scales so that the
 // largest met so far lies in [2^5, 2^6) (the accumulators are rescaled when a
-// larger one comes, as they are for the running maximum).
+// larger one comes, as they are for the running maximum).  A product of weight
+// and scale is thus rounded to 2^-12 of itself or 2^-30 of the largest weight
+// times the largest scale; where a causal mask hides the largest from some
+// rows, to 2^-39.
 //
 // Work split.  The unit is a step of some keys (STEP) of one sequence, KV head and
 // block of up to 8 NN query rows (GQA heads x new tokens); the units of the
@@ -350,8 +353,12 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             }
         }
         __syncthreads();
-        // every row of the block sees the keys below `all`
+        // every row of the block sees the keys below `all`, none those from
+        // `seen` on
         int all = 0x7fffffff;
+        const int seen =
+            !p.causal ? sq.len
+                      : min(sq.len, sq.len - sq.count + (rg * NQ + nlive - 1) / p.rep + 1);
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
@@ -427,7 +434,11 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 o[nn][j][3] *= c1;
             }
         };
-        // One step of 32 keys.  EDGE: some row does not see all of them.
+        // One step of 32 keys.  EDGE: some row does not see all of them.  The
+        // largest value scale may then be of a key that this row does not see:
+        // weights stay at 1 there instead of 2^8, and scales go up to 2^15
+        // instead of 2^6, so that keys of 2^24 times smaller scales keep their
+        // place in fp16.  (Such steps are the segment's last ones.)
         auto compute = [&](const unsigned char *stg, const int key0, auto edge_t) {
             constexpr bool EDGE = decltype(edge_t)::value;
             // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + HALF kk + kv_g,
@@ -497,7 +508,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn)
                         emax = fmaxf(emax, fmaxf(e[u][kk][nn][0], e[u][kk][nn][1]));
-            if (__any_sync(FULL, emax > kLazy)) {
+            if (__any_sync(FULL, emax > (EDGE ? 1.f : kLazy))) {
                 // a new maximum
 #pragma unroll
                 for (int nn = 0; nn < NN; ++nn) {
@@ -544,7 +555,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         w = *reinterpret_cast<const uint32_t *>(stg + L::VP_OFF + u * L::PB +
                                                                 ((kv_g + 8 * kk) * G + gg) * 4);
                         // past the end lie no parameters (but anything)
-                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= sq.len) w = 0u;
+                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= seen) w = 0u;
                         smax = fmaxf(smax, fabsf(bf16_lo(w)));
                     }
             if (__any_sync(FULL, smax > vlim)) {
@@ -563,9 +574,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 }
                 const float top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
                 if (top > vlim) {
-                    // 2^ex <= top < 2^(ex+1): times 2^(5-ex)
+                    // 2^ex <= top < 2^(ex+1): times 2^(kRange-ex)
+                    constexpr int kRange = EDGE ? 14 : 5;
                     const int ex = min(max(f32_exp_field(top), 6), 253);
-                    const float ninv = __uint_as_float((uint32_t)(259 - ex > 254 ? 254 : 259 - ex) << 23);
+                    const float ninv = __uint_as_float((uint32_t)min(254 + kRange - ex, 254) << 23);
                     const float vf = vlim < 0.f ? 1.f : ninv / vinv;
 #pragma unroll
                     for (int nn = 0; nn < NN; ++nn) scale_rows(nn, vf, vf);

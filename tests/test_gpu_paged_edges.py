@@ -108,3 +108,15 @@ def test_many_small_weights_beside_one_that_takes_all(q):
     got = bf16_to_f64(gwa.sdpa_paged(dev_bf16(np.tile(qb, (B, 1, 1))), c.cache, batch))
     for b in range(B):
         assert within(got[b * q:(b + 1) * q], want, np.abs(kv[0][1]).max())
+
+
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 16, 2.0 ** 24])
+@pytest.mark.parametrize("D,bits", [(64, 4), (128, 4), (256, 4), (64, 8), (128, 8), (256, 8)])
+def test_a_later_value_that_is_large_stays_with_its_readers_few_rows(D, bits, ratio):
+    for kv_len in (20, 300):
+        c = Case(D + bits, [(3, kv_len)], Hq=4, Hkv=2, D=D, bits=bits)
+        scale_values(c, 0, kv_len - 1, kv_len, ratio)
+        got, want, kv = attend(c, rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7))
+        v = np.abs(kv[0][1])
+        assert within(got[:-1], want[:-1], v[:-1].max())
+        assert within(got[-1:], want[-1:], v.max())
