@@ -821,13 +821,15 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
         float mx = m;
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) mx = fmaxf(mx, ml[j].x);
-        if (mx == -INFINITY) mx = 0.f;
-        const float f0 = ex2(m - mx);
+        // (where no piece of the group has a key that the row sees, m stays
+        // below every other's)
+        const float sub = mx == -INFINITY ? 0.f : mx;
+        const float f0 = ex2(m - sub);
         l *= f0;
         a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            const float f = ex2(ml[j].x - mx);
+            const float f = ex2(ml[j].x - sub);
             l = fmaf(f, ml[j].y, l);
             a.x = fmaf(f, v[j].x, a.x);
             a.y = fmaf(f, v[j].y, a.y);

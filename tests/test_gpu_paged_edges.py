@@ -120,3 +120,30 @@ def test_a_later_value_that_is_large_stays_with_its_readers_few_rows(D, bits, ra
         v = np.abs(kv[0][1])
         assert within(got[:-1], want[:-1], v[:-1].max())
         assert within(got[-1:], want[-1:], v.max())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q,kv", [(3, 129), (3, 385), (3, 1537), (80, 385), (80, 2049)])
+def test_scores_far_below_zero_in_cut_segments(D, q, kv):
+    # every score lies hundreds below zero, and the last piece of a cut
+    # segment holds keys that the earlier rows do not see
+    c = Case(D + kv, [(q, kv)], Hq=4, Hkv=2, D=D)
+    f = serving.bf16_value(c.kp).copy()
+    f[..., 1] -= np.float32(3000.0 / D)
+    c.kp = serving.bf16_round(f)
+    x = np.abs(serving.bf16_value(rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7)))
+    got, want, cache = attend(c, serving.bf16_round(x))
+    assert within(got, want, np.abs(cache[0][1]).max())
+
+
+@pytest.mark.parametrize("q,kv", [(3, 3000), (80, 3000)])
+def test_a_query_that_is_not_a_number_leaves_the_others(q, kv):
+    c = Case(41, [(q, kv)], Hq=4, Hkv=2)
+    x = rand_bf16(c.rng, c.T, c.Hq, c.D, scale=0.7)
+    c.device()
+    good = gwa.sdpa_paged(dev_bf16(x), c.cache, c.batch)
+    x[1, 2, 5] = 0x7fc0
+    got = gwa.sdpa_paged(dev_bf16(x), c.cache, c.batch)
+    assert torch.isnan(got[1, 2]).all()
+    got[1, 2], good[1, 2] = 0, 0
+    assert torch.equal(got, good)
