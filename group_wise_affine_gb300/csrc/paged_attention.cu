@@ -14,15 +14,16 @@
 //   scores  S^T = C_k Q^T    per 64 dimensions, fp32; then
 //           x = sum_g s_g S_g + b_g sum(Q_g);
 //   values  O^T += (C_v - c0)^T P'^T  with P' = p * s in fp16, plus
-//           sum_t p_t b'_t, b' = b + c0 s, c0 = 8 (u4) or 128 (u8).
+//           sum_t p_t b'_t in fp32, b' = b + c0 s, c0 = 8 (u4) or 128 (u8).
 // The centre c0 comes off by an MMA with a constant operand just before each
 // tile's codes: with it left in, an output that averages thousands of values
 // would be the small difference of two large sums (scores are summed afresh
 // for each tile and need none).  fp16 holds P' to 2^-12, bf16 only to 2^-9.
 // Its range is met by powers of two: a query row is scaled so that its
-// largest element lies in [2^12, 2^13), and the value scales so that the
-// largest met so far lies in [2^5, 2^6) (the accumulators are rescaled when a
-// larger one comes, as they are for the running maximum).  A product of weight
+// largest element lies in [2^12, 2^13), and the value scales and biases so
+// that the largest scale, or bias / (2 c0), met so far lies in [2^5, 2^6) (the
+// accumulators are rescaled when a larger one comes, as they are for the
+// running maximum).  A product of weight
 // and scale is thus rounded to 2^-12 of itself or 2^-30 of the largest weight
 // times the largest scale; where a causal mask hides the largest from some
 // rows, to 2^-39.
@@ -383,7 +384,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 for (int gg = 0; gg < G; ++gg) bs[nn][gg][h] = 0.f;
             }
         }
-        float vinv = 1.f, vlim = -1.f;  // value scales: times vinv, met up to vlim
+        // value scales and biases: times vinv, met up to vlim and 2 KC vlim
+        float vinv = 1.f, vlim = -1.f;
 
         // Page numbers of the tiles of 32 / U steps: lane U j + u holds those of
         // step j's tile u.
@@ -542,9 +544,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int u = 0; u < U; ++u) l[nn][h] += e[u][0][nn][h] + e[u][1][nn][h];
-            // ---- values: their parameters, and a larger scale than any so far
+            // ---- values: their parameters, and a larger one than any so far
             uint32_t vw[U][2][G];
-            float smax = 0.f;
+            float smax = 0.f, bmax = 0.f;
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -557,22 +559,28 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         // past the end lie no parameters (but anything)
                         if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= seen) w = 0u;
                         smax = fmaxf(smax, fabsf(bf16_lo(w)));
+                        // (the bias, and the scale's bits below its last place)
+                        bmax = fmaxf(bmax, fabsf(__uint_as_float(w)));
                     }
-            if (__any_sync(FULL, smax > vlim)) {
-                if (smax == INFINITY) {
-                    // an infinite scale makes its own readers' rows infinite,
-                    // and must not take the others' range
-                    smax = 0.f;
+            if (__any_sync(FULL, smax > vlim || bmax > 2.f * KC * vlim)) {
+                if (fmaxf(smax, bmax) == INFINITY) {
+                    // a key whose parameters are not finite makes its own
+                    // readers' rows so, and must not take the others' range
+                    smax = bmax = 0.f;
 #pragma unroll
                     for (int u = 0; u < U; ++u)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-                            for (int gg = 0; gg < G; ++gg)
-                                if (fabsf(bf16_lo(vw[u][kk][gg])) < INFINITY)
-                                    smax = fmaxf(smax, fabsf(bf16_lo(vw[u][kk][gg])));
+                            for (int gg = 0; gg < G; ++gg) {
+                                const float sv = fabsf(bf16_lo(vw[u][kk][gg])), bv = fabsf(bf16_hi(vw[u][kk][gg]));
+                                if (!(fmaxf(sv, bv) < INFINITY)) continue;
+                                smax = fmaxf(smax, sv);
+                                bmax = fmaxf(bmax, bv);
+                            }
                 }
-                const float top = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(smax)));
+                const float top = __uint_as_float(
+                    __reduce_max_sync(FULL, __float_as_uint(fmaxf(smax, bmax * (0.5f / KC)))));
                 if (top > vlim) {
                     // 2^ex <= top < 2^(ex+1): times 2^(kRange-ex)
                     constexpr int kRange = EDGE ? 14 : 5;
@@ -580,7 +588,14 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                     const float ninv = __uint_as_float((uint32_t)min(254 + kRange - ex, 254) << 23);
                     const float vf = vlim < 0.f ? 1.f : ninv / vinv;
 #pragma unroll
-                    for (int nn = 0; nn < NN; ++nn) scale_rows(nn, vf, vf);
+                    for (int nn = 0; nn < NN; ++nn) {
+                        scale_rows(nn, vf, vf);
+#pragma unroll
+                        for (int gg = 0; gg < G; ++gg) {
+                            bs[nn][gg][0] *= vf;
+                            bs[nn][gg][1] *= vf;
+                        }
+                    }
                     vinv = ninv;
                     vlim = __uint_as_float((uint32_t)(ex + 1) << 23);
                 }
@@ -592,8 +607,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
-                        const float s0 = bf16_lo(vw[u][kk][gg]);
-                        const float s = s0 * vinv, bb = fmaf(KC, s0, bf16_hi(vw[u][kk][gg]));
+                        const float s = bf16_lo(vw[u][kk][gg]) * vinv;
+                        const float bb = fmaf(KC, s, bf16_hi(vw[u][kk][gg]) * vinv);
 #pragma unroll
                         for (int nn = 0; nn < NN; ++nn) {
                             const float e0 = e[u][kk][nn][0], e1 = e[u][kk][nn][1];
@@ -701,8 +716,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 }
         __syncwarp();
         float *so = reinterpret_cast<float *>(wsm);
-        // powers of two: the value scales' and the codes' (rows g and g + 8)
-        const float back = 1.f / vinv * 0x1p24f, back1 = BITS == 4 ? back * 0.0625f : back;
+        // the codes' powers of two (rows g and g + 8); vinv's stays in
+        constexpr float back = 0x1p24f, back1 = BITS == 4 ? back * 0.0625f : back;
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn) {
 #pragma unroll
@@ -720,6 +735,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                     const int r = 8 * nn + 2 * t + h;
                     s_m[warp][r] = m[nn][h];
                     s_l[warp][r] = l[nn][h];
+                    s_f[warp][r] = vlim < 0.f ? 0x1p127f : vinv;
 #pragma unroll
                     for (int gg = 0; gg < G; ++gg) s_b[warp][r][gg] = bs[nn][gg][h];
                 }
@@ -729,20 +745,22 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         float *part = p.part + (int64_t)(2 * cta + piece) * NQ * (D + 4);
         if (threadIdx.x < NQ) {
             const int i = threadIdx.x;
-            float mx = kNone, den = 0.f;
+            // the merged rows are times the smallest of the warps' vinv
+            float mx = kNone, den = 0.f, v_all = 0x1p127f;
 #pragma unroll
-            for (int w = 0; w < kPgWarps; ++w) mx = fmaxf(mx, s_m[w][i]);
+            for (int w = 0; w < kPgWarps; ++w) {
+                mx = fmaxf(mx, s_m[w][i]);
+                v_all = fminf(v_all, s_f[w][i]);
+            }
 #pragma unroll
             for (int w = 0; w < kPgWarps; ++w) {
                 const float f = s_l[w][i] == 0.f ? 0.f : ex2(s_m[w][i] - mx);
-                s_f[w][i] = f;
+                s_f[w][i] = f * (v_all / s_f[w][i]);
                 den += f * s_l[w][i];
             }
-            s_den[i] = den;
-            if (!whole) {
-                part[i * (D + 4) + D] = mx == kNone ? -INFINITY : mx;
-                part[i * (D + 4) + D + 1] = den;
-            }
+            s_den[i] = den == 0.f ? 0.f : 1.f / den;
+            s_m[0][i] = 1.f / v_all;
+            if (!whole) part[i * (D + 4) + D] = den == 0.f ? -INFINITY : mx + __log2f(den);
         }
         __syncthreads();
         constexpr int C4 = D / 4;
@@ -760,12 +778,14 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                 a.z = fmaf(f, v.z + bw, a.z);
                 a.w = fmaf(f, v.w + bw, a.w);
             }
+            // (the sum first, the power second: both stay in range)
+            const float r = s_den[i], v_back = s_m[0][i];
+            a = make_float4(a.x * r * v_back, a.y * r * v_back, a.z * r * v_back, a.w * r * v_back);
             if (whole) {
-                const float r = s_den[i] == 0.f ? 0.f : 1.f / s_den[i];
                 const int rr = rg * NQ + i;
                 uint2 *dst = reinterpret_cast<uint2 *>(
                     p.out + ((int64_t)(sq.first + rr / p.rep) * p.Hq + hk * p.rep + rr % p.rep) * D);
-                dst[c4] = make_uint2(pack_bf16(a.x * r, a.y * r), pack_bf16(a.z * r, a.w * r));
+                dst[c4] = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
             } else {
                 reinterpret_cast<float4 *>(part + i * (D + 4))[c4] = a;
             }
@@ -787,11 +807,12 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 }
 
 // Joins the pieces of a (sequence, KV head, row block) that the cut spread
-// over several CTAs: piece i's output, max m_i and sum l_i give
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Block (x, y): row y of
-// cut x.  Threads take four dimensions each and every NG-th piece, eight
-// pieces' loads in flight, against a maximum of their own; the NG groups meet
-// in shared memory.
+// over several CTAs: piece i's mean value o_i and the base-2 logarithm c_i of
+// its weights' sum give out = sum_i 2^(c_i - M) o_i / sum_i 2^(c_i - M).
+// (Sums of weights times values would leave fp32's range where the values are
+// near its end.)  Block (x, y): row y of cut x.  Threads take four dimensions
+// each and every NG-th piece, eight pieces' loads in flight, against a maximum
+// of their own; the NG groups meet in shared memory.
 template <int D, int NQ>
 __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
     constexpr int C4 = D / 4, NG = 256 / C4, AHEAD = 8;
@@ -807,20 +828,20 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = grp; k0 < d.n; k0 += NG * AHEAD) {
         float4 v[AHEAD];
-        float2 ml[AHEAD];
+        float c[AHEAD];
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             const int k = k0 + j * NG;
-            ml[j] = make_float2(-INFINITY, 0.f);
+            c[j] = -INFINITY;
             v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (k >= d.n) continue;
             const float *src = p.part + ((int64_t)(k == 0 ? d.slot : 2 * (d.cta + k)) * NQ + i) * (D + 4);
             v[j] = reinterpret_cast<const float4 *>(src)[c4];
-            ml[j] = *reinterpret_cast<const float2 *>(src + D);
+            c[j] = src[D];
         }
         float mx = m;
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) mx = fmaxf(mx, ml[j].x);
+        for (int j = 0; j < AHEAD; ++j) mx = fmaxf(mx, c[j]);
         // (where no piece of the group has a key that the row sees, m stays
         // below every other's)
         const float sub = mx == -INFINITY ? 0.f : mx;
@@ -829,8 +850,8 @@ __global__ void __launch_bounds__(256) paged_join_kernel(PagedParams p) {
         a = make_float4(a.x * f0, a.y * f0, a.z * f0, a.w * f0);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
-            const float f = ex2(ml[j].x - sub);
-            l = fmaf(f, ml[j].y, l);
+            const float f = ex2(c[j] - sub - kPgJoin);
+            l += f;
             a.x = fmaf(f, v[j].x, a.x);
             a.y = fmaf(f, v[j].y, a.y);
             a.z = fmaf(f, v[j].z, a.z);

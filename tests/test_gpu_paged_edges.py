@@ -147,3 +147,32 @@ def test_a_query_that_is_not_a_number_leaves_the_others(q, kv):
     assert torch.isnan(got[1, 2]).all()
     got[1, 2], good[1, 2] = 0, 0
     assert torch.equal(got, good)
+
+
+@pytest.mark.parametrize("first,then", [(1e30, 1e-10), (1e-10, 1e30), (1e-30, 1e30)])
+@pytest.mark.parametrize("D", [128, 256])
+def test_values_that_fall_and_rise_by_many_powers_few_rows(D, first, then):
+    c = Case(31, [(1, 700)], Hq=4, Hkv=2, D=D)
+    scale_values(c, 0, 0, 256, first)
+    scale_values(c, 0, 256, 700, then)
+    check_attention(c)
+
+
+@pytest.mark.parametrize("vscale", [1e-36, 1e34, 3e37])
+@pytest.mark.parametrize("D,bits", [(64, 8), (128, 4), (256, 8)])
+def test_values_near_the_ends_of_the_range_few_rows(D, bits, vscale):
+    check_attention(Case(32, [(1, 30000)], Hq=4, Hkv=1, D=D, bits=bits, vscale=vscale))
+    check_attention(Case(33, [(5, 90)] * 2, Hq=4, Hkv=2, D=D, bits=bits, vscale=vscale))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_biases_far_above_their_scales_few_rows(bits):
+    # constant groups: a scale of zero and a large bias; their neighbours' 1e6
+    # times smaller
+    c = Case(34, [(2, 500)], Hq=4, Hkv=2, bits=bits)
+    f = serving.bf16_value(c.vp).copy()
+    f[::2, ..., 0] = 0.0
+    f[::2, ..., 1] = 3e38
+    f[1::2] *= np.float32(1e32)
+    c.vp = serving.bf16_round(f)
+    check_attention(c)
