@@ -12,10 +12,10 @@ namespace gwa {
 constexpr unsigned kKvBadPage = 1u;  // page outside the cache or the table
 constexpr unsigned kKvBadRope = 2u;  // position past the rotary table
 
-// New tokens [first, first + count) of sequence b, cache length len (0 <=
-// len <= the pages' capacity).
+// New tokens [first, first + count) of sequence b, which end at position end;
+// keys in the cache len = end, or the page table's capacity where that is less.
 struct KvSeq {
-    int first, count, len;
+    int first, count, end, len;
 };
 __device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int start, int next, int len) {
     const int n = (int)kv.tokens;
@@ -25,7 +25,8 @@ __device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int start, int next, i
     KvSeq s;
     s.first = a;
     s.count = e - a;
-    s.len = (int)min((int64_t)max(len, 0), min(cap, (int64_t)0x7fffff00));
+    s.end = min(max(len, 0), 0x7fffff00);
+    s.len = (int)min((int64_t)s.end, cap);
     return s;
 }
 __device__ __forceinline__ KvSeq kv_seq(const KvView &kv, int b) {
@@ -66,9 +67,16 @@ __device__ __forceinline__ KvToken kv_locate(const KvView &kv, int64_t tok, int 
     const int i = (int)(tok - s.first);
     if (i < 0 || i >= s.count) return r;
     r.seq = lo;
-    r.pos = s.len - s.count + i;
+    r.pos = s.end - s.count + i;
     return r;
 }
+
+// Keys that new token i of a sequence sees.
+__device__ __forceinline__ int kv_seen(const KvSeq &s, int i, int causal) {
+    return causal ? min(s.len, s.end - s.count + i + 1) : s.len;
+}
+// Whether new tokens lie past the page table.
+__device__ __forceinline__ bool kv_past(const KvSeq &s) { return s.end > s.len && s.count > 0; }
 
 // Row page * heads * page_size + slot of a position (-1: no such page); head
 // h's entry is kv_head_row of it.

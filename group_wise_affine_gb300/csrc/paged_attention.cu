@@ -104,7 +104,7 @@ struct PgLayout {
 // Keys that some row of the sequence sees, in steps; row blocks; segments
 // (KV head and row block) with keys.
 struct PgSeq {
-    int first, count, len, rows, nrg, nt, segs;
+    int first, base, len, rows, nrg, nt, segs;  // base: position of the first new token
 };
 // Steps that a segment's start and end (queries, merging the warps, the
 // output) count for in runs of kPgLong steps and more; shorter runs are cut by
@@ -115,7 +115,7 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     PgSeq r;
     r.first = s.first;
-    r.count = s.count;
+    r.base = s.end - s.count;
     r.len = s.len;
     r.rows = p.rep * min(s.count, p.kv.max_q);
     if (r.rows > p.split) r.rows = 0;  // the prompt kernel's
@@ -224,6 +224,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     // sequences without keys: their rows are zero
     for (int i = cta; i < B; i += gridDim.x) {
         const PgSeq s = pg_seq<NQ, STEP>(p, i);
+        if (p.status && threadIdx.x == 0 && kv_past(kv_seq(p.kv, i)))
+            atomicOr(p.status, (int)kKvBadPage);
         if (p.by_seg)
             for (int k = s.segs + threadIdx.x; k < p.segs; k += blockDim.x)
                 p.cuts[i * p.segs + k].slot = -1;
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                     qs[nn][gg][h] = __shfl_sync(FULL, sum[gg], from) * 0x1p-24f;
                 const int i = 8 * nn + 2 * t + h, rr = rg * NQ + i;
                 lim[nn][h] = i >= nlive ? 0
-                             : p.causal ? min(sq.len, sq.len - sq.count + rr / p.rep + 1)
+                             : p.causal ? min(sq.len, sq.base + rr / p.rep + 1)
                                         : sq.len;
             }
         }
@@ -358,14 +360,13 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         // `seen` on
         int all = 0x7fffffff;
         const int seen =
-            !p.causal ? sq.len
-                      : min(sq.len, sq.len - sq.count + (rg * NQ + nlive - 1) / p.rep + 1);
+            p.causal ? min(sq.len, sq.base + (rg * NQ + nlive - 1) / p.rep + 1) : sq.len;
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
             for (int h = 0; h < 2; ++h) all = min(all, lim[nn][h]);
         if (nlive < NQ) {  // padding rows: masked or not, they are never written
-            all = p.causal ? max(0, sq.len - sq.count + rg * NQ / p.rep + 1) : sq.len;
+            all = p.causal ? max(0, min(sq.len, sq.base + rg * NQ / p.rep + 1)) : sq.len;
         } else {
             all = __reduce_min_sync(FULL, all);
         }

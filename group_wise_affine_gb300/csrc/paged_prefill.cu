@@ -159,11 +159,7 @@ struct PfCursor {
 // Keys that rows [rb * RB, ...) of a sequence see, in tiles of KT.
 template <int RB, int KT>
 __device__ __forceinline__ int pf_tiles(const PagedParams &p, const KvSeq &s, int rows, int rb) {
-    int seen = s.len;
-    if (p.causal) {
-        const int last = (min(rows, (rb + 1) * RB) - 1) / p.rep;
-        seen = min(seen, s.len - s.count + last + 1);
-    }
+    const int seen = kv_seen(s, (min(rows, (rb + 1) * RB) - 1) / p.rep, p.causal);
     return seen > 0 ? (seen + KT - 1) / KT : 0;
 }
 template <int RB>
@@ -583,9 +579,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
 
                 const float fac = down * fabsf(p.scale) * 1.4426950408889634f;
-                const int lim = !live ? w.s.len
-                                : p.causal ? min(w.s.len, w.s.len - w.s.count + tok + 1)
-                                           : w.s.len;
+                const int lim = live ? kv_seen(w.s, tok, p.causal) : w.s.len;
                 const int least = __reduce_min_sync(FULL, lim);
                 float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
                 const int steps = tiles * NH;
@@ -1078,6 +1072,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         const int tid = threadIdx.x - 64;
         for (int b = cta; b < B; b += gridDim.x) {
             const KvSeq s = kv_seq(p.kv, b);
+            if (p.status && tid == 0 && kv_past(s)) atomicOr(p.status, (int)kKvBadPage);
             const int rows = pf_rows<RB>(p, s);
             for (int rb = 0; rb * RB < rows; ++rb) {
                 if (pf_tiles<RB, KT>(p, s, rows, rb) > 0) continue;

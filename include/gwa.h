@@ -338,11 +338,12 @@ typedef struct gwa_kv_cache {
  *               more has only its first max_q rows computed)
  *   max_kv      the longest kv_len, or more: sizes the launch, no result
  *               depends on it
- * Any value may be zero.  Lengths beyond max_pages * page_size are cut to it;
- * a token row that belongs to no sequence, or whose position is negative,
- * has no place in the cache.  `status` (NULL, or a device int32 that the
+ * Any value may be zero.  A token row that belongs to no sequence, or whose
+ * position is negative or past the page table (max_pages * page_size and on),
+ * has no place in the cache; attention goes over the keys that have one.
+ * `status` (NULL, or a device int32 that the
  * caller clears) collects by atomic OR: 1 a page number outside [0,
- * num_pages) or a position past the table; 2 a position past the rotary
+ * num_pages), or a length past the page table; 2 a position past the rotary
  * table.  What belongs to such a token is not written, a sequence that reads
  * such a page gives unspecified values; no address out of range is formed. */
 typedef struct gwa_kv_batch {

@@ -176,3 +176,53 @@ def test_biases_far_above_their_scales_few_rows(bits):
     f[1::2] *= np.float32(1e32)
     c.vp = serving.bf16_round(f)
     check_attention(c)
+
+
+@pytest.mark.parametrize("q", [3, 80])
+@pytest.mark.parametrize("causal", [True, False])
+def test_lengths_past_the_page_table(q, causal):
+    # tokens past the table have no place; the others keep their own
+    page, width = 16, 8
+    cap = page * width
+    c = Case(36, [(q, cap), (q, 40 + q)], Hq=4, Hkv=2, page=page).device()
+    table = np.full((2, width), -7, dtype=np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    kl = np.array([cap + 2, 40 + q])     # the first sequence's last two are past it
+    batch = gwa.KVBatch(i32(c.q_start), i32(kl), i32(table), c.T, q, int(kl.max()))
+    x = rand_bf16(c.rng, c.T, 8, c.D)
+    xd = dev_bf16(x)
+    kq0 = c.cache.kq.clone()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    gwa.kv_append(xd[:, 4:6], xd[:, 6:8], c.cache, batch, status=status)
+    assert int(status) == 1
+    pos = cap + 2 - q + np.arange(q)
+    live = pos < cap
+    codes, _ = serving.quantize(x[:q][live][:, 4:6], 4)
+    want_q = kq0.cpu().numpy().view(np.uint32).copy()
+    want_q[table[0, pos[live] // page], :, pos[live] % page] = serving.pack(codes, 4)
+    p2 = 40 + np.arange(q)
+    codes, _ = serving.quantize(x[q:, 4:6], 4)
+    want_q[table[1, p2 // page], :, p2 % page] = serving.pack(codes, 4)
+    assert np.array_equal(c.cache.kq.cpu().numpy().view(np.uint32), want_q)
+    status.zero_()
+    k, v = gwa.kv_read(c.cache, batch, status=status)
+    assert int(status) == 1
+    assert (k[q - 2:q] == 0).all() and (v[q - 2:q] == 0).all() and (k[:q - 2] != 0).any()
+    # attention: rows see the keys that are there, up to their own position
+    for name in ("kq", "kp", "vq", "vp"):
+        t = getattr(c.cache, name)
+        setattr(c, name, t.cpu().view(torch.int16).numpy().view(np.uint16).reshape(t.shape)
+                if t.dtype == torch.bfloat16 else t.cpu().numpy().view(np.uint32))
+    status.zero_()
+    got = bf16_to_f64(gwa.sdpa_paged(xd[:, :4], c.cache, batch, causal=causal, status=status))
+    assert int(status) == 1
+    kv = [c.sequence(b) for b in range(2)]
+    qf = serving.bf16_value(x[:, :4]).astype(np.float64)
+    for i in range(2 * q):
+        b, j = divmod(i, q)
+        seen = min(int(c.kl[b]), int(kl[b]) - q + j + 1) if causal else int(c.kl[b])
+        for h in range(4):
+            s = kv[b][0][:seen, h // 2] @ qf[i, h] / np.sqrt(c.D)
+            p = np.exp(s - s.max())
+            want = (p / p.sum()) @ kv[b][1][:seen, h // 2]
+            assert within(got[i, h], want, np.abs(kv[b][1]).max())
