@@ -836,6 +836,14 @@ static int check_rows(const void *x, int64_t stride, int64_t need, const char *w
     return GWA_OK;
 }
 
+static int clear_rows(uint16_t *x, int64_t n, void *stream, const char *fn) {
+    const int rc = check_device();
+    if (rc) return rc;
+    const cudaError_t e =
+        cudaMemsetAsync(x, 0, (size_t)n * 2, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
 int gwa_rope_table(float *table, int64_t n, int32_t rot_dim, double base,
                    void *stream) {
     const char *fn = "gwa_rope_table";
@@ -872,7 +880,13 @@ int gwa_kv_append(const uint16_t *q, int64_t q_stride, uint16_t *q_out,
     if (Hq < 0 || Hq > 65535 || rope_rows < 0)
         return fail(GWA_ERR_INVALID_ARG, "%s: Hq=%d rope_rows=%lld", fn, (int)Hq,
                     (long long)rope_rows);
-    if (kv.tokens == 0 || kv.batch == 0) return GWA_OK;
+    if (kv.tokens == 0) return GWA_OK;
+    if (kv.batch == 0) {  // tokens of no sequence: their queries are zero
+        if (Hq == 0) return GWA_OK;
+        const int64_t wide = (int64_t)Hq * kv.dim;
+        if ((rc = check_rows(q_out, wide, wide, "q_out", fn))) return rc;
+        return clear_rows(q_out, kv.tokens * wide, stream, fn);
+    }
     if ((rc = check_kv_ptrs(kv, fn))) return rc;
     const int64_t row = (int64_t)kv.heads * kv.dim;
     if ((rc = check_rows(k, k_stride, row, "k", fn))) return rc;
@@ -903,11 +917,14 @@ int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
     int rc = check_kv(cache, batch, &kv, fn);
     if (rc) return rc;
     if (kv.tokens == 0) return GWA_OK;
-    if (kv.batch == 0) return fail(GWA_ERR_INVALID_ARG, "%s: tokens of no sequence", fn);
-    if ((rc = check_kv_ptrs(kv, fn))) return rc;
     const int64_t row = (int64_t)kv.heads * kv.dim;
     if ((rc = check_rows(k, row, row, "k", fn))) return rc;
     if ((rc = check_rows(v, row, row, "v", fn))) return rc;
+    if (kv.batch == 0) {  // tokens of no sequence
+        rc = clear_rows(k, kv.tokens * row, stream, fn);
+        return rc ? rc : clear_rows(v, kv.tokens * row, stream, fn);
+    }
+    if ((rc = check_kv_ptrs(kv, fn))) return rc;
     if (!aligned(status, 4)) return fail(GWA_ERR_MISALIGNED, "%s: status (4 bytes)", fn);
     if ((rc = check_device())) return rc;
     cudaError_t e = launch_kv_read(kv, k, v, status, static_cast<cudaStream_t>(stream));

@@ -94,7 +94,10 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
     for (int64_t tok = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; tok < p.kv.tokens;
          tok += (int64_t)gridDim.x * 8) {
         const KvToken at = kv_locate(p.kv, tok, lane);
-        if (at.seq < 0) continue;  // a token of no sequence: nothing is written
+        // a token of no sequence has no keys and values to write, and its
+        // queries are zero; so are those past the rotary table
+        bool drop = at.seq < 0;
+        const int t_end = drop ? min(s_end, p.qsteps) : s_end;
         // where the token's keys and values go (-1: nowhere)
         int64_t row = -1;
         unsigned bad = 0u;
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
                 bad |= kKvBadRope;
                 row = -1;
                 turn = false;
+                drop = true;
             }
         }
         if (bad && lane == 0 && p.status) atomicOr(p.status, (int)bad);
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
                 cs[2 * i + 1] = make_float2(t.z, t.w);
             }
         }
-        for (int s0 = s_begin; s0 < s_end; s0 += UNROLL) {
+        for (int s0 = s_begin; s0 < t_end; s0 += UNROLL) {
             uint4 a[UNROLL], b[UNROLL];
             // a step: its kind (queries, keys, values), first head and heads
             auto step = [&](int s, int &kind, int &h, int &n) {
@@ -134,7 +138,7 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
                 int kind, h, n;
                 step(s0 + j, kind, h, n);
                 a[j] = b[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (s0 + j < s_end && h < n) {
+                if (s0 + j < t_end && h < n && !(kind == 0 && drop)) {
                     const uint4 *src = reinterpret_cast<const uint4 *>(
                         kind == 0   ? p.q + tok * p.q_stride
                         : kind == 1 ? p.k + tok * p.k_stride
@@ -145,7 +149,7 @@ __global__ void __launch_bounds__(256, 3) kv_append_kernel(AppendParams p) {
             }
 #pragma unroll
             for (int j = 0; j < UNROLL; ++j) {
-                if (s0 + j >= s_end) break;
+                if (s0 + j >= t_end) break;
                 int kind, h, n;
                 step(s0 + j, kind, h, n);
                 if (kind < 2 && turn) kv_turn(a[j], b[j], cs);

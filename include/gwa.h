@@ -344,8 +344,9 @@ typedef struct gwa_kv_cache {
  * `status` (NULL, or a device int32 that the
  * caller clears) collects by atomic OR: 1 a page number outside [0,
  * num_pages), or a length past the page table; 2 a position past the rotary
- * table.  What belongs to such a token is not written, a sequence that reads
- * such a page gives unspecified values; no address out of range is formed. */
+ * table.  Keys and values of such a token are not written, a sequence that
+ * reads such a page gives unspecified values; no address out of range is
+ * formed. */
 typedef struct gwa_kv_batch {
     const int32_t *q_start;
     const int32_t *kv_len;
@@ -377,7 +378,9 @@ int gwa_rope_table(float *table, int64_t n, int32_t rot_dim, double base,
  * quantized without rotation.  Finite inputs only.
  *   q         NULL (Hq = 0), or bf16 [tokens, Hq, head_dim]: queries, rotated
  *             the same way into q_out, contiguous [tokens, Hq, head_dim]
- *             (q_out may be q itself if q is contiguous)
+ *             (q_out may be q itself if q is contiguous).  At a negative
+ *             position as they are; past the rotary table, and of a token
+ *             of no sequence, zeros
  *   k, v      bf16 [tokens, heads, head_dim]
  *   *_stride  elements from one token to the next, a multiple of 8, at least
  *             a token's elements (views of one fused projection's rows)

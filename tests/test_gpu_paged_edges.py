@@ -226,3 +226,38 @@ def test_lengths_past_the_page_table(q, causal):
             p = np.exp(s - s.max())
             want = (p / p.sum()) @ kv[b][1][:seen, h // 2]
             assert within(got[i, h], want, np.abs(kv[b][1]).max())
+
+
+def test_rotated_queries_of_tokens_without_a_place():
+    # seven tokens: two of the first sequence (its page is bad), two of the
+    # second, of which the last is past the rotary table, three of none
+    c = Case(37, [(2, 40), (2, 21)], Hq=4, Hkv=2).device()
+    t = c.table.copy()
+    t[0, 2] = 1 << 20
+    batch = gwa.KVBatch(i32(c.q_start), i32(c.kl), i32(t), 7, 2, 40)
+    x = rand_bf16(c.rng, 7, 8, c.D)
+    xd = dev_bf16(x)
+    table = gwa.rope_table(40, c.D, 1e4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full((7, 4, c.D), float("nan"), dtype=torch.bfloat16, device="cuda")
+
+    def append(rope, b=batch):
+        status.zero_()
+        out.fill_(float("nan"))
+        return gwa.kv_append(xd[:, 4:6], xd[:, 6:8], c.cache, b, q=xd[:, :4], rope=rope,
+                             q_out=out, status=status)
+
+    pos = np.array([38, 39, 19, 20, -1, -1, -1])
+    rot = serving.bf16_value(serving.rotate(x[:, :4], serving.rope_table(40, c.D, 1e4), pos))
+    got = append(table).float().cpu().numpy()
+    assert int(status) == 1
+    assert np.array_equal(got[:4], rot[:4])         # a bad page: rotated all the same
+    assert (got[4:] == 0).all()                     # of no sequence: zero
+    got = append(table[:20].contiguous()).float().cpu().numpy()
+    assert int(status) == 3
+    assert np.array_equal(got[2], rot[2])
+    assert (got[[0, 1, 3, 4, 5, 6]] == 0).all()     # past the rotary table: zero
+    none = gwa.KVBatch(i32([0]), i32([]), i32(np.zeros((0, 1))), 7, 2, 40)
+    assert (append(table, none) == 0).all()
+    k, v = gwa.kv_read(c.cache, none)
+    assert (k == 0).all() and (v == 0).all()
