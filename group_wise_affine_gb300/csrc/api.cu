@@ -937,13 +937,12 @@ static int check_sdpa_paged(int32_t Hq, const KvView &kv, const char *fn) {
                     kv.heads);
     if ((int64_t)(Hq / kv.heads) * kv.max_q > (1 << 30))
         return fail(GWA_ERR_INVALID_ARG, "%s: max_q=%d", fn, kv.max_q);
-    // the kernels count (sequence, head, 8 rows, 64 keys) units in 31 bits
-    const double keys = (double)kv.max_pages * (double)(1 << kv.page_shift) / 64 + 1;
-    const double rows = (double)(Hq / kv.heads) * kv.max_q / 8 + 1;
-    if ((double)kv.batch * kv.heads * rows * keys > 2e9)
+    // (the kernels count units of work in 31 bits)
+    if (sdpa_paged_units(Hq, kv) > 2e9)
         return fail(GWA_ERR_UNSUPPORTED,
-                    "%s: batch=%d heads=%d max_q=%d max_pages=%d: more than 2^31 units of work",
-                    fn, kv.batch, kv.heads, kv.max_q, kv.max_pages);
+                    "%s: batch=%d heads=%d tokens=%lld max_q=%d max_pages=%d: more than 2^31 "
+                    "units of work", fn, kv.batch, kv.heads, (long long)kv.tokens, kv.max_q,
+                    kv.max_pages);
     return GWA_OK;
 }
 

@@ -103,6 +103,8 @@ cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
                               uint16_t *out, void *workspace, int32_t *status,
                               cudaStream_t st);
 size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv);
+// The most units of work that either of its kernels can find in such a batch.
+double sdpa_paged_units(int Hq, const KvView &kv);
 unsigned int prefill_timeouts(bool reset);  // paged_prefill.cu
 
 // Token sampling (sample.cu).

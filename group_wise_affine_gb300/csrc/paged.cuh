@@ -48,9 +48,19 @@ __device__ __forceinline__ int pg_owner(int quot, int rest, int unit) {
     return unit < big ? unit / (quot + 1) : rest + (unit - big) / quot;
 }
 
+// A total over the lanes of values whose own sums fit: as an int, or 0 if it
+// does not fit one (starts that decrease can name a token for many sequences;
+// of a batch that the entry point let through it always fits).
+__device__ __forceinline__ int pg_total(int64_t v) {
+    const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)v & 0xffffu);
+    const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)min(v >> 16, (int64_t)0x7ffffff));
+    return hi < 0x7fd0u ? (int)((hi << 16) + lo) : 0;
+}
+
 // Prompt kernel (paged_prefill.cu): its launch over the sequences with more
 // than p.split rows, and the bytes of its partial outputs.
 cudaError_t launch_paged_prefill(PagedParams p, void *workspace, cudaStream_t st);
 size_t paged_prefill_workspace_bytes(const KvView &kv, int rep);
+double paged_prefill_units(const KvView &kv, int rep, int split);
 
 }  // namespace gwa

@@ -79,6 +79,7 @@ struct PgLayout {
     static constexpr int U = 2;                  // tiles of a warp's step
     static constexpr int KEYS = 16 * U;          // keys of a warp's step
     static constexpr int STEP = kPgWarps * KEYS; // keys of a CTA's step
+    static_assert(STEP == 128, "sdpa_paged_units");
     static constexpr int TILE = 16 * G * GB;     // codes of a tile
     static constexpr int PB = 16 * G * 4;        // parameters of a tile
     static constexpr int K_OFF = 0;
@@ -899,10 +900,10 @@ static int pg_nn(int64_t rows, int D) {
 template <int BITS, int D, int NN>
 static int pg_grid(const KvView &kv, int64_t rows) {
     using L = PgLayout<BITS, D, NN>;
-    const int64_t units = (int64_t)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
-                          (((int64_t)kv.max_kv + L::STEP - 1) / L::STEP);
-    const int64_t full = (int64_t)num_sms() * L::CTAS;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(units, full), kPgMaxCtas));
+    const double units = (double)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
+                         (((int64_t)kv.max_kv + L::STEP - 1) / L::STEP);
+    const int full = std::min(num_sms() * L::CTAS, kPgMaxCtas);
+    return units < full ? std::max((int)units, 1) : full;
 }
 
 template <int BITS, int D, int NN>
@@ -957,6 +958,16 @@ static int pg_split(const KvView &kv, int rep) {
     const int most = pg_split_rows(kv.dim);
     if (rows <= most) return (int)rows;  // no prompts
     return kv.batch == 1 ? 0 : most;     // a prompt alone, or both
+}
+
+double sdpa_paged_units(int Hq, const KvView &kv) {
+    const int rep = Hq / kv.heads, split = pg_split(kv, rep);
+    const int rows = (int)std::min<int64_t>((int64_t)rep * kv.max_q, split);
+    const int nq = 8 * pg_nn(rows, kv.dim);
+    // every layout's step is 128 keys
+    const double steps = (double)kv.max_pages * (1 << kv.page_shift) / 128 + 1 + kPgHead;
+    const double few = (double)kv.batch * kv.heads * ((rows + nq - 1) / nq) * steps;
+    return std::max(few, paged_prefill_units(kv, rep, split));
 }
 
 size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {

@@ -172,9 +172,10 @@ __device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
 // keys takes 7, with one row tile 19 where a tile of 64 keys takes 4.5.  With
 // tiles alone as units, CTAs that hold many short blocks were the last to
 // finish (ragged prompts of 256 dimensions: 158 us, 126 with).
+constexpr int kPfMostHead = 4;
 template <int KT>
 __device__ __forceinline__ int pf_cost(int tiles) {
-    constexpr int kPfHead = KT == 64 ? 4 : 2;
+    constexpr int kPfHead = KT == 64 ? kPfMostHead : 2;
     return tiles > 0 ? tiles + kPfHead : 0;
 }
 template <int RB, int KT>
@@ -322,9 +323,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     const int cta = blockIdx.x, B = p.kv.batch;
     // ---- this CTA's run
     if (warp == 1) {
-        int total = 0;
+        int64_t units = 0;
         for (int b0 = 0; b0 < B; b0 += 32)
-            total += __reduce_add_sync(FULL, b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0);
+            units += b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0;
+        const int total = pg_total(units);
         const int ctas = min((int)gridDim.x, total);
         const int quot = ctas ? total / ctas : 0, rest = ctas ? total % ctas : 0;
         const int begin = pg_start(quot, rest, cta), end = pg_start(quot, rest, cta + 1);
@@ -1142,9 +1144,20 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, 
 // One CTA per SM, no more than there can be units of work.
 static int pf_grid(const KvView &kv, int rep) {
     const int rb = kv.dim <= 128 ? 256 : 128;
-    const int64_t units = (int64_t)kv.batch * kv.heads * (((int64_t)rep * kv.max_q + rb - 1) / rb) *
-                          (((int64_t)kv.max_kv + 63) / 64);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(units, num_sms()));
+    const double units = (double)kv.batch * kv.heads * (((int64_t)rep * kv.max_q + rb - 1) / rb) *
+                         (((int64_t)kv.max_kv + 63) / 64);
+    return units < num_sms() ? std::max((int)units, 1) : num_sms();
+}
+
+// The sequences' rows are at most those of all tokens together, and a sequence
+// with more than `split` of them has one block that may not be full.
+double paged_prefill_units(const KvView &kv, int rep, int split) {
+    if ((int64_t)rep * kv.max_q <= split) return 0.;
+    const int rb = kv.dim <= 128 ? 256 : 128, kt = kv.dim <= 128 ? 128 : 64;
+    const double rows = (double)rep * std::min((double)kv.tokens, (double)kv.batch * kv.max_q);
+    const double part = std::min((double)kv.batch, rows / (split + 1));
+    const double tiles = (double)kv.max_pages * (1 << kv.page_shift) / kt + 1 + kPfMostHead;
+    return kv.heads * (rows / rb + part) * tiles;
 }
 
 template <int BITS, int D>

@@ -417,6 +417,9 @@ int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
  *   out  bf16 [tokens, Hq, head_dim] contiguous, 16-byte aligned; rows that
  *        belong to no sequence are not written
  *   Hq a multiple of cache.heads; scale finite, usually 1/sqrt(head_dim).
+ *   The work is counted in 31 bits: heads x (batch + tokens x Hq / heads / 256)
+ *   x (page table capacity / 128 + 5), with heads of 256 four times that, has
+ *   to stay below 2e9, else GWA_ERR_UNSUPPORTED.
  *   workspace  >= gwa_sdpa_paged_workspace_bytes(...) for the same cache
  *        shape and batch bounds, 16-byte aligned; its contents are scratch.
  * Masked keys take no part whatever they hold (NaN and infinities included).

@@ -261,3 +261,14 @@ def test_rotated_queries_of_tokens_without_a_place():
     assert (append(table, none) == 0).all()
     k, v = gwa.kv_read(c.cache, none)
     assert (k == 0).all() and (v == 0).all()
+
+
+def test_a_prompt_chunk_beside_single_tokens_under_a_wide_page_table():
+    # 128 sequences, tables wide enough for a million positions each
+    rng = np.random.default_rng(38)
+    lens = [(260, 300)] + [(1, int(n)) for n in rng.integers(1, 200, 127)]
+    c = Case(38, lens, Hq=40, Hkv=8, D=64, page=4096)
+    wide = np.full((128, 256), -7, dtype=np.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    check_attention(c)

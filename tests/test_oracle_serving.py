@@ -149,3 +149,38 @@ def test_append_attend_and_sample_arguments_are_checked(lib):
     assert draw(V=0) == invalid and draw(stride=99) == invalid and draw(u=None) == invalid
     assert draw(x=ctypes.c_void_p((1 << 20) + 1)) == misaligned
     assert draw(rows=0) == 0
+
+
+def test_a_wide_page_table_beside_a_prompt_is_not_refused(lib):
+    # 128 sequences, one chunk of 2048 tokens among them, tables for 131072
+    # positions; and what passes the documented count of work
+    import group_wise_affine_gb300 as gwa
+    c, p = cache(gwa, heads=8, page_size=64), ctypes.c_void_p(1 << 20)
+    b = batch(gwa, batch=128, max_pages=2048, tokens=2175, max_q=2048, max_kv=131072)
+    assert lib.gwa_sdpa_paged_workspace_bytes(40, c, b) > 16
+    assert lib.gwa_sdpa_paged(p, 5120, 40, c, b, 0.1, 1, p, p, 16, None, None) == \
+        gwa.GWA_ERR_WORKSPACE
+    for kw in (dict(batch=1 << 20, tokens=1 << 20, max_q=1), dict(tokens=1 << 30, max_q=1 << 25)):
+        b = batch(gwa, **{**dict(batch=64, max_pages=1 << 16, max_kv=1 << 22), **kw})
+        assert lib.gwa_sdpa_paged_workspace_bytes(40, c, b) == 0
+        assert lib.gwa_sdpa_paged(p, 5120, 40, c, b, 0.1, 1, p, p, 1 << 40, None, None) == \
+            gwa.GWA_ERR_UNSUPPORTED
+        assert "units of work" in gwa.last_error()
+
+
+@pytest.mark.parametrize("dim,bits,rep", [(64, 4, 1), (128, 8, 5), (256, 4, 3), (256, 8, 16)])
+def test_batches_within_the_documented_count_of_work_pass(lib, dim, bits, rep):
+    import group_wise_affine_gb300 as gwa
+    rng = RNG(dim + rep)
+    seen = set()
+    for _ in range(3000):
+        B, H = int(2 ** rng.uniform(0, 17)), int(2 ** rng.uniform(0, 7))
+        T, mp = int(2 ** rng.uniform(0, 30)), int(2 ** rng.uniform(0, 24))
+        mq = max(1, min(T, int(2 ** rng.uniform(0, 22))))
+        c = cache(gwa, heads=H, head_dim=dim, bits=bits, page_size=64)
+        b = batch(gwa, batch=B, max_pages=mp, tokens=T, max_q=mq, max_kv=1 << 20)
+        n = H * (B + T * rep / 256) * (mp * 64 / 128 + 5) * (4 if dim == 256 else 1)
+        ok = lib.gwa_sdpa_paged_workspace_bytes(H * rep, c, b) > 0
+        assert ok or n >= 2e9, (B, H, T, mp, mq)
+        seen.add(ok)
+    assert seen == {True, False}
