@@ -691,7 +691,9 @@ def kv_read(cache: KVCache, batch: KVBatch,
 def make_sdpa_paged_workspace(cache: KVCache, batch: KVBatch,
                               Hq: int) -> torch.Tensor:
     n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.device)
+    if n == 0:
+        raise GwaError(GWA_ERR_INVALID_ARG, last_error())
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
@@ -713,6 +715,7 @@ def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
         _check_out(out, batch.tokens * Hq * D, "out")
         op = _ptr(out)
     if workspace is None:
+        # (0, on an error: the call reports it)
         n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
         workspace = _new(max(n, 16), torch.uint8, q.device, stream)
     wp, wn = _ws(workspace)

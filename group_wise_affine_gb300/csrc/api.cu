@@ -948,6 +948,7 @@ static int check_sdpa_paged(int32_t Hq, const KvView &kv, const char *fn) {
 
 size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
                                       gwa_kv_batch batch) {
+    g_last_error.clear();
     KvView kv{};
     if (check_kv(cache, batch, &kv, "gwa_sdpa_paged_workspace_bytes") ||
         check_sdpa_paged(Hq, kv, "gwa_sdpa_paged_workspace_bytes"))

@@ -434,6 +434,8 @@ int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
                    gwa_kv_cache cache, gwa_kv_batch batch, float scale,
                    int32_t causal, uint16_t *out, void *workspace,
                    size_t workspace_bytes, int32_t *status, void *stream);
+/* 0 (and gwa_last_error) for a cache, batch or Hq that gwa_sdpa_paged refuses;
+ * never 0 otherwise. */
 size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
                                       gwa_kv_batch batch);
 

@@ -184,3 +184,16 @@ def test_batches_within_the_documented_count_of_work_pass(lib, dim, bits, rep):
         assert ok or n >= 2e9, (B, H, T, mp, mq)
         seen.add(ok)
     assert seen == {True, False}
+
+
+def test_a_workspace_for_what_is_refused_is_an_error(lib):
+    from types import SimpleNamespace as S
+
+    import group_wise_affine_gb300 as gwa
+    dev = dict(device="cpu")
+    good = gwa.make_sdpa_paged_workspace(S(c=cache(gwa), **dev), S(c=batch(gwa)), 4)
+    assert good.numel() == lib.gwa_sdpa_paged_workspace_bytes(4, cache(gwa), batch(gwa)) > 0
+    for c, b, Hq in ((cache(gwa), batch(gwa), 3), (cache(gwa, bits=3), batch(gwa), 4),
+                     (cache(gwa), batch(gwa, tokens=-1), 4)):
+        with pytest.raises(gwa.GwaError, match="gwa_sdpa_paged_workspace_bytes"):
+            gwa.make_sdpa_paged_workspace(S(c=c, **dev), S(c=b), Hq)
