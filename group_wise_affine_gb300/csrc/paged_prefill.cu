@@ -168,15 +168,14 @@ __device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
     return rows > p.split ? rows : 0;
 }
 // Units of work.  A block's start and end (queries in, rows out) count as
-// kPfHead tiles in front of its own: 13 thousand cycles where a tile of 128
+// pf_head tiles in front of its own: 13 thousand cycles where a tile of 128
 // keys takes 7, with one row tile 19 where a tile of 64 keys takes 4.5.  With
 // tiles alone as units, CTAs that hold many short blocks were the last to
 // finish (ragged prompts of 256 dimensions: 158 us, 126 with).
-constexpr int kPfMostHead = 4;
+__host__ __device__ constexpr int pf_head(int kt) { return kt == 64 ? 4 : 2; }
 template <int KT>
 __device__ __forceinline__ int pf_cost(int tiles) {
-    constexpr int kPfHead = KT == 64 ? kPfMostHead : 2;
-    return tiles > 0 ? tiles + kPfHead : 0;
+    return tiles > 0 ? tiles + pf_head(KT) : 0;
 }
 template <int RB, int KT>
 __device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
@@ -1141,11 +1140,13 @@ __global__ void __launch_bounds__(256) paged_prefill_join_kernel(PagedParams p, 
     for (int x = 0; x < V; x += 2) dst[32 * (x / 2) + lane] = pack_bf16(a[x] * r, a[x + 1] * r);
 }
 
-// One CTA per SM, no more than there can be units of work.
+// One CTA per SM, no more than there can be units of work.  (No fewer than
+// there are, so that the cut, and with it the roundings, is the same for every
+// max_kv from the longest length on.)
 static int pf_grid(const KvView &kv, int rep) {
-    const int rb = kv.dim <= 128 ? 256 : 128;
+    const int rb = kv.dim <= 128 ? 256 : 128, kt = kv.dim <= 128 ? 128 : 64;
     const double units = (double)kv.batch * kv.heads * (((int64_t)rep * kv.max_q + rb - 1) / rb) *
-                         (((int64_t)kv.max_kv + 63) / 64);
+                         (((int64_t)kv.max_kv + kt - 1) / kt + pf_head(kt));
     return units < num_sms() ? std::max((int)units, 1) : num_sms();
 }
 
@@ -1156,7 +1157,7 @@ double paged_prefill_units(const KvView &kv, int rep, int split) {
     const int rb = kv.dim <= 128 ? 256 : 128, kt = kv.dim <= 128 ? 128 : 64;
     const double rows = (double)rep * std::min((double)kv.tokens, (double)kv.batch * kv.max_q);
     const double part = std::min((double)kv.batch, rows / (split + 1));
-    const double tiles = (double)kv.max_pages * (1 << kv.page_shift) / kt + 1 + kPfMostHead;
+    const double tiles = (double)kv.max_pages * (1 << kv.page_shift) / kt + 1 + pf_head(kt);
     return kv.heads * (rows / rb + part) * tiles;
 }
 

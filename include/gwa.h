@@ -336,8 +336,8 @@ typedef struct gwa_kv_cache {
  *               past the last used page are not read
  *   max_q       the most new tokens that one sequence has (a sequence with
  *               more has only its first max_q rows computed)
- *   max_kv      the longest kv_len, or more: sizes the launch, no result
- *               depends on it
+ *   max_kv      the longest kv_len, or more: sizes the launch, and no result
+ *               depends on how much more
  * Any value may be zero.  A token row that belongs to no sequence, or whose
  * position is negative or past the page table (max_pages * page_size and on),
  * has no place in the cache; attention goes over the keys that have one.

@@ -272,3 +272,21 @@ def test_a_prompt_chunk_beside_single_tokens_under_a_wide_page_table():
     wide[:, :c.table.shape[1]] = c.table
     c.table = wide
     check_attention(c)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,causal", [
+    ([(1, 900), (3, 40)], 8, 2, 128, True),
+    ([(1, 1000)], 8, 8, 64, True),
+    ([(80, 640)], 1, 1, 256, False),
+    ([(80, 640), (1, 64)], 2, 1, 128, True),
+    ([(100, 60), (90, 200), (1, 3000)], 4, 2, 256, True)])
+def test_results_do_not_depend_on_the_longest_length_given(lens, Hq, Hkv, D, causal):
+    c = Case(39, lens, Hq=Hq, Hkv=Hkv, D=D).device()
+    q = dev_bf16(rand_bf16(c.rng, c.T, c.Hq, c.D))
+    want = gwa.sdpa_paged(q, c.cache, c.batch, causal=causal)
+    for longest in (int(c.kl.max()) + 1, 4096, 100000):
+        loose = gwa.KVBatch(i32(c.q_start), i32(c.kl), i32(c.table), c.T, int(c.ql.max()), longest)
+        ws = gwa.make_sdpa_paged_workspace(c.cache, loose, Hq)
+        ws.fill_(255)
+        got = gwa.sdpa_paged(q, c.cache, loose, causal=causal, workspace=ws)
+        assert torch.equal(want, got)
