@@ -804,7 +804,8 @@ static int check_kv(const gwa_kv_cache &c, const gwa_kv_batch &b, KvView *kv,
     kv->page_table = b.page_table;
     kv->batch = b.batch;
     kv->max_pages = b.max_pages;
-    kv->max_q = b.max_q;
+    // (no sequence has more new tokens than there are)
+    kv->max_q = (int)(b.tokens < b.max_q ? b.tokens : b.max_q);
     kv->max_kv = b.max_kv;
     kv->tokens = b.tokens;
     return GWA_OK;

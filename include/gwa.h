@@ -335,7 +335,9 @@ typedef struct gwa_kv_cache {
  *               page_table[b][t / page_size], slot t mod page_size; entries
  *               past the last used page are not read
  *   max_q       the most new tokens that one sequence has (a sequence with
- *               more has only its first max_q rows computed)
+ *               more has only its first max_q rows computed); more than
+ *               tokens counts as tokens.  A looser bound may choose another
+ *               of gwa_sdpa_paged's kernels, whose last roundings differ
  *   max_kv      the longest kv_len, or more: sizes the launch, and no result
  *               depends on how much more
  * Any value may be zero.  A token row that belongs to no sequence, or whose

@@ -290,3 +290,12 @@ def test_results_do_not_depend_on_the_longest_length_given(lens, Hq, Hkv, D, cau
         ws.fill_(255)
         got = gwa.sdpa_paged(q, c.cache, loose, causal=causal, workspace=ws)
         assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("q", [1, 3])
+def test_one_sequence_does_not_depend_on_a_padded_number_of_new_tokens(q):
+    c = Case(40, [(q, 700)], Hq=8, Hkv=2).device()
+    x = dev_bf16(rand_bf16(c.rng, c.T, c.Hq, c.D))
+    want = gwa.sdpa_paged(x, c.cache, c.batch)
+    padded = gwa.KVBatch(i32(c.q_start), i32(c.kl), i32(c.table), c.T, 64, 700)
+    assert torch.equal(want, gwa.sdpa_paged(x, c.cache, padded))
