@@ -532,7 +532,20 @@ def sdpa_dequant_v(q: torch.Tensor, k: torch.Tensor, vq: torch.Tensor,
 
 
 # ------------------------------------------------------------------ serving
-class KVCache:
+class _Described:
+    """Attributes that the C structure ``c`` describes: once it is made, only
+    those named in ``_counts`` can be set, and are set in it too."""
+    _counts = ()
+
+    def __setattr__(self, name, value):
+        if "c" in self.__dict__:
+            if name not in self._counts:
+                raise AttributeError(f"{type(self).__name__}.{name} is fixed: make another")
+            setattr(self.c, name, value)
+        object.__setattr__(self, name, value)
+
+
+class KVCache(_Described):
     """A paged KV cache (gwa_kv_cache): caller-owned tensors kq, vq int32
     [pages, heads, page_size, head_dim*bits/32] and kp, vp bfloat16 [pages,
     heads, page_size, head_dim/64, 2] of (scale, bias).  ``KVCache.empty``
@@ -571,11 +584,13 @@ class KVCache:
         return cls(q(), p(), q(), p(), bits=bits)
 
 
-class KVBatch:
+class KVBatch(_Described):
     """A batch over a paged cache (gwa_kv_batch): int32 tensors q_start
     [batch + 1], kv_len [batch], page_table [batch, max_pages] on the device,
     and the host's bounds (see include/gwa.h).  The tensors are read when the
-    work runs, so a program may update them in place between steps."""
+    work runs, so a program may update them in place between steps; tokens,
+    max_q and max_kv may be set."""
+    _counts = ("tokens", "max_q", "max_kv")
 
     def __init__(self, q_start: torch.Tensor, kv_len: torch.Tensor,
                  page_table: torch.Tensor, tokens: int, max_q: int,

@@ -197,3 +197,22 @@ def test_a_workspace_for_what_is_refused_is_an_error(lib):
                      (cache(gwa), batch(gwa, tokens=-1), 4)):
         with pytest.raises(gwa.GwaError, match="gwa_sdpa_paged_workspace_bytes"):
             gwa.make_sdpa_paged_workspace(S(c=c, **dev), S(c=b), Hq)
+
+
+def test_a_batch_and_what_the_library_is_told_of_it_stay_the_same(monkeypatch):
+    import torch
+
+    import group_wise_affine_gb300 as gwa
+    monkeypatch.setattr(gwa, "_ptr", lambda t: t.data_ptr())
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    b = gwa.KVBatch(i(3), i(2), i(2, 4), tokens=9, max_q=5, max_kv=40)
+    for name, value in (("tokens", 4), ("max_q", 2), ("max_kv", 64)):
+        setattr(b, name, value)
+        assert getattr(b, name) == getattr(b.c, name) == value
+    c = gwa.KVCache.empty(2, 1, 16, 64, device="cpu")
+    for obj, name, value in ((b, "kv_len", i(2)), (b, "q_start", i(3)), (b, "page_table", i(2, 9)),
+                             (c, "kq", c.kq.clone()), (c, "heads", 2), (c, "dim", 128)):
+        was = getattr(obj, name)
+        with pytest.raises(AttributeError):
+            setattr(obj, name, value)
+        assert getattr(obj, name) is was
