@@ -108,9 +108,11 @@ struct PgSeq {
     int first, base, len, rows, nrg, nt, segs;  // base: position of the first new token
 };
 // Steps that a segment's start and end (queries, merging the warps, the
-// output) count for in runs of kPgLong steps and more; shorter runs are cut by
-// steps alone.  (64 sequences of many lengths: 82 us without, 70 with.)
-constexpr int kPgHead = 2, kPgLong = 6;
+// output) count for, where there are more steps than CTAs; else a CTA has a
+// step.  With it against without it, sequences of many lengths, u4, 32 over 8
+// heads of 128: 32 of about 400 keys 15.4 : 17.6 us, 1000 20.4 : 22.4, 4000
+// 44.2 : 45.8, 200 of about 1000 77.9 : 90.1; 64 of 2048 each 49.3 : 49.5.
+constexpr int kPgHead = 2;
 template <int NQ, int STEP>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         total += __reduce_add_sync(FULL, s.segs * s.nt);
         segs += __reduce_add_sync(FULL, s.segs);
     }
-    const int head = total / kPgLong >= (int)gridDim.x ? kPgHead : 0;
+    const int head = total > (int)gridDim.x ? kPgHead : 0;
     total += segs * head;
     // sequences without keys: their rows are zero
     for (int i = cta; i < B; i += gridDim.x) {
