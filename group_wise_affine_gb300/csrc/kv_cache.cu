@@ -25,10 +25,11 @@
 // pair; its cos and sin stay in registers for all the token's heads (reading
 // them per head would be four times the head's own bytes).  A rotated key
 // then goes through shared memory into the order of its groups, four lanes
-// each.  What the time above the bytes goes to is the instructions of the
-// quantization (about 350 of a step's 450): with 32 query heads 42 us, where
-// lanes that divide when a quotient is near a half-integer made it 78, and
-// eight values a lane with the pairs exchanged by shuffles 50.
+// each.  No unit is at its limit (issue 55%, HBM 46%): with 31% of the warps
+// resident a load's latency shows behind the quantization's instructions
+// (about 350 of a step's 450).  With 32 query heads 42 us, where lanes that
+// divide when a quotient is near a half-integer made it 78, and eight values a
+// lane with the pairs exchanged by shuffles 50.
 #include <algorithm>
 
 #include "common.cuh"

@@ -18,24 +18,24 @@
 // The centre c0 comes off by an MMA with a constant operand just before each
 // tile's codes: with it left in, an output that averages thousands of values
 // would be the small difference of two large sums (scores are summed afresh
-// for each tile and need none).  fp16 holds P' to 2^-12, bf16 only to 2^-9.
+// for each tile and need none).  fp16 holds P' to 2^-11, bf16 only to 2^-8.
 // Its range is met by powers of two: a query row is scaled so that its
 // largest element lies in [2^12, 2^13), and the value scales and biases so
 // that the largest scale, or bias / (2 c0), met so far lies in [2^5, 2^6) (the
 // accumulators are rescaled when a larger one comes, as they are for the
-// running maximum).  A product of weight
-// and scale is thus rounded to 2^-12 of itself or 2^-30 of the largest weight
-// times the largest scale; where a causal mask hides the largest from some
-// rows, to 2^-39.
+// running maximum).  A product of weight and scale is thus rounded to 2^-11 of
+// itself, or to 2^-30 of the largest weight times the largest scale met where
+// that is more; in steps that the causal mask hides from some rows to 2^-39.
 //
 // Work split.  The unit is a step of some keys (STEP) of one sequence, KV head and
 // block of up to 8 NN query rows (GQA heads x new tokens); the units of the
 // whole batch are laid end to end and cut into equal runs, one per CTA, so
 // ragged batches and single long sequences both fill the GPU.  A CTA that
 // holds a whole (sequence, head, row block) writes the output itself; the
-// pieces of one that was cut go to the workspace as (output, max, sum) and a
-// second kernel joins them.  Lengths are read from the device; nothing of
-// the split depends on host values but the grid.
+// pieces of one that was cut go to the workspace, each as its keys' mean value
+// and the logarithm of their weights' sum, and a second kernel joins them.
+// Lengths are read from the device; nothing of the split depends on host values
+// but the grid.
 //
 // A warp takes a quarter of the step (U MMA tiles of 16 keys), copies its
 // codes and parameters with cp.async into its own ring a step ahead, and
@@ -47,13 +47,15 @@
 // bound by the bytes of the cache and by unpacking codes, and their operands
 // live in registers beside the unpacking; a tcgen05 MMA has at least 64 rows.
 //
-// Measured (u4, both kernels): one token over 4096 keys of 8 heads of 128 10.7
-// us, over 131071 41.6 us (3.6 TB/s of cache); 64 sequences of up to 8192, 32
-// heads, 70 us (3.7 TB/s).  Bound: instructions.  A warp spends about 340 on
-// 16 keys of a head (128 of the MMAs, whose 8 cycles each fill half the tensor
-// pipe, the rest unpacking and softmax), issued at 2.1 a cycle and SM; the
-// bytes alone would take half the time.  Short caches are two launches and
-// their dependent reads (lengths, pages, codes).
+// Measured (u4, both kernels): one token over 4096 keys of 8 heads of 128 10.6
+// us, over 131071 42.8 us (3.5 TB/s of cache); 64 sequences of up to 8192, 32
+// heads, 70.6 us (3.7 TB/s).  No unit is at its limit: a warp spends 370
+// instructions on 16 keys of a head, 24 of them MMAs (of 8 cycles each, 29% of
+// the tensor pipe's), the rest unpacking, addresses and softmax; they are
+// issued at 2.2 a cycle and SM (55%), and the top stall is the fixed latency
+// from one to the next, with 16 warps an SM to hide it.  The bytes alone would
+// take half the time.  Short caches are two launches and their dependent reads
+// (lengths, pages, codes).
 #include <algorithm>
 #include <type_traits>
 

@@ -21,7 +21,7 @@
 // the rest of the affine map, b' = b + 8 s per group, goes into 16 further
 // columns as fp16 hi and lo parts against those of the queries' group sums.
 // (u8: scale * (code - 128) has up to 15 bits and is rounded to 11, relative
-// 2^-12; two exact parts would double the products.)  Values enter as fp16
+// 2^-11; two exact parts would double the products.)  Values enter as fp16
 // s c + b, rounded once, 2^-11 of a value, and weights as fp16.  A
 // query row is scaled by a power of two, and each tile's keys and values by
 // one each.  The keys' comes back in the row's factor f; the values' puts the
@@ -46,12 +46,12 @@
 // the kernel unwinds without hanging.
 //
 // Measured: 2048 tokens of 40 heads of 128 over 8192 keys (8 KV heads, u4, 301
-// GFLOP) 346 us, 870 TFLOP/s; ragged prompts of up to 1100 tokens, 16 heads of
-// 256 over 1733 keys, 126 us.  Bound: instructions and the latency from one
-// role to the next.  A step of 64 keys and 256 rows takes 2700 cycles; its
+// GFLOP) 354 us, 850 TFLOP/s; ragged prompts of up to 1100 tokens, 16 heads of
+// 256 over 1733 keys, 128.5 us.  Bound: instructions and the latency from one
+// role to the next.  A step of 64 keys and 256 rows takes 2750 cycles; its
 // MMAs take 1400 (those of 64 keys run at the rate of shared memory, 49
 // cycles each, the values' at the tensor cores', 64), its exponentials 1024
-// on the special-function units, and issue slots are used to 63% (39% with one
+// on the special-function units, and issue slots are used to 64% (41% with one
 // row tile).  The
 // roles' loops also displace one another in the instruction caches: rolling
 // the softmax's two passes over halves of the scores, which reads the scores

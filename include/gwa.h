@@ -343,10 +343,9 @@ typedef struct gwa_kv_cache {
  * Any value may be zero.  A token row that belongs to no sequence, or whose
  * position is negative or past the page table (max_pages * page_size and on),
  * has no place in the cache; attention goes over the keys that have one.
- * `status` (NULL, or a device int32 that the
- * caller clears) collects by atomic OR: 1 a page number outside [0,
- * num_pages), or a length past the page table; 2 a position past the rotary
- * table.  Keys and values of such a token are not written, a sequence that
+ * `status` (NULL, or a device int32 that the caller clears) collects by atomic
+ * OR: 1 a page number outside [0, num_pages), or a length past the page table;
+ * 2 a position past the rotary table.  Keys and values of such a token are not written, a sequence that
  * reads such a page gives unspecified values; no address out of range is
  * formed. */
 typedef struct gwa_kv_batch {
@@ -424,13 +423,19 @@ int gwa_kv_read(gwa_kv_cache cache, gwa_kv_batch batch, uint16_t *k,
  *   to stay below 2e9, else GWA_ERR_UNSUPPORTED.
  *   workspace  >= gwa_sdpa_paged_workspace_bytes(...) for the same cache
  *        shape and batch bounds, 16-byte aligned; its contents are scratch.
- * Masked keys take no part whatever they hold (NaN and infinities included).
- * Softmax state and sums are fp32; weights times value scales enter the value
- * product rounded to fp16, queries are exact in fp16 within 2^24 of their
- * row's largest element.  Sequences of many rows (new tokens x query heads of
- * a KV head; 33 and more, 65 with heads of 256) take values rounded to fp16,
- * and of 8-bit keys scale * (code - 128) rounded to 11 bits (2^-12 of it);
- * there a visible value that is not finite makes the whole row NaN.
+ * Masked keys take no part whatever they hold (NaN and infinities included),
+ * but a finite value far larger than those that a row sees takes part in the
+ * roundings below.  Softmax state and sums are fp32; queries are exact in fp16
+ * within 2^24 of their row's largest element (scale * q below 2^115).  Weights
+ * times value scales enter the value product in fp16, each rounded to 2^-11 of
+ * itself, or to 2^-30 of the largest weight times the largest scale (or |bias|
+ * / 2^bits) met where that is more, 2^-39 where the causal mask hides the
+ * larger from some rows.  Sequences of many rows (new tokens x query heads of a
+ * KV head; 33 and more, 65 with heads of 256) instead take weights rounded to
+ * 2^-11 of themselves or 2^-32 of the row's largest, values rounded to 2^-11 of
+ * themselves or 2^-39 of the largest near them, and of 8-bit keys scale * (code
+ * - 128) rounded to 11 bits; there a visible value that is not finite makes the
+ * whole row NaN.
  * Errors as gwa_kv_append, and GWA_ERR_WORKSPACE. */
 int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
                    gwa_kv_cache cache, gwa_kv_batch batch, float scale,
