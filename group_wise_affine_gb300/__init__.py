@@ -10,6 +10,7 @@ Names mirror the C entry points without the ``gwa_`` prefix:
 ``qmv_affine``, ``qmv_fused_sections``, ``qmv_gate_up_silu``,
 ``qmv_qkv_rope``, ``moe_qmv_gather``, ``quantize_affine``, ``sdpa_dequant_v``,
 ``rope_table``, ``kv_append``, ``kv_read``, ``sdpa_paged``, ``sample``,
+``lora_add``, ``lora_gate_up_silu``,
 ``workspace_bytes``, ``last_error``,
 ``debug_unpack``, ``debug_dequant``.
 
@@ -56,7 +57,8 @@ EXPORTS = ("gwa_qmv_affine", "gwa_qmv_fused_sections", "gwa_qmv_gate_up_silu",
            "gwa_qkv_rope_workspace_bytes", "gwa_sdpa_dequant_v",
            "gwa_sdpa_workspace_bytes", "gwa_debug_bounded_wait",
            "gwa_rope_table", "gwa_kv_append", "gwa_kv_read", "gwa_sdpa_paged",
-           "gwa_sdpa_paged_workspace_bytes", "gwa_sample")
+           "gwa_sdpa_paged_workspace_bytes", "gwa_sample", "gwa_lora_add",
+           "gwa_lora_gate_up_silu", "gwa_lora_workspace_bytes")
 
 
 class GwaError(RuntimeError):
@@ -85,6 +87,14 @@ class _KVBatch(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("batch", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("tokens", ctypes.c_int64),
                 ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
+
+
+class _Lora(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("N", ctypes.c_int64), ("K", ctypes.c_int64),
+                ("sections", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("adapters", ctypes.c_int32)]
 
 
 _lib = None
@@ -149,8 +159,14 @@ def load(path: str = LIB_PATH):
     lib.gwa_sdpa_paged_workspace_bytes.restype = sz
     lib.gwa_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp,
                                vp, vp]
+    lib.gwa_lora_add.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.gwa_lora_gate_up_silu.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz,
+                                          vp, vp]
+    lib.gwa_lora_workspace_bytes.argtypes = [_Lora, i64]
+    lib.gwa_lora_workspace_bytes.restype = sz
     for f in ("gwa_rope_table", "gwa_kv_append", "gwa_kv_read",
-              "gwa_sdpa_paged", "gwa_sample"):
+              "gwa_sdpa_paged", "gwa_sample", "gwa_lora_add",
+              "gwa_lora_gate_up_silu"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("gwa_qmv_affine", "gwa_qmv_fused_sections",
               "gwa_qmv_gate_up_silu", "gwa_moe_qmv_gather",
@@ -782,6 +798,113 @@ def sample(logits: torch.Tensor, u: torch.Tensor,
     if rc:
         _check(rc)
     return token, prob
+
+
+# ----------------------------------------------------------------- adapters
+class LoRA(_Described):
+    """Low-rank adapters of one projection (gwa_lora): caller-owned tensors a
+    bfloat16 [adapters, sections, rank, K], b bfloat16 [adapters, N, rank],
+    and optionally scale float32 and ranks int32 [adapters]."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor,
+                 scale: Optional[torch.Tensor] = None,
+                 ranks: Optional[torch.Tensor] = None):
+        if a.dim() != 4 or b.dim() != 3:
+            raise ValueError("a must be [adapters, sections, rank, K], "
+                             "b [adapters, N, rank]")
+        n, sections, rank, K = a.shape
+        _bf16(a, "a")
+        _bf16(b, "b")
+        if b.shape[0] != n or b.shape[2] != rank:
+            raise ValueError(f"b must be [{n}, N, {rank}] (got {list(b.shape)})")
+        for name, t, dtype in (("scale", scale, torch.float32),
+                               ("ranks", ranks, torch.int32)):
+            if t is not None and (t.dtype != dtype or t.numel() != n):
+                raise ValueError(f"{name} must be {dtype} [{n}]")
+        self.a, self.b, self.scale, self.ranks = a, b, scale, ranks
+        self.adapters, self.sections, self.rank = n, sections, rank
+        self.N, self.K, self.device = b.shape[1], K, a.device
+        self.c = _Lora(_ptr(a), _ptr(b), _ptr(scale), _ptr(ranks), self.N, K,
+                       sections, rank, n)
+
+
+def make_lora_workspace(lora: LoRA, M: int) -> Optional[torch.Tensor]:
+    n = int(load().gwa_lora_workspace_bytes(lora.c, M))
+    if n == 0:
+        if M == 0:
+            return None
+        raise GwaError(GWA_ERR_INVALID_ARG, last_error())
+    return torch.empty(n, dtype=torch.uint8, device=lora.device)
+
+
+def _lora_inputs(x, lora, ids, sizes, base, workspace, stream):
+    _bf16(x, "x")
+    if x.shape[-1] != lora.K:
+        raise ValueError(f"x must be [M, {lora.K}] (got {list(x.shape)})")
+    M = x.numel() // lora.K
+    if ids.dtype != torch.int32 or ids.numel() != M:
+        raise ValueError(f"ids must be int32 [{M}]")
+    if len(base) != lora.sections or sum(sizes) != lora.N:
+        raise ValueError(f"one buffer for each of {lora.sections} sections, "
+                         f"{lora.N} outputs together")
+    for i, (t, n) in enumerate(zip(base, sizes)):
+        _check_out(t, M * n, f"section {i}")
+    if workspace is None and M:
+        n = int(load().gwa_lora_workspace_bytes(lora.c, M))
+        workspace = _new(max(n, 16), torch.uint8, x.device, stream)
+    return M, workspace  # (alive until the call is enqueued)
+
+
+def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
+             ids: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
+             workspace: Optional[torch.Tensor] = None,
+             status: Optional[torch.Tensor] = None,
+             stream=None) -> List[torch.Tensor]:
+    """gwa_lora_add: ``base`` (a projection's outputs, one bfloat16 [M, size]
+    a section) plus each token's own low-rank adapter of x [M, K]; ids int32
+    [M] names it (negative: none).  ``out`` may be ``base``."""
+    sizes = [t.shape[-1] for t in base]
+    M, workspace = _lora_inputs(x, lora, ids, sizes, base, workspace, stream)
+    wp, wn = _ws(workspace)
+    if out is None:
+        out = [_new((M, n), torch.bfloat16, x.device, stream) for n in sizes]
+    if len(out) != len(sizes):
+        raise ValueError("one output per section")
+    for i, (t, n) in enumerate(zip(out, sizes)):
+        _check_out(t, M * n, f"out[{i}]")
+    n = len(sizes)
+    cs = (ctypes.c_int64 * n)(*sizes)
+    cb = (ctypes.c_void_p * n)(*[_ptr(t) for t in base])
+    co = (ctypes.c_void_p * n)(*[_ptr(t) for t in out])
+    rc = load().gwa_lora_add(_ptr(x), M, lora.c, _ptr(ids), cs, cb, co, wp, wn,
+                             _status(status), _stream(stream))
+    if rc:
+        _check(rc)
+    return list(out)
+
+
+def lora_gate_up_silu(x: torch.Tensor, gate_up: Sequence[torch.Tensor],
+                      lora: LoRA, ids: torch.Tensor,
+                      h: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      status: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """gwa_lora_gate_up_silu: h = SiLU(gate) * up, both with each token's own
+    low-rank adapter of x added; gate_up two bfloat16 [M, I]."""
+    sizes = [t.shape[-1] for t in gate_up]
+    M, workspace = _lora_inputs(x, lora, ids, sizes, gate_up, workspace, stream)
+    wp, wn = _ws(workspace)
+    if sizes[0] != sizes[1]:
+        raise ValueError("gate and up must have the same width")
+    if h is None:
+        h = _new((M, sizes[0]), torch.bfloat16, x.device, stream)
+    _check_out(h, M * sizes[0], "h")
+    rc = load().gwa_lora_gate_up_silu(
+        _ptr(x), M, lora.c, _ptr(ids), _ptr(gate_up[0]), _ptr(gate_up[1]),
+        _ptr(h), wp, wn, _status(status), _stream(stream))
+    if rc:
+        _check(rc)
+    return h
 
 
 def debug_unpack(w: QWeight, stream=None) -> torch.Tensor:

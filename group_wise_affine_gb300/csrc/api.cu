@@ -1024,6 +1024,123 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
     return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
 }
 
+// ------------------------------------------------------------ adapters
+static int check_lora(const gwa_lora &l, int64_t M, LoraParams *p, const char *fn) {
+    if (l.rank < 8 || l.rank > 128 || l.rank % 8 != 0 || l.sections < 1 ||
+        l.sections > kMaxSections)
+        return fail(GWA_ERR_UNSUPPORTED,
+                    "%s: rank=%d (a multiple of 8, 8 .. 128) sections=%d (1 .. %d)", fn,
+                    (int)l.rank, (int)l.sections, kMaxSections);
+    if (M < 0 || M > 0x7fffffffLL || l.K < 32 || l.K > (1 << 20) || l.K % 32 != 0 ||
+        l.N < 0 || l.N > 0x7fffffffLL || l.adapters < 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: M=%lld K=%lld (a multiple of 32) N=%lld adapters=%d",
+                    fn, (long long)M, (long long)l.K, (long long)l.N, (int)l.adapters);
+    p->a = l.a;
+    p->b = l.b;
+    p->scale = l.scale;
+    p->ranks = l.ranks;
+    p->N = l.N;
+    p->K = (int)l.K;
+    p->nsec = l.sections;
+    p->rank = l.rank;
+    p->adapters = l.adapters;
+    return GWA_OK;
+}
+
+size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M) {
+    g_last_error.clear();
+    LoraParams p{};
+    if (check_lora(lora, M, &p, "gwa_lora_workspace_bytes")) return 0;
+    return M == 0 ? 0 : lora_workspace_bytes(M, lora.K, lora.sections, lora.rank, lora.adapters);
+}
+
+static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *ids,
+                    void *workspace, size_t workspace_bytes, int32_t *status,
+                    void *stream, const char *fn) {
+    const int outs = p.silu ? 1 : p.nsec;
+    if (!x || !ids || (p.adapters > 0 && (!p.a || !p.b)))
+        return fail(GWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(p.a, 16) || !aligned(p.b, 16) ||
+        !aligned(p.scale, 4) || !aligned(p.ranks, 4) || !aligned(status, 4))
+        return fail(GWA_ERR_MISALIGNED, "%s: x, a, b (16 bytes), ids, scale, ranks, status (4)", fn);
+    p.vec = true;
+    p.in_place = !p.silu;
+    for (int s = 0; s < p.nsec; ++s) {
+        if (p.sec_n[s] == 0) continue;
+        if (!p.base[s] || (s < outs && !p.out[s]))
+            return fail(GWA_ERR_INVALID_ARG, "%s: null buffer of section %d", fn, s);
+        if (!aligned(p.base[s], 2) || (s < outs && !aligned(p.out[s], 2)))
+            return fail(GWA_ERR_MISALIGNED, "%s: buffer of section %d (2 bytes)", fn, s);
+        if (p.sec_n[s] % 8 || !aligned(p.base[s], 16) || (s < outs && !aligned(p.out[s], 16)))
+            p.vec = false;
+        if (s < outs && p.base[s] != p.out[s]) p.in_place = false;
+    }
+    const size_t need = lora_workspace_bytes(M, p.K, p.nsec, p.rank, p.adapters);
+    if (!workspace || workspace_bytes < need)
+        return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn,
+                    need, workspace_bytes);
+    if (!aligned(workspace, 16))
+        return fail(GWA_ERR_MISALIGNED, "%s: workspace (16 bytes)", fn);
+    const int rc = check_device();
+    if (rc) return rc;
+    p.x = x;
+    p.ids = ids;
+    p.status = status;
+    p.part = static_cast<float *>(workspace);
+    const cudaError_t e = launch_lora(p, M, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora, const int32_t *ids,
+                 const int64_t *section_sizes, const uint16_t *const *base,
+                 uint16_t *const *out, void *workspace, size_t workspace_bytes,
+                 int32_t *status, void *stream) {
+    const char *fn = "gwa_lora_add";
+    g_last_error.clear();
+    LoraParams p{};
+    int rc = check_lora(lora, M, &p, fn);
+    if (rc) return rc;
+    if (!section_sizes || !base || !out)
+        return fail(GWA_ERR_INVALID_ARG, "%s: null section arrays", fn);
+    int64_t sum = 0;
+    for (int s = 0; s < p.nsec; ++s) {
+        if (section_sizes[s] < 0 || section_sizes[s] > p.N)
+            return fail(GWA_ERR_INVALID_ARG, "%s: section %d of %lld", fn, s,
+                        (long long)section_sizes[s]);
+        p.sec_start[s] = sum;
+        p.sec_n[s] = section_sizes[s];
+        sum += section_sizes[s];
+        p.base[s] = base[s];
+        p.out[s] = out[s];
+    }
+    if (sum != p.N)
+        return fail(GWA_ERR_INVALID_ARG, "%s: sections add up to %lld, N=%lld", fn,
+                    (long long)sum, (long long)p.N);
+    if (M == 0 || p.N == 0) return GWA_OK;
+    return run_lora(p, x, M, ids, workspace, workspace_bytes, status, stream, fn);
+}
+
+int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
+                          const int32_t *ids, const uint16_t *gate,
+                          const uint16_t *up, uint16_t *h, void *workspace,
+                          size_t workspace_bytes, int32_t *status, void *stream) {
+    const char *fn = "gwa_lora_gate_up_silu";
+    g_last_error.clear();
+    LoraParams p{};
+    int rc = check_lora(lora, M, &p, fn);
+    if (rc) return rc;
+    if (p.nsec != 2 || p.N % 2 != 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: sections=%d N=%lld (two equal ones)", fn, p.nsec,
+                    (long long)p.N);
+    p.silu = true;
+    p.sec_n[0] = p.sec_n[1] = p.sec_start[1] = p.N / 2;
+    p.base[0] = gate;
+    p.base[1] = up;
+    p.out[0] = h;
+    if (M == 0 || p.N == 0) return GWA_OK;
+    return run_lora(p, x, M, ids, workspace, workspace_bytes, status, stream, fn);
+}
+
 int gwa_debug_bounded_wait(uint32_t limit_us, uint32_t *out, void *stream) {
     const char *fn = "gwa_debug_bounded_wait";
     g_last_error.clear();

@@ -118,6 +118,29 @@ struct SampleParams {
 };
 cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st);
 
+// Low-rank adapters of many requests (lora.cu).
+struct LoraParams {
+    const uint16_t *x;      // [M, K]
+    const int32_t *ids;     // [M]
+    const uint16_t *a;      // [adapters, nsec, rank, K]
+    const uint16_t *b;      // [adapters, N, rank]
+    const float *scale;     // [adapters], or NULL
+    const int32_t *ranks;   // [adapters], or NULL
+    int M, K, adapters, rank, nsec;
+    int64_t N, sec_start[kMaxSections], sec_n[kMaxSections];
+    const uint16_t *base[kMaxSections];
+    uint16_t *out[kMaxSections];  // silu: the first alone
+    bool silu, vec;         // vec: rows of 16-byte units
+    bool in_place;          // out is base: tokens without an adapter stay
+    int32_t *status;
+    float *part;            // [ks][M][nsec][rank], see lora_shrink_kernel
+    int ks;                 // shares of K
+    int steps;              // of a warp's block of outputs
+    int blocks, sec_blocks[kMaxSections];
+};
+cudaError_t launch_lora(LoraParams p, int64_t M, cudaStream_t st);
+size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters);
+
 // Launches `kernel` on `st` with programmatic stream serialization: it may
 // start while the previous kernel in the stream drains; the kernel itself
 // waits (griddepcontrol.wait) before touching anything that kernel wrote.

@@ -476,6 +476,66 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
                const int32_t *top_k, const float *top_p, const float *min_p,
                int32_t *token, float *prob, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection
+ * ("Sanctum-MLX", "File map": lora.rs merges one adapter into the weights at
+ * load; nothing is merged here, each token brings its own).  Adapter e of a
+ * projection with `sections` outputs side by side (as
+ * gwa_qmv_fused_sections; gate and up are two) holds
+ *   a  bf16 [adapters, sections, rank, K]
+ *   b  bf16 [adapters, N, rank], the sections' rows one after the other
+ *   scale  fp32 [adapters], or NULL (1)
+ *   ranks  int32 [adapters], or NULL: an adapter's own rank, 0 .. rank (a
+ *          value outside counts as the nearer end); what lies past it in a
+ *          and b is taken as zero, whatever it holds
+ * rank a multiple of 8, 8 .. 128; K a positive multiple of 32; sections 1 ..
+ * 8; adapters >= 0; a and b 16-byte aligned. */
+typedef struct gwa_lora {
+    const uint16_t *a;
+    const uint16_t *b;
+    const float *scale;
+    const int32_t *ranks;
+    int64_t N, K;
+    int32_t sections, rank, adapters;
+} gwa_lora;
+
+/* gwa_lora_add -- for every section s and token m with adapter e = ids[m]:
+ *   out_s[m,:] = base_s[m,:] + scale[e] * B_s[e] (A_s[e] x[m,:])
+ *   x     bf16 [M, K], the projection's input, 16-byte aligned
+ *   ids   int32 [M] on the device: a negative number is no adapter (out =
+ *         base); one of `adapters` and more counts as none and sets bit 1 of
+ *         `status` (NULL, or a device int32 that the caller clears)
+ *   section_sizes  host int64 [sections], adding up to N
+ *   base, out      host arrays of [M, size] bf16 buffers, 2-byte aligned
+ *         (rows of 16-byte units are read faster); out_s may be base_s, and
+ *         must not overlap anything else
+ *   workspace  >= gwa_lora_workspace_bytes(lora, M), 16-byte aligned
+ * Tokens of one adapter are computed together: up to 256 tokens in whatever
+ * order they come, of more those that follow one another.  fp32 sums of exact
+ * products; A x enters its product in two bf16 parts (2^-17 of it), and out is
+ * rounded once.  Not finite inputs make their own rows' outputs so.  Results
+ * do not depend on the other tokens of the call but through M, which may
+ * choose another order of the sums.
+ * Errors: GWA_ERR_UNSUPPORTED (rank, sections), GWA_ERR_INVALID_ARG,
+ * GWA_ERR_MISALIGNED, GWA_ERR_WORKSPACE; nothing is enqueued on error. */
+int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora,
+                 const int32_t *ids, const int64_t *section_sizes,
+                 const uint16_t *const *base, uint16_t *const *out,
+                 void *workspace, size_t workspace_bytes, int32_t *status,
+                 void *stream);
+
+/* gwa_lora_gate_up_silu -- the same for a gated projection (sections 2, N =
+ * 2 I): h = SiLU(g) * u with g and u the two sections' sums in fp32, rounded
+ * once.  gate, up, h bf16 [M, I]; h may be gate or up.  The shared halves come
+ * from gwa_qmv_fused_sections over the [gate; up] weight with sections (I, I). */
+int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
+                          const int32_t *ids, const uint16_t *gate,
+                          const uint16_t *up, uint16_t *h, void *workspace,
+                          size_t workspace_bytes, int32_t *status,
+                          void *stream);
+/* 0 (and gwa_last_error) for adapters or M that the calls refuse, and for M = 0. */
+size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M);
+
 /* Text of the last error raised on this thread ("" if none). */
 const char *gwa_last_error(void);
 

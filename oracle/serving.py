@@ -126,3 +126,21 @@ def sample_masses(x: np.ndarray, T: float) -> np.ndarray:
         return (x > -np.inf).astype(np.float64)
     with np.errstate(over="ignore"):
         return np.exp((x - m) / T)
+
+
+def lora(x, base, a, b, ids, scale=None, ranks=None):
+    """fp64 outputs [M, N]: base [M, N] plus scale B (A x) of each token's
+    adapter; a [adapters, sections, rank, K], b [adapters, N, rank], the
+    sections of N given by ``base``'s list of arrays."""
+    n = [t.shape[1] for t in base]
+    out = [t.copy() for t in base]
+    for m, e in enumerate(ids):
+        if not 0 <= e < a.shape[0]:
+            continue
+        r = a.shape[2] if ranks is None else min(max(int(ranks[e]), 0), a.shape[2])
+        at = 0
+        for s, size in enumerate(n):
+            t = a[e, s, :r] @ x[m]
+            out[s][m] += (1.0 if scale is None else float(scale[e])) * (b[e, at:at + size, :r] @ t)
+            at += size
+    return out
