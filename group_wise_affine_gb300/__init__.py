@@ -57,7 +57,8 @@ EXPORTS = ("gwa_qmv_affine", "gwa_qmv_fused_sections", "gwa_qmv_gate_up_silu",
            "gwa_qkv_rope_workspace_bytes", "gwa_sdpa_dequant_v",
            "gwa_sdpa_workspace_bytes", "gwa_debug_bounded_wait",
            "gwa_rope_table", "gwa_kv_append", "gwa_kv_read", "gwa_sdpa_paged",
-           "gwa_sdpa_paged_workspace_bytes", "gwa_sample", "gwa_lora_add",
+           "gwa_sdpa_paged_workspace_bytes", "gwa_sdpa_paged_window",
+           "gwa_sdpa_paged_window_workspace_bytes", "gwa_sample", "gwa_lora_add",
            "gwa_lora_gate_up_silu", "gwa_lora_workspace_bytes")
 
 
@@ -157,6 +158,12 @@ def load(path: str = LIB_PATH):
                                    ctypes.c_float, i32, vp, vp, sz, vp, vp]
     lib.gwa_sdpa_paged_workspace_bytes.argtypes = [i32, _KVCache, _KVBatch]
     lib.gwa_sdpa_paged_workspace_bytes.restype = sz
+    lib.gwa_sdpa_paged_window.argtypes = [vp, i64, i32, _KVCache, _KVBatch,
+                                          ctypes.c_float, i32, i32, vp, vp, sz,
+                                          vp, vp]
+    lib.gwa_sdpa_paged_window_workspace_bytes.argtypes = [i32, _KVCache,
+                                                          _KVBatch, i32, i32]
+    lib.gwa_sdpa_paged_window_workspace_bytes.restype = sz
     lib.gwa_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp,
                                vp, vp]
     lib.gwa_lora_add.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz, vp, vp]
@@ -165,7 +172,7 @@ def load(path: str = LIB_PATH):
     lib.gwa_lora_workspace_bytes.argtypes = [_Lora, i64]
     lib.gwa_lora_workspace_bytes.restype = sz
     for f in ("gwa_rope_table", "gwa_kv_append", "gwa_kv_read",
-              "gwa_sdpa_paged", "gwa_sample", "gwa_lora_add",
+              "gwa_sdpa_paged", "gwa_sdpa_paged_window", "gwa_sample", "gwa_lora_add",
               "gwa_lora_gate_up_silu"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("gwa_qmv_affine", "gwa_qmv_fused_sections",
@@ -719,9 +726,17 @@ def kv_read(cache: KVCache, batch: KVBatch,
     return k, v
 
 
-def make_sdpa_paged_workspace(cache: KVCache, batch: KVBatch,
-                              Hq: int) -> torch.Tensor:
-    n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
+def _sdpa_paged_bytes(cache, batch, Hq, window, sinks) -> int:
+    if window is None:
+        return int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
+    return int(load().gwa_sdpa_paged_window_workspace_bytes(
+        Hq, cache.c, batch.c, window, sinks))
+
+
+def make_sdpa_paged_workspace(cache: KVCache, batch: KVBatch, Hq: int,
+                              window: Optional[int] = None,
+                              sinks: int = 0) -> torch.Tensor:
+    n = _sdpa_paged_bytes(cache, batch, Hq, window, sinks)
     if n == 0:
         raise GwaError(GWA_ERR_INVALID_ARG, last_error())
     return torch.empty(n, dtype=torch.uint8, device=cache.device)
@@ -732,9 +747,16 @@ def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
                out: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None,
                status: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
+               stream=None, window: Optional[int] = None,
+               sinks: int = 0) -> torch.Tensor:
     """gwa_sdpa_paged: softmax attention of q [tokens, Hq, head_dim] (tokens
-    may be strided) over the paged cache; bfloat16 [tokens, Hq, head_dim]."""
+    may be strided) over the paged cache; bfloat16 [tokens, Hq, head_dim].
+    With ``window`` gwa_sdpa_paged_window: a token sees that many keys up to
+    its own, and the first ``sinks`` ones."""
+    if window is None and sinks:
+        raise ValueError("sinks are first keys beside a window")
+    if window is not None and not causal:
+        raise ValueError("a window is causal")
     if q.dim() != 3:
         raise ValueError("q must be [tokens, Hq, head_dim]")
     Hq, D = q.shape[1], cache.dim
@@ -747,13 +769,19 @@ def sdpa_paged(q: torch.Tensor, cache: KVCache, batch: KVBatch,
         op = _ptr(out)
     if workspace is None:
         # (0, on an error: the call reports it)
-        n = int(load().gwa_sdpa_paged_workspace_bytes(Hq, cache.c, batch.c))
+        n = _sdpa_paged_bytes(cache, batch, Hq, window, sinks)
         workspace = _new(max(n, 16), torch.uint8, q.device, stream)
     wp, wn = _ws(workspace)
-    rc = load().gwa_sdpa_paged(
-        qp, qs, Hq, cache.c, batch.c,
-        1.0 / float(D) ** 0.5 if scale is None else scale,
-        1 if causal else 0, op, wp, wn, _status(status), _stream(stream))
+    if scale is None:
+        scale = 1.0 / float(D) ** 0.5
+    if window is None:
+        rc = load().gwa_sdpa_paged(
+            qp, qs, Hq, cache.c, batch.c, scale, 1 if causal else 0, op, wp, wn,
+            _status(status), _stream(stream))
+    else:
+        rc = load().gwa_sdpa_paged_window(
+            qp, qs, Hq, cache.c, batch.c, scale, window, sinks, op, wp, wn,
+            _status(status), _stream(stream))
     if rc:
         _check(rc)
     return out

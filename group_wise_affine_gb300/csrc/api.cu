@@ -954,15 +954,35 @@ size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
     if (check_kv(cache, batch, &kv, "gwa_sdpa_paged_workspace_bytes") ||
         check_sdpa_paged(Hq, kv, "gwa_sdpa_paged_workspace_bytes"))
         return 0;
-    return sdpa_paged_workspace_bytes(Hq, kv);
+    return sdpa_paged_workspace_bytes(Hq, kv, 0, 0);
 }
 
-int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
-                   gwa_kv_cache cache, gwa_kv_batch batch, float scale,
-                   int32_t causal, uint16_t *out, void *workspace,
-                   size_t workspace_bytes, int32_t *status, void *stream) {
-    const char *fn = "gwa_sdpa_paged";
+// A window that reaches from every position to the first key is any that is
+// longer than positions go.
+static int check_window(int64_t window, int64_t sinks, const char *fn) {
+    if (window < 1 || sinks < 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: window=%lld sinks=%lld", fn, (long long)window,
+                    (long long)sinks);
+    return GWA_OK;
+}
+
+size_t gwa_sdpa_paged_window_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
+                                             gwa_kv_batch batch, int32_t window,
+                                             int32_t sinks) {
+    const char *fn = "gwa_sdpa_paged_window_workspace_bytes";
     g_last_error.clear();
+    KvView kv{};
+    if (check_kv(cache, batch, &kv, fn) || check_sdpa_paged(Hq, kv, fn) ||
+        check_window(window, sinks, fn))
+        return 0;
+    return sdpa_paged_workspace_bytes(Hq, kv, window, sinks);
+}
+
+static int run_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                          gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                          int32_t causal, int32_t window, int32_t sinks,
+                          uint16_t *out, void *workspace, size_t workspace_bytes,
+                          int32_t *status, void *stream, const char *fn) {
     KvView kv{};
     int rc = check_kv(cache, batch, &kv, fn);
     if (rc) return rc;
@@ -974,16 +994,38 @@ int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
     if ((rc = check_rows(q, q_stride, row, "q", fn))) return rc;
     if ((rc = check_rows(out, row, row, "out", fn))) return rc;
     if (!aligned(status, 4)) return fail(GWA_ERR_MISALIGNED, "%s: status (4 bytes)", fn);
-    const size_t need = sdpa_paged_workspace_bytes(Hq, kv);
+    const size_t need = sdpa_paged_workspace_bytes(Hq, kv, window, sinks);
     if (!workspace || workspace_bytes < need)
         return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn,
                     need, workspace_bytes);
     if (!aligned(workspace, 16))
         return fail(GWA_ERR_MISALIGNED, "%s: workspace alignment", fn);
     if ((rc = check_device())) return rc;
-    cudaError_t e = launch_sdpa_paged(q, q_stride, Hq, kv, scale, causal ? 1 : 0, out,
-                                      workspace, status, static_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_sdpa_paged(q, q_stride, Hq, kv, scale, causal ? 1 : 0, window, sinks,
+                                      out, workspace, status, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
+int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                   gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                   int32_t causal, uint16_t *out, void *workspace,
+                   size_t workspace_bytes, int32_t *status, void *stream) {
+    g_last_error.clear();
+    return run_sdpa_paged(q, q_stride, Hq, cache, batch, scale, causal, 0, 0, out, workspace,
+                          workspace_bytes, status, stream, "gwa_sdpa_paged");
+}
+
+int gwa_sdpa_paged_window(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                          gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                          int32_t window, int32_t sinks, uint16_t *out,
+                          void *workspace, size_t workspace_bytes,
+                          int32_t *status, void *stream) {
+    const char *fn = "gwa_sdpa_paged_window";
+    g_last_error.clear();
+    const int rc = check_window(window, sinks, fn);
+    if (rc) return rc;
+    return run_sdpa_paged(q, q_stride, Hq, cache, batch, scale, 1, window, sinks, out, workspace,
+                          workspace_bytes, status, stream, fn);
 }
 
 int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,

@@ -100,9 +100,9 @@ cudaError_t launch_kv_read(const KvView &kv, uint16_t *k, uint16_t *v,
 // Attention over the paged cache (paged_attention.cu).
 cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
                               const KvView &kv, float scale, int causal,
-                              uint16_t *out, void *workspace, int32_t *status,
-                              cudaStream_t st);
-size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv);
+                              int window, int sinks, uint16_t *out,
+                              void *workspace, int32_t *status, cudaStream_t st);
+size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv, int window, int sinks);
 // The most units of work that either of its kernels can find in such a batch.
 double sdpa_paged_units(int Hq, const KvView &kv);
 unsigned int prefill_timeouts(bool reset);  // paged_prefill.cu

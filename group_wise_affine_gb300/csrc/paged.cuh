@@ -28,6 +28,9 @@ struct PagedParams {
     KvView kv;
     float scale;
     int causal;
+    // 0, or (with causal) a token at position i sees the keys from i - window
+    // + 1 on, and those below sinks
+    int window, sinks;
     uint16_t *out;    // [tokens, Hq, dim]
     PgCut *cuts;      // what the join has to do
     int segs;         // (KV head, row block) pairs of a sequence, at most
@@ -46,6 +49,16 @@ __device__ __forceinline__ int pg_start(int quot, int rest, int c) {
 __device__ __forceinline__ int pg_owner(int quot, int rest, int unit) {
     const int big = rest * (quot + 1);
     return unit < big ? unit / (quot + 1) : rest + (unit - big) / quot;
+}
+
+// The first key of the window that ends with position `last`.
+__device__ __forceinline__ int pg_low(const PagedParams &p, int64_t last) {
+    return (int)max((int64_t)0, last + 1 - p.window);
+}
+// Whether no row takes part in any of the keys [key, key + n) through its
+// window, where the rows' first window starts at `low`, nor as first keys.
+__device__ __forceinline__ bool pg_hidden(const PagedParams &p, int key, int n, int low) {
+    return key + n <= low && key >= p.sinks;
 }
 
 // A total over the lanes of values whose own sums fit: as an int, or 0 if it

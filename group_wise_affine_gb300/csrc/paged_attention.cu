@@ -108,6 +108,19 @@ struct PgLayout {
 // (KV head and row block) with keys.
 struct PgSeq {
     int first, base, len, rows, nrg, nt, segs;  // base: position of the first new token
+    // with a window: steps [full, end) are inside every row's, [low, full)
+    // the windows' starts, and `first_keys` the ones in front of low that hold
+    // first keys
+    int full, low, end, first_keys;
+    // the step of the keys, of step j of nt: those that every row sees whole
+    // come first, so that the wider roundings of the others (see compute) do
+    // not reach them
+    template <bool WIN>
+    __device__ __forceinline__ int at(int j) const {
+        if (!WIN) return j;
+        if (j < end - full) return full + j;
+        return j < end - low ? j - (end - full) + low : j - (end - low);
+    }
 };
 // Steps that a segment's start and end (queries, merging the warps, the
 // output) count for, where there are more steps than CTAs; else a CTA has a
@@ -115,7 +128,7 @@ struct PgSeq {
 // heads of 128: 32 of about 400 keys 15.4 : 17.6 us, 1000 20.4 : 22.4, 4000
 // 44.2 : 45.8, 200 of about 1000 77.9 : 90.1; 64 of 2048 each 49.3 : 49.5.
 constexpr int kPgHead = 2;
-template <int NQ, int STEP>
+template <int NQ, int STEP, bool WIN>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     PgSeq r;
@@ -126,6 +139,15 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     if (r.rows > p.split) r.rows = 0;  // the prompt kernel's
     r.nrg = (r.rows + NQ - 1) / NQ;
     r.nt = (s.len + STEP - 1) / STEP;
+    if constexpr (WIN) {
+        const int n = min(s.count, p.kv.max_q);
+        const int seen = max(0, min(s.len, r.base + n));
+        r.end = (seen + STEP - 1) / STEP;
+        r.low = min(pg_low(p, r.base) / STEP, r.end);
+        r.full = min((pg_low(p, (int64_t)r.base + n - 1) + STEP - 1) / STEP, r.end);
+        r.first_keys = min((min(p.sinks, seen) + STEP - 1) / STEP, r.low);
+        r.nt = r.end - r.low + r.first_keys;
+    }
     r.segs = r.nt > 0 ? p.kv.heads * r.nrg : 0;  // (times nt: the entry point keeps the total below 2^31)
     return r;
 }
@@ -178,7 +200,7 @@ __device__ __forceinline__ void row_scale(float t, float &up, float &down) {
     down = __uint_as_float((uint32_t)(127 - p) << 23);
 }
 
-template <int BITS, int D, int NN>
+template <int BITS, int D, int NN, bool WIN>
 __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     paged_decode_kernel(PagedParams p) {
     using L = PgLayout<BITS, D, NN>;
@@ -195,6 +217,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     __shared__ float s_b[kPgWarps][NQ][G];
     __shared__ float s_den[NQ];
     __shared__ uint4 s_q[NN][G][2][kWarp];
+    __shared__ int s_low[WIN ? NQ : 1];  // where the rows' windows start
 
     const int lane = threadIdx.x & (kWarp - 1), warp = threadIdx.x / kWarp;
     const int g = lane >> 2, t = lane & 3;
@@ -220,7 +243,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     int total = 0, segs = 0;
     for (int b0 = 0; b0 < B; b0 += kWarp) {
         PgSeq s{};
-        if (b0 + lane < B) s = pg_seq<NQ, STEP>(p, b0 + lane);
+        if (b0 + lane < B) s = pg_seq<NQ, STEP, WIN>(p, b0 + lane);
         total += __reduce_add_sync(FULL, s.segs * s.nt);
         segs += __reduce_add_sync(FULL, s.segs);
     }
@@ -228,7 +251,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     total += segs * head;
     // sequences without keys: their rows are zero
     for (int i = cta; i < B; i += gridDim.x) {
-        const PgSeq s = pg_seq<NQ, STEP>(p, i);
+        const PgSeq s = pg_seq<NQ, STEP, WIN>(p, i);
         if (p.status && threadIdx.x == 0 && kv_past(kv_seq(p.kv, i)))
             atomicOr(p.status, (int)kKvBadPage);
         if (p.by_seg)
@@ -248,7 +271,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     int b = 0, at = 0;  // the sequence of the run's first unit, units before it
     for (int b0 = 0; b0 < B; b0 += kWarp) {
         PgSeq s{};
-        if (b0 + lane < B) s = pg_seq<NQ, STEP>(p, b0 + lane);
+        if (b0 + lane < B) s = pg_seq<NQ, STEP, WIN>(p, b0 + lane);
         const int u = s.segs * (s.nt + head);
         int incl = u;
 #pragma unroll
@@ -265,7 +288,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         }
         at += __shfl_sync(FULL, incl, kWarp - 1);
     }
-    PgSeq sq = pg_seq<NQ, STEP>(p, b);
+    PgSeq sq = pg_seq<NQ, STEP, WIN>(p, b);
     int cur = begin;
     int piece = 0;
     const float sl2 = p.scale * 1.4426950408889634f;  // scores in base 2
@@ -281,7 +304,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             // (never past the batch, unless the lengths change meanwhile)
             if (b + 1 >= B) break;
             at += sq.segs * cost;
-            sq = pg_seq<NQ, STEP>(p, ++b);
+            sq = pg_seq<NQ, STEP, WIN>(p, ++b);
             continue;
         }
         const int seg = (cur - at) / cost;  // hk * nrg + rg
@@ -360,6 +383,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                                         : sq.len;
             }
         }
+        if (WIN && threadIdx.x < NQ)
+            s_low[threadIdx.x] = pg_low(p, (int64_t)sq.base + (rg * NQ + (int)threadIdx.x) / p.rep);
         __syncthreads();
         // every row of the block sees the keys below `all`, none those from
         // `seen` on
@@ -370,6 +395,11 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
             for (int h = 0; h < 2; ++h) all = min(all, lim[nn][h]);
+        // with a window: the block's first row's starts at `low`
+        const int low = WIN ? pg_low(p, (int64_t)sq.base + rg * NQ / p.rep) : 0;
+        auto gone = [&](int key, int n) {  // no row of the block sees them
+            return key >= sq.len || (WIN && pg_hidden(p, key, n, low));
+        };
         if (nlive < NQ) {  // padding rows: masked or not, they are never written
             all = p.causal ? max(0, min(sq.len, sq.base + rg * NQ / p.rep + 1)) : sq.len;
         } else {
@@ -399,9 +429,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         auto issue = [&](int step, int to) {
             if (step - pages_at >= 32 / U) {
                 pages_at = step;
-                const int key = (step + lane / U) * STEP + warp * KEYS + lane % U * 16;
+                const int key = sq.at<WIN>(step + lane / U) * STEP + warp * KEYS + lane % U * 16;
                 pages = 0;
-                if (step + lane / U < tb && key < sq.len) {
+                if (step + lane / U < tb && !gone(key, 16)) {
                     pages = table[key >> p.kv.page_shift];
                     if ((unsigned)pages >= (unsigned)p.kv.num_pages) {
                         if (p.status) atomicOr(p.status, (int)kKvBadPage);
@@ -413,8 +443,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int page = __shfl_sync(FULL, pages, U * (step - pages_at) + u);
-                const int key = step * STEP + warp * KEYS + u * 16;
-                if (key >= sq.len) break;  // warp-uniform
+                const int key = sq.at<WIN>(step) * STEP + warp * KEYS + u * 16;
+                if (gone(key, 16)) continue;  // warp-uniform
                 const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
                                     (key & pmask);
                 const uint4 *ks = reinterpret_cast<const uint4 *>(p.kv.kq) + row * RCH + lane;
@@ -447,6 +477,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         // weights stay at 1 there instead of 2^8, and scales go up to 2^15
         // instead of 2^6, so that keys of 2^24 times smaller scales keep their
         // place in fp16.  (Such steps are the segment's last ones.)
+        auto masked = [&](int key, int nn, int h) {
+            if (key >= lim[nn][h]) return true;
+            return WIN && key >= p.sinks && key < s_low[WIN ? 8 * nn + 2 * t + h : 0];
+        };
         auto compute = [&](const unsigned char *stg, const int key0, auto edge_t) {
             constexpr bool EDGE = decltype(edge_t)::value;
             // ---- scores: x[u][kk][nn][h] of key key0 + 16 u + HALF kk + kv_g,
@@ -504,7 +538,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 e[u][kk][nn][h] = ex2(fmaf(x[u][kk][nn][h], fac[nn][h], -m[nn][h]));
-                                if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= lim[nn][h])
+                                if (EDGE && masked(key0 + 16 * u + 8 * kk + kv_g, nn, h))
                                     e[u][kk][nn][h] = 0.f;
                             }
             };
@@ -528,7 +562,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         for (int u = 0; u < U; ++u)
 #pragma unroll
                             for (int kk = 0; kk < 2; ++kk)
-                                if (!EDGE || key0 + 16 * u + 8 * kk + kv_g < lim[nn][h])
+                                if (!EDGE || !masked(key0 + 16 * u + 8 * kk + kv_g, nn, h))
                                     mt = fmaxf(mt, x[u][kk][nn][h] * fac[nn][h]);
 #pragma unroll
                         for (int off = 4; off < kWarp; off <<= 1)
@@ -563,7 +597,8 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                         w = *reinterpret_cast<const uint32_t *>(stg + L::VP_OFF + u * L::PB +
                                                                 ((kv_g + 8 * kk) * G + gg) * 4);
                         // past the end lie no parameters (but anything)
-                        if (EDGE && key0 + 16 * u + 8 * kk + kv_g >= seen) w = 0u;
+                        const int key = key0 + 16 * u + 8 * kk + kv_g;
+                        if (EDGE && (key >= seen || (WIN && pg_hidden(p, key, 1, low)))) w = 0u;
                         smax = fmaxf(smax, fabsf(bf16_lo(w)));
                         // (the bias, and the scale's bits below its last place)
                         bmax = fmaxf(bmax, fabsf(__uint_as_float(w)));
@@ -696,10 +731,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             cp_async_commit();
             cp_async_wait<S - 1>();
             __syncwarp();
-            const int key0 = step * STEP + warp * KEYS;
-            if (key0 < sq.len) {  // warp-uniform
+            const int key0 = sq.at<WIN>(step) * STEP + warp * KEYS;
+            if (!gone(key0, KEYS)) {  // warp-uniform
                 const unsigned char *stg = wsm + stage * L::STAGE;
-                if (key0 + KEYS > all)
+                if (key0 + KEYS > all || (WIN && step >= sq.end - sq.full))
                     compute(stg, key0, std::true_type{});
                 else
                     compute(stg, key0, std::false_type{});
@@ -902,23 +937,27 @@ static int pg_nn(int64_t rows, int D) {
 }
 
 template <int BITS, int D, int NN>
-static int pg_grid(const KvView &kv, int64_t rows) {
+static int pg_grid(const KvView &kv, int64_t rows, int window, int sinks) {
     using L = PgLayout<BITS, D, NN>;
-    const double units = (double)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) *
-                         (((int64_t)kv.max_kv + L::STEP - 1) / L::STEP);
+    int64_t steps = ((int64_t)kv.max_kv + L::STEP - 1) / L::STEP;
+    // (keys anywhere touch one step more than they fill)
+    if (window)
+        steps = std::min(steps, ((int64_t)window + kv.max_q - 1 + L::STEP - 1) / L::STEP + 1 +
+                                    ((int64_t)sinks + L::STEP - 1) / L::STEP);
+    const double units = (double)kv.batch * kv.heads * ((rows + L::NQ - 1) / L::NQ) * steps;
     const int full = std::min(num_sms() * L::CTAS, kPgMaxCtas);
     return units < full ? std::max((int)units, 1) : full;
 }
 
-template <int BITS, int D, int NN>
+template <int BITS, int D, int NN, bool WIN>
 static cudaError_t launch_pg_t(PagedParams p, void *workspace, cudaStream_t st) {
     using L = PgLayout<BITS, D, NN>;
-    const void *kfn = reinterpret_cast<const void *>(paged_decode_kernel<BITS, D, NN>);
+    const void *kfn = reinterpret_cast<const void *>(paged_decode_kernel<BITS, D, NN, WIN>);
     cudaError_t e = allow_smem(kfn, L::BYTES);
     if (e == cudaSuccess) e = prefer_max_shared(kfn);
     if (e != cudaSuccess) return e;
     const int64_t rows = std::min<int64_t>((int64_t)p.rep * p.kv.max_q, p.split);
-    const int grid = pg_grid<BITS, D, NN>(p.kv, rows);
+    const int grid = pg_grid<BITS, D, NN>(p.kv, rows, p.window, p.sinks);
     p.cuts = static_cast<PgCut *>(workspace);
     p.part = reinterpret_cast<float *>(p.cuts + kPgMaxCtas);
     const int64_t nrg = (rows + L::NQ - 1) / L::NQ;
@@ -974,14 +1013,14 @@ double sdpa_paged_units(int Hq, const KvView &kv) {
     return std::max(few, paged_prefill_units(kv, rep, split));
 }
 
-size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {
+size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv, int window, int sinks) {
     const int rep = Hq / kv.heads, split = pg_split(kv, rep);
     const int64_t rows = std::min<int64_t>((int64_t)rep * kv.max_q, split);
     const int nn = pg_nn(rows, kv.dim);
     size_t few = 0;
 #define GWA_PG(BB, DD, N)                                                              \
     if (kv.bits == BB && kv.dim == DD && nn == N)                                      \
-        few = (size_t)pg_grid<BB, DD, N>(kv, rows) * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
+        few = (size_t)pg_grid<BB, DD, N>(kv, rows, window, sinks) * 2 * 8 * nn * (kv.dim + 4) * sizeof(float);
     GWA_PG_ALL(GWA_PG)
 #undef GWA_PG
     const size_t many =
@@ -991,7 +1030,7 @@ size_t sdpa_paged_workspace_bytes(int Hq, const KvView &kv) {
 
 cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
                               const KvView &kv, float scale, int causal,
-                              uint16_t *out, void *workspace, int32_t *status,
+                              int window, int sinks, uint16_t *out, void *workspace, int32_t *status,
                               cudaStream_t st) {
     PagedParams p{};
     p.q = q;
@@ -1001,6 +1040,8 @@ cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
     p.kv = kv;
     p.scale = scale;
     p.causal = causal;
+    p.window = window;
+    p.sinks = sinks;
     p.out = out;
     p.status = status;
     p.split = pg_split(kv, p.rep);
@@ -1010,7 +1051,9 @@ cudaError_t launch_sdpa_paged(const uint16_t *q, int64_t q_stride, int Hq,
         const int nn = pg_nn(std::min<int64_t>(all, p.split), kv.dim);
         e = cudaErrorInvalidValue;
 #define GWA_PG(BB, DD, N) \
-    if (kv.bits == BB && kv.dim == DD && nn == N) e = launch_pg_t<BB, DD, N>(p, workspace, st);
+    if (kv.bits == BB && kv.dim == DD && nn == N)                          \
+        e = window ? launch_pg_t<BB, DD, N, true>(p, workspace, st)        \
+                   : launch_pg_t<BB, DD, N, false>(p, workspace, st);
         GWA_PG_ALL(GWA_PG)
 #undef GWA_PG
     }

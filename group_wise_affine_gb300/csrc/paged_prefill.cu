@@ -156,11 +156,28 @@ struct PfCursor {
     int rows, nrb;
 };
 
-// Keys that rows [rb * RB, ...) of a sequence see, in tiles of KT.
-template <int RB, int KT>
-__device__ __forceinline__ int pf_tiles(const PagedParams &p, const KvSeq &s, int rows, int rb) {
+// Keys that rows [rb * RB, ...) of a sequence see, in tiles of KT.  With a
+// window: the tiles up to `first_keys` that hold first keys, then those from
+// `skip` further on, where the first row's window starts (key `low`).
+struct PfTiles {
+    int n, first_keys, skip, low;
+};
+template <int RB, int KT, bool WIN>
+__device__ __forceinline__ PfTiles pf_span(const PagedParams &p, const KvSeq &s, int rows, int rb) {
     const int seen = kv_seen(s, (min(rows, (rb + 1) * RB) - 1) / p.rep, p.causal);
-    return seen > 0 ? (seen + KT - 1) / KT : 0;
+    PfTiles r{seen > 0 ? (seen + KT - 1) / KT : 0, 0, 0, 0};
+    if constexpr (WIN) {
+        r.low = pg_low(p, (int64_t)s.end - s.count + rb * RB / p.rep);
+        const int from = min(r.low / KT, r.n);
+        r.first_keys = min((min(p.sinks, max(seen, 0)) + KT - 1) / KT, from);
+        r.skip = from - r.first_keys;
+        r.n -= r.skip;
+    }
+    return r;
+}
+template <int RB, int KT, bool WIN>
+__device__ __forceinline__ int pf_tiles(const PagedParams &p, const KvSeq &s, int rows, int rb) {
+    return pf_span<RB, KT, WIN>(p, s, rows, rb).n;
 }
 template <int RB>
 __device__ __forceinline__ int pf_rows(const PagedParams &p, const KvSeq &s) {
@@ -177,14 +194,14 @@ template <int KT>
 __device__ __forceinline__ int pf_cost(int tiles) {
     return tiles > 0 ? tiles + pf_head(KT) : 0;
 }
-template <int RB, int KT>
+template <int RB, int KT, bool WIN>
 __device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
     const int rows = pf_rows<RB>(p, s);
     const int nrb = (rows + RB - 1) / RB;
     if (!p.causal) return p.kv.heads * nrb * pf_cost<KT>((s.len + KT - 1) / KT);
     int n = 0;
-    for (int rb = 0; rb < nrb; ++rb) n += pf_cost<KT>(pf_tiles<RB, KT>(p, s, rows, rb));
+    for (int rb = 0; rb < nrb; ++rb) n += pf_cost<KT>(pf_tiles<RB, KT, WIN>(p, s, rows, rb));
     return p.kv.heads * n;
 }
 
@@ -192,11 +209,17 @@ __device__ __forceinline__ int pf_units(const PagedParams &p, int b) {
 struct PfPiece {
     int b, hk, rb, ta, tb, nt, rows, last;
     KvSeq s;
+    PfTiles t;
+    // the tile of the keys, of tile j of nt
+    template <bool WIN>
+    __device__ __forceinline__ int at(int j) const {
+        return WIN && j >= t.first_keys ? j + t.skip : j;
+    }
 };
-template <int RB, int KT>
+template <int RB, int KT, bool WIN>
 __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece &w) {
     while (c.left > 0) {
-        int nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
+        int nt = pf_tiles<RB, KT, WIN>(p, c.s, c.rows, c.rb);
         while (c.unit >= pf_cost<KT>(nt)) {  // the next block that sees a key
             c.unit = 0;
             if (++c.rb >= c.nrb) {
@@ -212,7 +235,7 @@ __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece 
                     } while (c.nrb == 0);
                 }
             }
-            nt = pf_tiles<RB, KT>(p, c.s, c.rows, c.rb);
+            nt = pf_tiles<RB, KT, WIN>(p, c.s, c.rows, c.rb);
         }
         const int cost = pf_cost<KT>(nt), head = cost - nt;
         const int from = c.unit, to = min(cost, from + c.left);
@@ -229,21 +252,22 @@ __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece 
         w.nt = nt;
         w.rows = c.rows;
         w.s = c.s;
+        if (WIN) w.t = pf_span<RB, KT, WIN>(p, c.s, c.rows, c.rb);
         return true;
     }
     return false;
 }
 
 // Rows (of one head) of a tile's 16-key blocks, on the first lanes.
-template <int KT>
+template <int KT, bool WIN>
 struct PfPages {
     const PagedParams &p;
-    int len, tb, hk, b;
+    const PfPiece &w;
     __device__ __forceinline__ int64_t look(int tile, int lane) const {
-        const int key = tile * KT + lane * 16;
+        const int key = w.at<WIN>(tile) * KT + lane * 16, hk = w.hk;
         int pg = 0;
-        if (tile < tb && lane < KT / 16 && key < len) {
-            pg = p.kv.page_table[(int64_t)b * p.kv.max_pages + (key >> p.kv.page_shift)];
+        if (tile < w.tb && lane < KT / 16 && key < w.s.len && !(WIN && pg_hidden(p, key, 16, w.t.low))) {
+            pg = p.kv.page_table[(int64_t)w.b * p.kv.max_pages + (key >> p.kv.page_shift)];
             if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
                 if (p.status) atomicOr(p.status, (int)kKvBadPage);
                 pg = 0;
@@ -256,11 +280,11 @@ struct PfPages {
 
 // The next piece of a warp's own walk through the run, in shared memory (the
 // walk is the same for every warp; registers are short).
-template <int RB, int KT>
+template <int RB, int KT, bool WIN>
 __device__ __forceinline__ bool pf_next(const PagedParams &p, PfCursor *c, PfPiece *w, int lane) {
     __syncwarp();
     int more = 0;
-    if (lane == 0) more = pf_step<RB, KT>(p, *c, *w);
+    if (lane == 0) more = pf_step<RB, KT, WIN>(p, *c, *w);
     more = __shfl_sync(0xffffffffu, more, 0);
     __syncwarp();
     return more != 0;
@@ -275,7 +299,7 @@ __device__ __noinline__ bool pf_wait(uint64_t *bar, uint32_t parity, int *fail) 
     return false;
 }
 
-template <int BITS, int D>
+template <int BITS, int D, bool WIN>
 __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParams p) {
     using L = PfLayout<BITS, D>;
     constexpr int G = L::G, MT = L::MT, RB = L::RB, ST = L::ST, KT = L::KT, NH = L::NH;
@@ -324,14 +348,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
     if (warp == 1) {
         int64_t units = 0;
         for (int b0 = 0; b0 < B; b0 += 32)
-            units += b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0;
+            units += b0 + lane < B ? pf_units<RB, KT, WIN>(p, b0 + lane) : 0;
         const int total = pg_total(units);
         const int ctas = min((int)gridDim.x, total);
         const int quot = ctas ? total / ctas : 0, rest = ctas ? total % ctas : 0;
         const int begin = pg_start(quot, rest, cta), end = pg_start(quot, rest, cta + 1);
         int at = 0, b = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
-            const int u = b0 + lane < B ? pf_units<RB, KT>(p, b0 + lane) : 0;
+            const int u = b0 + lane < B ? pf_units<RB, KT, WIN>(p, b0 + lane) : 0;
             int incl = u;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -355,10 +379,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 c.s = kv_seq(p.kv, b);
                 c.rows = pf_rows<RB>(p, c.s);
                 c.nrb = (c.rows + RB - 1) / RB;
-                const int head = pf_units<RB, KT>(p, b) / p.kv.heads;
+                const int head = pf_units<RB, KT, WIN>(p, b) / p.kv.heads;
                 c.hk = (begin - at) / head;
                 int in = (begin - at) - c.hk * head;
-                for (int n; in >= (n = pf_cost<KT>(pf_tiles<RB, KT>(p, c.s, c.rows, c.rb))); ++c.rb) in -= n;
+                for (int n; in >= (n = pf_cost<KT>(pf_tiles<RB, KT, WIN>(p, c.s, c.rows, c.rb))); ++c.rb) in -= n;
                 c.unit = in;
                 c.at = begin;
             }
@@ -443,7 +467,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 if (h == NH - 1) tc_commit(&rempty[tile % kPfSlots]);
                 return true;
             };
-            while (ok && pf_step<RB, KT>(p, *cur, s_piece[warp])) {
+            while (ok && pf_step<RB, KT, WIN>(p, *cur, s_piece[warp])) {
                 const int nlive = min(RB, w.rows - w.rb * RB);
                 const int tiles = w.tb - w.ta, steps = tiles * NH;
                 if (MT == 2 && warp * 128 >= nlive) {
@@ -478,14 +502,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         int longer = 0;          // of the pieces, those of two steps and more
         bool ok = true;
         int turn = 0;
-        bool more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][0], lane);
+        bool more = pf_next<RB, KT, WIN>(p, cur, &s_soft[warp - 4][0], lane);
         for (; ok && more; turn ^= 1) {
             const PfPiece &w = s_soft[warp - 4][turn];
             more = false;
             const int nlive = min(RB, w.rows - w.rb * RB);
             const int tiles = w.tb - w.ta;
             if (r * 128 >= nlive) {
-                more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
+                more = pf_next<RB, KT, WIN>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
             } else {
                 // ---- the row's queries: fp16 at a power of two, the group
                 // sums in the further columns.  The warp copies its 32 rows
@@ -577,11 +601,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[r]);
                 // the next piece, while this one's scores start
-                more = pf_next<RB, KT>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
+                more = pf_next<RB, KT, WIN>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
 
                 const float fac = down * fabsf(p.scale) * 1.4426950408889634f;
                 const int lim = live ? kv_seen(w.s, tok, p.causal) : w.s.len;
                 const int least = __reduce_min_sync(FULL, lim);
+                // with a window: the row's start, and the latest of the warp's
+                const int low = WIN ? pg_low(p, (int64_t)w.s.end - w.s.count + tok) : 0;
+                const int latest = WIN ? __reduce_max_sync(FULL, low) : 0;
+                auto hide = [&](float (&v)[32], int key) {  // key: v[0]'s
+                    if (key >= latest || key + 32 <= p.sinks) return;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (k < low - key && k >= p.sinks - key) v[k] = -INFINITY;
+                };
                 float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
                 const int steps = tiles * NH;
                 for (int i = 0; ok && i < steps; ++i) {
@@ -595,7 +628,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // (never zero, so that a masked score stays -inf: a factor
                     // below leaves every score at zero either way)
                     const float f = fmaxf(fac * pt.k_down, 1e-37f);
-                    const int key0 = w.ta * KT + i * 64;
+                    const int key0 = WIN ? w.at<WIN>(w.ta + i / NH) * KT + i % NH * 64 : w.ta * KT + i * 64;
                     const int n_in = key0 + 64 > least ? lim - key0 : 64;
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -608,6 +641,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             for (int k = 0; k < 32; ++k)
                                 if (k + c >= n_in) v[k] = -INFINITY;
                         }
+                        if constexpr (WIN) hide(v, key0 + c);
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) mx = fmaxf(mx, fmaxf(v[k], v[k + 1]));
                     }
@@ -669,6 +703,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                             for (int k = 0; k < 32; ++k)
                                 if (k + c >= n_in) v[k] = -INFINITY;
                         }
+                        if constexpr (WIN) hide(v, key0 + c);
 #pragma unroll
                         for (int k = 0; k < 32; k += 2) {
                             float2 x = fma2(make_float2(v[k], v[k + 1]), f2, s2);
@@ -684,7 +719,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                         // rows that see it are not finite either
                         for (int k = 0; k < 64; ++k) {
                             const int x = (i % NH) * 64 + k;
-                            if ((pt.bad[x & 3] >> (x >> 2)) & 1 && key0 + k < lim) l = NAN;
+                            if ((pt.bad[x & 3] >> (x >> 2)) & 1 && key0 + k < lim &&
+                                !(WIN && pg_hidden(p, key0 + k, 1, low)))
+                                l = NAN;
                         }
                     }
                     tc_wait_st();
@@ -773,18 +810,21 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         const uint32_t *src = is_k ? p.kv.kp : p.kv.vp;
         uint32_t n = 0;
         bool ok = true;
-        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
-            const PfPages<KT> pages{p, w.s.len, w.tb, w.hk, w.b};
+        while (ok && pf_next<RB, KT, WIN>(p, cur, &s_piece[warp], lane)) {
+            const PfPages<KT, WIN> pages{p, w};
             float v_lim = -1.f, up = 1.f, down = 1.f;
             uint32_t x[4][G];  // keys 4 lane + j
             auto load = [&](int64_t base, int tile) {
                 const int64_t row = __shfl_sync(FULL, base, lane >> 2) + (lane & 3) * 4;
-                const int left = min(KT, w.s.len - tile * KT);
+                const int key0 = w.at<WIN>(tile) * KT, left = min(KT, w.s.len - key0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < 4; ++j) {
+                    // (keys that no row sees are zeros, whatever they hold)
+                    const bool in = 4 * lane + j < left &&
+                                    !(WIN && pg_hidden(p, key0 + 4 * lane + j, 1, w.t.low));
 #pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        x[j][g] = 4 * lane + j < left ? src[(row + j) * G + g] : 0u;
+                    for (int g = 0; g < G; ++g) x[j][g] = in ? src[(row + j) * G + g] : 0u;
+                }
             };
             int64_t base = pages.look(w.ta, lane);
             load(base, w.ta);
@@ -906,12 +946,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         const int vc = lane & 7, vd = lane >> 3;  // 8 keys and 8 dimensions of a value unit
         uint32_t n = 0;
         bool ok = true;
-        while (ok && pf_next<RB, KT>(p, cur, &s_piece[warp], lane)) {
-            const PfPages<KT> pages{p, w.s.len, w.tb, w.hk, w.b};
+        while (ok && pf_next<RB, KT, WIN>(p, cur, &s_piece[warp], lane)) {
+            const PfPages<KT, WIN> pages{p, w};
             uint4 kreg[KU];
             uint32_t vreg[VU][8][VW];
             auto load_k = [&](int64_t base, int tile) {
-                const int left = min(KT, w.s.len - tile * KT);  // keys of the tile
+                const int left = min(KT, w.s.len - w.at<WIN>(tile) * KT);  // keys of the tile
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
@@ -922,7 +962,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 }
             };
             auto load_v = [&](int64_t base, int tile) {
-                const int left = min(KT, w.s.len - tile * KT);
+                const int left = min(KT, w.s.len - w.at<WIN>(tile) * KT);
 #pragma unroll
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
@@ -1076,7 +1116,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             if (p.status && tid == 0 && kv_past(s)) atomicOr(p.status, (int)kKvBadPage);
             const int rows = pf_rows<RB>(p, s);
             for (int rb = 0; rb * RB < rows; ++rb) {
-                if (pf_tiles<RB, KT>(p, s, rows, rb) > 0) continue;
+                if (pf_tiles<RB, KT, WIN>(p, s, rows, rb) > 0) continue;
                 const int n = min(RB, rows - rb * RB);
                 for (int i = tid; i < n * p.kv.heads * (D / 8); i += 64) {
                     const int c = i % (D / 8), h = i / (D / 8) % p.kv.heads, rr = rb * RB + i / (D / 8) / p.kv.heads;
@@ -1161,10 +1201,10 @@ double paged_prefill_units(const KvView &kv, int rep, int split) {
     return kv.heads * (rows / rb + part) * tiles;
 }
 
-template <int BITS, int D>
+template <int BITS, int D, bool WIN>
 static cudaError_t launch_pf_t(PagedParams p, void *workspace, cudaStream_t st) {
     using L = PfLayout<BITS, D>;
-    const void *kfn = reinterpret_cast<const void *>(paged_prefill_kernel<BITS, D>);
+    const void *kfn = reinterpret_cast<const void *>(paged_prefill_kernel<BITS, D, WIN>);
     cudaError_t e = allow_smem(kfn, (int)L::SMEM);
     if (e != cudaSuccess) return e;
     const int grid = pf_grid(p.kv, p.rep);
@@ -1186,7 +1226,9 @@ static cudaError_t launch_pf_t(PagedParams p, void *workspace, cudaStream_t st) 
 
 cudaError_t launch_paged_prefill(PagedParams p, void *workspace, cudaStream_t st) {
 #define GWA_PF(BB, DD) \
-    if (p.kv.bits == BB && p.kv.dim == DD) return launch_pf_t<BB, DD>(p, workspace, st);
+    if (p.kv.bits == BB && p.kv.dim == DD)                               \
+        return p.window ? launch_pf_t<BB, DD, true>(p, workspace, st)    \
+                        : launch_pf_t<BB, DD, false>(p, workspace, st);
     GWA_PF(4, 64) GWA_PF(4, 128) GWA_PF(4, 256)
     GWA_PF(8, 64) GWA_PF(8, 128) GWA_PF(8, 256)
 #undef GWA_PF

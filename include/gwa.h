@@ -446,6 +446,26 @@ int gwa_sdpa_paged(const uint16_t *q, int64_t q_stride, int32_t Hq,
 size_t gwa_sdpa_paged_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
                                       gwa_kv_batch batch);
 
+/* gwa_sdpa_paged_window -- gwa_sdpa_paged with a sliding window and first
+ * tokens that stay visible: a token at position p sees key t where
+ *   t <= p  and  (t > p - window  or  t < sinks)
+ * (window >= 1, sinks >= 0; a window of p + 1 and more is the causal mask).
+ * Only pages with such a key for one of the batch's new tokens are read: the
+ * entries of the others in the page table may hold anything, so a caller may
+ * give their pages back.  A row that sees no key is zero.  Everything else as
+ * gwa_sdpa_paged, with the roundings that it states: a key in front of a
+ * token's window is one that the mask hides from it.  Errors as there, and
+ * GWA_ERR_INVALID_ARG (window, sinks). */
+int gwa_sdpa_paged_window(const uint16_t *q, int64_t q_stride, int32_t Hq,
+                          gwa_kv_cache cache, gwa_kv_batch batch, float scale,
+                          int32_t window, int32_t sinks, uint16_t *out,
+                          void *workspace, size_t workspace_bytes,
+                          int32_t *status, void *stream);
+/* 0 (and gwa_last_error) for what gwa_sdpa_paged_window refuses. */
+size_t gwa_sdpa_paged_window_workspace_bytes(int32_t Hq, gwa_kv_cache cache,
+                                             gwa_kv_batch batch, int32_t window,
+                                             int32_t sinks);
+
 /* gwa_sample -- one token a row from logits, by a given random number.
  *   logits       [rows, V], bf16 (dtype GWA_BF16) or fp32 (GWA_FP32), aligned
  *                to their element; row_stride elements from row to row

@@ -110,6 +110,32 @@ def attention(q, k, v, q_start, kv_len, scale: float, causal: bool):
     return out
 
 
+def attention_window(q, k, v, q_start, kv_len, scale: float, window: int, sinks: int):
+    """As ``attention`` with the causal mask, where a token at position p sees
+    key t if t > p - window or t < sinks."""
+    T, Hq, D = q.shape
+    out = np.full((T, Hq, D), np.nan)
+    for b in range(len(kv_len)):
+        a, e, n = int(q_start[b]), int(q_start[b + 1]), int(kv_len[b])
+        if e == a:
+            continue
+        rep = Hq // k[b].shape[1]
+        t = np.arange(n)
+        for i in range(e - a):
+            p = n - (e - a) + i
+            see = (t <= p) & ((t > p - window) | (t < sinks))
+            if not see.any():
+                out[a + i] = 0.0
+                continue
+            ks, vs = k[b][see], v[b][see]  # [keys, heads, D]
+            qs = q[a + i].reshape(-1, rep, D)
+            x = scale * np.einsum("hrd,thd->hrt", qs, ks)
+            w = np.exp(x - x.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            out[a + i] = np.einsum("hrt,thd->hrd", w, vs).reshape(Hq, D)
+    return out
+
+
 def sample_order(x: np.ndarray) -> np.ndarray:
     """Indices by logit, largest first, equal ones by index (NaN as -inf)."""
     x = np.where(np.isnan(x), -np.inf, x).astype(np.float64)
