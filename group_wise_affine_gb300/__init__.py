@@ -10,7 +10,7 @@ Names mirror the C entry points without the ``gwa_`` prefix:
 ``qmv_affine``, ``qmv_fused_sections``, ``qmv_gate_up_silu``,
 ``qmv_qkv_rope``, ``moe_qmv_gather``, ``quantize_affine``, ``sdpa_dequant_v``,
 ``rope_table``, ``kv_append``, ``kv_read``, ``sdpa_paged``, ``sample``,
-``lora_add``, ``lora_gate_up_silu``,
+``verify_draft``, ``lora_add``, ``lora_gate_up_silu``,
 ``workspace_bytes``, ``last_error``,
 ``debug_unpack``, ``debug_dequant``.
 
@@ -59,7 +59,8 @@ EXPORTS = ("gwa_qmv_affine", "gwa_qmv_fused_sections", "gwa_qmv_gate_up_silu",
            "gwa_rope_table", "gwa_kv_append", "gwa_kv_read", "gwa_sdpa_paged",
            "gwa_sdpa_paged_workspace_bytes", "gwa_sdpa_paged_window",
            "gwa_sdpa_paged_window_workspace_bytes", "gwa_sample", "gwa_lora_add",
-           "gwa_lora_gate_up_silu", "gwa_lora_workspace_bytes")
+           "gwa_lora_gate_up_silu", "gwa_lora_workspace_bytes",
+           "gwa_verify_draft", "gwa_verify_draft_workspace_bytes")
 
 
 class GwaError(RuntimeError):
@@ -166,6 +167,11 @@ def load(path: str = LIB_PATH):
     lib.gwa_sdpa_paged_window_workspace_bytes.restype = sz
     lib.gwa_sample.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, vp, vp,
                                vp, vp]
+    lib.gwa_verify_draft.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, i32,
+                                     vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz,
+                                     vp]
+    lib.gwa_verify_draft_workspace_bytes.argtypes = [i64]
+    lib.gwa_verify_draft_workspace_bytes.restype = sz
     lib.gwa_lora_add.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.gwa_lora_gate_up_silu.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz,
                                           vp, vp]
@@ -173,7 +179,7 @@ def load(path: str = LIB_PATH):
     lib.gwa_lora_workspace_bytes.restype = sz
     for f in ("gwa_rope_table", "gwa_kv_append", "gwa_kv_read",
               "gwa_sdpa_paged", "gwa_sdpa_paged_window", "gwa_sample", "gwa_lora_add",
-              "gwa_lora_gate_up_silu"):
+              "gwa_lora_gate_up_silu", "gwa_verify_draft"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("gwa_qmv_affine", "gwa_qmv_fused_sections",
               "gwa_qmv_gate_up_silu", "gwa_moe_qmv_gather",
@@ -826,6 +832,67 @@ def sample(logits: torch.Tensor, u: torch.Tensor,
     if rc:
         _check(rc)
     return token, prob
+
+
+def verify_draft(logits: torch.Tensor, ids: torch.Tensor, q_start: torch.Tensor,
+                 u: torch.Tensor, u_draw: torch.Tensor,
+                 draft_logits: Optional[torch.Tensor] = None,
+                 temperature: Optional[torch.Tensor] = None,
+                 top_k: Optional[torch.Tensor] = None,
+                 top_p: Optional[torch.Tensor] = None,
+                 min_p: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """gwa_verify_draft: (token int32 [rows], accepted int32 [batch], prob
+    float32 [rows]) for drafted tokens ids int32 [rows] in sequences q_start
+    int32 [batch + 1]: how many of each sequence's drafts stand against logits
+    [rows, V] (and draft_logits, or None), and the token behind them.  u
+    float32 [rows], u_draw float32 [batch]; filters by row as in ``sample``."""
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("logits must be bfloat16 or float32 [rows, V]")
+    R, V = logits.shape
+    for name, t in (("logits", logits), ("draft_logits", draft_logits)):
+        if t is None:
+            continue
+        if t.shape != logits.shape or t.dtype != logits.dtype:
+            raise ValueError(f"{name} must be {logits.dtype} [{R}, {V}]")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must live on a CUDA device")
+        if V > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: only the rows may be strided")
+    if q_start.dtype != torch.int32 or q_start.numel() < 1:
+        raise ValueError("q_start must be int32 [batch + 1]")
+    B = q_start.numel() - 1
+    args = [_row_values(t, name, dtype, n) for t, name, dtype, n in (
+        (ids, "ids", torch.int32, R), (u, "u", torch.float32, R),
+        (u_draw, "u_draw", torch.float32, B),
+        (temperature, "temperature", torch.float32, R),
+        (top_k, "top_k", torch.int32, R), (top_p, "top_p", torch.float32, R),
+        (min_p, "min_p", torch.float32, R))]
+    token = _new(R, torch.int32, logits.device, stream)
+    accepted = _new(B, torch.int32, logits.device, stream)
+    prob = _new(R, torch.float32, logits.device, stream)
+    if workspace is None:
+        n = int(load().gwa_verify_draft_workspace_bytes(R))
+        workspace = _new(max(n, 16), torch.uint8, logits.device, stream)
+    wp, wn = _ws(workspace)
+    row = lambda t: t.stride(0) if R > 1 else V  # noqa: E731
+    rc = load().gwa_verify_draft(
+        logits.data_ptr(),
+        GWA_BF16 if logits.dtype == torch.bfloat16 else GWA_FP32, R, V,
+        row(logits), draft_logits.data_ptr() if draft_logits is not None else None,
+        row(draft_logits) if draft_logits is not None else 0, args[0],
+        _ptr(q_start), B, *args[1:], token.data_ptr(), accepted.data_ptr(),
+        prob.data_ptr(), wp, wn, _stream(stream))
+    if rc:
+        _check(rc)
+    return token, accepted, prob
+
+
+def make_verify_workspace(rows: int, device=None) -> torch.Tensor:
+    n = int(load().gwa_verify_draft_workspace_bytes(rows))
+    if n == 0 and rows:
+        raise GwaError(GWA_ERR_INVALID_ARG, last_error())
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
 # ----------------------------------------------------------------- adapters

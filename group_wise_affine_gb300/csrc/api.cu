@@ -1066,6 +1066,91 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
     return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
 }
 
+size_t gwa_verify_draft_workspace_bytes(int64_t rows) {
+    g_last_error.clear();
+    if (rows < 0 || rows > (1 << 23)) {
+        fail(GWA_ERR_INVALID_ARG, "gwa_verify_draft_workspace_bytes: rows=%lld", (long long)rows);
+        return 0;
+    }
+    return verify_workspace_bytes(rows);
+}
+
+int gwa_verify_draft(const void *logits, int32_t dtype, int64_t rows, int64_t V,
+                     int64_t row_stride, const void *draft_logits,
+                     int64_t draft_stride, const int32_t *ids,
+                     const int32_t *q_start, int32_t batch, const float *u,
+                     const float *u_draw, const float *temperature,
+                     const int32_t *top_k, const float *top_p,
+                     const float *min_p, int32_t *token, int32_t *accepted,
+                     float *prob, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    const char *fn = "gwa_verify_draft";
+    g_last_error.clear();
+    if (dtype != GWA_BF16 && dtype != GWA_FP32)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: dtype=%d", fn, (int)dtype);
+    if (V > 524288)
+        return fail(GWA_ERR_UNSUPPORTED, "%s: V=%lld exceeds 524288", fn, (long long)V);
+    if (V < 1 || rows < 0 || rows > (1 << 23) || row_stride < V || batch < 0 || batch > (1 << 23) ||
+        (draft_logits && draft_stride < V))
+        return fail(GWA_ERR_INVALID_ARG,
+                    "%s: rows=%lld V=%lld row_stride=%lld draft_stride=%lld batch=%d", fn,
+                    (long long)rows, (long long)V, (long long)row_stride,
+                    (long long)draft_stride, (int)batch);
+    if (rows == 0 && batch == 0) return GWA_OK;
+    if (batch == 0)
+        return fail(GWA_ERR_INVALID_ARG, "%s: rows=%lld without a sequence", fn, (long long)rows);
+    if (!q_start || !u_draw || !accepted ||
+        (rows > 0 && (!logits || !ids || !u || !token)))
+        return fail(GWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const size_t a = dtype == GWA_BF16 ? 2 : 4;
+    if (!aligned(logits, a) || !aligned(draft_logits, a) || !aligned(ids, 4) ||
+        !aligned(q_start, 4) || !aligned(u, 4) || !aligned(u_draw, 4) ||
+        !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(token, 4) || !aligned(accepted, 4) || !aligned(prob, 4))
+        return fail(GWA_ERR_MISALIGNED, "%s: alignment", fn);
+    const size_t need = verify_workspace_bytes(rows);
+    if (rows > 0 && (!workspace || workspace_bytes < need))
+        return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn, need,
+                    workspace_bytes);
+    if (!aligned(workspace, 16))
+        return fail(GWA_ERR_MISALIGNED, "%s: workspace (16 bytes)", fn);
+    int rc = check_device();
+    if (rc) return rc;
+    SampleParams s{};
+    s.logits = logits;
+    s.V = V;
+    s.stride = row_stride;
+    s.temperature = temperature;
+    s.top_k = top_k;
+    s.top_p = top_p;
+    s.min_p = min_p;
+    s.draft = draft_logits;
+    s.draft_stride = draft_stride;
+    s.targets = rows;
+    s.rows = draft_logits ? 2 * rows : rows;
+    s.q_start = q_start;
+    s.batch = batch;
+    s.plan = static_cast<SmPlan *>(workspace);
+    VerifyParams v{};
+    v.logits = logits;
+    v.draft = draft_logits;
+    v.rows = rows;
+    v.V = V;
+    v.stride = row_stride;
+    v.draft_stride = draft_stride;
+    v.ids = ids;
+    v.q_start = q_start;
+    v.batch = batch;
+    v.u = u;
+    v.u_draw = u_draw;
+    v.plan = s.plan;
+    v.token = token;
+    v.accepted = accepted;
+    v.prob = prob;
+    cudaError_t e = launch_verify(s, v, dtype == GWA_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+}
+
 // ------------------------------------------------------------ adapters
 static int check_lora(const gwa_lora &l, int64_t M, LoraParams *p, const char *fn) {
     if (l.rank < 8 || l.rank > 128 || l.rank % 8 != 0 || l.sections < 1 ||

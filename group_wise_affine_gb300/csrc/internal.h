@@ -115,8 +115,31 @@ struct SampleParams {
     const int32_t *top_k;
     int32_t *token;
     float *prob;
+    // launch_sample_plan: rows [0, targets) of `logits`, then those of `draft`
+    // (NULL: rows = targets) by the same filters; sequence b's are
+    // [q_start[b], q_start[b + 1])
+    const void *draft;
+    int64_t draft_stride, targets;
+    const int32_t *q_start;
+    int batch;
+    struct SmPlan *plan;
 };
 cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st);
+cudaError_t launch_sample_plan(const SampleParams &p, bool bf16, cudaStream_t st);
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyParams {
+    const void *logits, *draft;
+    int64_t rows, V, stride, draft_stride;
+    const int32_t *ids, *q_start;
+    int batch;
+    const float *u, *u_draw;
+    const struct SmPlan *plan;  // targets', then drafts'
+    int32_t *token, *accepted;
+    float *prob;
+};
+cudaError_t launch_verify(const SampleParams &s, const VerifyParams &v, bool bf16, cudaStream_t st);
+size_t verify_workspace_bytes(int64_t rows);
 
 // Low-rank adapters of many requests (lora.cu).
 struct LoraParams {

@@ -51,10 +51,7 @@
 #include <set>
 #include <utility>
 
-#include "cluster.cuh"
-#include "common.cuh"
-#include "internal.h"
-#include "mma.cuh"
+#include "sample.cuh"
 
 namespace gwa {
 
@@ -68,8 +65,6 @@ constexpr int kSmList = 2048;  // tokens that one CTA ranks
 constexpr int kSmShort = kSmThreads / 2;
 constexpr int kSmMaxCluster = 16;
 constexpr int64_t kSmSliceBytes = 152 * 1024;
-
-using u64 = unsigned long long;
 
 // Logits as order-preserving keys; 0 is below every logit (no token there),
 // NaN counts as -inf and -0 as +0.
@@ -134,55 +129,6 @@ struct SmShared {
     u64 cut_mass;                   // of the tokens kept by a count
 };
 
-template <typename T>
-__device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
-    u64 a;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<u64>(local)), "r"(rank));
-    return reinterpret_cast<T *>(a);
-}
-
-// A row's weights.
-struct SmRow {
-    float top, per;
-    // base-2 exponent of a logit's mass relative to the largest's: <= 0; for
-    // a NaN NaN, for -inf -inf or (infinite T) NaN
-    __device__ __forceinline__ float expo(float x) const {
-        return x == top ? 0.f : __fmul_rn(__fsub_rn(x, top), per);
-    }
-    // floor(2^40 exp2f(y)): the 24-bit significand shifted by the exponent.
-    // From -44 to 0 exp2f gives ex2's value (checked for every float there);
-    // below -40 the shifts leave zero, and so they do for a NaN, whose counts
-    // all lie past 31.
-    static __device__ __forceinline__ u64 mass_of(float y) {
-        const uint32_t b = __float_as_uint(ex2(y)), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
-        return ((u64)shr(m, 142u - e) << 32) | (shl(m, e - 110u) | shr(m, 110u - e));
-    }
-    // exp2f(y), and for a NaN zero: the mass times 2^-40, before its floor.
-    static __device__ __forceinline__ float part_of(float y) { return fmaxf(ex2(y), 0.f); }
-    __device__ __forceinline__ u64 mass(float x) const { return mass_of(expo(x)); }
-    // (zero past 31)
-    static __device__ __forceinline__ uint32_t shl(uint32_t v, uint32_t n) {
-        uint32_t r;
-        asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
-        return r;
-    }
-    static __device__ __forceinline__ uint32_t shr(uint32_t v, uint32_t n) {
-        uint32_t r;
-        asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(n));
-        return r;
-    }
-};
-
-// Of a warp's 32 lanes: the sums up to and with one's own.
-template <typename T>
-__device__ __forceinline__ T warp_scan(T v) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const T w = __shfl_up_sync(0xffffffffu, v, o);
-        if ((int)(threadIdx.x & 31) >= o) v += w;
-    }
-    return v;
-}
 // A sum of masses, each from its part t = exp2f(y), without a shift: 8 + t
 // rounded towards zero holds the mass's upper 21 bits at the end of its
 // significand, 2^-17 plus what is left of t its lower 20.  The words are
@@ -200,12 +146,6 @@ struct MassSum {
                (u64)(uint32_t)(lo - count * __float_as_uint(0x1p-17f));
     }
 };
-
-__device__ __forceinline__ u64 warp_sum64(u64 v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
 
 template <bool BF16>
 struct Sampler {
@@ -517,26 +457,39 @@ struct Sampler {
             before += own[j];
         }
     }
-    // floor(total f) for f in [0, 1): the float's significand times the total,
-    // shifted (64-bit floating point takes thousands of cycles here).
-    static __device__ __forceinline__ u64 part(u64 total, float f) {
-        const uint32_t b = __float_as_uint(fmaxf(f, 0.f));
-        const u64 m = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
-        const int sh = 150 - max((int)(b >> 23), 1);  // f = m 2^-sh, sh >= 24
-        const u64 lo = total * m, hi = __umul64hi(total, m);
-        return sh < 64 ? lo >> sh | hi << (64 - sh) : sh < 128 ? hi >> (sh - 64) : 0;
-    }
     // What top-p has to reach, and where a random number falls.
     static __device__ __forceinline__ u64 share_of(u64 total, float tp) {
         const u64 goal = part(total, tp);
         return goal < 1 ? 1 : goal;
     }
-    static __device__ __forceinline__ u64 drawn_at(u64 total, float u) {
-        return u >= 1.f ? total - 1 : part(total, u);
-    }
-    // A token's share of the kept (rounded three times).
-    static __device__ __forceinline__ float share(u64 w, u64 total) {
-        return __fdiv_rn(__ull2float_rn(w), __ull2float_rn(total));
+
+    // ---- what that draw would keep
+    __device__ void plan(int n, u64 goal, float tp, u64 least, SmPlan *out) {
+        u64 own[PT], sum = 0, total;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            const int i = threadIdx.x * PT + j;
+            own[j] = i < n ? row.mass(SmKey<false>::value(~(uint32_t)(sh.list[i] >> 32))) : 0;
+            sum += own[j];
+        }
+        u64 before = scan(sum, total), kept = 0, count = 0;
+        if (goal == 0) goal = tp < 1.f ? share_of(total, tp) : ~0ull;
+#pragma unroll
+        for (int j = 0; j < PT; ++j) {
+            if ((int)threadIdx.x * PT + j < n && before < goal && own[j] >= least) {
+                kept += own[j];
+                ++count;
+            }
+            before += own[j];
+        }
+        scan(kept, total);
+        u64 tokens;
+        scan(count, tokens);
+        if (threadIdx.x == 0) {
+            const u64 last = sh.list[max((int)tokens, 1) - 1];  // (the first is always kept)
+            *out = SmPlan{row.top, row.per, SmKey<false>::value(~(uint32_t)(last >> 32)), (uint32_t)last,
+                          least, total};
+        }
     }
 
     // ---- the cut among the tokens of histogram step `bin` that lie above
@@ -680,7 +633,9 @@ struct Sampler {
     }
 };
 
-template <bool BF16>
+// PLAN: not a token, but what each row's filters keep (SmPlan), of the target
+// rows and behind them the draft rows of a batch of sequences.
+template <bool BF16, bool PLAN>
 __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, int cl, bool in_turn) {
     using S = Sampler<BF16>;
     using Raw = typename S::Raw;
@@ -700,10 +655,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         // short top-k, other draws, greedy rows
         int cls = 3;
         if (tid < p.rows) {
-            const int k = p.top_k ? p.top_k[tid] : 0;
-            cls = p.temperature && !(p.temperature[tid] > 0.f)      ? 2
+            const int f = PLAN && tid >= p.targets ? tid - (int)p.targets : tid;
+            const int k = p.top_k ? p.top_k[f] : 0;
+            cls = p.temperature && !(p.temperature[f] > 0.f)        ? 2
                   : k > 0 && k <= kSmShort                          ? 1
-                  : p.top_p && p.top_p[tid] < 1.f                   ? 0
+                  : p.top_p && p.top_p[f] < 1.f                     ? 0
                                                                     : 1;
         }
         const u64 one = cls < 3 ? 1ull << (16 * cls) : 0;  // three counts in a word
@@ -729,7 +685,18 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     // slice starts at element `mis` of its first chunk
     const int64_t per_cta = (p.V + cl - 1) / cl;
     const int64_t lo = min(p.V, rank * per_cta), hi = min(p.V, lo + per_cta);
-    const Raw *src = static_cast<const Raw *>(p.logits) + r * p.stride + lo;
+    const bool draft = PLAN && r >= p.targets;
+    const int64_t fr = draft ? r - p.targets : r;  // the row of the filters
+    const Raw *src = draft ? static_cast<const Raw *>(p.draft) + fr * p.draft_stride + lo
+                           : static_cast<const Raw *>(p.logits) + r * p.stride + lo;
+    if constexpr (PLAN) {
+        // whether the row is of a sequence, and a draft's one with a token
+        // behind it (the others' plans are not read)
+        if (warp == 0) {
+            const SmSeq q = sm_sequence(p.q_start, p.batch, fr);
+            if (lane == 0) sh.f_bin = q.seq >= 0 && (!draft || fr + 1 < min((int64_t)q.next, p.targets));
+        }
+    }
     const int len = (int)(hi - lo);
     const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Raw));
     const int chunks = (len + mis + PER - 1) / PER;
@@ -801,19 +768,23 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             low = fminf(low, sh.x_low[c]);
         }
     }
+    if (PLAN && !sh.f_bin) return;  // (the whole cluster)
     if (top == -INFINITY) {  // nothing to draw (the whole cluster leaves)
-        if (rank == 0 && tid == 0) {
+        if (PLAN) {
+            if (rank == 0 && tid == 0) p.plan[r] = SmPlan{top, 0.f, INFINITY, 0, 0, 0};
+        } else if (rank == 0 && tid == 0) {
             p.token[r] = -1;
             if (p.prob) p.prob[r] = 0.f;
         }
         return;
     }
 
-    const float T = p.temperature ? p.temperature[r] : 1.f;
-    const int kq = p.top_k ? p.top_k[r] : 0;
-    const float tp = p.top_p ? p.top_p[r] : 1.f;
-    const float mp = p.min_p ? p.min_p[r] : 0.f;
-    const float u = p.u[r];
+    const float T = p.temperature ? p.temperature[fr] : 1.f;
+    const int kq = p.top_k ? p.top_k[fr] : 0;
+    const float tp = p.top_p ? p.top_p[fr] : 1.f;
+    const float mp = p.min_p ? p.min_p[fr] : 0.f;
+    const float u = PLAN ? 0.f : p.u[r];
+    if (PLAN) __syncthreads();  // (f_bin is read)
     const bool greedy = !(T > 0.f);
     S s{sh, slice, mis, mis + len, lo - mis, cl, rank, {top, 0.f}, 0.f};
     s.row.per = __fmul_rn(__fdiv_rn(1.f, T), 1.4426950408889634f);
@@ -832,7 +803,9 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             }
         }
         s.sync_all();
-        if (rank == 0 && tid == 0) {
+        if (PLAN) {
+            if (rank == 0 && tid == 0) p.plan[r] = SmPlan{top, 0.f, top, sh.list_n, 0, 1ull << 40};
+        } else if (rank == 0 && tid == 0) {
             p.token[r] = (int32_t)sh.list_n;
             if (p.prob) p.prob[r] = 1.f;
         }
@@ -862,7 +835,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         if (n <= kSmList) {
             if (rank == 0) {
                 s.sort((int)n);
-                s.draw(min((int)n, kq), 0, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
+                if (PLAN)
+                    s.plan(min((int)n, kq), 0, tp, least, p.plan + r);
+                else
+                    s.draw(min((int)n, kq), 0, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
             }
             return;
         }
@@ -899,7 +875,10 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             n = (int)s.gather(x_thr, INFINITY, [&](float x, uint32_t) { return s.row.mass(x) >= thr; });
             if (rank == 0) {
                 s.sort(n);
-                s.draw(n, goal_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
+                if (PLAN)
+                    s.plan(n, goal_p, tp, least, p.plan + r);
+                else
+                    s.draw(n, goal_p, tp, least, u, p.token + r, p.prob ? p.prob + r : nullptr);
             }
             return;
         }
@@ -989,8 +968,13 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     u64 cta_before;
     cluster_sync_all();  // x_mass may still be read
     const u64 all = s.cluster_total(cta, cta_before);
+    if constexpr (PLAN) {
+        if (rank == 0 && tid == 0)
+            p.plan[r] = SmPlan{top, s.row.per, floor_x, cut ? cut_idx : 0xffffffffu, least, all};
+        return;
+    }
     // the first token whose running mass passes u * all 
-    const u64 goal = S::drawn_at(all, u);
+    const u64 goal = drawn_at(all, u);
     const u64 start = cta_before + warp_before;
     if (goal >= start && goal < start + mine) {
         u64 at = start;
@@ -1010,7 +994,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             const unsigned past = __ballot_sync(FULL, at + incl > goal);
             if (lane == __ffs(past) - 1) {
                 p.token[r] = (int32_t)(s.base + e0 + lane);
-                if (p.prob) p.prob[r] = S::share(w, all);
+                if (p.prob) p.prob[r] = share(w, all);
             }
             break;
         }
@@ -1031,10 +1015,10 @@ static cudaError_t allow_wide_clusters(const void *kernel) {
     return e;
 }
 
-template <bool BF16>
+template <bool BF16, bool PLAN>
 static cudaError_t launch_sample_t(const SampleParams &p, cudaStream_t st) {
     constexpr int esz = BF16 ? 2 : 4;
-    const void *kfn = reinterpret_cast<const void *>(sample_kernel<BF16>);
+    const void *kfn = reinterpret_cast<const void *>(sample_kernel<BF16, PLAN>);
     constexpr size_t head = ((sizeof(SmShared) + 15) / 16) * 16;
     int cl = 1;
     while (cl < kSmMaxCluster && (p.V + cl - 1) / cl * esz > kSmSliceBytes) cl *= 2;
@@ -1051,7 +1035,11 @@ static cudaError_t launch_sample_t(const SampleParams &p, cudaStream_t st) {
 }
 
 cudaError_t launch_sample(const SampleParams &p, bool bf16, cudaStream_t st) {
-    return bf16 ? launch_sample_t<true>(p, st) : launch_sample_t<false>(p, st);
+    return bf16 ? launch_sample_t<true, false>(p, st) : launch_sample_t<false, false>(p, st);
+}
+
+cudaError_t launch_sample_plan(const SampleParams &p, bool bf16, cudaStream_t st) {
+    return bf16 ? launch_sample_t<true, true>(p, st) : launch_sample_t<false, true>(p, st);
 }
 
 }  // namespace gwa

@@ -496,6 +496,49 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
                const int32_t *top_k, const float *top_p, const float *min_p,
                int32_t *token, float *prob, void *stream);
 
+/* gwa_verify_draft -- drafted tokens against the target model's logits: which
+ * stand, and the token behind them.  A batch as gwa_kv_batch's, q_start int32
+ * [batch + 1] on the device: sequence b's rows are [q_start[b], q_start[b +
+ * 1]), the last accepted token and the drafts behind it as they went through
+ * the model, so that row i holds the logits of the token behind row i.
+ *   logits        [rows, V] as gwa_sample: the target's
+ *   draft_logits  [rows, V] of the same dtype, row i the draft model's for the
+ *                 token behind row i, which ids[i + 1] was drawn from under
+ *                 the same filters (a sequence's last row is not read); or
+ *                 NULL: drafts from elsewhere, taken as certain (q(d) = 1)
+ *   ids           int32 [rows]: the tokens of the rows; ids[i + 1] is row i's
+ *                 draft (one outside [0, V) never stands)
+ *   u             fp32 [rows]: for row i's draft, uniform in [0, 1), taken in
+ *                 steps of 2^-24
+ *   u_draw        fp32 [batch]: for the token that is drawn
+ *   temperature, top_k, top_p, min_p  by row, as gwa_sample
+ *   token         int32 [rows]: a sequence's drafts that stand, the drawn
+ *                 token (-1 where the row has none to draw), then -1
+ *   accepted      int32 [batch]: how many stand; 0 for a sequence without rows
+ *   prob          NULL or fp32 [rows]: min(1, p(d) / q(d)) of row i's draft, 0
+ *                 in a sequence's last row
+ * With p and q the shares of the masses that gwa_sample's rule keeps of the
+ * two rows, draft d stands if u q(d) < p(d) and all before it stand.  Drawn is
+ * from max(p - q, 0) in the row of the first that falls (p where that is zero
+ * everywhere), from p in the last row where none falls: the first token, by
+ * index, at which the running mass passes u_draw's share.  Compared are whole
+ * numbers, so the result does not depend on how the work is split; in p - q
+ * both are taken to 2^-40 of their row's likeliest token's.  Tokens of no
+ * sequence: token -1, prob 0.
+ *   workspace  >= gwa_verify_draft_workspace_bytes(rows), 16-byte aligned
+ *   1 <= V <= 524288, rows <= 2^23.  Errors as gwa_sample, and
+ * GWA_ERR_WORKSPACE. */
+int gwa_verify_draft(const void *logits, int32_t dtype, int64_t rows, int64_t V,
+                     int64_t row_stride, const void *draft_logits,
+                     int64_t draft_stride, const int32_t *ids,
+                     const int32_t *q_start, int32_t batch, const float *u,
+                     const float *u_draw, const float *temperature,
+                     const int32_t *top_k, const float *top_p,
+                     const float *min_p, int32_t *token, int32_t *accepted,
+                     float *prob, void *workspace, size_t workspace_bytes,
+                     void *stream);
+size_t gwa_verify_draft_workspace_bytes(int64_t rows);
+
 /* ------------------------------------------------------------------------
  * Low-rank adapters of many requests beside a shared projection
  * ("Sanctum-MLX", "File map": lora.rs merges one adapter into the weights at

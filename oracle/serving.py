@@ -170,3 +170,50 @@ def lora(x, base, a, b, ids, scale=None, ranks=None):
             out[s][m] += (1.0 if scale is None else float(scale[e])) * (b[e, at:at + size, :r] @ t)
             at += size
     return out
+
+
+def kept_shares(x: np.ndarray, T: float, k: int, p: float, mp: float, count=None):
+    """Shares fp64 [V] of what the sampling rule keeps of a row, with real
+    masses (``count``: the first so many of the order instead); zeros for a
+    row without a finite logit."""
+    x = np.where(np.isnan(x), -np.inf, x).astype(np.float64)
+    out = np.zeros(len(x))
+    if x.max() == -np.inf:
+        return out
+    order = sample_order(x)
+    if not T > 0:
+        out[order[0]] = 1.0
+        return out
+    w = sample_masses(x, T)
+    if count is None:
+        count = int(k) if 0 < k < len(x) else len(x)
+        if p < 1:
+            ws = w[order[:count]]
+            count = max(1, int((np.cumsum(ws) - ws < p * ws.sum()).sum()))
+        if mp > 0:
+            count = min(count, max(1, int((w[order[:count]] >= min(mp, 1.0)).sum())))
+    keep = order[:count]
+    out[keep] = w[keep] / w[keep].sum()
+    return out
+
+
+def verify(ps, qs, drafts, us, u_draw):
+    """A sequence's tokens and how many drafts stand: ps the shares of its
+    rows, qs of its drafts' rows (None: certain), one fewer."""
+    fell = len(drafts)
+    for j, d in enumerate(drafts):
+        q = qs[j][d] if qs is not None else 1.0
+        if not us[j] * q < ps[j][d]:
+            fell = j
+            break
+    rest = ps[fell].copy()
+    if fell < len(drafts):
+        if qs is None:
+            rest[drafts[fell]] = 0.0
+        else:
+            rest = np.maximum(rest - qs[fell], 0.0)
+        if rest.sum() == 0:
+            rest = ps[fell].copy()
+    c = np.cumsum(rest)
+    drawn = int(np.searchsorted(c, u_draw * c[-1], side="right")) if c[-1] > 0 else -1
+    return list(drafts[:fell]) + [drawn], fell
