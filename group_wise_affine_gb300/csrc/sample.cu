@@ -129,24 +129,6 @@ struct SmShared {
     u64 cut_mass;                   // of the tokens kept by a count
 };
 
-// A sum of masses, each from its part t = exp2f(y), without a shift: 8 + t
-// rounded towards zero holds the mass's upper 21 bits at the end of its
-// significand, 2^-17 plus what is left of t its lower 20.  The words are
-// added as they are and the constants taken off at the end; up to 2048 masses
-// a thread (of 2^19 tokens on 1024 threads at most 512).
-struct MassSum {
-    uint32_t hi = 0, lo = 0;
-    __device__ __forceinline__ void add(float t) {
-        const float s = __fadd_rz(t, 8.f);
-        hi += __float_as_uint(s);
-        lo += __float_as_uint(__fadd_rz(__fsub_rn(t, __fsub_rn(s, 8.f)), 0x1p-17f));
-    }
-    __device__ __forceinline__ u64 total(uint32_t count) const {
-        return ((u64)(hi - count * __float_as_uint(8.f)) << 20) +
-               (u64)(uint32_t)(lo - count * __float_as_uint(0x1p-17f));
-    }
-};
-
 template <bool BF16>
 struct Sampler {
     using K = SmKey<BF16>;

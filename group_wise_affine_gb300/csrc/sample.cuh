@@ -31,8 +31,10 @@ struct SmRow {
     // From -44 to 0 exp2f gives ex2's value (checked for every float there);
     // below -40 the shifts leave zero, and so they do for a NaN, whose counts
     // all lie past 31.
-    static __device__ __forceinline__ u64 mass_of(float y) {
-        const uint32_t b = __float_as_uint(ex2(y)), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
+    static __device__ __forceinline__ u64 mass_of(float y) { return whole(ex2(y)); }
+    // floor(2^40 t), t >= 0
+    static __device__ __forceinline__ u64 whole(float t) {
+        const uint32_t b = __float_as_uint(t), e = b >> 23, m = (b & 0x7fffffu) | 0x800000u;
         return ((u64)shr(m, 142u - e) << 32) | (shl(m, e - 110u) | shr(m, 110u - e));
     }
     // exp2f(y), and for a NaN zero: the mass times 2^-40, before its floor.
@@ -61,6 +63,24 @@ __device__ __forceinline__ T warp_scan(T v) {
     }
     return v;
 }
+// A sum of masses, each from its part t = exp2f(y), without a shift: 8 + t
+// rounded towards zero holds the mass's upper 21 bits at the end of its
+// significand, 2^-17 plus what is left of t its lower 20.  The words are
+// added as they are and the constants taken off at the end; up to 2048 masses
+// a thread (of 2^19 tokens on 1024 threads at most 512).
+struct MassSum {
+    uint32_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(float t) {
+        const float s = __fadd_rz(t, 8.f);
+        hi += __float_as_uint(s);
+        lo += __float_as_uint(__fadd_rz(__fsub_rn(t, __fsub_rn(s, 8.f)), 0x1p-17f));
+    }
+    __device__ __forceinline__ u64 total(uint32_t count) const {
+        return ((u64)(hi - count * __float_as_uint(8.f)) << 20) +
+               (u64)(uint32_t)(lo - count * __float_as_uint(0x1p-17f));
+    }
+};
+
 __device__ __forceinline__ u64 warp_sum64(u64 v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -96,6 +116,12 @@ struct SmPlan {
         if (!(x > cut_x || (x == cut_x && token <= cut_idx))) return 0;
         const u64 w = SmRow{top, per}.mass(x);
         return w >= least ? w : 0;
+    }
+    // its part, for tokens other than the cut's equals: zero where nothing is
+    // kept.  least_t: least times 2^-40 (a float holds it: it comes from one)
+    __device__ __forceinline__ float part(float x, float least_t) const {
+        const float t = SmRow::part_of(SmRow{top, per}.expo(x));
+        return x > cut_x && t >= least_t ? t : 0.f;
     }
 };
 

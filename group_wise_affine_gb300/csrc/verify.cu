@@ -9,18 +9,23 @@
 // drawn from max(p - q, 0) in the row of the first that falls, from p where none
 // fell.  So the tokens are distributed as the target's own would be.
 //
-// Everything is decided in whole numbers, as in sampling (sample.cuh): p(d) =
-// P / SP with 41-bit masses and 60-bit sums, compared as products of 128 bits;
-// max(p - q, 0) as P SQ - Q SP, both products cut to 64 bits at one common
-// scale, so that their sum over the row fits.  The result depends on no split
-// and no order.
+// Drafts are settled in whole numbers, as sampling's tokens are (sample.cuh):
+// p(d) = P / SP with 41-bit masses and 60-bit sums, compared as products of 128
+// bits.  A token's mass in max(p - q, 0) is the whole number of 2^-40 in
+//   t_p - (SP / SQ) t_q,   t = exp2f(y) the parts that the masses are floors of,
+// formed in fp32 with the quotient as two of them, so that each token's mass
+// has a rounding of its own and none is common to the whole row.  (Exact
+// products of 64-bit masses took 120 instructions a token, 78 us for 64 rows
+// of 151669 with 4 drafts each; so it takes 25.)  Sums are integer sums: the
+// result depends on no split and no order.
 //
 // Two kernels.  The first is sampling's own (sample_kernel, PLAN), over the
 // target rows and the draft rows at once: it leaves what each row's filters
 // keep, as a cut and a sum.  This one then has one row a sequence to go over
 // (two where a draft fell): a cluster of CTAs a sequence, each a slice of the
-// row, each warp a run of it; the runs' sums are joined and the warp that
-// holds the drawn mass looks for the token.
+// row in pieces of 256 tokens, a warp to a piece.  The pieces' sums are
+// scanned, and one warp looks for the token in the piece that holds the drawn
+// mass.
 #include <algorithm>
 
 #include "sample.cuh"
@@ -29,8 +34,10 @@ namespace gwa {
 
 constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxCluster = 8;
+constexpr int kVfPiece = 256;                           // tokens
+constexpr int kVfPieces = 524288 / kVfPiece;            // of a CTA, at most
+constexpr int kVfScan = kVfPieces / kVfThreads;         // of a thread
 
-// The logits of a 16-byte chunk, or one.
 template <bool BF16>
 struct VfRow {
     using Raw = typename std::conditional<BF16, uint16_t, uint32_t>::type;
@@ -40,29 +47,39 @@ struct VfRow {
     }
 };
 
-// Masses of max(p - q, 0), or of p alone, at a common scale.
+// What the row's token is drawn from: the kept of p (kind 0), without token
+// `drop` (1), or max(p - q, 0) (2).
 struct VfMass {
     SmPlan p, q;
-    int shift_p, shift_q;  // of the products' upper 64 bits
-    u64 norm_p, norm_q;    // the other row's sum, its top bit set
-    int kind;              // 0: p; 1: p without token `drop`; 2: p - q
+    float least_p, least_q;  // times 2^-40
+    float hi, lo;            // SP / SQ = hi + lo
+    int kind;
     int64_t drop;
-    __device__ __forceinline__ void scales() {
-        const int lp = __clzll(p.total), lq = __clzll(q.total), e = min(lp, lq);
-        // P SQ 2^(lq - 41): of a sum below 2^63 after z more
-        const int z = max(0, 24 - max(lp, lq));
-        shift_p = lq - e + z;
-        shift_q = lp - e + z;
-        norm_p = q.total << lq;
-        norm_q = p.total << lp;
+    __device__ __forceinline__ void prepare() {
+        least_p = (float)p.least * 0x1p-40f;
+        least_q = (float)q.least * 0x1p-40f;
+        // hi the rounded quotient m 2^e (of sums from 2^40 to 2^59, so e < 0),
+        // lo from its exact remainder, SP - m 2^e SQ
+        hi = share(p.total, q.total);
+        const int e = f32_exp_field(hi) - 150;
+        const uint32_t m = (__float_as_uint(hi) & 0x7fffffu) | 0x800000u;
+        const __int128 left = ((__int128)p.total << -e) - (__int128)q.total * m;
+        lo = __fdiv_rn(__ll2float_rn((long long)left), __ull2float_rn(q.total)) *
+             __uint_as_float((uint32_t)(127 + e) << 23);
     }
-    __device__ __forceinline__ u64 of(float xp, float xq, int64_t token) const {
-        const u64 a = p.kept(xp, (uint32_t)token);
-        if (kind == 0 || a == 0) return a;
-        if (kind == 1) return token == drop ? 0 : a;
-        const u64 b = q.kept(xq, (uint32_t)token);
-        const u64 l = __umul64hi(a << 23, norm_p) >> shift_p, r = __umul64hi(b << 23, norm_q) >> shift_q;
-        return l > r ? l - r : 0;
+    __device__ __forceinline__ float kept(const SmPlan &s, float least, float x, int64_t token) const {
+        const float t = s.part(x, least);
+        // the cut's equals, up to its token (-inf's mass is zero anyway)
+        if (x == s.cut_x && x > -INFINITY)
+            return s.kept(x, (uint32_t)token) ? SmRow::part_of(SmRow{s.top, s.per}.expo(x)) : 0.f;
+        return t;
+    }
+    __device__ __forceinline__ float of(float xp, float xq, int64_t token) const {
+        const float a = kept(p, least_p, xp, token);
+        if (kind == 0) return a;
+        if (kind == 1) return token == drop ? 0.f : a;
+        const float b = kept(q, least_q, xq, token);
+        return fmaxf(a - fmaf(b, hi, b * lo), 0.f);
     }
 };
 
@@ -71,8 +88,8 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int 
     constexpr unsigned FULL = 0xffffffffu;
     using Row = VfRow<BF16>;
     using Raw = typename Row::Raw;
-    __shared__ u64 s_warp[kVfWarps], s_cta[kVfMaxCluster];
-    __shared__ int s_fell;
+    __shared__ u64 s_piece[kVfPieces], s_warp[kVfWarps], s_cta[kVfMaxCluster], s_left;
+    __shared__ int s_fell, s_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
     const int rank = cl > 1 ? (int)cluster_rank() : 0, b = blockIdx.x / cl;
     if (tid == 0) pdl_launch_dependents();
@@ -157,20 +174,45 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int 
             if (w.q.total) w.kind = 2;
         }
     }
-    w.scales();
+    w.prepare();
     const Row rp = row_of(at), rq = w.kind == 2 ? draft_of(at) : rp;
     const int64_t per_cta = (p.V + cl - 1) / cl;
     const int64_t lo = min(p.V, rank * per_cta), hi = min(p.V, lo + per_cta);
-    const int64_t run = ((hi - lo + kVfWarps - 1) / kVfWarps + 31) & ~31ll;
-    const int64_t a = min(hi, lo + warp * run), e = min(hi, a + run);
+    const int pieces = (int)((hi - lo + kVfPiece - 1) / kVfPiece);
+    constexpr int PER = kVfPiece / 32;  // tokens of a lane and piece
     const float u = p.u_draw[b];
     while (true) {
-        u64 mine = 0;
-        for (int64_t i = a + lane; i < e; i += 32) mine += w.of(rp.at(i), rq.at(i), i);
-        mine = warp_sum64(mine);
-        if (lane == 0) s_warp[warp] = mine;
+        for (int c = warp; c < pieces; c += kVfWarps) {
+            const int64_t i0 = lo + (int64_t)c * kVfPiece + lane;
+            float xp[PER], xq[PER];
+#pragma unroll
+            for (int j = 0; j < PER; ++j) xp[j] = i0 + 32 * j < hi ? rp.at(i0 + 32 * j) : -INFINITY;
+            if (w.kind == 2)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) xq[j] = i0 + 32 * j < hi ? rq.at(i0 + 32 * j) : -INFINITY;
+            MassSum sum;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) sum.add(w.of(xp[j], xq[j], i0 + 32 * j));
+            // (the constants that the words carry come off once a lane, before
+            // the lanes' sums, which then have room)
+            const u64 mine = sum.total(PER);
+            const uint32_t low = __reduce_add_sync(FULL, (uint32_t)mine & 0xfffffu);
+            const uint32_t high = __reduce_add_sync(FULL, (uint32_t)(mine >> 20));
+            if (lane == 0) s_piece[c] = ((u64)high << 20) + low;
+        }
         __syncthreads();
-        u64 before = 0, cta = 0, all = 0;
+        // ---- the pieces' sums in order, those of the CTA and of the cluster
+        u64 own[kVfScan], mine = 0;
+#pragma unroll
+        for (int j = 0; j < kVfScan; ++j) {
+            const int c = tid * kVfScan + j;
+            own[j] = c < pieces ? s_piece[c] : 0;
+            mine += own[j];
+        }
+        const u64 incl = warp_scan(mine);
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        u64 before = incl - mine, cta = 0, all = 0;
         for (int k = 0; k < kVfWarps; ++k) {
             if (k < warp) before += s_warp[k];
             cta += s_warp[k];
@@ -195,18 +237,35 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int 
             continue;
         }
         const u64 goal = drawn_at(all, u);
-        if (goal < before || goal >= before + mine) return;
-        u64 sum = before;
-        for (int64_t i0 = a; i0 < e; i0 += 32) {
-            const int64_t i = i0 + lane;
-            const u64 v = i < e ? w.of(rp.at(i), rq.at(i), i) : 0;
-            const u64 incl = warp_scan(v);
-            const unsigned past = __ballot_sync(FULL, sum + incl > goal);
+        if (tid == 0) s_at = -1;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kVfScan; ++j) {
+            if (goal >= before && goal < before + own[j]) {
+                s_at = tid * kVfScan + j;
+                s_left = goal - before;
+            }
+            before += own[j];
+        }
+        __syncthreads();
+        if (s_at < 0 || warp > 0) return;
+        const int64_t i0 = lo + (int64_t)s_at * kVfPiece + lane;
+        float xp[PER], xq[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            xp[j] = i0 + 32 * j < hi ? rp.at(i0 + 32 * j) : -INFINITY;
+            xq[j] = w.kind == 2 && i0 + 32 * j < hi ? rq.at(i0 + 32 * j) : -INFINITY;
+        }
+        u64 sum = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+            const u64 up = sum + warp_scan(SmRow::whole(w.of(xp[j], xq[j], i0 + 32 * j)));
+            const unsigned past = __ballot_sync(FULL, up > s_left);
             if (past) {
-                if (lane == __ffs(past) - 1) p.token[at] = (int32_t)i;
+                if (lane == __ffs(past) - 1) p.token[at] = (int32_t)(i0 + 32 * j);
                 return;
             }
-            sum += __shfl_sync(FULL, incl, 31);
+            sum = __shfl_sync(FULL, up, 31);
         }
         return;
     }

@@ -522,9 +522,9 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
  * from max(p - q, 0) in the row of the first that falls (p where that is zero
  * everywhere), from p in the last row where none falls: the first token, by
  * index, at which the running mass passes u_draw's share.  Compared are whole
- * numbers, so the result does not depend on how the work is split; in p - q
- * both are taken to 2^-40 of their row's likeliest token's.  Tokens of no
- * sequence: token -1, prob 0.
+ * numbers, so the result does not depend on how the work is split; a token's
+ * p - q is formed in fp32, as a whole number of 2^-40 of the likeliest token's
+ * p.  Tokens of no sequence: token -1, prob 0.
  *   workspace  >= gwa_verify_draft_workspace_bytes(rows), 16-byte aligned
  *   1 <= V <= 524288, rows <= 2^23.  Errors as gwa_sample, and
  * GWA_ERR_WORKSPACE. */
