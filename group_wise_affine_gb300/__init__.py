@@ -926,9 +926,9 @@ class LoRA(_Described):
 def make_lora_workspace(lora: LoRA, M: int) -> Optional[torch.Tensor]:
     n = int(load().gwa_lora_workspace_bytes(lora.c, M))
     if n == 0:
-        if M == 0:
-            return None
-        raise GwaError(GWA_ERR_INVALID_ARG, last_error())
+        if last_error():
+            raise GwaError(GWA_ERR_INVALID_ARG, last_error())
+        return None
     return torch.empty(n, dtype=torch.uint8, device=lora.device)
 
 
@@ -944,7 +944,7 @@ def _lora_inputs(x, lora, ids, sizes, base, workspace, stream):
                          f"{lora.N} outputs together")
     for i, (t, n) in enumerate(zip(base, sizes)):
         _check_out(t, M * n, f"section {i}")
-    if workspace is None and M:
+    if workspace is None and M > 256:
         n = int(load().gwa_lora_workspace_bytes(lora.c, M))
         workspace = _new(max(n, 16), torch.uint8, x.device, stream)
     return M, workspace  # (alive until the call is enqueued)

@@ -49,4 +49,24 @@ __device__ __forceinline__ void ld_cluster_f32_n(const float *local, uint32_t ra
                      : "memory");
 }
 
+// The same place in CTA `rank`'s shared memory, as a generic address.
+template <typename T>
+__device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
+    unsigned long long a;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<unsigned long long>(local)), "r"(rank));
+    return reinterpret_cast<T *>(a);
+}
+
+// Four fp32 at the same place in CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster_f32x4(const float *local, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
 }  // namespace gwa

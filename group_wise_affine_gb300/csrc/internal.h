@@ -220,6 +220,9 @@ cudaError_t prefer_max_shared(const void *kernel);
 // Opts a kernel in to `bytes` of dynamic shared memory (once per device).
 cudaError_t allow_smem(const void *kernel, int bytes);
 
+// Clusters of more than eight CTAs, once per device and kernel.
+cudaError_t allow_wide_clusters(const void *kernel);
+
 cudaError_t launch_dense(int mode, const DenseParams &p, cudaStream_t st);
 cudaError_t launch_stream(int mode, const DenseParams &p, cudaStream_t st,
                           bool *used);

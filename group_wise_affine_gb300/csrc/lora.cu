@@ -17,6 +17,7 @@
 // come (a prompt's tokens are neighbours).
 #include <algorithm>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "mma.cuh"
@@ -352,6 +353,282 @@ __global__ void __launch_bounds__(kLoThreads) lora_expand_kernel(LoraParams p) {
     }
 }
 
+// ------------------------------------------------------------ few tokens
+// Both products in one launch: a cluster of CTAs a tile.  Each CTA takes a
+// share of K for all of the adapter's rows; the shares' sums go round through
+// distributed shared memory, each CTA adding up a part and handing it to all as
+// MMA fragments (hi and lo bf16 parts); then each takes a share of the outputs.
+// The outputs' first loads (base and B) are on their way before the sums are.
+//
+// Fragments in shared memory: of a section's k step 32 lanes' hi words, then
+// their lo words.
+struct LoFragments {
+    uint4 hi[32], lo[32];
+};
+
+template <int KS, bool SILU, bool VEC>
+__global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) lora_few_kernel(LoraParams p, int cl) {
+    constexpr int S = SILU ? 2 : 1, Q = KS == 1 ? 1 : KS / 2;  // Q: B's loads of a row
+    extern __shared__ __align__(16) unsigned char lo_raw[];
+    __shared__ LoTiles<true> sh;
+    __shared__ float s_acc[kLoWarps][16 * kLoTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
+    const int share = cl > 1 ? (int)cluster_rank() : 0;
+    if (tid == 0) pdl_launch_dependents();
+    pdl_wait_primary();
+    const int tiles = lo_tiles<true, kLoTile>(p, sh), tile = blockIdx.x / cl;
+    if (tile >= tiles) return;  // (the whole cluster)
+    const int at = sh.start[tile], n = sh.start[tile + 1] - at;
+    const int id = lo_id(p, sh.token(at)), rank = lo_rank(p, id);
+    if (rank == 0 && p.in_place) return;
+    const int nb = (rank + 15) / 16, blocks = p.nsec * nb;   // 16-row blocks of A
+    const int nk = KS == 1 ? 1 : (nb + 1) & ~1;              // k steps of a section
+    float *const red = reinterpret_cast<float *>(lo_raw);
+    LoFragments *const frag = reinterpret_cast<LoFragments *>(
+        lo_raw + (size_t)p.nsec * ((p.rank + 15) / 16) * 256 * sizeof(float));
+
+    // ---- this CTA's outputs: steps of 32, a warp every eighth
+    const int steps = p.blocks, s0 = (int)((int64_t)steps * share / cl), s1 = (int)((int64_t)steps * (share + 1) / cl);
+    const bool live[2] = {g < n, g + 8 < n};
+    const int64_t tok[2] = {sh.token(at + (live[0] ? g : 0)), sh.token(at + (live[1] ? g + 8 : 0))};
+    struct Step {
+        int sec;
+        int64_t n0, N;
+    };
+    struct Loads {
+        uint4 base[S][2], b[S][4][Q];  // (KS 1: half of b)
+    };
+    auto place = [&](int step) {
+        Step r;
+        r.sec = 0;
+        if constexpr (!SILU)
+            while (step >= p.sec_blocks[r.sec]) step -= p.sec_blocks[r.sec++];
+        r.n0 = (int64_t)step * 32;
+        r.N = p.sec_n[r.sec];
+        return r;
+    };
+    auto load = [&](Loads &l, int step) {
+        const Step r = place(step);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const uint16_t *brow = p.b + ((int64_t)max(id, 0) * p.N + p.sec_start[r.sec + s]) * p.rank;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t c = r.n0 + 8 * (g >> 1) + 2 * j + (g & 1);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    if constexpr (KS == 1) {
+                        uint2 w = make_uint2(0u, 0u);
+                        if (c < r.N && 4 * t < rank) w = *reinterpret_cast<const uint2 *>(brow + c * p.rank + 4 * t);
+                        l.b[s][j][q].x = w.x;
+                        l.b[s][j][q].y = w.y;
+                    } else {
+                        const int rr = 32 * q + 8 * t;
+                        l.b[s][j][q] = lo_load(brow + c * p.rank + rr, c < r.N && rr < rank);
+                    }
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t col = r.n0 + 8 * t;
+                const uint16_t *src = p.base[r.sec + s] + tok[h] * r.N + col;
+                if constexpr (VEC) {
+                    l.base[s][h] = lo_load(src, live[h] && col < r.N);
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t x = live[h] && col + 2 * i < r.N ? src[2 * i] : 0u;
+                        const uint32_t y = live[h] && col + 2 * i + 1 < r.N ? src[2 * i + 1] : 0u;
+                        w[i] = x | (y << 16);
+                    }
+                    l.base[s][h] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+    };
+    auto use = [&](Loads &l, int step) {
+        const Step r = place(step);
+        float acc[S][4][4];
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t w[4] = {l.base[s][h].x, l.base[s][h].y, l.base[s][h].z, l.base[s][h].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[s][j][2 * h] = bf16_lo(w[j]);
+                    acc[s][j][2 * h + 1] = bf16_hi(w[j]);
+                }
+            }
+        if (rank % 8) {
+            // entries past the adapter's rank, whatever they hold, are zero
+            auto mask = [&](uint32_t &w, int k) { w = k + 1 < rank ? w : k < rank ? w & 0xffffu : 0u; };
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int k = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                        mask(l.b[s][j][q].x, k);
+                        mask(l.b[s][j][q].y, k + 2);
+                        if constexpr (KS > 1) {
+                            mask(l.b[s][j][q].z, k + 4);
+                            mask(l.b[s][j][q].w, k + 6);
+                        }
+                    }
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            const LoFragments *f = frag + (r.sec + s) * nk;
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                if (32 * q >= rank) break;
+#pragma unroll
+                for (int b = 0; b < (KS == 1 ? 1 : 2); ++b) {
+                    const uint4 hi = f[(KS == 1 ? 0 : 2 * q) + b].hi[lane], lo = f[(KS == 1 ? 0 : 2 * q) + b].lo[lane];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 &w = l.b[s][j][q];
+                        const uint32_t b0 = b ? w.z : w.x, b1 = b ? w.w : w.y;
+                        mma_bf16(acc[s][j], hi.x, hi.y, hi.z, hi.w, b0, b1);
+                        mma_bf16(acc[s][j], lo.x, lo.y, lo.z, lo.w, b0, b1);
+                    }
+                }
+            }
+        }
+        if constexpr (SILU) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[0][j][i] = acc[0][j][i] / (1.f + __expf(-acc[0][j][i])) * acc[1][j][i];
+        }
+        const int64_t col = r.n0 + 8 * t;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!live[h]) continue;
+            uint16_t *dst = p.out[r.sec] + tok[h] * r.N + col;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[0][j][2 * h], acc[0][j][2 * h + 1]);
+            if constexpr (VEC) {
+                if (col < r.N) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (col + i < r.N) dst[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+            }
+        }
+    };
+
+    // ---- x against A: `side` blocks of A at a time, 8 / side warps each
+    int side = 1;
+    while (side < 8 && side < blocks) side *= 2;
+    const int deep = kLoWarps / side, groups = (p.K / 32 + 3) / 4;
+    const int g0 = (int)((int64_t)groups * share / cl), g1 = (int)((int64_t)groups * (share + 1) / cl);
+    const bool wide = n > 8;
+    for (int b0 = 0; b0 < blocks; b0 += side) {
+        const int blk = b0 + warp / deep, sec = blk / max(nb, 1), r0 = blk % max(nb, 1) * 16;
+        float acc[2][4] = {};
+        if (blk < blocks) {
+            const uint16_t *a0 = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + 8 * t;
+            const uint16_t *a1 = a0 + (int64_t)8 * p.K;
+            const bool in0 = r0 + g < rank, in1 = r0 + g + 8 < rank;
+            const uint16_t *x0 = p.x + tok[0] * p.K + 8 * t, *x1 = p.x + tok[1] * p.K + 8 * t;
+            for (int gr = g0 + warp % deep; gr < g1; gr += deep) {
+                uint4 va[4], vb[4], xa[4], xb[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const bool ok = gr * 4 + c < p.K / 32;
+                    const int o = (gr * 4 + c) * 32;
+                    va[c] = lo_load(a0 + o, ok && in0);
+                    vb[c] = lo_load(a1 + o, ok && in1);
+                    xa[c] = lo_load(x0 + o, ok && live[0]);
+                    xb[c] = lo_load(x1 + o, ok && live[1]);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mma_bf16(acc[0], va[c].x, vb[c].x, va[c].y, vb[c].y, xa[c].x, xa[c].y);
+                    mma_bf16(acc[0], va[c].z, vb[c].z, va[c].w, vb[c].w, xa[c].z, xa[c].w);
+                    if (wide) {
+                        mma_bf16(acc[1], va[c].x, vb[c].x, va[c].y, vb[c].y, xb[c].x, xb[c].y);
+                        mma_bf16(acc[1], va[c].z, vb[c].z, va[c].w, vb[c].w, xb[c].z, xb[c].w);
+                    }
+                }
+            }
+        }
+        // [token][row]
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s_acc[warp][(8 * h + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[h][i];
+        __syncthreads();
+        for (int j = 0; j < side && b0 + j < blocks; ++j) {
+            float v = 0.f;
+            for (int w = 0; w < deep; ++w) v += s_acc[j * deep + w][tid];
+            red[(b0 + j) * 256 + tid] = v;
+        }
+        __syncthreads();
+    }
+    Loads first, second;
+    if (s0 + warp < s1) load(first, s0 + warp);
+
+    // ---- the CTAs' sums: units of a token's four rows
+    if (rank > 0) {
+        if (cl > 1) cluster_sync_all();
+        const float scale = p.scale ? p.scale[id] : 1.f;
+        const int units = p.nsec * nk * 64;
+        for (int u = (int)((int64_t)units * share / cl) + tid; u < (int)((int64_t)units * (share + 1) / cl); u += kLoThreads) {
+            const int sec = u / (nk * 64), blk = u / 64 % nk, m = u / 4 % 16, r4 = u % 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (blk < nb) {
+                const float *src = red + (sec * nb + blk) * 256 + m * 16 + 4 * r4;
+                if (cl == 1) {
+                    v = *reinterpret_cast<const float4 *>(src);
+                } else {
+                    for (int c = 0; c < cl; ++c) {
+                        const float4 f = ld_cluster_f32x4(src, c);
+                        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+                    }
+                }
+            }
+            v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+            // where the expansion's fragments have it
+            const int r = 16 * blk + 4 * r4;
+            const int ks = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2, ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8), h = m / 8;
+            const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
+            const uint32_t l0 = pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0));
+            const uint32_t l1 = pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1));
+            uint32_t *dh = reinterpret_cast<uint32_t *>(&frag[sec * nk + ks].hi[ln]) + h;
+            uint32_t *dl = reinterpret_cast<uint32_t *>(&frag[sec * nk + ks].lo[ln]) + h;
+            for (int c = 0; c < cl; ++c) {
+                uint32_t *rh = cl > 1 ? cluster_ptr(dh, c) : dh, *rl = cl > 1 ? cluster_ptr(dl, c) : dl;
+                rh[0] = h0;
+                rh[2] = h1;
+                rl[0] = l0;
+                rl[2] = l1;
+            }
+        }
+        if (cl > 1)
+            cluster_sync_all();
+        else
+            __syncthreads();
+    }
+
+    // ---- the outputs, two steps' loads in turn
+    for (int step = s0 + warp; step < s1; step += 2 * kLoWarps) {
+        const bool more = step + kLoWarps < s1;
+        if (more) load(second, step + kLoWarps);
+        use(first, step);
+        if (!more) break;
+        if (step + 2 * kLoWarps < s1) load(first, step + 2 * kLoWarps);
+        use(second, step + kLoWarps);
+    }
+}
+
 // ---------------------------------------------------------------- host side
 static int lora_split(int64_t M, int K, int nsec, int rank, int adapters) {
     const int64_t tiles = std::min<int64_t>(M, adapters) + M / kLoTile;
@@ -362,6 +639,7 @@ static int lora_split(int64_t M, int K, int nsec, int rank, int adapters) {
 }
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters) {
+    if (M <= kLoSort) return 0;
     const int64_t m = std::min<int64_t>(M, kLoChunk);
     return (size_t)lora_split(m, (int)K, nsec, rank, adapters) * m * nsec * rank * sizeof(float);
 }
@@ -378,6 +656,38 @@ static cudaError_t pick_expand(const LoraParams &p, int grid, cudaStream_t st) {
                      : launch_expand<FEW, KS, true, false>(p, grid, st);
     return p.vec ? launch_expand<FEW, KS, false, true>(p, grid, st)
                  : launch_expand<FEW, KS, false, false>(p, grid, st);
+}
+
+template <int KS, bool SILU, bool VEC>
+static cudaError_t launch_few(const LoraParams &p, int tiles, cudaStream_t st) {
+    const void *kfn = reinterpret_cast<const void *>(lora_few_kernel<KS, SILU, VEC>);
+    const int nb = (p.rank + 15) / 16, nk = KS == 1 ? 1 : (nb + 1) & ~1;
+    const int smem = p.nsec * (nb * 256 * (int)sizeof(float) + nk * (int)sizeof(LoFragments));
+    cudaError_t e = allow_smem(kfn, kMaxSections * (8 * 1024 + 8 * (int)sizeof(LoFragments)));
+    if (e == cudaSuccess) e = allow_wide_clusters(kfn);
+    if (e != cudaSuccess) return e;
+    int cl = 1;
+    while (cl < 16 && tiles * cl * 2 <= 2 * num_sms()) cl *= 2;
+    return launch_pdl_cluster(kfn, (unsigned)(tiles * cl), (unsigned)cl, kLoThreads, (size_t)smem, st, p, cl);
+}
+template <int KS>
+static cudaError_t pick_few(const LoraParams &p, int tiles, cudaStream_t st) {
+    if (p.silu)
+        return p.vec ? launch_few<KS, true, true>(p, tiles, st) : launch_few<KS, true, false>(p, tiles, st);
+    return p.vec ? launch_few<KS, false, true>(p, tiles, st) : launch_few<KS, false, false>(p, tiles, st);
+}
+
+static cudaError_t launch_lora_few(LoraParams p, cudaStream_t st) {
+    const int tiles = std::min<int64_t>(p.M, std::min<int64_t>(p.M, (int64_t)p.adapters + 1) + p.M / kLoTile);
+    p.blocks = 0;
+    for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) {
+        p.sec_blocks[s] = (int)((p.sec_n[s] + 31) / 32);
+        p.blocks += p.sec_blocks[s];
+    }
+    return p.rank <= 16   ? pick_few<1>(p, tiles, st)
+           : p.rank <= 32 ? pick_few<2>(p, tiles, st)
+           : p.rank <= 64 ? pick_few<4>(p, tiles, st)
+                          : pick_few<8>(p, tiles, st);
 }
 
 template <bool FEW>
@@ -409,7 +719,7 @@ cudaError_t launch_lora(LoraParams p, int64_t M, cudaStream_t st) {
     p.ks = lora_split(std::min<int64_t>(M, kLoChunk), p.K, p.nsec, p.rank, p.adapters);
     for (int64_t m = 0; m < M; m += kLoChunk) {
         p.M = (int)std::min<int64_t>(kLoChunk, M - m);
-        const cudaError_t e = p.M <= kLoSort ? launch_lora_t<true>(p, st) : launch_lora_t<false>(p, st);
+        const cudaError_t e = p.M <= kLoSort ? launch_lora_few(p, st) : launch_lora_t<false>(p, st);
         if (e != cudaSuccess) return e;
         p.x += (int64_t)p.M * p.K;
         p.ids += p.M;

@@ -983,8 +983,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     }
 }
 
-// Clusters of more than eight CTAs, once per device and kernel.
-static cudaError_t allow_wide_clusters(const void *kernel) {
+
+cudaError_t allow_wide_clusters(const void *kernel) {
     static std::mutex mu;
     static std::set<std::pair<int, const void *>> done;
     int dev = 0;

@@ -12,13 +12,6 @@ namespace gwa {
 
 using u64 = unsigned long long;
 
-template <typename T>
-__device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
-    u64 a;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<u64>(local)), "r"(rank));
-    return reinterpret_cast<T *>(a);
-}
-
 // A row's weights.
 struct SmRow {
     float top, per;
@@ -117,11 +110,12 @@ struct SmPlan {
         const u64 w = SmRow{top, per}.mass(x);
         return w >= least ? w : 0;
     }
-    // its part, for tokens other than the cut's equals: zero where nothing is
-    // kept.  least_t: least times 2^-40 (a float holds it: it comes from one)
-    __device__ __forceinline__ float part(float x, float least_t) const {
+    // its part, zero where it is not kept.  least_t: least times 2^-40 (a float
+    // holds it: it comes from one)
+    __device__ __forceinline__ float part(float x, uint32_t token, float least_t) const {
         const float t = SmRow::part_of(SmRow{top, per}.expo(x));
-        return x > cut_x && t >= least_t ? t : 0.f;
+        const bool in = x > cut_x || (x == cut_x && token <= cut_idx);
+        return in && t >= least_t ? t : 0.f;
     }
 };
 

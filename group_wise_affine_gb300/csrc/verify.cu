@@ -27,13 +27,14 @@
 // scanned, and one warp looks for the token in the piece that holds the drawn
 // mass.
 #include <algorithm>
+#include <type_traits>
 
 #include "sample.cuh"
 
 namespace gwa {
 
-constexpr int kVfThreads = 512, kVfWarps = kVfThreads / 32;
-constexpr int kVfMaxCluster = 8;
+constexpr int kVfThreads = 256, kVfWarps = kVfThreads / 32;
+constexpr int kVfMaxCluster = 16;
 constexpr int kVfPiece = 256;                           // tokens
 constexpr int kVfPieces = 524288 / kVfPiece;            // of a CTA, at most
 constexpr int kVfScan = kVfPieces / kVfThreads;         // of a thread
@@ -53,8 +54,7 @@ struct VfMass {
     SmPlan p, q;
     float least_p, least_q;  // times 2^-40
     float hi, lo;            // SP / SQ = hi + lo
-    int kind;
-    int64_t drop;
+    int kind, drop;
     __device__ __forceinline__ void prepare() {
         least_p = (float)p.least * 0x1p-40f;
         least_q = (float)q.least * 0x1p-40f;
@@ -67,24 +67,18 @@ struct VfMass {
         lo = __fdiv_rn(__ll2float_rn((long long)left), __ull2float_rn(q.total)) *
              __uint_as_float((uint32_t)(127 + e) << 23);
     }
-    __device__ __forceinline__ float kept(const SmPlan &s, float least, float x, int64_t token) const {
-        const float t = s.part(x, least);
-        // the cut's equals, up to its token (-inf's mass is zero anyway)
-        if (x == s.cut_x && x > -INFINITY)
-            return s.kept(x, (uint32_t)token) ? SmRow::part_of(SmRow{s.top, s.per}.expo(x)) : 0.f;
-        return t;
-    }
-    __device__ __forceinline__ float of(float xp, float xq, int64_t token) const {
-        const float a = kept(p, least_p, xp, token);
-        if (kind == 0) return a;
-        if (kind == 1) return token == drop ? 0.f : a;
-        const float b = kept(q, least_q, xq, token);
+    template <int KIND>
+    __device__ __forceinline__ float of(float xp, float xq, int token) const {
+        const float a = p.part(xp, (uint32_t)token, least_p);
+        if (KIND == 0) return a;
+        if (KIND == 1) return token == drop ? 0.f : a;
+        const float b = q.part(xq, (uint32_t)token, least_q);
         return fmaxf(a - fmaf(b, hi, b * lo), 0.f);
     }
 };
 
 template <bool BF16>
-__global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int cl) {
+__global__ void __launch_bounds__(kVfThreads, 4) verify_kernel(VerifyParams p, int cl) {
     constexpr unsigned FULL = 0xffffffffu;
     using Row = VfRow<BF16>;
     using Raw = typename Row::Raw;
@@ -176,30 +170,43 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int 
     }
     w.prepare();
     const Row rp = row_of(at), rq = w.kind == 2 ? draft_of(at) : rp;
-    const int64_t per_cta = (p.V + cl - 1) / cl;
-    const int64_t lo = min(p.V, rank * per_cta), hi = min(p.V, lo + per_cta);
-    const int pieces = (int)((hi - lo + kVfPiece - 1) / kVfPiece);
+    const int V = (int)p.V, per_cta = (V + cl - 1) / cl;
+    const int lo = min(V, rank * per_cta), hi = min(V, lo + per_cta);
+    const int pieces = (hi - lo + kVfPiece - 1) / kVfPiece;
     constexpr int PER = kVfPiece / 32;  // tokens of a lane and piece
+    auto fetch = [&](float (&x)[PER], const Row &row, int i0) {
+        const Row from{row.x + i0};
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[j] = i0 + 32 * j < hi ? from.at(32 * j) : -INFINITY;
+    };
+    auto each_kind = [&](auto body) {
+        if (w.kind == 2)
+            body(std::integral_constant<int, 2>{});
+        else if (w.kind == 1)
+            body(std::integral_constant<int, 1>{});
+        else
+            body(std::integral_constant<int, 0>{});
+    };
     const float u = p.u_draw[b];
     while (true) {
-        for (int c = warp; c < pieces; c += kVfWarps) {
-            const int64_t i0 = lo + (int64_t)c * kVfPiece + lane;
-            float xp[PER], xq[PER];
+        each_kind([&](auto kind_t) {
+            constexpr int kind = decltype(kind_t)::value;
+            for (int c = warp; c < pieces; c += kVfWarps) {
+                const int i0 = lo + c * kVfPiece + lane;
+                float xp[PER], xq[PER] = {};
+                fetch(xp, rp, i0);
+                if (kind == 2) fetch(xq, rq, i0);
+                MassSum sum;
 #pragma unroll
-            for (int j = 0; j < PER; ++j) xp[j] = i0 + 32 * j < hi ? rp.at(i0 + 32 * j) : -INFINITY;
-            if (w.kind == 2)
-#pragma unroll
-                for (int j = 0; j < PER; ++j) xq[j] = i0 + 32 * j < hi ? rq.at(i0 + 32 * j) : -INFINITY;
-            MassSum sum;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) sum.add(w.of(xp[j], xq[j], i0 + 32 * j));
-            // (the constants that the words carry come off once a lane, before
-            // the lanes' sums, which then have room)
-            const u64 mine = sum.total(PER);
-            const uint32_t low = __reduce_add_sync(FULL, (uint32_t)mine & 0xfffffu);
-            const uint32_t high = __reduce_add_sync(FULL, (uint32_t)(mine >> 20));
-            if (lane == 0) s_piece[c] = ((u64)high << 20) + low;
-        }
+                for (int j = 0; j < PER; ++j) sum.add(w.template of<kind>(xp[j], xq[j], i0 + 32 * j));
+                // (the constants that the words carry come off once a lane,
+                // before the lanes' sums, which then have room)
+                const u64 mine = sum.total(PER);
+                const uint32_t low = __reduce_add_sync(FULL, (uint32_t)mine & 0xfffffu);
+                const uint32_t high = __reduce_add_sync(FULL, (uint32_t)(mine >> 20));
+                if (lane == 0) s_piece[c] = ((u64)high << 20) + low;
+            }
+        });
         __syncthreads();
         // ---- the pieces' sums in order, those of the CTA and of the cluster
         u64 own[kVfScan], mine = 0;
@@ -249,24 +256,24 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyParams p, int 
         }
         __syncthreads();
         if (s_at < 0 || warp > 0) return;
-        const int64_t i0 = lo + (int64_t)s_at * kVfPiece + lane;
-        float xp[PER], xq[PER];
+        each_kind([&](auto kind_t) {
+            constexpr int kind = decltype(kind_t)::value;
+            const int i0 = lo + s_at * kVfPiece + lane;
+            float xp[PER], xq[PER] = {};
+            fetch(xp, rp, i0);
+            if (kind == 2) fetch(xq, rq, i0);
+            u64 sum = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            xp[j] = i0 + 32 * j < hi ? rp.at(i0 + 32 * j) : -INFINITY;
-            xq[j] = w.kind == 2 && i0 + 32 * j < hi ? rq.at(i0 + 32 * j) : -INFINITY;
-        }
-        u64 sum = 0;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const u64 up = sum + warp_scan(SmRow::whole(w.of(xp[j], xq[j], i0 + 32 * j)));
-            const unsigned past = __ballot_sync(FULL, up > s_left);
-            if (past) {
-                if (lane == __ffs(past) - 1) p.token[at] = (int32_t)(i0 + 32 * j);
-                return;
+            for (int j = 0; j < PER; ++j) {
+                const u64 up = sum + warp_scan(SmRow::whole(w.template of<kind>(xp[j], xq[j], i0 + 32 * j)));
+                const unsigned past = __ballot_sync(FULL, up > s_left);
+                if (past) {
+                    if (lane == __ffs(past) - 1) p.token[at] = i0 + 32 * j;
+                    return;
+                }
+                sum = __shfl_sync(FULL, up, 31);
             }
-            sum = __shfl_sync(FULL, up, 31);
-        }
+        });
         return;
     }
 }
@@ -275,10 +282,14 @@ size_t verify_workspace_bytes(int64_t rows) { return (size_t)rows * 2 * sizeof(S
 
 template <bool BF16>
 static cudaError_t launch_verify_t(const VerifyParams &v, cudaStream_t st) {
+    const void *kfn = reinterpret_cast<const void *>(verify_kernel<BF16>);
+    const cudaError_t e = allow_wide_clusters(kfn);
+    if (e != cudaSuccess) return e;
+    // Four CTAs an SM.  64 sequences of 151669 tokens, both kernels: clusters of
+    // 4 CTAs 162 us, 8 144, 16 148; half as many CTAs of twice the threads 148.
     int cl = 1;
-    while (cl < kVfMaxCluster && (int64_t)v.batch * cl * 2 <= 2 * num_sms() && v.V / (2 * cl) >= 4096) cl *= 2;
-    return launch_pdl_cluster(reinterpret_cast<const void *>(verify_kernel<BF16>), (unsigned)(v.batch * cl),
-                              (unsigned)cl, kVfThreads, 0, st, v, cl);
+    while (cl < kVfMaxCluster && (int64_t)v.batch * cl * 2 <= 4 * num_sms() && v.V / (2 * cl) >= 4096) cl *= 2;
+    return launch_pdl_cluster(kfn, (unsigned)(v.batch * cl), (unsigned)cl, kVfThreads, 0, st, v, cl);
 }
 
 cudaError_t launch_verify(const SampleParams &s, const VerifyParams &v, bool bf16, cudaStream_t st) {
