@@ -944,7 +944,7 @@ def _lora_inputs(x, lora, ids, sizes, base, workspace, stream):
                          f"{lora.N} outputs together")
     for i, (t, n) in enumerate(zip(base, sizes)):
         _check_out(t, M * n, f"section {i}")
-    if workspace is None and M > 256:
+    if workspace is None and M:
         n = int(load().gwa_lora_workspace_bytes(lora.c, M))
         workspace = _new(max(n, 16), torch.uint8, x.device, stream)
     return M, workspace  # (alive until the call is enqueued)

@@ -1178,7 +1178,7 @@ size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M) {
     g_last_error.clear();
     LoraParams p{};
     if (check_lora(lora, M, &p, "gwa_lora_workspace_bytes")) return 0;
-    return lora_workspace_bytes(M, lora.K, lora.sections, lora.rank, lora.adapters);
+    return M == 0 ? 0 : lora_workspace_bytes(M, lora.K, lora.sections, lora.rank, lora.adapters);
 }
 
 static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *ids,
@@ -1203,7 +1203,7 @@ static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *
         if (s < outs && p.base[s] != p.out[s]) p.in_place = false;
     }
     const size_t need = lora_workspace_bytes(M, p.K, p.nsec, p.rank, p.adapters);
-    if (need > 0 && (!workspace || workspace_bytes < need))
+    if (!workspace || workspace_bytes < need)
         return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn,
                     need, workspace_bytes);
     if (!aligned(workspace, 16))

@@ -157,7 +157,7 @@ struct LoraParams {
     bool in_place;          // out is base: tokens without an adapter stay
     int32_t *status;
     float *part;            // [ks][M][nsec][rank], see lora_shrink_kernel
-    int ks;                 // shares of K
+    int ks, share;          // shares of K, and inputs of one
     int steps;              // of a warp's block of outputs
     int blocks, sec_blocks[kMaxSections];
 };

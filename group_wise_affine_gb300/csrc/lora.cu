@@ -36,18 +36,20 @@ template <bool FEW>
 struct LoTiles {
     uint16_t start[(FEW ? kLoSort : kLoChunk) + 1];
     uint16_t order[FEW ? kLoSort : 1];
-    int key[FEW ? kLoSort : 1];
+    __align__(16) int key[FEW ? kLoSort : 1];  // of the places: adapter
+    int rank[FEW ? kLoSort : 1];               // and its rank
+    int base[FEW ? kLoSort + 1 : 1];           // of the tiles: 16-row blocks of A before it
     int w_max[kLoWarps], w_sum[kLoWarps];
     __device__ __forceinline__ int token(int place) const { return FEW ? order[place] : place; }
 };
 
 // A token's adapter, -1 for none.
 __device__ __forceinline__ int lo_id(const LoraParams &p, int tok) {
-    const int id = p.ids[tok];
+    const int id = __ldcg(p.ids + tok);
     return (unsigned)id < (unsigned)p.adapters ? id : -1;
 }
 __device__ __forceinline__ int lo_rank(const LoraParams &p, int id) {
-    return id < 0 ? 0 : p.ranks ? min(max(p.ranks[id], 0), p.rank) : p.rank;
+    return id < 0 ? 0 : p.ranks ? min(max(__ldcg(p.ranks + id), 0), p.rank) : p.rank;
 }
 
 // Cuts the tokens into tiles (all threads of the CTA); returns their number.
@@ -60,17 +62,20 @@ __device__ int lo_tiles(const LoraParams &p, LoTiles<FEW> &sh) {
     if constexpr (FEW) {
         const int mine = tid < p.M ? lo_id(p, tid) : 0x7fffffff;
         if (tid < p.M && blockIdx.x == 0 && p.status && p.ids[tid] >= p.adapters) atomicOr(p.status, 1);
+        const int rank = tid < p.M ? lo_rank(p, mine) : 0;  // (there by the end of the sort)
         sh.key[tid] = mine;
         __syncthreads();
         int at = 0;
-        for (int j = 0; j < p.M; ++j) {
-            const int k = sh.key[j];
-            at += k < mine || (k == mine && j < tid);
+        for (int j = 0; j < p.M; j += 4) {
+            const int4 k = *reinterpret_cast<const int4 *>(sh.key + j);
+            at += (k.x < mine || (k.x == mine && j < tid)) + (k.y < mine || (k.y == mine && j + 1 < tid)) +
+                  (k.z < mine || (k.z == mine && j + 2 < tid)) + (k.w < mine || (k.w == mine && j + 3 < tid));
         }
         __syncthreads();
         if (tid < p.M) {
             sh.order[at] = (uint16_t)tid;
             sh.key[at] = mine;
+            sh.rank[at] = rank;
         }
         __syncthreads();
         id[0] = sh.key[tid];
@@ -354,208 +359,68 @@ __global__ void __launch_bounds__(kLoThreads) lora_expand_kernel(LoraParams p) {
 }
 
 // ------------------------------------------------------------ few tokens
-// Both products in one launch: a cluster of CTAs a tile.  Each CTA takes a
-// share of K for all of the adapter's rows; the shares' sums go round through
-// distributed shared memory, each CTA adding up a part and handing it to all as
-// MMA fragments (hi and lo bf16 parts); then each takes a share of the outputs.
-// The outputs' first loads (base and B) are on their way before the sums are.
-//
-// Fragments in shared memory: of a section's k step 32 lanes' hi words, then
-// their lo words.
-struct LoFragments {
-    uint4 hi[32], lo[32];
-};
-
-template <int KS, bool SILU, bool VEC>
-__global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) lora_few_kernel(LoraParams p, int cl) {
-    constexpr int S = SILU ? 2 : 1, Q = KS == 1 ? 1 : KS / 2;  // Q: B's loads of a row
-    extern __shared__ __align__(16) unsigned char lo_raw[];
+// part[k][m][s][r]: share k's sum of A x.  A CTA's unit is 16 rows of an
+// adapter's A and a share of K for a tile; its warps take 256 inputs at a time
+// (a warp's loads all at once, straight from global memory as MMA fragments: a
+// lane's 16 bytes are the k positions of two MMAs, in the same order on both
+// sides).  The shares depend on K alone, and so does the order of a token's sums.
+__global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraParams p) {
     __shared__ LoTiles<true> sh;
     __shared__ float s_acc[kLoWarps][16 * kLoTile];
+    __shared__ int s_sum[kLoWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
-    const int share = cl > 1 ? (int)cluster_rank() : 0;
-    if (tid == 0) pdl_launch_dependents();
     pdl_wait_primary();
-    const int tiles = lo_tiles<true, kLoTile>(p, sh), tile = blockIdx.x / cl;
-    if (tile >= tiles) return;  // (the whole cluster)
-    const int at = sh.start[tile], n = sh.start[tile + 1] - at;
-    const int id = lo_id(p, sh.token(at)), rank = lo_rank(p, id);
-    if (rank == 0 && p.in_place) return;
-    const int nb = (rank + 15) / 16, blocks = p.nsec * nb;   // 16-row blocks of A
-    const int nk = KS == 1 ? 1 : (nb + 1) & ~1;              // k steps of a section
-    float *const red = reinterpret_cast<float *>(lo_raw);
-    LoFragments *const frag = reinterpret_cast<LoFragments *>(
-        lo_raw + (size_t)p.nsec * ((p.rank + 15) / 16) * 256 * sizeof(float));
-
-    // ---- this CTA's outputs: steps of 32, a warp every eighth
-    const int steps = p.blocks, s0 = (int)((int64_t)steps * share / cl), s1 = (int)((int64_t)steps * (share + 1) / cl);
-    const bool live[2] = {g < n, g + 8 < n};
-    const int64_t tok[2] = {sh.token(at + (live[0] ? g : 0)), sh.token(at + (live[1] ? g + 8 : 0))};
-    struct Step {
-        int sec;
-        int64_t n0, N;
-    };
-    struct Loads {
-        uint4 base[S][2], b[S][4][Q];  // (KS 1: half of b)
-    };
-    auto place = [&](int step) {
-        Step r;
-        r.sec = 0;
-        if constexpr (!SILU)
-            while (step >= p.sec_blocks[r.sec]) step -= p.sec_blocks[r.sec++];
-        r.n0 = (int64_t)step * 32;
-        r.N = p.sec_n[r.sec];
-        return r;
-    };
-    auto load = [&](Loads &l, int step) {
-        const Step r = place(step);
+    // (behind the wait: what the next kernel reads before its own wait was
+    // written before this one's)
+    if (tid == 0) pdl_launch_dependents();
+    const int tiles = lo_tiles<true, kLoTile>(p, sh);
+    // ---- units: blocks of the tiles in order, each in ks shares
+    const int mine = tid < tiles ? p.nsec * ((sh.rank[sh.start[tid]] + 15) / 16) : 0;
+    int incl = mine;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint16_t *brow = p.b + ((int64_t)max(id, 0) * p.N + p.sec_start[r.sec + s]) * p.rank;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int64_t c = r.n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    if constexpr (KS == 1) {
-                        uint2 w = make_uint2(0u, 0u);
-                        if (c < r.N && 4 * t < rank) w = *reinterpret_cast<const uint2 *>(brow + c * p.rank + 4 * t);
-                        l.b[s][j][q].x = w.x;
-                        l.b[s][j][q].y = w.y;
-                    } else {
-                        const int rr = 32 * q + 8 * t;
-                        l.b[s][j][q] = lo_load(brow + c * p.rank + rr, c < r.N && rr < rank);
-                    }
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t col = r.n0 + 8 * t;
-                const uint16_t *src = p.base[r.sec + s] + tok[h] * r.N + col;
-                if constexpr (VEC) {
-                    l.base[s][h] = lo_load(src, live[h] && col < r.N);
-                } else {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t x = live[h] && col + 2 * i < r.N ? src[2 * i] : 0u;
-                        const uint32_t y = live[h] && col + 2 * i + 1 < r.N ? src[2 * i + 1] : 0u;
-                        w[i] = x | (y << 16);
-                    }
-                    l.base[s][h] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            }
-        }
-    };
-    auto use = [&](Loads &l, int step) {
-        const Step r = place(step);
-        float acc[S][4][4];
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t w[4] = {l.base[s][h].x, l.base[s][h].y, l.base[s][h].z, l.base[s][h].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    acc[s][j][2 * h] = bf16_lo(w[j]);
-                    acc[s][j][2 * h + 1] = bf16_hi(w[j]);
-                }
-            }
-        if (rank % 8) {
-            // entries past the adapter's rank, whatever they hold, are zero
-            auto mask = [&](uint32_t &w, int k) { w = k + 1 < rank ? w : k < rank ? w & 0xffffu : 0u; };
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int q = 0; q < Q; ++q) {
-                        const int k = KS == 1 ? 4 * t : 32 * q + 8 * t;
-                        mask(l.b[s][j][q].x, k);
-                        mask(l.b[s][j][q].y, k + 2);
-                        if constexpr (KS > 1) {
-                            mask(l.b[s][j][q].z, k + 4);
-                            mask(l.b[s][j][q].w, k + 6);
-                        }
-                    }
-        }
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const LoFragments *f = frag + (r.sec + s) * nk;
-#pragma unroll
-            for (int q = 0; q < Q; ++q) {
-                if (32 * q >= rank) break;
-#pragma unroll
-                for (int b = 0; b < (KS == 1 ? 1 : 2); ++b) {
-                    const uint4 hi = f[(KS == 1 ? 0 : 2 * q) + b].hi[lane], lo = f[(KS == 1 ? 0 : 2 * q) + b].lo[lane];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 &w = l.b[s][j][q];
-                        const uint32_t b0 = b ? w.z : w.x, b1 = b ? w.w : w.y;
-                        mma_bf16(acc[s][j], hi.x, hi.y, hi.z, hi.w, b0, b1);
-                        mma_bf16(acc[s][j], lo.x, lo.y, lo.z, lo.w, b0, b1);
-                    }
-                }
-            }
-        }
-        if constexpr (SILU) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[0][j][i] = acc[0][j][i] / (1.f + __expf(-acc[0][j][i])) * acc[1][j][i];
-        }
-        const int64_t col = r.n0 + 8 * t;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (!live[h]) continue;
-            uint16_t *dst = p.out[r.sec] + tok[h] * r.N + col;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[0][j][2 * h], acc[0][j][2 * h + 1]);
-            if constexpr (VEC) {
-                if (col < r.N) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col + i < r.N) dst[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
-            }
-        }
-    };
-
-    // ---- x against A: `side` blocks of A at a time, 8 / side warps each
-    int side = 1;
-    while (side < 8 && side < blocks) side *= 2;
-    const int deep = kLoWarps / side, groups = (p.K / 32 + 3) / 4;
-    const int g0 = (int)((int64_t)groups * share / cl), g1 = (int)((int64_t)groups * (share + 1) / cl);
-    const bool wide = n > 8;
-    for (int b0 = 0; b0 < blocks; b0 += side) {
-        const int blk = b0 + warp / deep, sec = blk / max(nb, 1), r0 = blk % max(nb, 1) * 16;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_sum[warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += s_sum[w];
+    if (tid < tiles) sh.base[tid + 1] = incl;
+    if (tid == 0) sh.base[0] = 0;
+    __syncthreads();
+    const int units = sh.base[tiles] * p.ks;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int blk = u / p.ks, k = u - blk * p.ks;
+        int tile = 0;  // the last whose base is not past blk
+        for (int o = 128; o; o >>= 1)
+            if (tile + o < tiles && sh.base[tile + o] <= blk) tile += o;
+        const int at = sh.start[tile], n = sh.start[tile + 1] - at, id = sh.key[at], rank = sh.rank[at];
+        const int nb = (rank + 15) / 16, in = blk - sh.base[tile], sec = in / nb, r0 = (in - sec * nb) * 16;
+        const uint16_t *a = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + 8 * t;
+        const bool in0 = r0 + g < rank, in1 = r0 + g + 8 < rank, tok0 = g < n, tok1 = g + 8 < n;
+        const uint16_t *x0 = p.x + (int64_t)sh.token(at + (tok0 ? g : 0)) * p.K + 8 * t;
+        const uint16_t *x1 = p.x + (int64_t)sh.token(at + (tok1 ? g + 8 : 0)) * p.K + 8 * t;
         float acc[2][4] = {};
-        if (blk < blocks) {
-            const uint16_t *a0 = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + 8 * t;
-            const uint16_t *a1 = a0 + (int64_t)8 * p.K;
-            const bool in0 = r0 + g < rank, in1 = r0 + g + 8 < rank;
-            const uint16_t *x0 = p.x + tok[0] * p.K + 8 * t, *x1 = p.x + tok[1] * p.K + 8 * t;
-            for (int gr = g0 + warp % deep; gr < g1; gr += deep) {
-                uint4 va[4], vb[4], xa[4], xb[4];
+        const int end = min(p.K, (k + 1) * p.share);
+        for (int i0 = k * p.share + warp * 256; i0 < end; i0 += kLoWarps * 256) {
+            uint4 va[8], vb[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const bool ok = gr * 4 + c < p.K / 32;
-                    const int o = (gr * 4 + c) * 32;
-                    va[c] = lo_load(a0 + o, ok && in0);
-                    vb[c] = lo_load(a1 + o, ok && in1);
-                    xa[c] = lo_load(x0 + o, ok && live[0]);
-                    xb[c] = lo_load(x1 + o, ok && live[1]);
-                }
+            for (int c = 0; c < 8; ++c) {
+                const bool ok = i0 + 32 * c < end;
+                va[c] = lo_load(a + i0 + 32 * c, ok && in0);
+                vb[c] = lo_load(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1);
+            }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    mma_bf16(acc[0], va[c].x, vb[c].x, va[c].y, vb[c].y, xa[c].x, xa[c].y);
-                    mma_bf16(acc[0], va[c].z, vb[c].z, va[c].w, vb[c].w, xa[c].z, xa[c].w);
-                    if (wide) {
-                        mma_bf16(acc[1], va[c].x, vb[c].x, va[c].y, vb[c].y, xb[c].x, xb[c].y);
-                        mma_bf16(acc[1], va[c].z, vb[c].z, va[c].w, vb[c].w, xb[c].z, xb[c].w);
-                    }
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && n <= 8) break;
+                uint4 x[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    x[c] = lo_load((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c < end && (h ? tok1 : tok0));
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    mma_bf16(acc[h], va[c].x, vb[c].x, va[c].y, vb[c].y, x[c].x, x[c].y);
+                    mma_bf16(acc[h], va[c].z, vb[c].z, va[c].w, vb[c].w, x[c].z, x[c].w);
                 }
             }
         }
@@ -566,84 +431,202 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
             for (int i = 0; i < 4; ++i)
                 s_acc[warp][(8 * h + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[h][i];
         __syncthreads();
-        for (int j = 0; j < side && b0 + j < blocks; ++j) {
+        const int m = tid / 16, r = tid % 16;
+        if (m < n && r0 + r < p.rank) {
             float v = 0.f;
-            for (int w = 0; w < deep; ++w) v += s_acc[j * deep + w][tid];
-            red[(b0 + j) * 256 + tid] = v;
+#pragma unroll
+            for (int w = 0; w < kLoWarps; ++w) v += s_acc[w][tid];
+            p.part[(((int64_t)k * p.M + sh.token(at + m)) * p.nsec + sec) * p.rank + r0 + r] = v;
         }
         __syncthreads();
     }
-    Loads first, second;
-    if (s0 + warp < s1) load(first, s0 + warp);
+}
 
-    // ---- the CTAs' sums: units of a token's four rows
-    if (rank > 0) {
-        if (cl > 1) cluster_sync_all();
-        const float scale = p.scale ? p.scale[id] : 1.f;
-        const int units = p.nsec * nk * 64;
-        for (int u = (int)((int64_t)units * share / cl) + tid; u < (int)((int64_t)units * (share + 1) / cl); u += kLoThreads) {
-            const int sec = u / (nk * 64), blk = u / 64 % nk, m = u / 4 % 16, r4 = u % 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (blk < nb) {
-                const float *src = red + (sec * nb + blk) * 256 + m * 16 + 4 * r4;
-                if (cl == 1) {
-                    v = *reinterpret_cast<const float4 *>(src);
-                } else {
-                    for (int c = 0; c < cl; ++c) {
-                        const float4 f = ld_cluster_f32x4(src, c);
-                        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+// out = base + scale B t.  A CTA's unit is a tile and some octets of steps of
+// 32 outputs of one section, a warp a step; t, summed over the shares, lies in
+// shared memory as fragments of the MMA's 16 rows, hi and lo bf16 parts.  B's
+// rows and the base come straight from global memory, the first of them before
+// the wait for t.  Lane t's outputs of a step are eight neighbours (column c of
+// the step's MMA j is output 8 (c / 2) + 2 j + c % 2).
+//
+// Fragments: of a section's k step, each lane's words 0 and 2 of the hi and of
+// the lo part, then its words 1 and 3.  Of a pair of k steps, lane t's ranks are
+// 8 t .. 8 t + 7.
+constexpr int kLoFrag = 64;  // 16-byte units of a k step
+
+template <int KS, bool SILU, bool VEC>
+__global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) lora_few_expand_kernel(LoraParams p) {
+    constexpr int S = SILU ? 2 : 1, Q = KS == 1 ? 1 : KS / 2;  // Q: B's loads of a row
+    __shared__ LoTiles<true> sh;
+    __shared__ uint4 frag[S * KS * kLoFrag];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
+    if (tid == 0) pdl_launch_dependents();
+    const int tiles = lo_tiles<true, kLoTile>(p, sh);
+    // ---- units of `run` octets
+    int octets = 0;
+    for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) octets += p.sec_blocks[s];
+    const int run = max(1, (int)(((int64_t)tiles * octets + gridDim.x - 1) / gridDim.x));
+    int per = 0;  // of a tile
+    for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) per += (p.sec_blocks[s] + run - 1) / run;
+    bool waited = false;
+    for (int64_t u = blockIdx.x; u < (int64_t)tiles * per; u += gridDim.x) {
+        const int tile = (int)(u / per);
+        int in = (int)(u - (int64_t)tile * per), sec = 0;
+        if constexpr (!SILU)
+            for (int c; in >= (c = (p.sec_blocks[sec] + run - 1) / run); ++sec) in -= c;
+        const int at = sh.start[tile], n = sh.start[tile + 1] - at, id = sh.key[at], rank = sh.rank[at];
+        if (rank == 0 && p.in_place) continue;
+        const bool live[2] = {g < n, g + 8 < n};
+        const int tok[2] = {sh.token(at + (live[0] ? g : 0)), sh.token(at + (live[1] ? g + 8 : 0))};
+        const int64_t N = p.sec_n[sec];
+        const int last = min(p.sec_blocks[sec], (in + 1) * run);
+        for (int oct = in * run; oct < last; ++oct) {
+            const int64_t n0 = ((int64_t)oct * kLoWarps + warp) * 32, col = n0 + 8 * t;
+            uint4 base[S][2], b[S][4][Q];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const int64_t c0 = n0 + 8 * (g >> 1) + (g & 1);  // of MMA j: c0 + 2 j
+                const uint16_t *brow = p.b + ((int64_t)max(id, 0) * p.N + p.sec_start[sec + s] + c0) * p.rank;
+#pragma unroll
+                for (int j = 0; j < 4; ++j, brow += 2 * p.rank)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int r = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                        const bool ok = c0 + 2 * j < N && r < rank;
+                        b[s][j][q] = make_uint4(0u, 0u, 0u, 0u);
+                        if constexpr (KS == 1) {
+                            if (ok) {
+                                const uint2 w = __ldcg(reinterpret_cast<const uint2 *>(brow + r));
+                                b[s][j][q].x = w.x;
+                                b[s][j][q].y = w.y;
+                            }
+                        } else {
+                            if (ok) b[s][j][q] = __ldcg(reinterpret_cast<const uint4 *>(brow + r));
+                        }
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint16_t *src = p.base[sec + s] + tok[h] * N + col;
+                    base[s][h] = make_uint4(0u, 0u, 0u, 0u);
+                    if constexpr (VEC) {
+                        if (live[h] && col < N) base[s][h] = __ldcg(reinterpret_cast<const uint4 *>(src));
+                    } else {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t x = live[h] && col + 2 * i < N ? __ldcg(src + 2 * i) : 0u;
+                            const uint32_t y = live[h] && col + 2 * i + 1 < N ? __ldcg(src + 2 * i + 1) : 0u;
+                            w[i] = x | (y << 16);
+                        }
+                        base[s][h] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }
-            v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
-            // where the expansion's fragments have it
-            const int r = 16 * blk + 4 * r4;
-            const int ks = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2, ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8), h = m / 8;
-            const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
-            const uint32_t l0 = pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0));
-            const uint32_t l1 = pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1));
-            uint32_t *dh = reinterpret_cast<uint32_t *>(&frag[sec * nk + ks].hi[ln]) + h;
-            uint32_t *dl = reinterpret_cast<uint32_t *>(&frag[sec * nk + ks].lo[ln]) + h;
-            for (int c = 0; c < cl; ++c) {
-                uint32_t *rh = cl > 1 ? cluster_ptr(dh, c) : dh, *rl = cl > 1 ? cluster_ptr(dl, c) : dl;
-                rh[0] = h0;
-                rh[2] = h1;
-                rl[0] = l0;
-                rl[2] = l1;
+            if (oct == in * run && rank > 0) {
+                // ---- t of this unit
+                if (!waited) pdl_wait_primary();
+                waited = true;
+                __syncthreads();  // (the last unit's is read)
+                const float scale = p.scale ? p.scale[id] : 1.f;
+                const int nk = KS == 1 ? 1 : ((rank + 31) / 32) * 2;
+                for (int i = tid; i < S * nk * 64; i += kLoThreads) {
+                    // four ranks of a token
+                    const int s = i / (nk * 64), j = i - s * nk * 64, m = j / (4 * nk), r = (j - m * 4 * nk) * 4;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (m < n && r < rank) {
+                        const float *src = p.part + ((int64_t)sh.token(at + m) * p.nsec + sec + s) * p.rank + r;
+#pragma unroll 4
+                        for (int k = 0; k < p.ks; ++k) {
+                            const float4 e = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * p.M * p.nsec * p.rank));
+                            v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
+                        }
+                    }
+                    v.x = v.x * scale;
+                    v.y = r + 1 < rank ? v.y * scale : 0.f;
+                    v.z = r + 2 < rank ? v.z * scale : 0.f;
+                    v.w = r + 3 < rank ? v.w * scale : 0.f;
+                    const int ks = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2;
+                    const int ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8);
+                    const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
+                    frag[(s * KS + ks) * kLoFrag + m / 8 * 32 + ln] =
+                        make_uint4(h0, h1, pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
+                                   pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1)));
+                }
+                __syncthreads();
+            }
+            if (rank % 8) {
+                // entries past the adapter's rank, whatever they hold, are zero
+                auto mask = [&](uint32_t &w, int k) { w = k + 1 < rank ? w : k < rank ? w & 0xffffu : 0u; };
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) {
+                            const int k = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                            mask(b[s][j][q].x, k);
+                            mask(b[s][j][q].y, k + 2);
+                            if constexpr (KS > 1) {
+                                mask(b[s][j][q].z, k + 4);
+                                mask(b[s][j][q].w, k + 6);
+                            }
+                        }
+            }
+            float acc[S][4][4];
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w[4] = {base[s][h].x, base[s][h].y, base[s][h].z, base[s][h].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[s][j][2 * h] = bf16_lo(w[j]);
+                        acc[s][j][2 * h + 1] = bf16_hi(w[j]);
+                    }
+                }
+                const uint4 *fr = frag + s * KS * kLoFrag + lane;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    if (16 * (KS == 1 ? k : k & ~1) >= rank) break;
+                    const uint4 even = fr[k * kLoFrag], odd = fr[k * kLoFrag + 32];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 &w = b[s][j][KS == 1 ? 0 : k / 2];
+                        const uint32_t b0 = k & 1 ? w.z : w.x, b1 = k & 1 ? w.w : w.y;
+                        mma_bf16(acc[s][j], even.x, odd.x, even.y, odd.y, b0, b1);
+                        mma_bf16(acc[s][j], even.z, odd.z, even.w, odd.w, b0, b1);
+                    }
+                }
+            }
+            if constexpr (SILU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[0][j][i] = __fdividef(acc[0][j][i], 1.f + __expf(-acc[0][j][i])) * acc[1][j][i];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (!live[h]) continue;
+                uint16_t *dst = p.out[sec] + tok[h] * N + col;
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[0][j][2 * h], acc[0][j][2 * h + 1]);
+                if constexpr (VEC) {
+                    if (col < N) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col + i < N) dst[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
+                }
             }
         }
-        if (cl > 1)
-            cluster_sync_all();
-        else
-            __syncthreads();
     }
-
-    // ---- the outputs, two steps' loads in turn
-    for (int step = s0 + warp; step < s1; step += 2 * kLoWarps) {
-        const bool more = step + kLoWarps < s1;
-        if (more) load(second, step + kLoWarps);
-        use(first, step);
-        if (!more) break;
-        if (step + 2 * kLoWarps < s1) load(first, step + 2 * kLoWarps);
-        use(second, step + kLoWarps);
-    }
+    // (what runs next waits for this kernel alone)
+    pdl_wait_primary();
 }
 
 // ---------------------------------------------------------------- host side
-static int lora_split(int64_t M, int K, int nsec, int rank, int adapters) {
-    const int64_t tiles = std::min<int64_t>(M, adapters) + M / kLoTile;
-    const int64_t units = std::max<int64_t>(1, tiles * nsec * ((rank + 15) / 16));
-    int ks = 1;
-    while (ks < 8 && units * ks * 2 <= 2 * num_sms() && K / (2 * ks) >= 512) ks *= 2;
-    return ks;
-}
-
-size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters) {
-    if (M <= kLoSort) return 0;
-    const int64_t m = std::min<int64_t>(M, kLoChunk);
-    return (size_t)lora_split(m, (int)K, nsec, rank, adapters) * m * nsec * rank * sizeof(float);
-}
-
 template <bool FEW, int KS, bool SILU, bool VEC>
 static cudaError_t launch_expand(const LoraParams &p, int grid, cudaStream_t st) {
     return launch_pdl(reinterpret_cast<const void *>(lora_expand_kernel<FEW, KS, SILU, VEC>), dim3(grid),
@@ -659,35 +642,40 @@ static cudaError_t pick_expand(const LoraParams &p, int grid, cudaStream_t st) {
 }
 
 template <int KS, bool SILU, bool VEC>
-static cudaError_t launch_few(const LoraParams &p, int tiles, cudaStream_t st) {
-    const void *kfn = reinterpret_cast<const void *>(lora_few_kernel<KS, SILU, VEC>);
-    const int nb = (p.rank + 15) / 16, nk = KS == 1 ? 1 : (nb + 1) & ~1;
-    const int smem = p.nsec * (nb * 256 * (int)sizeof(float) + nk * (int)sizeof(LoFragments));
-    cudaError_t e = allow_smem(kfn, kMaxSections * (8 * 1024 + 8 * (int)sizeof(LoFragments)));
-    if (e == cudaSuccess) e = allow_wide_clusters(kfn);
-    if (e != cudaSuccess) return e;
-    int cl = 1;
-    while (cl < 16 && tiles * cl * 2 <= 2 * num_sms()) cl *= 2;
-    return launch_pdl_cluster(kfn, (unsigned)(tiles * cl), (unsigned)cl, kLoThreads, (size_t)smem, st, p, cl);
+static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
+    return launch_pdl(reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC>), dim3(grid),
+                      kLoThreads, 0, st, p);
 }
 template <int KS>
-static cudaError_t pick_few(const LoraParams &p, int tiles, cudaStream_t st) {
+static cudaError_t pick_few(const LoraParams &p, int grid, cudaStream_t st) {
     if (p.silu)
-        return p.vec ? launch_few<KS, true, true>(p, tiles, st) : launch_few<KS, true, false>(p, tiles, st);
-    return p.vec ? launch_few<KS, false, true>(p, tiles, st) : launch_few<KS, false, false>(p, tiles, st);
+        return p.vec ? launch_few<KS, true, true>(p, grid, st) : launch_few<KS, true, false>(p, grid, st);
+    return p.vec ? launch_few<KS, false, true>(p, grid, st) : launch_few<KS, false, false>(p, grid, st);
 }
 
+// A share of K: 2048 inputs (a CTA's loads at once), more where there would be
+// more than eight.
+static int lora_share(int K) { return std::max(2048, ((K + 7) / 8 + 255) / 256 * 256); }
+
 static cudaError_t launch_lora_few(LoraParams p, cudaStream_t st) {
-    const int tiles = std::min<int64_t>(p.M, std::min<int64_t>(p.M, (int64_t)p.adapters + 1) + p.M / kLoTile);
-    p.blocks = 0;
+    // (no more tiles than these)
+    const int64_t tiles = std::min<int64_t>(p.M, std::min<int64_t>(p.M, (int64_t)p.adapters + 1) + p.M / kLoTile);
+    const int full = 2 * num_sms();
+    p.share = lora_share(p.K);
+    const int64_t down = tiles * p.nsec * ((p.rank + 15) / 16) * p.ks;
+    cudaError_t e = launch_pdl(reinterpret_cast<const void *>(lora_few_shrink_kernel),
+                               dim3((unsigned)std::min<int64_t>(full, down)), kLoThreads, 0, st, p);
+    if (e != cudaSuccess) return e;
+    int64_t octets = 0;
     for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) {
-        p.sec_blocks[s] = (int)((p.sec_n[s] + 31) / 32);
-        p.blocks += p.sec_blocks[s];
+        p.sec_blocks[s] = (int)((p.sec_n[s] + 32 * kLoWarps - 1) / (32 * kLoWarps));
+        octets += p.sec_blocks[s];
     }
-    return p.rank <= 16   ? pick_few<1>(p, tiles, st)
-           : p.rank <= 32 ? pick_few<2>(p, tiles, st)
-           : p.rank <= 64 ? pick_few<4>(p, tiles, st)
-                          : pick_few<8>(p, tiles, st);
+    const int grid = (int)std::min<int64_t>(full, tiles * octets);
+    return p.rank <= 16   ? pick_few<1>(p, grid, st)
+           : p.rank <= 32 ? pick_few<2>(p, grid, st)
+           : p.rank <= 64 ? pick_few<4>(p, grid, st)
+                          : pick_few<8>(p, grid, st);
 }
 
 template <bool FEW>
@@ -715,10 +703,28 @@ static cudaError_t launch_lora_t(LoraParams p, cudaStream_t st) {
                           : pick_expand<FEW, 8>(p, grid, st);
 }
 
+static int lora_split(int64_t M, int K, int nsec, int rank, int adapters) {
+    if (M <= kLoSort) return (K + lora_share(K) - 1) / lora_share(K);
+    const int64_t tiles = std::min<int64_t>(M, adapters) + M / kLoTile;
+    const int64_t units = std::max<int64_t>(1, tiles * nsec * ((rank + 15) / 16));
+    int ks = 1;
+    while (ks < 8 && units * ks * 2 <= 2 * num_sms() && K / (2 * ks) >= 512) ks *= 2;
+    return ks;
+}
+
+size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters) {
+    const int64_t m = std::min<int64_t>(M, kLoChunk);
+    const int64_t tail = M > m && M % kLoChunk <= kLoSort ? M % kLoChunk : 0;
+    auto bytes = [&](int64_t n) {
+        return (size_t)lora_split(n, (int)K, nsec, rank, adapters) * n * nsec * rank * sizeof(float);
+    };
+    return std::max(bytes(m), bytes(tail));
+}
+
 cudaError_t launch_lora(LoraParams p, int64_t M, cudaStream_t st) {
-    p.ks = lora_split(std::min<int64_t>(M, kLoChunk), p.K, p.nsec, p.rank, p.adapters);
     for (int64_t m = 0; m < M; m += kLoChunk) {
         p.M = (int)std::min<int64_t>(kLoChunk, M - m);
+        p.ks = lora_split(p.M, p.K, p.nsec, p.rank, p.adapters);
         const cudaError_t e = p.M <= kLoSort ? launch_lora_few(p, st) : launch_lora_t<false>(p, st);
         if (e != cudaSuccess) return e;
         p.x += (int64_t)p.M * p.K;

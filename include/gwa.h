@@ -572,8 +572,7 @@ typedef struct gwa_lora {
  *   base, out      host arrays of [M, size] bf16 buffers, 2-byte aligned
  *         (rows of 16-byte units are read faster); out_s may be base_s, and
  *         must not overlap anything else
- *   workspace  >= gwa_lora_workspace_bytes(lora, M), 16-byte aligned (NULL
- *         where that is 0: up to 256 tokens)
+ *   workspace  >= gwa_lora_workspace_bytes(lora, M), 16-byte aligned
  * Tokens of one adapter are computed together: up to 256 tokens in whatever
  * order they come, of more those that follow one another.  fp32 sums of exact
  * products; A x enters its product in two bf16 parts (2^-17 of it), and out is
@@ -597,8 +596,7 @@ int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
                           const uint16_t *up, uint16_t *h, void *workspace,
                           size_t workspace_bytes, int32_t *status,
                           void *stream);
-/* 0 for up to 256 tokens; also, with gwa_last_error, for adapters or M that the
- * calls refuse. */
+/* 0 (and gwa_last_error) for adapters or M that the calls refuse, and for M = 0. */
 size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M);
 
 /* Text of the last error raised on this thread ("" if none). */
