@@ -360,7 +360,8 @@ int gwa_pipeline_status(uint32_t *timeouts, int32_t reset) {
     if (e != cudaSuccess) return cuda_fail(e, "gwa_pipeline_status");
     *timeouts = group_timeouts(reset != 0) + stream_timeouts(reset != 0) +
                 moe_stream_timeouts(reset != 0) + qmm_timeouts(reset != 0) +
-                mma_timeouts(reset != 0) + prefill_timeouts(reset != 0);
+                mma_timeouts(reset != 0) + prefill_timeouts(reset != 0) +
+                lora_timeouts(reset != 0);
     e = cudaGetLastError();
     return e == cudaSuccess ? GWA_OK : cuda_fail(e, "gwa_pipeline_status");
 }
@@ -1178,7 +1179,7 @@ size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M) {
     g_last_error.clear();
     LoraParams p{};
     if (check_lora(lora, M, &p, "gwa_lora_workspace_bytes")) return 0;
-    return M == 0 ? 0 : lora_workspace_bytes(M, lora.K, lora.sections, lora.rank, lora.adapters);
+    return M == 0 ? 0 : lora_workspace_bytes(M, lora.K, lora.sections, lora.rank);
 }
 
 static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *ids,
@@ -1202,7 +1203,7 @@ static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *
             p.vec = false;
         if (s < outs && p.base[s] != p.out[s]) p.in_place = false;
     }
-    const size_t need = lora_workspace_bytes(M, p.K, p.nsec, p.rank, p.adapters);
+    const size_t need = lora_workspace_bytes(M, p.K, p.nsec, p.rank);
     if (!workspace || workspace_bytes < need)
         return fail(GWA_ERR_WORKSPACE, "%s: needs %zu bytes of workspace (got %zu)", fn,
                     need, workspace_bytes);
@@ -1213,9 +1214,7 @@ static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *
     p.x = x;
     p.ids = ids;
     p.status = status;
-    p.part = static_cast<float *>(workspace);
-    const cudaError_t e = launch_lora(p, M, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? GWA_OK : cuda_fail(e, fn);
+    return launch_lora(p, M, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora, const int32_t *ids,

@@ -156,13 +156,14 @@ struct LoraParams {
     bool silu, vec;         // vec: rows of 16-byte units
     bool in_place;          // out is base: tokens without an adapter stay
     int32_t *status;
-    float *part;            // [ks][M][nsec][rank], see lora_shrink_kernel
-    int ks, share;          // shares of K, and inputs of one
-    int steps;              // of a warp's block of outputs
-    int blocks, sec_blocks[kMaxSections];
+    float *part;            // [ks][M][nsec][rank], see the few tokens' kernel
+    int ks, share;          // shares of K (many tokens: at most), inputs of one
+    int32_t *shares;        // many tokens: how many there are
+    int sec_blocks[kMaxSections];  // blocks of a section's outputs
 };
-cudaError_t launch_lora(LoraParams p, int64_t M, cudaStream_t st);
-size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters);
+int launch_lora(LoraParams p, int64_t M, void *workspace, cudaStream_t st);  // a status
+size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank);
+unsigned int lora_timeouts(bool reset);
 
 // Launches `kernel` on `st` with programmatic stream serialization: it may
 // start while the previous kernel in the stream drains; the kernel itself

@@ -21,6 +21,8 @@
 #include "common.cuh"
 #include "internal.h"
 #include "mma.cuh"
+#include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace gwa {
 
@@ -142,220 +144,6 @@ __device__ int lo_tiles(const LoraParams &p, LoTiles<FEW> &sh) {
 
 __device__ __forceinline__ uint4 lo_load(const uint16_t *p, bool ok) {
     return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
-}
-
-// part[k][m][s][r]: split k's share of scale A x.  A unit is a tile, 16 rows
-// of one section's A and a share of K; a warp takes 128 inputs at a time, 16
-// rows of A against 8 or 16 tokens, both straight from global memory as MMA
-// fragments (a lane's 16 bytes are the k positions of two MMAs, in the same
-// order on both sides).
-template <bool FEW>
-__global__ void __launch_bounds__(kLoThreads, 2) lora_shrink_kernel(LoraParams p) {
-    __shared__ LoTiles<FEW> sh;
-    __shared__ float s_acc[kLoWarps][16 * kLoTile];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
-    if (tid == 0) pdl_launch_dependents();
-    pdl_wait_primary();
-    const int tiles = lo_tiles<FEW, kLoTile>(p, sh);
-    const int blocks = p.nsec * ((p.rank + 15) / 16), per = blocks * p.ks;
-    const int chunks = p.K / 32;
-    for (int64_t u = blockIdx.x; u < (int64_t)tiles * per; u += gridDim.x) {
-        const int tile = (int)(u / per), rem = (int)(u % per);
-        const int k = rem % p.ks, sec = rem / p.ks % p.nsec, r0 = rem / p.ks / p.nsec * 16;
-        const int at = sh.start[tile], n = sh.start[tile + 1] - at;
-        const int id = lo_id(p, sh.token(at)), rank = lo_rank(p, id);
-        if (r0 >= rank) continue;
-        const uint16_t *a0 = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + 8 * t;
-        const uint16_t *a1 = a0 + (int64_t)8 * p.K;
-        const bool in0 = r0 + g < rank, in1 = r0 + g + 8 < rank;
-        const bool tok0 = g < n, tok1 = g + 8 < n;
-        const uint16_t *x0 = p.x + (int64_t)sh.token(at + (tok0 ? g : 0)) * p.K + 8 * t;
-        const uint16_t *x1 = p.x + (int64_t)sh.token(at + (tok1 ? g + 8 : 0)) * p.K + 8 * t;
-        const bool wide = n > 8;
-        float acc[2][4] = {};
-        for (int c0 = (k * kLoWarps + warp) * 4; c0 < chunks; c0 += p.ks * kLoWarps * 4) {
-            uint4 va[4], vb[4], xa[4], xb[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const bool ok = c0 + c < chunks;
-                const int64_t o = (int64_t)(c0 + c) * 32;
-                va[c] = lo_load(a0 + o, ok && in0);
-                vb[c] = lo_load(a1 + o, ok && in1);
-                xa[c] = lo_load(x0 + o, ok && tok0);
-                xb[c] = lo_load(x1 + o, ok && tok1);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mma_bf16(acc[0], va[c].x, vb[c].x, va[c].y, vb[c].y, xa[c].x, xa[c].y);
-                mma_bf16(acc[0], va[c].z, vb[c].z, va[c].w, vb[c].w, xa[c].z, xa[c].w);
-                if (wide) {
-                    mma_bf16(acc[1], va[c].x, vb[c].x, va[c].y, vb[c].y, xb[c].x, xb[c].y);
-                    mma_bf16(acc[1], va[c].z, vb[c].z, va[c].w, vb[c].w, xb[c].z, xb[c].w);
-                }
-            }
-        }
-        // [token][row]
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                s_acc[warp][(8 * h + 2 * t + (i & 1)) * 16 + g + 8 * (i >> 1)] = acc[h][i];
-        __syncthreads();
-        const int tok = tid / 16, r = tid % 16;
-        if (tok < n && r0 + r < p.rank) {
-            float v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kLoWarps; ++w) v += s_acc[w][tid];
-            if (p.scale) v *= p.scale[id];
-            p.part[(((int64_t)k * p.M + sh.token(at + tok)) * p.nsec + sec) * p.rank + r0 + r] = v;
-        }
-        __syncthreads();
-    }
-}
-
-// out = base + B t.  A warp takes a tile and some steps of 32 outputs of one
-// section; t as fragments of the MMA's 16 rows, hi and lo bf16 parts, B's rows
-// straight from global memory.  Lane t's outputs of a step are eight
-// neighbours (column c of the step's MMA j is output 8 (c / 2) + 2 j + c % 2).
-template <bool FEW, int KS, bool SILU, bool VEC>
-__global__ void __launch_bounds__(kLoThreads) lora_expand_kernel(LoraParams p) {
-    constexpr int S = SILU ? 2 : 1;
-    __shared__ LoTiles<FEW> sh;
-    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    if (tid == 0) pdl_launch_dependents();
-    pdl_wait_primary();
-    const int tiles = lo_tiles<FEW, kLoTile>(p, sh);
-    const int64_t units = (int64_t)tiles * p.blocks;
-    for (int64_t u = (int64_t)blockIdx.x * kLoWarps + tid / 32; u < units; u += (int64_t)gridDim.x * kLoWarps) {
-        // few tokens: a CTA's warps side by side along one tile's outputs;
-        // many: a tile each, over the same outputs
-        const int tile = FEW ? (int)(u / p.blocks) : (int)(u % tiles);
-        int blk = FEW ? (int)(u % p.blocks) : (int)(u / tiles), sec = 0;
-        if constexpr (!SILU)
-            while (blk >= p.sec_blocks[sec]) blk -= p.sec_blocks[sec++];
-        const int at = sh.start[tile], n = sh.start[tile + 1] - at;
-        const int id = lo_id(p, sh.token(at)), rank = lo_rank(p, id);
-        if (rank == 0 && p.in_place) continue;
-        const int64_t N = p.sec_n[sec];
-        const bool live[2] = {g < n, g + 8 < n};
-        const int64_t tok[2] = {sh.token(at + (live[0] ? g : 0)), sh.token(at + (live[1] ? g + 8 : 0))};
-        // ---- t: of a pair of k steps, lane t's ranks are 8 t .. 8 t + 7
-        uint32_t hi[S][KS][4], lo[S][KS][4];
-#pragma unroll
-        for (int s = 0; s < S; ++s)
-#pragma unroll
-            for (int j = 0; j < KS; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = KS == 1 ? 4 * t : 32 * (j / 2) + 8 * t + 4 * (j & 1);
-                    float v[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (live[h] && r < rank) {
-                        const float *src = p.part + (tok[h] * p.nsec + sec + s) * p.rank + r;
-                        for (int k = 0; k < p.ks; ++k) {
-                            const float4 f = *reinterpret_cast<const float4 *>(src + (int64_t)k * p.M * p.nsec * p.rank);
-                            v[0] += f.x;
-                            v[1] += f.y;
-                            v[2] += f.z;
-                            v[3] += f.w;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (r + i >= rank) v[i] = 0.f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w = pack_bf16(v[2 * i], v[2 * i + 1]);
-                        hi[s][j][h + 2 * i] = w;
-                        lo[s][j][h + 2 * i] = pack_bf16(v[2 * i] - bf16_lo(w), v[2 * i + 1] - bf16_hi(w));
-                    }
-                }
-        const uint16_t *brow = p.b + ((int64_t)max(id, 0) * p.N + p.sec_start[sec]) * p.rank;
-        for (int step = 0; step < p.steps; ++step) {
-            const int64_t n0 = ((int64_t)blk * p.steps + step) * 32;
-            if (n0 >= N) break;
-            const int64_t col = n0 + 8 * t;
-            float acc[S][4][4];
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint16_t *src = p.base[sec + s] + tok[h] * N + col;
-                    if constexpr (VEC) {
-                        const uint4 v = lo_load(src, live[h] && col < N);
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[s][j][2 * h] = bf16_lo(w[j]);
-                            acc[s][j][2 * h + 1] = bf16_hi(w[j]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            acc[s][i / 2][2 * h + (i & 1)] =
-                                live[h] && col + i < N ? __uint_as_float((uint32_t)src[i] << 16) : 0.f;
-                    }
-                }
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t c = n0 + 8 * (g >> 1) + 2 * j + (g & 1);
-                    const uint16_t *b = brow + (s * N + c) * p.rank;
-                    // entries past the adapter's rank, whatever they hold, are zero
-                    auto mask = [&](uint32_t w, int r) {
-                        return r + 1 < rank ? w : r < rank ? w & 0xffffu : 0u;
-                    };
-                    if constexpr (KS == 1) {
-                        uint2 w = make_uint2(0u, 0u);
-                        if (c < N && 4 * t < rank) w = *reinterpret_cast<const uint2 *>(b + 4 * t);
-                        w.x = mask(w.x, 4 * t);
-                        w.y = mask(w.y, 4 * t + 2);
-                        mma_bf16(acc[s][j], hi[s][0][0], hi[s][0][1], hi[s][0][2], hi[s][0][3], w.x, w.y);
-                        mma_bf16(acc[s][j], lo[s][0][0], lo[s][0][1], lo[s][0][2], lo[s][0][3], w.x, w.y);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < KS / 2; ++q) {
-                            if (32 * q >= rank) break;
-                            const int r = 32 * q + 8 * t;
-                            uint4 w = lo_load(b + r, c < N && r < rank);
-                            if (rank % 8) {
-                                w.x = mask(w.x, r);
-                                w.y = mask(w.y, r + 2);
-                                w.z = mask(w.z, r + 4);
-                                w.w = mask(w.w, r + 6);
-                            }
-                            uint32_t(&h0)[4] = hi[s][2 * q], (&l0)[4] = lo[s][2 * q];
-                            uint32_t(&h1)[4] = hi[s][2 * q + 1], (&l1)[4] = lo[s][2 * q + 1];
-                            mma_bf16(acc[s][j], h0[0], h0[1], h0[2], h0[3], w.x, w.y);
-                            mma_bf16(acc[s][j], h1[0], h1[1], h1[2], h1[3], w.z, w.w);
-                            mma_bf16(acc[s][j], l0[0], l0[1], l0[2], l0[3], w.x, w.y);
-                            mma_bf16(acc[s][j], l1[0], l1[1], l1[2], l1[3], w.z, w.w);
-                        }
-                    }
-                }
-            if constexpr (SILU) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[0][j][i] = acc[0][j][i] / (1.f + __expf(-acc[0][j][i])) * acc[1][j][i];
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!live[h]) continue;
-                uint16_t *dst = p.out[sec] + tok[h] * N + col;
-                uint32_t w[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[0][j][2 * h], acc[0][j][2 * h + 1]);
-                if constexpr (VEC) {
-                    if (col < N) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + i < N) dst[i] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
-                }
-            }
-        }
-    }
 }
 
 // ------------------------------------------------------------ few tokens
@@ -626,21 +414,430 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
     pdl_wait_primary();
 }
 
-// ---------------------------------------------------------------- host side
-template <bool FEW, int KS, bool SILU, bool VEC>
-static cudaError_t launch_expand(const LoraParams &p, int grid, cudaStream_t st) {
-    return launch_pdl(reinterpret_cast<const void *>(lora_expand_kernel<FEW, KS, SILU, VEC>), dim3(grid),
-                      kLoThreads, 0, st, p);
+// ------------------------------------------------------------ many tokens
+// x against A on the 5th-generation tensor cores: D (128 tokens x C rows of A)
+// = x A^T, x and A by TMA in steps of 64 inputs, all sections' rows (up to 256)
+// at once, so that x is read once.  Tiles are runs of neighbours of one adapter;
+// of a short one only its rows, by sixteens, are copied, and what the MMA makes
+// of the others is not stored.  The bytes of x bound it; K is shared out over
+// so many CTAs that the last round is nearly full (lo_shares).  fp32 sums go to
+// part[k][m][s][r] (see the few tokens' kernel).
+//
+// Warps: 0 issues the copies, 1 the MMAs (a thread each), 4 to 7 bring the
+// results out, two accumulators in turn.  Every wait is bounded (2 s); one that
+// runs out is counted and the kernel unwinds.
+constexpr int kLtTile = 128, kLtStages = 6;  // (fewer where they do not fit)
+constexpr int kLtSmem = 200 * 1024;
+
+static __device__ unsigned int g_lora_timeouts;
+
+__device__ __noinline__ bool lt_wait_slow(uint64_t *bar, uint32_t parity, int *fail) {
+    if (mbar_wait_sleep(bar, parity)) return true;
+    atomicAdd(&g_lora_timeouts, 1u);
+    *fail = 1;
+    return false;
 }
-template <bool FEW, int KS>
-static cudaError_t pick_expand(const LoraParams &p, int grid, cudaStream_t st) {
-    if (p.silu)
-        return p.vec ? launch_expand<FEW, KS, true, true>(p, grid, st)
-                     : launch_expand<FEW, KS, true, false>(p, grid, st);
-    return p.vec ? launch_expand<FEW, KS, false, true>(p, grid, st)
-                 : launch_expand<FEW, KS, false, false>(p, grid, st);
+__device__ __forceinline__ bool lt_wait(uint64_t *bar, uint32_t parity, int *fail) {
+    return mbar_try_wait(bar, parity) || lt_wait_slow(bar, parity, fail);
+}
+__device__ __forceinline__ void lt_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
+// Shares of K for so many units: the fewest steps of 64 inputs in a CTA's row,
+// where a unit's start and end count as eight.
+__device__ __forceinline__ int lo_shares(int units, int ctas, int steps, int most) {
+    int best = 1, least = 0x7fffffff;
+    for (int k = 1; k <= most && k <= steps; ++k) {
+        const int cost = (units * k + ctas - 1) / ctas * ((steps + k - 1) / k + 8);
+        if (cost < least) {
+            least = cost;
+            best = k;
+        }
+    }
+    return best;
+}
+
+__global__ void __launch_bounds__(kLoThreads, 1)
+    lora_many_shrink_kernel(const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xmap16,
+                            const __grid_constant__ CUtensorMap amap, LoraParams p, int cols, int half, int stages) {
+    extern __shared__ __align__(1024) unsigned char lo_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(lo_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ LoTiles<false> sh;
+    __shared__ uint64_t full[kLtStages], empty[kLtStages], accfull[2], accfree[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail, s_issued;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    if (tid == 0) {
+        for (int i = 0; i < kLtStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accfree[i], 4);
+        }
+        fence_mbar_init();
+        s_fail = s_issued = 0;
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, 2 * half);
+    pdl_wait_primary();
+    if (tid == 0) pdl_launch_dependents();  // (see the few tokens' kernel)
+    tc_fence_before();
+    const int tiles = lo_tiles<false, kLtTile>(p, sh);  // (synchronizes)
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int rows = p.nsec * p.rank, passes = (rows + cols - 1) / cols, steps = (p.K + 63) / 64;
+    const int ks = lo_shares(tiles * passes, gridDim.x, steps, p.ks);
+    if (blockIdx.x == 0 && tid == 0) *p.shares = ks;
+    const int units = tiles * passes * ks;
+    const int stage_bytes = kLtTile * 128 + cols * 128;
+
+    struct Unit {
+        int at, n, id, row, k, c0, c1;
+    };
+    auto unit = [&](int u, Unit &w) {  // false: nothing to do
+        const int tile = u / (passes * ks), in = u - tile * passes * ks, pass = in / ks;
+        w.at = sh.start[tile];
+        w.n = sh.start[tile + 1] - w.at;
+        w.id = lo_id(p, w.at);
+        w.row = pass * cols;
+        w.k = in - pass * ks;
+        w.c0 = (int)((int64_t)steps * w.k / ks);
+        w.c1 = (int)((int64_t)steps * (w.k + 1) / ks);
+        return lo_rank(p, w.id) > 0;
+    };
+    Unit w;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                if (!unit(u, w)) continue;
+                const int arow = w.id * rows + w.row;
+                const bool whole = w.n == kLtTile;
+                const int boxes = (w.n + 15) / 16;
+                for (int c = w.c0; c < w.c1; ++c, ++it) {
+                    const uint32_t s = it % stages;
+                    if (it >= stages && !(ok = lt_wait(&empty[s], ((it / stages) & 1) ^ 1, &s_fail))) break;
+                    unsigned char *xs = smem + s * stage_bytes, *as = xs + kLtTile * 128;
+                    mbar_expect_tx(&full[s], (whole ? kLtTile : boxes * 16) * 128 + cols * 128);
+                    if (whole)
+                        tma_load_2d(xs, &xmap, c * 64, w.at, &full[s]);
+                    else
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(xs + b * 2048, &xmap16, c * 64, w.at + 16 * b, &full[s]);
+                    tma_load_2d(as, &amap, c * 64, arow, &full[s]);
+                    s_issued = it + 1;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // bf16 inputs, fp32 accumulators, both K-major, M = 128
+            const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) |
+                                   ((uint32_t)(kLtTile >> 4) << 24);
+            uint32_t it = 0, j = 0;
+            for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+                if (!unit(u, w)) continue;
+                const uint32_t buf = j & 1;
+                if (j >= 2 && !(ok = lt_wait(&accfree[buf], ((j >> 1) - 1) & 1, &s_fail))) break;
+                for (int c = w.c0; c < w.c1; ++c, ++it) {
+                    const uint32_t s = it % stages;
+                    if (!(ok = lt_wait(&full[s], (it / stages) & 1, &s_fail))) break;
+                    tc_fence_after();
+                    const uint64_t a = smem_desc_sw128(smem_u32(smem + s * stage_bytes));
+                    const uint64_t b = smem_desc_sw128(smem_u32(smem + s * stage_bytes + kLtTile * 128));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        lt_mma(tmem + buf * half, a + 2 * k, b + 2 * k, idesc, c > w.c0 || k > 0 ? 1u : 0u);
+                    tc_commit(&empty[s]);
+                }
+                if (!ok) break;
+                tc_commit(&accfull[buf]);
+                ++j;
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3, row = q * 32 + lane;
+        uint32_t j = 0;
+        for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+            if (!unit(u, w)) continue;
+            const uint32_t buf = j & 1;
+            ok = __all_sync(0xffffffffu, lt_wait(&accfull[buf], (j >> 1) & 1, &s_fail));
+            if (!ok) break;
+            tc_fence_after();
+            const int valid = min(cols, rows - w.row);
+            float *dst = p.part + ((int64_t)w.k * p.M + w.at + row) * rows + w.row;
+            for (int c = 0; c < valid && q * 32 < w.n; c += 16) {
+                float v[16];
+                tc_ld16(tmem + buf * half + c + ((uint32_t)(q * 32) << 16), v);
+                if (row < w.n)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        if (c + i < valid)
+                            *reinterpret_cast<float4 *>(dst + c + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accfree[buf]);
+            ++j;
+        }
+    }
+    // ---- teardown: without a wait that ran out, every copy and MMA was waited for
+    tc_fence_before();
+    __syncthreads();
+    if (s_fail) {
+        if (tid == 0)
+            for (int k = max(0, s_issued - stages); k < s_issued; ++k)
+                if (!mbar_wait(&full[k % stages], (k / stages) & 1)) break;
+        if (tid == 32) {
+            tc_commit(&accfull[0]);  // completes after every MMA this thread issued
+            mbar_wait(&accfull[0], 0, 1000000ull);
+            mbar_wait(&accfull[0], 1, 1000000ull);
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 2 * half);
+}
+
+// out = base + scale B t.  A warp's unit is a tile of 16 MT tokens and some
+// steps of 32 outputs of one section; the eight warps of a CTA take
+// neighbouring tiles of the same outputs, so that B comes out of the L1 cache.
+// t as in the few tokens' kernel, each warp's own in shared memory; the next
+// step's base is on its way during the products, its B during the stores.
+// Warp-level MMAs serve: the work is bound by the bytes of base and output (at
+// rank 64 the products are 2 x 64 x 2 FLOP for each 4 bytes).
+template <int KS, bool SILU>
+struct LoMany {
+    static constexpr int S = SILU ? 2 : 1, MT = KS * S <= 4 && !SILU ? 2 : 1, TM = 16 * MT;
+    static constexpr int FRAGS = MT * S * KS * kLoFrag;   // of a warp, 16 bytes each
+    static constexpr int SMEM = kLoWarps * FRAGS * 16;
+    static constexpr int CTAS = KS * S <= 4 ? 2 : 1;
+};
+template <int KS, bool SILU, bool VEC>
+__global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_expand_kernel(LoraParams p) {
+    using L = LoMany<KS, SILU>;
+    constexpr int S = L::S, MT = L::MT, Q = KS == 1 ? 1 : KS / 2;
+    extern __shared__ __align__(16) unsigned char lo_raw[];
+    __shared__ LoTiles<false> sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
+    uint4 *const frag = reinterpret_cast<uint4 *>(lo_raw) + warp * L::FRAGS;
+    if (tid == 0) pdl_launch_dependents();
+    const int tiles = lo_tiles<false, L::TM>(p, sh), groups = (tiles + kLoWarps - 1) / kLoWarps;
+    // ---- units: a group of tiles and a run of a section's steps, as long as
+    // leaves the last round of CTAs fullest
+    auto units_of = [&](int run) {
+        int n = 0;
+        for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) n += (p.sec_blocks[s] + run - 1) / run;
+        return n;
+    };
+    int run = 1;
+    {
+        int steps = 0;
+        for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) steps += p.sec_blocks[s];
+        int64_t least = 0x7fffffffffffffffll;
+        for (int i = 0; i < 12; ++i) {
+            // for i / 4 + 1 rounds, and a few steps longer
+            const int c = (int)(((int64_t)groups * steps + gridDim.x * (i / 4 + 1) - 1) / (gridDim.x * (i / 4 + 1))) + i % 4;
+            const int64_t rounds = ((int64_t)groups * units_of(c) + gridDim.x - 1) / gridDim.x, cost = rounds * (c + 2);
+            if (cost < least) {
+                least = cost;
+                run = c;
+            }
+        }
+    }
+    const int per = units_of(run);
+    int ks = 0;  // (known once t is)
+    for (int64_t u = blockIdx.x; u < (int64_t)groups * per; u += gridDim.x) {
+        const int tile = (int)(u / per) * kLoWarps + warp;
+        if (tile >= tiles) break;
+        int in = (int)(u % per), sec = 0;
+        if constexpr (!SILU)
+            for (int c; in >= (c = (p.sec_blocks[sec] + run - 1) / run); ++sec) in -= c;
+        const int at = sh.start[tile], n = sh.start[tile + 1] - at;
+        const int id = lo_id(p, at), rank = lo_rank(p, id);
+        if (rank == 0 && p.in_place) continue;
+        const int64_t N = p.sec_n[sec];
+        const int last = min(p.sec_blocks[sec], (in + 1) * run);
+        uint4 base[S][MT][2], b[S][4][Q];
+        auto load_base = [&](int step) {
+            const int64_t col = (int64_t)step * 32 + 8 * t;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int i = 16 * m + 8 * h + g;
+                        const uint16_t *src = p.base[sec + s] + (at + i) * N + col;
+                        base[s][m][h] = make_uint4(0u, 0u, 0u, 0u);
+                        if constexpr (VEC) {
+                            if (i < n && col < N) base[s][m][h] = __ldcg(reinterpret_cast<const uint4 *>(src));
+                        } else {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t x = i < n && col + 2 * k < N ? __ldcg(src + 2 * k) : 0u;
+                                const uint32_t y = i < n && col + 2 * k + 1 < N ? __ldcg(src + 2 * k + 1) : 0u;
+                                w[k] = x | (y << 16);
+                            }
+                            base[s][m][h] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+        };
+        auto load_b = [&](int step) {
+            const int64_t c0 = (int64_t)step * 32 + 8 * (g >> 1) + (g & 1);  // of MMA j: c0 + 2 j
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint16_t *brow = p.b + ((int64_t)max(id, 0) * p.N + p.sec_start[sec + s] + c0) * p.rank;
+#pragma unroll
+                for (int j = 0; j < 4; ++j, brow += 2 * p.rank)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int r = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                        const bool in = c0 + 2 * j < N && r < rank;
+                        b[s][j][q] = make_uint4(0u, 0u, 0u, 0u);
+                        if constexpr (KS == 1) {
+                            if (in) {
+                                const uint2 w = *reinterpret_cast<const uint2 *>(brow + r);
+                                b[s][j][q].x = w.x;
+                                b[s][j][q].y = w.y;
+                            }
+                        } else {
+                            if (in) b[s][j][q] = *reinterpret_cast<const uint4 *>(brow + r);
+                        }
+                    }
+            }
+            if (rank % 8) {
+                // entries past the adapter's rank, whatever they hold, are zero
+                auto mask = [&](uint32_t &w, int k) { w = k + 1 < rank ? w : k < rank ? w & 0xffffu : 0u; };
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int q = 0; q < Q; ++q) {
+                            const int k = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                            mask(b[s][j][q].x, k);
+                            mask(b[s][j][q].y, k + 2);
+                            if constexpr (KS > 1) {
+                                mask(b[s][j][q].z, k + 4);
+                                mask(b[s][j][q].w, k + 6);
+                            }
+                        }
+            }
+        };
+        load_base(in * run);
+        load_b(in * run);
+        if (ks == 0) {
+            pdl_wait_primary();
+            ks = __ldcg(p.shares);
+        }
+        __syncwarp();  // (the last unit's t is read)
+        const float scale = rank > 0 && p.scale ? __ldcg(p.scale + id) : 1.f;
+        const int nk = KS == 1 ? 1 : ((rank + 31) / 32) * 2;
+        for (int i = lane; rank > 0 && i < S * nk * MT * 64; i += 32) {
+            // four ranks of a token
+            const int s = i / (nk * MT * 64), j = i - s * nk * MT * 64, m = j / (4 * nk), r = (j - m * 4 * nk) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m < n && r < rank) {
+                const float *src = p.part + ((int64_t)(at + m) * p.nsec + sec + s) * p.rank + r;
+                for (int k = 0; k < ks; ++k) {
+                    const float4 e = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * p.M * p.nsec * p.rank));
+                    v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
+                }
+            }
+            v.x = v.x * scale;
+            v.y = r + 1 < rank ? v.y * scale : 0.f;
+            v.z = r + 2 < rank ? v.z * scale : 0.f;
+            v.w = r + 3 < rank ? v.w * scale : 0.f;
+            const int k = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2;
+            const int ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8);
+            const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
+            frag[((m / 16 * S + s) * KS + k) * kLoFrag + m / 8 % 2 * 32 + ln] =
+                make_uint4(h0, h1, pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
+                           pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1)));
+        }
+        __syncwarp();
+        for (int step = in * run; step < last; ++step) {
+            const int64_t col = (int64_t)step * 32 + 8 * t;
+            float acc[MT][S][4][4];
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 &v = base[s][m][h];
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            acc[m][s][j][2 * h] = bf16_lo(w[j]);
+                            acc[m][s][j][2 * h + 1] = bf16_hi(w[j]);
+                        }
+                    }
+            if (step + 1 < last) load_base(step + 1);
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    if (16 * (KS == 1 ? k : k & ~1) >= rank) break;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint4 *fr = frag + ((m * S + s) * KS + k) * kLoFrag + lane;
+                        const uint4 even = fr[0], odd = fr[32];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint4 &w = b[s][j][KS == 1 ? 0 : k / 2];
+                            const uint32_t b0 = k & 1 ? w.z : w.x, b1 = k & 1 ? w.w : w.y;
+                            mma_bf16(acc[m][s][j], even.x, odd.x, even.y, odd.y, b0, b1);
+                            mma_bf16(acc[m][s][j], even.z, odd.z, even.w, odd.w, b0, b1);
+                        }
+                    }
+                }
+            if (step + 1 < last) load_b(step + 1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if constexpr (SILU) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            acc[m][0][j][i] =
+                                __fdividef(acc[m][0][j][i], 1.f + __expf(-acc[m][0][j][i])) * acc[m][1][j][i];
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int i = 16 * m + 8 * h + g;
+                    if (i >= n) continue;
+                    uint16_t *dst = p.out[sec] + (at + i) * N + col;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = pack_bf16(acc[m][0][j][2 * h], acc[m][0][j][2 * h + 1]);
+                    if constexpr (VEC) {
+                        if (col < N) *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (col + k < N) dst[k] = (uint16_t)(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+                    }
+                }
+            }
+        }
+    }
+    // (what runs next waits for this kernel alone)
+    pdl_wait_primary();
+}
+
+// ---------------------------------------------------------------- host side
 template <int KS, bool SILU, bool VEC>
 static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
     return launch_pdl(reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC>), dim3(grid),
@@ -678,61 +875,97 @@ static cudaError_t launch_lora_few(LoraParams p, cudaStream_t st) {
                           : pick_few<8>(p, grid, st);
 }
 
-template <bool FEW>
-static cudaError_t launch_lora_t(LoraParams p, cudaStream_t st) {
-    const int64_t tiles = std::min<int64_t>(p.M, std::min<int64_t>(p.M, p.adapters + 1) + p.M / kLoTile);
-    const int64_t units = (FEW ? tiles : (int64_t)p.M) * p.nsec * ((p.rank + 15) / 16) * p.ks;
-    const int full = 2 * num_sms();
-    cudaError_t e = launch_pdl(reinterpret_cast<const void *>(lora_shrink_kernel<FEW>),
-                               dim3((unsigned)std::min<int64_t>(full, units)), kLoThreads, 0, st, p);
+template <int KS, bool SILU, bool VEC>
+static cudaError_t launch_many(const LoraParams &p, cudaStream_t st) {
+    using L = LoMany<KS, SILU>;
+    const void *kfn = reinterpret_cast<const void *>(lora_many_expand_kernel<KS, SILU, VEC>);
+    const cudaError_t e = allow_smem(kfn, L::SMEM);
     if (e != cudaSuccess) return e;
-    // steps of a warp: as many as leave every warp of the GPU one
-    const int64_t all = p.silu ? p.sec_n[0] : p.N;
-    int64_t steps = tiles * ((all + 31) / 32) / ((int64_t)full * kLoWarps);
-    p.steps = (int)std::min<int64_t>(std::max<int64_t>(steps, 1), 16);
-    p.blocks = 0;
-    for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) {
-        p.sec_blocks[s] = (int)((p.sec_n[s] + 32 * p.steps - 1) / (32 * p.steps));
-        p.blocks += p.sec_blocks[s];
+    const dim3 grid(L::CTAS * num_sms());
+    if (p.adapters > 0) return launch_pdl(kfn, grid, kLoThreads, L::SMEM, st, p);
+    // (alone: what it reads ahead of its wait is another kernel's)
+    LoraParams args = p;
+    void *argv[] = {&args};
+    return cudaLaunchKernel(kfn, grid, dim3(kLoThreads), argv, L::SMEM, st);
+}
+template <int KS>
+static cudaError_t pick_many(const LoraParams &p, cudaStream_t st) {
+    if (p.silu) return p.vec ? launch_many<KS, true, true>(p, st) : launch_many<KS, true, false>(p, st);
+    return p.vec ? launch_many<KS, false, true>(p, st) : launch_many<KS, false, false>(p, st);
+}
+
+static int launch_lora_many(LoraParams p, cudaStream_t st) {
+    const int rows = p.nsec * p.rank, cols = std::min(256, (rows + 15) / 16 * 16);
+    if (p.adapters > 0) {
+        CUtensorMap xmap, xmap16, amap;
+        const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+        int rc = encode_2d(&xmap, bf, 2, p.x, p.K, p.M, 64, kLtTile, sw, "activations");
+        if (!rc) rc = encode_2d(&xmap16, bf, 2, p.x, p.K, p.M, 64, 16, sw, "activations");
+        if (!rc) rc = encode_2d(&amap, bf, 2, p.a, p.K, (int64_t)p.adapters * rows, 64, cols, sw, "adapters");
+        if (rc) return rc;
+        int half = 16;  // columns of an accumulator: a power of two, both at least 32
+        while (half < cols) half *= 2;
+        const int stages = std::min(kLtStages, kLtSmem / ((kLtTile + cols) * 128));
+        const size_t smem = 1024 + (size_t)stages * (kLtTile + cols) * 128;
+        const void *kfn = reinterpret_cast<const void *>(lora_many_shrink_kernel);
+        cudaError_t e = allow_smem(kfn, 1024 + kLtSmem);
+        if (e == cudaSuccess)
+            e = launch_pdl(kfn, dim3(num_sms()), kLoThreads, smem, st, xmap, xmap16, amap, p, cols, half, stages);
+        if (e != cudaSuccess) return set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
     }
-    const int64_t want = ((FEW ? tiles : (int64_t)p.M) * p.blocks + kLoWarps - 1) / kLoWarps;
-    const int grid = (int)std::min<int64_t>(full, want);
-    return p.rank <= 16   ? pick_expand<FEW, 1>(p, grid, st)
-           : p.rank <= 32 ? pick_expand<FEW, 2>(p, grid, st)
-           : p.rank <= 64 ? pick_expand<FEW, 4>(p, grid, st)
-                          : pick_expand<FEW, 8>(p, grid, st);
+    for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) p.sec_blocks[s] = (int)((p.sec_n[s] + 31) / 32);
+    const cudaError_t e = p.rank <= 16   ? pick_many<1>(p, st)
+                          : p.rank <= 32 ? pick_many<2>(p, st)
+                          : p.rank <= 64 ? pick_many<4>(p, st)
+                                         : pick_many<8>(p, st);
+    return e == cudaSuccess ? GWA_OK : set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
 }
 
-static int lora_split(int64_t M, int K, int nsec, int rank, int adapters) {
+// The most shares of K: a few tokens' exactly so many, many tokens' up to so
+// many (their kernel chooses).
+static int lora_shares(int64_t M, int K) {
     if (M <= kLoSort) return (K + lora_share(K) - 1) / lora_share(K);
-    const int64_t tiles = std::min<int64_t>(M, adapters) + M / kLoTile;
-    const int64_t units = std::max<int64_t>(1, tiles * nsec * ((rank + 15) / 16));
-    int ks = 1;
-    while (ks < 8 && units * ks * 2 <= 2 * num_sms() && K / (2 * ks) >= 512) ks *= 2;
-    return ks;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(8, 24576 / M));
 }
 
-size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank, int adapters) {
-    const int64_t m = std::min<int64_t>(M, kLoChunk);
-    const int64_t tail = M > m && M % kLoChunk <= kLoSort ? M % kLoChunk : 0;
-    auto bytes = [&](int64_t n) {
-        return (size_t)lora_split(n, (int)K, nsec, rank, adapters) * n * nsec * rank * sizeof(float);
-    };
-    return std::max(bytes(m), bytes(tail));
+// 256 bytes (the shares of K that were chosen), then the partial sums.
+size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
+    const int64_t m = std::min<int64_t>(M, kLoChunk), tail = M % kLoChunk;
+    const int64_t rows = std::max(lora_shares(m, (int)K) * m, M > m && tail ? lora_shares(tail, (int)K) * tail : 0);
+    return 256 + (size_t)rows * nsec * rank * sizeof(float);
 }
 
-cudaError_t launch_lora(LoraParams p, int64_t M, cudaStream_t st) {
+int launch_lora(LoraParams p, int64_t M, void *workspace, cudaStream_t st) {
+    p.shares = static_cast<int32_t *>(workspace);
+    p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + 256);
     for (int64_t m = 0; m < M; m += kLoChunk) {
         p.M = (int)std::min<int64_t>(kLoChunk, M - m);
-        p.ks = lora_split(p.M, p.K, p.nsec, p.rank, p.adapters);
-        const cudaError_t e = p.M <= kLoSort ? launch_lora_few(p, st) : launch_lora_t<false>(p, st);
-        if (e != cudaSuccess) return e;
+        p.ks = lora_shares(p.M, p.K);
+        int rc = GWA_OK;
+        if (p.M <= kLoSort) {
+            const cudaError_t e = launch_lora_few(p, st);
+            if (e != cudaSuccess) rc = set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
+        } else {
+            rc = launch_lora_many(p, st);
+        }
+        if (rc) return rc;
         p.x += (int64_t)p.M * p.K;
         p.ids += p.M;
         for (int s = 0; s < p.nsec; ++s) p.base[s] += p.M * p.sec_n[s];
         for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) p.out[s] += p.M * p.sec_n[s];
     }
-    return cudaSuccess;
+    return GWA_OK;
+}
+
+unsigned int lora_timeouts(bool reset) {
+    unsigned int v = 0;
+    cudaMemcpyFromSymbol(&v, g_lora_timeouts, sizeof v);
+    if (reset) {
+        const unsigned int z = 0;
+        cudaMemcpyToSymbol(g_lora_timeouts, &z, sizeof z);
+    }
+    return v;
 }
 
 }  // namespace gwa

@@ -57,15 +57,11 @@
 // (qmm_tc_kernel<..., true>).
 // Every wait is bounded (2 s); a wait that runs out flags the workspace
 // status word and the kernel unwinds without hanging.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <mutex>
-
 #include "cluster.cuh"
 #include "common.cuh"
 #include "qmm.h"
 #include "tcgen05.cuh"
+#include "tma.cuh"
 
 namespace gwa {
 
@@ -101,16 +97,6 @@ size_t qmm_workspace_bytes(int64_t M, int64_t K) {
 }
 
 // ------------------------------------------------------------ PTX wrappers
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map,
-                                            int x, int y, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::"
-        "bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y),
-        "r"(smem_u32(bar))
-        : "memory");
-}
-
 // Instruction descriptor, kind::f16: fp16 A and B, fp32 D, both K-major,
 // N = NT tokens, M = 128 rows.
 template <int NT>
@@ -851,43 +837,6 @@ __global__ void __launch_bounds__(kQmmThreads, 1)
 }
 
 // ------------------------------------------------------------ host side
-static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr,
-                                             12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    });
-    return fn;
-}
-
-// 2-D tensor map over a row-major [rows, cols] array.
-static int encode_2d(CUtensorMap *map, CUtensorMapDataType type, int esize,
-                     const void *base, int64_t cols, int64_t rows,
-                     uint32_t box_cols, uint32_t box_rows,
-                     CUtensorMapSwizzle swz, const char *what) {
-    PFN_cuTensorMapEncodeTiled_v12000 encode = get_encode();
-    if (!encode)
-        return set_error(GWA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
-    const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t gstride[1] = {(cuuint64_t)cols * esize};
-    const cuuint32_t box[2] = {box_cols, box_rows};
-    const cuuint32_t estride[2] = {1, 1};
-    CUresult cr = encode(map, type, 2, const_cast<void *>(base), gdim, gstride,
-                         box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (cr != CUDA_SUCCESS)
-        return set_error(GWA_ERR_CUDA, "tensor map (%s) encode failed (%d)",
-                         what, (int)cr);
-    return GWA_OK;
-}
-
 
 template <int BITS, int NT>
 static int qmm_launch(const QmmArgs &a, unsigned char *ws, cudaStream_t st) {
