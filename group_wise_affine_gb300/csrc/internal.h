@@ -157,6 +157,7 @@ struct LoraParams {
     bool in_place;          // out is base: tokens without an adapter stay
     int32_t *status;
     float *part;            // [ks][M][nsec][rank], see the few tokens' kernel
+    uint4 *low;             // many tokens: [M][nsec][rank / 4], see the join
     int ks, share;          // shares of K (many tokens: at most), inputs of one
     int32_t *shares;        // many tokens: how many there are
     int sec_blocks[kMaxSections];  // blocks of a section's outputs

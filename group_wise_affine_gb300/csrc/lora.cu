@@ -54,76 +54,103 @@ __device__ __forceinline__ int lo_rank(const LoraParams &p, int id) {
     return id < 0 ? 0 : p.ranks ? min(max(__ldcg(p.ranks + id), 0), p.rank) : p.rank;
 }
 
-// Cuts the tokens into tiles (all threads of the CTA); returns their number.
-template <bool FEW, int TM>
-__device__ int lo_tiles(const LoraParams &p, LoTiles<FEW> &sh) {
-    constexpr int PER = FEW ? 1 : kLoPer;
+// Cuts the tokens into tiles of up to TM (all threads of the CTA); returns their
+// number.  Up to kLoSort tokens: in the order of their adapters, a thread each.
+template <int TM>
+__device__ int lo_tiles(const LoraParams &p, LoTiles<true> &sh) {
     constexpr unsigned FULL = 0xffffffffu;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
-    int id[PER], before;  // the places of this thread, and the one in front
-    if constexpr (FEW) {
-        const int mine = tid < p.M ? lo_id(p, tid) : 0x7fffffff;
-        if (tid < p.M && blockIdx.x == 0 && p.status && p.ids[tid] >= p.adapters) atomicOr(p.status, 1);
-        const int rank = tid < p.M ? lo_rank(p, mine) : 0;  // (there by the end of the sort)
-        sh.key[tid] = mine;
-        __syncthreads();
-        int at = 0;
-        for (int j = 0; j < p.M; j += 4) {
-            const int4 k = *reinterpret_cast<const int4 *>(sh.key + j);
-            at += (k.x < mine || (k.x == mine && j < tid)) + (k.y < mine || (k.y == mine && j + 1 < tid)) +
-                  (k.z < mine || (k.z == mine && j + 2 < tid)) + (k.w < mine || (k.w == mine && j + 3 < tid));
-        }
-        __syncthreads();
-        if (tid < p.M) {
-            sh.order[at] = (uint16_t)tid;
-            sh.key[at] = mine;
-            sh.rank[at] = rank;
-        }
-        __syncthreads();
-        id[0] = sh.key[tid];
-        before = tid ? sh.key[tid - 1] : 0x7ffffffe;
-    } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int tok = tid * PER + j;
-            id[j] = tok < p.M ? lo_id(p, tok) : 0x7fffffff;
-            if (tok < p.M && blockIdx.x == 0 && p.status && p.ids[tok] >= p.adapters) atomicOr(p.status, 1);
-        }
-        before = tid == 0 ? 0x7ffffffe : tid * PER <= p.M ? lo_id(p, tid * PER - 1) : 0x7fffffff;
+    const int mine = tid < p.M ? lo_id(p, tid) : 0x7fffffff;
+    if (tid < p.M && blockIdx.x == 0 && p.status && __ldcg(p.ids + tid) >= p.adapters) atomicOr(p.status, 1);
+    const int rank = tid < p.M ? lo_rank(p, mine) : 0;  // (there by the end of the sort)
+    sh.key[tid] = mine;
+    __syncthreads();
+    int at = 0;
+    for (int j = 0; j < p.M; j += 4) {
+        const int4 k = *reinterpret_cast<const int4 *>(sh.key + j);
+        at += (k.x < mine || (k.x == mine && j < tid)) + (k.y < mine || (k.y == mine && j + 1 < tid)) +
+              (k.z < mine || (k.z == mine && j + 2 < tid)) + (k.w < mine || (k.w == mine && j + 3 < tid));
     }
-    // where the run of this thread's first place starts
-    int last = -1, prev = before;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        if (id[j] != prev) last = tid * PER + j;
-        prev = id[j];
+    __syncthreads();
+    if (tid < p.M) {
+        sh.order[at] = (uint16_t)tid;
+        sh.key[at] = mine;
+        sh.rank[at] = rank;
     }
-    int incl = last;
+    __syncthreads();
+    // where the run of this place starts: the last place that differs from the
+    // one in front of it
+    int run = tid == 0 || sh.key[tid] != sh.key[tid - 1] ? tid : -1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(FULL, incl, o);
-        if (lane >= o) incl = max(incl, v);
+        const int v = __shfl_up_sync(FULL, run, o);
+        if (lane >= o) run = max(run, v);
     }
-    if (lane == 31) sh.w_max[warp] = incl;
+    if (lane == 31) sh.w_max[warp] = run;
     __syncthreads();
-    int run = __shfl_up_sync(FULL, incl, 1);
+    for (int w = 0; w < warp; ++w) run = max(run, sh.w_max[w]);
+    const bool starts = tid < p.M && (tid - run) % TM == 0;
+    const unsigned all = __ballot_sync(FULL, starts);
+    if (lane == 0) sh.w_sum[warp] = __popc(all);
+    __syncthreads();
+    int before = __popc(all & ((1u << lane) - 1u)), total = 0;
+    for (int w = 0; w < kLoWarps; ++w) {
+        if (w < warp) before += sh.w_sum[w];
+        total += sh.w_sum[w];
+    }
+    if (starts) sh.start[before] = (uint16_t)tid;
+    if (tid == 0) sh.start[total] = (uint16_t)p.M;
+    __syncthreads();
+    return total;
+}
+// More: runs of neighbours.  A warp reads a share of the tokens, 32 at a time,
+// and marks where the adapter changes; then each lane takes one such group.
+template <int TM>
+__device__ int lo_tiles(const LoraParams &p, LoTiles<false> &sh) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    const int chunk = (p.M + kLoThreads - 1) / kLoThreads * 32, first = warp * chunk;  // tokens of a warp
+    int id[kLoPer];
+    int before = first > 0 && first <= p.M && lane == 0 ? lo_id(p, first - 1) : 0x7fffffff;
+#pragma unroll
+    for (int j = 0; j < kLoPer; ++j) {
+        const int tok = first + 32 * j + lane;
+        id[j] = 32 * j < chunk && tok < p.M ? __ldcg(p.ids + tok) : -1;
+    }
+    unsigned mask = 0;  // of the lane's group: where runs start
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kLoPer; ++j) {
+        if (32 * j >= chunk) break;
+        bad |= id[j] >= p.adapters;
+        const int v = (unsigned)id[j] < (unsigned)p.adapters ? id[j] : -1;
+        int prev = __shfl_up_sync(FULL, v, 1);
+        if (lane == 0) prev = before;
+        const unsigned m = __ballot_sync(FULL, first + 32 * j + lane < p.M && v != prev);
+        if (lane == j) mask = m;
+        before = __shfl_sync(FULL, v, 31);
+    }
+    if (bad && blockIdx.x == 0 && p.status) atomicOr(p.status, 1);
+    const int base = first + 32 * lane;
+    int last = mask ? base + 31 - __clz(mask) : -1;  // up to and with the lane's group
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, last, o);
+        if (lane >= o) last = max(last, v);
+    }
+    if (lane == 31) sh.w_max[warp] = last;
+    __syncthreads();
+    int run = __shfl_up_sync(FULL, last, 1);
     if (lane == 0) run = -1;
     for (int w = 0; w < warp; ++w) run = max(run, sh.w_max[w]);
-    // places where a tile starts
-    int n = 0, r = run;
-    prev = before;
-    uint32_t starts = 0;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int at = tid * PER + j;
-        if (id[j] != prev) r = at;
-        prev = id[j];
-        if (at < p.M && (at - r) % TM == 0) {
-            starts |= 1u << j;
-            ++n;
-        }
+    unsigned starts = 0;
+    const int n = 32 * lane < chunk ? min(32, p.M - base) : 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+        if ((mask >> i) & 1u) run = base + i;
+        if (i < n && (base + i - run) % TM == 0) starts |= 1u << i;
     }
-    int sum = n;
+    int sum = __popc(starts);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(FULL, sum, o);
@@ -131,12 +158,12 @@ __device__ int lo_tiles(const LoraParams &p, LoTiles<FEW> &sh) {
     }
     if (lane == 31) sh.w_sum[warp] = sum;
     __syncthreads();
-    int at = sum - n, total = 0;
+    int at = sum - __popc(starts), total = 0;
     for (int w = 0; w < kLoWarps; ++w) {
         if (w < warp) at += sh.w_sum[w];
         total += sh.w_sum[w];
     }
-    for (; starts; starts &= starts - 1) sh.start[at++] = (uint16_t)(tid * PER + __ffs(starts) - 1);
+    for (; starts; starts &= starts - 1) sh.start[at++] = (uint16_t)(base + __ffs(starts) - 1);
     if (tid == 0) sh.start[total] = (uint16_t)p.M;
     __syncthreads();
     return total;
@@ -161,7 +188,7 @@ __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraPara
     // (behind the wait: what the next kernel reads before its own wait was
     // written before this one's)
     if (tid == 0) pdl_launch_dependents();
-    const int tiles = lo_tiles<true, kLoTile>(p, sh);
+    const int tiles = lo_tiles<kLoTile>(p, sh);
     // ---- units: blocks of the tiles in order, each in ks shares
     const int mine = tid < tiles ? p.nsec * ((sh.rank[sh.start[tid]] + 15) / 16) : 0;
     int incl = mine;
@@ -249,7 +276,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
     __shared__ uint4 frag[S * KS * kLoFrag];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
     if (tid == 0) pdl_launch_dependents();
-    const int tiles = lo_tiles<true, kLoTile>(p, sh);
+    const int tiles = lo_tiles<kLoTile>(p, sh);
     // ---- units of `run` octets
     int octets = 0;
     for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) octets += p.sec_blocks[s];
@@ -426,7 +453,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
 // Warps: 0 issues the copies, 1 the MMAs (a thread each), 4 to 7 bring the
 // results out, two accumulators in turn.  Every wait is bounded (2 s); one that
 // runs out is counted and the kernel unwinds.
-constexpr int kLtTile = 128, kLtStages = 6;  // (fewer where they do not fit)
+constexpr int kLtTile = 128, kLtStages = 5;  // (fewer where they do not fit)
 constexpr int kLtSmem = 200 * 1024;
 
 static __device__ unsigned int g_lora_timeouts;
@@ -486,11 +513,14 @@ __global__ void __launch_bounds__(kLoThreads, 1)
         fence_mbar_init();
         s_fail = s_issued = 0;
     }
+    if (tid == 0)
+        for (const CUtensorMap *m : {&xmap, &xmap16, &amap})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
     if (warp == 1) tmem_alloc(&s_tmem, 2 * half);
     pdl_wait_primary();
     if (tid == 0) pdl_launch_dependents();  // (see the few tokens' kernel)
     tc_fence_before();
-    const int tiles = lo_tiles<false, kLtTile>(p, sh);  // (synchronizes)
+    const int tiles = lo_tiles<kLtTile>(p, sh);  // (synchronizes)
     tc_fence_after();
     const uint32_t tmem = s_tmem;
     const int rows = p.nsec * p.rank, passes = (rows + cols - 1) / cols, steps = (p.K + 63) / 64;
@@ -509,8 +539,8 @@ __global__ void __launch_bounds__(kLoThreads, 1)
         w.id = lo_id(p, w.at);
         w.row = pass * cols;
         w.k = in - pass * ks;
-        w.c0 = (int)((int64_t)steps * w.k / ks);
-        w.c1 = (int)((int64_t)steps * (w.k + 1) / ks);
+        w.c0 = steps * w.k / ks;
+        w.c1 = steps * (w.k + 1) / ks;
         return lo_rank(p, w.id) > 0;
     };
     Unit w;
@@ -521,7 +551,9 @@ __global__ void __launch_bounds__(kLoThreads, 1)
             for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
                 if (!unit(u, w)) continue;
                 const int arow = w.id * rows + w.row;
-                const bool whole = w.n == kLtTile;
+                // (eight boxes a step are slow to issue: most of a tile is copied
+                // whole, its neighbours' rows with it)
+                const bool whole = w.n > 48;
                 const int boxes = (w.n + 15) / 16;
                 for (int c = w.c0; c < w.c1; ++c, ++it) {
                     const uint32_t s = it % stages;
@@ -608,11 +640,62 @@ __global__ void __launch_bounds__(kLoThreads, 1)
     if (warp == 1) tmem_dealloc(tmem, 2 * half);
 }
 
+// low[m][s][r / 4]: t of many tokens, the shares' sums times the scale, as hi and
+// lo bf16 parts; zero past the adapter's rank.  (Made once here; each of a
+// dozen expanding CTAs summing its tokens' up again took 10 us.)
+__global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p) {
+    // (before the wait: this kernel starts behind the first one's wait already)
+    if (threadIdx.x == 0) pdl_launch_dependents();
+    constexpr int AT = 4;  // units of a thread at a time
+    const int quads = p.rank / 4, of_token = p.nsec * quads, stride = gridDim.x * kLoThreads;
+    const int all = p.M * of_token;  // (8192 tokens x 8 sections x 32 at most)
+    int ks = 0;
+    for (int i0 = blockIdx.x * kLoThreads + threadIdx.x; i0 < all; i0 += AT * stride) {
+        int rank[AT];
+        float scale[AT];
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            const int i = i0 + x * stride, id = i < all ? lo_id(p, i / of_token) : -1;
+            rank[x] = lo_rank(p, id);
+            scale[x] = id >= 0 && p.scale ? __ldcg(p.scale + id) : 1.f;
+        }
+        if (ks == 0) {
+            pdl_wait_primary();
+            ks = __ldcg(p.shares);
+        }
+        float4 v[AT];
+#pragma unroll
+        for (int x = 0; x < AT; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int k = 0; k < ks; ++k) {
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (int64_t)k * all;
+#pragma unroll
+            for (int x = 0; x < AT; ++x) {
+                const int i = i0 + x * stride;
+                if (i % quads * 4 >= rank[x]) continue;
+                const float4 e = __ldcg(src + i);
+                v[x] = make_float4(v[x].x + e.x, v[x].y + e.y, v[x].z + e.z, v[x].w + e.w);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < AT; ++x) {
+            const int i = i0 + x * stride, r = i % quads * 4;
+            if (i >= all) break;
+            const float a = v[x].x * scale[x], b = r + 1 < rank[x] ? v[x].y * scale[x] : 0.f;
+            const float c = r + 2 < rank[x] ? v[x].z * scale[x] : 0.f, d = r + 3 < rank[x] ? v[x].w * scale[x] : 0.f;
+            const uint32_t h0 = pack_bf16(a, b), h1 = pack_bf16(c, d);
+            p.low[i] = make_uint4(h0, h1, pack_bf16(a - bf16_lo(h0), b - bf16_hi(h0)),
+                                  pack_bf16(c - bf16_lo(h1), d - bf16_hi(h1)));
+        }
+    }
+    pdl_wait_primary();
+}
+
 // out = base + scale B t.  A warp's unit is a tile of 16 MT tokens and some
 // steps of 32 outputs of one section; the eight warps of a CTA take
 // neighbouring tiles of the same outputs, so that B comes out of the L1 cache.
-// t as in the few tokens' kernel, each warp's own in shared memory; the next
-// step's base is on its way during the products, its B during the stores.
+// t's fragments are each warp's own copy in shared memory; the next step's base
+// is on its way during the products, its B during the stores.
 // Warp-level MMAs serve: the work is bound by the bytes of base and output (at
 // rank 64 the products are 2 x 64 x 2 FLOP for each 4 bytes).
 template <int KS, bool SILU>
@@ -631,7 +714,7 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
     uint4 *const frag = reinterpret_cast<uint4 *>(lo_raw) + warp * L::FRAGS;
     if (tid == 0) pdl_launch_dependents();
-    const int tiles = lo_tiles<false, L::TM>(p, sh), groups = (tiles + kLoWarps - 1) / kLoWarps;
+    const int tiles = lo_tiles<L::TM>(p, sh), groups = (tiles + kLoWarps - 1) / kLoWarps;
     // ---- units: a group of tiles and a run of a section's steps, as long as
     // leaves the last round of CTAs fullest
     auto units_of = [&](int run) {
@@ -643,11 +726,12 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
     {
         int steps = 0;
         for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) steps += p.sec_blocks[s];
-        int64_t least = 0x7fffffffffffffffll;
-        for (int i = 0; i < 12; ++i) {
-            // for i / 4 + 1 rounds, and a few steps longer
-            const int c = (int)(((int64_t)groups * steps + gridDim.x * (i / 4 + 1) - 1) / (gridDim.x * (i / 4 + 1))) + i % 4;
-            const int64_t rounds = ((int64_t)groups * units_of(c) + gridDim.x - 1) / gridDim.x, cost = rounds * (c + 2);
+        const unsigned all = (unsigned)min(steps, 1 << 20) * groups, ctas = gridDim.x;
+        unsigned least = 0xffffffffu;
+        for (unsigned i = 1; i <= 3; ++i) {
+            // for i rounds (a run's start counts as two steps)
+            const int c = (int)((all + ctas * i - 1) / (ctas * i)) + (i < 3);
+            const unsigned rounds = (groups * min(units_of(c), 1 << 20) + ctas - 1) / ctas, cost = rounds * (c + 2);
             if (cost < least) {
                 least = cost;
                 run = c;
@@ -655,7 +739,7 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
         }
     }
     const int per = units_of(run);
-    int ks = 0;  // (known once t is)
+    bool waited = false;
     for (int64_t u = blockIdx.x; u < (int64_t)groups * per; u += gridDim.x) {
         const int tile = (int)(u / per) * kLoWarps + warp;
         if (tile >= tiles) break;
@@ -737,34 +821,30 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
         };
         load_base(in * run);
         load_b(in * run);
-        if (ks == 0) {
-            pdl_wait_primary();
-            ks = __ldcg(p.shares);
-        }
+        if (!waited) pdl_wait_primary();
+        waited = true;
         __syncwarp();  // (the last unit's t is read)
-        const float scale = rank > 0 && p.scale ? __ldcg(p.scale + id) : 1.f;
         const int nk = KS == 1 ? 1 : ((rank + 31) / 32) * 2;
-        for (int i = lane; rank > 0 && i < S * nk * MT * 64; i += 32) {
-            // four ranks of a token
-            const int s = i / (nk * MT * 64), j = i - s * nk * MT * 64, m = j / (4 * nk), r = (j - m * 4 * nk) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m < n && r < rank) {
-                const float *src = p.part + ((int64_t)(at + m) * p.nsec + sec + s) * p.rank + r;
-                for (int k = 0; k < ks; ++k) {
-                    const float4 e = __ldcg(reinterpret_cast<const float4 *>(src + (int64_t)k * p.M * p.nsec * p.rank));
-                    v = make_float4(v.x + e.x, v.y + e.y, v.z + e.z, v.w + e.w);
-                }
-            }
-            v.x = v.x * scale;
-            v.y = r + 1 < rank ? v.y * scale : 0.f;
-            v.z = r + 2 < rank ? v.z * scale : 0.f;
-            v.w = r + 3 < rank ? v.w * scale : 0.f;
-            const int k = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2;
-            const int ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8);
-            const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
-            frag[((m / 16 * S + s) * KS + k) * kLoFrag + m / 8 % 2 * 32 + ln] =
-                make_uint4(h0, h1, pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
-                           pack_bf16(v.z - bf16_lo(h1), v.w - bf16_hi(h1)));
+        if (rank > 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        if (k >= nk) break;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int i = 16 * m + 8 * h + g, q = KS == 1 ? t : 8 * (k / 2) + 2 * t + k % 2;
+                            uint4 *dst = frag + ((m * S + s) * KS + k) * kLoFrag + 32 * h + lane;
+                            if (i < n && 4 * q < p.rank)
+                                cp_async<16>(dst, p.low + ((int64_t)(at + i) * p.nsec + sec + s) * (p.rank / 4) + q);
+                            else
+                                *dst = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+            cp_async_commit();
+            cp_async_wait<0>();
         }
         __syncwarp();
         for (int step = in * run; step < last; ++step) {
@@ -879,7 +959,8 @@ template <int KS, bool SILU, bool VEC>
 static cudaError_t launch_many(const LoraParams &p, cudaStream_t st) {
     using L = LoMany<KS, SILU>;
     const void *kfn = reinterpret_cast<const void *>(lora_many_expand_kernel<KS, SILU, VEC>);
-    const cudaError_t e = allow_smem(kfn, L::SMEM);
+    cudaError_t e = allow_smem(kfn, L::SMEM);
+    if (e == cudaSuccess) e = prefer_max_shared(kfn);
     if (e != cudaSuccess) return e;
     const dim3 grid(L::CTAS * num_sms());
     if (p.adapters > 0) return launch_pdl(kfn, grid, kLoThreads, L::SMEM, st, p);
@@ -910,8 +991,15 @@ static int launch_lora_many(LoraParams p, cudaStream_t st) {
         const size_t smem = 1024 + (size_t)stages * (kLtTile + cols) * 128;
         const void *kfn = reinterpret_cast<const void *>(lora_many_shrink_kernel);
         cudaError_t e = allow_smem(kfn, 1024 + kLtSmem);
+        if (e == cudaSuccess) e = prefer_max_shared(kfn);
         if (e == cudaSuccess)
             e = launch_pdl(kfn, dim3(num_sms()), kLoThreads, smem, st, xmap, xmap16, amap, p, cols, half, stages);
+        if (e == cudaSuccess) {
+            const int64_t units = (int64_t)p.M * rows / 4;
+            e = launch_pdl(reinterpret_cast<const void *>(lora_many_join_kernel),
+                           dim3((unsigned)std::min<int64_t>(num_sms(), (units + kLoThreads - 1) / kLoThreads)),
+                           kLoThreads, 0, st, p);
+        }
         if (e != cudaSuccess) return set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
     }
     for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) p.sec_blocks[s] = (int)((p.sec_n[s] + 31) / 32);
@@ -929,11 +1017,13 @@ static int lora_shares(int64_t M, int K) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(8, 24576 / M));
 }
 
-// 256 bytes (the shares of K that were chosen), then the partial sums.
+// 256 bytes (the shares of K that were chosen), the partial sums, and of many
+// tokens what they add up to (see lora_many_join_kernel).
+static int64_t lora_sums(int64_t M, int K) { return (int64_t)lora_shares(M, K) * M; }
 size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
-    const int64_t m = std::min<int64_t>(M, kLoChunk), tail = M % kLoChunk;
-    const int64_t rows = std::max(lora_shares(m, (int)K) * m, M > m && tail ? lora_shares(tail, (int)K) * tail : 0);
-    return 256 + (size_t)rows * nsec * rank * sizeof(float);
+    const int64_t m = std::min<int64_t>(M, kLoChunk), tail = M > m ? M % kLoChunk : 0;
+    const int64_t rows = std::max(lora_sums(m, (int)K), tail ? lora_sums(tail, (int)K) : 0);
+    return 256 + (size_t)(rows + (m > kLoSort ? m : 0)) * nsec * rank * sizeof(float);
 }
 
 int launch_lora(LoraParams p, int64_t M, void *workspace, cudaStream_t st) {
@@ -942,6 +1032,7 @@ int launch_lora(LoraParams p, int64_t M, void *workspace, cudaStream_t st) {
     for (int64_t m = 0; m < M; m += kLoChunk) {
         p.M = (int)std::min<int64_t>(kLoChunk, M - m);
         p.ks = lora_shares(p.M, p.K);
+        p.low = reinterpret_cast<uint4 *>(p.part + lora_sums(p.M, p.K) * p.nsec * p.rank);
         int rc = GWA_OK;
         if (p.M <= kLoSort) {
             const cudaError_t e = launch_lora_few(p, st);
