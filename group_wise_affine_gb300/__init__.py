@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -868,9 +869,9 @@ def verify_draft(logits: torch.Tensor, ids: torch.Tensor, q_start: torch.Tensor,
         (temperature, "temperature", torch.float32, R),
         (top_k, "top_k", torch.int32, R), (top_p, "top_p", torch.float32, R),
         (min_p, "min_p", torch.float32, R))]
-    token = _new(R, torch.int32, logits.device, stream)
-    accepted = _new(B, torch.int32, logits.device, stream)
-    prob = _new(R, torch.float32, logits.device, stream)
+    token, accepted, prob = _new(2 * R + B, torch.int32, logits.device,
+                                 stream).split((R, B, R))
+    prob = prob.view(torch.float32)
     if workspace is None:
         n = int(load().gwa_verify_draft_workspace_bytes(R))
         workspace = _new(max(n, 16), torch.uint8, logits.device, stream)
@@ -932,22 +933,25 @@ def make_lora_workspace(lora: LoRA, M: int) -> Optional[torch.Tensor]:
     return torch.empty(n, dtype=torch.uint8, device=lora.device)
 
 
-def _lora_inputs(x, lora, ids, sizes, base, workspace, stream):
-    _bf16(x, "x")
-    if x.shape[-1] != lora.K:
-        raise ValueError(f"x must be [M, {lora.K}] (got {list(x.shape)})")
+def _lora_inputs(x, lora, ids, base, workspace, stream):
+    """M, the sections' sizes and base pointers, and the workspace (alive
+    until the call is enqueued)."""
+    if x.dtype != torch.bfloat16 or x.shape[-1] != lora.K:
+        raise ValueError(f"x must be bfloat16 [M, {lora.K}] "
+                         f"(got {x.dtype} {list(x.shape)})")
     M = x.numel() // lora.K
     if ids.dtype != torch.int32 or ids.numel() != M:
         raise ValueError(f"ids must be int32 [{M}]")
-    if len(base) != lora.sections or sum(sizes) != lora.N:
+    sizes = [t.shape[-1] for t in base]
+    if len(sizes) != lora.sections or sum(sizes) != lora.N:
         raise ValueError(f"one buffer for each of {lora.sections} sections, "
                          f"{lora.N} outputs together")
-    for i, (t, n) in enumerate(zip(base, sizes)):
-        _check_out(t, M * n, f"section {i}")
+    for i, t in enumerate(base):
+        _check_out(t, M * sizes[i], f"section {i}")
     if workspace is None and M:
         n = int(load().gwa_lora_workspace_bytes(lora.c, M))
         workspace = _new(max(n, 16), torch.uint8, x.device, stream)
-    return M, workspace  # (alive until the call is enqueued)
+    return M, sizes, [_ptr(t) for t in base], workspace
 
 
 def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
@@ -958,21 +962,23 @@ def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
     """gwa_lora_add: ``base`` (a projection's outputs, one bfloat16 [M, size]
     a section) plus each token's own low-rank adapter of x [M, K]; ids int32
     [M] names it (negative: none).  ``out`` may be ``base``."""
-    sizes = [t.shape[-1] for t in base]
-    M, workspace = _lora_inputs(x, lora, ids, sizes, base, workspace, stream)
+    M, sizes, bp, workspace = _lora_inputs(x, lora, ids, base, workspace, stream)
     wp, wn = _ws(workspace)
     if out is None:
         out = [_new((M, n), torch.bfloat16, x.device, stream) for n in sizes]
-    if len(out) != len(sizes):
-        raise ValueError("one output per section")
-    for i, (t, n) in enumerate(zip(out, sizes)):
-        _check_out(t, M * n, f"out[{i}]")
-    n = len(sizes)
-    cs = (ctypes.c_int64 * n)(*sizes)
-    cb = (ctypes.c_void_p * n)(*[_ptr(t) for t in base])
-    co = (ctypes.c_void_p * n)(*[_ptr(t) for t in out])
-    rc = load().gwa_lora_add(_ptr(x), M, lora.c, _ptr(ids), cs, cb, co, wp, wn,
-                             _status(status), _stream(stream))
+        op = [t.data_ptr() for t in out]
+    else:
+        if len(out) != len(sizes):
+            raise ValueError("one output per section")
+        for i, t in enumerate(out):
+            _check_out(t, M * sizes[i], f"out[{i}]")
+        op = [_ptr(t) for t in out]
+    # host arrays as bytes (a ctypes array takes 2 us to make)
+    form = f"{len(sizes)}q"
+    rc = load().gwa_lora_add(_ptr(x), M, lora.c, _ptr(ids),
+                             struct.pack(form, *sizes), struct.pack(form, *bp),
+                             struct.pack(form, *op), wp, wn, _status(status),
+                             _stream(stream))
     if rc:
         _check(rc)
     return list(out)
@@ -986,17 +992,17 @@ def lora_gate_up_silu(x: torch.Tensor, gate_up: Sequence[torch.Tensor],
                       stream=None) -> torch.Tensor:
     """gwa_lora_gate_up_silu: h = SiLU(gate) * up, both with each token's own
     low-rank adapter of x added; gate_up two bfloat16 [M, I]."""
-    sizes = [t.shape[-1] for t in gate_up]
-    M, workspace = _lora_inputs(x, lora, ids, sizes, gate_up, workspace, stream)
+    M, sizes, bp, workspace = _lora_inputs(x, lora, ids, gate_up, workspace,
+                                           stream)
     wp, wn = _ws(workspace)
-    if sizes[0] != sizes[1]:
+    if len(sizes) != 2 or sizes[0] != sizes[1]:
         raise ValueError("gate and up must have the same width")
     if h is None:
         h = _new((M, sizes[0]), torch.bfloat16, x.device, stream)
     _check_out(h, M * sizes[0], "h")
-    rc = load().gwa_lora_gate_up_silu(
-        _ptr(x), M, lora.c, _ptr(ids), _ptr(gate_up[0]), _ptr(gate_up[1]),
-        _ptr(h), wp, wn, _status(status), _stream(stream))
+    rc = load().gwa_lora_gate_up_silu(_ptr(x), M, lora.c, _ptr(ids), bp[0],
+                                      bp[1], _ptr(h), wp, wn, _status(status),
+                                      _stream(stream))
     if rc:
         _check(rc)
     return h

@@ -55,10 +55,31 @@ __device__ __forceinline__ int pg_owner(int quot, int rest, int unit) {
 __device__ __forceinline__ int pg_low(const PagedParams &p, int64_t last) {
     return (int)max((int64_t)0, last + 1 - p.window);
 }
-// Whether no row takes part in any of the keys [key, key + n) through its
-// window, where the rows' first window starts at `low`, nor as first keys.
-__device__ __forceinline__ bool pg_hidden(const PagedParams &p, int key, int n, int low) {
-    return key + n <= low && key >= p.sinks;
+// The keys that some rows see, side by side: the first ones, in sixteens up to
+// key `first`, then those from `first + gap` on, where (in sixteens) the rows'
+// first window starts.  Steps and tiles are counted over these, and masks
+// compare places among them; a sixteen lies in one page, so only the addresses
+// know of the gap.
+struct PgSpan {
+    int first, gap;
+    __device__ __forceinline__ int place(int key) const {
+        return key <= first ? key : max(first, key - gap);
+    }
+    __device__ __forceinline__ int key(int place) const { return place < first ? place : place + gap; }
+};
+// `low`: where the first of the windows starts; no row sees the keys from
+// `seen` on.
+__device__ __forceinline__ PgSpan pg_span(const PagedParams &p, int low, int seen) {
+    const int from = min(low >> 4, (seen + 15) >> 4), sinks = min(p.sinks, seen);
+    PgSpan s;
+    s.first = min((sinks + 15) >> 4, from) << 4;
+    s.gap = (from << 4) - s.first;
+    return s;
+}
+// Whether rows whose first window starts at place `low` see none of the places
+// [place, place + n).
+__device__ __forceinline__ bool pg_hidden(const PagedParams &p, int place, int n, int low) {
+    return place + n <= low && place >= p.sinks;
 }
 
 // A total over the lanes of values whose own sums fit: as an int, or 0 if it

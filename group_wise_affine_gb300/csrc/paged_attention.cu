@@ -108,18 +108,15 @@ struct PgLayout {
 // (KV head and row block) with keys.
 struct PgSeq {
     int first, base, len, rows, nrg, nt, segs;  // base: position of the first new token
-    // with a window: steps [full, end) are inside every row's, [low, full)
-    // the windows' starts, and `first_keys` the ones in front of low that hold
-    // first keys
-    int full, low, end, first_keys;
-    // the step of the keys, of step j of nt: those that every row sees whole
-    // come first, so that the wider roundings of the others (see compute) do
-    // not reach them
+    // with a window: the places of the keys (len is one, too), of which some
+    // row does not see all in the first `edge` steps
+    PgSpan span;
+    int edge;
+    // the j-th step to take: those that every row sees whole come first, so
+    // that the wider roundings of the others (see compute) do not reach them
     template <bool WIN>
     __device__ __forceinline__ int at(int j) const {
-        if (!WIN) return j;
-        if (j < end - full) return full + j;
-        return j < end - low ? j - (end - full) + low : j - (end - low);
+        return !WIN ? j : j < nt - edge ? j + edge : j - (nt - edge);
     }
 };
 // Steps that a segment's start and end (queries, merging the warps, the
@@ -128,6 +125,10 @@ struct PgSeq {
 // heads of 128: 32 of about 400 keys 15.4 : 17.6 us, 1000 20.4 : 22.4, 4000
 // 44.2 : 45.8, 200 of about 1000 77.9 : 90.1; 64 of 2048 each 49.3 : 49.5.
 constexpr int kPgHead = 2;
+// With a window segments are alike and short: where whole ones, a CTA each in
+// rounds, take no more than this many steps longer than the cut, they are not
+// cut, which saves the pieces' way through the workspace.
+constexpr int kPgUncut = 4;
 template <int NQ, int STEP, bool WIN>
 __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     const KvSeq s = kv_seq(p.kv, b);
@@ -142,11 +143,11 @@ __device__ __forceinline__ PgSeq pg_seq(const PagedParams &p, int b) {
     if constexpr (WIN) {
         const int n = min(s.count, p.kv.max_q);
         const int seen = max(0, min(s.len, r.base + n));
-        r.end = (seen + STEP - 1) / STEP;
-        r.low = min(pg_low(p, r.base) / STEP, r.end);
-        r.full = min((pg_low(p, (int64_t)r.base + n - 1) + STEP - 1) / STEP, r.end);
-        r.first_keys = min((min(p.sinks, seen) + STEP - 1) / STEP, r.low);
-        r.nt = r.end - r.low + r.first_keys;
+        r.span = pg_span(p, pg_low(p, r.base), seen);
+        r.len = r.span.place(s.len);
+        r.nt = (r.span.place(seen) + STEP - 1) / STEP;
+        const int low = r.span.place(pg_low(p, (int64_t)r.base + n - 1));
+        r.edge = low > p.sinks ? min((low + STEP - 1) / STEP, r.nt) : 0;
     }
     r.segs = r.nt > 0 ? p.kv.heads * r.nrg : 0;  // (times nt: the entry point keeps the total below 2^31)
     return r;
@@ -240,15 +241,21 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     // ---- this CTA's run of units, found by every warp for itself
     const int B = p.kv.batch;
     const int cta = blockIdx.x;
-    int total = 0, segs = 0;
+    int total = 0, segs = 0, most = 0;
     for (int b0 = 0; b0 < B; b0 += kWarp) {
         PgSeq s{};
         if (b0 + lane < B) s = pg_seq<NQ, STEP, WIN>(p, b0 + lane);
         total += __reduce_add_sync(FULL, s.segs * s.nt);
         segs += __reduce_add_sync(FULL, s.segs);
+        if (WIN) most = max(most, __reduce_max_sync(FULL, s.segs ? s.nt : 0));
     }
     const int head = total > (int)gridDim.x ? kPgHead : 0;
-    total += segs * head;
+    bool uncut = false;  // a segment is a unit
+    if (WIN && head) {
+        const int ctas = gridDim.x, cut = (total + segs * head + ctas - 1) / ctas;
+        uncut = (segs + ctas - 1) / ctas * (most + head) <= cut + kPgUncut;
+    }
+    total = uncut ? segs : total + segs * head;
     // sequences without keys: their rows are zero
     for (int i = cta; i < B; i += gridDim.x) {
         const PgSeq s = pg_seq<NQ, STEP, WIN>(p, i);
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     for (int b0 = 0; b0 < B; b0 += kWarp) {
         PgSeq s{};
         if (b0 + lane < B) s = pg_seq<NQ, STEP, WIN>(p, b0 + lane);
-        const int u = s.segs * (s.nt + head);
+        const int u = s.segs * (uncut ? 1 : s.nt + head);
         int incl = u;
 #pragma unroll
         for (int o = 1; o < kWarp; o <<= 1) {
@@ -299,7 +306,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
     const int pmask = (1 << p.kv.page_shift) - 1;
 
     while (cur < end) {
-        const int cost = sq.nt + head;  // of a segment
+        const int cost = uncut ? 1 : sq.nt + head;  // of a segment
         if (cur >= at + sq.segs * cost) {
             // (never past the batch, unless the lengths change meanwhile)
             if (b + 1 >= B) break;
@@ -310,9 +317,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         const int seg = (cur - at) / cost;  // hk * nrg + rg
         const int from = cur - at - seg * cost, to = min(cost, from + (end - cur));
         cur += to - from;
-        if (to <= head) continue;  // none of its steps
+        if (!uncut && to <= head) continue;  // none of its steps
         const int hk = seg / sq.nrg, rg = seg % sq.nrg;
-        const int ta = max(from - head, 0), tb = to - head;
+        const int ta = uncut ? 0 : max(from - head, 0), tb = uncut ? sq.nt : to - head;
         const int nlive = min(NQ, sq.rows - rg * NQ);
         const int32_t *table = p.kv.page_table + (int64_t)b * p.kv.max_pages;
 
@@ -379,29 +386,35 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
                     qs[nn][gg][h] = __shfl_sync(FULL, sum[gg], from) * 0x1p-24f;
                 const int i = 8 * nn + 2 * t + h, rr = rg * NQ + i;
                 lim[nn][h] = i >= nlive ? 0
+                             : WIN      ? min(sq.len, sq.span.place(sq.base + rr / p.rep + 1))
                              : p.causal ? min(sq.len, sq.base + rr / p.rep + 1)
                                         : sq.len;
             }
         }
         if (WIN && threadIdx.x < NQ)
-            s_low[threadIdx.x] = pg_low(p, (int64_t)sq.base + (rg * NQ + (int)threadIdx.x) / p.rep);
+            s_low[threadIdx.x] =
+                sq.span.place(pg_low(p, (int64_t)sq.base + (rg * NQ + (int)threadIdx.x) / p.rep));
         __syncthreads();
         // every row of the block sees the keys below `all`, none those from
         // `seen` on
         int all = 0x7fffffff;
         const int seen =
-            p.causal ? min(sq.len, sq.base + (rg * NQ + nlive - 1) / p.rep + 1) : sq.len;
+            WIN        ? min(sq.len, sq.span.place(sq.base + (rg * NQ + nlive - 1) / p.rep + 1))
+            : p.causal ? min(sq.len, sq.base + (rg * NQ + nlive - 1) / p.rep + 1)
+                       : sq.len;
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
             for (int h = 0; h < 2; ++h) all = min(all, lim[nn][h]);
         // with a window: the block's first row's starts at `low`
-        const int low = WIN ? pg_low(p, (int64_t)sq.base + rg * NQ / p.rep) : 0;
+        const int low = WIN ? sq.span.place(pg_low(p, (int64_t)sq.base + rg * NQ / p.rep)) : 0;
         auto gone = [&](int key, int n) {  // no row of the block sees them
             return key >= sq.len || (WIN && pg_hidden(p, key, n, low));
         };
         if (nlive < NQ) {  // padding rows: masked or not, they are never written
-            all = p.causal ? max(0, min(sq.len, sq.base + rg * NQ / p.rep + 1)) : sq.len;
+            all = WIN        ? max(0, min(sq.len, sq.span.place(sq.base + rg * NQ / p.rep + 1)))
+                  : p.causal ? max(0, min(sq.len, sq.base + rg * NQ / p.rep + 1))
+                             : sq.len;
         } else {
             all = __reduce_min_sync(FULL, all);
         }
@@ -429,10 +442,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
         auto issue = [&](int step, int to) {
             if (step - pages_at >= 32 / U) {
                 pages_at = step;
-                const int key = sq.at<WIN>(step + lane / U) * STEP + warp * KEYS + lane % U * 16;
+                const int at = sq.at<WIN>(step + lane / U) * STEP + warp * KEYS + lane % U * 16;
                 pages = 0;
-                if (step + lane / U < tb && !gone(key, 16)) {
-                    pages = table[key >> p.kv.page_shift];
+                if (step + lane / U < tb && !gone(at, 16)) {
+                    pages = table[(WIN ? sq.span.key(at) : at) >> p.kv.page_shift];
                     if ((unsigned)pages >= (unsigned)p.kv.num_pages) {
                         if (p.status) atomicOr(p.status, (int)kKvBadPage);
                         pages = 0;
@@ -443,8 +456,9 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int page = __shfl_sync(FULL, pages, U * (step - pages_at) + u);
-                const int key = sq.at<WIN>(step) * STEP + warp * KEYS + u * 16;
-                if (gone(key, 16)) continue;  // warp-uniform
+                const int at = sq.at<WIN>(step) * STEP + warp * KEYS + u * 16;
+                if (gone(at, 16)) continue;  // warp-uniform
+                const int key = WIN ? sq.span.key(at) : at;
                 const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
                                     (key & pmask);
                 const uint4 *ks = reinterpret_cast<const uint4 *>(p.kv.kq) + row * RCH + lane;
@@ -734,7 +748,7 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             const int key0 = sq.at<WIN>(step) * STEP + warp * KEYS;
             if (!gone(key0, KEYS)) {  // warp-uniform
                 const unsigned char *stg = wsm + stage * L::STAGE;
-                if (key0 + KEYS > all || (WIN && step >= sq.end - sq.full))
+                if (key0 + KEYS > all || (WIN && step >= sq.nt - sq.edge))
                     compute(stg, key0, std::true_type{});
                 else
                     compute(stg, key0, std::false_type{});

@@ -157,21 +157,22 @@ struct PfCursor {
 };
 
 // Keys that rows [rb * RB, ...) of a sequence see, in tiles of KT.  With a
-// window: the tiles up to `first_keys` that hold first keys, then those from
-// `skip` further on, where the first row's window starts (key `low`).
+// window: of their places (see PgSpan), `len` of them, the first row's window
+// starting at `low`.
 struct PfTiles {
-    int n, first_keys, skip, low;
+    int n, len, low;
+    PgSpan span;
 };
 template <int RB, int KT, bool WIN>
 __device__ __forceinline__ PfTiles pf_span(const PagedParams &p, const KvSeq &s, int rows, int rb) {
     const int seen = kv_seen(s, (min(rows, (rb + 1) * RB) - 1) / p.rep, p.causal);
-    PfTiles r{seen > 0 ? (seen + KT - 1) / KT : 0, 0, 0, 0};
+    PfTiles r{seen > 0 ? (seen + KT - 1) / KT : 0, s.len, 0, {0, 0}};
     if constexpr (WIN) {
-        r.low = pg_low(p, (int64_t)s.end - s.count + rb * RB / p.rep);
-        const int from = min(r.low / KT, r.n);
-        r.first_keys = min((min(p.sinks, max(seen, 0)) + KT - 1) / KT, from);
-        r.skip = from - r.first_keys;
-        r.n -= r.skip;
+        const int low = pg_low(p, (int64_t)s.end - s.count + rb * RB / p.rep);
+        r.span = pg_span(p, low, max(seen, 0));
+        r.low = r.span.place(low);
+        r.len = r.span.place(s.len);
+        r.n = (r.span.place(max(seen, 0)) + KT - 1) / KT;
     }
     return r;
 }
@@ -210,11 +211,8 @@ struct PfPiece {
     int b, hk, rb, ta, tb, nt, rows, last;
     KvSeq s;
     PfTiles t;
-    // the tile of the keys, of tile j of nt
     template <bool WIN>
-    __device__ __forceinline__ int at(int j) const {
-        return WIN && j >= t.first_keys ? j + t.skip : j;
-    }
+    __device__ __forceinline__ int len() const { return WIN ? t.len : s.len; }
 };
 template <int RB, int KT, bool WIN>
 __device__ __noinline__ bool pf_step(const PagedParams &p, PfCursor &c, PfPiece &w) {
@@ -264,9 +262,9 @@ struct PfPages {
     const PagedParams &p;
     const PfPiece &w;
     __device__ __forceinline__ int64_t look(int tile, int lane) const {
-        const int key = w.at<WIN>(tile) * KT + lane * 16, hk = w.hk;
+        const int at = tile * KT + lane * 16, key = WIN ? w.t.span.key(at) : at, hk = w.hk;
         int pg = 0;
-        if (tile < w.tb && lane < KT / 16 && key < w.s.len && !(WIN && pg_hidden(p, key, 16, w.t.low))) {
+        if (tile < w.tb && lane < KT / 16 && at < w.len<WIN>() && !(WIN && pg_hidden(p, at, 16, w.t.low))) {
             pg = p.kv.page_table[(int64_t)w.b * p.kv.max_pages + (key >> p.kv.page_shift)];
             if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
                 if (p.status) atomicOr(p.status, (int)kKvBadPage);
@@ -604,16 +602,20 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 more = pf_next<RB, KT, WIN>(p, cur, &s_soft[warp - 4][turn ^ 1], lane);
 
                 const float fac = down * fabsf(p.scale) * 1.4426950408889634f;
-                const int lim = live ? kv_seen(w.s, tok, p.causal) : w.s.len;
+                const int seen = live ? kv_seen(w.s, tok, p.causal) : w.s.len;
+                const int lim = WIN ? w.t.span.place(seen) : seen;
                 const int least = __reduce_min_sync(FULL, lim);
                 // with a window: the row's start, and the latest of the warp's
-                const int low = WIN ? pg_low(p, (int64_t)w.s.end - w.s.count + tok) : 0;
+                const int low = WIN ? w.t.span.place(pg_low(p, (int64_t)w.s.end - w.s.count + tok)) : 0;
                 const int latest = WIN ? __reduce_max_sync(FULL, low) : 0;
-                auto hide = [&](float (&v)[32], int key) {  // key: v[0]'s
-                    if (key >= latest || key + 32 <= p.sinks) return;
+                auto hide = [&](float (&v)[32], int at) {  // at: v[0]'s place
+                    if (at >= latest || at + 32 <= p.sinks) return;
+                    // those from `sinks` to `low`
+                    auto below = [&](int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; };
+                    const uint32_t gone = below(low - at) & ~below(p.sinks - at);
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (k < low - key && k >= p.sinks - key) v[k] = -INFINITY;
+                        if ((gone >> k) & 1u) v[k] = -INFINITY;
                 };
                 float m = -INFINITY, l = 0.f, v_up = 0.f, v_down = 1.f;
                 const int steps = tiles * NH;
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                     // (never zero, so that a masked score stays -inf: a factor
                     // below leaves every score at zero either way)
                     const float f = fmaxf(fac * pt.k_down, 1e-37f);
-                    const int key0 = WIN ? w.at<WIN>(w.ta + i / NH) * KT + i % NH * 64 : w.ta * KT + i * 64;
+                    const int key0 = w.ta * KT + i * 64;
                     const int n_in = key0 + 64 > least ? lim - key0 : 64;
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             uint32_t x[4][G];  // keys 4 lane + j
             auto load = [&](int64_t base, int tile) {
                 const int64_t row = __shfl_sync(FULL, base, lane >> 2) + (lane & 3) * 4;
-                const int key0 = w.at<WIN>(tile) * KT, left = min(KT, w.s.len - key0);
+                const int key0 = tile * KT, left = min(KT, w.len<WIN>() - key0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // (keys that no row sees are zeros, whatever they hold)
@@ -951,7 +953,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
             uint4 kreg[KU];
             uint32_t vreg[VU][8][VW];
             auto load_k = [&](int64_t base, int tile) {
-                const int left = min(KT, w.s.len - w.at<WIN>(tile) * KT);  // keys of the tile
+                const int left = min(KT, w.len<WIN>() - tile * KT);  // keys of the tile
 #pragma unroll
                 for (int u = 0; u < KU; ++u) {
                     const int id = dw + u * kPfDeqWarps;
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
                 }
             };
             auto load_v = [&](int64_t base, int tile) {
-                const int left = min(KT, w.s.len - w.at<WIN>(tile) * KT);
+                const int left = min(KT, w.len<WIN>() - tile * KT);
 #pragma unroll
                 for (int u = 0; u < VU; ++u) {
                     const int id = dw + u * kPfDeqWarps;  // half, then 32 dimensions
