@@ -869,9 +869,9 @@ def verify_draft(logits: torch.Tensor, ids: torch.Tensor, q_start: torch.Tensor,
         (temperature, "temperature", torch.float32, R),
         (top_k, "top_k", torch.int32, R), (top_p, "top_p", torch.float32, R),
         (min_p, "min_p", torch.float32, R))]
-    token, accepted, prob = _new(2 * R + B, torch.int32, logits.device,
-                                 stream).split((R, B, R))
-    prob = prob.view(torch.float32)
+    token = _new(R, torch.int32, logits.device, stream)
+    accepted = _new(B, torch.int32, logits.device, stream)
+    prob = _new(R, torch.float32, logits.device, stream)
     if workspace is None:
         n = int(load().gwa_verify_draft_workspace_bytes(R))
         workspace = _new(max(n, 16), torch.uint8, logits.device, stream)

@@ -126,7 +126,7 @@ struct SmShared {
     u64 f_above_mass;
     float cut_x;
     uint32_t cut_idx;
-    u64 cut_mass;                   // of the tokens kept by a count
+    u64 cut_mass;                   // of a step's tokens up to the cut
 };
 
 template <bool BF16>
@@ -476,8 +476,8 @@ struct Sampler {
 
     // ---- the cut among the tokens of histogram step `bin` that lie above
     // (x, idx): their first `want` (by count), or as many as reach `want`
-    // (by mass).  Leaves the last kept token in cut_x, cut_idx, and for a
-    // count the mass of the kept in cut_mass.
+    // (by mass).  Leaves the last kept token in cut_x, cut_idx, and the mass of
+    // the kept in cut_mass.
     __device__ void refine(int bin, bool mass, u64 want, bool cut, float cut_x, uint32_t cut_idx) {
         auto in = [&](float x, uint32_t idx) {
             return bin_of(x) == bin && (!cut || x > cut_x || (x == cut_x && idx <= cut_idx));
@@ -505,6 +505,7 @@ struct Sampler {
                         for (int r = 0; r < cl; ++r) {
                             *cluster_ptr(&sh.cut_x, r) = x[j];
                             *cluster_ptr(&sh.cut_idx, r) = (uint32_t)sh.list[threadIdx.x * PT + j];
+                            if (mass) *cluster_ptr(&sh.cut_mass, r) = before + own[j];
                         }
                     before += own[j];
                 }
@@ -572,7 +573,9 @@ struct Sampler {
                 at += __popc(m);
             }
         cluster_sync_all();
-        if (!mass) {
+        if (mass) {
+            if (threadIdx.x == 0) sh.cut_mass = above + nth * own;
+        } else {
             // the mass of the kept
             const float cx = sh.cut_x;
             const uint32_t ci = sh.cut_idx;
@@ -912,6 +915,11 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             cut = true;
             cut_x = sh.cut_x;
             cut_idx = sh.cut_idx;
+            if (PLAN && least == 0) {  // all below the cut is counted
+                if (rank == 0 && tid == 0)
+                    p.plan[r] = SmPlan{top, s.row.per, cut_x, cut_idx, 0, above + sh.cut_mass};
+                return;
+            }
         }
     }
     // ---- the kept masses: a warp takes a run of whole 32-token steps, in
