@@ -293,8 +293,10 @@ static cudaError_t launch_verify_t(const VerifyParams &v, cudaStream_t st) {
 }
 
 cudaError_t launch_verify(const SampleParams &s, const VerifyParams &v, bool bf16, cudaStream_t st) {
-    const cudaError_t e = launch_sample_plan(s, bf16, st);
-    if (e != cudaSuccess) return e;
+    if (s.rows > 0) {  // (sequences without rows accept nothing)
+        const cudaError_t e = launch_sample_plan(s, bf16, st);
+        if (e != cudaSuccess) return e;
+    }
     return bf16 ? launch_verify_t<true>(v, st) : launch_verify_t<false>(v, st);
 }
 

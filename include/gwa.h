@@ -576,9 +576,9 @@ typedef struct gwa_lora {
  * Tokens of one adapter are computed together: up to 256 tokens in whatever
  * order they come, of more those that follow one another.  fp32 sums of exact
  * products; A x enters its product in two bf16 parts (2^-17 of it), and out is
- * rounded once.  Not finite inputs make their own rows' outputs so.  Results
- * do not depend on the other tokens of the call but through M, which may
- * choose another order of the sums.
+ * rounded once.  Not finite inputs make their own rows' outputs so.  Nothing
+ * of a token's result comes from other tokens; the order of its sums is one of
+ * M and K up to 256 tokens, of more also of how the adapters' runs lie.
  * Errors: GWA_ERR_UNSUPPORTED (rank, sections), GWA_ERR_INVALID_ARG,
  * GWA_ERR_MISALIGNED, GWA_ERR_WORKSPACE; nothing is enqueued on error. */
 int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora,

@@ -173,6 +173,26 @@ def test_gate_up(M, I, rank):
     assert again is gate and torch.equal(again.float(), torch.from_numpy(h).cuda().float())
 
 
+@pytest.mark.parametrize("M", [5, 300])
+def test_no_adapters_at_all(M):
+    """A server without one loaded: the base as it is, every id told."""
+    c = Case(M, np.zeros(M), adapters=1, sizes=(40, 40))
+    x, base, _, ids = c.device()
+    lora = gwa.LoRA(*(torch.empty(0, *s, dtype=torch.bfloat16, device="cuda") for s in ((2, 16, 256), (80, 16))))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = gwa.lora_add(x, base, lora, ids, status=status)
+    assert all(torch.equal(g, b) for g, b in zip(got, base)) and int(status) == 1
+    h = gwa.lora_gate_up_silu(x, base, lora, ids).float()
+    g, u = (b.double() for b in base)
+    assert ((h - g * torch.sigmoid(g) * u).abs() <= 2.0 ** -7 * h.abs() + 1e-30).all()
+
+
+def test_many_sections_of_wide_adapters():
+    """More rows of A than one pass of the tensor cores takes (256)."""
+    run(Case(9, ids_of(9, 400, 3), sizes=(16,) * 8, rank=64, adapters=3, K=96))
+    run(Case(10, ids_of(10, 400, 2), sizes=(16, 24, 8), rank=128, adapters=2, K=96))
+
+
 def test_ids_past_the_adapters_are_told():
     for M in (10, 300):
         c = Case(M, ids_of(3, M, 4))

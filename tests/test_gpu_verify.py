@@ -264,6 +264,12 @@ def test_rows_outside_every_sequence():
     run(rng, [3, 0, 4], x, y, lead=2)
 
 
+def test_no_rows_at_all():
+    z = lambda *s, t=torch.float32: torch.zeros(s, dtype=t, device="cuda")  # noqa: E731
+    token, accepted, prob = gwa.verify_draft(z(0, 50), z(0, t=torch.int32), z(4, t=torch.int32), z(0), z(3))
+    assert token.numel() == prob.numel() == 0 and accepted.tolist() == [0, 0, 0]
+
+
 @pytest.mark.parametrize("with_draft", [True, False])
 def test_the_tokens_are_the_targets(with_draft):
     """Over many sequences the first token has the target's distribution, and
