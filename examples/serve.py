@@ -162,7 +162,7 @@ class Server:
 
             def adapt(name, x, ys):
                 if lora:
-                    gwa.lora_add(x, ys, lora[name], own, out=ys, status=self.status)
+                    gwa.lora_add(x, ys, lora[name], own, out=ys, status=self.status, runs=len(todo))
                 return ys
 
             h = rms(x)
@@ -175,7 +175,7 @@ class Server:
             h = rms(x)
             if lora:
                 h = gwa.lora_gate_up_silu(h, gwa.qmv_fused_sections(h, w["gate_up"], [c.ffn, c.ffn]), lora["gate_up"],
-                                          own, status=self.status)
+                                          own, status=self.status, runs=len(todo))
             else:
                 h = gwa.qmv_gate_up_silu(h, w["gate_up"])
             x = x + adapt("down", h, [gwa.qmv_affine(h, w["down"])])[0]

@@ -173,9 +173,10 @@ def load(path: str = LIB_PATH):
                                      vp]
     lib.gwa_verify_draft_workspace_bytes.argtypes = [i64]
     lib.gwa_verify_draft_workspace_bytes.restype = sz
-    lib.gwa_lora_add.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz, vp, vp]
-    lib.gwa_lora_gate_up_silu.argtypes = [vp, i64, _Lora, vp, vp, vp, vp, vp, sz,
-                                          vp, vp]
+    lib.gwa_lora_add.argtypes = [vp, i64, _Lora, vp, i64, vp, vp, vp, vp, sz, vp,
+                                 vp]
+    lib.gwa_lora_gate_up_silu.argtypes = [vp, i64, _Lora, vp, i64, vp, vp, vp, vp,
+                                          sz, vp, vp]
     lib.gwa_lora_workspace_bytes.argtypes = [_Lora, i64]
     lib.gwa_lora_workspace_bytes.restype = sz
     for f in ("gwa_rope_table", "gwa_kv_append", "gwa_kv_read",
@@ -664,6 +665,13 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(t: torch.Tensor, stream) -> torch.Tensor:
+    """One of the shape and type of ``t``."""
+    if stream is None:
+        return torch.empty_like(t)
+    return _new(t.shape, t.dtype, t.device, stream)
+
+
 def _status(status: Optional[torch.Tensor]) -> Optional[int]:
     if status is not None and (status.dtype != torch.int32
                                or status.numel() < 1):
@@ -958,14 +966,16 @@ def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
              ids: torch.Tensor, out: Optional[Sequence[torch.Tensor]] = None,
              workspace: Optional[torch.Tensor] = None,
              status: Optional[torch.Tensor] = None,
-             stream=None) -> List[torch.Tensor]:
+             stream=None, runs: int = 0) -> List[torch.Tensor]:
     """gwa_lora_add: ``base`` (a projection's outputs, one bfloat16 [M, size]
     a section) plus each token's own low-rank adapter of x [M, K]; ids int32
-    [M] names it (negative: none).  ``out`` may be ``base``."""
+    [M] names it (negative: none).  ``out`` may be ``base``.  ``runs``: how
+    many runs of neighbours with one adapter there are at most (0: not
+    known; of more than 256 tokens it chooses the kernels)."""
     M, sizes, bp, workspace = _lora_inputs(x, lora, ids, base, workspace, stream)
     wp, wn = _ws(workspace)
     if out is None:
-        out = [_new((M, n), torch.bfloat16, x.device, stream) for n in sizes]
+        out = [_new_like(t, stream) for t in base]
         op = [t.data_ptr() for t in out]
     else:
         if len(out) != len(sizes):
@@ -975,7 +985,7 @@ def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
         op = [_ptr(t) for t in out]
     # host arrays as bytes (a ctypes array takes 2 us to make)
     form = f"{len(sizes)}q"
-    rc = load().gwa_lora_add(_ptr(x), M, lora.c, _ptr(ids),
+    rc = load().gwa_lora_add(_ptr(x), M, lora.c, _ptr(ids), runs,
                              struct.pack(form, *sizes), struct.pack(form, *bp),
                              struct.pack(form, *op), wp, wn, _status(status),
                              _stream(stream))
@@ -989,7 +999,7 @@ def lora_gate_up_silu(x: torch.Tensor, gate_up: Sequence[torch.Tensor],
                       h: Optional[torch.Tensor] = None,
                       workspace: Optional[torch.Tensor] = None,
                       status: Optional[torch.Tensor] = None,
-                      stream=None) -> torch.Tensor:
+                      stream=None, runs: int = 0) -> torch.Tensor:
     """gwa_lora_gate_up_silu: h = SiLU(gate) * up, both with each token's own
     low-rank adapter of x added; gate_up two bfloat16 [M, I]."""
     M, sizes, bp, workspace = _lora_inputs(x, lora, ids, gate_up, workspace,
@@ -998,11 +1008,11 @@ def lora_gate_up_silu(x: torch.Tensor, gate_up: Sequence[torch.Tensor],
     if len(sizes) != 2 or sizes[0] != sizes[1]:
         raise ValueError("gate and up must have the same width")
     if h is None:
-        h = _new((M, sizes[0]), torch.bfloat16, x.device, stream)
+        h = _new_like(gate_up[0], stream)
     _check_out(h, M * sizes[0], "h")
-    rc = load().gwa_lora_gate_up_silu(_ptr(x), M, lora.c, _ptr(ids), bp[0],
-                                      bp[1], _ptr(h), wp, wn, _status(status),
-                                      _stream(stream))
+    rc = load().gwa_lora_gate_up_silu(_ptr(x), M, lora.c, _ptr(ids), runs,
+                                      bp[0], bp[1], _ptr(h), wp, wn,
+                                      _status(status), _stream(stream))
     if rc:
         _check(rc)
     return h

@@ -1160,7 +1160,8 @@ static int check_lora(const gwa_lora &l, int64_t M, LoraParams *p, const char *f
                     "%s: rank=%d (a multiple of 8, 8 .. 128) sections=%d (1 .. %d)", fn,
                     (int)l.rank, (int)l.sections, kMaxSections);
     if (M < 0 || M > 0x7fffffffLL || l.K < 32 || l.K > (1 << 20) || l.K % 32 != 0 ||
-        l.N < 0 || l.N > 0x7fffffffLL || l.adapters < 0)
+        l.N < 0 || l.N > 0x7fffffffLL || l.adapters < 0 ||
+        (int64_t)l.adapters * l.sections * l.rank > 0x7fffffffLL)
         return fail(GWA_ERR_INVALID_ARG, "%s: M=%lld K=%lld (a multiple of 32) N=%lld adapters=%d",
                     fn, (long long)M, (long long)l.K, (long long)l.N, (int)l.adapters);
     p->a = l.a;
@@ -1183,11 +1184,12 @@ size_t gwa_lora_workspace_bytes(gwa_lora lora, int64_t M) {
 }
 
 static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *ids,
-                    void *workspace, size_t workspace_bytes, int32_t *status,
+                    int64_t runs, void *workspace, size_t workspace_bytes, int32_t *status,
                     void *stream, const char *fn) {
     const int outs = p.silu ? 1 : p.nsec;
     if (!x || !ids || (p.adapters > 0 && (!p.a || !p.b)))
         return fail(GWA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (runs < 0) return fail(GWA_ERR_INVALID_ARG, "%s: runs=%lld", fn, (long long)runs);
     if (!aligned(x, 16) || !aligned(ids, 4) || !aligned(p.a, 16) || !aligned(p.b, 16) ||
         !aligned(p.scale, 4) || !aligned(p.ranks, 4) || !aligned(status, 4))
         return fail(GWA_ERR_MISALIGNED, "%s: x, a, b (16 bytes), ids, scale, ranks, status (4)", fn);
@@ -1214,11 +1216,11 @@ static int run_lora(LoraParams &p, const uint16_t *x, int64_t M, const int32_t *
     p.x = x;
     p.ids = ids;
     p.status = status;
-    return launch_lora(p, M, workspace, static_cast<cudaStream_t>(stream));
+    return launch_lora(p, M, runs, workspace, static_cast<cudaStream_t>(stream));
 }
 
 int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora, const int32_t *ids,
-                 const int64_t *section_sizes, const uint16_t *const *base,
+                 int64_t runs, const int64_t *section_sizes, const uint16_t *const *base,
                  uint16_t *const *out, void *workspace, size_t workspace_bytes,
                  int32_t *status, void *stream) {
     const char *fn = "gwa_lora_add";
@@ -1243,11 +1245,11 @@ int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora, const int32_t *ids
         return fail(GWA_ERR_INVALID_ARG, "%s: sections add up to %lld, N=%lld", fn,
                     (long long)sum, (long long)p.N);
     if (M == 0 || p.N == 0) return GWA_OK;
-    return run_lora(p, x, M, ids, workspace, workspace_bytes, status, stream, fn);
+    return run_lora(p, x, M, ids, runs, workspace, workspace_bytes, status, stream, fn);
 }
 
 int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
-                          const int32_t *ids, const uint16_t *gate,
+                          const int32_t *ids, int64_t runs, const uint16_t *gate,
                           const uint16_t *up, uint16_t *h, void *workspace,
                           size_t workspace_bytes, int32_t *status, void *stream) {
     const char *fn = "gwa_lora_gate_up_silu";
@@ -1264,7 +1266,7 @@ int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
     p.base[1] = up;
     p.out[0] = h;
     if (M == 0 || p.N == 0) return GWA_OK;
-    return run_lora(p, x, M, ids, workspace, workspace_bytes, status, stream, fn);
+    return run_lora(p, x, M, ids, runs, workspace, workspace_bytes, status, stream, fn);
 }
 
 int gwa_debug_bounded_wait(uint32_t limit_us, uint32_t *out, void *stream) {

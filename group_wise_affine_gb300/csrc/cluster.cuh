@@ -57,16 +57,4 @@ __device__ __forceinline__ T *cluster_ptr(T *local, uint32_t rank) {
     return reinterpret_cast<T *>(a);
 }
 
-// Four fp32 at the same place in CTA `rank`.
-__device__ __forceinline__ float4 ld_cluster_f32x4(const float *local, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a)
-                 : "memory");
-    return v;
-}
-
 }  // namespace gwa

@@ -162,7 +162,8 @@ struct LoraParams {
     int32_t *shares;        // many tokens: how many there are
     int sec_blocks[kMaxSections];  // blocks of a section's outputs
 };
-int launch_lora(LoraParams p, int64_t M, void *workspace, cudaStream_t st);  // a status
+// (a status; runs of neighbours with one adapter, at most, 0: not known)
+int launch_lora(LoraParams p, int64_t M, int64_t runs, void *workspace, cudaStream_t st);
 size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank);
 unsigned int lora_timeouts(bool reset);
 

@@ -552,7 +552,7 @@ size_t gwa_verify_draft_workspace_bytes(int64_t rows);
  *          value outside counts as the nearer end); what lies past it in a
  *          and b is taken as zero, whatever it holds
  * rank a multiple of 8, 8 .. 128; K a positive multiple of 32; sections 1 ..
- * 8; adapters >= 0; a and b 16-byte aligned. */
+ * 8; adapters >= 0, fewer than 2^31 rows of a; a and b 16-byte aligned. */
 typedef struct gwa_lora {
     const uint16_t *a;
     const uint16_t *b;
@@ -568,6 +568,11 @@ typedef struct gwa_lora {
  *   ids   int32 [M] on the device: a negative number is no adapter (out =
  *         base); one of `adapters` and more counts as none and sets bit 1 of
  *         `status` (NULL, or a device int32 that the caller clears)
+ *   runs  how many runs of neighbours with one adapter there are at most (0:
+ *         not known).  Chooses kernels for more than 256 tokens: where there
+ *         are more than M / 8, as single tokens of many conversations have,
+ *         256 tokens at a time are put in order, else runs are taken as they
+ *         come
  *   section_sizes  host int64 [sections], adding up to N
  *   base, out      host arrays of [M, size] bf16 buffers, 2-byte aligned
  *         (rows of 16-byte units are read faster); out_s may be base_s, and
@@ -578,11 +583,12 @@ typedef struct gwa_lora {
  * products; A x enters its product in two bf16 parts (2^-17 of it), and out is
  * rounded once.  Not finite inputs make their own rows' outputs so.  Nothing
  * of a token's result comes from other tokens; the order of its sums is one of
- * M and K up to 256 tokens, of more also of how the adapters' runs lie.
+ * M and K up to 256 tokens, of more also of `runs` and how the runs lie.
  * Errors: GWA_ERR_UNSUPPORTED (rank, sections), GWA_ERR_INVALID_ARG,
  * GWA_ERR_MISALIGNED, GWA_ERR_WORKSPACE; nothing is enqueued on error. */
 int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora,
-                 const int32_t *ids, const int64_t *section_sizes,
+                 const int32_t *ids, int64_t runs,
+                 const int64_t *section_sizes,
                  const uint16_t *const *base, uint16_t *const *out,
                  void *workspace, size_t workspace_bytes, int32_t *status,
                  void *stream);
@@ -592,8 +598,9 @@ int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora,
  * once.  gate, up, h bf16 [M, I]; h may be gate or up.  The shared halves come
  * from gwa_qmv_fused_sections over the [gate; up] weight with sections (I, I). */
 int gwa_lora_gate_up_silu(const uint16_t *x, int64_t M, gwa_lora lora,
-                          const int32_t *ids, const uint16_t *gate,
-                          const uint16_t *up, uint16_t *h, void *workspace,
+                          const int32_t *ids, int64_t runs,
+                          const uint16_t *gate, const uint16_t *up,
+                          uint16_t *h, void *workspace,
                           size_t workspace_bytes, int32_t *status,
                           void *stream);
 /* 0 (and gwa_last_error) for adapters or M that the calls refuse, and for M = 0. */

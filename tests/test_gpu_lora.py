@@ -129,6 +129,16 @@ def test_prompts(runs):
     run(Case(sum(runs), ids, sizes=(48, 8), adapters=3))
 
 
+@pytest.mark.parametrize("M", [257, 511, 512, 700, 9000])
+def test_short_runs_that_are_told(M):
+    """256 tokens at a time, in order; the same values up to the order of sums."""
+    run(Case(M, ids_of(M, M, 5), adapters=5, K=96), runs=M)
+    c = Case(M + 1, ids_of(M, M, 5), sizes=(24, 24), rank=32, adapters=5, K=64)
+    x, (gate, up), lora, ids = c.device()
+    a, b = (gwa.lora_gate_up_silu(x, (gate, up), lora, ids, runs=r).double() for r in (0, M))
+    assert ((a - b).abs() <= 2.0 ** -7 * a.abs() + 1e-3).all()
+
+
 def test_one_adapter_for_all_and_one_for_each():
     run(Case(1, np.zeros(200), adapters=1))
     run(Case(2, np.arange(200), adapters=200, K=64))

@@ -43,10 +43,10 @@ BAD = [("rank", 4, "UNSUPPORTED"), ("rank", 12, "UNSUPPORTED"), ("rank", 136, "U
        ("ranks", (1 << 20) + 1, "MISALIGNED")]
 
 
-def call(lib, l, x=1 << 20, M=4, ids=1 << 20, sizes=(64, 32), base=(1 << 20, 1 << 20), out=(1 << 20, 1 << 20), ws=1 << 20,
+def call(lib, l, x=1 << 20, M=4, ids=1 << 20, runs=0, sizes=(64, 32), base=(1 << 20, 1 << 20), out=(1 << 20, 1 << 20), ws=1 << 20,
          n=1 << 30, status=None):
     c = lambda t, v: (t * len(v))(*v)  # noqa: E731
-    return lib.gwa_lora_add(x, M, l, ids, c(ctypes.c_int64, sizes), c(ctypes.c_void_p, base), c(ctypes.c_void_p, out), ws, n,
+    return lib.gwa_lora_add(x, M, l, ids, runs, c(ctypes.c_int64, sizes), c(ctypes.c_void_p, base), c(ctypes.c_void_p, out), ws, n,
                             status, None)
 
 
@@ -56,12 +56,12 @@ def test_adapters_are_checked(lib, field, value, code):
     want = getattr(gwa, "GWA_ERR_" + code)
     assert call(lib, lora(gwa, **{field: value})) == want
     assert gwa.last_error()
-    assert lib.gwa_lora_gate_up_silu(1 << 20, 4, lora(gwa, **{field: value}), 1 << 20, 1 << 20, 1 << 20, 1 << 20, 1 << 20, 1 << 30,
+    assert lib.gwa_lora_gate_up_silu(1 << 20, 4, lora(gwa, **{field: value}), 1 << 20, 0, 1 << 20, 1 << 20, 1 << 20, 1 << 20, 1 << 30,
                                      None, None) == want
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(x=None), "INVALID_ARG"), (dict(ids=None), "INVALID_ARG"), (dict(M=-1), "INVALID_ARG"),
+    (dict(x=None), "INVALID_ARG"), (dict(ids=None), "INVALID_ARG"), (dict(runs=-1), "INVALID_ARG"), (dict(M=-1), "INVALID_ARG"),
     (dict(sizes=(64, 31)), "INVALID_ARG"), (dict(sizes=(-1, 97)), "INVALID_ARG"), (dict(base=(1 << 20, None)), "INVALID_ARG"),
     (dict(out=(None, 1 << 20)), "INVALID_ARG"), (dict(out=((1 << 20) + 1, 1 << 20)), "MISALIGNED"),
     (dict(x=(1 << 20) + 8), "MISALIGNED"), (dict(ids=(1 << 20) + 2), "MISALIGNED"), (dict(status=(1 << 20) + 2), "MISALIGNED"),
@@ -75,7 +75,13 @@ def test_gate_up_wants_two_equal_sections(lib):
     import group_wise_affine_gb300 as gwa
     p = 1 << 20
     for l in (lora(gwa, sections=3), lora(gwa, N=97), lora(gwa, sections=1)):
-        assert lib.gwa_lora_gate_up_silu(p, 4, l, p, p, p, p, p, 1 << 30, None, None) == gwa.GWA_ERR_INVALID_ARG
+        assert lib.gwa_lora_gate_up_silu(p, 4, l, p, 0, p, p, p, p, 1 << 30, None, None) == gwa.GWA_ERR_INVALID_ARG
+
+
+def test_rows_past_31_bits_are_refused(lib):
+    import group_wise_affine_gb300 as gwa
+    assert call(lib, lora(gwa, adapters=1 << 27)) == gwa.GWA_ERR_INVALID_ARG
+    assert "adapters=134217728" in gwa.last_error()
 
 
 def test_nothing_to_do_and_workspaces(lib):
