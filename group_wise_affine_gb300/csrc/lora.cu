@@ -5,19 +5,36 @@
 //   t[m,s,:] = scale_a (A_a[s] x_m),       a = ids[m], rank_a rows of A_a[s]
 //   y_s[m,n] = base_s[m,n] + B_a[s][n,:] . t[m,s,:]
 //
-// and for the gated projection SiLU(y_0) y_1.  Two kernels: x against the A's
+// and for the gated projection SiLU(y_0) y_1.  Two products: x against the A's
 // (shrink), whose few results a token go through the workspace, and those
 // against the B's (expand).  Products are exact, sums fp32; t enters its
 // product as two bf16 parts (together 2^-17 of it), so the output's rounding
 // is the only one to count.
 //
-// Tokens of one adapter are taken together, 16 to a tile, so that an adapter
-// is read once for them: up to kLoSort tokens every CTA puts them in the order
-// of their adapters itself, beyond that runs of neighbours are taken as they
-// come (a prompt's tokens are neighbours).
+// Tokens of one adapter are taken together, in tiles, so that an adapter is
+// read once for them.  Two ways, by the number of tokens:
+//   up to kLoSort: every CTA of both kernels puts the tokens in the order of
+//     their adapters itself (1.5 us; a kernel for it would cost a launch).
+//     Warp-level MMAs (m16n8k16, an adapter's rows the 16): a tile has few
+//     tokens, and the bytes of A and B bound the work.
+//   more: runs of neighbours as they come (a prompt's tokens are neighbours),
+//     x against A on tcgen05, a kernel that adds up the shares of K once, and
+//     the outputs by warp-level MMAs.
+// Each kernel starts while the one in front of it ends, and does what does not
+// depend on it (tiles, the first loads of B and base) before it waits.
+//
+// Bound by bytes: A and B of the adapters at hand, x, base and out.  Measured
+// (bf16, replayed with the adapters in L2 where they fit; of the 6.68 TB/s of a
+// copy): one token, rank 16, 5120 to 7168, 8.3 us, 0.1 of them bytes: two
+// launches that depend on each other, tiles, a round of loads each.  54 tokens
+// of 24 adapters of ranks 8 to 64 there, 45 MB, 18.6 us (2.4 TB/s, 0.36): lines
+// of L1, as a fragment load of 8 rows touches 8, and two rounds of units.  14
+// sequences of up to 5 tokens, gate and up of 13824, rank 32, 19 MB, 12.4 us
+// (1.5 TB/s).  Prompts of 5560 tokens, 13824 to 5120, rank 64, 272 MB, 93 us
+// (2.9 TB/s): shrink 38 (x at 4 TB/s), join 5, expand 50 (L1 at 55%, issue 41%:
+// B's and t's fragments and the base pass through it).
 #include <algorithm>
 
-#include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
 #include "mma.cuh"

@@ -56,6 +56,17 @@
 // from one to the next, with 16 warps an SM to hide it.  The bytes alone would
 // take half the time.  Short caches are two launches and their dependent reads
 // (lengths, pages, codes).
+//
+// A window (WIN).  A token at position p then sees the keys from p - window + 1
+// on and those below `sinks`, and nothing else of the cache is read: steps are
+// counted over the places of PgSpan (the sinks, then the window's keys, in
+// sixteens), whatever the cache's length.  Steps that every row sees whole come
+// first, so that what the mask hides does not decide their roundings.  Measured:
+// one token over 131071 keys through 4096 and 4 sinks 14.5 us, as over a
+// cache of 4096; 54 sequences of up to 4 drafted tokens through 1024 and 16, u8,
+// 32 heads over 8, 57 us (120 MB, 2.1 TB/s): 1050 instructions for a warp's 32 keys of 16
+// rows, issued at 36% with three CTAs an SM (the u8 ring), waiting for one
+// another and, at 13%, for instructions.
 #include <algorithm>
 #include <type_traits>
 

@@ -58,6 +58,14 @@
 // twice, took 395 us to 346.  A block of 256 dimensions has one row tile, so
 // nothing hides its start and end (19 thousand cycles of loading queries and
 // writing rows beside 13 steps of 4500).
+//
+// With a window (WIN, see paged_attention.cu) a block's tiles are those of its
+// own span of places, and rows are masked at both ends of it.  2048 tokens of
+// 40 heads of 128 through 2048 keys and 4 sinks of 16384 157 us (86 GFLOP of
+// unmasked pairs, 550 TFLOP/s): a block has some 34 tiles of which 4 or 5 are
+// cut by a window's end, its start and end count as much as two, and every
+// block unpacks its own.  Ragged prompts of up to 1100, 16 heads of 256 over 2,
+// through 501 and 3, 118 us: short blocks of one row tile.
 #include <algorithm>
 
 #include "common.cuh"

@@ -46,6 +46,9 @@
 // histogram 45, ranking and the last pass 45), and nothing of the next row is
 // loaded meanwhile: 101 us for those rows with filters of all kinds, 16 us for
 // one row of 131072 fp32 on 16 CTAs.
+//
+// With PLAN the same passes end before the draw, and leave the cut and the sum
+// (of a row cut by top-p alone the sum is known with the cut: no last pass).
 #include <algorithm>
 #include <mutex>
 #include <set>
