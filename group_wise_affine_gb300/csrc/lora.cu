@@ -19,7 +19,7 @@
 //     tokens, and the bytes of A and B bound the work.
 //   more: runs of neighbours as they come (a prompt's tokens are neighbours),
 //     x against A on tcgen05, a kernel that adds up the shares of K once, and
-//     the outputs by warp-level MMAs.
+//     the outputs on tcgen05 too, or by warp-level MMAs (see lora_out_tc).
 // Each kernel starts while the one in front of it ends, and does what does not
 // depend on it (tiles, the first loads of B and base) before it waits.
 //
@@ -30,9 +30,9 @@
 // of 24 adapters of ranks 8 to 64 there, 45 MB, 18.6 us (2.4 TB/s, 0.36): lines
 // of L1, as a fragment load of 8 rows touches 8, and two rounds of units.  14
 // sequences of up to 5 tokens, gate and up of 13824, rank 32, 19 MB, 12.4 us
-// (1.5 TB/s).  Prompts of 5560 tokens, 13824 to 5120, rank 64, 272 MB, 93 us
-// (2.9 TB/s): shrink 38 (x at 4 TB/s), join 5, expand 50 (L1 at 55%, issue 41%:
-// B's and t's fragments and the base pass through it).
+// (1.5 TB/s).  Prompts of 5560 tokens, 13824 to 5120, rank 64, 272 MB, 74 us
+// (3.7 TB/s): shrink 38 (x at 4 TB/s), join 5, outputs some 27 (the rest is
+// launches).
 #include <algorithm>
 
 #include "common.cuh"
@@ -58,7 +58,7 @@ struct LoTiles {
     __align__(16) int key[FEW ? kLoSort : 1];  // of the places: adapter
     int rank[FEW ? kLoSort : 1];               // and its rank
     int base[FEW ? kLoSort + 1 : 1];           // of the tiles: 16-row blocks of A before it
-    int w_max[kLoWarps], w_sum[kLoWarps];
+    int w_max[FEW ? kLoWarps : 16], w_sum[FEW ? kLoWarps : 16];
     __device__ __forceinline__ int token(int place) const { return FEW ? order[place] : place; }
 };
 
@@ -122,6 +122,7 @@ __device__ int lo_tiles(const LoraParams &p, LoTiles<true> &sh) {
 }
 // More: runs of neighbours.  A warp reads a share of the tokens, 32 at a time,
 // and marks where the adapter changes; then each lane takes one such group.
+// (Warps past the kLoWarps have no share.)
 template <int TM>
 __device__ int lo_tiles(const LoraParams &p, LoTiles<false> &sh) {
     constexpr unsigned FULL = 0xffffffffu;
@@ -659,13 +660,17 @@ __global__ void __launch_bounds__(kLoThreads, 1)
 
 // low[m][s][r / 4]: t of many tokens, the shares' sums times the scale, as hi and
 // lo bf16 parts; zero past the adapter's rank.  (Made once here; each of a
-// dozen expanding CTAs summing its tokens' up again took 10 us.)
-__global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p) {
+// dozen expanding CTAs summing its tokens' up again took 10 us.)  PLANES: two
+// rows of `pitch` bf16 a section instead, the hi and the lo parts, as TMA brings
+// them to the tensor cores.
+template <bool PLANES>
+__global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p, int pitch) {
     // (before the wait: this kernel starts behind the first one's wait already)
     if (threadIdx.x == 0) pdl_launch_dependents();
     constexpr int AT = 4;  // units of a thread at a time
-    const int quads = p.rank / 4, of_token = p.nsec * quads, stride = gridDim.x * kLoThreads;
+    const int quads = (PLANES ? pitch : p.rank) / 4, of_token = p.nsec * quads, stride = gridDim.x * kLoThreads;
     const int all = p.M * of_token;  // (8192 tokens x 8 sections x 32 at most)
+    const int of_share = p.M * p.nsec * (p.rank / 4);
     int ks = 0;
     for (int i0 = blockIdx.x * kLoThreads + threadIdx.x; i0 < all; i0 += AT * stride) {
         int rank[AT];
@@ -685,12 +690,12 @@ __global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p
         for (int x = 0; x < AT; ++x) v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
         for (int k = 0; k < ks; ++k) {
-            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (int64_t)k * all;
+            const float4 *src = reinterpret_cast<const float4 *>(p.part) + (int64_t)k * of_share;
 #pragma unroll
             for (int x = 0; x < AT; ++x) {
-                const int i = i0 + x * stride;
-                if (i % quads * 4 >= rank[x]) continue;
-                const float4 e = __ldcg(src + i);
+                const int i = i0 + x * stride, q = i % quads;
+                if (q * 4 >= rank[x]) continue;
+                const float4 e = __ldcg(src + (PLANES ? i / quads * (p.rank / 4) + q : i));
                 v[x] = make_float4(v[x].x + e.x, v[x].y + e.y, v[x].z + e.z, v[x].w + e.w);
             }
         }
@@ -701,8 +706,15 @@ __global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p
             const float a = v[x].x * scale[x], b = r + 1 < rank[x] ? v[x].y * scale[x] : 0.f;
             const float c = r + 2 < rank[x] ? v[x].z * scale[x] : 0.f, d = r + 3 < rank[x] ? v[x].w * scale[x] : 0.f;
             const uint32_t h0 = pack_bf16(a, b), h1 = pack_bf16(c, d);
-            p.low[i] = make_uint4(h0, h1, pack_bf16(a - bf16_lo(h0), b - bf16_hi(h0)),
-                                  pack_bf16(c - bf16_lo(h1), d - bf16_hi(h1)));
+            const uint32_t l0 = pack_bf16(a - bf16_lo(h0), b - bf16_hi(h0));
+            const uint32_t l1 = pack_bf16(c - bf16_lo(h1), d - bf16_hi(h1));
+            if constexpr (PLANES) {
+                uint16_t *dst = reinterpret_cast<uint16_t *>(p.low) + (int64_t)(i / quads) * 2 * pitch + r;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(h0, h1);
+                *reinterpret_cast<uint2 *>(dst + pitch) = make_uint2(l0, l1);
+            } else {
+                p.low[i] = make_uint4(h0, h1, l0, l1);
+            }
         }
     }
     pdl_wait_primary();
@@ -934,6 +946,315 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
     pdl_wait_primary();
 }
 
+// The same on tcgen05, where TMA can bring base and out (rows of 16-byte units)
+// and ranks are up to 64: D (128 tokens x 64 outputs, two such chunks a block) =
+// t_hi B^T + t_lo B^T, with the parts of t as rows of 128 bytes, and B's rows as
+// they lie.  Work is the bytes of base and out; a CTA takes an equal run of the
+// blocks of all tiles, one section of a tile after the other, so that t stays.
+// Gate and up are the two chunks of a block.  A block of 128 tokens takes some
+// 2500 to 3000 cycles: the three stages' turn is loads 2500, MMAs 1000 (110 each
+// at N = 64 and 128 alike, so both chunks of a section go at once), adding 1500,
+// out 1000; the bytes would take 2750 at HBM's rate.
+//
+// Warps: 0 issues the copies of base, B and t, 1 the MMAs (a thread each; with
+// a rank inside a k step it first clears what B holds past it), 4 to 11 add D to
+// the base where it lies, a thread to a token and half a block, 2 sends the
+// results out, 128 or 16 tokens a copy; the rest of a tile below 16 is stored by
+// the adding threads, as its neighbours' rows are others'.
+constexpr int kLeThreads = 384;
+constexpr int kLeStage = 48 * 1024, kLeB = 32 * 1024;  // base's two chunks, then B's
+struct LoMaps {
+    CUtensorMap t, b, base[kMaxSections], out[kMaxSections];  // 16 tokens
+    CUtensorMap base_all[kMaxSections], out_all[kMaxSections];  // a tile's 128
+};
+template <bool SILU>
+struct LoOut {
+    static constexpr int COLS = SILU ? 64 : 128;      // outputs of a block
+    static constexpr int PARTS = SILU ? 4 : 2;        // operand tiles of t
+    static constexpr int STAGES = 3;
+    static constexpr int SMEM = 1024 + PARTS * 16384 + STAGES * kLeStage;
+};
+__device__ __forceinline__ void lt_store(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+
+template <bool SILU>
+__global__ void __launch_bounds__(kLeThreads, 1)
+    lora_many_out_kernel(const __grid_constant__ LoMaps maps, const __grid_constant__ LoraParams p, int pitch) {
+    using L = LoOut<SILU>;
+    constexpr int ST = L::STAGES;
+    constexpr unsigned FULL = 0xffffffffu;
+    extern __shared__ __align__(1024) unsigned char lo_raw[];
+    unsigned char *const parts = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(lo_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *const stages = parts + L::PARTS * 16384;
+    __shared__ LoTiles<false> sh;
+    __shared__ uint16_t list[SILU ? 1 : kLoChunk];  // tiles with something to do (SILU: all)
+    __shared__ uint64_t full[ST], empty[ST], ready[ST], accfull[2], accfree[2], tfull, tfree;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_fail, s_issued, s_parts, s_count[kLeThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+    if (tid == 0) {
+        pdl_launch_dependents();
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+            mbar_init(&ready[i], 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&accfull[i], 1);
+            mbar_init(&accfree[i], 8);
+        }
+        mbar_init(&tfull, 1);
+        mbar_init(&tfree, 1);
+        fence_mbar_init();
+        s_fail = s_issued = s_parts = 0;
+    }
+    if (warp == 1) tmem_alloc(&s_tmem, 256);
+    tc_fence_before();
+    const int tiles = lo_tiles<kLtTile>(p, sh);  // (synchronizes)
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    int active = SILU ? tiles : 0;
+    for (int t0 = 0; !SILU && t0 < tiles; t0 += kLeThreads) {
+        const int i = t0 + tid;
+        const bool on = i < tiles && (!p.in_place || lo_rank(p, lo_id(p, sh.start[i])) > 0);
+        const unsigned all = __ballot_sync(FULL, on);
+        if (lane == 0) s_count[warp] = __popc(all);
+        __syncthreads();
+        int at = active + __popc(all & ((1u << lane) - 1u));
+        for (int w = 0; w < kLeThreads / 32; ++w) {
+            if (w < warp) at += s_count[w];
+            active += s_count[w];
+        }
+        if (on) list[at] = (uint16_t)i;
+        __syncthreads();
+    }
+
+    // ---- the CTA's blocks
+    struct Block {
+        int64_t left;
+        int tile, sec, blk;
+        int at, n, id, rank;
+        bool fresh;  // t is another than the last block's
+    };
+    int per = 0;
+    for (int s = 0; s < (SILU ? 1 : p.nsec); ++s) per += p.sec_blocks[s];
+    auto open = [&](Block &c) {
+        const int i = SILU ? c.tile : list[c.tile];
+        c.at = sh.start[i];
+        c.n = sh.start[i + 1] - c.at;
+        c.id = lo_id(p, c.at);
+        c.rank = lo_rank(p, c.id);
+    };
+    auto first = [&] {
+        Block c;
+        const int64_t all = (int64_t)active * per, from = all * blockIdx.x / gridDim.x;
+        c.left = all * (blockIdx.x + 1) / gridDim.x - from;
+        c.sec = 0;
+        c.fresh = true;
+        if (c.left > 0) {
+            c.tile = (int)(from / per);
+            c.blk = (int)(from - (int64_t)c.tile * per);
+            while (c.blk >= p.sec_blocks[c.sec]) c.blk -= p.sec_blocks[c.sec++];
+            open(c);
+        }
+        return c;
+    };
+    auto next = [&](Block &c) {
+        c.fresh = false;
+        if (--c.left <= 0) return;
+        ++c.blk;
+        while (c.blk >= p.sec_blocks[c.sec]) {
+            c.blk = 0;
+            c.fresh = true;
+            if (++c.sec == (SILU ? 1 : p.nsec)) {
+                c.sec = 0;
+                ++c.tile;
+                open(c);
+            }
+        }
+    };
+    bool ok = true;
+    uint32_t it = 0, t = 0;
+    if (warp == 0) {
+        if (lane == 0) {
+            for (Block c = first(); c.left > 0; next(c), ++it) {
+                const uint32_t s = it % ST;
+                if (it >= ST && !(ok = lt_wait(&empty[s], ((it / ST) & 1) ^ 1, &s_fail))) break;
+                unsigned char *st = stages + s * kLeStage;
+                const int col = c.blk * L::COLS;
+                const bool all = c.n > 32;  // (a copy takes 100 cycles to issue)
+                const int boxes = all ? 8 : (c.n + 15) / 16;
+                const int chunks = SILU || col + 64 < p.sec_n[c.sec] ? 2 : 1;
+                mbar_expect_tx(&full[s], chunks * boxes * 2048 + 2 * 8192);
+                for (int x = 0; x < chunks; ++x) {
+                    const int sec = SILU ? x : c.sec, at = SILU ? col : col + 64 * x;
+                    if (all)
+                        tma_load_2d(st + x * 16384, &maps.base_all[sec], at, c.at, &full[s]);
+                    else
+                        for (int b = 0; b < boxes; ++b)
+                            tma_load_2d(st + x * 16384 + b * 2048, &maps.base[sec], at, c.at + 16 * b, &full[s]);
+                }
+                for (int x = 0; x < 2; ++x)
+                    tma_load_2d(st + kLeB + x * 8192, &maps.b, 0,
+                                (int)(max(c.id, 0) * p.N + p.sec_start[SILU ? x : c.sec]) +
+                                    (SILU ? col : col + 64 * x),
+                                &full[s]);
+                s_issued = it + 1;
+                if (!c.fresh) continue;
+                if (t == 0) {
+                    pdl_wait_primary();
+                    asm volatile("fence.proxy.async;" ::: "memory");
+                } else if (!(ok = lt_wait(&tfree, (t - 1) & 1, &s_fail))) {
+                    break;
+                }
+                mbar_expect_tx(&tfull, L::PARTS * 16384);
+                for (int x = 0; x < L::PARTS; ++x)
+                    tma_load_2d(parts + x * 16384, &maps.t, ((SILU ? 0 : 2 * c.sec) + x) * pitch, c.at, &tfull);
+                s_parts = ++t;
+            }
+        }
+    } else if (warp == 1) {
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(L::COLS >> 3) << 17) |
+                               ((uint32_t)(kLtTile >> 4) << 24);
+        for (Block c = first(); c.left > 0; ++it) {
+            const uint32_t s = it % ST, buf = it & 1;
+            unsigned char *bs = stages + s * kLeStage + kLeB;
+            if (c.fresh && !__all_sync(FULL, lt_wait(&tfull, t++ & 1, &s_fail))) break;
+            if (!__all_sync(FULL, lt_wait(&full[s], (it / ST) & 1, &s_fail))) break;
+            if (it >= 2 && !__all_sync(FULL, lt_wait(&accfree[buf], ((it >> 1) - 1) & 1, &s_fail))) break;
+            if (c.rank % 16) {
+                for (int r = lane; r < 128; r += 32)
+                    for (int k = c.rank; k % 16; ++k)
+                        *reinterpret_cast<uint16_t *>(bs + r * 128 + (((k >> 3) ^ (r & 7)) << 4) + (k & 7) * 2) = 0;
+                fence_proxy_async();
+                __syncwarp();
+            }
+            tc_fence_after();
+            const int nk = (c.rank + 15) / 16;
+            Block then = c;
+            next(then);
+            if (lane == 0) {
+                // (both chunks of a section at once, 128 outputs, half the MMAs)
+                for (int x = 0; x < (SILU ? 2 : 1); ++x) {
+                    const uint64_t b = smem_desc_sw128(smem_u32(bs + x * 8192));
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t a = smem_desc_sw128(smem_u32(parts + (2 * x + h) * 16384));
+                        for (int k = 0; k < nk; ++k)
+                            lt_mma(tmem + buf * 128 + x * 64, a + 2 * k, b + 2 * k, idesc, h + k > 0 ? 1u : 0u);
+                    }
+                }
+                tc_commit(&accfull[buf]);
+                if (then.left > 0 && then.fresh) tc_commit(&tfree);
+            }
+            __syncwarp();
+            c = then;
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            for (Block c = first(); c.left > 0; next(c), ++it) {
+                const uint32_t s = it % ST;
+                if (!(ok = lt_wait(&ready[s], (it / ST) & 1, &s_fail))) break;
+                const int col = c.blk * L::COLS;
+                for (int x = 0; x < (SILU ? 1 : 2); ++x)
+                    if (col + 64 * x < p.sec_n[c.sec]) {
+                        unsigned char *src = stages + s * kLeStage + x * 16384;
+                        if (c.n == kLtTile)
+                            lt_store(&maps.out_all[c.sec], src, col + 64 * x, c.at);
+                        else
+                            for (int b = 0; b < c.n / 16; ++b)
+                                lt_store(&maps.out[c.sec], src + b * 2048, col + 64 * x, c.at + 16 * b);
+                    }
+                asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(&empty[s]);
+            }
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3, row = q * 32 + lane, half = (warp - 4) / 4;
+        for (Block c = first(); c.left > 0; next(c), ++it) {
+            const uint32_t s = it % ST, buf = it & 1;
+            ok = lt_wait(&full[s], (it / ST) & 1, &s_fail) && lt_wait(&accfull[buf], (it >> 1) & 1, &s_fail);
+            if (!__all_sync(FULL, ok)) break;
+            tc_fence_after();
+            const int64_t N = p.sec_n[c.sec];
+            // 64 outputs of a chunk, or 32 of both
+            const int in = SILU ? 32 * half : 0, chunk = SILU ? 0 : half;
+            const int64_t col = (int64_t)c.blk * L::COLS + 64 * chunk + in;
+            unsigned char *src = stages + s * kLeStage + chunk * 16384 + row * 128;
+            if (q * 32 < c.n && col < N) {
+                float v[2][32];
+                if (c.rank > 0) {
+                    const uint32_t d = tmem + buf * 128 + chunk * 64 + in + ((uint32_t)(q * 32) << 16);
+                    tc_ld32_async(d, v[0]);
+                    tc_ld32_async(d + (SILU ? 64 : 32), v[1]);
+                    tc_ld_wait(v[0]);
+                    tc_ld_tie(v[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i / 32][i % 32] = -0.f;  // (a base of -0 stays)
+                }
+                const bool sent = row < (c.n & ~15);
+                uint16_t *dst = p.out[c.sec] + (int64_t)(c.at + row) * N + col;
+#pragma unroll
+                for (int j = 0; j < (SILU ? 4 : 8); ++j) {  // 8 outputs
+                    unsigned char *place = src + (((in / 8 + j) ^ (row & 7)) << 4);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(place);
+                    const uint4 e = SILU ? *reinterpret_cast<const uint4 *>(place + 16384) : b;
+                    const uint32_t bw[4] = {b.x, b.y, b.z, b.w}, ew[4] = {e.x, e.y, e.z, e.w};
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = 8 * j + 2 * i;
+                        float lo = bf16_lo(bw[i]) + v[SILU ? 0 : at / 32][at % 32];
+                        float hi = bf16_hi(bw[i]) + v[SILU ? 0 : at / 32][at % 32 + 1];
+                        if constexpr (SILU) {
+                            lo = __fdividef(lo, 1.f + __expf(-lo)) * (bf16_lo(ew[i]) + v[1][at]);
+                            hi = __fdividef(hi, 1.f + __expf(-hi)) * (bf16_hi(ew[i]) + v[1][at + 1]);
+                        }
+                        w[i] = pack_bf16(lo, hi);
+                    }
+                    if (sent)
+                        *reinterpret_cast<uint4 *>(place) = make_uint4(w[0], w[1], w[2], w[3]);
+                    else if (row < c.n && col + 8 * j < N)
+                        *reinterpret_cast<uint4 *>(dst + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            tc_fence_before();
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&accfree[buf]);
+                mbar_arrive(&ready[s]);
+            }
+        }
+    }
+    // ---- teardown: without a wait that ran out, every copy and MMA was waited for
+    tc_fence_before();
+    __syncthreads();
+    if (s_fail) {
+        if (tid == 0) {
+            for (int k = max(0, s_issued - ST); k < s_issued; ++k)
+                if (!mbar_wait(&full[k % ST], (k / ST) & 1)) break;
+            if (s_parts > 0) mbar_wait(&tfull, (s_parts - 1) & 1);
+        }
+        if (tid == 32) {
+            tc_commit(&accfull[0]);  // completes after every MMA this thread issued
+            mbar_wait(&accfull[0], 0, 1000000ull);
+            mbar_wait(&accfull[0], 1, 1000000ull);
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 256);
+    // (what runs next waits for this kernel alone)
+    pdl_wait_primary();
+}
+
 // ---------------------------------------------------------------- host side
 template <int KS, bool SILU, bool VEC>
 static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
@@ -992,7 +1313,48 @@ static cudaError_t pick_many(const LoraParams &p, cudaStream_t st) {
     return p.vec ? launch_many<KS, false, true>(p, st) : launch_many<KS, false, false>(p, st);
 }
 
-static int launch_lora_many(LoraParams p, cudaStream_t st) {
+template <bool SILU>
+static int launch_out(LoraParams p, int pitch, cudaStream_t st) {
+    using L = LoOut<SILU>;
+    const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    LoMaps maps{};
+    int rc = encode_2d(&maps.t, bf, 2, p.low, (int64_t)p.nsec * 2 * pitch, p.M, 64, kLtTile, sw, "low-rank sums");
+    if (!rc) rc = encode_2d(&maps.b, bf, 2, p.b, p.rank, p.adapters * p.N, 64, 64, sw, "adapters");
+    for (int s = 0; s < p.nsec && !rc; ++s) {
+        p.sec_blocks[s] = (int)((p.sec_n[s] + L::COLS - 1) / L::COLS);
+        if (p.sec_n[s] == 0) continue;
+        rc = encode_2d(&maps.base[s], bf, 2, p.base[s], p.sec_n[s], p.M, 64, 16, sw, "base");
+        if (!rc) rc = encode_2d(&maps.base_all[s], bf, 2, p.base[s], p.sec_n[s], p.M, 64, kLtTile, sw, "base");
+        if (rc || (SILU && s)) continue;
+        rc = encode_2d(&maps.out[s], bf, 2, p.out[s], p.sec_n[s], p.M, 64, 16, sw, "outputs");
+        if (!rc) rc = encode_2d(&maps.out_all[s], bf, 2, p.out[s], p.sec_n[s], p.M, 64, kLtTile, sw, "outputs");
+    }
+    if (rc) return rc;
+    const void *kfn = reinterpret_cast<const void *>(lora_many_out_kernel<SILU>);
+    cudaError_t e = allow_smem(kfn, L::SMEM);
+    if (e == cudaSuccess) e = launch_pdl(kfn, dim3(num_sms()), kLeThreads, L::SMEM, st, maps, p, pitch);
+    return e == cudaSuccess ? GWA_OK : set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
+}
+
+// (rows of t's parts in the tensor cores' k steps)
+static int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
+
+// Outputs on tcgen05 where TMA can bring them (and a row of B has an int's
+// coordinate), for long runs: a block takes some 2400 cycles whatever its tokens.
+// The whole call there against warp-level MMAs, us: rank 16, 5120 to 7168, one
+// run of 512 tokens 24.7 / 20.6, 1024 26.8 / 24.8, 2048 30.9 / 30.8, 4096 47 /
+// 57; rank 64 512 28.9 / 33.7, 1024 34.9 / 39.0; 5560 tokens,
+// 13824 to 5120, 74.3 / 93.8; gate and up of 13824, rank 32, 2048 65.8 / 76.7.  54 runs of 30 to 60
+// tokens 64 / 53.
+constexpr int kLoOutTokens = 2048, kLoOutWide = 512, kLoOutRun = 64;
+static bool lora_out_tc(const LoraParams &p, int64_t runs) {
+    return p.vec && p.adapters > 0 && p.rank <= 64 && p.adapters * p.N <= 0x7ffffe00LL &&
+           p.M >= (p.rank > 32 ? kLoOutWide : kLoOutTokens) && runs <= p.M / kLoOutRun;
+}
+
+static int launch_lora_many(LoraParams p, bool out_tc, cudaStream_t st) {
+    const int pitch = lora_pitch(p.rank);
     const int rows = p.nsec * p.rank, cols = std::min(256, (rows + 15) / 16 * 16);
     if (p.adapters > 0) {
         CUtensorMap xmap, xmap16, amap;
@@ -1012,13 +1374,15 @@ static int launch_lora_many(LoraParams p, cudaStream_t st) {
         if (e == cudaSuccess)
             e = launch_pdl(kfn, dim3(num_sms()), kLoThreads, smem, st, xmap, xmap16, amap, p, cols, half, stages);
         if (e == cudaSuccess) {
-            const int64_t units = (int64_t)p.M * rows / 4;
-            e = launch_pdl(reinterpret_cast<const void *>(lora_many_join_kernel),
+            const int64_t units = (int64_t)p.M * p.nsec * (out_tc ? pitch : p.rank) / 4;
+            e = launch_pdl(out_tc ? reinterpret_cast<const void *>(lora_many_join_kernel<true>)
+                                  : reinterpret_cast<const void *>(lora_many_join_kernel<false>),
                            dim3((unsigned)std::min<int64_t>(num_sms(), (units + kLoThreads - 1) / kLoThreads)),
-                           kLoThreads, 0, st, p);
+                           kLoThreads, 0, st, p, pitch);
         }
         if (e != cudaSuccess) return set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
     }
+    if (out_tc) return p.silu ? launch_out<true>(p, pitch, st) : launch_out<false>(p, pitch, st);
     for (int s = 0; s < (p.silu ? 1 : p.nsec); ++s) p.sec_blocks[s] = (int)((p.sec_n[s] + 31) / 32);
     const cudaError_t e = p.rank <= 16   ? pick_many<1>(p, st)
                           : p.rank <= 32 ? pick_many<2>(p, st)
@@ -1042,7 +1406,7 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
     const int64_t m = std::min<int64_t>(M, kLoChunk), tail = M > m ? M % kLoChunk : 0;
     const int64_t rows = std::max({lora_sums(m, (int)K), tail ? lora_sums(tail, (int)K) : 0,
                                    M > kLoSort ? lora_sums(kLoSort, (int)K) : 0});
-    return 256 + (size_t)(rows + (m > kLoSort ? m : 0)) * nsec * rank * sizeof(float);
+    return 256 + (size_t)(rows * rank + (m > kLoSort ? m * lora_pitch(rank) : 0)) * nsec * sizeof(float);
 }
 
 // Runs shorter than this on the whole go kLoSort tokens at a time through the
@@ -1064,7 +1428,7 @@ int launch_lora(LoraParams p, int64_t M, int64_t runs, void *workspace, cudaStre
             const cudaError_t e = launch_lora_few(p, st);
             if (e != cudaSuccess) rc = set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
         } else {
-            rc = launch_lora_many(p, st);
+            rc = launch_lora_many(p, lora_out_tc(p, runs), st);
         }
         if (rc) return rc;
         p.x += (int64_t)p.M * p.K;

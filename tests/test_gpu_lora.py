@@ -129,10 +129,44 @@ def test_prompts(runs):
     run(Case(sum(runs), ids, sizes=(48, 8), adapters=3))
 
 
+@pytest.mark.parametrize("rank", [8, 16, 40, 64, 72])
+@pytest.mark.parametrize("runs", [(128, 128, 128), (127, 129, 16, 15, 1, 130), (1000, 3, 300), (31, 1, 2, 300, 17), (2000, 15, 129, 200)])
+def test_prompts_of_whole_rows(runs, rank):
+    """Outputs in units of 16 bytes, ends of tiles and of sections anywhere,
+    ranks of the adapters' own, in place and not."""
+    ids = np.repeat(np.arange(len(runs)) % 3 - (len(runs) == 5), runs)
+    c = Case(sum(runs) + rank, ids, sizes=(136, 64, 8, 200), rank=rank, adapters=3, K=96,
+             ranks=[rank, max(1, rank // 2 - 1), rank - 3])
+    out = run(c)
+    x, base, lora, ids = c.device()
+    gwa.lora_add(x, base, lora, ids, out=base)
+    assert all(torch.equal(a, b) for a, b in zip(out, base))
+
+
+@pytest.mark.parametrize("more", [0, 1600])
+@pytest.mark.parametrize("rank", [16, 40, 64])
+@pytest.mark.parametrize("I", [8, 64, 200])
+def test_gate_up_of_prompts(I, rank, more):
+    c = Case(I + rank, np.repeat([0, -1, 2, 1], (300, 20, 129 + more, 15)), sizes=(I, I), rank=rank, adapters=3,
+             ranks=[rank, rank // 2, rank - 5])
+    x, (gate, up), lora, ids = c.device()
+    h = bf16_to_f64(gwa.lora_gate_up_silu(x, (gate, up), lora, ids))
+    (g, u), (eg, eu) = c.want()
+    sig = 1 / (1 + np.exp(-g))
+    want = g * sig * u
+    slope = np.abs(sig * (1 + g * (1 - sig))) + eg
+    check(h, want, slope * np.abs(u) * eg + (np.abs(g * sig) + eg) * eu + 2.0 ** -19 * np.abs(want))
+    for at in (0, 1):
+        x, y, lora, ids = c.device()
+        again = gwa.lora_gate_up_silu(x, y, lora, ids, h=y[at])
+        assert torch.equal(again.float(), torch.from_numpy(h).cuda().float())
+
+
 @pytest.mark.parametrize("M", [257, 511, 512, 700, 9000])
 def test_short_runs_that_are_told(M):
     """256 tokens at a time, in order; the same values up to the order of sums."""
     run(Case(M, ids_of(M, M, 5), adapters=5, K=96), runs=M)
+    run(Case(M, np.repeat(ids_of(M, M // 10 + 1, 5), 10)[:M], adapters=5, K=96), runs=M // 10 + 1)
     c = Case(M + 1, ids_of(M, M, 5), sizes=(24, 24), rank=32, adapters=5, K=64)
     x, (gate, up), lora, ids = c.device()
     a, b = (gwa.lora_gate_up_silu(x, (gate, up), lora, ids, runs=r).double() for r in (0, M))
