@@ -27,7 +27,7 @@
 // (bf16, replayed with the adapters in L2 where they fit; of the 6.68 TB/s of a
 // copy): one token, rank 16, 5120 to 7168, 8.3 us, 0.1 of them bytes: two
 // launches that depend on each other, tiles, a round of loads each.  54 tokens
-// of 24 adapters of ranks 8 to 64 there, 45 MB, 18.6 us (2.4 TB/s, 0.36): lines
+// of 24 adapters of ranks 8 to 64 there, 45 MB, 17.6 us (2.6 TB/s, 0.39): lines
 // of L1, as a fragment load of 8 rows touches 8, and two rounds of units.  14
 // sequences of up to 5 tokens, gate and up of 13824, rank 32, 19 MB, 12.4 us
 // (1.5 TB/s).  Prompts of 5560 tokens, 13824 to 5120, rank 64, 272 MB, 74 us
@@ -191,13 +191,24 @@ __device__ __forceinline__ uint4 lo_load(const uint16_t *p, bool ok) {
     return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
+// 32 bytes at once: a fragment's 8 rows are 8 lines of L1, whatever each gives.
+__device__ __forceinline__ void lo_load32(const uint16_t *p, bool ok, uint4 &a, uint4 &b) {
+    a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (ok)
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                     : "l"(p));
+}
+
 // ------------------------------------------------------------ few tokens
 // part[k][m][s][r]: share k's sum of A x.  A CTA's unit is 16 rows of an
 // adapter's A and a share of K for a tile; its warps take 256 inputs at a time
 // (a warp's loads all at once, straight from global memory as MMA fragments: a
-// lane's 16 bytes are the k positions of two MMAs, in the same order on both
-// sides).  The shares depend on K alone, and so does the order of a token's sums.
+// lane's 16 bytes are the k positions of two MMAs, or 32 bytes of four, in the
+// same order on both sides).  The shares depend on K alone, and so does the order of a token's sums.
+template <bool WIDE>
 __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraParams p) {
+    constexpr int LANE = WIDE ? 16 : 8;  // inputs of a lane side by side
     __shared__ LoTiles<true> sh;
     __shared__ float s_acc[kLoWarps][16 * kLoTile];
     __shared__ int s_sum[kLoWarps];
@@ -229,27 +240,43 @@ __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraPara
             if (tile + o < tiles && sh.base[tile + o] <= blk) tile += o;
         const int at = sh.start[tile], n = sh.start[tile + 1] - at, id = sh.key[at], rank = sh.rank[at];
         const int nb = (rank + 15) / 16, in = blk - sh.base[tile], sec = in / nb, r0 = (in - sec * nb) * 16;
-        const uint16_t *a = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + 8 * t;
+        const uint16_t *a = p.a + (((int64_t)id * p.nsec + sec) * p.rank + r0 + g) * p.K + LANE * t;
         const bool in0 = r0 + g < rank, in1 = r0 + g + 8 < rank, tok0 = g < n, tok1 = g + 8 < n;
-        const uint16_t *x0 = p.x + (int64_t)sh.token(at + (tok0 ? g : 0)) * p.K + 8 * t;
-        const uint16_t *x1 = p.x + (int64_t)sh.token(at + (tok1 ? g + 8 : 0)) * p.K + 8 * t;
+        const uint16_t *x0 = p.x + (int64_t)sh.token(at + (tok0 ? g : 0)) * p.K + LANE * t;
+        const uint16_t *x1 = p.x + (int64_t)sh.token(at + (tok1 ? g + 8 : 0)) * p.K + LANE * t;
         float acc[2][4] = {};
         const int end = min(p.K, (k + 1) * p.share);
         for (int i0 = k * p.share + warp * 256; i0 < end; i0 += kLoWarps * 256) {
             uint4 va[8], vb[8];
+            if constexpr (WIDE) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const bool ok = i0 + 32 * c < end;
-                va[c] = lo_load(a + i0 + 32 * c, ok && in0);
-                vb[c] = lo_load(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1);
+                for (int c = 0; c < 8; c += 2) {
+                    const bool ok = i0 + 32 * c + 16 * t < end;
+                    lo_load32(a + i0 + 32 * c, ok && in0, va[c], va[c + 1]);
+                    lo_load32(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1, vb[c], vb[c + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const bool ok = i0 + 32 * c < end;
+                    va[c] = lo_load(a + i0 + 32 * c, ok && in0);
+                    vb[c] = lo_load(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1);
+                }
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (h == 1 && n <= 8) break;
                 uint4 x[8];
+                if constexpr (WIDE) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    x[c] = lo_load((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c < end && (h ? tok1 : tok0));
+                    for (int c = 0; c < 8; c += 2)
+                        lo_load32((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c + 16 * t < end && (h ? tok1 : tok0), x[c],
+                                  x[c + 1]);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        x[c] = lo_load((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c < end && (h ? tok1 : tok0));
+                }
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     mma_bf16(acc[h], va[c].x, vb[c].x, va[c].y, vb[c].y, x[c].x, x[c].y);
@@ -287,9 +314,12 @@ __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraPara
 // 8 t .. 8 t + 7.
 constexpr int kLoFrag = 64;  // 16-byte units of a k step
 
-template <int KS, bool SILU, bool VEC>
+template <int KS, bool SILU, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) lora_few_expand_kernel(LoraParams p) {
-    constexpr int S = SILU ? 2 : 1, Q = KS == 1 ? 1 : KS / 2;  // Q: B's loads of a row
+    constexpr int S = SILU ? 2 : 1, Q = KS == 1 ? 1 : KS / 2;  // Q: 16-byte units of a lane and row of B
+    constexpr int SPAN = WIDE ? 64 : KS == 1 ? 16 : 32;        // ranks whose k steps share lanes
+    // first rank of unit q of lane t
+    auto rank_of = [](int q, int t) { return WIDE ? 64 * (q / 2) + 16 * t + 8 * (q & 1) : KS == 1 ? 4 * t : 32 * q + 8 * t; };
     __shared__ LoTiles<true> sh;
     __shared__ uint4 frag[S * KS * kLoFrag];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
@@ -324,8 +354,12 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                 for (int j = 0; j < 4; ++j, brow += 2 * p.rank)
 #pragma unroll
                     for (int q = 0; q < Q; ++q) {
-                        const int r = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                        const int r = rank_of(q, t);
                         const bool ok = c0 + 2 * j < N && r < rank;
+                        if constexpr (WIDE) {
+                            if (q % 2 == 0) lo_load32(brow + r, ok, b[s][j][q], b[s][j][q + 1]);
+                            continue;
+                        }
                         b[s][j][q] = make_uint4(0u, 0u, 0u, 0u);
                         if constexpr (KS == 1) {
                             if (ok) {
@@ -361,7 +395,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                 waited = true;
                 __syncthreads();  // (the last unit's is read)
                 const float scale = p.scale ? p.scale[id] : 1.f;
-                const int nk = KS == 1 ? 1 : ((rank + 31) / 32) * 2;
+                const int nk = (rank + SPAN - 1) / SPAN * (SPAN / 16);
                 for (int i = tid; i < S * nk * 64; i += kLoThreads) {
                     // four ranks of a token
                     const int s = i / (nk * 64), j = i - s * nk * 64, m = j / (4 * nk), r = (j - m * 4 * nk) * 4;
@@ -378,8 +412,8 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                     v.y = r + 1 < rank ? v.y * scale : 0.f;
                     v.z = r + 2 < rank ? v.z * scale : 0.f;
                     v.w = r + 3 < rank ? v.w * scale : 0.f;
-                    const int ks = KS == 1 ? 0 : r / 32 * 2 + (r / 4) % 2;
-                    const int ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % 32 / 8);
+                    const int ks = KS == 1 ? 0 : WIDE ? r / 64 * 4 + r / 4 % 4 : r / 32 * 2 + (r / 4) % 2;
+                    const int ln = (m % 8) * 4 + (KS == 1 ? r / 4 : r % SPAN / (SPAN / 4));
                     const uint32_t h0 = pack_bf16(v.x, v.y), h1 = pack_bf16(v.z, v.w);
                     frag[(s * KS + ks) * kLoFrag + m / 8 * 32 + ln] =
                         make_uint4(h0, h1, pack_bf16(v.x - bf16_lo(h0), v.y - bf16_hi(h0)),
@@ -387,7 +421,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                 }
                 __syncthreads();
             }
-            if (rank % 8) {
+            if (rank % (WIDE ? 16 : 8)) {
                 // entries past the adapter's rank, whatever they hold, are zero
                 auto mask = [&](uint32_t &w, int k) { w = k + 1 < rank ? w : k < rank ? w & 0xffffu : 0u; };
 #pragma unroll
@@ -396,7 +430,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int q = 0; q < Q; ++q) {
-                            const int k = KS == 1 ? 4 * t : 32 * q + 8 * t;
+                            const int k = rank_of(q, t);
                             mask(b[s][j][q].x, k);
                             mask(b[s][j][q].y, k + 2);
                             if constexpr (KS > 1) {
@@ -420,7 +454,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                 const uint4 *fr = frag + s * KS * kLoFrag + lane;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    if (16 * (KS == 1 ? k : k & ~1) >= rank) break;
+                    if (16 * (k & ~(SPAN / 16 - 1)) >= rank) break;
                     const uint4 even = fr[k * kLoFrag], odd = fr[k * kLoFrag + 32];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -738,7 +772,7 @@ template <int KS, bool SILU, bool VEC>
 __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_expand_kernel(LoraParams p) {
     using L = LoMany<KS, SILU>;
     constexpr int S = L::S, MT = L::MT, Q = KS == 1 ? 1 : KS / 2;
-    extern __shared__ __align__(16) unsigned char lo_raw[];
+    extern __shared__ __align__(1024) unsigned char lo_raw[];
     __shared__ LoTiles<false> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, g = lane >> 2, t = lane & 3;
     uint4 *const frag = reinterpret_cast<uint4 *>(lo_raw) + warp * L::FRAGS;
@@ -1258,8 +1292,14 @@ __global__ void __launch_bounds__(kLeThreads, 1)
 // ---------------------------------------------------------------- host side
 template <int KS, bool SILU, bool VEC>
 static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
-    return launch_pdl(reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC>), dim3(grid),
-                      kLoThreads, 0, st, p);
+    // Rows of B in 32-byte units, where adapters do not have smaller ranks of their
+    // own (whose lanes then have less to do together): 250 tokens of rank 64, 5120
+    // to 7168, 31.7 us against 32.9, gate and up of 13824 90 against 94; ranks 8 to
+    // 64, 54 tokens, 18.6 against 17.6.
+    const bool wide = KS >= 4 && !p.ranks && p.rank % 16 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 31) == 0;
+    return launch_pdl(wide ? reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC, (KS >= 4)>)
+                           : reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC, false>),
+                      dim3(grid), kLoThreads, 0, st, p);
 }
 template <int KS>
 static cudaError_t pick_few(const LoraParams &p, int grid, cudaStream_t st) {
@@ -1278,7 +1318,10 @@ static cudaError_t launch_lora_few(LoraParams p, cudaStream_t st) {
     const int full = 2 * num_sms();
     p.share = lora_share(p.K);
     const int64_t down = tiles * p.nsec * ((p.rank + 15) / 16) * p.ks;
-    cudaError_t e = launch_pdl(reinterpret_cast<const void *>(lora_few_shrink_kernel),
+    // (54 tokens of ranks 8 to 64 17.6 us, in 16-byte loads 18.6)
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.a)) & 31) == 0;
+    cudaError_t e = launch_pdl(wide ? reinterpret_cast<const void *>(lora_few_shrink_kernel<true>)
+                                    : reinterpret_cast<const void *>(lora_few_shrink_kernel<false>),
                                dim3((unsigned)std::min<int64_t>(full, down)), kLoThreads, 0, st, p);
     if (e != cudaSuccess) return e;
     int64_t octets = 0;

@@ -173,6 +173,29 @@ def test_short_runs_that_are_told(M):
     assert ((a - b).abs() <= 2.0 ** -7 * a.abs() + 1e-3).all()
 
 
+@pytest.mark.parametrize("M,rank", [(3, 16), (40, 64), (40, 128), (600, 64)])
+def test_rows_on_16_bytes(M, rank):
+    """x, A and B that begin on 16 bytes and not on 32: the same values."""
+    c = Case(M, ids_of(M, M, 4), rank=rank, K=2080)
+    x, base, lora, ids = c.device()
+
+    def moved(t):
+        room = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")
+        at = 8 if room.data_ptr() % 32 == 0 else 0
+        return room[at:at + t.numel()].view(t.shape).copy_(t)
+
+    other = gwa.LoRA(moved(lora.a), moved(lora.b), scale=lora.scale)
+    x = moved(x)
+    assert x.data_ptr() % 32 == 16 and other.a.data_ptr() % 32 == 16 and other.b.data_ptr() % 32 == 16
+    for g, w, b in zip(gwa.lora_add(x, base, other, ids), *c.want()):
+        check(bf16_to_f64(g), w, b)
+
+
+def test_sections_without_outputs():
+    run(Case(2100, np.repeat([0, 1, -1], 700), sizes=(0, 64, 0, 8), adapters=2, K=64))
+    run(Case(2101, np.repeat([0, 1, -1], 700), sizes=(0, 64, 0, 0, 8, 0), rank=40, adapters=2, K=64))
+
+
 def test_one_adapter_for_all_and_one_for_each():
     run(Case(1, np.zeros(200), adapters=1))
     run(Case(2, np.arange(200), adapters=200, K=64))
