@@ -312,6 +312,49 @@ def test_runs_repeat_and_replay():
     assert all(torch.equal(a, b) for a, b in zip(first, out))
 
 
+@pytest.mark.parametrize("M,rank", [(700, 16), (2100, 40)])
+def test_prompts_replay(M, rank):
+    """A captured call of prompts, replayed with other runs, in place."""
+    lens = [M // 3, 40, M // 2, 9]
+    ids_a = np.repeat([1, -1, 0, 2, 1], lens + [M - sum(lens)]).astype(np.int32)
+    c = Case(M, ids_a, sizes=(64, 24), rank=rank, adapters=3, K=96)
+    x, base, lora, ids = c.device()
+    y = [b.clone() for b in base]
+    work = gwa.make_lora_workspace(lora, M)
+    gwa.lora_add(x, y, lora, ids, out=y, workspace=work)
+    first = [t.clone() for t in y]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        gwa.lora_add(x, y, lora, ids, out=y, workspace=work)
+    for order in (ids_a[::-1].copy(), np.full(M, 2, np.int32), ids_a):
+        c.ids = order
+        ids.copy_(torch.from_numpy(order))
+        for t, b in zip(y, base):
+            t.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w, b in zip(y, *c.want()):
+            check(bf16_to_f64(g), w, b)
+    assert all(torch.equal(a, b) for a, b in zip(first, y))
+
+
+def test_two_streams_at_once():
+    cases = [Case(i, np.repeat([0, 2, 1], 800), sizes=(128, 8), rank=rank, adapters=3, K=512) for i, rank in ((1, 16), (2, 64))]
+    args = [c.device() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    work = [gwa.make_lora_workspace(a[2], 2400) for a in args]
+    out = [[torch.empty_like(b) for b in a[1]] for a in args]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a, s, w, o in zip(args, streams, work, out):
+            gwa.lora_add(*a, out=o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    for c, o in zip(cases, out):
+        for g, w, b in zip(o, *c.want()):
+            check(bf16_to_f64(g), w, b)
+
+
 def test_another_stream():
     c = Case(6, ids_of(6, 300, 4))
     s = torch.cuda.Stream()
