@@ -665,6 +665,16 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
         __syncthreads();
     }
 
+    const bool draft = PLAN && r >= p.targets;
+    const int64_t fr = draft ? r - p.targets : r;  // the row of the filters
+    if constexpr (PLAN) {
+        // A row of no sequence, and a draft's without a token behind it: its plan
+        // is not read, and of the draft's nor is the row, which need not be there
+        // (every warp finds out for itself; the whole cluster leaves)
+        const SmSeq q = sm_sequence(p.q_start, p.batch, fr);
+        if (q.seq < 0 || (draft && fr + 1 >= min((int64_t)q.next, p.targets))) return;
+    }
+
     // (waited for before the first word goes to another CTA: all of the
     // cluster run by then)
     if (cl > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
@@ -673,18 +683,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     // slice starts at element `mis` of its first chunk
     const int64_t per_cta = (p.V + cl - 1) / cl;
     const int64_t lo = min(p.V, rank * per_cta), hi = min(p.V, lo + per_cta);
-    const bool draft = PLAN && r >= p.targets;
-    const int64_t fr = draft ? r - p.targets : r;  // the row of the filters
     const Raw *src = draft ? static_cast<const Raw *>(p.draft) + fr * p.draft_stride + lo
                            : static_cast<const Raw *>(p.logits) + r * p.stride + lo;
-    if constexpr (PLAN) {
-        // whether the row is of a sequence, and a draft's one with a token
-        // behind it (the others' plans are not read)
-        if (warp == 0) {
-            const SmSeq q = sm_sequence(p.q_start, p.batch, fr);
-            if (lane == 0) sh.f_bin = q.seq >= 0 && (!draft || fr + 1 < min((int64_t)q.next, p.targets));
-        }
-    }
     const int len = (int)(hi - lo);
     const int mis = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(Raw));
     const int chunks = (len + mis + PER - 1) / PER;
@@ -756,7 +756,6 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
             low = fminf(low, sh.x_low[c]);
         }
     }
-    if (PLAN && !sh.f_bin) return;  // (the whole cluster)
     if (top == -INFINITY) {  // nothing to draw (the whole cluster leaves)
         if (PLAN) {
             if (rank == 0 && tid == 0) p.plan[r] = SmPlan{top, 0.f, INFINITY, 0, 0, 0};
@@ -772,7 +771,6 @@ __global__ void __launch_bounds__(kSmThreads, 1) sample_kernel(SampleParams p, i
     const float tp = p.top_p ? p.top_p[fr] : 1.f;
     const float mp = p.min_p ? p.min_p[fr] : 0.f;
     const float u = PLAN ? 0.f : p.u[r];
-    if (PLAN) __syncthreads();  // (f_bin is read)
     const bool greedy = !(T > 0.f);
     S s{sh, slice, mis, mis + len, lo - mis, cl, rank, {top, 0.f}, 0.f};
     s.row.per = __fmul_rn(__fdiv_rn(1.f, T), 1.4426950408889634f);

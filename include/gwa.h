@@ -504,7 +504,8 @@ int gwa_sample(const void *logits, int32_t dtype, int64_t rows, int64_t V,
  *   logits        [rows, V] as gwa_sample: the target's
  *   draft_logits  [rows, V] of the same dtype, row i the draft model's for the
  *                 token behind row i, which ids[i + 1] was drawn from under
- *                 the same filters (a sequence's last row is not read); or
+ *                 the same filters (a sequence's last row is not read, nor one
+ *                 of no sequence: they need not be there); or
  *                 NULL: drafts from elsewhere, taken as certain (q(d) = 1)
  *   ids           int32 [rows]: the tokens of the rows; ids[i + 1] is row i's
  *                 draft (one outside [0, V) never stands)
