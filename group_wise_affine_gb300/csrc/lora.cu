@@ -1436,19 +1436,21 @@ static int launch_lora_many(LoraParams p, bool out_tc, cudaStream_t st) {
 
 // The most shares of K: a few tokens' exactly so many, many tokens' up to so
 // many (their kernel chooses).
+constexpr int kLoShares = 8, kLoSums = 3 * kLoChunk;  // (of all tokens together)
 static int lora_shares(int64_t M, int K) {
     if (M <= kLoSort) return (K + lora_share(K) - 1) / lora_share(K);
-    return (int)std::max<int64_t>(1, std::min<int64_t>(8, 24576 / M));
+    return (int)std::min<int64_t>(kLoShares, kLoSums / M);
 }
 
 // 256 bytes (the shares of K that were chosen), the partial sums, and of many
 // tokens what they add up to (see lora_many_join_kernel); enough for either way
-// of taking more than kLoSort tokens (see launch_lora).
+// of taking more than kLoSort tokens (see launch_lora), and for fewer tokens
+// (the whole shares times M go up and down): up to kLoSort tokens have kLoShares
+// shares at most, and more have no more sums than both factors allow.
 static int64_t lora_sums(int64_t M, int K) { return (int64_t)lora_shares(M, K) * M; }
 size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
-    const int64_t m = std::min<int64_t>(M, kLoChunk), tail = M > m ? M % kLoChunk : 0;
-    const int64_t rows = std::max({lora_sums(m, (int)K), tail ? lora_sums(tail, (int)K) : 0,
-                                   M > kLoSort ? lora_sums(kLoSort, (int)K) : 0});
+    const int64_t m = std::min<int64_t>(M, kLoChunk);
+    const int64_t rows = m <= kLoSort ? lora_sums(m, (int)K) : std::min<int64_t>(kLoShares * m, kLoSums);
     return 256 + (size_t)(rows * rank + (m > kLoSort ? m * lora_pitch(rank) : 0)) * nsec * sizeof(float);
 }
 

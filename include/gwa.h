@@ -578,7 +578,8 @@ typedef struct gwa_lora {
  *   base, out      host arrays of [M, size] bf16 buffers, 2-byte aligned
  *         (rows of 16-byte units are read faster); out_s may be base_s, and
  *         must not overlap anything else
- *   workspace  >= gwa_lora_workspace_bytes(lora, M), 16-byte aligned
+ *   workspace  >= gwa_lora_workspace_bytes(lora, M), 16-byte aligned; one for
+ *         M tokens serves fewer
  * Tokens of one adapter are computed together: up to 256 tokens in whatever
  * order they come, of more those that follow one another.  fp32 sums of exact
  * products; A x enters its product in two bf16 parts (2^-17 of it), and out is

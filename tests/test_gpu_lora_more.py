@@ -1,0 +1,44 @@
+"""Adapters (gwa_lora_add, gwa_lora_gate_up_silu): workspaces, alignment, far
+gates, and what lies around and in front of their buffers.  Values against the
+formula in 64 bits, tolerances as in test_gpu_lora; the rest bit for bit.
+"""
+import numpy as np
+import pytest
+import torch
+
+import group_wise_affine_gb300 as gwa
+from helpers import bf16_to_f64
+from test_gpu_lora import Case, check, ids_of
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    gwa.build()
+    gwa.load()
+    assert torch.cuda.is_available()
+    gwa.pipeline_status()
+    yield
+    assert gwa.pipeline_status() == 0
+
+
+# ---------------------------------------------------------------- workspaces
+def test_a_workspace_for_more_tokens_serves_fewer():
+    """Made once, for the largest step."""
+    rank, most = 64, 5000
+    work = None
+    for M in (most, 4096, 4999, 2731, 2000, 257, 256, 1):
+        c = Case(M, ids_of(M, M, 3), K=64, sizes=(48,), rank=rank, adapters=3)
+        args = c.device()
+        if work is None:
+            work = gwa.make_lora_workspace(c.lora, most)
+        got = gwa.lora_add(*args, workspace=work)
+        for g, w, b in zip(got, *c.want()):
+            check(bf16_to_f64(g), w, b)
+    for M in (500, 6144, 8200):
+        c = Case(M, ids_of(M, M, 3), K=64, sizes=(48,), rank=rank, adapters=3)
+        args = c.device()
+        got = gwa.lora_add(*args, workspace=gwa.make_lora_workspace(c.lora, M + 1), runs=M)
+        for g, w, b in zip(got, *c.want()):
+            check(bf16_to_f64(g), w, b)
