@@ -1391,9 +1391,9 @@ static int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
 // 13824 to 5120, 74.3 / 93.8; gate and up of 13824, rank 32, 2048 65.8 / 76.7.  54 runs of 30 to 60
 // tokens 64 / 53.
 constexpr int kLoOutTokens = 2048, kLoOutWide = 512, kLoOutRun = 64;
-static bool lora_out_tc(const LoraParams &p, int64_t runs) {
+static bool lora_out_tc(const LoraParams &p) {
     return p.vec && p.adapters > 0 && p.rank <= 64 && p.adapters * p.N <= 0x7ffffe00LL &&
-           p.M >= (p.rank > 32 ? kLoOutWide : kLoOutTokens) && runs <= p.M / kLoOutRun;
+           p.M >= (p.rank > 32 ? kLoOutWide : kLoOutTokens);
 }
 
 static int launch_lora_many(LoraParams p, bool out_tc, cudaStream_t st) {
@@ -1461,7 +1461,9 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
 constexpr int kLoShortRun = 8;
 
 int launch_lora(LoraParams p, int64_t M, int64_t runs, void *workspace, cudaStream_t st) {
+    // (both rules are of the call's mean run: a launch's own runs are not known)
     const int64_t chunk = runs > M / kLoShortRun ? kLoSort : kLoChunk;
+    const bool long_runs = runs <= M / kLoOutRun;
     p.shares = static_cast<int32_t *>(workspace);
     p.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + 256);
     for (int64_t m = 0; m < M; m += chunk) {
@@ -1473,7 +1475,7 @@ int launch_lora(LoraParams p, int64_t M, int64_t runs, void *workspace, cudaStre
             const cudaError_t e = launch_lora_few(p, st);
             if (e != cudaSuccess) rc = set_error(GWA_ERR_CUDA, "lora: %s", cudaGetErrorString(e));
         } else {
-            rc = launch_lora_many(p, lora_out_tc(p, runs), st);
+            rc = launch_lora_many(p, long_runs && lora_out_tc(p), st);
         }
         if (rc) return rc;
         p.x += (int64_t)p.M * p.K;

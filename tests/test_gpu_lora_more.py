@@ -42,3 +42,16 @@ def test_a_workspace_for_more_tokens_serves_fewer():
         got = gwa.lora_add(*args, workspace=gwa.make_lora_workspace(c.lora, M + 1), runs=M)
         for g, w, b in zip(got, *c.want()):
             check(bf16_to_f64(g), w, b)
+
+
+# ---------------------------------------------------------------- dispatch
+def test_long_runs_of_a_long_call_that_are_told():
+    """200 runs in 16384 tokens are long ones, in each of the launches that the
+    call is made of: the same kernels, and bits, as where nothing is told."""
+    M = 16384
+    c = Case(1, np.repeat(np.arange(200) % 4, 82)[:M], K=64, sizes=(256,), rank=40)
+    x, base, lora, ids = c.device()
+    plain, = gwa.lora_add(x, base, lora, ids)
+    told, = gwa.lora_add(x, base, lora, ids, runs=200)
+    assert torch.equal(plain, told)
+    check(bf16_to_f64(told[-600:]), c.want()[0][0][-600:], c.want()[1][0][-600:])
