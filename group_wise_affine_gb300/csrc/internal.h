@@ -155,6 +155,7 @@ struct LoraParams {
     uint16_t *out[kMaxSections];  // silu: the first alone
     bool silu, vec;         // vec: rows of 16-byte units
     bool in_place;          // out is base: tokens without an adapter stay
+    bool b32;               // few tokens: b begins on 32 bytes
     int32_t *status;
     float *part;            // [ks][M][nsec][rank], see the few tokens' kernel
     uint4 *low;             // many tokens: [M][nsec][rank / 4], see the join

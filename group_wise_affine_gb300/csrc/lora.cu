@@ -191,24 +191,31 @@ __device__ __forceinline__ uint4 lo_load(const uint16_t *p, bool ok) {
     return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-// 32 bytes at once: a fragment's 8 rows are 8 lines of L1, whatever each gives.
-__device__ __forceinline__ void lo_load32(const uint16_t *p, bool ok, uint4 &a, uint4 &b) {
-    a = b = make_uint4(0u, 0u, 0u, 0u);
-    if (ok)
-        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
-                     : "l"(p));
+// 32 bytes, at once where they begin on 32: a fragment's 8 rows are 8 lines of
+// L1, whatever each gives.
+__device__ __forceinline__ void lo_load32(const uint16_t *p, bool ok, bool at_once, uint4 &a, uint4 &b) {
+    if (at_once) {
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        if (ok)
+            asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                         : "l"(p));
+    } else {
+        a = lo_load(p, ok);
+        b = lo_load(p + 8, ok);
+    }
 }
 
 // ------------------------------------------------------------ few tokens
 // part[k][m][s][r]: share k's sum of A x.  A CTA's unit is 16 rows of an
 // adapter's A and a share of K for a tile; its warps take 256 inputs at a time
 // (a warp's loads all at once, straight from global memory as MMA fragments: a
-// lane's 16 bytes are the k positions of two MMAs, or 32 bytes of four, in the
-// same order on both sides).  The shares depend on K alone, and so does the order of a token's sums.
+// lane's 32 bytes are the k positions of four MMAs, in the same order on both
+// sides).  The shares depend on K alone, and so does the order of a token's
+// sums.  WIDE: x and A begin on 32 bytes (see lo_load32).
 template <bool WIDE>
 __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraParams p) {
-    constexpr int LANE = WIDE ? 16 : 8;  // inputs of a lane side by side
+    constexpr int LANE = 16;  // inputs of a lane side by side
     __shared__ LoTiles<true> sh;
     __shared__ float s_acc[kLoWarps][16 * kLoTile];
     __shared__ int s_sum[kLoWarps];
@@ -248,35 +255,20 @@ __global__ void __launch_bounds__(kLoThreads, 2) lora_few_shrink_kernel(LoraPara
         const int end = min(p.K, (k + 1) * p.share);
         for (int i0 = k * p.share + warp * 256; i0 < end; i0 += kLoWarps * 256) {
             uint4 va[8], vb[8];
-            if constexpr (WIDE) {
 #pragma unroll
-                for (int c = 0; c < 8; c += 2) {
-                    const bool ok = i0 + 32 * c + 16 * t < end;
-                    lo_load32(a + i0 + 32 * c, ok && in0, va[c], va[c + 1]);
-                    lo_load32(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1, vb[c], vb[c + 1]);
-                }
-            } else {
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const bool ok = i0 + 32 * c < end;
-                    va[c] = lo_load(a + i0 + 32 * c, ok && in0);
-                    vb[c] = lo_load(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1);
-                }
+            for (int c = 0; c < 8; c += 2) {
+                const bool ok = i0 + 32 * c + LANE * t < end;
+                lo_load32(a + i0 + 32 * c, ok && in0, WIDE, va[c], va[c + 1]);
+                lo_load32(a + i0 + 32 * c + (int64_t)8 * p.K, ok && in1, WIDE, vb[c], vb[c + 1]);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (h == 1 && n <= 8) break;
                 uint4 x[8];
-                if constexpr (WIDE) {
 #pragma unroll
-                    for (int c = 0; c < 8; c += 2)
-                        lo_load32((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c + 16 * t < end && (h ? tok1 : tok0), x[c],
-                                  x[c + 1]);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        x[c] = lo_load((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c < end && (h ? tok1 : tok0));
-                }
+                for (int c = 0; c < 8; c += 2)
+                    lo_load32((h ? x1 : x0) + i0 + 32 * c, i0 + 32 * c + LANE * t < end && (h ? tok1 : tok0), WIDE, x[c],
+                              x[c + 1]);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     mma_bf16(acc[h], va[c].x, vb[c].x, va[c].y, vb[c].y, x[c].x, x[c].y);
@@ -357,7 +349,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                         const int r = rank_of(q, t);
                         const bool ok = c0 + 2 * j < N && r < rank;
                         if constexpr (WIDE) {
-                            if (q % 2 == 0) lo_load32(brow + r, ok, b[s][j][q], b[s][j][q + 1]);
+                            if (q % 2 == 0) lo_load32(brow + r, ok, p.b32, b[s][j][q], b[s][j][q + 1]);
                             continue;
                         }
                         b[s][j][q] = make_uint4(0u, 0u, 0u, 0u);
@@ -1295,8 +1287,9 @@ static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
     // Rows of B in 32-byte units, where adapters do not have smaller ranks of their
     // own (whose lanes then have less to do together): 250 tokens of rank 64, 5120
     // to 7168, 31.7 us against 32.9, gate and up of 13824 90 against 94; ranks 8 to
-    // 64, 54 tokens, 18.6 against 17.6.
-    const bool wide = KS >= 4 && !p.ranks && p.rank % 16 == 0 && (reinterpret_cast<uintptr_t>(p.b) & 31) == 0;
+    // 64, 54 tokens, 18.6 against 17.6.  Where B begins does not count: ranks go to
+    // the same k steps wherever it does, so that the sums are the same.
+    const bool wide = KS >= 4 && !p.ranks && p.rank % 16 == 0;
     return launch_pdl(wide ? reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC, (KS >= 4)>)
                            : reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC, false>),
                       dim3(grid), kLoThreads, 0, st, p);
@@ -1317,6 +1310,7 @@ static cudaError_t launch_lora_few(LoraParams p, cudaStream_t st) {
     const int64_t tiles = std::min<int64_t>(p.M, std::min<int64_t>(p.M, (int64_t)p.adapters + 1) + p.M / kLoTile);
     const int full = 2 * num_sms();
     p.share = lora_share(p.K);
+    p.b32 = (reinterpret_cast<uintptr_t>(p.b) & 31) == 0;
     const int64_t down = tiles * p.nsec * ((p.rank + 15) / 16) * p.ks;
     // (54 tokens of ranks 8 to 64 17.6 us, in 16-byte loads 18.6)
     const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.a)) & 31) == 0;

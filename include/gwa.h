@@ -585,7 +585,9 @@ typedef struct gwa_lora {
  * products; A x enters its product in two bf16 parts (2^-17 of it), and out is
  * rounded once.  Not finite inputs make their own rows' outputs so.  Nothing
  * of a token's result comes from other tokens; the order of its sums is one of
- * M and K up to 256 tokens, of more also of `runs` and how the runs lie.
+ * K, rank and whether `ranks` is given up to 256 tokens, of more also of M, of
+ * `runs`, of how the runs lie and of whether base and out have rows of 16-byte
+ * units.
  * Errors: GWA_ERR_UNSUPPORTED (rank, sections), GWA_ERR_INVALID_ARG,
  * GWA_ERR_MISALIGNED, GWA_ERR_WORKSPACE; nothing is enqueued on error. */
 int gwa_lora_add(const uint16_t *x, int64_t M, gwa_lora lora,

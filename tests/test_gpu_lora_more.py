@@ -55,3 +55,27 @@ def test_long_runs_of_a_long_call_that_are_told():
     told, = gwa.lora_add(x, base, lora, ids, runs=200)
     assert torch.equal(plain, told)
     check(bf16_to_f64(told[-600:]), c.want()[0][0][-600:], c.want()[1][0][-600:])
+
+
+# ---------------------------------------------------------------- alignment
+def moved(t):
+    """A copy that begins on 16 bytes and not on 32."""
+    room = torch.empty(t.numel() + 16, dtype=t.dtype, device="cuda")
+    at = 8 if room.data_ptr() % 32 == 0 else 0
+    out = room[at:at + t.numel()].view(t.shape).copy_(t)
+    assert out.data_ptr() % 32 == 16
+    return out
+
+
+@pytest.mark.parametrize("M", [1, 40, 256])
+@pytest.mark.parametrize("rank", [16, 64, 128])
+@pytest.mark.parametrize("own", [False, True])
+def test_bits_do_not_depend_on_where_buffers_begin(M, rank, own):
+    c = Case(M, ids_of(M, M, 4, none=0.0), K=4128, sizes=(4096, 1024), rank=rank, ranks=[rank] * 4 if own else None)
+    x, base, lora, ids = c.device()
+    want = gwa.lora_add(x, base, lora, ids)
+    for what in ("x", "a", "b", "xab"):
+        other = gwa.LoRA(moved(lora.a) if "a" in what else lora.a, moved(lora.b) if "b" in what else lora.b,
+                         scale=lora.scale, ranks=lora.ranks)
+        got = gwa.lora_add(moved(x) if "x" in what else x, base, other, ids)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), what
