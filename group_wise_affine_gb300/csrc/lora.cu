@@ -206,6 +206,17 @@ __device__ __forceinline__ void lo_load32(const uint16_t *p, bool ok, bool at_on
     }
 }
 
+// g / (1 + e^-g).  e^-g passes fp32's range at -88.7 (and 2^126, past which a
+// fast quotient gives zero, at -87.3), and the other half may be as large again:
+// so 2^-24 / (2^-24 + 2^-24 e^-g), which reaches the least that fp32 can hold.
+// The exponent's rounding next to -24 is 2^-21 of the result.  (An infinite g
+// below zero gives NaN.)
+__device__ __forceinline__ float lo_silu(float g) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(fmaf(g, -1.4426950408889634f, -24.f)) + 0x1p-24f));
+    return g * (r * 0x1p-24f);
+}
+
 // ------------------------------------------------------------ few tokens
 // part[k][m][s][r]: share k's sum of A x.  A CTA's unit is 16 rows of an
 // adapter's A and a share of K for a tile; its warps take 256 inputs at a time
@@ -462,7 +473,7 @@ __global__ void __launch_bounds__(kLoThreads, KS * (SILU ? 2 : 1) <= 4 ? 2 : 1) 
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        acc[0][j][i] = __fdividef(acc[0][j][i], 1.f + __expf(-acc[0][j][i])) * acc[1][j][i];
+                        acc[0][j][i] = lo_silu(acc[0][j][i]) * acc[1][j][i];
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -946,8 +957,7 @@ __global__ void __launch_bounds__(kLoThreads, LoMany<KS, SILU>::CTAS) lora_many_
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            acc[m][0][j][i] =
-                                __fdividef(acc[m][0][j][i], 1.f + __expf(-acc[m][0][j][i])) * acc[m][1][j][i];
+                            acc[m][0][j][i] = lo_silu(acc[m][0][j][i]) * acc[m][1][j][i];
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -1239,8 +1249,8 @@ __global__ void __launch_bounds__(kLeThreads, 1)
                         float lo = bf16_lo(bw[i]) + v[SILU ? 0 : at / 32][at % 32];
                         float hi = bf16_hi(bw[i]) + v[SILU ? 0 : at / 32][at % 32 + 1];
                         if constexpr (SILU) {
-                            lo = __fdividef(lo, 1.f + __expf(-lo)) * (bf16_lo(ew[i]) + v[1][at]);
-                            hi = __fdividef(hi, 1.f + __expf(-hi)) * (bf16_hi(ew[i]) + v[1][at + 1]);
+                            lo = lo_silu(lo) * (bf16_lo(ew[i]) + v[1][at]);
+                            hi = lo_silu(hi) * (bf16_hi(ew[i]) + v[1][at + 1]);
                         }
                         w[i] = pack_bf16(lo, hi);
                     }

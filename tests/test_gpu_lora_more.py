@@ -8,6 +8,7 @@ import torch
 
 import group_wise_affine_gb300 as gwa
 from helpers import bf16_to_f64
+from oracle import serving
 from test_gpu_lora import Case, check, ids_of
 
 pytestmark = pytest.mark.gpu
@@ -21,6 +22,15 @@ def _lib():
     gwa.pipeline_status()
     yield
     assert gwa.pipeline_status() == 0
+
+
+def some(M):
+    """Ids of three adapters: in no order, of more than 256 tokens runs of a
+    third, 20, a half, 9 and what is left."""
+    if M <= 256:
+        return ids_of(M, M, 3)
+    lens = [M // 3, 20, M // 2, 9]
+    return np.repeat([1, -1, 0, 2, 1], lens + [M - sum(lens)])
 
 
 # ---------------------------------------------------------------- workspaces
@@ -79,3 +89,33 @@ def test_bits_do_not_depend_on_where_buffers_begin(M, rank, own):
                          scale=lora.scale, ranks=lora.ranks)
         got = gwa.lora_add(moved(x) if "x" in what else x, base, other, ids)
         assert all(torch.equal(a, b) for a, b in zip(got, want)), what
+
+
+# ---------------------------------------------------------------- far gates
+@pytest.mark.parametrize("M", [3, 60, 300, 2100])
+@pytest.mark.parametrize("size", [0, 100])
+def test_gates_far_from_zero(M, size):
+    """Gates of 60 to 100 on either side, where e^-g leaves fp32's range, and
+    up to 2^100 on the other half.  Beside the bar of test_gpu_lora: the fast
+    exponential is off by 2 + 1.173 |g| steps of fp32 (2^-23), the quotient by
+    2, the slope is taken at the far end of g's error, and below fp32's normal
+    range e^-|g| is a whole number of 2^-149 (a bf16 of 2^-133)."""
+    I, rank = 64, 16
+    c = Case(M + size, some(M), sizes=(I, I), rank=rank, adapters=3, K=96)
+    rng = np.random.default_rng(M)
+    g0 = rng.uniform(60, 100, (M, I)) * rng.choice([-1.0, 1.0], (M, I))
+    c.base[0] = serving.bf16_round(g0.astype(np.float32))
+    c.base[1] = serving.bf16_round((rng.standard_normal((M, I)) * 2.0 ** size).astype(np.float32))
+    x, (gate, up), lora, ids = c.device()
+    h = bf16_to_f64(gwa.lora_gate_up_silu(x, (gate, up), lora, ids))
+    (g, u), (eg, eu) = c.want()
+    e = np.exp(-np.abs(g))
+    sig = np.where(g < 0, e, 1.0) / (1 + e)
+    want = g * sig * u
+    slope = (np.abs(sig * (1 + g * (1 - sig))) + np.minimum(eg, e)) * np.exp(eg)
+    fast = (4 + 1.173 * np.abs(g)) * 2.0 ** -23 + 2.0 ** -22
+    bar = slope * np.abs(u) * eg + np.abs(g * sig) * eu * (1 + eg) + fast * np.abs(want) \
+        + np.abs(g * u) * 2.0 ** -149 + 2.0 ** -133
+    check(h, want, bar)
+    if size:
+        assert (np.abs(h[(g < -88) & (g > -95)]) > 0).all()
