@@ -54,6 +54,25 @@ def test_a_workspace_for_more_tokens_serves_fewer():
             check(bf16_to_f64(g), w, b)
 
 
+@pytest.mark.parametrize("M", [5, 250, 700, 2100])
+@pytest.mark.parametrize("rank", [16, 40, 128])
+def test_whatever_the_workspace_holds(M, rank):
+    """Nothing is taken from it that the call has not put there: the rows of
+    tokens without an adapter, what lies past an adapter's rank, shares of K
+    that are not used."""
+    c = Case(M + rank, some(M), K=2080, sizes=(64, 24), rank=rank, adapters=3, ranks=[rank, 0, rank // 2 - 3])
+    x, base, lora, ids = c.device()
+    work = gwa.make_lora_workspace(lora, M)
+    outs = []
+    for fill in (0x00, 0xff, 0x7f):  # zeros, NaN, 3.4e38
+        work.fill_(fill)
+        outs.append(gwa.lora_add(x, base, lora, ids, workspace=work))
+    for g, w, b in zip(outs[0], *c.want()):
+        check(bf16_to_f64(g), w, b)
+    for other in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
+
+
 # ---------------------------------------------------------------- dispatch
 def test_long_runs_of_a_long_call_that_are_told():
     """200 runs in 16384 tokens are long ones, in each of the launches that the
@@ -119,3 +138,74 @@ def test_gates_far_from_zero(M, size):
     check(h, want, bar)
     if size:
         assert (np.abs(h[(g < -88) & (g > -95)]) > 0).all()
+
+
+@pytest.mark.parametrize("M", [3, 300, 2100])
+def test_infinite_gates_and_inputs(M):
+    """An infinite gate makes its own output not finite, an infinite input its
+    own token's outputs; no other bit moves."""
+    I = 64
+    c = Case(M, np.full(M, 1), sizes=(I, I), rank=16, adapters=2, K=96)
+    x, (gate, up), lora, ids = c.device()
+    want = gwa.lora_gate_up_silu(x, (gate, up), lora, ids)
+    gate[0, 3], gate[1, 5], gate[2, 63] = float("inf"), float("-inf"), float("nan")
+    got = gwa.lora_gate_up_silu(x, (gate, up), lora, ids)
+    hit = torch.zeros(M, I, dtype=torch.bool, device="cuda")
+    hit[0, 3] = hit[1, 5] = hit[2, 63] = True
+    assert torch.equal(got[~hit], want[~hit]) and not got[hit].isfinite().any()
+    x, base, lora, ids = c.device()
+    want = gwa.lora_add(x, base, lora, ids)
+    x[M // 2, 7] = float("-inf")
+    rows = torch.arange(M, device="cuda") != M // 2
+    for g, w in zip(gwa.lora_add(x, base, lora, ids), want):
+        assert torch.equal(g[rows], w[rows]) and not g[M // 2].isfinite().any()
+
+
+# ---------------------------------------------------------------- buffers
+def guarded(M, n, dtype=torch.bfloat16):
+    wide = torch.full((M * n + 256,), 3.0, dtype=dtype, device="cuda")
+    return wide, wide[128:-128].view(M, n)
+
+
+@pytest.mark.parametrize("M,rank", [(40, 16), (300, 24), (2100, 16), (700, 40), (513, 64), (2050, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_buffers_between_guards(M, rank, in_place):
+    """Rows of 16-byte units, ends of tiles and of blocks of outputs anywhere."""
+    sizes = (136, 8, 200)
+    c = Case(M + rank, some(M), sizes=sizes, rank=rank, adapters=3, K=96, ranks=[rank, rank - 3, rank // 2])
+    x, base, lora, ids = c.device()
+    rooms = [guarded(M, n) for n in sizes]
+    out = [o for _, o in rooms]
+    if in_place:
+        for o, b in zip(out, base):
+            o.copy_(b)
+    gwa.lora_add(x, out if in_place else base, lora, ids, out=out)
+    for o, w, b in zip(out, *c.want()):
+        check(bf16_to_f64(o), w, b)
+    for wide, _ in rooms:
+        assert (wide[:128] == 3).all() and (wide[-128:] == 3).all()
+
+
+@pytest.mark.parametrize("M,rank,I", [(40, 16, 72), (300, 24, 72), (2100, 16, 200), (700, 40, 8), (700, 64, 136)])
+def test_gate_up_between_guards(M, rank, I):
+    c = Case(M + I, some(M), sizes=(I, I), rank=rank, adapters=3, K=96)
+    x, base, lora, ids = c.device()
+    want = gwa.lora_gate_up_silu(x, base, lora, ids)
+    wide, h = guarded(M, I)
+    gwa.lora_gate_up_silu(x, base, lora, ids, h=h)
+    assert torch.equal(h, want)
+    for at in (0, 1):
+        (wide, h), x_base = guarded(M, I), list(base)
+        x_base[at] = h.copy_(base[at])
+        gwa.lora_gate_up_silu(x, x_base, lora, ids, h=h)
+        assert torch.equal(h, want)
+        assert (wide[:128] == 3).all() and (wide[-128:] == 3).all()
+
+
+@pytest.mark.parametrize("M,rank,runs", [(40, 64, 0), (700, 16, 0), (700, 16, 700), (2100, 16, 0), (9000, 64, 0)])
+def test_calls_repeat_bit_for_bit(M, rank, runs):
+    c = Case(M, ids_of(M, M, 3) if runs else some(M), sizes=(264, 64), rank=rank, adapters=3, K=1056)
+    args = c.device()
+    first = gwa.lora_add(*args, runs=runs)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(first, gwa.lora_add(*args, runs=runs)))
