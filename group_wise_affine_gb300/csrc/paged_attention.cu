@@ -468,7 +468,10 @@ __global__ void __launch_bounds__(kPgWarps * kWarp, PgLayout<BITS, D, NN>::CTAS)
             for (int u = 0; u < U; ++u) {
                 const int page = __shfl_sync(FULL, pages, U * (step - pages_at) + u);
                 const int at = sq.at<WIN>(step) * STEP + warp * KEYS + u * 16;
-                if (gone(at, 16)) continue;  // warp-uniform
+                if (gone(at, 16)) {  // warp-uniform
+                    if (WIN) continue;
+                    break;
+                }
                 const int key = WIN ? sq.span.key(at) : at;
                 const int64_t row = (((int64_t)page * p.kv.heads + hk) << p.kv.page_shift) +
                                     (key & pmask);
