@@ -269,11 +269,12 @@ template <int KT, bool WIN>
 struct PfPages {
     const PagedParams &p;
     const PfPiece &w;
+    int len, tb, hk, b;  // of w
     __device__ __forceinline__ int64_t look(int tile, int lane) const {
-        const int at = tile * KT + lane * 16, key = WIN ? w.t.span.key(at) : at, hk = w.hk;
+        const int at = tile * KT + lane * 16, key = WIN ? w.t.span.key(at) : at;
         int pg = 0;
-        if (tile < w.tb && lane < KT / 16 && at < w.len<WIN>() && !(WIN && pg_hidden(p, at, 16, w.t.low))) {
-            pg = p.kv.page_table[(int64_t)w.b * p.kv.max_pages + (key >> p.kv.page_shift)];
+        if (tile < tb && lane < KT / 16 && at < len && !(WIN && pg_hidden(p, at, 16, w.t.low))) {
+            pg = p.kv.page_table[(int64_t)b * p.kv.max_pages + (key >> p.kv.page_shift)];
             if ((unsigned)pg >= (unsigned)p.kv.num_pages) {
                 if (p.status) atomicOr(p.status, (int)kKvBadPage);
                 pg = 0;
@@ -821,7 +822,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         uint32_t n = 0;
         bool ok = true;
         while (ok && pf_next<RB, KT, WIN>(p, cur, &s_piece[warp], lane)) {
-            const PfPages<KT, WIN> pages{p, w};
+            const PfPages<KT, WIN> pages{p, w, w.len<WIN>(), w.tb, w.hk, w.b};
             float v_lim = -1.f, up = 1.f, down = 1.f;
             uint32_t x[4][G];  // keys 4 lane + j
             auto load = [&](int64_t base, int tile) {
@@ -957,7 +958,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) paged_prefill_kernel(PagedParam
         uint32_t n = 0;
         bool ok = true;
         while (ok && pf_next<RB, KT, WIN>(p, cur, &s_piece[warp], lane)) {
-            const PfPages<KT, WIN> pages{p, w};
+            const PfPages<KT, WIN> pages{p, w, w.len<WIN>(), w.tb, w.hk, w.b};
             uint4 kreg[KU];
             uint32_t vreg[VU][8][VW];
             auto load_k = [&](int64_t base, int tile) {
