@@ -970,8 +970,9 @@ def lora_add(x: torch.Tensor, base: Sequence[torch.Tensor], lora: LoRA,
     """gwa_lora_add: ``base`` (a projection's outputs, one bfloat16 [M, size]
     a section) plus each token's own low-rank adapter of x [M, K]; ids int32
     [M] names it (negative: none).  ``out`` may be ``base``.  ``runs``: how
-    many runs of neighbours with one adapter there are at most (0: not
-    known; of more than 256 tokens it chooses the kernels)."""
+    many runs of neighbours with one adapter there are at most; of more than
+    256 tokens it chooses the kernels (0: not known, taken as few and long:
+    many single tokens want it told)."""
     M, sizes, bp, workspace = _lora_inputs(x, lora, ids, base, workspace, stream)
     wp, wn = _ws(workspace)
     if out is None:

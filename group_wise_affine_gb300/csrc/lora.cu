@@ -762,8 +762,10 @@ __global__ void __launch_bounds__(kLoThreads) lora_many_join_kernel(LoraParams p
 // neighbouring tiles of the same outputs, so that B comes out of the L1 cache.
 // t's fragments are each warp's own copy in shared memory; the next step's base
 // is on its way during the products, its B during the stores.
-// Warp-level MMAs serve: the work is bound by the bytes of base and output (at
-// rank 64 the products are 2 x 64 x 2 FLOP for each 4 bytes).
+// For what lora_many_out_kernel, below, does not take: rows that are no 16-byte
+// units, ranks above 64, fewer tokens or short runs, where a tile of 16 or 32
+// tokens leaves less of a product unused than one of 128.  Long runs are slower
+// here: 5560 tokens of rank 64, 13824 to 5120, 52 us for 30 there.
 template <int KS, bool SILU>
 struct LoMany {
     static constexpr int S = SILU ? 2 : 1, MT = KS * S <= 4 && !SILU ? 2 : 1, TM = 16 * MT;
@@ -1295,9 +1297,9 @@ __global__ void __launch_bounds__(kLeThreads, 1)
 template <int KS, bool SILU, bool VEC>
 static cudaError_t launch_few(const LoraParams &p, int grid, cudaStream_t st) {
     // Rows of B in 32-byte units, where adapters do not have smaller ranks of their
-    // own (whose lanes then have less to do together): 250 tokens of rank 64, 5120
-    // to 7168, 31.7 us against 32.9, gate and up of 13824 90 against 94; ranks 8 to
-    // 64, 54 tokens, 18.6 against 17.6.  Where B begins does not count: ranks go to
+    // own (whose lanes then have less to do together): 250 single tokens over 32
+    // adapters of rank 64, 5120 to 7168, 33.4 us against 34.8, gate and up of 13824
+    // 57.4 against 59.5; ranks 8 to 64, 54 tokens, 18.6 against 17.6.  Where B begins does not count: ranks go to
     // the same k steps wherever it does, so that the sums are the same.
     const bool wide = KS >= 4 && !p.ranks && p.rank % 16 == 0;
     return launch_pdl(wide ? reinterpret_cast<const void *>(lora_few_expand_kernel<KS, SILU, VEC, (KS >= 4)>)
@@ -1390,10 +1392,10 @@ static int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
 // Outputs on tcgen05 where TMA can bring them (and a row of B has an int's
 // coordinate), for long runs: a block takes some 2400 cycles whatever its tokens.
 // The whole call there against warp-level MMAs, us: rank 16, 5120 to 7168, one
-// run of 512 tokens 24.7 / 20.6, 1024 26.8 / 24.8, 2048 30.9 / 30.8, 4096 47 /
-// 57; rank 64 512 28.9 / 33.7, 1024 34.9 / 39.0; 5560 tokens,
-// 13824 to 5120, 74.3 / 93.8; gate and up of 13824, rank 32, 2048 65.8 / 76.7.  54 runs of 30 to 60
-// tokens 64 / 53.
+// run of 512 tokens 24.7 / 20.6, 1024 26.8 / 24.8, 2048 31.0 / 30.9, 4096 48.5 /
+// 57.1; rank 64 512 29.5 / 33.4, 1024 34.9 / 38.7; 5560 tokens, 13824 to 5120, 74.8
+// / 94.3; gate and up of 13824, rank 32, 2048 64.2 / 75.9, 4096 104.5 / 132.7, rank
+// 64, 512 35.5 / 41.2.  54 runs of 30 to 60 tokens 64 / 53.
 constexpr int kLoOutTokens = 2048, kLoOutWide = 512, kLoOutRun = 64;
 static bool lora_out_tc(const LoraParams &p) {
     return p.vec && p.adapters > 0 && p.rank <= 64 && p.adapters * p.N <= 0x7ffffe00LL &&
@@ -1459,9 +1461,12 @@ size_t lora_workspace_bytes(int64_t M, int64_t K, int nsec, int rank) {
 }
 
 // Runs shorter than this on the whole go kLoSort tokens at a time through the
-// kernels that put them in order.  Rank 16, 32 adapters, 5120 to 7168, in order
-// against as they come: 500 single tokens 42 us against 160, 530 in runs of five
-// 35 against 47, 640 in runs of twelve 39 against 34.
+// kernels that put them in order.  520 tokens of 32 adapters in runs of 1, 3, 5
+// and 8, in order against as they come, us: rank 16, 5120 to 7168, 45 / 158, 46 /
+// 70, 45 / 43, 43 / 34; gate and up of 13824, rank 32, 75 / 295, 74 / 115, 72 / 76,
+// 64 / 55; rank 16, 13824 to 5120, 43 / 314, 45 / 117, 43 / 72, 42 / 57; 1024 to
+// 1024, 25 / 43, 27 / 27, 27 / 21, 23 / 19.  The sides meet at runs of 3 (small
+// projections) to more than 8 (many inputs).
 constexpr int kLoShortRun = 8;
 
 int launch_lora(LoraParams p, int64_t M, int64_t runs, void *workspace, cudaStream_t st) {

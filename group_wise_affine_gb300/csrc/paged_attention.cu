@@ -62,8 +62,9 @@
 // counted over the places of PgSpan (the sinks, then the window's keys, in
 // sixteens), whatever the cache's length.  Steps that every row sees whole come
 // first, so that what the mask hides does not decide their roundings.  Measured:
-// one token over 131071 keys through 4096 and 4 sinks 14.5 us, as over a
-// cache of 4096; 54 sequences of up to 4 drafted tokens through 1024 and 16, u8,
+// one token of 40 heads over 131071 keys through 4096 and 4 sinks 14.4 us, where a
+// cache of 4096 takes 12.4 (the same call in a graph of its own; the two us have
+// not been traced); 54 sequences of up to 4 drafted tokens through 1024 and 16, u8,
 // 32 heads over 8, 57 us (120 MB, 2.1 TB/s): 1050 instructions for a warp's 32 keys of 16
 // rows, issued at 36% with three CTAs an SM (the u8 ring), waiting for one
 // another and, at 13%, for instructions.

@@ -28,9 +28,9 @@
 // mass.
 //
 // Measured, both kernels: 54 sequences with up to 4 drafts, 151669 bf16 tokens,
-// filters of all kinds, 140 us: sampling's 113 (318 rows, 96 MB, 14.4 us of HBM
-// bandwidth; see there what a row takes), this one's 27: issue 44% at four
-// CTAs an SM, 25 instructions a token of two rows, scans and cluster barriers.
+// filters of all kinds, 134 us: sampling's 112 alone (318 rows, 96.6 MB read, 14.4
+// us of HBM bandwidth; see there what a row takes), then this one: issue 44% at
+// four CTAs an SM, 25 instructions a token of two rows, scans and cluster barriers.
 // 16 sequences with 7 looked-up drafts, 50021 tokens, top-p, 47 us; one
 // sequence with 4 drafts, 131072 fp32 tokens, 26.8 us, two launches of a dozen
 // barriers each.
